@@ -474,6 +474,186 @@ const char* fa_strerror(fa_status status);
  * also written to stderr as "[fedavg] <status text>: <detail>". */
 const char* fa_last_error(const fa_ctx* ctx);
 
+/* ------------------------------------------------------------------------------------
+ * Server-side training operators: what a server computes on the model it holds, next to
+ * averaging updates.  [FLARE] names exchanging distilled knowledge instead of weights as
+ * an alternative, and adapters on a frozen backbone; these operators are a distillation
+ * step of the global model (the student) from the clients' top logits, and the merge of
+ * an aggregated adapter into the frozen weights.
+ *
+ * A work handle holds what these calls share: a device workspace that grows to the
+ * largest call's need and is kept, a device error word, and the order of its calls.
+ * Calls on one handle may use any streams; each starts after the handle's previous call
+ * (they share the workspace).  All tensors are in the handle's device memory, row-major
+ * with a row stride in elements (`ld...`), and are read and written on `stream`; what was
+ * queued on other streams is the caller's to order.  No call waits for the GPU, except
+ * to free a workspace that has to grow.  Calls can be captured into a CUDA graph once the
+ * workspace is large enough (a call that would have to grow it returns FA_ERR_STATE while
+ * capturing); replays use the handle's workspace, so they and direct calls on the handle
+ * must be ordered by the caller.
+ */
+typedef struct fa_work fa_work;   /* opaque; owned by the library */
+
+typedef struct {
+    uint32_t size;             /* sizeof(fa_work_opts): lets the struct grow */
+    uint32_t timeout_ms;       /* bound on every host-side wait (0 = default 60000) */
+    uint64_t workspace_bytes;  /* device workspace allocated at open (0 = at first need) */
+    uint32_t flags;            /* 0 (or FA_TEST_WAIT_EXPIRES, see below) */
+    uint32_t reserved;         /* 0 */
+} fa_work_opts;
+
+typedef struct {
+    uint64_t kernel_launches;  /* kernels launched since fa_work_open */
+    uint64_t workspace_bytes;  /* the workspace's present size */
+} fa_work_stats;
+
+/* Open a work handle on the current device.  opts: NULL for defaults.
+ * Errors: FA_ERR_ARG, FA_ERR_NOMEM, FA_ERR_CUDA. */
+fa_status fa_work_open(const fa_work_opts* opts, fa_work** out);
+
+/* Wait (bounded) for the handle's work and free it.  NULL is a no-op.  On FA_ERR_TIMEOUT
+ * the handle stays open. */
+fa_status fa_work_close(fa_work* w);
+
+/* Wait (bounded) for the handle's last call and report what its kernels found since the
+ * last check: FA_ERR_INTERNAL (a bounded device-side wait gave up: outputs are invalid),
+ * FA_ERR_RANGE (a client's list named a vocabulary entry >= vocab; such entries were left
+ * out), FA_ERR_TIMEOUT. */
+fa_status fa_work_sync(fa_work* w);
+
+fa_status fa_work_get_stats(fa_work* w, fa_work_stats* out);
+
+/* Detail of the last error on this handle ("" if none); valid until the next call. */
+const char* fa_work_last_error(const fa_work* w);
+
+typedef enum { FA_ACT_NONE = 0, FA_ACT_RELU = 1, FA_ACT_GELU = 2, FA_ACT_SILU = 3 } fa_act;
+
+#define FA_TRANS_A 1u   /* a is stored [k, m] (else [m, k]) */
+#define FA_TRANS_B 2u   /* b is stored [n, k], a linear layer's weight (else [k, n]) */
+
+/* out[m,n] = act(alpha * A . B + bias) + beta * residual,   A = op(a) [m,k], B = op(b) [k,n]
+ *
+ * Products of bf16 operands are exact and summed in fp32; fp32 operands are each split
+ * exactly enough into three bf16 terms (24 bits) and the products down to 2^-24 of the
+ * largest are summed in fp32, so an fp32 result keeps fp32 accuracy.  Bias, activation
+ * and residual are applied to the fp32 sum and the result is rounded once (RNE).  A NaN
+ * or an infinity in an operand makes the outputs that depend on it non-finite; where an
+ * operand is fp32 these may be NaN where IEEE arithmetic gives an infinity (the terms of
+ * a split infinity meet zeros).
+ *   gelu is z * Phi(z) (the erf form), silu is z / (1 + exp(-z)). */
+typedef struct {
+    uint32_t size;             /* sizeof(fa_product_args) */
+    uint32_t flags;            /* FA_TRANS_A | FA_TRANS_B */
+    int32_t dtype_in;          /* a, b and bias: FA_F32 or FA_BF16 */
+    int32_t dtype_out;         /* out, residual and pre */
+    int32_t act;               /* fa_act */
+    uint32_t reserved;         /* 0 */
+    uint64_t m, n, k;          /* each < 2^31; m or n of 0 is a no-op, k of 0 an empty sum */
+    const void* a;
+    uint64_t lda;
+    const void* b;
+    uint64_t ldb;
+    const void* bias;          /* [n], or NULL */
+    const void* residual;      /* [m,n], or NULL; may be `out` itself; not read if beta == 0 */
+    uint64_t ldr;
+    void* out;                 /* [m,n]; must not overlap a or b */
+    uint64_t ldo;
+    void* pre;                 /* [m,n] with stride ldo: alpha * A . B + bias, for the backward
+                                  call; or NULL */
+    double alpha, beta;        /* finite; used in fp32 */
+} fa_product_args;
+
+/* Errors: FA_ERR_ARG (null or host pointer, unknown flag or activation, alpha or beta not
+ * finite, overlap), FA_ERR_DTYPE, FA_ERR_RANGE (a size of 2^31 or more, a stride shorter
+ * than its row), FA_ERR_STATE (workspace growth while capturing), FA_ERR_NOMEM,
+ * FA_ERR_CUDA. */
+fa_status fa_product(fa_work* w, const fa_product_args* args, void* stream);
+
+/* Gradients of fa_product: with dZ = dout * act'(pre),
+ *     d_a = alpha * dZ . B^T,   d_b = alpha * A^T . dZ   (each stored like a / b),
+ *     d_bias[n] = sum over m of dZ.
+ * The residual's gradient is beta * dout itself.  dZ is formed in fp32.  For the two
+ * products it is held in bf16 where the gradients are bf16 (its rounding is of the size of
+ * theirs), and in three bf16 terms where they are fp32; d_bias sums the unrounded dZ in
+ * fp32, in an order that does not depend on the run.  Any gradient may be NULL. */
+typedef struct {
+    uint32_t size;             /* sizeof(fa_product_backward_args) */
+    uint32_t flags;            /* FA_TRANS_A | FA_TRANS_B, as in the forward call */
+    int32_t dtype_in;          /* a and b */
+    int32_t dtype_dout;        /* dout and pre */
+    int32_t dtype_grad;        /* d_a, d_b and d_bias */
+    int32_t act;
+    uint64_t m, n, k;          /* m or n of 0: empty sums, so zero gradients of what has elements */
+    const void* a;             /* needed for d_b */
+    uint64_t lda;
+    const void* b;             /* needed for d_a */
+    uint64_t ldb;
+    const void* dout;          /* [m,n] */
+    uint64_t ldd;
+    const void* pre;           /* [m,n], needed unless act is FA_ACT_NONE */
+    uint64_t ldp;
+    void* d_a;
+    uint64_t ldda;
+    void* d_b;
+    uint64_t lddb;
+    void* d_bias;              /* [n] */
+    double alpha;
+} fa_product_backward_args;
+
+/* Errors: as fa_product. */
+fa_status fa_product_backward(fa_work* w, const fa_product_backward_args* args, void* stream);
+
+/* One client's top logits on the rows of a public batch, as the client sent them. */
+typedef struct {
+    const int32_t* index;      /* [rows, topk] vocabulary entries; negative: an unused place */
+    const void* value;         /* [rows, topk] that client's logits there (dtype_value) */
+    uint32_t topk;             /* 1..FA_DISTILL_MAX_TOPK */
+    uint32_t reserved;         /* 0 */
+    double weight;             /* n_j: finite, >= 0, <= 2^24 (its sample count) */
+} fa_distill_client;
+
+#define FA_DISTILL_MAX_CLIENTS 16
+#define FA_DISTILL_MAX_TOPK    2048   /* per client, and summed over the clients */
+
+/* Distillation of the student's logits z[rows, vocab] from the clients' top logits at
+ * temperature T.  In row r, client j is present if its list has a used place with a value
+ * above -inf; p_j is the softmax of its values / T over those places, q the softmax of
+ * z / T over the vocabulary, N_r the sum of n_j over the clients present, and
+ *
+ *   loss[r] = row_weight[r] * T^2 * sum_j (n_j / N_r) * sum_c p_jc * (log p_jc - log q[i_jc])
+ *   grad[r] = d loss[r] / d z[r] = row_weight[r] * T * (q - sum_j (n_j / N_r) p_j)
+ *
+ * -- the weighted mean over the clients that sent something for the row, as the per-key
+ * means of this library.  A row with no client present, or with row_weight 0 (padding:
+ * its logits are not looked at), has loss 0 and a zero gradient.  An entry of z at -inf
+ * has q = 0 (a closed vocabulary entry); a row whose every entry is -inf gives NaN.
+ * Several clients (or places) may name the same entry; their shares are added in fixed
+ * point (2^-62), so the order of the sum does not matter. */
+typedef struct {
+    uint32_t size;                    /* sizeof(fa_distill_args) */
+    uint32_t n_clients;               /* 1..FA_DISTILL_MAX_CLIENTS */
+    int32_t dtype;                    /* logits and grad: FA_F32 or FA_BF16 */
+    int32_t dtype_value;              /* the clients' values */
+    uint64_t rows, vocab;             /* each < 2^31; 0 rows is a no-op, vocab >= 1 */
+    const void* logits;
+    uint64_t ld;
+    const fa_distill_client* clients; /* [n_clients] */
+    double temperature;               /* finite, > 0 */
+    const float* row_weight;          /* [rows] >= 0, or NULL for 1 */
+    float* loss;                      /* [rows]; fa_distill_grad: may be NULL */
+    float* lse;                       /* [rows] log sum exp(z / T) (0 in rows of weight 0):
+                                         fa_distill_loss writes it unless NULL;
+                                         fa_distill_grad reads it unless NULL, else it
+                                         computes the sum in the same pass over the row */
+    void* grad;                       /* fa_distill_grad: [rows, vocab]; may be `logits` itself */
+    uint64_t ldg;
+} fa_distill_args;
+
+/* Errors: FA_ERR_ARG, FA_ERR_DTYPE, FA_ERR_RANGE (sizes, strides, topk), FA_ERR_WEIGHT,
+ * FA_ERR_CUDA.  List entries >= vocab are left out and reported by fa_work_sync. */
+fa_status fa_distill_loss(fa_work* w, const fa_distill_args* args, void* stream);
+fa_status fa_distill_grad(fa_work* w, const fa_distill_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

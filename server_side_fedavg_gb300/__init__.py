@@ -37,6 +37,19 @@ FA_COMPENSATED = 4
 FA_TEST_WAIT_EXPIRES = 0x80000000
 FA_NOALLOC_MAX_ELEMS = 1 << 22
 
+FA_ACT_NONE = 0
+FA_ACT_RELU = 1
+FA_ACT_GELU = 2
+FA_ACT_SILU = 3
+FA_TRANS_A = 1
+FA_TRANS_B = 2
+FA_DISTILL_MAX_CLIENTS = 16
+FA_DISTILL_MAX_TOPK = 2048
+
+ACTS = {"none": FA_ACT_NONE, "relu": FA_ACT_RELU, "gelu": FA_ACT_GELU, "silu": FA_ACT_SILU,
+        FA_ACT_NONE: FA_ACT_NONE, FA_ACT_RELU: FA_ACT_RELU, FA_ACT_GELU: FA_ACT_GELU,
+        FA_ACT_SILU: FA_ACT_SILU}
+
 DTYPES = {"f32": FA_F32, "bf16": FA_BF16, FA_F32: FA_F32, FA_BF16: FA_BF16}
 
 
@@ -59,6 +72,54 @@ class fa_stats(ctypes.Structure):
 class fa_partition_opts(ctypes.Structure):
     _fields_ = [("w_time", ctypes.c_double), ("w_energy", ctypes.c_double),
                 ("ema_alpha", ctypes.c_double), ("deadband", ctypes.c_double)]
+
+
+class fa_work_opts(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("timeout_ms", ctypes.c_uint32),
+                ("workspace_bytes", ctypes.c_uint64), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class fa_work_stats(ctypes.Structure):
+    _fields_ = [("kernel_launches", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class fa_product_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("dtype_in", ctypes.c_int32),
+                ("dtype_out", ctypes.c_int32), ("act", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("m", ctypes.c_uint64), ("n", ctypes.c_uint64), ("k", ctypes.c_uint64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_uint64),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_uint64), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_uint64),
+                ("out", ctypes.c_void_p), ("ldo", ctypes.c_uint64), ("pre", ctypes.c_void_p),
+                ("alpha", ctypes.c_double), ("beta", ctypes.c_double)]
+
+
+class fa_product_backward_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("dtype_in", ctypes.c_int32),
+                ("dtype_dout", ctypes.c_int32), ("dtype_grad", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("m", ctypes.c_uint64), ("n", ctypes.c_uint64), ("k", ctypes.c_uint64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_uint64),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_uint64),
+                ("dout", ctypes.c_void_p), ("ldd", ctypes.c_uint64),
+                ("pre", ctypes.c_void_p), ("ldp", ctypes.c_uint64),
+                ("d_a", ctypes.c_void_p), ("ldda", ctypes.c_uint64),
+                ("d_b", ctypes.c_void_p), ("lddb", ctypes.c_uint64),
+                ("d_bias", ctypes.c_void_p), ("alpha", ctypes.c_double)]
+
+
+class fa_distill_client(ctypes.Structure):
+    _fields_ = [("index", ctypes.c_void_p), ("value", ctypes.c_void_p), ("topk", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("weight", ctypes.c_double)]
+
+
+class fa_distill_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("n_clients", ctypes.c_uint32), ("dtype", ctypes.c_int32),
+                ("dtype_value", ctypes.c_int32), ("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint64),
+                ("logits", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("clients", ctypes.c_void_p),
+                ("temperature", ctypes.c_double), ("row_weight", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("ldg", ctypes.c_uint64)]
 
 
 class FedAvgError(RuntimeError):
@@ -108,6 +169,16 @@ def lib():
         L.fa_aggregate_noalloc_status.restype = i32
         L.fa_partition_plan.argtypes = [u32, vp, vp, vp, vp, vp, ctypes.POINTER(fa_partition_opts), vp]
         L.fa_partition_plan.restype = i32
+        L.fa_work_open.argtypes = [ctypes.POINTER(fa_work_opts), ctypes.POINTER(vp)]
+        L.fa_work_close.argtypes = [vp]
+        L.fa_work_sync.argtypes = [vp]
+        L.fa_work_get_stats.argtypes = [vp, ctypes.POINTER(fa_work_stats)]
+        L.fa_work_last_error.argtypes = [vp]
+        L.fa_work_last_error.restype = ctypes.c_char_p
+        L.fa_product.argtypes = [vp, ctypes.POINTER(fa_product_args), vp]
+        L.fa_product_backward.argtypes = [vp, ctypes.POINTER(fa_product_backward_args), vp]
+        L.fa_distill_loss.argtypes = [vp, ctypes.POINTER(fa_distill_args), vp]
+        L.fa_distill_grad.argtypes = [vp, ctypes.POINTER(fa_distill_args), vp]
         L.fa_strerror.argtypes = [i32]
         L.fa_strerror.restype = ctypes.c_char_p
         L.fa_last_error.argtypes = [vp]
@@ -115,7 +186,9 @@ def lib():
         for name in ("fa_open", "fa_accumulate", "fa_accumulate_batch", "fa_accumulate_keys",
                      "fa_accumulate_final", "fa_finalize",
                      "fa_finalize_apply", "fa_reduce_resident", "fa_reduce_subsets", "fa_reset",
-                     "fa_close", "fa_key_total", "fa_sync", "fa_get_stats"):
+                     "fa_close", "fa_key_total", "fa_sync", "fa_get_stats", "fa_work_open", "fa_work_close",
+                     "fa_work_sync", "fa_work_get_stats", "fa_product", "fa_product_backward",
+                     "fa_distill_loss", "fa_distill_grad"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -345,3 +418,97 @@ def fa_partition_plan(time_s, energy_j, samples, ema_tau=None, ema_eps=None, w_t
     _check(lib().fa_partition_plan(m, t.ctypes.data, e.ctypes.data, n.ctypes.data, tau.ctypes.data,
                                    eps.ctypes.data, ctypes.byref(o), out.ctypes.data))
     return [int(v) for v in out], tau.tolist(), eps.tolist()
+
+
+# ---------------------------------------------------------------- training operators
+def _check_work(status: int, work):
+    if status != FA_OK:
+        raise FedAvgError(status, fa_work_last_error(work))
+
+
+def fa_work_last_error(work) -> str:
+    r = lib().fa_work_last_error(work)
+    return r.decode() if r else ""
+
+
+def fa_work_open(timeout_ms=0, workspace_bytes=0, flags=0):
+    """A work handle on the current device: what fa_product, fa_product_backward,
+    fa_distill_loss and fa_distill_grad share (workspace, error word, order of calls)."""
+    opts = fa_work_opts(ctypes.sizeof(fa_work_opts), timeout_ms, workspace_bytes, flags, 0)
+    work = ctypes.c_void_p()
+    _check(lib().fa_work_open(ctypes.byref(opts), ctypes.byref(work)))
+    return work
+
+
+def fa_work_close(work):
+    _check_work(lib().fa_work_close(work), work)
+
+
+def fa_work_sync(work):
+    """Wait (bounded) for the handle's work; raises what its kernels reported."""
+    _check_work(lib().fa_work_sync(work), work)
+
+
+def fa_work_get_stats(work) -> dict:
+    st = fa_work_stats()
+    _check_work(lib().fa_work_get_stats(work, ctypes.byref(st)), work)
+    return {f: getattr(st, f) for f, _ in fa_work_stats._fields_}
+
+
+def fa_product(work, m, n, k, a, lda, b, ldb, out, ldo, dtype_in, dtype_out, trans_a=False,
+               trans_b=False, alpha=1.0, bias=None, act="none", residual=None, ldr=0, beta=1.0,
+               pre=None, stream=None):
+    """out[m,n] = act(alpha * op(a) . op(b) + bias) + beta * residual.  a is [m,k] (trans_a:
+    stored [k,m]), b is [k,n] (trans_b: stored [n,k], a linear layer's weight); `pre`, if
+    given, receives the value before the activation (stride ldo)."""
+    args = fa_product_args(ctypes.sizeof(fa_product_args), bool(trans_a) | bool(trans_b) << 1,
+                           DTYPES[dtype_in], DTYPES[dtype_out], ACTS[act], 0, m, n, k, _ptr(a), lda,
+                           _ptr(b), ldb, _ptr(bias), _ptr(residual), ldr, _ptr(out), ldo, _ptr(pre),
+                           alpha, beta)
+    _check_work(lib().fa_product(work, args, _stream(stream)), work)
+
+
+def fa_product_backward(work, m, n, k, a, lda, b, ldb, dout, ldd, d_a, ldda, d_b, lddb, dtype_in,
+                        dtype_dout, dtype_grad, trans_a=False, trans_b=False, alpha=1.0, act="none",
+                        pre=None, ldp=0, d_bias=None, stream=None):
+    """Gradients of fa_product with respect to a, b and the bias (None: not wanted), from
+    dout and -- unless act is "none" -- the kept `pre`; each stored like its operand."""
+    args = fa_product_backward_args(
+        ctypes.sizeof(fa_product_backward_args), bool(trans_a) | bool(trans_b) << 1, DTYPES[dtype_in],
+        DTYPES[dtype_dout], DTYPES[dtype_grad], ACTS[act], m, n, k, _ptr(a), lda, _ptr(b), ldb,
+        _ptr(dout), ldd, _ptr(pre), ldp, _ptr(d_a), ldda, _ptr(d_b), lddb, _ptr(d_bias), alpha)
+    _check_work(lib().fa_product_backward(work, args, _stream(stream)), work)
+
+
+def distill_lists(index, value, topk, weights, dtype_value="f32"):
+    """The clients' top-logit lists for fa_distill_loss and fa_distill_grad, marshalled once:
+    per client its index array [rows, topk] (int32, negative: unused), its value array, its
+    topk and its weight (sample count).  The arrays are kept alive by the result."""
+    _same_length(index=index, value=value, topk=topk, weights=weights)
+    n = len(index)
+    arr = (fa_distill_client * max(n, 1))()
+    for c, i, v, t, w in zip(arr, index, value, topk, weights):
+        c.index, c.value, c.topk, c.weight = _ptr(i), _ptr(v), t, w
+    return arr, n, DTYPES[dtype_value], (list(index), list(value))
+
+
+def _distill_args(rows, vocab, logits, ld, dtype, lists, temperature, row_weight, loss, lse, grad, ldg):
+    return fa_distill_args(ctypes.sizeof(fa_distill_args), lists[1], DTYPES[dtype], lists[2], rows, vocab,
+                           _ptr(logits), ld, ctypes.addressof(lists[0]), temperature, _ptr(row_weight),
+                           _ptr(loss), _ptr(lse), _ptr(grad), ldg)
+
+
+def fa_distill_loss(work, rows, vocab, logits, ld, dtype, lists, temperature, row_weight, loss,
+                    lse=None, stream=None):
+    """Per-row distillation loss of the student's logits from the clients' lists (a
+    distill_lists result), and optionally the rows' log sum exp(z / T) for the gradient."""
+    args = _distill_args(rows, vocab, logits, ld, dtype, lists, temperature, row_weight, loss, lse, None, 0)
+    _check_work(lib().fa_distill_loss(work, args, _stream(stream)), work)
+
+
+def fa_distill_grad(work, rows, vocab, logits, ld, dtype, lists, temperature, row_weight, lse, loss, grad,
+                    ldg, stream=None):
+    """Gradient of the rows' losses with respect to the logits (grad may be logits itself).
+    lse: kept by fa_distill_loss, or None to compute it here; loss: written unless None."""
+    args = _distill_args(rows, vocab, logits, ld, dtype, lists, temperature, row_weight, loss, lse, grad, ldg)
+    _check_work(lib().fa_distill_grad(work, args, _stream(stream)), work)

@@ -1,0 +1,61 @@
+// Matrix products with bias, activation and residual in their epilogue, and what their
+// gradients need: the launch interface (internal to the library).
+//
+//   out[m,n] = act(alpha * sum_k A(m,k) B(k,n) + bias[n]) + beta * residual[m,n]
+//
+// dtype codes as in kernels.cuh: 0 = fp32, 1 = bf16.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace fa {
+
+// One operand: element (x, kk) -- x is m of A or n of B -- at p[x * ld + kk] if kmajor
+// (the summed index runs along a row), else at p[kk * ld + x].
+struct ProdOperand {
+    const void* p;
+    uint64_t ld;
+    int dtype;
+    bool kmajor;
+};
+
+struct ProdEpilogue {
+    float alpha, beta;
+    const void* bias;       // [n] of bias_dtype, or nullptr
+    const void* res;        // [m,n] of out_dtype, or nullptr; may be out
+    void* out;              // [m,n] of out_dtype
+    void* pre;              // [m,n] of out_dtype with stride ldo, or nullptr
+    uint64_t ldr, ldo;
+    int bias_dtype, out_dtype, act;
+};
+
+struct ProdArgs {
+    uint32_t m, n, k;
+    ProdOperand a, b;
+    ProdEpilogue e;
+};
+
+// Any types, strides and sizes, plain fp32 arithmetic.
+cudaError_t launch_product_plain(const ProdArgs& p, cudaStream_t stream);
+
+// dz[m,n] = dout * act'(pre) in fp32, written as fp32 (dz == nullptr: not written), and
+// its column sums over blocks of kColRows rows to part[ceil(m / kColRows)][n]
+// (part == nullptr: none).
+constexpr uint32_t kColRows = 64;
+struct ActGradArgs {
+    uint32_t m, n;
+    const void* dout;
+    const void* pre;        // nullptr: act is none
+    uint64_t ldd, ldp;
+    int dtype, act;
+    float* dz;              // [m][n]
+    float* part;
+};
+cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream);
+
+// out[n] = sum over blocks of part[blocks][n], in block order, rounded to out_dtype.
+cudaError_t launch_col_sum(const float* part, uint32_t blocks, uint32_t n, void* out, int out_dtype,
+                           cudaStream_t stream);
+
+}  // namespace fa

@@ -1,0 +1,530 @@
+// Work handles and the server-side training operators (declared in include/fedavg.h): argument
+// checks, workspace, order of a handle's calls, launches.
+#include <fedavg.h>
+
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <algorithm>
+#include <chrono>
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+#include <new>
+#include <string>
+#include <thread>
+
+#include "distill.cuh"
+#include "kernels.cuh"
+#include "product.cuh"
+
+struct fa_work {
+    std::mutex mu;
+    int device = 0;
+    uint32_t timeout_ms = 60000;
+    uint32_t flags = 0;
+    uint8_t* ws = nullptr;               // the workspace shared by the handle's calls
+    uint64_t ws_bytes = 0;
+    cudaEvent_t chain = nullptr;         // recorded after the last queued call
+    bool chain_valid = false;
+    unsigned long long chain_stream_id = 0;
+    unsigned int* err_dev = nullptr;     // device error word (kernels OR bits in)
+    unsigned int* err_host = nullptr;    // pinned copy
+    cudaStream_t err_stream = nullptr;
+    cudaEvent_t err_ev = nullptr;
+    fa_work_stats stats{};
+    std::string err;
+};
+
+namespace {
+
+struct Range {
+    explicit Range(const char* name) { nvtxRangePushA(name); }
+    ~Range() { nvtxRangePop(); }
+};
+
+class DeviceGuard {
+public:
+    explicit DeviceGuard(int dev) {
+        if (cudaGetDevice(&prev_) == cudaSuccess && prev_ != dev) restore_ = cudaSetDevice(dev) == cudaSuccess;
+    }
+    ~DeviceGuard() {
+        if (restore_) cudaSetDevice(prev_);
+    }
+
+private:
+    int prev_ = 0;
+    bool restore_ = false;
+};
+
+fa_status fail(fa_work* w, fa_status s, const std::string& what) {
+    w->err = what;
+    const char* v = std::getenv("FA_LOG");
+    if (v != nullptr && v[0] != '\0' && std::strcmp(v, "0") != 0)
+        std::fprintf(stderr, "[fedavg] %s: %s\n", fa_strerror(s), what.c_str());
+    return s;
+}
+
+fa_status cuda_fail(fa_work* w, cudaError_t e, const char* where) {
+    cudaGetLastError();
+    return fail(w, e == cudaErrorMemoryAllocation ? FA_ERR_NOMEM : FA_ERR_CUDA,
+                std::string(where) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
+}
+
+#define FW_CUDA(w, call)                                       \
+    do {                                                       \
+        const cudaError_t e_ = (call);                         \
+        if (e_ != cudaSuccess) return cuda_fail(w, e_, #call); \
+    } while (0)
+
+fa_status wait_event(fa_work* w, cudaEvent_t ev, const char* what) {
+    const auto t0 = std::chrono::steady_clock::now();
+    for (uint32_t spins = 0;; ++spins) {
+        const cudaError_t e = cudaEventQuery(ev);
+        if (e == cudaSuccess) return FA_OK;
+        if (e != cudaErrorNotReady) return cuda_fail(w, e, what);
+        const auto ms =
+            std::chrono::duration_cast<std::chrono::milliseconds>(std::chrono::steady_clock::now() - t0).count();
+        if (ms > static_cast<long long>(w->timeout_ms))
+            return fail(w, FA_ERR_TIMEOUT, std::string(what) + ": no completion within timeout_ms");
+        if (spins < 64)
+            std::this_thread::yield();
+        else
+            std::this_thread::sleep_for(std::chrono::microseconds(50));
+    }
+}
+
+bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(s, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
+}
+
+// Make `s` wait for the handle's earlier calls.  Captured work is ordered by the stream
+// its graph is replayed on.
+fa_status chain_in(fa_work* w, cudaStream_t s, bool capture) {
+    if (!w->chain_valid || capture) return FA_OK;
+    unsigned long long id = 0;
+    FW_CUDA(w, cudaStreamGetId(s, &id));
+    if (id != w->chain_stream_id) FW_CUDA(w, cudaStreamWaitEvent(s, w->chain, 0));
+    return FA_OK;
+}
+
+fa_status chain_out(fa_work* w, cudaStream_t s, bool capture) {
+    if (capture) return FA_OK;
+    FW_CUDA(w, cudaEventRecord(w->chain, s));
+    FW_CUDA(w, cudaStreamGetId(s, &w->chain_stream_id));
+    w->chain_valid = true;
+    return FA_OK;
+}
+
+// At least `bytes` of workspace.  Growing waits for the handle's queued calls, which may
+// still use the old one.
+fa_status ensure_ws(fa_work* w, uint64_t bytes, bool capture) {
+    if (bytes <= w->ws_bytes) return FA_OK;
+    if (capture)
+        return fail(w, FA_ERR_STATE, "the workspace would have to grow during capture: run the call once before, "
+                                     "or open the handle with workspace_bytes");
+    if (w->chain_valid) {
+        const fa_status r = wait_event(w, w->chain, "workspace growth");
+        if (r != FA_OK) return r;
+    }
+    bytes = (bytes + (1ull << 21) - 1) >> 21 << 21;
+    if (w->ws) FW_CUDA(w, cudaFree(w->ws));
+    w->ws = nullptr;
+    w->ws_bytes = 0;
+    FW_CUDA(w, cudaMalloc(reinterpret_cast<void**>(&w->ws), bytes));
+    w->ws_bytes = bytes;
+    w->stats.workspace_bytes = bytes;
+    return FA_OK;
+}
+
+// A tensor the kernels read or write: in this device's memory.
+fa_status check_ptr(fa_work* w, const void* p, const char* name) {
+    if (p == nullptr) return fail(w, FA_ERR_ARG, std::string(name) + " is NULL");
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(w, FA_ERR_ARG, std::string(name) + " is not device memory");
+    }
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
+        return fail(w, FA_ERR_ARG, std::string(name) + " is not device memory");
+    if (at.type == cudaMemoryTypeDevice && at.device != w->device)
+        return fail(w, FA_ERR_ARG, std::string(name) + " is on another device");
+    return FA_OK;
+}
+
+bool dtype_ok(int32_t d) { return d == FA_F32 || d == FA_BF16; }
+uint64_t size_of(int32_t d) { return d == FA_F32 ? 4 : 2; }
+int code_of(int32_t d) { return d == FA_F32 ? 0 : 1; }
+
+// A matrix argument: rows of `width` elements `ld` apart, `rows` of them.
+fa_status check_mat(fa_work* w, const void* p, uint64_t rows, uint64_t width, uint64_t ld, int32_t dt,
+                    const char* name) {
+    if (rows == 0 || width == 0) return FA_OK;      // not read
+    if (ld < width) return fail(w, FA_ERR_RANGE, std::string(name) + ": stride shorter than a row");
+    if (ld >> 40) return fail(w, FA_ERR_RANGE, std::string(name) + ": stride of 2^40 or more");
+    if (reinterpret_cast<uintptr_t>(p) % size_of(dt))
+        return fail(w, FA_ERR_ARG, std::string(name) + " is not aligned to its element type");
+    return check_ptr(w, p, name);
+}
+
+bool overlap(const void* p, uint64_t prows, uint64_t pwidth, uint64_t pld, uint64_t ps, const void* q, uint64_t qrows,
+             uint64_t qwidth, uint64_t qld, uint64_t qs) {
+    if (!p || !q || !prows || !pwidth || !qrows || !qwidth) return false;
+    const uintptr_t p0 = reinterpret_cast<uintptr_t>(p), q0 = reinterpret_cast<uintptr_t>(q);
+    const uintptr_t p1 = p0 + ((prows - 1) * pld + pwidth) * ps, q1 = q0 + ((qrows - 1) * qld + qwidth) * qs;
+    return p0 < q1 && q0 < p1;
+}
+
+constexpr uint64_t kMaxSize = 1ull << 31;
+
+fa_status launched(fa_work* w, cudaError_t e, const char* what) {
+    if (e != cudaSuccess) return cuda_fail(w, e, what);
+    w->stats.kernel_launches++;
+    return FA_OK;
+}
+
+fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
+    if (p.flags & ~(FA_TRANS_A | FA_TRANS_B)) return fail(w, FA_ERR_ARG, "unknown flag");
+    if (!dtype_ok(p.dtype_in) || !dtype_ok(p.dtype_out)) return fail(w, FA_ERR_DTYPE, "dtype");
+    if (p.act < FA_ACT_NONE || p.act > FA_ACT_SILU) return fail(w, FA_ERR_ARG, "unknown activation");
+    if (!std::isfinite(p.alpha) || !std::isfinite(p.beta)) return fail(w, FA_ERR_ARG, "alpha or beta not finite");
+    if (p.m >= kMaxSize || p.n >= kMaxSize || p.k >= kMaxSize)
+        return fail(w, FA_ERR_RANGE, "a size of 2^31 or more");
+    if (p.m == 0 || p.n == 0) return FA_OK;
+    const bool ta = p.flags & FA_TRANS_A, tb = p.flags & FA_TRANS_B;
+    const uint64_t ar = ta ? p.k : p.m, aw = ta ? p.m : p.k, br = tb ? p.n : p.k, bw = tb ? p.k : p.n;
+    const uint64_t si = size_of(p.dtype_in), so = size_of(p.dtype_out);
+    const void* res = p.beta != 0.0 ? p.residual : nullptr;
+    fa_status r = check_mat(w, p.a, ar, aw, p.lda, p.dtype_in, "a");
+    if (r == FA_OK) r = check_mat(w, p.b, br, bw, p.ldb, p.dtype_in, "b");
+    if (r == FA_OK) r = check_mat(w, p.out, p.m, p.n, p.ldo, p.dtype_out, "out");
+    if (r == FA_OK && p.bias) r = check_mat(w, p.bias, 1, p.n, p.n, p.dtype_in, "bias");
+    if (r == FA_OK && res) r = check_mat(w, res, p.m, p.n, p.ldr, p.dtype_out, "residual");
+    if (r == FA_OK && p.pre) r = check_mat(w, p.pre, p.m, p.n, p.ldo, p.dtype_out, "pre");
+    if (r != FA_OK) return r;
+    for (const void* o : {static_cast<const void*>(p.out), static_cast<const void*>(p.pre)})
+        if (overlap(o, p.m, p.n, p.ldo, so, p.a, ar, aw, p.lda, si) ||
+            overlap(o, p.m, p.n, p.ldo, so, p.b, br, bw, p.ldb, si) ||
+            overlap(o, p.m, p.n, p.ldo, so, p.bias, 1, p.n, p.n, si))
+            return fail(w, FA_ERR_ARG, "an output overlaps a, b or bias");
+    if (overlap(p.out, p.m, p.n, p.ldo, so, p.pre, p.m, p.n, p.ldo, so))
+        return fail(w, FA_ERR_ARG, "out overlaps pre");
+    if (res && overlap(p.pre, p.m, p.n, p.ldo, so, res, p.m, p.n, p.ldr, so))
+        return fail(w, FA_ERR_ARG, "pre overlaps residual");
+    if (res && !(res == p.out && p.ldr == p.ldo) && overlap(p.out, p.m, p.n, p.ldo, so, res, p.m, p.n, p.ldr, so))
+        return fail(w, FA_ERR_ARG, "out overlaps residual without being it");
+    const bool cap = capturing(s);
+    r = chain_in(w, s, cap);
+    if (r != FA_OK) return r;
+    fa::ProdArgs q{};
+    q.m = static_cast<uint32_t>(p.m);
+    q.n = static_cast<uint32_t>(p.n);
+    q.k = static_cast<uint32_t>(p.k);
+    q.a = {p.a, p.lda, code_of(p.dtype_in), !ta};
+    q.b = {p.b, p.ldb, code_of(p.dtype_in), tb};
+    q.e = {static_cast<float>(p.alpha), static_cast<float>(p.beta), p.bias, res, p.out, p.pre, p.ldr, p.ldo,
+           code_of(p.dtype_in), code_of(p.dtype_out), p.act};
+    r = launched(w, fa::launch_product_plain(q, s), "product");
+    if (r != FA_OK) return r;
+    return chain_out(w, s, cap);
+}
+
+fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStream_t s) {
+    if (p.flags & ~(FA_TRANS_A | FA_TRANS_B)) return fail(w, FA_ERR_ARG, "unknown flag");
+    if (!dtype_ok(p.dtype_in) || !dtype_ok(p.dtype_dout) || !dtype_ok(p.dtype_grad))
+        return fail(w, FA_ERR_DTYPE, "dtype");
+    if (p.act < FA_ACT_NONE || p.act > FA_ACT_SILU) return fail(w, FA_ERR_ARG, "unknown activation");
+    if (!std::isfinite(p.alpha)) return fail(w, FA_ERR_ARG, "alpha not finite");
+    if (p.m >= kMaxSize || p.n >= kMaxSize || p.k >= kMaxSize)
+        return fail(w, FA_ERR_RANGE, "a size of 2^31 or more");
+    const bool ta = p.flags & FA_TRANS_A, tb = p.flags & FA_TRANS_B;
+    const bool act = p.act != FA_ACT_NONE;
+    const uint64_t ar = ta ? p.k : p.m, aw = ta ? p.m : p.k, br = tb ? p.n : p.k, bw = tb ? p.k : p.n;
+    const uint64_t si = size_of(p.dtype_in), sd = size_of(p.dtype_dout), sg = size_of(p.dtype_grad);
+    fa_status r = check_mat(w, p.dout, p.m, p.n, p.ldd, p.dtype_dout, "dout");
+    if (r == FA_OK && act) r = check_mat(w, p.pre, p.m, p.n, p.ldp, p.dtype_dout, "pre");
+    if (r == FA_OK && p.d_b) r = check_mat(w, p.a, ar, aw, p.lda, p.dtype_in, "a");
+    if (r == FA_OK && p.d_a) r = check_mat(w, p.b, br, bw, p.ldb, p.dtype_in, "b");
+    if (r == FA_OK && p.d_a) r = check_mat(w, p.d_a, ar, aw, p.ldda, p.dtype_grad, "d_a");
+    if (r == FA_OK && p.d_b) r = check_mat(w, p.d_b, br, bw, p.lddb, p.dtype_grad, "d_b");
+    if (r == FA_OK && p.d_bias) r = check_mat(w, p.d_bias, 1, p.n, p.n, p.dtype_grad, "d_bias");
+    if (r != FA_OK) return r;
+    const struct {
+        const void* p;
+        uint64_t rows, width, ld, size;
+        bool out;
+    } t[] = {{p.d_a, ar, aw, p.ldda, sg, true}, {p.d_b, br, bw, p.lddb, sg, true}, {p.d_bias, 1, p.n, p.n, sg, true},
+             {p.d_b ? p.a : nullptr, ar, aw, p.lda, si, false}, {p.d_a ? p.b : nullptr, br, bw, p.ldb, si, false},
+             {p.dout, p.m, p.n, p.ldd, sd, false}, {act ? p.pre : nullptr, p.m, p.n, p.ldp, sd, false}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (overlap(t[i].p, t[i].rows, t[i].width, t[i].ld, t[i].size, t[j].p, t[j].rows, t[j].width, t[j].ld,
+                        t[j].size))
+                return fail(w, FA_ERR_ARG, "a gradient overlaps another tensor of the call");
+    const bool want_a = p.d_a && p.m && p.k, want_b = p.d_b && p.n && p.k, want_bias = p.d_bias && p.n;
+    if (!want_a && !want_b && !want_bias) return FA_OK;
+    const uint32_t m = static_cast<uint32_t>(p.m), n = static_cast<uint32_t>(p.n), k = static_cast<uint32_t>(p.k);
+    const uint32_t blocks = (m + fa::kColRows - 1) / fa::kColRows;
+    const uint64_t dz_bytes = act ? p.m * p.n * 4 : 0, part_bytes = want_bias ? uint64_t(blocks) * p.n * 4 : 0;
+    const uint64_t dz_pad = (dz_bytes + 255) / 256 * 256;
+    const bool cap = capturing(s);
+    r = ensure_ws(w, dz_pad + part_bytes, cap);
+    if (r == FA_OK) r = chain_in(w, s, cap);
+    if (r != FA_OK) return r;
+    float* dz = act ? reinterpret_cast<float*>(w->ws) : nullptr;
+    float* part = want_bias ? reinterpret_cast<float*>(w->ws + dz_pad) : nullptr;
+    if ((dz || part) && m && n) {
+        const fa::ActGradArgs g{m, n, p.dout, act ? p.pre : nullptr, p.ldd, p.ldp, code_of(p.dtype_dout), p.act, dz, part};
+        r = launched(w, fa::launch_act_grad(g, s), "activation gradient");
+    }
+    if (r == FA_OK && want_bias)
+        r = launched(w, fa::launch_col_sum(part, blocks, n, p.d_bias, code_of(p.dtype_grad), s), "bias gradient");
+    const void* z = act ? static_cast<const void*>(dz) : p.dout;
+    const uint64_t ldz = act ? p.n : p.ldd;
+    const int zt = act ? 0 : code_of(p.dtype_dout), it = code_of(p.dtype_in);
+    const fa::ProdOperand z_m{z, ldz, zt, true}, z_n{z, ldz, zt, false};   // x = m (sum over n), x = n (sum over m)
+    fa::ProdEpilogue e{};
+    e.alpha = static_cast<float>(p.alpha);
+    e.out_dtype = code_of(p.dtype_grad);
+    if (r == FA_OK && want_a) {
+        const fa::ProdOperand b{p.b, p.ldb, it, !tb};      // x = k, sum over n
+        e.out = p.d_a;
+        e.ldo = p.ldda;
+        const fa::ProdArgs q = ta ? fa::ProdArgs{k, m, n, b, z_m, e} : fa::ProdArgs{m, k, n, z_m, b, e};
+        r = launched(w, fa::launch_product_plain(q, s), "gradient of a");
+    }
+    if (r == FA_OK && want_b) {
+        const fa::ProdOperand a{p.a, p.lda, it, ta};       // x = k, sum over m
+        e.out = p.d_b;
+        e.ldo = p.lddb;
+        const fa::ProdArgs q = tb ? fa::ProdArgs{n, k, m, z_n, a, e} : fa::ProdArgs{k, n, m, a, z_n, e};
+        r = launched(w, fa::launch_product_plain(q, s), "gradient of b");
+    }
+    if (r != FA_OK) return r;
+    return chain_out(w, s, cap);
+}
+
+fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStream_t s) {
+    if (!dtype_ok(p.dtype) || !dtype_ok(p.dtype_value)) return fail(w, FA_ERR_DTYPE, "dtype");
+    if (p.n_clients < 1 || p.n_clients > FA_DISTILL_MAX_CLIENTS || p.clients == nullptr)
+        return fail(w, FA_ERR_ARG, "1 to 16 clients are needed");
+    if (!std::isfinite(p.temperature) || !(p.temperature > 0.0) || !(static_cast<float>(p.temperature) > 0.0f) ||
+        !std::isfinite(1.0f / static_cast<float>(p.temperature)) || !std::isfinite(static_cast<float>(p.temperature)))
+        return fail(w, FA_ERR_ARG, "temperature must be a positive fp32 number");
+    if (p.rows >= kMaxSize || p.vocab >= kMaxSize || p.vocab == 0)
+        return fail(w, FA_ERR_RANGE, "rows or vocab out of range");
+    fa::DistillArgs a{};
+    uint64_t entries = 0;
+    double total = 0.0;
+    for (uint32_t j = 0; j < p.n_clients; ++j) {
+        const fa_distill_client& c = p.clients[j];
+        if (c.topk < 1 || c.topk > FA_DISTILL_MAX_TOPK) return fail(w, FA_ERR_RANGE, "topk out of range");
+        if (!std::isfinite(c.weight) || c.weight < 0.0 || c.weight > 16777216.0)
+            return fail(w, FA_ERR_WEIGHT, "client weight");
+        entries += c.topk;
+        total += c.weight;
+    }
+    if (entries > FA_DISTILL_MAX_TOPK) return fail(w, FA_ERR_RANGE, "more than 2048 list places per row");
+    if (p.rows == 0) return FA_OK;
+    fa_status r = check_mat(w, p.logits, p.rows, p.vocab, p.ld, p.dtype, "logits");
+    for (uint32_t j = 0; r == FA_OK && j < p.n_clients; ++j) {
+        const fa_distill_client& c = p.clients[j];
+        r = check_mat(w, c.index, p.rows, c.topk, c.topk, FA_F32, "index");
+        if (r == FA_OK) r = check_mat(w, c.value, p.rows, c.topk, c.topk, p.dtype_value, "value");
+        a.client[j] = {c.index, c.value, c.topk, static_cast<float>(c.weight),
+                       total > 0.0 ? static_cast<float>(c.weight / total) : 0.0f};
+    }
+    if (r == FA_OK && p.row_weight) r = check_mat(w, p.row_weight, 1, p.rows, p.rows, FA_F32, "row_weight");
+    if (r == FA_OK && (p.loss || !grad)) r = check_mat(w, p.loss, 1, p.rows, p.rows, FA_F32, "loss");
+    if (r == FA_OK && p.lse) r = check_mat(w, p.lse, 1, p.rows, p.rows, FA_F32, "lse");
+    if (r == FA_OK && grad) r = check_mat(w, p.grad, p.rows, p.vocab, p.ldg, p.dtype, "grad");
+    if (r != FA_OK) return r;
+    const uint64_t sz = size_of(p.dtype);
+    const bool inplace = grad && p.grad == p.logits && p.ldg == p.ld;
+    const struct {
+        const void* p;
+        uint64_t rows, width, ld, size;
+    } out[] = {{p.loss, 1, p.rows, p.rows, 4},
+               {grad ? nullptr : p.lse, 1, p.rows, p.rows, 4},
+               {grad ? p.grad : nullptr, p.rows, p.vocab, p.ldg, sz}};
+    for (int i = 0; i < 3; ++i) {
+        const auto& o = out[i];
+        auto hits = [&](const void* q, uint64_t rows, uint64_t width, uint64_t ld, uint64_t size) {
+            return overlap(o.p, o.rows, o.width, o.ld, o.size, q, rows, width, ld, size);
+        };
+        bool bad = (!(i == 2 && inplace) && hits(p.logits, p.rows, p.vocab, p.ld, sz)) ||
+                   hits(p.row_weight, 1, p.rows, p.rows, 4) || (grad && hits(p.lse, 1, p.rows, p.rows, 4));
+        for (uint32_t j = 0; !bad && j < p.n_clients; ++j)
+            bad = hits(p.clients[j].index, p.rows, p.clients[j].topk, p.clients[j].topk, 4) ||
+                  hits(p.clients[j].value, p.rows, p.clients[j].topk, p.clients[j].topk, size_of(p.dtype_value));
+        for (int k = 0; !bad && k < i; ++k) bad = hits(out[k].p, out[k].rows, out[k].width, out[k].ld, out[k].size);
+        if (bad) return fail(w, FA_ERR_ARG, "an output overlaps another tensor of the call");
+    }
+    const bool cap = capturing(s);
+    r = chain_in(w, s, cap);
+    if (r != FA_OK) return r;
+    a.logits = p.logits;
+    a.grad = grad ? p.grad : nullptr;
+    a.row_weight = p.row_weight;
+    a.loss = p.loss;
+    a.lse_in = grad ? p.lse : nullptr;
+    a.lse_out = grad ? nullptr : p.lse;
+    a.err = w->err_dev;
+    a.ld = p.ld;
+    a.ldg = p.ldg;
+    a.rows = static_cast<uint32_t>(p.rows);
+    a.vocab = static_cast<uint32_t>(p.vocab);
+    a.nclients = p.n_clients;
+    a.temperature = static_cast<float>(p.temperature);
+    a.inv_t = static_cast<float>(1.0 / p.temperature);
+    a.total = static_cast<float>(total);
+    a.dtype = code_of(p.dtype);
+    a.value_dtype = code_of(p.dtype_value);
+    r = launched(w, fa::launch_distill(a, s), grad ? "distillation gradient" : "distillation loss");
+    if (r != FA_OK) return r;
+    return chain_out(w, s, cap);
+}
+
+void free_work(fa_work* w) {
+    if (w->ws) cudaFree(w->ws);
+    if (w->chain) cudaEventDestroy(w->chain);
+    if (w->err_ev) cudaEventDestroy(w->err_ev);
+    if (w->err_stream) cudaStreamDestroy(w->err_stream);
+    if (w->err_host) cudaFreeHost(w->err_host);
+    if (w->err_dev) cudaFree(w->err_dev);
+    delete w;
+}
+
+// Every operator entry point: the argument struct copied up to the caller's size, the
+// handle locked, its device current, no exception past the C boundary.
+template <typename Args, typename F>
+fa_status enter(const char* name, fa_work* w, const Args* args, F f) {
+    if (!w) return FA_ERR_ARG;
+    try {
+        Range range(name);
+        std::lock_guard<std::mutex> lk(w->mu);
+        DeviceGuard dg(w->device);
+        w->err.clear();
+        if (!args || args->size < sizeof(Args)) return fail(w, FA_ERR_ARG, "args is NULL or args.size too small");
+        return f(*args);
+    } catch (const std::bad_alloc&) {
+        return FA_ERR_NOMEM;
+    } catch (...) {
+        return FA_ERR_INTERNAL;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_work_open(const fa_work_opts* opts, fa_work** out) {
+    if (out == nullptr) return FA_ERR_ARG;
+    *out = nullptr;
+    fa_work_opts o{};
+    if (opts) {
+        if (opts->size < sizeof(uint32_t) * 2) return FA_ERR_ARG;
+        std::memcpy(&o, opts, std::min<size_t>(opts->size, sizeof o));
+    }
+    if (o.flags & ~FA_TEST_WAIT_EXPIRES) return FA_ERR_ARG;
+    if (o.workspace_bytes >> 40) return FA_ERR_ARG;
+    fa_work* w = new (std::nothrow) fa_work;
+    if (!w) return FA_ERR_NOMEM;
+    if (o.timeout_ms) w->timeout_ms = o.timeout_ms;
+    w->flags = o.flags;
+    cudaError_t ce = cudaGetDevice(&w->device);
+    if (ce == cudaSuccess) ce = fa::prepare_distill();
+    if (ce == cudaSuccess) ce = cudaMalloc(reinterpret_cast<void**>(&w->err_dev), 256);
+    if (ce == cudaSuccess) ce = cudaMemset(w->err_dev, 0, 256);
+    if (ce == cudaSuccess) ce = cudaEventCreateWithFlags(&w->chain, cudaEventDisableTiming);
+    if (ce == cudaSuccess) ce = cudaEventCreateWithFlags(&w->err_ev, cudaEventDisableTiming);
+    if (ce == cudaSuccess) ce = cudaStreamCreateWithFlags(&w->err_stream, cudaStreamNonBlocking);
+    if (ce == cudaSuccess)
+        ce = cudaHostAlloc(reinterpret_cast<void**>(&w->err_host), sizeof(unsigned int), cudaHostAllocDefault);
+    if (ce == cudaSuccess && o.workspace_bytes) {
+        const uint64_t bytes = (o.workspace_bytes + (1ull << 21) - 1) >> 21 << 21;
+        ce = cudaMalloc(reinterpret_cast<void**>(&w->ws), bytes);
+        if (ce == cudaSuccess) w->ws_bytes = w->stats.workspace_bytes = bytes;
+    }
+    if (ce != cudaSuccess) {
+        cudaGetLastError();
+        free_work(w);
+        return ce == cudaErrorMemoryAllocation ? FA_ERR_NOMEM : FA_ERR_CUDA;
+    }
+    *out = w;
+    return FA_OK;
+}
+
+fa_status fa_work_close(fa_work* w) {
+    if (!w) return FA_OK;
+    {
+        std::lock_guard<std::mutex> lk(w->mu);
+        DeviceGuard dg(w->device);
+        if (w->chain_valid) {
+            const fa_status r = wait_event(w, w->chain, "fa_work_close");
+            if (r == FA_ERR_TIMEOUT) return r;
+        }
+    }
+    DeviceGuard dg(w->device);
+    free_work(w);
+    return FA_OK;
+}
+
+fa_status fa_work_sync(fa_work* w) {
+    if (!w) return FA_ERR_ARG;
+    std::lock_guard<std::mutex> lk(w->mu);
+    DeviceGuard dg(w->device);
+    w->err.clear();
+    if (w->chain_valid) {
+        const fa_status r = wait_event(w, w->chain, "fa_work_sync");
+        if (r != FA_OK) return r;
+    }
+    *w->err_host = 0;
+    FW_CUDA(w, cudaMemcpyAsync(w->err_host, w->err_dev, sizeof(unsigned int), cudaMemcpyDeviceToHost, w->err_stream));
+    FW_CUDA(w, cudaMemsetAsync(w->err_dev, 0, sizeof(unsigned int), w->err_stream));
+    FW_CUDA(w, cudaEventRecord(w->err_ev, w->err_stream));
+    const fa_status r = wait_event(w, w->err_ev, "fa_work_sync (error word)");
+    if (r != FA_OK) return r;
+    if (*w->err_host & fa::kErrWaitTimeout)
+        return fail(w, FA_ERR_INTERNAL, "a device-side wait gave up (bounded mbarrier wait): outputs are invalid");
+    if (*w->err_host & fa::kErrListIndex)
+        return fail(w, FA_ERR_RANGE, "a client's list named a vocabulary entry >= vocab (left out)");
+    return FA_OK;
+}
+
+fa_status fa_work_get_stats(fa_work* w, fa_work_stats* out) {
+    if (!w || !out) return FA_ERR_ARG;
+    std::lock_guard<std::mutex> lk(w->mu);
+    *out = w->stats;
+    return FA_OK;
+}
+
+const char* fa_work_last_error(const fa_work* w) { return w ? w->err.c_str() : ""; }
+
+fa_status fa_product(fa_work* w, const fa_product_args* args, void* stream) {
+    return enter("fa_product", w, args,
+                 [&](const fa_product_args& p) { return product_impl(w, p, static_cast<cudaStream_t>(stream)); });
+}
+
+fa_status fa_product_backward(fa_work* w, const fa_product_backward_args* args, void* stream) {
+    return enter("fa_product_backward", w, args, [&](const fa_product_backward_args& p) {
+        return backward_impl(w, p, static_cast<cudaStream_t>(stream));
+    });
+}
+
+fa_status fa_distill_loss(fa_work* w, const fa_distill_args* args, void* stream) {
+    return enter("fa_distill_loss", w, args, [&](const fa_distill_args& p) {
+        return distill_impl(w, p, false, static_cast<cudaStream_t>(stream));
+    });
+}
+
+fa_status fa_distill_grad(fa_work* w, const fa_distill_args* args, void* stream) {
+    return enter("fa_distill_grad", w, args, [&](const fa_distill_args& p) {
+        return distill_impl(w, p, true, static_cast<cudaStream_t>(stream));
+    });
+}
+
+}  // extern "C"
