@@ -17,7 +17,8 @@ SO = os.path.join(BUILD, "libfedavg.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["accumulate.cu", "reduce.cu", "gather.cu", "finalize.cu", "noalloc.cu", "fedavg.cpp",
-           "ledger.cpp", "partition.cpp", "gather_plan.cpp", "product_plain.cu", "distill.cu", "work.cpp"]
+           "ledger.cpp", "partition.cpp", "gather_plan.cpp", "product_plain.cu", "product_prep.cu", "product_tc.cu",
+           "distill.cu", "work.cpp"]
 
 
 def _common():

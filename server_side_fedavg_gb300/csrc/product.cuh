@@ -39,9 +39,17 @@ struct ProdArgs {
 // Any types, strides and sizes, plain fp32 arithmetic.
 cudaError_t launch_product_plain(const ProdArgs& p, cudaStream_t stream);
 
-// dz[m,n] = dout * act'(pre) in fp32, written as fp32 (dz == nullptr: not written), and
-// its column sums over blocks of kColRows rows to part[ceil(m / kColRows)][n]
-// (part == nullptr: none).
+// The products' operands where they are not as the tensor-core kernel reads them (bf16,
+// 16-byte aligned base and row stride): the matrix [rows][cols] as `planes` bf16 planes
+// [plane][rows][ldd], ldd a multiple of 8 -- one plane for bf16 sources, three for fp32:
+// x = x0 + x1 + x2, each term the remainder rounded to nearest, 24 bits in all.
+cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols, uint32_t planes, void* dst,
+                         uint64_t ldd, cudaStream_t stream);
+
+// dZ[m,n] = dout * act'(pre), computed in fp32 and written (dz != nullptr) with row stride
+// ldz as fp32 (dz_planes 0), rounded to bf16 (1) or as three bf16 planes (3), m * ldz
+// elements apart; and its column sums over blocks of kColRows rows, to
+// part[ceil(m / kColRows)][n] (part != nullptr).
 constexpr uint32_t kColRows = 64;
 struct ActGradArgs {
     uint32_t m, n;
@@ -49,7 +57,9 @@ struct ActGradArgs {
     const void* pre;        // nullptr: act is none
     uint64_t ldd, ldp;
     int dtype, act;
-    float* dz;              // [m][n]
+    void* dz;
+    uint64_t ldz;
+    int dz_planes;
     float* part;
 };
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream);

@@ -1,5 +1,4 @@
-// Products in plain fp32 arithmetic for any type, stride and size, and the elementwise
-// part of the gradients.
+// Products in plain fp32 arithmetic for any type, stride and size.
 #include "product_device.cuh"
 
 namespace fa {
@@ -56,33 +55,6 @@ __global__ void __launch_bounds__(256) product_plain_kernel(const __grid_constan
         }
 }
 
-// A block of kColRows rows and 256 columns per CTA: thread = column.
-__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a) {
-    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.n) return;
-    const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
-    for (uint32_t blk = blockIdx.y; blk < blocks; blk += gridDim.y) {
-        const uint32_t r0 = blk * kColRows, r1 = a.m - r0 < kColRows ? a.m : r0 + kColRows;
-        float sum = 0.0f;
-        for (uint32_t r = r0; r < r1; ++r) {
-            float d = elem(a.dout, r * a.ldd + c, a.dtype);
-            if (a.pre) d *= act_grad(a.act, elem(a.pre, r * a.ldp + c, a.dtype));
-            if (a.dz) a.dz[(uint64_t)r * a.n + c] = d;
-            sum += d;
-        }
-        if (a.part) a.part[(uint64_t)blk * a.n + c] = sum;
-    }
-}
-
-__global__ void __launch_bounds__(256) col_sum_kernel(const float* part, uint32_t blocks, uint32_t n, void* out,
-                                                      int out_dtype) {
-    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
-    float s = 0.0f;
-    for (uint32_t b = 0; b < blocks; ++b) s += part[(uint64_t)b * n + c];
-    put(out, c, out_dtype, s);
-}
-
 }  // namespace
 
 cudaError_t launch_product_plain(const ProdArgs& p, cudaStream_t stream) {
@@ -101,18 +73,6 @@ cudaError_t launch_product_plain(const ProdArgs& p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
-}
-
-cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream) {
-    const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
-    act_grad_kernel<<<dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, 0, stream>>>(a);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_col_sum(const float* part, uint32_t blocks, uint32_t n, void* out, int out_dtype,
-                           cudaStream_t stream) {
-    col_sum_kernel<<<(n + 255) / 256, 256, 0, stream>>>(part, blocks, n, out, out_dtype);
-    return cudaGetLastError();
 }
 
 }  // namespace fa

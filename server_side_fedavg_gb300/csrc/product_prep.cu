@@ -1,0 +1,156 @@
+// What goes before the products: operands laid out as bf16 planes, and the elementwise part
+// of the gradients with the bias gradient's column sums.  Streaming passes, bound by HBM.
+#include "product_device.cuh"
+
+namespace fa {
+
+namespace {
+
+// x as three bf16 terms: each the remainder so far rounded to nearest even, so that 24 bits
+// of x are kept.  A finite x that would round to infinity takes the largest finite bf16
+// first.  An infinity or NaN is the first term alone.
+__device__ __forceinline__ void split3(float x, uint16_t (&t)[3]) {
+    uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    if ((h & 0x7FFF) == 0x7F80 && isfinite(x)) h = (h & 0x8000) | 0x7F7F;
+    t[0] = h;
+    t[1] = t[2] = 0;
+    if (!isfinite(x)) return;
+    float r = x - __uint_as_float(static_cast<uint32_t>(h) << 16);     // exact
+    t[1] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
+    r -= __uint_as_float(static_cast<uint32_t>(t[1]) << 16);           // exact
+    t[2] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
+}
+
+// Eight values to each of the planes at element `at` (a multiple of 8 from a 16-byte
+// aligned base).
+__device__ __forceinline__ void store_planes(uint16_t* dst, uint64_t at, uint64_t plane, int planes,
+                                             const float (&x)[8]) {
+    if (planes == 1) {
+        store8_global<uint16_t>(dst, at, x);
+        return;
+    }
+    uint32_t w[3][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint16_t lo[3], hi[3];
+        split3(x[2 * i], lo);
+        split3(x[2 * i + 1], hi);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) w[p][i] = lo[p] | static_cast<uint32_t>(hi[p]) << 16;
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) st_v4u(dst + p * plane + at, make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]));
+}
+
+// Columns c .. c + 7 of a row of `cols` (those past its end as 0).
+__device__ __forceinline__ void load8(const void* p, uint64_t row_at, uint32_t c, uint32_t cols, int dt, bool vec,
+                                      float (&x)[8]) {
+    if (vec && c + 8 <= cols) {
+        if (dt)
+            plain_vec8(static_cast<const uint16_t*>(p) + row_at + c, x);
+        else
+            plain_vec8(static_cast<const float*>(p) + row_at + c, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = c + i < cols ? elem(p, row_at + c + i, dt) : 0.0f;
+    }
+}
+
+// Eight elements per thread and step, rows in turn.
+__global__ void __launch_bounds__(256) split_kernel(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols,
+                                                    int planes, uint16_t* dst, uint64_t ldd, bool vec) {
+    const uint64_t per = ldd / 8, all = per * rows, plane = rows * ldd;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
+        const uint64_t r = i / per;
+        const uint32_t c = static_cast<uint32_t>(i - r * per) * 8;
+        float x[8];
+        load8(src, r * ld, c, cols, dtype, vec, x);
+        store_planes(dst, r * ldd + c, plane, planes, x);
+    }
+}
+
+// A block of kColRows rows by 256 columns per CTA: a lane holds 8 columns, a warp every
+// eighth row; the column sums join over the warps in warp order.
+__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a, bool vd, bool vp, bool vz) {
+    __shared__ float sums[8][256];
+    const uint32_t c = blockIdx.x * 256 + threadIdx.x % 32 * 8, warp = threadIdx.x / 32;
+    const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
+    const uint64_t plane = a.m * a.ldz;
+    for (uint32_t blk = blockIdx.y; blk < blocks; blk += gridDim.y) {
+        float s[8] = {};
+        if (c < a.n)
+            for (uint32_t i = 0; i < kColRows / 8; ++i) {
+                const uint32_t r = blk * kColRows + warp + 8 * i;
+                if (r >= a.m) break;
+                float d[8];
+                load8(a.dout, r * a.ldd, c, a.n, a.dtype, vd, d);
+                if (a.pre) {
+                    float z[8];
+                    load8(a.pre, r * a.ldp, c, a.n, a.dtype, vp, z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] = c + j < a.n ? d[j] * act_grad(a.act, z[j]) : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] += d[j];
+                if (!a.dz) continue;
+                if (a.dz_planes) {
+                    store_planes(static_cast<uint16_t*>(a.dz), r * a.ldz + c, plane, a.dz_planes, d);
+                } else if (vz && c + 8 <= a.n) {
+                    store8_global<float>(a.dz, r * a.ldz + c, d);
+                } else {
+                    for (int j = 0; j < 8; ++j)
+                        if (c + j < a.n) static_cast<float*>(a.dz)[r * a.ldz + c + j] = d[j];
+                }
+            }
+        if (!a.part) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[warp][threadIdx.x % 32 * 8 + j] = s[j];
+        __syncthreads();
+        const uint32_t col = blockIdx.x * 256 + threadIdx.x;
+        if (col < a.n) {
+            float t = 0.0f;
+            for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+            a.part[static_cast<uint64_t>(blk) * a.n + col] = t;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(256) col_sum_kernel(const float* part, uint32_t blocks, uint32_t n, void* out,
+                                                      int out_dtype) {
+    const uint32_t c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= n) return;
+    float s = 0.0f;
+    for (uint32_t b = 0; b < blocks; ++b) s += part[static_cast<uint64_t>(b) * n + c];
+    put(out, c, out_dtype, s);
+}
+
+bool vec_ok(const void* p, uint64_t ld, int dtype) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (dtype ? 2 : 4) % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols, uint32_t planes, void* dst,
+                         uint64_t ldd, cudaStream_t stream) {
+    const uint64_t groups = ldd / 8 * rows, blocks = (groups + 255) / 256;
+    const uint32_t grid = blocks < 152 * 8 ? static_cast<uint32_t>(blocks) : 152 * 8;
+    split_kernel<<<grid, 256, 0, stream>>>(src, ld, dtype, rows, cols, planes, static_cast<uint16_t*>(dst), ldd,
+                                           vec_ok(src, ld, dtype));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream) {
+    const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
+    act_grad_kernel<<<dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, 0, stream>>>(
+        a, vec_ok(a.dout, a.ldd, a.dtype), vec_ok(a.pre, a.ldp, a.dtype), vec_ok(a.dz, a.ldz, 0));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_col_sum(const float* part, uint32_t blocks, uint32_t n, void* out, int out_dtype,
+                           cudaStream_t stream) {
+    col_sum_kernel<<<(n + 255) / 256, 256, 0, stream>>>(part, blocks, n, out, out_dtype);
+    return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -1,0 +1,707 @@
+// Products on the tensor cores (tcgen05): bf16 operands, fp32 accumulators in TMEM, operands
+// staged in shared memory by TMA, the epilogue fused.
+//
+//   acc[x,y] = sum over pairs (i, j) of planes, sum over kk of P_i(x,kk) Q_j(y,kk)
+//
+// An operand is 1 plane (bf16 as it is) or 3 (an fp32 operand as the sum of three bf16 terms,
+// 24 bits).  Of 3 x 3 planes the six products with i + j <= 2 are taken: the others are below
+// 2^-25 of the largest.  Smaller products come first, so that they meet a small accumulator.
+//
+// A CTA's tile is 128 rows of P (TMEM lanes) by kBN rows of Q (TMEM columns); with kCtas == 2
+// a pair of SMs holds 256 rows of P and each half of the Q rows (cta_group::2), which halves
+// the operand traffic from L2.  Warps 0-7 drain and finish tiles, warp 8 issues TMA loads,
+// warp 9 the MMAs.  TMEM holds two accumulators, so the next tile's (or chunk's) products run
+// while one is drained.
+//
+// kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates; over thousands of
+// terms that adds up to about 1e-5.  So the accumulator is emptied every chunk_kb blocks of 64
+// terms into registers, which sum with rounding to nearest.
+//
+// kSwap: Q (columns) holds the tokens and P the weights -- for few tokens, where the 128 lanes
+// are better filled with weights.  The output is then written column by column.
+//
+// splits > 1 (kCtas == 1): a cluster of `splits` CTAs divides the summed index; each puts its
+// part into its own shared memory, and each finishes a share of the tile, summing the parts
+// in rank order over distributed shared memory.
+#include "product_tc.cuh"
+#include "product_device.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kBK = 64;                    // summed elements per block: 128 bytes, one swizzle row
+constexpr int kDrainWarps = 8;
+// The pair kernel's drain form holds 128 sums per thread: three warpgroups, of which the
+// third (loads, MMAs, two idle warps) gives registers to the first two:
+// 128 x 72 + 256 x 216 = 384 x 168, what the block is launched with.
+template <int kBN, bool kDrain>
+constexpr bool kRegSplit = kDrain && kBN == 256;
+template <int kBN, bool kDrain>
+constexpr int kThreads = kRegSplit<kBN, kDrain> ? 384 : (kDrainWarps + 2) * 32;
+constexpr uint32_t kPBytes = 128 * kBK * 2;
+constexpr uint32_t kUnit = 32 * 32 * 4;    // a 32 x 32 block of fp32 partial results
+
+// ----------------------------------------------------------------- PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done;
+}
+
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Wait for a phase, acquiring at cluster scope (the arrivals may come from another CTA).
+// False where the cluster has given up (`gone` is set) or the wait has lasted kMaxWaitNs:
+// it then sets the flag of every CTA of the cluster, so that every role leaves.
+constexpr uint64_t kMaxWaitNs = 20ull * 1000 * 1000 * 1000;
+__device__ __forceinline__ void give_up(uint32_t gone, uint32_t ctas) {
+    for (uint32_t r = 0; r < ctas; ++r)
+        asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(ctas > 1 ? in_cta(gone, r) : gone) : "memory");
+}
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t gone, uint32_t ctas) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (bar_try(bar, parity)) return true;
+        if (i % 16) continue;
+        uint32_t g;
+        asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(g) : "r"(gone) : "memory");
+        if (g) return false;
+        if (t0 == 0) {
+            t0 = now_ns();
+        } else if (now_ns() - t0 > kMaxWaitNs) {
+            give_up(gone, ctas);
+            return false;
+        }
+    }
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                         uint32_t bar) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
+            "r"(static_cast<uint32_t>(add))
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
+            "r"(static_cast<uint32_t>(add))
+            : "memory");
+}
+
+// Arrive on `bar` (the same offset in both CTAs of a pair) when the MMAs issued so far are done.
+template <int kCtas>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+    if constexpr (kCtas == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+
+// 32 columns of this warp's 32 lanes; the values are there after tmem_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Four floats at `addr` of CTA q's shared memory; parts == 1: this CTA's.
+__device__ __forceinline__ float4 ld_part(uint32_t addr, uint32_t q, uint32_t parts) {
+    float4 v;
+    if (parts == 1)
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(in_cta(addr, q))
+                     : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle (version 1 of the format, layout type 2).
+// Summed index along the rows (K-major): groups of 8 rows are 1024 bytes apart.  Else
+// (MN-major): slabs of 64 x-elements are `slab` bytes apart, groups of 8 summed rows 1024.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool kmajor, uint32_t slab) {
+    const uint64_t lead = kmajor ? 1 : slab >> 4;
+    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | lead << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+
+// Swizzled place of float4 `j` (0..7) of row `r` in a 32 x 32 unit: writes by row and reads
+// of two adjacent float4 by four lanes of a row are both free of bank conflicts.
+__device__ __forceinline__ uint32_t unit_at(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+
+// ----------------------------------------------------------------- epilogue
+// Eight outputs of one row, columns c .. c + 7, from their sums: vectors where `vec`.
+__device__ __forceinline__ void finish8(const ProdEpilogue& e, const float (&s)[8], const float (&bias)[8],
+                                        const float (&res)[8], uint64_t row, uint32_t c, uint32_t cols, bool vec) {
+    float z[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = fmaf(e.alpha, s[i], bias[i]);
+    const uint64_t at = row * e.ldo + c;
+    if (e.act == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = z[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = act_fwd(e.act, z[i]);
+    }
+    if (e.res) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(e.beta, res[i], y[i]);
+    }
+    if (vec) {
+        if (e.pre) {
+            if (e.out_dtype)
+                store8_global<uint16_t>(e.pre, at, z);
+            else
+                store8_global<float>(e.pre, at, z);
+        }
+        if (e.out_dtype)
+            store8_global<uint16_t>(e.out, at, y);
+        else
+            store8_global<float>(e.out, at, y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) {
+                if (e.pre) put(e.pre, at + i, e.out_dtype, z[i]);
+                put(e.out, at + i, e.out_dtype, y[i]);
+            }
+    }
+}
+
+__device__ __forceinline__ void load_res8(const ProdEpilogue& e, float (&res)[8], uint64_t row, uint32_t c, uint32_t cols,
+                                          bool vec) {
+    if (!e.res) return;
+    const uint64_t at = row * e.ldr + c;
+    if (vec) {
+        if (e.out_dtype)
+            plain_vec8(static_cast<const uint16_t*>(e.res) + at, res);
+        else
+            plain_vec8(static_cast<const float*>(e.res) + at, res);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) res[i] = c + i < cols ? elem(e.res, at + i, e.out_dtype) : 0.0f;
+    }
+}
+
+// A 32 x 32 unit of sums at `unit` (of each of `parts` CTAs' shared memory; 1: this CTA's)
+// with its corner at (row0, col0): lane = 8 columns of rows lane / 4 + 8 i.
+__device__ __forceinline__ void finish_unit(const TcArgs& a, uint32_t unit, uint32_t parts, uint32_t row0, uint32_t col0) {
+    const int lane = threadIdx.x % 32;
+    const uint32_t c = col0 + (lane % 4) * 8;
+    if (c >= a.cols) return;
+    const bool vec = a.vec && c + 8 <= a.cols;
+    float bias[8] = {};
+    if (a.e.bias)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bias[i] = c + i < a.cols ? elem(a.e.bias, c + i, a.e.bias_dtype) : 0.0f;
+    float res[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = row0 + lane / 4 + 8 * i;
+        if (row < a.rows) load_res8(a.e, res[i], row, c, a.cols, vec);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = lane / 4 + 8 * i, row = row0 + r, j = (lane % 4) * 2;
+        if (row >= a.rows) continue;
+        float s[8] = {};
+        for (uint32_t q = 0; q < parts; ++q) {
+            const float4 u = ld_part(unit + unit_at(r, j), q, parts), v = ld_part(unit + unit_at(r, j + 1), q, parts);
+            s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
+            s[4] += v.x; s[5] += v.y; s[6] += v.z; s[7] += v.w;
+        }
+        finish8(a.e, s, bias, res[i], row, c, a.cols, vec);
+    }
+}
+
+// kSwap: lane = one output column (P row), the unit's columns = output rows.
+__device__ __forceinline__ void finish_unit_swapped(const TcArgs& a, uint32_t unit, uint32_t parts, uint32_t prow0,
+                                                    uint32_t qrow0, uint32_t qcount) {
+    const uint32_t lane = threadIdx.x % 32, col = prow0 + lane;
+    if (col >= a.cols) return;
+    const float bias = a.e.bias ? elem(a.e.bias, col, a.e.bias_dtype) : 0.0f;
+    for (uint32_t j = 0; j * 4 < qcount; ++j) {
+        float s[4] = {};
+        for (uint32_t q = 0; q < parts; ++q) {
+            const float4 u = ld_part(unit + unit_at(lane, j), q, parts);
+            s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t row = qrow0 + j * 4 + i;
+            if (row >= a.rows) break;
+            const float z = fmaf(a.e.alpha, s[i], bias);
+            const uint64_t at = row * a.e.ldo + col;
+            if (a.e.pre) put(a.e.pre, at, a.e.out_dtype, z);
+            float y = act_fwd(a.e.act, z);
+            if (a.e.res) y = fmaf(a.e.beta, elem(a.e.res, row * a.e.ldr + col, a.e.out_dtype), y);
+            put(a.e.out, at, a.e.out_dtype, y);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- kernel
+template <int kCtas, int kBN, bool kDrain, bool kSwap>
+__global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(const __grid_constant__ TcArgs a) {
+    constexpr int kQRows = kBN / kCtas;                     // rows of Q that this CTA loads
+    constexpr uint32_t kQBytes = kQRows * kBK * 2;
+    constexpr int kHalf = kBN >= 64 ? kBN / 2 : kBN;        // columns drained by one warp
+    constexpr int kHalves = kBN / kHalf;                    // warps sharing a lane quadrant
+    constexpr int kChunkCols = kHalf < 32 ? kHalf : 32;
+    constexpr int kChunks = kHalf / kChunkCols;
+    constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
+    extern __shared__ uint8_t dyn[];
+    __shared__ uint64_t bars[2 * kTcMaxStages + 4];
+    __shared__ uint32_t tmem_slot, gone_flag;
+    const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
+    const uint32_t full = smem_addr(&bars[0]), empty = smem_addr(&bars[kTcMaxStages]);
+    const uint32_t acc_full = smem_addr(&bars[2 * kTcMaxStages]), acc_empty = acc_full + 16;
+    const uint32_t stage_bytes = a.planes_p * kPBytes + a.planes_q * kQBytes;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = kCtas == 2 || a.splits > 1 ? cluster_rank() : 0;
+    const uint32_t split = kCtas == 2 ? 0 : rank;
+    const bool leader = kCtas == 1 || rank == 0;
+    const uint32_t gone = smem_addr(&gone_flag), ctas = kCtas == 2 ? 2 : a.splits;
+
+    if (warp == 8 && lane == 0) {
+        for (uint32_t s = 0; s < a.stages; ++s) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(acc_full + 8 * b, 1);
+            bar_init(acc_empty + 8 * b, kCtas * kHalves * 4);
+        }
+        gone_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc<kCtas>(smem_addr(&tmem_slot), kTmemCols);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (kCtas == 2 || a.splits > 1) cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_slot;
+
+    // this cluster's tiles, and this CTA's blocks of the summed index
+    const uint32_t group = kCtas == 2 ? 2 : a.splits;
+    const uint32_t first = blockIdx.x / group, step = gridDim.x / group;
+    const uint32_t kb0 = static_cast<uint64_t>(a.kblocks) * split / a.splits;
+    const uint32_t kb1 = static_cast<uint64_t>(a.kblocks) * (split + 1) / a.splits;
+    bool ok = true;                      // of this thread: no wait gave up
+
+    if (warp >= 8) {
+        if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8 && lane == 0) {
+            const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
+            uint32_t it = 0;
+            for (uint32_t t = first; ok && t < a.tiles; t += step) {
+                const TcTile tile = tc_tile(a, t);
+                const int32_t p0 = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0);
+                const int32_t q0 = tile.q * kBN + (kCtas == 2 ? rank * kQRows : 0);
+                for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % a.stages;
+                    if (it >= a.stages && !bar_wait(empty + 8 * s, (it / a.stages - 1) & 1, gone, ctas)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_expect(full + 8 * s, stage_bytes * kCtas);
+                    uint32_t dst = base + s * stage_bytes;
+                    const int32_t k0 = kb * kBK;
+                    for (int z = 0; z < static_cast<int>(a.planes_p); ++z, dst += kPBytes) {
+                        if (a.p_kmajor)
+                            tma_load<kCtas>(dst, &a.map_p, k0, p0, z, lead_full + 8 * s);
+                        else
+                            for (int h = 0; h < 2; ++h)
+                                tma_load<kCtas>(dst + h * 8192, &a.map_p, p0 + 64 * h, k0, z, lead_full + 8 * s);
+                    }
+                    for (int z = 0; z < static_cast<int>(a.planes_q); ++z, dst += kQBytes) {
+                        if (a.q_kmajor)
+                            tma_load<kCtas>(dst, &a.map_q, k0, q0, z, lead_full + 8 * s);
+                        else
+                            for (int h = 0; h < kQRows / 64; ++h)
+                                tma_load<kCtas>(dst + h * 8192, &a.map_q, q0 + 64 * h, k0, z, lead_full + 8 * s);
+                    }
+                }
+            }
+        } else if (warp == 9 && lane == 0 && leader) {
+            const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (a.p_kmajor ? 0u : 1u << 15) |
+                                   (a.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 | (128 * kCtas / 16) << 24;
+            const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
+            uint32_t it = 0, ch = 0;
+            for (uint32_t t = first; ok && t < a.tiles; t += step) {
+                for (uint32_t kb = kb0; ok && kb < kb1; ++ch) {
+                    const uint32_t b = ch & 1;
+                    if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, ctas)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t d = tmem + b * kBN;
+                    const uint32_t end = kDrain && kb1 - kb > a.chunk_kb ? kb + a.chunk_kb : kb1;
+                    bool add = false;
+                    for (; kb < end; ++kb, ++it) {
+                        const uint32_t s = it % a.stages;
+                        if (a.test_expire || !bar_wait(full + 8 * s, (it / a.stages) & 1, gone, ctas)) {
+                            ok = false;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint32_t at = base + s * stage_bytes;
+                        const uint32_t left = a.k - kb * kBK, steps = left >= kBK ? 4 : (left + 15) / 16;
+                        for (int sum = 2; sum >= 0; --sum)
+                            for (int i = 0; i <= sum; ++i) {
+                                const int j = sum - i;
+                                if (i >= static_cast<int>(a.planes_p) || j >= static_cast<int>(a.planes_q)) continue;
+                                const uint64_t dp = operand_desc(at + i * kPBytes, a.p_kmajor, 8192);
+                                const uint64_t dq =
+                                    operand_desc(at + a.planes_p * kPBytes + j * kQBytes, a.q_kmajor, 8192);
+                                for (uint32_t x = 0; x < steps; ++x) {
+                                    mma<kCtas>(d, dp + x * step_p, dq + x * step_q, idesc, add);
+                                    add = true;
+                                }
+                            }
+                        commit<kCtas>(empty + 8 * s);
+                    }
+                    if (ok) commit<kCtas>(acc_full + 8 * b);
+                }
+            }
+            if (!ok) {
+                // the loads in flight land before the CTA leaves
+                atomicOr(a.err, kErrWaitTimeout);
+                give_up(gone, ctas);
+                const uint32_t blocks = (kb1 - kb0) * ((a.tiles - first + step - 1) / step);
+                for (uint32_t n = 0; n < a.stages && it < blocks; ++n, ++it) {
+                    for (uint32_t i = 0; i < 1000 && !bar_try(full + 8 * (it % a.stages), (it / a.stages) & 1); ++i) {}
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp / 4 < kHalves) {
+        if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const uint32_t quad = warp % 4, half = warp / 4;
+        const uint32_t mine = tmem + (quad << 21) + half * kHalf;    // lane 32 quad, column half * kHalf
+        const uint32_t stage_unit = base + a.stages * stage_bytes + warp * kUnit;
+        const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty;
+        uint32_t ch = 0;
+        for (uint32_t t = first; ok && t < a.tiles; t += step) {
+            const TcTile tile = tc_tile(a, t);
+            const uint32_t prow = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0) + quad * 32;
+            const uint32_t qrow = tile.q * kBN + half * kHalf;
+            float acc[kDrain ? kHalf : 1];
+            if constexpr (kDrain) {
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) acc[i] = 0.0f;
+                for (uint32_t kb = kb0; kb < kb1; kb += a.chunk_kb, ++ch) {
+                    const uint32_t b = ch & 1;
+                    if (!bar_wait(acc_full + 8 * b, (ch / 2) & 1, gone, ctas)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        float v[kChunkCols];
+                        if constexpr (kChunkCols == 32)
+                            tmem_ld32(mine + b * kBN + c * 32, v);
+                        else
+                            tmem_ld16(mine + b * kBN, v);
+#pragma unroll
+                        for (int i = 0; i < kChunkCols; ++i) acc[c * kChunkCols + i] += v[i];
+                    }
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
+                }
+            } else {
+                if (!bar_wait(acc_full + 8 * (ch & 1), (ch / 2) & 1, gone, ctas)) ok = false;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            const uint32_t b = ch & 1;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float v[kChunkCols];
+                if constexpr (kDrain) {
+#pragma unroll
+                    for (int i = 0; i < kChunkCols; ++i) v[i] = acc[c * kChunkCols + i];
+                } else if constexpr (kChunkCols == 32) {
+                    tmem_ld32(mine + b * kBN + c * 32, v);
+                } else {
+                    tmem_ld16(mine + b * kBN, v);
+                }
+                if (!kDrain && c == kChunks - 1) {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
+                }
+                // unit order of the split exchange: [quad][half][chunk]
+                const uint32_t unit = a.splits > 1 ? base + ((quad * kHalves + half) * kChunks + c) * kUnit : stage_unit;
+#pragma unroll
+                for (int j = 0; j < kChunkCols / 4; ++j)
+                    st_shared4(unit + unit_at(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                if (a.splits == 1) {
+                    __syncwarp();
+                    if constexpr (kSwap)
+                        finish_unit_swapped(a, unit, 1, prow, qrow + c * 32, kChunkCols);
+                    else
+                        finish_unit(a, unit, 1, prow, qrow + c * 32);
+                    __syncwarp();
+                }
+            }
+            if constexpr (!kDrain) ++ch;
+        }
+        if (!ok && lane == 0) atomicOr(a.err, kErrWaitTimeout);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (kCtas == 2 || a.splits > 1) cluster_sync();
+    if (kCtas == 1 && a.splits > 1) {
+        // every CTA's part of the one tile is in place: this CTA finishes its share of the units
+        if (warp < kDrainWarps) {
+            const TcTile tile = tc_tile(a, first);
+            constexpr uint32_t kUnits = 4 * kHalves * kChunks;
+            for (uint32_t u = rank + a.splits * warp; u < kUnits; u += a.splits * kDrainWarps) {
+                const uint32_t quad = u / (kHalves * kChunks), rest = u % (kHalves * kChunks);
+                const uint32_t prow = tile.p * 128 + quad * 32, qrow = tile.q * kBN + rest * kChunkCols;
+                if constexpr (kSwap)
+                    finish_unit_swapped(a, base + u * kUnit, a.splits, prow, qrow, kChunkCols);
+                else
+                    finish_unit(a, base + u * kUnit, a.splits, prow, qrow);
+            }
+        }
+        cluster_sync();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        tmem_free<kCtas>(tmem, kTmemCols);
+    }
+}
+
+// The instantiation for a.cfg: kernel, block-independent facts.
+struct Config {
+    int ctas, bn;
+    bool swap;
+};
+constexpr Config kConfigs[kTcConfigs] = {{2, 256, false}, {1, 128, false}, {1, 64, false},
+                                         {1, 64, true},   {1, 32, true},   {1, 16, true}};
+using Kernel = void (*)(TcArgs);
+const Kernel kKernels[kTcConfigs][2] = {
+    {product_tc_kernel<2, 256, false, false>, product_tc_kernel<2, 256, true, false>},
+    {product_tc_kernel<1, 128, false, false>, product_tc_kernel<1, 128, true, false>},
+    {product_tc_kernel<1, 64, false, false>, product_tc_kernel<1, 64, true, false>},
+    {product_tc_kernel<1, 64, false, true>, product_tc_kernel<1, 64, true, true>},
+    {product_tc_kernel<1, 32, false, true>, product_tc_kernel<1, 32, true, true>},
+    {product_tc_kernel<1, 16, false, true>, product_tc_kernel<1, 16, true, true>}};
+
+constexpr uint32_t kSmemMost = 231424;    // dynamic shared memory a CTA may take, with room for the static part
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;
+
+// [planes][outer][inner] bf16, boxes of `rows` x 64 elements, 128-byte swizzle, zeros outside.
+bool encode(CUtensorMap* map, const TcOperand& o, uint64_t inner, uint64_t outer, uint32_t rows) {
+    const cuuint64_t dims[3] = {inner, outer, o.planes};
+    const cuuint64_t strides[2] = {o.ld * 2, o.planes > 1 ? o.plane * 2 : o.ld * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kBK), rows, 1}, one[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t prepare_product_tc(TcShape* shape) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&shape->sms, cudaDevAttrMultiProcessorCount, dev);
+    for (int c = 0; c < kTcConfigs; ++c)
+        for (int d = 0; d < 2 && e == cudaSuccess; ++d)
+            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kKernels[c][d]),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    if (e == cudaSuccess && !g_encode) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        if (e == cudaSuccess && (q != cudaDriverEntryPointSuccess || !f)) e = cudaErrorNotSupported;
+        if (e == cudaSuccess) g_encode = reinterpret_cast<EncodeTiled>(f);
+    }
+    return e;
+}
+
+cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned int* err, bool test_expire,
+                              cudaStream_t stream) {
+    TcArgs a{};
+    const Config& c = kConfigs[p.cfg];
+    const bool drain = p.drain;
+    a.e = p.e;
+    a.rows = p.m;
+    a.cols = p.n;
+    a.k = p.k;
+    a.kblocks = (p.k + kBK - 1) / kBK;
+    const TcOperand& P = c.swap ? p.b : p.a;
+    const TcOperand& Q = c.swap ? p.a : p.b;
+    const uint32_t px = c.swap ? p.n : p.m, qx = c.swap ? p.m : p.n;
+    a.p_kmajor = P.kmajor;
+    a.q_kmajor = Q.kmajor;
+    a.planes_p = P.planes;
+    a.planes_q = Q.planes;
+    const uint32_t qrows = c.bn / c.ctas;
+    const bool okp = P.kmajor ? encode(&a.map_p, P, p.k, px, 128) : encode(&a.map_p, P, px, p.k, kBK);
+    const bool okq = Q.kmajor ? encode(&a.map_q, Q, p.k, qx, qrows) : encode(&a.map_q, Q, qx, p.k, kBK);
+    if (!okp || !okq) return cudaErrorInvalidValue;
+    a.tiles_p = (px + 128 * c.ctas - 1) / (128 * c.ctas);
+    a.tiles_q = (qx + c.bn - 1) / c.bn;
+    a.tiles = a.tiles_p * a.tiles_q;
+    a.group = 8;
+    a.splits = c.ctas == 2 ? 1 : p.splits;
+    if (a.splits > a.kblocks) a.splits = a.kblocks;
+    a.chunk_kb = P.planes + Q.planes > 2 ? 1 : 2;
+    const uint32_t stage = P.planes * kPBytes + Q.planes * qrows * kBK * 2;
+    const uint32_t extra = 1024 + (a.splits == 1 ? kDrainWarps * kUnit : 0);
+    // one CTA per SM for the pair kernel and where two would leave each fewer than 3 stages
+    const uint32_t half = kSmemMost / 2 - 512;
+    uint32_t stages = c.ctas == 1 && half > extra ? (half - extra) / stage : 0;
+    if (stages < 3) stages = (kSmemMost - extra) / stage;
+    if (stages > static_cast<uint32_t>(kTcMaxStages)) stages = kTcMaxStages;
+    if (stages < 1) return cudaErrorInvalidValue;
+    a.stages = stages;
+    uint32_t smem = extra + stages * stage;
+    if (a.splits > 1 && smem < 1024 + 128 * c.bn * 4) smem = 1024 + 128 * c.bn * 4;
+    a.err = err;
+    a.test_expire = test_expire;
+    const uint64_t so = a.e.out_dtype ? 2 : 4;
+    auto vec = [&](const void* q, uint64_t ld) { return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * so % 16 == 0); };
+    a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
+    const uint32_t per = c.ctas == 2 ? 2 : a.splits;
+    uint32_t clusters = a.tiles;
+    if (a.splits == 1) {
+        const uint32_t room = shape.sms / c.ctas * (c.ctas == 1 && smem <= kSmemMost / 2 ? 2 : 1);
+        if (clusters > room) clusters = room;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(clusters * per);
+    cfg.blockDim = dim3(c.bn == 256 && drain ? kThreads<256, true> : kThreads<128, false>);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = per;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = per > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kKernels[p.cfg][drain], a);
+}
+
+}  // namespace fa

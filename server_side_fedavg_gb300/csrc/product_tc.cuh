@@ -1,0 +1,72 @@
+// Tensor-core products: launch interface (internal to the library).
+#pragma once
+
+#include <cuda.h>
+
+#include "product.cuh"
+
+namespace fa {
+
+constexpr int kTcMaxStages = 8;
+constexpr int kTcConfigs = 6;
+
+// Kernel configurations (rows x columns of a tile of the output).
+enum TcConfig {
+    kTcPair256 = 0,     // 256 x 256 on two SMs
+    kTc128 = 1,         // 128 x 128
+    kTc64 = 2,          // 128 x 64
+    kTcSwap64 = 3,      // 64 x 128, tokens in the MMA's columns
+    kTcSwap32 = 4,      // 32 x 128
+    kTcSwap16 = 5,      // 16 x 128
+};
+
+// An operand the kernel can read: bf16, base and row stride multiples of 16 bytes.
+struct TcOperand {
+    const void* p;
+    uint64_t ld;        // elements
+    uint64_t plane;     // elements between planes
+    uint32_t planes;    // 1, or 3 (an fp32 operand's terms)
+    bool kmajor;
+};
+
+struct TcProduct {
+    uint32_t m, n, k;   // each >= 1
+    TcOperand a, b;
+    ProdEpilogue e;
+    int cfg;
+    bool drain;         // fp32 results: sums rounded to nearest
+    uint32_t splits;    // of the summed index: 1..8
+};
+
+struct TcShape {
+    int sms = 0;
+};
+
+struct TcArgs {
+    CUtensorMap map_p, map_q;
+    ProdEpilogue e;
+    unsigned int* err;
+    uint32_t rows, cols, k, kblocks;          // of the output and the sum
+    uint32_t tiles, tiles_p, tiles_q, group;
+    uint32_t splits, stages, chunk_kb, planes_p, planes_q;
+    bool p_kmajor, q_kmajor, vec, test_expire;
+};
+
+struct TcTile {
+    uint32_t p, q;
+};
+
+// Tiles in bands of a.group tiles of P, down the band first: the CTAs at work at one time
+// share few rows of either operand, which stay in L2.
+__device__ __forceinline__ TcTile tc_tile(const TcArgs& a, uint32_t t) {
+    const uint32_t band = t / (a.group * a.tiles_q), p0 = band * a.group;
+    const uint32_t height = a.tiles_p - p0 < a.group ? a.tiles_p - p0 : a.group;
+    const uint32_t r = t - p0 * a.tiles_q;
+    return {p0 + r % height, r / height};
+}
+
+cudaError_t prepare_product_tc(TcShape* shape);
+cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned int* err, bool test_expire,
+                              cudaStream_t stream);
+
+}  // namespace fa

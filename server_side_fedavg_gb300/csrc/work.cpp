@@ -18,7 +18,7 @@
 
 #include "distill.cuh"
 #include "kernels.cuh"
-#include "product.cuh"
+#include "product_tc.cuh"
 
 struct fa_work {
     std::mutex mu;
@@ -34,6 +34,7 @@ struct fa_work {
     unsigned int* err_host = nullptr;    // pinned copy
     cudaStream_t err_stream = nullptr;
     cudaEvent_t err_ev = nullptr;
+    fa::TcShape tc;
     fa_work_stats stats{};
     std::string err;
 };
@@ -186,6 +187,85 @@ fa_status launched(fa_work* w, cudaError_t e, const char* what) {
     return FA_OK;
 }
 
+// ----------------------------------------------------------------- products
+uint64_t pad256(uint64_t b) { return (b + 255) / 256 * 256; }
+
+// Workspace handed out piece by piece.  A first run with base 0 adds the sizes up.
+struct Carve {
+    uint8_t* base;
+    uint64_t used = 0;
+    void* take(uint64_t bytes) {
+        uint8_t* p = base ? base + used : nullptr;
+        used += pad256(bytes);
+        return p;
+    }
+};
+
+// Whether the product is for the plain kernel: too little work to fill a tensor-core tile.
+bool use_plain(uint64_t m, uint64_t n, uint64_t k) { return k == 0 || m * n * k <= (1ull << 16); }
+
+bool tma_ready(const fa::ProdOperand& o) {
+    return o.dtype == 1 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 && o.ld < (1ull << 36);
+}
+
+// The operand as the tensor-core kernel reads it: as it is, or laid out in the workspace
+// (launching that if `run`).  x: its extent beside the summed one.
+fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, Carve* c, fa::TcOperand* t, bool run,
+                  cudaStream_t s) {
+    if (tma_ready(o)) {
+        *t = {o.p, o.ld, 0, 1, o.kmajor};
+        return FA_OK;
+    }
+    const uint32_t rows = o.kmajor ? x : k, cols = o.kmajor ? k : x, planes = o.dtype ? 1 : 3;
+    const uint64_t ldd = (cols + 7ull) / 8 * 8;
+    void* dst = c->take(ldd * rows * planes * 2);
+    *t = {dst, ldd, ldd * rows, planes, o.kmajor};
+    if (!run) return FA_OK;
+    return launched(w, fa::launch_split(o.p, o.ld, o.dtype, rows, cols, planes, dst, ldd, s), "operand layout");
+}
+
+// Tile configuration and split of the summed index.  sms CTAs fill the GPU once.
+void choose(fa::TcProduct* p, int sms) {
+    const auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
+    const uint64_t kb = up(p->k, 64);
+    p->drain = p->e.out_dtype == 0;
+    p->splits = 1;
+    if (p->m <= 64 && (p->a.kmajor || p->m > 32)) {
+        p->cfg = p->m <= 16 ? fa::kTcSwap16 : p->m <= 32 ? fa::kTcSwap32 : fa::kTcSwap64;
+    } else if (up(p->m, 256) * up(p->n, 256) * 2 >= static_cast<uint64_t>(sms)) {
+        p->cfg = fa::kTcPair256;
+    } else {
+        p->cfg = p->n <= 64 ? fa::kTc64 : fa::kTc128;
+    }
+    if (p->cfg == fa::kTcPair256) return;
+    const uint64_t tiles = p->cfg == fa::kTc128  ? up(p->m, 128) * up(p->n, 128)
+                           : p->cfg == fa::kTc64 ? up(p->m, 128) * up(p->n, 64)
+                                                 : up(p->n, 128);
+    while (p->splits < 8 && tiles * p->splits * 2 <= static_cast<uint64_t>(2 * sms) && kb >= p->splits * 2 * 4) p->splits *= 2;
+}
+
+// A product by the kernel that suits its size.  run == false only adds up the workspace.
+fa_status do_product(fa_work* w, const fa::ProdArgs& q, const fa::TcOperand* ready_a, const fa::TcOperand* ready_b, Carve* c,
+                     bool run, cudaStream_t s, const char* what) {
+    fa::TcProduct t{};
+    t.m = q.m;
+    t.n = q.n;
+    t.k = q.k;
+    t.e = q.e;
+    fa_status r = FA_OK;
+    if (ready_a)
+        t.a = *ready_a;
+    else
+        r = lay_out(w, q.a, q.m, q.k, c, &t.a, run, s);
+    if (ready_b)
+        t.b = *ready_b;
+    else if (r == FA_OK)
+        r = lay_out(w, q.b, q.n, q.k, c, &t.b, run, s);
+    if (r != FA_OK || !run) return r;
+    choose(&t, w->tc.sms);
+    return launched(w, fa::launch_product_tc(t, w->tc, w->err_dev, (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s), what);
+}
+
 fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     if (p.flags & ~(FA_TRANS_A | FA_TRANS_B)) return fail(w, FA_ERR_ARG, "unknown flag");
     if (!dtype_ok(p.dtype_in) || !dtype_ok(p.dtype_out)) return fail(w, FA_ERR_DTYPE, "dtype");
@@ -217,8 +297,6 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     if (res && !(res == p.out && p.ldr == p.ldo) && overlap(p.out, p.m, p.n, p.ldo, so, res, p.m, p.n, p.ldr, so))
         return fail(w, FA_ERR_ARG, "out overlaps residual without being it");
     const bool cap = capturing(s);
-    r = chain_in(w, s, cap);
-    if (r != FA_OK) return r;
     fa::ProdArgs q{};
     q.m = static_cast<uint32_t>(p.m);
     q.n = static_cast<uint32_t>(p.n);
@@ -227,7 +305,15 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     q.b = {p.b, p.ldb, code_of(p.dtype_in), tb};
     q.e = {static_cast<float>(p.alpha), static_cast<float>(p.beta), p.bias, res, p.out, p.pre, p.ldr, p.ldo,
            code_of(p.dtype_in), code_of(p.dtype_out), p.act};
-    r = launched(w, fa::launch_product_plain(q, s), "product");
+    const bool plain = use_plain(p.m, p.n, p.k);
+    Carve need{nullptr};
+    if (!plain) do_product(w, q, nullptr, nullptr, &need, false, s, "product");
+    r = ensure_ws(w, need.used, cap);
+    if (r == FA_OK) r = chain_in(w, s, cap);
+    if (r != FA_OK) return r;
+    Carve c{w->ws};
+    r = plain ? launched(w, fa::launch_product_plain(q, s), "product")
+              : do_product(w, q, nullptr, nullptr, &c, true, s, "product");
     if (r != FA_OK) return r;
     return chain_out(w, s, cap);
 }
@@ -268,42 +354,67 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     if (!want_a && !want_b && !want_bias) return FA_OK;
     const uint32_t m = static_cast<uint32_t>(p.m), n = static_cast<uint32_t>(p.n), k = static_cast<uint32_t>(p.k);
     const uint32_t blocks = (m + fa::kColRows - 1) / fa::kColRows;
-    const uint64_t dz_bytes = act ? p.m * p.n * 4 : 0, part_bytes = want_bias ? uint64_t(blocks) * p.n * 4 : 0;
-    const uint64_t dz_pad = (dz_bytes + 255) / 256 * 256;
+    const int it = code_of(p.dtype_in), dt = code_of(p.dtype_dout), gt = code_of(p.dtype_grad);
+    // dZ is dout itself, or is written to the workspace: in fp32 for the plain kernel, else
+    // as bf16 planes
+    const bool plain = use_plain(p.m, p.n, p.k);
+    const bool products = want_a || want_b;
+    const fa::ProdOperand d_in{p.dout, p.ldd, dt, true};
+    const bool write_dz = products && m && n && (act || (!plain && !tma_ready(d_in)));
+    const int planes = plain ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
+    const uint64_t ldz = plain ? p.n : (p.n + 7) / 8 * 8;
     const bool cap = capturing(s);
-    r = ensure_ws(w, dz_pad + part_bytes, cap);
-    if (r == FA_OK) r = chain_in(w, s, cap);
-    if (r != FA_OK) return r;
-    float* dz = act ? reinterpret_cast<float*>(w->ws) : nullptr;
-    float* part = want_bias ? reinterpret_cast<float*>(w->ws + dz_pad) : nullptr;
-    if ((dz || part) && m && n) {
-        const fa::ActGradArgs g{m, n, p.dout, act ? p.pre : nullptr, p.ldd, p.ldp, code_of(p.dtype_dout), p.act, dz, part};
-        r = launched(w, fa::launch_act_grad(g, s), "activation gradient");
+    // two passes over the same steps: the first adds up the workspace
+    Carve c{nullptr};
+    for (int run = 0; run < 2; ++run) {
+        if (run) {
+            r = ensure_ws(w, c.used, cap);
+            if (r == FA_OK) r = chain_in(w, s, cap);
+            if (r != FA_OK) return r;
+            c = Carve{w->ws};
+        }
+        void* dz = write_dz ? c.take(p.m * ldz * (planes ? 2 * planes : 4)) : nullptr;
+        float* part = want_bias ? static_cast<float*>(c.take(blocks * p.n * 4)) : nullptr;
+        if (run && (write_dz || want_bias) && m && n) {
+            const fa::ActGradArgs g{m, n, p.dout, act ? p.pre : nullptr, p.ldd, p.ldp, dt, p.act, dz, ldz, planes, part};
+            r = launched(w, fa::launch_act_grad(g, s), "activation gradient");
+        }
+        if (run && r == FA_OK && want_bias)
+            r = launched(w, fa::launch_col_sum(part, blocks, n, p.d_bias, gt, s), "bias gradient");
+        const fa::ProdOperand z = write_dz ? fa::ProdOperand{dz, ldz, planes ? 1 : 0, true} : d_in;
+        fa::ProdOperand z_n = z;         // x = n (sum over m); z: x = m (sum over n)
+        z_n.kmajor = false;
+        const uint32_t zp = write_dz && planes ? planes : 1;
+        const fa::TcOperand tz{z.p, z.ld, p.m * ldz, zp, true}, tz_n{z.p, z.ld, p.m * ldz, zp, false};
+        fa::ProdEpilogue e{};
+        e.alpha = static_cast<float>(p.alpha);
+        e.out_dtype = gt;
+        const uint64_t mark = c.used;
+        if (r == FA_OK && want_a) {
+            const fa::ProdOperand b{p.b, p.ldb, it, !tb};      // x = k, sum over n
+            e.out = p.d_a;
+            e.ldo = p.ldda;
+            const fa::ProdArgs q = ta ? fa::ProdArgs{k, m, n, b, z, e} : fa::ProdArgs{m, k, n, z, b, e};
+            if (plain || n == 0)
+                r = run ? launched(w, fa::launch_product_plain(q, s), "gradient of a") : FA_OK;
+            else
+                r = do_product(w, q, ta ? nullptr : &tz, ta ? &tz : nullptr, &c, run, s, "gradient of a");
+        }
+        const uint64_t after_a = c.used;
+        c.used = mark;                    // the second product's operand may take the first's place
+        if (r == FA_OK && want_b) {
+            const fa::ProdOperand a{p.a, p.lda, it, ta};       // x = k, sum over m
+            e.out = p.d_b;
+            e.ldo = p.lddb;
+            const fa::ProdArgs q = tb ? fa::ProdArgs{n, k, m, z_n, a, e} : fa::ProdArgs{k, n, m, a, z_n, e};
+            if (plain || m == 0)
+                r = run ? launched(w, fa::launch_product_plain(q, s), "gradient of b") : FA_OK;
+            else
+                r = do_product(w, q, tb ? &tz_n : nullptr, tb ? nullptr : &tz_n, &c, run, s, "gradient of b");
+        }
+        c.used = std::max(c.used, after_a);
+        if (r != FA_OK) return r;
     }
-    if (r == FA_OK && want_bias)
-        r = launched(w, fa::launch_col_sum(part, blocks, n, p.d_bias, code_of(p.dtype_grad), s), "bias gradient");
-    const void* z = act ? static_cast<const void*>(dz) : p.dout;
-    const uint64_t ldz = act ? p.n : p.ldd;
-    const int zt = act ? 0 : code_of(p.dtype_dout), it = code_of(p.dtype_in);
-    const fa::ProdOperand z_m{z, ldz, zt, true}, z_n{z, ldz, zt, false};   // x = m (sum over n), x = n (sum over m)
-    fa::ProdEpilogue e{};
-    e.alpha = static_cast<float>(p.alpha);
-    e.out_dtype = code_of(p.dtype_grad);
-    if (r == FA_OK && want_a) {
-        const fa::ProdOperand b{p.b, p.ldb, it, !tb};      // x = k, sum over n
-        e.out = p.d_a;
-        e.ldo = p.ldda;
-        const fa::ProdArgs q = ta ? fa::ProdArgs{k, m, n, b, z_m, e} : fa::ProdArgs{m, k, n, z_m, b, e};
-        r = launched(w, fa::launch_product_plain(q, s), "gradient of a");
-    }
-    if (r == FA_OK && want_b) {
-        const fa::ProdOperand a{p.a, p.lda, it, ta};       // x = k, sum over m
-        e.out = p.d_b;
-        e.ldo = p.lddb;
-        const fa::ProdArgs q = tb ? fa::ProdArgs{n, k, m, z_n, a, e} : fa::ProdArgs{k, n, m, a, z_n, e};
-        r = launched(w, fa::launch_product_plain(q, s), "gradient of b");
-    }
-    if (r != FA_OK) return r;
     return chain_out(w, s, cap);
 }
 
@@ -437,6 +548,7 @@ fa_status fa_work_open(const fa_work_opts* opts, fa_work** out) {
     w->flags = o.flags;
     cudaError_t ce = cudaGetDevice(&w->device);
     if (ce == cudaSuccess) ce = fa::prepare_distill();
+    if (ce == cudaSuccess) ce = fa::prepare_product_tc(&w->tc);
     if (ce == cudaSuccess) ce = cudaMalloc(reinterpret_cast<void**>(&w->err_dev), 256);
     if (ce == cudaSuccess) ce = cudaMemset(w->err_dev, 0, 256);
     if (ce == cudaSuccess) ce = cudaEventCreateWithFlags(&w->chain, cudaEventDisableTiming);
