@@ -40,13 +40,22 @@ constexpr bool kRegSplit = kDrain && kBN == 256;
 template <int kBN, bool kDrain>
 constexpr int kThreads = kRegSplit<kBN, kDrain> ? 384 : (kDrainWarps + 2) * 32;
 constexpr uint32_t kPBytes = 128 * kBK * 2;
-constexpr uint32_t kUnit = 32 * 32 * 4;    // a 32 x 32 block of fp32 partial results
+constexpr uint32_t kUnit = 4096;           // a 32 x 32 block of fp32, or 32 rows x 128 bytes of outputs
 
 // ----------------------------------------------------------------- PTX
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
+}
+
+// One lane of a converged warp.  In this form the compiler knows that a single thread goes
+// on: the tensor-core and TMA instructions then take their operands from uniform registers
+// directly (with `lane == 0` each MMA took some 290 cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
@@ -78,32 +87,26 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return done;
 }
 
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
 // Wait for a phase, acquiring at cluster scope (the arrivals may come from another CTA).
-// False where the cluster has given up (`gone` is set) or the wait has lasted kMaxWaitNs:
-// it then sets the flag of every CTA of the cluster, so that every role leaves.
-constexpr uint64_t kMaxWaitNs = 20ull * 1000 * 1000 * 1000;
+// False where the cluster has given up (`gone` is set) or the wait has lasted kMaxWaitClocks
+// (some 20 s): it then sets the flag of every CTA of the cluster, so that every role leaves.
+constexpr long long kMaxWaitClocks = 40ll * 1000 * 1000 * 1000;
 __device__ __forceinline__ void give_up(uint32_t gone, uint32_t ctas) {
     for (uint32_t r = 0; r < ctas; ++r)
         asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(ctas > 1 ? in_cta(gone, r) : gone) : "memory");
 }
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t gone, uint32_t ctas) {
-    uint64_t t0 = 0;
+    long long t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
-        if (i % 16) continue;
+        if (i % 64) continue;
         uint32_t g;
         asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(g) : "r"(gone) : "memory");
         if (g) return false;
         if (t0 == 0) {
-            t0 = now_ns();
-        } else if (now_ns() - t0 > kMaxWaitNs) {
+            t0 = clock64();
+        } else if (clock64() - t0 > kMaxWaitClocks) {
             give_up(gone, ctas);
             return false;
         }
@@ -123,6 +126,30 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
             " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
+}
+
+// Boxes of the output side, 2-D, 128-byte swizzle: x and y in elements and rows.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared4u(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared4u(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 template <int kCtas>
@@ -349,24 +376,120 @@ __device__ __forceinline__ void finish_unit_swapped(const TcArgs& a, uint32_t un
     }
 }
 
+// Outputs by TMA: a drain warp's tile part is cut into blocks of 32 rows x 128 bytes, each in
+// one of the warp's `slots` buffers.  Without `pre`, a block's residual is loaded into its
+// buffer slots - 1 blocks ahead (so that HBM-bound products keep some 100 KB of loads in
+// flight per SM), replaced by the output in place and stored from there.  With `pre`, buffer 0
+// holds it, buffer 1 the output, and the residual is read directly.
+struct OutWarp {
+    uint32_t buf, bar, slots;      // this warp's buffers and their load barriers
+    uint32_t issued, block;        // loads issued; blocks finished
+    uint32_t row_off, col_off;     // of the warp's part within the CTA's tile
+    uint32_t blocks;               // per tile
+    bool ahead;                    // residuals come by TMA
+};
+
+template <int kCtas, int kBN>
+__device__ __forceinline__ void load_ahead(const TcArgs& a, OutWarp& o, uint32_t upto, uint32_t first, uint32_t step,
+                                           uint32_t width, uint32_t rank) {
+    for (; o.issued < upto; ++o.issued) {
+        const uint32_t t = first + o.issued / o.blocks * step;
+        if (t >= a.tiles) return;
+        const TcTile tile = tc_tile(a, t);
+        const uint32_t row = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0) + o.row_off;
+        const uint32_t col = tile.q * kBN + o.col_off + o.issued % o.blocks * width;
+        const uint32_t s = o.issued % o.slots;
+        // a block outside the output is all zeros: in range for a load
+        mbar_expect(o.bar + 8 * s, kUnit);
+        tma_load_2d(o.buf + s * kUnit, &a.map_res, col, row, o.bar + 8 * s);
+    }
+}
+
+// 32 columns of one row (this lane's), sums in v, to 16-byte pieces first, first + 1, ... of
+// the row's 128 bytes.  bias: 32 floats in shared memory.
+template <bool kBf16>
+__device__ __forceinline__ void finish_row(const TcArgs& a, const float (&v)[32], uint32_t bias, uint32_t out, uint32_t pre,
+                                           uint32_t piece0, uint32_t row, uint32_t col, bool res_here) {
+    constexpr int kPer = kBf16 ? 8 : 4;       // elements per piece
+    const uint32_t lane = threadIdx.x % 32;
+    const ProdEpilogue& e = a.e;
+#pragma unroll
+    for (int p = 0; p < 32 / kPer; ++p) {
+        const uint32_t at = unit_at(lane, piece0 + p);
+        float y[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) y[i] = e.alpha * v[p * kPer + i];
+        if (e.bias)
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4) {
+                const uint4 b = ld_shared4u(bias + (p * kPer + i) * 4);
+                y[i] += __uint_as_float(b.x);
+                y[i + 1] += __uint_as_float(b.y);
+                y[i + 2] += __uint_as_float(b.z);
+                y[i + 3] += __uint_as_float(b.w);
+            }
+        if (e.pre && pre == out) {            // one buffer, which is the output's
+            const uint32_t c = col + p * kPer;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (row < a.rows && c + i < a.cols) put(e.pre, row * e.ldo + c + i, e.out_dtype, y[i]);
+        } else if (e.pre) {
+            if constexpr (kBf16)
+                st_shared4u(pre + at, pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+            else
+                st_shared4(pre + at, y[0], y[1], y[2], y[3]);
+        }
+        if (e.act)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) y[i] = act_fwd(e.act, y[i]);
+        if (e.res) {
+            float r[8];
+            if (res_here) {
+                const uint4 q = ld_shared4u(out + at);
+                if constexpr (kBf16) {
+                    r[0] = bf16_lo(q.x); r[1] = bf16_hi(q.x); r[2] = bf16_lo(q.y); r[3] = bf16_hi(q.y);
+                    r[4] = bf16_lo(q.z); r[5] = bf16_hi(q.z); r[6] = bf16_lo(q.w); r[7] = bf16_hi(q.w);
+                } else {
+                    r[0] = __uint_as_float(q.x); r[1] = __uint_as_float(q.y);
+                    r[2] = __uint_as_float(q.z); r[3] = __uint_as_float(q.w);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const uint32_t c = col + p * kPer + i;
+                    r[i] = row < a.rows && c < a.cols ? elem(e.res, row * e.ldr + c, e.out_dtype) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) y[i] = fmaf(e.beta, r[i], y[i]);
+        }
+        if constexpr (kBf16)
+            st_shared4u(out + at, pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        else
+            st_shared4(out + at, y[0], y[1], y[2], y[3]);
+    }
+}
+
 // ----------------------------------------------------------------- kernel
 template <int kCtas, int kBN, bool kDrain, bool kSwap>
 __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(const __grid_constant__ TcArgs a) {
     constexpr int kQRows = kBN / kCtas;                     // rows of Q that this CTA loads
     constexpr uint32_t kQBytes = kQRows * kBK * 2;
-    constexpr int kHalf = kBN >= 64 ? kBN / 2 : kBN;        // columns drained by one warp
+    constexpr int kHalf = kBN >= 128 ? kBN / 2 : kBN;       // columns drained by one warp
     constexpr int kHalves = kBN / kHalf;                    // warps sharing a lane quadrant
     constexpr int kChunkCols = kHalf < 32 ? kHalf : 32;
     constexpr int kChunks = kHalf / kChunkCols;
     constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
     extern __shared__ uint8_t dyn[];
-    __shared__ uint64_t bars[2 * kTcMaxStages + 4];
+    __shared__ uint64_t bars[2 * kTcMaxStages + 4 + kDrainWarps * kTcMaxSlots];
+    __shared__ __align__(16) float bias_rows[kDrainWarps][32];
     __shared__ uint32_t tmem_slot, gone_flag;
     const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
     const uint32_t full = smem_addr(&bars[0]), empty = smem_addr(&bars[kTcMaxStages]);
     const uint32_t acc_full = smem_addr(&bars[2 * kTcMaxStages]), acc_empty = acc_full + 16;
+    const uint32_t res_bars = acc_full + 32;
     const uint32_t stage_bytes = a.planes_p * kPBytes + a.planes_q * kQBytes;
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 || a.splits > 1 ? cluster_rank() : 0;
     const uint32_t split = kCtas == 2 ? 0 : rank;
     const bool leader = kCtas == 1 || rank == 0;
@@ -381,6 +504,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             bar_init(acc_full + 8 * b, 1);
             bar_init(acc_empty + 8 * b, kCtas * kHalves * 4);
         }
+        for (uint32_t i = 0; i < kDrainWarps * kTcMaxSlots; ++i) bar_init(res_bars + 8 * i, 1);
         gone_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -400,16 +524,15 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
 
     if (warp >= 8) {
         if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8 && lane == 0) {
+        if (warp == 8 && elect_one()) {
             const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
-            uint32_t it = 0;
+            uint32_t s = 0, phase = 1;          // the first round of stages is free
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
                 const TcTile tile = tc_tile(a, t);
                 const int32_t p0 = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0);
                 const int32_t q0 = tile.q * kBN + (kCtas == 2 ? rank * kQRows : 0);
-                for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % a.stages;
-                    if (it >= a.stages && !bar_wait(empty + 8 * s, (it / a.stages - 1) & 1, gone, ctas)) {
+                for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                    if (!bar_wait(empty + 8 * s, phase, gone, ctas)) {
                         ok = false;
                         break;
                     }
@@ -430,13 +553,19 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                             for (int h = 0; h < kQRows / 64; ++h)
                                 tma_load<kCtas>(dst + h * 8192, &a.map_q, q0 + 64 * h, k0, z, lead_full + 8 * s);
                     }
+                    if (++s == a.stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
-        } else if (warp == 9 && lane == 0 && leader) {
+        } else if (warp == 9 && leader && elect_one()) {
             const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (a.p_kmajor ? 0u : 1u << 15) |
                                    (a.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 | (128 * kCtas / 16) << 24;
             const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
-            uint32_t it = 0, ch = 0;
+            const uint64_t desc_p = operand_desc(base, a.p_kmajor, 8192);
+            const uint64_t desc_q = operand_desc(base + a.planes_p * kPBytes, a.q_kmajor, 8192);
+            uint32_t it = 0, ch = 0, s = 0, phase = 0;      // it: blocks so far; s, phase: its stage
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
                 for (uint32_t kb = kb0; ok && kb < kb1; ++ch) {
                     const uint32_t b = ch & 1;
@@ -449,27 +578,35 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                     const uint32_t end = kDrain && kb1 - kb > a.chunk_kb ? kb + a.chunk_kb : kb1;
                     bool add = false;
                     for (; kb < end; ++kb, ++it) {
-                        const uint32_t s = it % a.stages;
-                        if (a.test_expire || !bar_wait(full + 8 * s, (it / a.stages) & 1, gone, ctas)) {
+                        if (a.test_expire || !bar_wait(full + 8 * s, phase, gone, ctas)) {
                             ok = false;
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint32_t at = base + s * stage_bytes;
-                        const uint32_t left = a.k - kb * kBK, steps = left >= kBK ? 4 : (left + 15) / 16;
-                        for (int sum = 2; sum >= 0; --sum)
-                            for (int i = 0; i <= sum; ++i) {
-                                const int j = sum - i;
-                                if (i >= static_cast<int>(a.planes_p) || j >= static_cast<int>(a.planes_q)) continue;
-                                const uint64_t dp = operand_desc(at + i * kPBytes, a.p_kmajor, 8192);
-                                const uint64_t dq =
-                                    operand_desc(at + a.planes_p * kPBytes + j * kQBytes, a.q_kmajor, 8192);
-                                for (uint32_t x = 0; x < steps; ++x) {
-                                    mma<kCtas>(d, dp + x * step_p, dq + x * step_q, idesc, add);
-                                    add = true;
-                                }
+                        // all four steps of 16 terms: what lies past the sum's end is zeros
+                        const uint64_t dp = desc_p + (s * stage_bytes >> 4), dq = desc_q + (s * stage_bytes >> 4);
+                        if (a.planes_p == 1 && a.planes_q == 1) {
+#pragma unroll
+                            for (uint32_t x = 0; x < kBK / 16; ++x)
+                                mma<kCtas>(d, dp + x * step_p, dq + x * step_q, idesc, add || x > 0);
+                        } else {
+                            for (uint32_t pair = 0; pair < 6; ++pair) {
+                                // (i, j): 2 0, 1 1, 0 2, 1 0, 0 1, 0 0
+                                const uint32_t i = 0x001012 >> (pair * 4) & 3, j = 0x010210 >> (pair * 4) & 3;
+                                if (i >= a.planes_p || j >= a.planes_q) continue;
+#pragma unroll
+                                for (uint32_t x = 0; x < kBK / 16; ++x)
+                                    mma<kCtas>(d, dp + (i * kPBytes >> 4) + x * step_p,
+                                               dq + (j * kQBytes >> 4) + x * step_q, idesc, add || x > 0);
+                                add = true;
                             }
+                        }
+                        add = true;
                         commit<kCtas>(empty + 8 * s);
+                        if (++s == a.stages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
                     if (ok) commit<kCtas>(acc_full + 8 * b);
                 }
@@ -489,7 +626,21 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
         if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const uint32_t quad = warp % 4, half = warp / 4;
         const uint32_t mine = tmem + (quad << 21) + half * kHalf;    // lane 32 quad, column half * kHalf
-        const uint32_t stage_unit = base + a.stages * stage_bytes + warp * kUnit;
+        const uint32_t bias_at = smem_addr(bias_rows[warp]);
+        const bool bf16 = a.e.out_dtype != 0;
+        const uint32_t width = bf16 ? 64 : 32;           // columns of a block of outputs
+        const bool by_tma = !kSwap && a.vec && a.splits == 1;
+        OutWarp o;
+        o.slots = a.slots;
+        o.buf = base + a.stages * stage_bytes + warp * a.slots * kUnit;
+        o.bar = res_bars + warp * kTcMaxSlots * 8;
+        o.issued = o.block = 0;
+        o.row_off = quad * 32;
+        o.col_off = half * kHalf;
+        o.blocks = kHalf / width;
+        o.ahead = by_tma && a.e.res && !a.e.pre;
+        const uint32_t stage_unit = o.buf;
+        if (o.ahead && lane == 0) load_ahead<kCtas, kBN>(a, o, o.slots, first, step, width, rank);
         const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty;
         uint32_t ch = 0;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
@@ -544,6 +695,54 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                     __syncwarp();
                     if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
                 }
+                if constexpr (!kSwap && kChunkCols == 32) {
+                    if (by_tma) {
+                        const uint32_t col = qrow + c * 32, part = bf16 ? c % 2 : 0;
+                        const bool two = a.e.pre && o.slots > 1;
+                        const uint32_t slot = two ? 1 : o.block % o.slots;
+                        const uint32_t out = o.buf + slot * kUnit;
+                        if (part == 0) {
+                            // the block's buffer: its residual has come, or its last store has left
+                            if (o.ahead) {
+                                ok = bar_wait(o.bar + 8 * slot, (o.block / o.slots) & 1, gone, ctas);
+                            } else if (lane == 0) {
+                                if (two || o.slots == 1)
+                                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                                else
+                                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            }
+                        }
+                        if (a.e.bias)
+                            bias_rows[warp][lane] = col + lane < a.cols ? elem(a.e.bias, col + lane, a.e.bias_dtype) : 0.0f;
+                        __syncwarp();
+                        if (bf16)
+                            finish_row<true>(a, v, bias_at, out, o.buf, part * 4, prow + lane, col, o.ahead);
+                        else
+                            finish_row<false>(a, v, bias_at, out, o.buf, 0, prow + lane, col, o.ahead);
+                        if (!bf16 || part == 1) {
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) {
+                                const uint32_t c0 = bf16 ? col - 32 : col;
+                                if (prow < a.rows && c0 < a.cols) {
+                                    if (two) tma_store_2d(&a.map_pre, o.buf, c0, prow);
+                                    tma_store_2d(&a.map_out, out, c0, prow);
+                                }
+                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                                if (o.ahead) {
+                                    if (o.slots == 1)
+                                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                                    else
+                                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                                    load_ahead<kCtas, kBN>(a, o, o.block + (o.slots > 1 ? o.slots : 2), first, step, width, rank);
+                                }
+                            }
+                            ++o.block;
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                }
                 // unit order of the split exchange: [quad][half][chunk]
                 const uint32_t unit = a.splits > 1 ? base + ((quad * kHalves + half) * kChunks + c) * kUnit : stage_unit;
 #pragma unroll
@@ -559,8 +758,16 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                 }
             }
             if constexpr (!kDrain) ++ch;
+            ok = __all_sync(~0u, ok);
         }
-        if (!ok && lane == 0) atomicOr(a.err, kErrWaitTimeout);
+        if (lane == 0) {
+            if (!ok) {
+                atomicOr(a.err, kErrWaitTimeout);
+                for (; o.block < o.issued; ++o.block)       // the loads in flight land first
+                    for (uint32_t i = 0; i < 1000 && !bar_try(o.bar + 8 * (o.block % o.slots), (o.block / o.slots) & 1); ++i) {}
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -603,7 +810,7 @@ const Kernel kKernels[kTcConfigs][2] = {
     {product_tc_kernel<1, 32, false, true>, product_tc_kernel<1, 32, true, true>},
     {product_tc_kernel<1, 16, false, true>, product_tc_kernel<1, 16, true, true>}};
 
-constexpr uint32_t kSmemMost = 231424;    // dynamic shared memory a CTA may take, with room for the static part
+constexpr uint32_t kSmemMost = 230400;    // dynamic shared memory a CTA may take, with room for the static part
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -617,6 +824,22 @@ bool encode(CUtensorMap* map, const TcOperand& o, uint64_t inner, uint64_t outer
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(kBK), rows, 1}, one[3] = {1, 1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, one,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool out_ready(const void* p, uint64_t ld, int dtype) {
+    const uint64_t size = dtype ? 2 : 4;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && ld * size < (1ull << 40);
+}
+
+// The output's matrix in boxes of 32 rows x 128 bytes.
+bool encode_out(CUtensorMap* map, const void* p, uint64_t ld, const TcArgs& a) {
+    const bool bf16 = a.e.out_dtype != 0;
+    const cuuint64_t dims[2] = {a.cols, a.rows}, strides[1] = {ld * (bf16 ? 2 : 4)};
+    const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32}, one[2] = {1, 1};
+    return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                    const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -668,12 +891,22 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.splits = c.ctas == 2 ? 1 : p.splits;
     if (a.splits > a.kblocks) a.splits = a.kblocks;
     a.chunk_kb = P.planes + Q.planes > 2 ? 1 : 2;
+    auto vec = [&](const void* q, uint64_t ld) { return !q || out_ready(q, ld, a.e.out_dtype); };
+    a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
+    const bool by_tma = a.vec && a.splits == 1 && !c.swap;
+    if (by_tma && !(encode_out(&a.map_out, a.e.out, a.e.ldo, a) && (!a.e.pre || encode_out(&a.map_pre, a.e.pre, a.e.ldo, a)) &&
+                    (!a.e.res || encode_out(&a.map_res, a.e.res, a.e.ldr, a))))
+        return cudaErrorInvalidValue;
+    // Short sums are bound by the output side: more residual blocks ahead.  Operands of three
+    // planes fill shared memory: one block, so that two stages fit.
     const uint32_t stage = P.planes * kPBytes + Q.planes * qrows * kBK * 2;
-    const uint32_t extra = 1024 + (a.splits == 1 ? kDrainWarps * kUnit : 0);
-    // one CTA per SM for the pair kernel and where two would leave each fewer than 3 stages
-    const uint32_t half = kSmemMost / 2 - 512;
-    uint32_t stages = c.ctas == 1 && half > extra ? (half - extra) / stage : 0;
-    if (stages < 3) stages = (kSmemMost - extra) / stage;
+    const uint32_t warps = c.bn >= 128 ? 8 : 4;
+    a.slots = by_tma && a.e.res && !a.e.pre && a.kblocks <= 4 ? kTcMaxSlots : 2;
+    if (1024 + warps * a.slots * kUnit + 2 * stage > kSmemMost) a.slots = 1;
+    const uint32_t extra = 1024 + (a.splits == 1 ? warps * a.slots * kUnit : 0);
+    // two CTAs per SM for the forms that take few registers
+    const uint32_t occupancy = c.swap && !drain ? 2 : 1;
+    uint32_t stages = (kSmemMost / occupancy - 1024 * (occupancy - 1) - extra) / stage;
     if (stages > static_cast<uint32_t>(kTcMaxStages)) stages = kTcMaxStages;
     if (stages < 1) return cudaErrorInvalidValue;
     a.stages = stages;
@@ -681,13 +914,10 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     if (a.splits > 1 && smem < 1024 + 128 * c.bn * 4) smem = 1024 + 128 * c.bn * 4;
     a.err = err;
     a.test_expire = test_expire;
-    const uint64_t so = a.e.out_dtype ? 2 : 4;
-    auto vec = [&](const void* q, uint64_t ld) { return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * so % 16 == 0); };
-    a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
     const uint32_t per = c.ctas == 2 ? 2 : a.splits;
     uint32_t clusters = a.tiles;
     if (a.splits == 1) {
-        const uint32_t room = shape.sms / c.ctas * (c.ctas == 1 && smem <= kSmemMost / 2 ? 2 : 1);
+        const uint32_t room = shape.sms / c.ctas * occupancy;
         if (clusters > room) clusters = room;
     }
     cudaLaunchConfig_t cfg = {};

@@ -8,6 +8,7 @@
 namespace fa {
 
 constexpr int kTcMaxStages = 8;
+constexpr int kTcMaxSlots = 4;
 constexpr int kTcConfigs = 6;
 
 // Kernel configurations (rows x columns of a tile of the output).
@@ -44,11 +45,13 @@ struct TcShape {
 
 struct TcArgs {
     CUtensorMap map_p, map_q;
+    CUtensorMap map_out, map_res, map_pre;    // boxes of 32 rows x 128 bytes; with `vec` and splits == 1
     ProdEpilogue e;
     unsigned int* err;
     uint32_t rows, cols, k, kblocks;          // of the output and the sum
     uint32_t tiles, tiles_p, tiles_q, group;
     uint32_t splits, stages, chunk_kb, planes_p, planes_q;
+    uint32_t slots;                           // 4 KB epilogue buffers per drain warp: 2..kTcMaxSlots
     bool p_kmajor, q_kmajor, vec, test_expire;
 };
 
