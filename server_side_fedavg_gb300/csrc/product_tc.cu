@@ -31,15 +31,23 @@ namespace fa {
 namespace {
 
 constexpr int kBK = 64;                    // summed elements per block: 128 bytes, one swizzle row
-constexpr int kDrainWarps = 8;
-// The pair kernel's drain form holds 128 sums per thread: three warpgroups, of which the
-// third (loads, MMAs, two idle warps) gives registers to the first two:
-// 128 x 72 + 256 x 216 = 384 x 168, what the block is launched with.
+// Drain warps: each has the 32 lanes of its quadrant (warp % 4) and a part of the columns.
+// The epilogue is bound by instruction latency, so the pair kernel has 16 of them (with 8, the
+// adapter merge took 29 us instead of %MERGE%).
+template <int kBN>
+constexpr int kDrainWarps = kBN == 256 ? 16 : kBN >= 64 ? 8 : 4;
+// Drain warps sharing a quadrant: a block of outputs by TMA is 64 columns wide, so that the
+// 128 x 64 form has one, and half of its drain warps idle.
+__host__ __device__ constexpr int drain_parts(int bn, bool swap) { return bn == 256 ? 4 : bn == 128 || (swap && bn == 64) ? 2 : 1; }
+// The pair kernel's drain form holds 64 sums per thread: the last warpgroup (loads, MMAs, two
+// idle warps) gives registers to the others.  128 x 56 + 512 x 104 <= 640 x 96, what the block
+// is launched with.
 template <int kBN, bool kDrain>
 constexpr bool kRegSplit = kDrain && kBN == 256;
 template <int kBN, bool kDrain>
-constexpr int kThreads = kRegSplit<kBN, kDrain> ? 384 : (kDrainWarps + 2) * 32;
+constexpr int kThreads = (kDrainWarps<kBN> + (kRegSplit<kBN, kDrain> ? 4 : 2)) * 32;
 constexpr uint32_t kPBytes = 128 * kBK * 2;
+constexpr uint32_t kBiasRow = 64 * 4;     // a block's columns of the bias
 constexpr uint32_t kUnit = 4096;           // a 32 x 32 block of fp32, or 32 rows x 128 bytes of outputs
 
 // ----------------------------------------------------------------- PTX
@@ -200,35 +208,32 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
 
-// 32 columns of this warp's 32 lanes; the values are there after tmem_wait.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
+// 16 columns of this warp's 32 lanes; the values are there after tmem_wait16.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-        "%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(addr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
-    uint32_t r[16];
+// All loads of this warp have completed.  The values pass through, so that no use of them can
+// be moved ahead of the wait.
+__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float* v) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Four floats at `addr` of CTA q's shared memory; parts == 1: this CTA's.
@@ -245,6 +250,10 @@ __device__ __forceinline__ float4 ld_part(uint32_t addr, uint32_t q, uint32_t pa
                      : "r"(in_cta(addr, q))
                      : "memory");
     return v;
+}
+
+__device__ __forceinline__ void st_shared1(uint32_t addr, float a) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
 }
 
 __device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, float c, float d) {
@@ -265,122 +274,18 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool kmajor, uin
 __device__ __forceinline__ uint32_t unit_at(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
 // ----------------------------------------------------------------- epilogue
-// Eight outputs of one row, columns c .. c + 7, from their sums: vectors where `vec`.
-__device__ __forceinline__ void finish8(const ProdEpilogue& e, const float (&s)[8], const float (&bias)[8],
-                                        const float (&res)[8], uint64_t row, uint32_t c, uint32_t cols, bool vec) {
-    float z[8], y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = fmaf(e.alpha, s[i], bias[i]);
-    const uint64_t at = row * e.ldo + c;
-    if (e.act == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = z[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = act_fwd(e.act, z[i]);
-    }
-    if (e.res) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(e.beta, res[i], y[i]);
-    }
-    if (vec) {
-        if (e.pre) {
-            if (e.out_dtype)
-                store8_global<uint16_t>(e.pre, at, z);
-            else
-                store8_global<float>(e.pre, at, z);
-        }
-        if (e.out_dtype)
-            store8_global<uint16_t>(e.out, at, y);
-        else
-            store8_global<float>(e.out, at, y);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < cols) {
-                if (e.pre) put(e.pre, at + i, e.out_dtype, z[i]);
-                put(e.out, at + i, e.out_dtype, y[i]);
-            }
-    }
-}
-
-__device__ __forceinline__ void load_res8(const ProdEpilogue& e, float (&res)[8], uint64_t row, uint32_t c, uint32_t cols,
-                                          bool vec) {
-    if (!e.res) return;
-    const uint64_t at = row * e.ldr + c;
-    if (vec) {
-        if (e.out_dtype)
-            plain_vec8(static_cast<const uint16_t*>(e.res) + at, res);
-        else
-            plain_vec8(static_cast<const float*>(e.res) + at, res);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) res[i] = c + i < cols ? elem(e.res, at + i, e.out_dtype) : 0.0f;
-    }
-}
-
-// A 32 x 32 unit of sums at `unit` (of each of `parts` CTAs' shared memory; 1: this CTA's)
-// with its corner at (row0, col0): lane = 8 columns of rows lane / 4 + 8 i.
-__device__ __forceinline__ void finish_unit(const TcArgs& a, uint32_t unit, uint32_t parts, uint32_t row0, uint32_t col0) {
-    const int lane = threadIdx.x % 32;
-    const uint32_t c = col0 + (lane % 4) * 8;
-    if (c >= a.cols) return;
-    const bool vec = a.vec && c + 8 <= a.cols;
-    float bias[8] = {};
-    if (a.e.bias)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = c + i < a.cols ? elem(a.e.bias, c + i, a.e.bias_dtype) : 0.0f;
-    float res[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t row = row0 + lane / 4 + 8 * i;
-        if (row < a.rows) load_res8(a.e, res[i], row, c, a.cols, vec);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = lane / 4 + 8 * i, row = row0 + r, j = (lane % 4) * 2;
-        if (row >= a.rows) continue;
-        float s[8] = {};
-        for (uint32_t q = 0; q < parts; ++q) {
-            const float4 u = ld_part(unit + unit_at(r, j), q, parts), v = ld_part(unit + unit_at(r, j + 1), q, parts);
-            s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
-            s[4] += v.x; s[5] += v.y; s[6] += v.z; s[7] += v.w;
-        }
-        finish8(a.e, s, bias, res[i], row, c, a.cols, vec);
-    }
-}
-
-// kSwap: lane = one output column (P row), the unit's columns = output rows.
-__device__ __forceinline__ void finish_unit_swapped(const TcArgs& a, uint32_t unit, uint32_t parts, uint32_t prow0,
-                                                    uint32_t qrow0, uint32_t qcount) {
-    const uint32_t lane = threadIdx.x % 32, col = prow0 + lane;
-    if (col >= a.cols) return;
-    const float bias = a.e.bias ? elem(a.e.bias, col, a.e.bias_dtype) : 0.0f;
-    for (uint32_t j = 0; j * 4 < qcount; ++j) {
-        float s[4] = {};
-        for (uint32_t q = 0; q < parts; ++q) {
-            const float4 u = ld_part(unit + unit_at(lane, j), q, parts);
-            s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t row = qrow0 + j * 4 + i;
-            if (row >= a.rows) break;
-            const float z = fmaf(a.e.alpha, s[i], bias);
-            const uint64_t at = row * a.e.ldo + col;
-            if (a.e.pre) put(a.e.pre, at, a.e.out_dtype, z);
-            float y = act_fwd(a.e.act, z);
-            if (a.e.res) y = fmaf(a.e.beta, elem(a.e.res, row * a.e.ldr + col, a.e.out_dtype), y);
-            put(a.e.out, at, a.e.out_dtype, y);
-        }
-    }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // Outputs by TMA: a drain warp's tile part is cut into blocks of 32 rows x 128 bytes, each in
 // one of the warp's `slots` buffers.  Without `pre`, a block's residual is loaded into its
-// buffer slots - 1 blocks ahead (so that HBM-bound products keep some 100 KB of loads in
-// flight per SM), replaced by the output in place and stored from there.  With `pre`, buffer 0
-// holds it, buffer 1 the output, and the residual is read directly.
+// buffer up to slots - 1 blocks ahead (so that HBM-bound products keep some 100 KB of loads in
+// flight per SM), replaced by the output in place and stored from there.  With `pre`, the
+// block is read from TMEM twice: for `pre`, then for the output, whose residual is read
+// directly.
 struct OutWarp {
     uint32_t buf, bar, slots;      // this warp's buffers and their load barriers
     uint32_t issued, block;        // loads issued; blocks finished
@@ -405,69 +310,174 @@ __device__ __forceinline__ void load_ahead(const TcArgs& a, OutWarp& o, uint32_t
     }
 }
 
-// 32 columns of one row (this lane's), sums in v, to 16-byte pieces first, first + 1, ... of
-// the row's 128 bytes.  bias: 32 floats in shared memory.
+// 16 columns of one row (this lane's), sums in v, to the row's 16-byte pieces piece0, ... of
+// the output's buffer, which holds the residual there if res_here.  bias: the columns' floats
+// in shared memory.  In stages over the 16 values, each stage's choice made once: the code has
+// to be small, since a launch starts with a cold instruction cache.
 template <bool kBf16>
-__device__ __forceinline__ void finish_row(const TcArgs& a, const float (&v)[32], uint32_t bias, uint32_t out, uint32_t pre,
-                                           uint32_t piece0, uint32_t row, uint32_t col, bool res_here) {
-    constexpr int kPer = kBf16 ? 8 : 4;       // elements per piece
+__device__ __forceinline__ void store_row(uint32_t at, uint32_t piece0, const float (&v)[16]) {
+    const uint32_t lane = threadIdx.x % 32;
+    if constexpr (kBf16) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            st_shared4u(at + unit_at(lane, piece0 + p), pack2(v[8 * p], v[8 * p + 1]), pack2(v[8 * p + 2], v[8 * p + 3]),
+                        pack2(v[8 * p + 4], v[8 * p + 5]), pack2(v[8 * p + 6], v[8 * p + 7]));
+    } else {
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            st_shared4(at + unit_at(lane, piece0 + p), v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+    }
+}
+
+template <int kN>
+__device__ __forceinline__ void activate(int act, float (&v)[kN]) {
+    if (act == kActRelu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActRelu, v[i]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActGelu, v[i]);
+    } else if (act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActSilu, v[i]);
+    }
+}
+
+__device__ __forceinline__ void finish_row(const TcArgs& a, float (&v)[16], uint32_t bias, uint32_t out, uint32_t piece0,
+                                           uint32_t row, uint32_t col, bool res_here, bool pre) {
     const uint32_t lane = threadIdx.x % 32;
     const ProdEpilogue& e = a.e;
+    const bool bf16 = e.out_dtype != 0;
+    if (e.bias) {
 #pragma unroll
-    for (int p = 0; p < 32 / kPer; ++p) {
-        const uint32_t at = unit_at(lane, piece0 + p);
-        float y[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) y[i] = e.alpha * v[p * kPer + i];
-        if (e.bias)
-#pragma unroll
-            for (int i = 0; i < kPer; i += 4) {
-                const uint4 b = ld_shared4u(bias + (p * kPer + i) * 4);
-                y[i] += __uint_as_float(b.x);
-                y[i + 1] += __uint_as_float(b.y);
-                y[i + 2] += __uint_as_float(b.z);
-                y[i + 3] += __uint_as_float(b.w);
-            }
-        if (e.pre && pre == out) {            // one buffer, which is the output's
-            const uint32_t c = col + p * kPer;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (row < a.rows && c + i < a.cols) put(e.pre, row * e.ldo + c + i, e.out_dtype, y[i]);
-        } else if (e.pre) {
-            if constexpr (kBf16)
-                st_shared4u(pre + at, pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-            else
-                st_shared4(pre + at, y[0], y[1], y[2], y[3]);
+        for (int i = 0; i < 16; i += 4) {
+            const uint4 b = ld_shared4u(bias + i * 4);
+            v[i] = fmaf(e.alpha, v[i], __uint_as_float(b.x));
+            v[i + 1] = fmaf(e.alpha, v[i + 1], __uint_as_float(b.y));
+            v[i + 2] = fmaf(e.alpha, v[i + 2], __uint_as_float(b.z));
+            v[i + 3] = fmaf(e.alpha, v[i + 3], __uint_as_float(b.w));
         }
-        if (e.act)
+    } else {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) y[i] = act_fwd(e.act, y[i]);
-        if (e.res) {
-            float r[8];
-            if (res_here) {
-                const uint4 q = ld_shared4u(out + at);
-                if constexpr (kBf16) {
-                    r[0] = bf16_lo(q.x); r[1] = bf16_hi(q.x); r[2] = bf16_lo(q.y); r[3] = bf16_hi(q.y);
-                    r[4] = bf16_lo(q.z); r[5] = bf16_hi(q.z); r[6] = bf16_lo(q.w); r[7] = bf16_hi(q.w);
-                } else {
-                    r[0] = __uint_as_float(q.x); r[1] = __uint_as_float(q.y);
-                    r[2] = __uint_as_float(q.z); r[3] = __uint_as_float(q.w);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const uint32_t c = col + p * kPer + i;
-                    r[i] = row < a.rows && c < a.cols ? elem(e.res, row * e.ldr + c, e.out_dtype) : 0.0f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) y[i] = fmaf(e.beta, r[i], y[i]);
-        }
-        if constexpr (kBf16)
-            st_shared4u(out + at, pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        else
-            st_shared4(out + at, y[0], y[1], y[2], y[3]);
+        for (int i = 0; i < 16; ++i) v[i] *= e.alpha;
     }
+    if (!pre) {
+    activate(e.act, v);
+    if (e.res) {
+        if (!res_here) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (row < a.rows && col + i < a.cols)
+                    v[i] = fmaf(e.beta, elem(e.res, row * e.ldr + col + i, e.out_dtype), v[i]);
+        } else if (bf16) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint4 q = ld_shared4u(out + unit_at(lane, piece0 + p));
+                v[8 * p] = fmaf(e.beta, bf16_lo(q.x), v[8 * p]);
+                v[8 * p + 1] = fmaf(e.beta, bf16_hi(q.x), v[8 * p + 1]);
+                v[8 * p + 2] = fmaf(e.beta, bf16_lo(q.y), v[8 * p + 2]);
+                v[8 * p + 3] = fmaf(e.beta, bf16_hi(q.y), v[8 * p + 3]);
+                v[8 * p + 4] = fmaf(e.beta, bf16_lo(q.z), v[8 * p + 4]);
+                v[8 * p + 5] = fmaf(e.beta, bf16_hi(q.z), v[8 * p + 5]);
+                v[8 * p + 6] = fmaf(e.beta, bf16_lo(q.w), v[8 * p + 6]);
+                v[8 * p + 7] = fmaf(e.beta, bf16_hi(q.w), v[8 * p + 7]);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint4 q = ld_shared4u(out + unit_at(lane, piece0 + p));
+                v[4 * p] = fmaf(e.beta, __uint_as_float(q.x), v[4 * p]);
+                v[4 * p + 1] = fmaf(e.beta, __uint_as_float(q.y), v[4 * p + 1]);
+                v[4 * p + 2] = fmaf(e.beta, __uint_as_float(q.z), v[4 * p + 2]);
+                v[4 * p + 3] = fmaf(e.beta, __uint_as_float(q.w), v[4 * p + 3]);
+            }
+        }
+    }
+    }
+    if (bf16)
+        store_row<true>(out, piece0, v);
+    else
+        store_row<false>(out, piece0, v);
+}
+
+// Eight output elements of one row from a unit: lane = columns 8 (lane % 4) of row
+// lane / 4 + 8 `part`.  `parts` CTAs hold a share of the sums (1: this CTA's shared memory).
+__device__ __forceinline__ void finish_item(const TcArgs& a, uint32_t unit, uint32_t part, uint32_t parts, uint32_t row0,
+                                            uint32_t col0) {
+    const uint32_t lane = threadIdx.x % 32, r = lane / 4 + 8 * part, j = (lane % 4) * 2;
+    const uint32_t row = row0 + r, c = col0 + j * 4;
+    if (row >= a.rows || c >= a.cols) return;
+    const ProdEpilogue& e = a.e;
+    const bool vec = a.vec && c + 8 <= a.cols, bf16 = e.out_dtype != 0;
+    float res[8] = {}, v[8] = {};
+    if (e.res) {
+        const uint64_t at = row * e.ldr + c;
+        if (vec && bf16)
+            plain_vec8(static_cast<const uint16_t*>(e.res) + at, res);
+        else if (vec)
+            plain_vec8(static_cast<const float*>(e.res) + at, res);
+        else
+            for (int i = 0; i < 8; ++i)
+                if (c + i < a.cols) res[i] = elem(e.res, at + i, e.out_dtype);
+    }
+    float bias[8] = {};
+    if (e.bias)
+        for (int i = 0; i < 8; ++i)
+            if (c + i < a.cols) bias[i] = elem(e.bias, c + i, e.bias_dtype);
+    for (uint32_t q = 0; q < parts; ++q) {
+        const float4 x = ld_part(unit + unit_at(r, j), q, parts), y = ld_part(unit + unit_at(r, j + 1), q, parts);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    const uint64_t at = row * e.ldo + c;
+    auto write = [&](void* p) {
+        if (vec && bf16)
+            store8_global<uint16_t>(p, at, v);
+        else if (vec)
+            store8_global<float>(p, at, v);
+        else
+            for (int i = 0; i < 8; ++i)
+                if (c + i < a.cols) put(p, at + i, e.out_dtype, v[i]);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(e.alpha, v[i], bias[i]);
+    if (e.pre) write(e.pre);
+    activate(e.act, v);
+    if (e.res)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.beta, res[i], v[i]);
+    write(e.out);
+}
+
+// kSwap: lane = one output column (P row); four output rows, columns 4 `part` of the unit.
+__device__ __forceinline__ void finish_item_swapped(const TcArgs& a, uint32_t unit, uint32_t part, uint32_t parts,
+                                                    uint32_t prow0, uint32_t qrow0) {
+    const uint32_t lane = threadIdx.x % 32, col = prow0 + lane, row0 = qrow0 + part * 4;
+    if (col >= a.cols || row0 >= a.rows) return;
+    const ProdEpilogue& e = a.e;
+    const float bias = e.bias ? elem(e.bias, col, e.bias_dtype) : 0.0f;
+    float res[4] = {}, v[4] = {};
+    if (e.res)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row0 + i < a.rows) res[i] = elem(e.res, (row0 + i) * e.ldr + col, e.out_dtype);
+    for (uint32_t q = 0; q < parts; ++q) {
+        const float4 x = ld_part(unit + unit_at(lane, part), q, parts);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    }
+    auto write = [&](void* p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row0 + i < a.rows) put(p, (row0 + i) * e.ldo + col, e.out_dtype, v[i]);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(e.alpha, v[i], bias);
+    if (e.pre) write(e.pre);
+    activate(e.act, v);
+    if (e.res)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(e.beta, res[i], v[i]);
+    write(e.out);
 }
 
 // ----------------------------------------------------------------- kernel
@@ -475,16 +485,16 @@ template <int kCtas, int kBN, bool kDrain, bool kSwap>
 __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(const __grid_constant__ TcArgs a) {
     constexpr int kQRows = kBN / kCtas;                     // rows of Q that this CTA loads
     constexpr uint32_t kQBytes = kQRows * kBK * 2;
-    constexpr int kHalf = kBN >= 128 ? kBN / 2 : kBN;       // columns drained by one warp
-    constexpr int kHalves = kBN / kHalf;                    // warps sharing a lane quadrant
-    constexpr int kChunkCols = kHalf < 32 ? kHalf : 32;
-    constexpr int kChunks = kHalf / kChunkCols;
+    constexpr int kWarps = kDrainWarps<kBN>, kLoadWarp = kWarps, kMmaWarp = kWarps + 1;
+    constexpr int kHalves = drain_parts(kBN, kSwap);
+    constexpr int kHalf = kBN / kHalves;                            // columns of each
+    constexpr int kUnitCols = kHalf < 32 ? kHalf : 32;      // of a unit of the split exchange
+    constexpr int kPieces = kHalf / 16;                     // 16 columns at a time
     constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
-    extern __shared__ uint8_t dyn[];
-    __shared__ uint64_t bars[2 * kTcMaxStages + 4 + kDrainWarps * kTcMaxSlots];
-    __shared__ __align__(16) float bias_rows[kDrainWarps][32];
+    extern __shared__ __align__(1024) uint8_t dyn[];     // stages, output buffers, bias rows
+    __shared__ uint64_t bars[2 * kTcMaxStages + 4 + kWarps * kTcMaxSlots];
     __shared__ uint32_t tmem_slot, gone_flag;
-    const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
+    const uint32_t base = smem_addr(dyn);
     const uint32_t full = smem_addr(&bars[0]), empty = smem_addr(&bars[kTcMaxStages]);
     const uint32_t acc_full = smem_addr(&bars[2 * kTcMaxStages]), acc_empty = acc_full + 16;
     const uint32_t res_bars = acc_full + 32;
@@ -495,7 +505,14 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
     const bool leader = kCtas == 1 || rank == 0;
     const uint32_t gone = smem_addr(&gone_flag), ctas = kCtas == 2 ? 2 : a.splits;
 
-    if (warp == 8 && lane == 0) {
+    // The next kernel on the stream may set itself up while this one runs; it, as this one,
+    // waits for its predecessor's end before it touches global memory.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.map_p) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.map_q) : "memory");
+    }
+    if (warp == kLoadWarp && lane == 0) {
         for (uint32_t s = 0; s < a.stages; ++s) {
             bar_init(full + 8 * s, 1);
             bar_init(empty + 8 * s, 1);
@@ -504,16 +521,17 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             bar_init(acc_full + 8 * b, 1);
             bar_init(acc_empty + 8 * b, kCtas * kHalves * 4);
         }
-        for (uint32_t i = 0; i < kDrainWarps * kTcMaxSlots; ++i) bar_init(res_bars + 8 * i, 1);
+        for (uint32_t i = 0; i < kWarps * kTcMaxSlots; ++i) bar_init(res_bars + 8 * i, 1);
         gone_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc<kCtas>(smem_addr(&tmem_slot), kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc<kCtas>(smem_addr(&tmem_slot), kTmemCols);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (kCtas == 2 || a.splits > 1) cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // this cluster's tiles, and this CTA's blocks of the summed index
     const uint32_t group = kCtas == 2 ? 2 : a.splits;
@@ -522,9 +540,9 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
     const uint32_t kb1 = static_cast<uint64_t>(a.kblocks) * (split + 1) / a.splits;
     bool ok = true;                      // of this thread: no wait gave up
 
-    if (warp >= 8) {
-        if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8 && elect_one()) {
+    if (warp >= kWarps) {
+        if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kLoadWarp && elect_one()) {
             const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
             uint32_t s = 0, phase = 1;          // the first round of stages is free
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
@@ -559,7 +577,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                     }
                 }
             }
-        } else if (warp == 9 && leader && elect_one()) {
+        } else if (warp == kMmaWarp && leader && elect_one()) {
             const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (a.p_kmajor ? 0u : 1u << 15) |
                                    (a.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 | (128 * kCtas / 16) << 24;
             const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
@@ -623,10 +641,10 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
         }
         __syncwarp();
     } else if (warp / 4 < kHalves) {
-        if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const uint32_t quad = warp % 4, half = warp / 4;
         const uint32_t mine = tmem + (quad << 21) + half * kHalf;    // lane 32 quad, column half * kHalf
-        const uint32_t bias_at = smem_addr(bias_rows[warp]);
+        const uint32_t bias_at = base + a.stages * stage_bytes + 4 * kHalves * a.slots * kUnit + warp * kBiasRow;
         const bool bf16 = a.e.out_dtype != 0;
         const uint32_t width = bf16 ? 64 : 32;           // columns of a block of outputs
         const bool by_tma = !kSwap && a.vec && a.splits == 1;
@@ -647,30 +665,39 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             const TcTile tile = tc_tile(a, t);
             const uint32_t prow = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0) + quad * 32;
             const uint32_t qrow = tile.q * kBN + half * kHalf;
-            float acc[kDrain ? kHalf : 1];
             if constexpr (kDrain) {
+                // all chunks but the last are summed in registers; the sums join the last one
+                // in TMEM, from where the tile is finished
+                const uint32_t chunks = (kb1 - kb0 + a.chunk_kb - 1) / a.chunk_kb;
+                float acc[kHalf];
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) acc[i] = 0.0f;
-                for (uint32_t kb = kb0; kb < kb1; kb += a.chunk_kb, ++ch) {
+                for (uint32_t n = 1; n <= chunks; ++n) {
                     const uint32_t b = ch & 1;
                     if (!bar_wait(acc_full + 8 * b, (ch / 2) & 1, gone, ctas)) {
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (chunks == 1) break;
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        float v[kChunkCols];
-                        if constexpr (kChunkCols == 32)
-                            tmem_ld32(mine + b * kBN + c * 32, v);
-                        else
-                            tmem_ld16(mine + b * kBN, v);
+                    for (int c = 0; c < kPieces; ++c) {
+                        float v[16];
+                        tmem_ld16(mine + b * kBN + c * 16, v);
+                        tmem_wait16(v);
 #pragma unroll
-                        for (int i = 0; i < kChunkCols; ++i) acc[c * kChunkCols + i] += v[i];
+                        for (int i = 0; i < 16; ++i) acc[c * 16 + i] += v[i];
                     }
+                    if (n == chunks) break;
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
+                    ++ch;
+                }
+                if (chunks > 1) {
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c) tmem_st16(mine + (ch & 1) * kBN + c * 16, acc + c * 16);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
             } else {
                 if (!bar_wait(acc_full + 8 * (ch & 1), (ch / 2) & 1, gone, ctas)) ok = false;
@@ -679,85 +706,85 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             const uint32_t b = ch & 1;
+            const auto release = [&] {       // this warp has read the accumulator
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
+            };
+            if (!kSwap && by_tma) {
+#pragma unroll 1
+                for (uint32_t blk = 0; blk < o.blocks; ++blk, ++o.block) {
+                    const uint32_t slot = o.block % o.slots, out = o.buf + slot * kUnit, col = qrow + blk * width;
+                    if (a.e.bias)
+                        for (uint32_t i = lane; i < width; i += 32)
+                            st_shared1(bias_at + i * 4, col + i < a.cols ? elem(a.e.bias, col + i, a.e.bias_dtype) : 0.0f);
+#pragma unroll 1
+                    for (int pre = a.e.pre != nullptr; pre >= 0; --pre) {
+                        // the block's buffer: its residual has come, or its last store has left
+                        if (o.ahead)
+                            ok = bar_wait(o.bar + 8 * slot, (o.block / o.slots) & 1, gone, ctas);
+                        else if (lane == 0 && (o.slots == 1 || a.e.pre))
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        else if (lane == 0)
+                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
+                        float v[16], next[16] = {};
+                        tmem_ld16(mine + b * kBN + blk * width, v);
+                        tmem_wait16(v);
+#pragma unroll 1
+                        for (uint32_t in = 0; in < width; in += 16) {
+                            if (in + 16 < width)
+                                tmem_ld16(mine + b * kBN + blk * width + in + 16, next);
+                            else if (blk + 1 == o.blocks && !pre)
+                                release();
+                            finish_row(a, v, bias_at + in * 4, out, in * (bf16 ? 2 : 4) / 16, prow + lane, col + in, o.ahead, pre);
+                            tmem_wait16(next);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                float v[kChunkCols];
-                if constexpr (kDrain) {
-#pragma unroll
-                    for (int i = 0; i < kChunkCols; ++i) v[i] = acc[c * kChunkCols + i];
-                } else if constexpr (kChunkCols == 32) {
-                    tmem_ld32(mine + b * kBN + c * 32, v);
-                } else {
-                    tmem_ld16(mine + b * kBN, v);
-                }
-                if (!kDrain && c == kChunks - 1) {
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
-                }
-                if constexpr (!kSwap && kChunkCols == 32) {
-                    if (by_tma) {
-                        const uint32_t col = qrow + c * 32, part = bf16 ? c % 2 : 0;
-                        const bool two = a.e.pre && o.slots > 1;
-                        const uint32_t slot = two ? 1 : o.block % o.slots;
-                        const uint32_t out = o.buf + slot * kUnit;
-                        if (part == 0) {
-                            // the block's buffer: its residual has come, or its last store has left
+                            for (int i = 0; i < 16; ++i) v[i] = next[i];
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (prow < a.rows && col < a.cols) tma_store_2d(pre ? &a.map_pre : &a.map_out, out, col, prow);
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                             if (o.ahead) {
-                                ok = bar_wait(o.bar + 8 * slot, (o.block / o.slots) & 1, gone, ctas);
-                            } else if (lane == 0) {
-                                if (two || o.slots == 1)
+                                if (o.slots == 1)
                                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                                 else
                                     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                                load_ahead<kCtas, kBN>(a, o, o.block + (o.slots > 1 ? o.slots : 2), first, step, width, rank);
                             }
                         }
-                        if (a.e.bias)
-                            bias_rows[warp][lane] = col + lane < a.cols ? elem(a.e.bias, col + lane, a.e.bias_dtype) : 0.0f;
-                        __syncwarp();
-                        if (bf16)
-                            finish_row<true>(a, v, bias_at, out, o.buf, part * 4, prow + lane, col, o.ahead);
-                        else
-                            finish_row<false>(a, v, bias_at, out, o.buf, 0, prow + lane, col, o.ahead);
-                        if (!bf16 || part == 1) {
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                            if (lane == 0) {
-                                const uint32_t c0 = bf16 ? col - 32 : col;
-                                if (prow < a.rows && c0 < a.cols) {
-                                    if (two) tma_store_2d(&a.map_pre, o.buf, c0, prow);
-                                    tma_store_2d(&a.map_out, out, c0, prow);
-                                }
-                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                                if (o.ahead) {
-                                    if (o.slots == 1)
-                                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                                    else
-                                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                                    load_ahead<kCtas, kBN>(a, o, o.block + (o.slots > 1 ? o.slots : 2), first, step, width, rank);
-                                }
-                            }
-                            ++o.block;
-                        }
-                        __syncwarp();
-                        continue;
                     }
                 }
-                // unit order of the split exchange: [quad][half][chunk]
-                const uint32_t unit = a.splits > 1 ? base + ((quad * kHalves + half) * kChunks + c) * kUnit : stage_unit;
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < kPieces; ++c) {
+                    float v[16];
+                    tmem_ld16(mine + b * kBN + c * 16, v);
+                    tmem_wait16(v);
+                    if (c == kPieces - 1) release();
+                    // by units of 32 rows x kUnitCols columns, in the exchange's order [quad][half][unit]
+                    const uint32_t u = c * 16 / kUnitCols;
+                    const uint32_t unit =
+                        a.splits > 1 ? base + ((quad * kHalves + half) * (kHalf / kUnitCols) + u) * kUnit : stage_unit;
+                    const uint32_t j0 = c * 16 % kUnitCols / 4;
 #pragma unroll
-                for (int j = 0; j < kChunkCols / 4; ++j)
-                    st_shared4(unit + unit_at(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                if (a.splits == 1) {
-                    __syncwarp();
-                    if constexpr (kSwap)
-                        finish_unit_swapped(a, unit, 1, prow, qrow + c * 32, kChunkCols);
-                    else
-                        finish_unit(a, unit, 1, prow, qrow + c * 32);
-                    __syncwarp();
+                    for (int j = 0; j < 4; ++j)
+                        st_shared4(unit + unit_at(lane, j0 + j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    if (a.splits == 1 && (c + 1) * 16 % kUnitCols == 0) {
+                        __syncwarp();
+#pragma unroll 1
+                        for (uint32_t i = 0; i < (kSwap ? kUnitCols / 4 : 4); ++i)
+                            if constexpr (kSwap)
+                                finish_item_swapped(a, unit, i, 1, prow, qrow + u * 32);
+                            else
+                                finish_item(a, unit, i, 1, prow, qrow + u * 32);
+                        __syncwarp();
+                    }
                 }
             }
-            if constexpr (!kDrain) ++ch;
+            ++ch;
             ok = __all_sync(~0u, ok);
         }
         if (lane == 0) {
@@ -773,22 +800,23 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
     __syncthreads();
     if (kCtas == 2 || a.splits > 1) cluster_sync();
     if (kCtas == 1 && a.splits > 1) {
-        // every CTA's part of the one tile is in place: this CTA finishes its share of the units
-        if (warp < kDrainWarps) {
+        // every CTA's part of the one tile is in place: this CTA finishes its share of the rows
+        if (warp < kWarps) {
             const TcTile tile = tc_tile(a, first);
-            constexpr uint32_t kUnits = 4 * kHalves * kChunks;
-            for (uint32_t u = rank + a.splits * warp; u < kUnits; u += a.splits * kDrainWarps) {
-                const uint32_t quad = u / (kHalves * kChunks), rest = u % (kHalves * kChunks);
-                const uint32_t prow = tile.p * 128 + quad * 32, qrow = tile.q * kBN + rest * kChunkCols;
+            constexpr uint32_t kPerQuad = kBN / kUnitCols, kItems = kSwap ? kUnitCols / 4 : 4;
+#pragma unroll 1
+            for (uint32_t x = rank + a.splits * warp; x < 4 * kPerQuad * kItems; x += a.splits * kWarps) {
+                const uint32_t u = x / kItems, i = x % kItems;
+                const uint32_t prow = tile.p * 128 + u / kPerQuad * 32, qrow = tile.q * kBN + u % kPerQuad * kUnitCols;
                 if constexpr (kSwap)
-                    finish_unit_swapped(a, base + u * kUnit, a.splits, prow, qrow, kChunkCols);
+                    finish_item_swapped(a, base + u * kUnit, i, a.splits, prow, qrow);
                 else
-                    finish_unit(a, base + u * kUnit, a.splits, prow, qrow);
+                    finish_item(a, base + u * kUnit, i, a.splits, prow, qrow);
             }
         }
         cluster_sync();
     }
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         tmem_free<kCtas>(tmem, kTmemCols);
     }
@@ -800,7 +828,7 @@ struct Config {
     bool swap;
 };
 constexpr Config kConfigs[kTcConfigs] = {{2, 256, false}, {1, 128, false}, {1, 64, false},
-                                         {1, 64, true},   {1, 32, true},   {1, 16, true}};
+                                         {1, 64, true},   {1, 32, true},   {1, 16, true}, {2, 128, false}};
 using Kernel = void (*)(TcArgs);
 const Kernel kKernels[kTcConfigs][2] = {
     {product_tc_kernel<2, 256, false, false>, product_tc_kernel<2, 256, true, false>},
@@ -808,9 +836,15 @@ const Kernel kKernels[kTcConfigs][2] = {
     {product_tc_kernel<1, 64, false, false>, product_tc_kernel<1, 64, true, false>},
     {product_tc_kernel<1, 64, false, true>, product_tc_kernel<1, 64, true, true>},
     {product_tc_kernel<1, 32, false, true>, product_tc_kernel<1, 32, true, true>},
-    {product_tc_kernel<1, 16, false, true>, product_tc_kernel<1, 16, true, true>}};
+    {product_tc_kernel<1, 16, false, true>, product_tc_kernel<1, 16, true, true>},
+    {product_tc_kernel<2, 128, false, false>, product_tc_kernel<2, 128, true, false>}};
 
-constexpr uint32_t kSmemMost = 230400;    // dynamic shared memory a CTA may take, with room for the static part
+constexpr int kTcThreads[kTcConfigs][2] = {{kThreads<256, false>, kThreads<256, true>}, {kThreads<128, false>, kThreads<128, true>},
+                                       {kThreads<64, false>, kThreads<64, true>},   {kThreads<64, false>, kThreads<64, true>},
+                                       {kThreads<32, false>, kThreads<32, true>},   {kThreads<16, false>, kThreads<16, true>},
+                                            {kThreads<128, false>, kThreads<128, true>}};
+
+constexpr uint32_t kSmemMost = 231424;    // dynamic: 227 KB less 1 KB, which the static part begins
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -890,28 +924,29 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.group = 8;
     a.splits = c.ctas == 2 ? 1 : p.splits;
     if (a.splits > a.kblocks) a.splits = a.kblocks;
-    a.chunk_kb = P.planes + Q.planes > 2 ? 1 : 2;
+    a.chunk_kb = P.planes + Q.planes > 2 ? 1 : 4;
     auto vec = [&](const void* q, uint64_t ld) { return !q || out_ready(q, ld, a.e.out_dtype); };
     a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
     const bool by_tma = a.vec && a.splits == 1 && !c.swap;
     if (by_tma && !(encode_out(&a.map_out, a.e.out, a.e.ldo, a) && (!a.e.pre || encode_out(&a.map_pre, a.e.pre, a.e.ldo, a)) &&
                     (!a.e.res || encode_out(&a.map_res, a.e.res, a.e.ldr, a))))
         return cudaErrorInvalidValue;
-    // Short sums are bound by the output side: more residual blocks ahead.  Operands of three
-    // planes fill shared memory: one block, so that two stages fit.
     const uint32_t stage = P.planes * kPBytes + Q.planes * qrows * kBK * 2;
-    const uint32_t warps = c.bn >= 128 ? 8 : 4;
-    a.slots = by_tma && a.e.res && !a.e.pre && a.kblocks <= 4 ? kTcMaxSlots : 2;
-    if (1024 + warps * a.slots * kUnit + 2 * stage > kSmemMost) a.slots = 1;
-    const uint32_t extra = 1024 + (a.splits == 1 ? warps * a.slots * kUnit : 0);
-    // two CTAs per SM for the forms that take few registers
-    const uint32_t occupancy = c.swap && !drain ? 2 : 1;
-    uint32_t stages = (kSmemMost / occupancy - 1024 * (occupancy - 1) - extra) / stage;
+    const uint32_t warps = 4 * drain_parts(c.bn, c.swap);
+    // Short sums with a residual are bound by the output side: more blocks ahead.  Else as many
+    // stages as fit.
+    a.slots = c.swap ? 1 : by_tma && a.e.res && !a.e.pre && a.kblocks <= 4 ? (c.bn == 256 ? 2 : kTcMaxSlots) : c.bn == 256 ? 1 : 2;
+    if (warps * (a.slots * kUnit + kBiasRow) + 2 * stage > kSmemMost) a.slots = 1;
+    const uint32_t extra = a.splits == 1 ? warps * (a.slots * kUnit + kBiasRow) : 0;
+    // two CTAs per SM for the forms that take few registers, if each has four stages
+    const auto fit = [&](uint32_t ctas) { return (kSmemMost / ctas - 2048 * (ctas - 1) - extra) / stage; };
+    const uint32_t occupancy = c.swap && !drain && fit(2) >= 4 ? 2 : 1;
+    uint32_t stages = fit(occupancy);
     if (stages > static_cast<uint32_t>(kTcMaxStages)) stages = kTcMaxStages;
     if (stages < 1) return cudaErrorInvalidValue;
     a.stages = stages;
     uint32_t smem = extra + stages * stage;
-    if (a.splits > 1 && smem < 1024 + 128 * c.bn * 4) smem = 1024 + 128 * c.bn * 4;
+    if (a.splits > 1 && smem < 128u * c.bn * 4) smem = 128 * c.bn * 4;
     a.err = err;
     a.test_expire = test_expire;
     const uint32_t per = c.ctas == 2 ? 2 : a.splits;
@@ -922,15 +957,17 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * per);
-    cfg.blockDim = dim3(c.bn == 256 && drain ? kThreads<256, true> : kThreads<128, false>);
+    cfg.blockDim = dim3(kTcThreads[p.cfg][drain]);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = per;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = per;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = per > 1 ? 1 : 0;
+    cfg.numAttrs = per > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kKernels[p.cfg][drain], a);
 }
 

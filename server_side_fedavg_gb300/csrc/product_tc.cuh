@@ -9,7 +9,7 @@ namespace fa {
 
 constexpr int kTcMaxStages = 8;
 constexpr int kTcMaxSlots = 4;
-constexpr int kTcConfigs = 6;
+constexpr int kTcConfigs = 7;
 
 // Kernel configurations (rows x columns of a tile of the output).
 enum TcConfig {
@@ -19,6 +19,7 @@ enum TcConfig {
     kTcSwap64 = 3,      // 64 x 128, tokens in the MMA's columns
     kTcSwap32 = 4,      // 32 x 128
     kTcSwap16 = 5,      // 16 x 128
+    kTcPair128 = 6,     // 256 x 128 on two SMs
 };
 
 // An operand the kernel can read: bf16, base and row stride multiples of 16 bytes.

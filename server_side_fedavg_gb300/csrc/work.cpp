@@ -224,24 +224,39 @@ fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, 
     return launched(w, fa::launch_split(o.p, o.ld, o.dtype, rows, cols, planes, dst, ldd, s), "operand layout");
 }
 
-// Tile configuration and split of the summed index.  sms CTAs fill the GPU once.
+// Tile configuration and split of the summed index: the one that needs the fewest steps, a
+// step being one block of 64 summed elements on the CTA with the most work.
 void choose(fa::TcProduct* p, int sms) {
     const auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
-    const uint64_t kb = up(p->k, 64);
+    const uint64_t kb = up(p->k, 64), n_sm = static_cast<uint64_t>(sms);
     p->drain = p->e.out_dtype == 0;
     p->splits = 1;
     if (p->m <= 64 && (p->a.kmajor || p->m > 32)) {
         p->cfg = p->m <= 16 ? fa::kTcSwap16 : p->m <= 32 ? fa::kTcSwap32 : fa::kTcSwap64;
-    } else if (up(p->m, 256) * up(p->n, 256) * 2 >= static_cast<uint64_t>(sms)) {
-        p->cfg = fa::kTcPair256;
-    } else {
-        p->cfg = p->n <= 64 ? fa::kTc64 : fa::kTc128;
+        const uint64_t tiles = up(p->n, 128);
+        while (p->splits < 8 && tiles * p->splits <= n_sm && kb >= p->splits * 2 * 4) p->splits *= 2;
+        return;
     }
-    if (p->cfg == fa::kTcPair256) return;
-    const uint64_t tiles = p->cfg == fa::kTc128  ? up(p->m, 128) * up(p->n, 128)
-                           : p->cfg == fa::kTc64 ? up(p->m, 128) * up(p->n, 64)
-                                                 : up(p->n, 128);
-    while (p->splits < 8 && tiles * p->splits * 2 <= static_cast<uint64_t>(2 * sms) && kb >= p->splits * 2 * 4) p->splits *= 2;
+    // cost of a tile's block, in units of an SM's MMA time for 128 x 128 x 64: a pair's tile
+    // of 256 columns takes 2; the 128-row forms are bound by operand traffic and take 1.5 / 1.2
+    // with what each tile costs besides (fill, drain, stores) in blocks
+    const uint64_t m256 = up(p->m, 256), m128 = up(p->m, 128), pairs = n_sm / 2;
+    const bool wide = p->a.planes + p->b.planes < 6;      // three planes of both: 256 columns do not fit
+    double best = 1e300;
+    const auto consider = [&](int cfg, uint64_t tiles, uint64_t room, double block, uint32_t splits) {
+        const double cost = up(tiles * splits, room) * (up(kb, splits) * block + 6.0) + (splits > 1 ? 3.0 : 0.0);
+        if (cost < best) {
+            best = cost;
+            p->cfg = cfg;
+            p->splits = splits;
+        }
+    };
+    if (wide) consider(fa::kTcPair256, m256 * up(p->n, 256), pairs, 2.0, 1);
+    consider(fa::kTcPair128, m256 * up(p->n, 128), pairs, 1.1, 1);
+    for (uint32_t s = 1; s <= 8 && kb >= s * 2; s *= 2) {
+        if (p->n > 64) consider(fa::kTc128, m128 * up(p->n, 128), n_sm, 1.5, s);
+        consider(fa::kTc64, m128 * up(p->n, 64), n_sm, 1.2, s);
+    }
 }
 
 // A product by the kernel that suits its size.  run == false only adds up the workspace.
