@@ -13,9 +13,11 @@
 // warp 9 the MMAs.  TMEM holds two accumulators, so the next tile's (or chunk's) products run
 // while one is drained.
 //
-// kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates; over thousands of
-// terms that adds up to about 1e-5.  So the accumulator is emptied every chunk_kb blocks of 64
-// terms into registers, which sum with rounding to nearest.
+// kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates: 4.4e-6 off over 4096
+// terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms into
+// registers, which sum with rounding to nearest: 2.4e-7 (every block 1.6e-7, every 8 blocks
+// 4.8e-7).  The products of planes other than the first two have an accumulator of their own,
+// which is 2^-8 of the first and is read once a tile.
 //
 // kSwap: Q (columns) holds the tokens and P the weights -- for few tokens, where the 128 lanes
 // are better filled with weights.  The output is then written column by column.
@@ -84,13 +86,14 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+constexpr uint32_t kSuspendNs = 1000000;   // a try may sleep this long before it answers no
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(done)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
         : "memory");
     return done;
 }
@@ -108,7 +111,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t
     long long t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
-        if (i % 64) continue;
         uint32_t g;
         asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(g) : "r"(gone) : "memory");
         if (g) return false;
@@ -160,19 +162,20 @@ __device__ __forceinline__ void st_shared4u(uint32_t addr, uint32_t a, uint32_t 
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// lo_a, lo_b: the descriptors' low words; `hi` is the high word of both.
 template <int kCtas>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t lo_a, uint32_t lo_b, uint32_t hi, uint32_t idesc, bool add) {
     if constexpr (kCtas == 2)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
-            "r"(static_cast<uint32_t>(add))
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %5, 0;\n mov.b64 da, {%1, %3};\n"
+            " mov.b64 db, {%2, %3};\n tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n}" ::"r"(d), "r"(lo_a),
+            "r"(lo_b), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(add))
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
-            "r"(static_cast<uint32_t>(add))
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %5, 0;\n mov.b64 da, {%1, %3};\n"
+            " mov.b64 db, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n}" ::"r"(d), "r"(lo_a),
+            "r"(lo_b), "r"(hi), "r"(idesc), "r"(static_cast<uint32_t>(add))
             : "memory");
 }
 
@@ -262,11 +265,11 @@ __device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, floa
 
 // Shared-memory operand descriptor, 128-byte swizzle (version 1 of the format, layout type 2).
 // Summed index along the rows (K-major): groups of 8 rows are 1024 bytes apart.  Else
-// (MN-major): slabs of 64 x-elements are `slab` bytes apart, groups of 8 summed rows 1024.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool kmajor, uint32_t slab) {
-    const uint64_t lead = kmajor ? 1 : slab >> 4;
-    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | lead << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
+// (MN-major): slabs of 64 x-elements are 8192 bytes apart, groups of 8 summed rows 1024.  The
+// address and the slab distance are in the low word.
+constexpr uint32_t kDescHi = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t operand_desc_lo(uint32_t addr, bool kmajor) {
+    return (addr & 0x3FFFF) >> 4 | (kmajor ? 1u : 8192u >> 4) << 16;
 }
 
 // Swizzled place of float4 `j` (0..7) of row `r` in a 32 x 32 unit: writes by row and reads
@@ -490,15 +493,19 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
     constexpr int kHalf = kBN / kHalves;                            // columns of each
     constexpr int kUnitCols = kHalf < 32 ? kHalf : 32;      // of a unit of the split exchange
     constexpr int kPieces = kHalf / 16;                     // 16 columns at a time
-    constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
+    // two accumulators; the drain forms of up to 128 columns a third, for the small products
+    constexpr uint32_t kTmemWant = kDrain && kBN <= 128 ? 3 * kBN : 2 * kBN;
+    constexpr uint32_t kTmemCols = kTmemWant <= 32 ? 32 : kTmemWant <= 64 ? 64 : kTmemWant <= 128 ? 128 : kTmemWant <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) uint8_t dyn[];     // stages, output buffers, bias rows
-    __shared__ uint64_t bars[2 * kTcMaxStages + 4 + kWarps * kTcMaxSlots];
+    __shared__ uint64_t bars[2 * kTcMaxStages + 5 + kWarps * kTcMaxSlots];
     __shared__ uint32_t tmem_slot, gone_flag;
     const uint32_t base = smem_addr(dyn);
     const uint32_t full = smem_addr(&bars[0]), empty = smem_addr(&bars[kTcMaxStages]);
     const uint32_t acc_full = smem_addr(&bars[2 * kTcMaxStages]), acc_empty = acc_full + 16;
-    const uint32_t res_bars = acc_full + 32;
-    const uint32_t stage_bytes = a.planes_p * kPBytes + a.planes_q * kQBytes;
+    const uint32_t small_empty = acc_full + 32, res_bars = acc_full + 40;
+    const bool split_planes = a.planes_p + a.planes_q > 2;
+    const uint32_t plane_p = a.sub * kPBytes, plane_q = a.sub * kQBytes;      // of a stage
+    const uint32_t stage_bytes = a.planes_p * plane_p + a.planes_q * plane_q;
     const uint32_t warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 || a.splits > 1 ? cluster_rank() : 0;
     const uint32_t split = kCtas == 2 ? 0 : rank;
@@ -521,6 +528,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             bar_init(acc_full + 8 * b, 1);
             bar_init(acc_empty + 8 * b, kCtas * kHalves * 4);
         }
+        bar_init(small_empty, kCtas * kHalves * 4);
         for (uint32_t i = 0; i < kWarps * kTcMaxSlots; ++i) bar_init(res_bars + 8 * i, 1);
         gone_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -544,34 +552,52 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
         if constexpr (kRegSplit<kBN, kDrain>) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kLoadWarp && elect_one()) {
             const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
+            // the parameters in registers: the asm statements' memory clobbers would have them
+            // loaded again for every block, and this thread's latency sets the pace of short tiles
+            const bool pk = a.p_kmajor, qk = a.q_kmajor, plain = a.planes_p + a.planes_q == 2;
+            const uint32_t sub = a.sub, stages = a.stages, terms = a.k, np = a.planes_p, nq = a.planes_q;
+            const uint32_t block_bytes = stage_bytes / sub * kCtas, at_q = base + np * plane_p;
+            const CUtensorMap *mp = &a.map_p, *mq = &a.map_q;
+            const auto load_p = [&](uint32_t dst, uint32_t k, uint32_t p0, uint32_t z, uint32_t bar) {
+                if (pk) {
+                    tma_load<kCtas>(dst, mp, k, p0, z, bar);
+                } else {
+                    tma_load<kCtas>(dst, mp, p0, k, z, bar);
+                    tma_load<kCtas>(dst + 8192, mp, p0 + 64, k, z, bar);
+                }
+            };
+            const auto load_q = [&](uint32_t dst, uint32_t k, uint32_t q0, uint32_t z, uint32_t bar) {
+                if (qk)
+                    tma_load<kCtas>(dst, mq, k, q0, z, bar);
+                else
+#pragma unroll
+                    for (int h = 0; h < kQRows / 64; ++h) tma_load<kCtas>(dst + h * 8192, mq, q0 + 64 * h, k, z, bar);
+            };
             uint32_t s = 0, phase = 1;          // the first round of stages is free
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
                 const TcTile tile = tc_tile(a, t);
-                const int32_t p0 = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0);
-                const int32_t q0 = tile.q * kBN + (kCtas == 2 ? rank * kQRows : 0);
+                const uint32_t p0 = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0);
+                const uint32_t q0 = tile.q * kBN + (kCtas == 2 ? rank * kQRows : 0);
                 for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                    const uint32_t k0 = kb * sub * kBK, bar = lead_full + 8 * s, off = s * stage_bytes;
+                    const bool second = sub == 2 && terms - k0 > kBK;
                     if (!bar_wait(empty + 8 * s, phase, gone, ctas)) {
                         ok = false;
                         break;
                     }
-                    if (leader) mbar_expect(full + 8 * s, stage_bytes * kCtas);
-                    uint32_t dst = base + s * stage_bytes;
-                    const int32_t k0 = kb * kBK;
-                    for (int z = 0; z < static_cast<int>(a.planes_p); ++z, dst += kPBytes) {
-                        if (a.p_kmajor)
-                            tma_load<kCtas>(dst, &a.map_p, k0, p0, z, lead_full + 8 * s);
-                        else
-                            for (int h = 0; h < 2; ++h)
-                                tma_load<kCtas>(dst + h * 8192, &a.map_p, p0 + 64 * h, k0, z, lead_full + 8 * s);
+                    if (leader) mbar_expect(full + 8 * s, second ? 2 * block_bytes : block_bytes);
+                    if (plain) {
+                        load_p(base + off, k0, p0, 0, bar);
+                        load_q(at_q + off, k0, q0, 0, bar);
+                        if (second) {
+                            load_p(base + off + kPBytes, k0 + kBK, p0, 0, bar);
+                            load_q(at_q + off + kQBytes, k0 + kBK, q0, 0, bar);
+                        }
+                    } else {
+                        for (uint32_t z = 0; z < np; ++z) load_p(base + off + z * plane_p, k0, p0, z, bar);
+                        for (uint32_t z = 0; z < nq; ++z) load_q(at_q + off + z * plane_q, k0, q0, z, bar);
                     }
-                    for (int z = 0; z < static_cast<int>(a.planes_q); ++z, dst += kQBytes) {
-                        if (a.q_kmajor)
-                            tma_load<kCtas>(dst, &a.map_q, k0, q0, z, lead_full + 8 * s);
-                        else
-                            for (int h = 0; h < kQRows / 64; ++h)
-                                tma_load<kCtas>(dst + h * 8192, &a.map_q, q0 + 64 * h, k0, z, lead_full + 8 * s);
-                    }
-                    if (++s == a.stages) {
+                    if (++s == stages) {
                         s = 0;
                         phase ^= 1;
                     }
@@ -581,10 +607,15 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (a.p_kmajor ? 0u : 1u << 15) |
                                    (a.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 | (128 * kCtas / 16) << 24;
             const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
-            const uint64_t desc_p = operand_desc(base, a.p_kmajor, 8192);
-            const uint64_t desc_q = operand_desc(base + a.planes_p * kPBytes, a.q_kmajor, 8192);
+            const uint32_t desc_p = operand_desc_lo(base, a.p_kmajor);
+            const uint32_t desc_q = operand_desc_lo(base + a.planes_p * plane_p, a.q_kmajor);
+            const uint32_t small = tmem + 2 * kBN;
+            const bool plain = a.planes_p + a.planes_q == 2;
+            const uint32_t sub = a.sub, stages = a.stages, terms = a.k, np = a.planes_p, nq = a.planes_q, chunk = a.chunk_kb;
+            bool add_small = false;
             uint32_t it = 0, ch = 0, s = 0, phase = 0;      // it: blocks so far; s, phase: its stage
-            for (uint32_t t = first; ok && t < a.tiles; t += step) {
+            uint32_t n_tile = 0;
+            for (uint32_t t = first; ok && t < a.tiles; t += step, ++n_tile) {
                 for (uint32_t kb = kb0; ok && kb < kb1; ++ch) {
                     const uint32_t b = ch & 1;
                     if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, ctas)) {
@@ -592,36 +623,59 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (kDrain && split_planes && kb == kb0 && t != first &&
+                        !bar_wait(small_empty, (n_tile - 1) & 1, gone, ctas)) {
+                        ok = false;
+                        break;
+                    }
                     const uint32_t d = tmem + b * kBN;
-                    const uint32_t end = kDrain && kb1 - kb > a.chunk_kb ? kb + a.chunk_kb : kb1;
+                    const uint32_t end = kDrain && kb1 - kb > chunk ? kb + chunk : kb1;
                     bool add = false;
+                    if (kb == kb0) add_small = false;
                     for (; kb < end; ++kb, ++it) {
+                        const bool second = sub == 2 && terms - kb * 2 * kBK > kBK;
+                        // descriptors before the wait: the issuing thread's own latency counts
+                        const uint32_t dp = desc_p + (s * stage_bytes >> 4), dq = desc_q + (s * stage_bytes >> 4);
+                        uint32_t lp[kBK / 16], lq[kBK / 16];
+#pragma unroll
+                        for (uint32_t x = 0; x < kBK / 16; ++x) {
+                            lp[x] = dp + x * step_p;
+                            lq[x] = dq + x * step_q;
+                        }
                         if (a.test_expire || !bar_wait(full + 8 * s, phase, gone, ctas)) {
                             ok = false;
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         // all four steps of 16 terms: what lies past the sum's end is zeros
-                        const uint64_t dp = desc_p + (s * stage_bytes >> 4), dq = desc_q + (s * stage_bytes >> 4);
-                        if (a.planes_p == 1 && a.planes_q == 1) {
+                        if (plain) {
 #pragma unroll
                             for (uint32_t x = 0; x < kBK / 16; ++x)
-                                mma<kCtas>(d, dp + x * step_p, dq + x * step_q, idesc, add || x > 0);
-                        } else {
-                            for (uint32_t pair = 0; pair < 6; ++pair) {
-                                // (i, j): 2 0, 1 1, 0 2, 1 0, 0 1, 0 0
-                                const uint32_t i = 0x001012 >> (pair * 4) & 3, j = 0x010210 >> (pair * 4) & 3;
-                                if (i >= a.planes_p || j >= a.planes_q) continue;
+                                mma<kCtas>(d, lp[x], lq[x], kDescHi, idesc, add || x > 0);
+                            if (second)
 #pragma unroll
                                 for (uint32_t x = 0; x < kBK / 16; ++x)
-                                    mma<kCtas>(d, dp + (i * kPBytes >> 4) + x * step_p,
-                                               dq + (j * kQBytes >> 4) + x * step_q, idesc, add || x > 0);
-                                add = true;
+                                    mma<kCtas>(d, lp[x] + (kPBytes >> 4), lq[x] + (kQBytes >> 4), kDescHi, idesc, true);
+                        } else {
+                            for (uint32_t pair = 0; pair < 6; ++pair) {       // planes: one block per stage
+                                // (i, j): 2 0, 1 1, 0 2, 1 0, 0 1, 0 0
+                                const uint32_t i = 0x001012 >> (pair * 4) & 3, j = 0x010210 >> (pair * 4) & 3;
+                                if (i >= np || j >= nq) continue;
+                                const bool main = !kDrain || pair == 5;      // see kDrain above
+                                const uint32_t op = i * plane_p >> 4, oq = j * plane_q >> 4;
+#pragma unroll
+                                for (uint32_t x = 0; x < kBK / 16; ++x)
+                                    mma<kCtas>(main ? d : small, lp[x] + op, lq[x] + oq, kDescHi, idesc,
+                                               (main ? add : add_small) || x > 0);
+                                if (main)
+                                    add = true;
+                                else
+                                    add_small = true;
                             }
                         }
                         add = true;
                         commit<kCtas>(empty + 8 * s);
-                        if (++s == a.stages) {
+                        if (++s == stages) {
                             s = 0;
                             phase ^= 1;
                         }
@@ -659,7 +713,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
         o.ahead = by_tma && a.e.res && !a.e.pre;
         const uint32_t stage_unit = o.buf;
         if (o.ahead && lane == 0) load_ahead<kCtas, kBN>(a, o, o.slots, first, step, width, rank);
-        const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty;
+        const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty, lead_small = lead_empty + 16;
         uint32_t ch = 0;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
             const TcTile tile = tc_tile(a, t);
@@ -679,7 +733,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    if (chunks == 1) break;
+                    if (chunks == 1 && !split_planes) break;
 #pragma unroll
                     for (int c = 0; c < kPieces; ++c) {
                         float v[16];
@@ -688,13 +742,28 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
 #pragma unroll
                         for (int i = 0; i < 16; ++i) acc[c * 16 + i] += v[i];
                     }
-                    if (n == chunks) break;
+                    if (n == chunks) {
+                        if (kBN <= 128 && split_planes) {
+#pragma unroll
+                            for (int c = 0; c < kPieces; ++c) {
+                                float v[16];
+                                tmem_ld16(mine + 2 * kBN + c * 16, v);
+                                tmem_wait16(v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) acc[c * 16 + i] += v[i];
+                            }
+                            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) bar_arrive_cluster(lead_small);
+                        }
+                        break;
+                    }
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
                     ++ch;
                 }
-                if (chunks > 1) {
+                if (chunks > 1 || split_planes) {
 #pragma unroll
                     for (int c = 0; c < kPieces; ++c) tmem_st16(mine + (ch & 1) * kBN + c * 16, acc + c * 16);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -793,7 +862,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                 for (; o.block < o.issued; ++o.block)       // the loads in flight land first
                     for (uint32_t i = 0; i < 1000 && !bar_try(o.bar + 8 * (o.block % o.slots), (o.block / o.slots) & 1); ++i) {}
             }
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -906,7 +975,10 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.rows = p.m;
     a.cols = p.n;
     a.k = p.k;
-    a.kblocks = (p.k + kBK - 1) / kBK;
+    // Two blocks of 64 terms per stage where a tile's MMAs are short: a stage's waits, issue and
+    // commit take some 500 cycles, a block of 256 x 256 products 512, of 128 x 128 only 256.
+    a.sub = c.bn < 256 && p.a.planes + p.b.planes == 2 && p.k > kBK ? 2 : 1;
+    a.kblocks = (p.k + a.sub * kBK - 1) / (a.sub * kBK);
     const TcOperand& P = c.swap ? p.b : p.a;
     const TcOperand& Q = c.swap ? p.a : p.b;
     const uint32_t px = c.swap ? p.n : p.m, qx = c.swap ? p.m : p.n;
@@ -924,23 +996,23 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.group = 8;
     a.splits = c.ctas == 2 ? 1 : p.splits;
     if (a.splits > a.kblocks) a.splits = a.kblocks;
-    a.chunk_kb = P.planes + Q.planes > 2 ? 1 : 4;
+    a.chunk_kb = 4 / a.sub;
     auto vec = [&](const void* q, uint64_t ld) { return !q || out_ready(q, ld, a.e.out_dtype); };
     a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
     const bool by_tma = a.vec && a.splits == 1 && !c.swap;
     if (by_tma && !(encode_out(&a.map_out, a.e.out, a.e.ldo, a) && (!a.e.pre || encode_out(&a.map_pre, a.e.pre, a.e.ldo, a)) &&
                     (!a.e.res || encode_out(&a.map_res, a.e.res, a.e.ldr, a))))
         return cudaErrorInvalidValue;
-    const uint32_t stage = P.planes * kPBytes + Q.planes * qrows * kBK * 2;
+    const uint32_t stage = a.sub * (P.planes * kPBytes + Q.planes * qrows * kBK * 2);
     const uint32_t warps = 4 * drain_parts(c.bn, c.swap);
     // Short sums with a residual are bound by the output side: more blocks ahead.  Else as many
     // stages as fit.
-    a.slots = c.swap ? 1 : by_tma && a.e.res && !a.e.pre && a.kblocks <= 4 ? (c.bn == 256 ? 2 : kTcMaxSlots) : c.bn == 256 ? 1 : 2;
+    a.slots = c.swap ? 1 : by_tma && a.e.res && !a.e.pre && p.k <= 4 * kBK ? (c.bn == 256 ? 2 : kTcMaxSlots) : 1;
     if (warps * (a.slots * kUnit + kBiasRow) + 2 * stage > kSmemMost) a.slots = 1;
     const uint32_t extra = a.splits == 1 ? warps * (a.slots * kUnit + kBiasRow) : 0;
-    // two CTAs per SM for the forms that take few registers, if each has four stages
+    // two CTAs per SM for the forms that take few registers, if each has three stages
     const auto fit = [&](uint32_t ctas) { return (kSmemMost / ctas - 2048 * (ctas - 1) - extra) / stage; };
-    const uint32_t occupancy = c.swap && !drain && fit(2) >= 4 ? 2 : 1;
+    const uint32_t occupancy = c.swap && !drain && fit(2) >= 3 ? 2 : 1;
     uint32_t stages = fit(occupancy);
     if (stages > static_cast<uint32_t>(kTcMaxStages)) stages = kTcMaxStages;
     if (stages < 1) return cudaErrorInvalidValue;

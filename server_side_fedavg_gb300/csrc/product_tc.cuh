@@ -49,7 +49,8 @@ struct TcArgs {
     CUtensorMap map_out, map_res, map_pre;    // boxes of 32 rows x 128 bytes; with `vec` and splits == 1
     ProdEpilogue e;
     unsigned int* err;
-    uint32_t rows, cols, k, kblocks;          // of the output and the sum
+    uint32_t rows, cols, k;                   // of the output and the sum
+    uint32_t sub, kblocks;                    // blocks of 64 terms per stage (1 or 2); stages of a sum
     uint32_t tiles, tiles_p, tiles_q, group;
     uint32_t splits, stages, chunk_kb, planes_p, planes_q;
     uint32_t slots;                           // 4 KB epilogue buffers per drain warp: 2..kTcMaxSlots

@@ -224,38 +224,49 @@ fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, 
     return launched(w, fa::launch_split(o.p, o.ld, o.dtype, rows, cols, planes, dst, ldd, s), "operand layout");
 }
 
-// Tile configuration and split of the summed index: the one that needs the fewest steps, a
-// step being one block of 64 summed elements on the CTA with the most work.
+// Tile configuration and split of the summed index: the least time by a model in
+// microseconds, fitted to sweeps of every configuration over 29 shapes on GB300.  A launch
+// takes 4, a tile 1 (256 columns: 2) beside its blocks of 64 terms, the exchange of a split
+// 1.5.  A block takes the larger of its latency and its MMA time, or its operand bytes at the
+// 112 GB/s that L2 gives each SM when all of them load.  The choice was within 10 % of the best
+// configuration in 26 of the 29.
 void choose(fa::TcProduct* p, int sms) {
     const auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
     const uint64_t kb = up(p->k, 64), n_sm = static_cast<uint64_t>(sms);
+    const uint32_t planes = p->a.planes + p->b.planes, products = planes == 6 ? 6 : planes == 4 ? 3 : 1;
     p->drain = p->e.out_dtype == 0;
-    p->splits = 1;
-    if (p->m <= 64 && (p->a.kmajor || p->m > 32)) {
-        p->cfg = p->m <= 16 ? fa::kTcSwap16 : p->m <= 32 ? fa::kTcSwap32 : fa::kTcSwap64;
-        const uint64_t tiles = up(p->n, 128);
-        while (p->splits < 8 && tiles * p->splits <= n_sm && kb >= p->splits * 2 * 4) p->splits *= 2;
-        return;
-    }
-    // cost of a tile's block, in units of an SM's MMA time for 128 x 128 x 64: a pair's tile
-    // of 256 columns takes 2; the 128-row forms are bound by operand traffic and take 1.5 / 1.2
-    // with what each tile costs besides (fill, drain, stores) in blocks
-    const uint64_t m256 = up(p->m, 256), m128 = up(p->m, 128), pairs = n_sm / 2;
-    const bool wide = p->a.planes + p->b.planes < 6;      // three planes of both: 256 columns do not fit
     double best = 1e300;
-    const auto consider = [&](int cfg, uint64_t tiles, uint64_t room, double block, uint32_t splits) {
-        const double cost = up(tiles * splits, room) * (up(kb, splits) * block + 6.0) + (splits > 1 ? 3.0 : 0.0);
+    const auto consider = [&](int cfg, uint64_t tiles, uint32_t ctas, double kbytes, double latency, double mma,
+                              double per_tile, uint32_t splits) {
+        // clusters of 4 and 8 CTAs leave SMs of a GPC unused
+        const uint64_t room = splits == 8 ? n_sm * 16 / 19 : splits == 4 ? n_sm * 18 / 19 : n_sm;
+        const uint64_t all = tiles * splits * ctas, active = std::min(all, room);
+        const double load = kbytes * 1.024 * planes / 2 / 112 * static_cast<double>(active) / static_cast<double>(n_sm);
+        const double block = std::max(std::max(latency, load), mma * products);
+        // a split's clusters do one tile each: a further wave starts anew
+        const double start = splits > 1 ? 4.0 : 0.0, waves = static_cast<double>(up(all, room));
+        const double cost = waves * (static_cast<double>(up(kb, splits)) * block + per_tile + start) - start +
+                            (splits > 1 ? 1.5 : 0.0);
         if (cost < best) {
             best = cost;
             p->cfg = cfg;
             p->splits = splits;
         }
     };
-    if (wide) consider(fa::kTcPair256, m256 * up(p->n, 256), pairs, 2.0, 1);
-    consider(fa::kTcPair128, m256 * up(p->n, 128), pairs, 1.1, 1);
-    for (uint32_t s = 1; s <= 8 && kb >= s * 2; s *= 2) {
-        if (p->n > 64) consider(fa::kTc128, m128 * up(p->n, 128), n_sm, 1.5, s);
-        consider(fa::kTc64, m128 * up(p->n, 64), n_sm, 1.2, s);
+    const uint64_t m128 = up(p->m, 128), m256 = up(p->m, 256), n64 = up(p->n, 64), n128 = up(p->n, 128), n256 = up(p->n, 256);
+    // few tokens: in the MMA's columns
+    if (p->m <= 64 && (p->a.kmajor || p->m > 32)) {
+        const int cfg = p->m <= 16 ? fa::kTcSwap16 : p->m <= 32 ? fa::kTcSwap32 : fa::kTcSwap64;
+        const double kbytes = p->m <= 16 ? 18 : p->m <= 32 ? 20 : 24;
+        for (uint32_t s = 1; s <= 8 && kb >= s; s *= 2) consider(cfg, n128, 1, kbytes, 0.15, 0.13, p->m > 32 ? 1.5 : 1.0, s);
+        if (p->m <= 32) return;
+    }
+    // planes need TMEM and shared memory beside 256 columns
+    if (planes == 2) consider(fa::kTcPair256, m256 * n256, 2, 32, 0.30, 0.30, 2.0, 1);
+    consider(fa::kTcPair128, m256 * n128, 2, 24, 0.165, 0.16, 1.0, 1);
+    for (uint32_t s = 1; s <= 8 && kb >= s; s *= 2) {
+        consider(fa::kTc128, m128 * n128, 1, 32, 0.185, 0.165, 1.0, s);
+        consider(fa::kTc64, m128 * n64, 1, 24, 0.16, 0.13, 1.0, s);
     }
 }
 
