@@ -614,6 +614,8 @@ typedef struct {
 
 #define FA_DISTILL_MAX_CLIENTS 16
 #define FA_DISTILL_MAX_TOPK    2048   /* per client, and summed over the clients */
+#define FA_DISTILL_MIN_TEMPERATURE 0.0009765625
+#define FA_DISTILL_MAX_TEMPERATURE 1048576.0
 
 /* Distillation of the student's logits z[rows, vocab] from the clients' top logits at
  * temperature T.  In row r, client j is present if its list has a used place with a value
@@ -638,7 +640,7 @@ typedef struct {
     const void* logits;
     uint64_t ld;
     const fa_distill_client* clients; /* [n_clients] */
-    double temperature;               /* finite, > 0 */
+    double temperature;               /* FA_DISTILL_MIN_TEMPERATURE (2^-10) to _MAX_ (2^20) */
     const float* row_weight;          /* [rows] >= 0, or NULL for 1 */
     float* loss;                      /* [rows]; fa_distill_grad: may be NULL */
     float* lse;                       /* [rows] log sum exp(z / T) (0 in rows of weight 0):

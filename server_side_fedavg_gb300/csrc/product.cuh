@@ -36,8 +36,11 @@ struct ProdArgs {
     ProdEpilogue e;
 };
 
-// Any types, strides and sizes, plain fp32 arithmetic.
-cudaError_t launch_product_plain(const ProdArgs& p, cudaStream_t stream);
+// Any types, strides and storage orders; for small m * n * k (and k == 0).
+cudaError_t launch_product_tiny(const ProdArgs& p, cudaStream_t stream);
+
+// Few rows of a; both operands K-major and of one type.
+cudaError_t launch_product_thin(const ProdArgs& p, cudaStream_t stream);
 
 // The products' operands where they are not as the tensor-core kernel reads them (bf16,
 // 16-byte aligned base and row stride): the matrix [rows][cols] as `planes` bf16 planes

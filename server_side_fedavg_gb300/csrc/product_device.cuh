@@ -56,6 +56,27 @@ __device__ __forceinline__ void finish_one(const ProdEpilogue& e, float sum, uin
     put(e.out, row * e.ldo + col, e.out_dtype, y);
 }
 
+// Every kernel of the products is launched as a programmatic dependent of its predecessor on the
+// stream: its launch and set-up overlap that kernel's end.  Each thread begins with
+// wait_predecessor before it touches global memory.
+__device__ __forceinline__ void wait_predecessor() {
+    asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_next(void (*kern)(Params...), dim3 grid, uint32_t block, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 }  // namespace
 
 }  // namespace fa

@@ -1,78 +1,150 @@
-// Products in plain fp32 arithmetic for any type, stride and size.
+// Products on the FP32 units: those too small for the tensor cores, and few fp32 rows against
+// a weight matrix, where reading the weights is the work.
 #include "product_device.cuh"
 
 namespace fa {
 
 namespace {
 
-constexpr int kPt = 64;    // outputs per tile side
-constexpr int kPk = 16;    // summed elements per step
-constexpr int kPlainBlock = 128;
+constexpr int kBlockThreads = 256;
 
-// out tile 64 x 64 per CTA of 256 threads, 4 x 4 outputs each; both operands staged as
-// fp32 in shared memory, [kk][x], with the summed index or x along the global row.
-__global__ void __launch_bounds__(256) product_plain_kernel(const __grid_constant__ ProdArgs p) {
-    __shared__ float sa[kPk][kPt + 4], sb[kPk][kPt + 4];
-    const uint32_t m0 = blockIdx.y * kPt, n0 = blockIdx.x * kPt;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    // sums over blocks of kPlainBlock terms, then over the blocks: a single chain of 11008
-    // additions was 2e-6 off, twice what blocks leave
-    float acc[4][4] = {}, tot[4][4] = {};
-    for (uint32_t k0 = 0; k0 < p.k; k0 += kPk) {
-        for (int i = threadIdx.x; i < kPk * kPt; i += 256) {
-            int kk = p.a.kmajor ? i % kPk : i / kPt, x = p.a.kmajor ? i / kPk : i % kPt;
-            bool in = m0 + x < p.m && k0 + kk < p.k;
-            uint64_t at = p.a.kmajor ? (uint64_t)(m0 + x) * p.a.ld + k0 + kk : (uint64_t)(k0 + kk) * p.a.ld + m0 + x;
-            sa[kk][x] = in ? elem(p.a.p, at, p.a.dtype) : 0.0f;
-            kk = p.b.kmajor ? i % kPk : i / kPt, x = p.b.kmajor ? i / kPk : i % kPt;
-            in = n0 + x < p.n && k0 + kk < p.k;
-            at = p.b.kmajor ? (uint64_t)(n0 + x) * p.b.ld + k0 + kk : (uint64_t)(k0 + kk) * p.b.ld + n0 + x;
-            sb[kk][x] = in ? elem(p.b.p, at, p.b.dtype) : 0.0f;
-        }
-        __syncthreads();
-        const int kn = p.k - k0 < kPk ? p.k - k0 : kPk;
-        for (int kk = 0; kk < kn; ++kk)
+// ----------------------------------------------------------------- tiny products
+// One output per kLanes lanes (1 or 32), any storage order.  Bound by launch and load latency.
+template <int kLanes>
+__global__ void __launch_bounds__(kBlockThreads) product_tiny_kernel(const __grid_constant__ ProdArgs p) {
+    wait_predecessor();
+    const uint64_t at = (blockIdx.x * static_cast<uint64_t>(kBlockThreads) + threadIdx.x) / kLanes;
+    if (at >= static_cast<uint64_t>(p.m) * p.n) return;
+    const uint32_t r = static_cast<uint32_t>(at / p.n), c = static_cast<uint32_t>(at - static_cast<uint64_t>(r) * p.n);
+    const uint64_t sa = p.a.kmajor ? 1 : p.a.ld, sb = p.b.kmajor ? 1 : p.b.ld;
+    const uint64_t a0 = p.a.kmajor ? r * p.a.ld : r, b0 = p.b.kmajor ? c * p.b.ld : c;
+    float sum = 0.0f;
+    for (uint32_t kk = threadIdx.x % kLanes; kk < p.k; kk += kLanes)
+        sum = fmaf(elem(p.a.p, a0 + kk * sa, p.a.dtype), elem(p.b.p, b0 + kk * sb, p.b.dtype), sum);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+    for (int d = kLanes / 2; d; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+    if (threadIdx.x % kLanes == 0) finish_one(p.e, sum, r, c);
+}
+
+// ----------------------------------------------------------------- few rows
+// A CTA has kCols columns of the output (rows of b, which is K-major as a is) and walks over
+// the rows of a in groups of kRows.  Its eight warps divide the summed index; a lane loads 16
+// bytes of each of its rows at a time (kVec; else one element), so that a warp keeps
+// kCols x 512 bytes of weights in flight.  Bound by HBM for the weights up to some 16 rows, by
+// the FMA rate beyond.  Sums: per lane, then over the lanes by halving (a lane ends up with
+// one output of the group), then over the warps in order.
+template <int kRows>
+constexpr int kCols = kRows == 8 ? 8 : 4;      // 8 x 8: as many loads from L1 as FMAs can feed on
+
+// Value i of a group of kN, summed over the lanes, ends in the lanes with lane % kN == i.
+template <int kN, int kAll = kN>
+__device__ __forceinline__ float reduce_lanes(const float (&v)[kN]) {
+    constexpr int kHalf = kN / 2;
+    const bool up = threadIdx.x & kHalf;
+    float h[kHalf];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[kk][ty * 4 + i], sb[kk][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-        if ((k0 / kPk + 1) % (kPlainBlock / kPk) == 0)
+    for (int i = 0; i < kHalf; ++i)
+        h[i] = (up ? v[i + kHalf] : v[i]) + __shfl_xor_sync(~0u, up ? v[i] : v[i + kHalf], kHalf);
+    if constexpr (kHalf > 1) {
+        return reduce_lanes<kHalf, kAll>(h);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    tot[i][j] += acc[i][j];
-                    acc[i][j] = 0.0f;
-                }
+        for (int d = kAll; d < 32; d *= 2) h[0] += __shfl_xor_sync(~0u, h[0], d);
+        return h[0];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t r = m0 + ty * 4 + i, c = n0 + tx + 16 * j;
-            if (r < p.m && c < p.n) finish_one(p.e, tot[i][j] + acc[i][j], r, c);
+}
+
+template <typename T, bool kVec>
+struct Piece {                          // what a lane loads of a row at a time
+    static constexpr int kElems = kVec ? 16 / sizeof(T) : 1;
+    float x[kElems];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (!kVec) {
+            x[0] = elem(p, 0, sizeof(T) == 2);
+        } else if constexpr (sizeof(T) == 2) {
+            plain_vec8(p, x);
+        } else {
+            const float4 v = *reinterpret_cast<const float4*>(p);
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
         }
+    }
+};
+
+template <typename T, int kRows, bool kVec>
+__global__ void __launch_bounds__(kBlockThreads) product_thin_kernel(const __grid_constant__ ProdArgs p) {
+    constexpr int kC = kCols<kRows>, kWarps = kBlockThreads / 32, kOut = kRows * kC, kE = Piece<T, kVec>::kElems;
+    constexpr int kGroup = kOut < 32 ? kOut : 32;
+    __shared__ float part[kWarps][kOut];
+    wait_predecessor();
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t c0 = blockIdx.x * kC;
+    const T *a = static_cast<const T*>(p.a.p), *b = static_cast<const T*>(p.b.p);
+    const T* rows[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) rows[c] = b + min(c0 + c, p.n - 1) * p.b.ld;     // past the end: the last row again
+    for (uint32_t r0 = 0; r0 < p.m; r0 += kRows) {
+        float acc[kOut] = {};
+        for (uint32_t k0 = (warp * 32 + lane) * kE; k0 < p.k; k0 += kBlockThreads * kE) {
+            Piece<T, kVec> w[kC];
+#pragma unroll
+            for (int c = 0; c < kC; ++c) w[c].load(rows[c] + k0);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                Piece<T, kVec> x;
+                x.load(a + min(r0 + r, p.m - 1) * p.a.ld + k0);
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+#pragma unroll
+                    for (int i = 0; i < kE; ++i) acc[r * kC + c] = fmaf(x.x[i], w[c].x[i], acc[r * kC + c]);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < kOut; g += kGroup) {
+            float v[kGroup];
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) v[i] = acc[g + i];
+            const float mine = reduce_lanes<kGroup>(v);
+            if (lane < kGroup) part[warp][g + lane] = mine;
+        }
+        __syncthreads();
+        if (threadIdx.x < kOut) {
+            float sum = 0.0f;
+            for (int w = 0; w < kWarps; ++w) sum += part[w][threadIdx.x];
+            const uint32_t r = r0 + threadIdx.x / kC, c = c0 + threadIdx.x % kC;
+            if (r < p.m && c < p.n) finish_one(p.e, sum, r, c);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, bool kVec>
+cudaError_t thin(const ProdArgs& p, cudaStream_t stream) {
+    if (p.m == 1)
+        return launch_next(product_thin_kernel<T, 1, kVec>, dim3((p.n + kCols<1> - 1) / kCols<1>), kBlockThreads, stream, p);
+    if (p.m <= 4)
+        return launch_next(product_thin_kernel<T, 4, kVec>, dim3((p.n + kCols<4> - 1) / kCols<4>), kBlockThreads, stream, p);
+    return launch_next(product_thin_kernel<T, 8, kVec>, dim3((p.n + kCols<8> - 1) / kCols<8>), kBlockThreads, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_product_plain(const ProdArgs& p, cudaStream_t stream) {
-    // rows beyond 65535 tiles (4 M rows) go in several launches
-    const uint32_t per = 65535u * kPt;
-    for (uint32_t r = 0; r < p.m; r += per) {
-        ProdArgs q = p;
-        const uint64_t so = p.e.out_dtype ? 2 : 4, sa = p.a.dtype ? 2 : 4;
-        q.m = p.m - r < per ? p.m - r : per;
-        q.a.p = static_cast<const char*>(p.a.p) + (p.a.kmajor ? r * p.a.ld : r) * sa;
-        q.e.out = static_cast<char*>(p.e.out) + r * p.e.ldo * so;
-        if (p.e.pre) q.e.pre = static_cast<char*>(p.e.pre) + r * p.e.ldo * so;
-        if (p.e.res) q.e.res = static_cast<const char*>(p.e.res) + r * p.e.ldr * so;
-        product_plain_kernel<<<dim3((p.n + kPt - 1) / kPt, (q.m + kPt - 1) / kPt), 256, 0, stream>>>(q);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+cudaError_t launch_product_tiny(const ProdArgs& p, cudaStream_t stream) {
+    // short sums: a thread per output
+    const uint64_t lanes = p.k <= 32 ? 1 : 32;
+    const uint64_t grid = (static_cast<uint64_t>(p.m) * p.n * lanes + kBlockThreads - 1) / kBlockThreads;
+    if (grid >= (1ull << 31)) return cudaErrorInvalidConfiguration;
+    return launch_next(lanes == 1 ? product_tiny_kernel<1> : product_tiny_kernel<32>, dim3(static_cast<uint32_t>(grid)),
+                       kBlockThreads, stream, p);
+}
+
+cudaError_t launch_product_thin(const ProdArgs& p, cudaStream_t stream) {
+    const uint64_t size = p.a.dtype ? 2 : 4;
+    const auto aligned = [&](const ProdOperand& o) {
+        return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld * size % 16 == 0;
+    };
+    const bool vec = aligned(p.a) && aligned(p.b) && p.k * size % 16 == 0;
+    if (p.a.dtype) return vec ? thin<uint16_t, true>(p, stream) : thin<uint16_t, false>(p, stream);
+    return vec ? thin<float, true>(p, stream) : thin<float, false>(p, stream);
 }
 
 }  // namespace fa

@@ -59,6 +59,7 @@ __device__ __forceinline__ void load8(const void* p, uint64_t row_at, uint32_t c
 // Eight elements per thread and step, rows in turn.
 __global__ void __launch_bounds__(256) split_kernel(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols,
                                                     int planes, uint16_t* dst, uint64_t ldd, bool vec) {
+    wait_predecessor();
     const uint64_t per = ldd / 8, all = per * rows, plane = rows * ldd;
     for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
         const uint64_t r = i / per;
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(256) split_kernel(const void* src, uint64_t ld
 // eighth row; the column sums join over the warps in warp order.
 __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a, bool vd, bool vp, bool vz) {
     __shared__ float sums[8][256];
+    wait_predecessor();
     const uint32_t c = blockIdx.x * 256 + threadIdx.x % 32 * 8, warp = threadIdx.x / 32;
     const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
     const uint64_t plane = a.m * a.ldz;
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
 
 __global__ void __launch_bounds__(256) col_sum_kernel(const float* part, uint32_t blocks, uint32_t n, void* out,
                                                       int out_dtype) {
+    wait_predecessor();
     const uint32_t c = blockIdx.x * 256 + threadIdx.x;
     if (c >= n) return;
     float s = 0.0f;
@@ -135,22 +138,19 @@ cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows,
                          uint64_t ldd, cudaStream_t stream) {
     const uint64_t groups = ldd / 8 * rows, blocks = (groups + 255) / 256;
     const uint32_t grid = blocks < 152 * 8 ? static_cast<uint32_t>(blocks) : 152 * 8;
-    split_kernel<<<grid, 256, 0, stream>>>(src, ld, dtype, rows, cols, planes, static_cast<uint16_t*>(dst), ldd,
-                                           vec_ok(src, ld, dtype));
-    return cudaGetLastError();
+    return launch_next(split_kernel, dim3(grid), 256, stream, src, ld, dtype, rows, cols, planes, static_cast<uint16_t*>(dst),
+                       ldd, vec_ok(src, ld, dtype));
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream) {
     const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
-    act_grad_kernel<<<dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, 0, stream>>>(
-        a, vec_ok(a.dout, a.ldd, a.dtype), vec_ok(a.pre, a.ldp, a.dtype), vec_ok(a.dz, a.ldz, 0));
-    return cudaGetLastError();
+    return launch_next(act_grad_kernel, dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, stream, a,
+                       vec_ok(a.dout, a.ldd, a.dtype), vec_ok(a.pre, a.ldp, a.dtype), vec_ok(a.dz, a.ldz, 0));
 }
 
 cudaError_t launch_col_sum(const float* part, uint32_t blocks, uint32_t n, void* out, int out_dtype,
                            cudaStream_t stream) {
-    col_sum_kernel<<<(n + 255) / 256, 256, 0, stream>>>(part, blocks, n, out, out_dtype);
-    return cudaGetLastError();
+    return launch_next(col_sum_kernel, dim3((n + 255) / 256), 256, stream, part, blocks, n, out, out_dtype);
 }
 
 }  // namespace fa

@@ -956,6 +956,22 @@ cudaError_t prepare_product_tc(TcShape* shape) {
         for (int d = 0; d < 2 && e == cudaSuccess; ++d)
             e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kKernels[c][d]),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    // how many clusters the GPCs hold (of 8 CTAs, fewer than SMs / 8)
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1024);
+        cfg.blockDim = dim3(kTcThreads[kTc128][0]);
+        cfg.dynamicSmemBytes = kSmemMost;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 1u << i;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kKernels[kTc128][0]), &cfg);
+        shape->split_ctas[i] = n << i;
+    }
     if (e == cudaSuccess && !g_encode) {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;

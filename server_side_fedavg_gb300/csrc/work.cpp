@@ -201,8 +201,8 @@ struct Carve {
     }
 };
 
-// Whether the product is for the plain kernel: too little work to fill a tensor-core tile.
-bool use_plain(uint64_t m, uint64_t n, uint64_t k) { return k == 0 || m * n * k <= (1ull << 16); }
+// Too little work to fill a tensor-core tile: a thread or warp per output.
+bool use_tiny(uint64_t m, uint64_t n, uint64_t k) { return k == 0 || (m * n * k <= (1ull << 16) && k <= 1024); }
 
 bool tma_ready(const fa::ProdOperand& o) {
     return o.dtype == 1 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 && o.ld < (1ull << 36);
@@ -225,21 +225,21 @@ fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, 
 }
 
 // Tile configuration and split of the summed index: the least time by a model in
-// microseconds, fitted to sweeps of every configuration over 29 shapes on GB300.  A launch
+// microseconds, fitted to sweeps of every configuration over 35 shapes on GB300.  A launch
 // takes 4, a tile 1 (256 columns: 2) beside its blocks of 64 terms, the exchange of a split
 // 1.5.  A block takes the larger of its latency and its MMA time, or its operand bytes at the
-// 112 GB/s that L2 gives each SM when all of them load.  The choice was within 10 % of the best
-// configuration in 26 of the 29.
-void choose(fa::TcProduct* p, int sms) {
+// 112 GB/s that L2 gives each SM when all of them load.  The choice was within 15 % of the best
+// configuration in all but one of 35 shapes.
+void choose(fa::TcProduct* p, const fa::TcShape& shape) {
     const auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
-    const uint64_t kb = up(p->k, 64), n_sm = static_cast<uint64_t>(sms);
+    const uint64_t kb = up(p->k, 64), n_sm = static_cast<uint64_t>(shape.sms);
     const uint32_t planes = p->a.planes + p->b.planes, products = planes == 6 ? 6 : planes == 4 ? 3 : 1;
     p->drain = p->e.out_dtype == 0;
     double best = 1e300;
     const auto consider = [&](int cfg, uint64_t tiles, uint32_t ctas, double kbytes, double latency, double mma,
                               double per_tile, uint32_t splits) {
-        // clusters of 4 and 8 CTAs leave SMs of a GPC unused
-        const uint64_t room = splits == 8 ? n_sm * 16 / 19 : splits == 4 ? n_sm * 18 / 19 : n_sm;
+        const int at = splits == 8 ? 3 : splits == 4 ? 2 : splits == 2 ? 1 : 0;
+        const uint64_t room = std::max(1, shape.split_ctas[at]);      // larger clusters leave SMs of a GPC unused
         const uint64_t all = tiles * splits * ctas, active = std::min(all, room);
         const double load = kbytes * 1.024 * planes / 2 / 112 * static_cast<double>(active) / static_cast<double>(n_sm);
         const double block = std::max(std::max(latency, load), mma * products);
@@ -270,6 +270,15 @@ void choose(fa::TcProduct* p, int sms) {
     }
 }
 
+// Few rows that the tensor cores could only take after a pass over the weights (fp32 ones into
+// three planes, 16 bytes moved per weight instead of 4; bf16 ones of an odd stride into an
+// aligned copy): read as they are on the FP32 units.  Against 4096 x 4096 fp32 weights: 16
+// rows 23.5 us (tensor cores with their pass 46), 32 rows 46 (48), 64 rows 90 (50).
+bool use_thin(const fa::ProdArgs& q) {
+    if (!q.a.kmajor || !q.b.kmajor || q.a.dtype != q.b.dtype) return false;
+    return q.a.dtype == 0 ? q.m <= 24 : q.m <= 8 && !tma_ready(q.b);
+}
+
 // A product by the kernel that suits its size.  run == false only adds up the workspace.
 fa_status do_product(fa_work* w, const fa::ProdArgs& q, const fa::TcOperand* ready_a, const fa::TcOperand* ready_b, Carve* c,
                      bool run, cudaStream_t s, const char* what) {
@@ -279,6 +288,7 @@ fa_status do_product(fa_work* w, const fa::ProdArgs& q, const fa::TcOperand* rea
     t.k = q.k;
     t.e = q.e;
     fa_status r = FA_OK;
+    if (!ready_a && !ready_b && use_thin(q)) return run ? launched(w, fa::launch_product_thin(q, s), what) : FA_OK;
     if (ready_a)
         t.a = *ready_a;
     else
@@ -288,7 +298,7 @@ fa_status do_product(fa_work* w, const fa::ProdArgs& q, const fa::TcOperand* rea
     else if (r == FA_OK)
         r = lay_out(w, q.b, q.n, q.k, c, &t.b, run, s);
     if (r != FA_OK || !run) return r;
-    choose(&t, w->tc.sms);
+    choose(&t, w->tc);
     return launched(w, fa::launch_product_tc(t, w->tc, w->err_dev, (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s), what);
 }
 
@@ -331,14 +341,14 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     q.b = {p.b, p.ldb, code_of(p.dtype_in), tb};
     q.e = {static_cast<float>(p.alpha), static_cast<float>(p.beta), p.bias, res, p.out, p.pre, p.ldr, p.ldo,
            code_of(p.dtype_in), code_of(p.dtype_out), p.act};
-    const bool plain = use_plain(p.m, p.n, p.k);
+    const bool tiny = use_tiny(p.m, p.n, p.k);
     Carve need{nullptr};
-    if (!plain) do_product(w, q, nullptr, nullptr, &need, false, s, "product");
+    if (!tiny) do_product(w, q, nullptr, nullptr, &need, false, s, "product");
     r = ensure_ws(w, need.used, cap);
     if (r == FA_OK) r = chain_in(w, s, cap);
     if (r != FA_OK) return r;
     Carve c{w->ws};
-    r = plain ? launched(w, fa::launch_product_plain(q, s), "product")
+    r = tiny ? launched(w, fa::launch_product_tiny(q, s), "product")
               : do_product(w, q, nullptr, nullptr, &c, true, s, "product");
     if (r != FA_OK) return r;
     return chain_out(w, s, cap);
@@ -381,14 +391,14 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     const uint32_t m = static_cast<uint32_t>(p.m), n = static_cast<uint32_t>(p.n), k = static_cast<uint32_t>(p.k);
     const uint32_t blocks = (m + fa::kColRows - 1) / fa::kColRows;
     const int it = code_of(p.dtype_in), dt = code_of(p.dtype_dout), gt = code_of(p.dtype_grad);
-    // dZ is dout itself, or is written to the workspace: in fp32 for the plain kernel, else
+    // dZ is dout itself, or is written to the workspace: in fp32 for the tiny kernel, else
     // as bf16 planes
-    const bool plain = use_plain(p.m, p.n, p.k);
+    const bool tiny = use_tiny(p.m, p.n, p.k);
     const bool products = want_a || want_b;
     const fa::ProdOperand d_in{p.dout, p.ldd, dt, true};
-    const bool write_dz = products && m && n && (act || (!plain && !tma_ready(d_in)));
-    const int planes = plain ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
-    const uint64_t ldz = plain ? p.n : (p.n + 7) / 8 * 8;
+    const bool write_dz = products && m && n && (act || (!tiny && !tma_ready(d_in)));
+    const int planes = tiny ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
+    const uint64_t ldz = tiny ? p.n : (p.n + 7) / 8 * 8;
     const bool cap = capturing(s);
     // two passes over the same steps: the first adds up the workspace
     Carve c{nullptr};
@@ -421,8 +431,8 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
             e.out = p.d_a;
             e.ldo = p.ldda;
             const fa::ProdArgs q = ta ? fa::ProdArgs{k, m, n, b, z, e} : fa::ProdArgs{m, k, n, z, b, e};
-            if (plain || n == 0)
-                r = run ? launched(w, fa::launch_product_plain(q, s), "gradient of a") : FA_OK;
+            if (tiny || n == 0)
+                r = run ? launched(w, fa::launch_product_tiny(q, s), "gradient of a") : FA_OK;
             else
                 r = do_product(w, q, ta ? nullptr : &tz, ta ? &tz : nullptr, &c, run, s, "gradient of a");
         }
@@ -433,8 +443,8 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
             e.out = p.d_b;
             e.ldo = p.lddb;
             const fa::ProdArgs q = tb ? fa::ProdArgs{n, k, m, z_n, a, e} : fa::ProdArgs{k, n, m, a, z_n, e};
-            if (plain || m == 0)
-                r = run ? launched(w, fa::launch_product_plain(q, s), "gradient of b") : FA_OK;
+            if (tiny || m == 0)
+                r = run ? launched(w, fa::launch_product_tiny(q, s), "gradient of b") : FA_OK;
             else
                 r = do_product(w, q, tb ? &tz_n : nullptr, tb ? nullptr : &tz_n, &c, run, s, "gradient of b");
         }
@@ -448,9 +458,8 @@ fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStre
     if (!dtype_ok(p.dtype) || !dtype_ok(p.dtype_value)) return fail(w, FA_ERR_DTYPE, "dtype");
     if (p.n_clients < 1 || p.n_clients > FA_DISTILL_MAX_CLIENTS || p.clients == nullptr)
         return fail(w, FA_ERR_ARG, "1 to 16 clients are needed");
-    if (!std::isfinite(p.temperature) || !(p.temperature > 0.0) || !(static_cast<float>(p.temperature) > 0.0f) ||
-        !std::isfinite(1.0f / static_cast<float>(p.temperature)) || !std::isfinite(static_cast<float>(p.temperature)))
-        return fail(w, FA_ERR_ARG, "temperature must be a positive fp32 number");
+    if (!(p.temperature >= FA_DISTILL_MIN_TEMPERATURE && p.temperature <= FA_DISTILL_MAX_TEMPERATURE))
+        return fail(w, FA_ERR_ARG, "temperature out of range");
     if (p.rows >= kMaxSize || p.vocab >= kMaxSize || p.vocab == 0)
         return fail(w, FA_ERR_RANGE, "rows or vocab out of range");
     fa::DistillArgs a{};
