@@ -630,7 +630,7 @@ typedef struct {
  * its logits are not looked at), has loss 0 and a zero gradient.  An entry of z at -inf
  * has q = 0 (a closed vocabulary entry); a row whose every entry is -inf gives NaN.
  * Several clients (or places) may name the same entry; their shares are added in fixed
- * point (2^-62), so the order of the sum does not matter. */
+ * point (2^-51 units), so the order of the sum does not matter. */
 typedef struct {
     uint32_t size;                    /* sizeof(fa_distill_args) */
     uint32_t n_clients;               /* 1..FA_DISTILL_MAX_CLIENTS */

@@ -3,10 +3,10 @@
 //   loss   log sum exp of the row, and over the clients' lists sum p (log p - log q)
 //   grad   w T (q - share), share being nonzero at the lists' entries alone
 //
-// Rows of up to 8 x 64 KB are held in registers: a CTA (or a cluster of 2, 4 or 8, each with a
-// slice) loads its row once with every load in flight at the same time, finds maximum and sum
-// together -- each thread over its own maximum, pairs (maximum, sum) merged over warp, CTA and,
-// through distributed shared memory, cluster -- and writes the gradient from the registers.
+// Rows of up to 8 x 64 KB are held in shared memory: a CTA (or a cluster of 2, 4 or 8, each with
+// a slice) loads its row once with every load in flight at the same time, finds maximum and sum
+// -- each thread over its own maximum, pairs (maximum, sum) merged over warp, CTA and, through
+// distributed shared memory, cluster -- and writes the gradient from there.
 // The row is read once and written once: bound by HBM.  Longer rows are streamed from memory
 // (and L2) twice or three times.
 //
@@ -16,8 +16,8 @@
 // the type's lowest value throughout, or with infinities) take 2^((z - maximum) c) instead.
 //
 // The shares of the entries are gathered in a hash table in shared memory (entry -> sum of
-// (n_j / total) p_jc): several clients name the same entry, and 64-bit integer adds of
-// 2^-62 units give the same sum in any order.  The row is written without the shares
+// (n_j / total) p_jc): several clients name the same entry, and integer adds of fixed-point
+// units give the same sum in any order.  The row is written without the shares
 // first, then the table's entries are written over it.
 #include "distill.cuh"
 #include "device.cuh"
@@ -27,8 +27,34 @@ namespace fa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFix = 4611686018427387904.0f;           // 2^62
-constexpr unsigned long long kPoison = 1ull << 63;       // the sum is NaN
+
+// A table slot: an entry and the sum of its shares in 2^-51 units, as two 32-bit words (2^-30
+// units, and the 21 bits below them: the low words of 2048 terms cannot overflow).  32-bit
+// adds in shared memory are single instructions, 64-bit ones loops.
+struct Slots {
+    int32_t* key;          // -1: free
+    uint32_t* hi;          // bit 31: the sum is NaN; once the sums are used, the value's bits
+    uint32_t* lo;
+};
+constexpr uint32_t kPoison = 1u << 31;
+
+__device__ __forceinline__ Slots slots_at(void* p, uint32_t n) {
+    int32_t* key = static_cast<int32_t*>(p);
+    return {key, reinterpret_cast<uint32_t*>(key + n), reinterpret_cast<uint32_t*>(key + 2 * n)};
+}
+
+__device__ __forceinline__ void add_share(const Slots& s, uint32_t h, float x) {
+    const float units = x * 1073741824.0f;                       // 2^30: exact
+    const uint32_t hi = __float2uint_rz(units);
+    atomicAdd(&s.hi[h], hi);
+    atomicAdd(&s.lo[h], __float2uint_rn((units - __uint2float_rn(hi)) * 2097152.0f));
+}
+
+__device__ __forceinline__ float share_of(const Slots& s, uint32_t h) {
+    if (s.hi[h] & kPoison) return NAN;
+    const unsigned long long v = (static_cast<unsigned long long>(s.hi[h]) << 21) + s.lo[h];
+    return static_cast<float>(v) * 4.4408920985006262e-16f;      // 2^-51
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -87,16 +113,16 @@ __device__ __forceinline__ uint32_t hash_of(int32_t key, uint32_t slots) {
 
 // ----------------------------------------------------------------- the clients' lists
 struct Lists {
+    float on[kMaxDistillClients];       // n_j, 0 if absent (zeroed before)
     float loss[kMaxDistillClients];     // sum p (log p - z / T) of client j
     float mass[kMaxDistillClients];     // sum p: 1 (or 0) up to rounding
-    float on[kMaxDistillClients];       // n_j, 0 if absent
 };
 
 // A warp per client: softmax of its values over its used places, its part of the loss (kLoss)
 // and its shares into the table, as far as they fall into [lo, hi) (kGrad).
 template <typename T, bool kGrad, int kThreads>
 __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uint32_t row, bool want_loss, uint32_t lo,
-                                           uint32_t hi, Lists& l, unsigned long long* sums, int32_t* keys) {
+                                           uint32_t hi, Lists& l, const Slots& table) {
     const int lane = threadIdx.x % 32;
     const float c = a.inv_t * kLog2e;
     for (uint32_t j = threadIdx.x / 32; j < a.nclients; j += kThreads / 32) {
@@ -134,13 +160,13 @@ __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uin
                 if (kGrad && static_cast<uint32_t>(e) >= lo && static_cast<uint32_t>(e) < hi) {
                     uint32_t h = hash_of(e, a.slots);
                     for (;; h = (h + 1) & (a.slots - 1)) {
-                        const int32_t was = atomicCAS(&keys[h], -1, e);
+                        const int32_t was = atomicCAS(&table.key[h], -1, e);
                         if (was == -1 || was == e) break;
                     }
                     if (p != p)
-                        atomicOr(&sums[h], kPoison);
+                        atomicOr(&table.hi[h], kPoison);
                     else
-                        atomicAdd(&sums[h], __float2ull_rn(p * cl.share * kFix));
+                        add_share(table, h, p * cl.share);
                 }
             }
         loss = warp_sum(loss);
@@ -156,7 +182,10 @@ __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uin
 // N_r; 0: no client.  The lists have been read by the whole CTA.
 __device__ __forceinline__ float total_weight(const DistillArgs& a, const Lists& l) {
     float total = 0.0f;
-    for (uint32_t j = 0; j < a.nclients; ++j) total += l.on[j];
+    for (uint32_t j = 0; j < a.nclients; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&l.on[j]);
+        total += (v.x + v.y) + (v.z + v.w);
+    }
     return total;
 }
 
@@ -194,22 +223,20 @@ __device__ __forceinline__ Exp from_lse(const DistillArgs& a, float lse, float& 
 // written, since grad may be logits; then, after a barrier, over the written row.
 template <typename T, int kThreads>
 __device__ __forceinline__ void entry_values(const DistillArgs& a, const T* z, const Exp& e, float coef, float scale,
-                                             float back, unsigned long long* sums, const int32_t* keys) {
+                                             float back, const Slots& table) {
     for (uint32_t h = threadIdx.x; h < a.slots; h += kThreads)
-        if (keys[h] >= 0) {
-            const float share = sums[h] & kPoison ? NAN : static_cast<float>(sums[h]) * (1.0f / kFix) * back;
-            sums[h] = __float_as_uint(coef * (e(at(z, keys[h])) * scale - share));
-        }
+        if (table.key[h] >= 0)
+            table.hi[h] = __float_as_uint(coef * (e(at(z, table.key[h])) * scale - share_of(table, h) * back));
 }
 
 template <typename T, int kThreads>
-__device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, const unsigned long long* sums, const int32_t* keys) {
+__device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, const Slots& table) {
     for (uint32_t h = threadIdx.x; h < a.slots; h += kThreads)
-        if (keys[h] >= 0) set(g, keys[h], __uint_as_float(static_cast<uint32_t>(sums[h])));
+        if (table.key[h] >= 0) set(g, table.key[h], __uint_as_float(table.hi[h]));
 }
 
-// ----------------------------------------------------------------- rows in registers
-constexpr int kMaxSlice = 65536;       // bytes of a row that a CTA of 512 threads holds
+// ----------------------------------------------------------------- rows held on chip
+constexpr uint32_t kMaxSlice = 65536;  // bytes of a row that a CTA holds: three CTAs per SM
 
 __device__ __forceinline__ uint32_t rank_in_cluster() {
     uint32_t r;
@@ -260,17 +287,62 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, fl
     m = top;
 }
 
-// One row (or slice) in the registers of kThreads threads, kNv x 16 bytes each.  A slice starts
+// Two floats at a time (packed fp32 arithmetic).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+        " mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
+        " mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The larger of m and the elements of 16 bytes (NaNs left out).
+template <typename T>
+__device__ __forceinline__ float max_of(float m, const uint4& q) {
+    if constexpr (sizeof(T) == 2) {
+        const auto two = [](uint32_t x, uint32_t y) {
+            uint32_t r;
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+            return r;
+        };
+        const uint32_t r = two(two(q.x, q.y), two(q.z, q.w));
+        return fmaxf(m, fmaxf(bf16_lo(r), bf16_hi(r)));
+    } else {
+        return fmaxf(fmaxf(m, fmaxf(__uint_as_float(q.x), __uint_as_float(q.y))),
+                     fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+    }
+}
+
+// One row (or slice) in shared memory: each thread copies its own 16-byte vectors there
+// (cp.async: no registers held, no barrier needed) and goes over them twice.  A slice starts
 // anywhere: elements before its first 16-byte boundary and after its last are held one per
 // thread in `edge`.
-template <typename T, bool kGrad, int kThreads, int kNv>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(const __grid_constant__ DistillArgs a) {
+template <typename T, bool kGrad, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(const __grid_constant__ DistillArgs a) {
     constexpr int kV = 16 / sizeof(T), kWarps = kThreads / 32;
-    extern __shared__ unsigned long long sums[];                 // [slots]
-    int32_t* keys = reinterpret_cast<int32_t*>(sums + a.slots);  // [slots], -1 free
+    extern __shared__ __align__(16) uint8_t dyn[];               // the slice's vectors, the table
     __shared__ float tmp[kWarps], tmp2[kWarps];
     __shared__ float2 mine;
-    __shared__ Lists lists;
+    __shared__ __align__(16) Lists lists;
     const uint32_t ctas = a.cluster, rank = ctas > 1 ? rank_in_cluster() : 0;
     const uint32_t row = blockIdx.x / ctas, t = threadIdx.x;
     const float w = a.row_weight ? a.row_weight[row] : 1.0f;
@@ -285,20 +357,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
     const bool has_edge = t < head || (t >= kV && t - kV < tail);
     const uint32_t edge_at = t < head ? t : head + nvec * kV + t - kV;
     const bool same_phase = kGrad && reinterpret_cast<uintptr_t>(gs) % 16 == reinterpret_cast<uintptr_t>(zs) % 16;
-    const auto put_vec = [&](uint32_t v, const float (&x)[kV]) {
+    const auto put_vec = [&](uint32_t v, const uint4& x) {
         T* p = gs + head + v * kV;
         if (same_phase) {
-            st_v4u(p, pack<T>(x));
+            st_v4u(p, x);
         } else {
+            const T* e = reinterpret_cast<const T*>(&x);
 #pragma unroll
-            for (int i = 0; i < kV; ++i) set(p, i, x[i]);
+            for (int i = 0; i < kV; ++i) p[i] = e[i];
         }
     };
     const auto write_zeros = [&] {
-        const float zero[kV] = {};
-#pragma unroll
-        for (int i = 0; i < kNv; ++i)
-            if (t + i * kThreads < nvec) put_vec(t + i * kThreads, zero);
+        for (uint32_t v = t; v < nvec; v += kThreads) put_vec(v, make_uint4(0, 0, 0, 0));
         if (has_edge) set(gs, edge_at, 0.0f);
     };
     if (!(w > 0.0f)) {
@@ -309,24 +379,25 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
         }
         return;
     }
-    // the row, all loads in flight; what is not there counts as -inf
-    constexpr uint32_t kNone = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-    uint4 q[kNv];
-#pragma unroll
-    for (int i = 0; i < kNv; ++i)
-        q[i] = t + i * kThreads < nvec ? ld_plain_v4(zs + head + (t + i * kThreads) * kV) : make_uint4(kNone, kNone, kNone, kNone);
+    const uint4* mem = reinterpret_cast<const uint4*>(zs + head);
+    const uint4* held = reinterpret_cast<const uint4*>(dyn);
+    const uint32_t held_at = smem_addr(dyn);
+    for (uint32_t v = t; v < nvec; v += kThreads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(held_at + v * 16), "l"(mem + v) : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
     const float edge = has_edge ? at(zs, edge_at) : -INFINITY;
-    if (kGrad) {
+    const Slots table = slots_at(dyn + a.table_at, a.slots);
+    if (kGrad)
         for (uint32_t i = t; i < a.slots; i += kThreads) {
-            sums[i] = 0;
-            keys[i] = -1;
+            table.key[i] = -1;
+            table.hi[i] = table.lo[i] = 0;
         }
-        __syncthreads();
-    }
-    read_lists<T, kGrad, kThreads>(a, z, row, rank == 0 && a.loss, lo, hi, lists, sums, keys);
+    if (t < kMaxDistillClients) lists.on[t] = 0.0f;
+    __syncthreads();
+    read_lists<T, kGrad, kThreads>(a, z, row, rank == 0 && a.loss, lo, hi, lists, table);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-    const float c = a.inv_t * kLog2e;
-    const float most = kFastMost / c;      // of a maximum, for the fast form
+    const float c = a.inv_t * kLog2e, most = kFastMost / c;      // of a maximum, for the fast form
     Exp e{c, 0.0f, 0.0f, 0.0f, true};
     float scale = 1.0f, lse;               // q = e(z) * scale
     if (a.lse_in) {
@@ -336,23 +407,24 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
     } else {
         // each thread's own maximum, floored where the fast form ends
         float m = fmaxf(edge, -most);
-#pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            float x[kV];
-            unpack<T>(q[i], x);
-#pragma unroll
-            for (int j = 0; j < kV; ++j) m = fmaxf(m, x[j]);
-        }
+#pragma unroll 4
+        for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, held[v]);
         e.k = m * c;
-        float s = e.quick(edge);
+        float2 s2 = make_float2(e.quick(edge), 0.0f);
+        const float2 cc = make_float2(c, c), kk = make_float2(-e.k, -e.k);
+#pragma unroll 2
+        for (uint32_t v = t; v < nvec; v += kThreads) {
+            float x[kV];
+            unpack<T>(held[v], x);
+            float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            float x[kV], part = 0.0f;
-            unpack<T>(q[i], x);
-#pragma unroll
-            for (int j = 0; j < kV; ++j) part += e.quick(x[j]);
-            s += part;
+            for (int j = 0; j < kV; j += 2) {
+                const float2 y = fma2(make_float2(x[j], x[j + 1]), cc, kk);
+                part = add2(part, make_float2(ex2(y.x), ex2(y.y)));
+            }
+            s2 = add2(s2, part);
         }
+        float s = s2.x + s2.y;
         // merged over the warp, the CTA and the cluster, in a fixed order
 #pragma unroll
         for (int d = 16; d; d >>= 1) merge(m, s, __shfl_xor_sync(~0u, m, d), __shfl_xor_sync(~0u, s, d), c);
@@ -379,13 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
         if (!(fabsf(m) < most)) {
             // the same for every thread of the cluster: the plain form, maximum first
             m = edge;
-#pragma unroll 1
-            for (uint32_t v = t; v < nvec; v += kThreads) {
-                float x[kV];
-                unpack<T>(ld_plain_v4(zs + head + v * kV), x);
-#pragma unroll
-                for (int j = 0; j < kV; ++j) m = fmaxf(m, x[j]);
-            }
+            for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, held[v]);
             m = block_reduce<kThreads, true>(m, tmp);
             if (ctas > 1) {
                 sync_cluster();
@@ -395,10 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
             }
             e = {0.0f, m, 1.0f, c, false};
             s = has_edge ? e.slow(edge) : 0.0f;
-#pragma unroll 1
             for (uint32_t v = t; v < nvec; v += kThreads) {
                 float x[kV];
-                unpack<T>(ld_plain_v4(zs + head + v * kV), x);
+                unpack<T>(held[v], x);
 #pragma unroll
                 for (int j = 0; j < kV; ++j) s += e.slow(x[j]);
             }
@@ -421,33 +486,36 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
     if (t == 0 && rank == 0) write_loss(a, lists, row, w, total, lse);
     if constexpr (kGrad) {
         if (total > 0.0f) {
-            const float coef = w * a.temperature, back = a.total / total;
-            entry_values<T, kThreads>(a, z, e, coef, scale, back, sums, keys);
+            const float coef = w * a.temperature, back = a.total / total, by = scale * coef;
+            entry_values<T, kThreads>(a, z, e, coef, scale, back, table);
             __syncthreads();
-            const float by = scale * coef;
             if (e.fast) {
-#pragma unroll
-                for (int i = 0; i < kNv; ++i)
-                    if (t + i * kThreads < nvec) {
-                        float x[kV];
-                        unpack<T>(q[i], x);
-#pragma unroll
-                        for (int j = 0; j < kV; ++j) x[j] = e.quick(x[j]) * by;
-                        put_vec(t + i * kThreads, x);
-                    }
-            } else {
-#pragma unroll 1
+                const float2 cc = make_float2(e.c, e.c), kk = make_float2(-e.k, -e.k), bb = make_float2(by, by);
+#pragma unroll 2
                 for (uint32_t v = t; v < nvec; v += kThreads) {
                     float x[kV];
-                    unpack<T>(ld_plain_v4(zs + head + v * kV), x);
+                    unpack<T>(held[v], x);
+#pragma unroll
+                    for (int j = 0; j < kV; j += 2) {
+                        float2 y = fma2(make_float2(x[j], x[j + 1]), cc, kk);
+                        y = mul2(make_float2(ex2(y.x), ex2(y.y)), bb);
+                        x[j] = y.x;
+                        x[j + 1] = y.y;
+                    }
+                    put_vec(v, pack<T>(x));
+                }
+            } else {
+                for (uint32_t v = t; v < nvec; v += kThreads) {
+                    float x[kV];
+                    unpack<T>(held[v], x);
 #pragma unroll
                     for (int j = 0; j < kV; ++j) x[j] = e.slow(x[j]) * by;
-                    put_vec(v, x);
+                    put_vec(v, pack<T>(x));
                 }
             }
             if (has_edge) set(gs, edge_at, e(edge) * by);
             __syncthreads();
-            write_entries<T, kThreads>(a, g, sums, keys);
+            write_entries<T, kThreads>(a, g, table);
         } else {
             write_zeros();
         }
@@ -460,10 +528,10 @@ constexpr int kDThreads = 512;
 
 template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_constant__ DistillArgs a) {
-    extern __shared__ unsigned long long sums[];                 // [slots]
-    int32_t* keys = reinterpret_cast<int32_t*>(sums + a.slots);  // [slots], -1 free
+    extern __shared__ __align__(16) uint8_t dyn[];               // the table
     __shared__ float tmp[kDThreads / 32];
-    __shared__ Lists lists;
+    __shared__ __align__(16) Lists lists;
+    const Slots table = slots_at(dyn, a.slots);
     const uint32_t row = blockIdx.x;
     const float w = a.row_weight ? a.row_weight[row] : 1.0f;
     const T* z = static_cast<const T*>(a.logits) + row * a.ld;
@@ -477,14 +545,14 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
         }
         return;
     }
-    if (kGrad) {
+    if (kGrad)
         for (uint32_t i = threadIdx.x; i < a.slots; i += kDThreads) {
-            sums[i] = 0;
-            keys[i] = -1;
+            table.key[i] = -1;
+            table.hi[i] = table.lo[i] = 0;
         }
-        __syncthreads();
-    }
-    read_lists<T, kGrad, kDThreads>(a, z, row, a.loss != nullptr, 0, a.vocab, lists, sums, keys);
+    if (threadIdx.x < kMaxDistillClients) lists.on[threadIdx.x] = 0.0f;
+    __syncthreads();
+    read_lists<T, kGrad, kDThreads>(a, z, row, a.loss != nullptr, 0, a.vocab, lists, table);
     const float c = a.inv_t * kLog2e;
     Exp e{0.0f, 0.0f, 1.0f, c, false};
     float scale = 1.0f, lse;
@@ -509,34 +577,32 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
     if constexpr (kGrad) {
         const bool some = total > 0.0f;
         const float coef = some ? w * a.temperature : 0.0f, back = some ? a.total / total : 0.0f, by = scale * coef;
-        if (some) entry_values<T, kDThreads>(a, z, e, coef, scale, back, sums, keys);
+        if (some) entry_values<T, kDThreads>(a, z, e, coef, scale, back, table);
         __syncthreads();
 #pragma unroll 8
         for (uint32_t i = threadIdx.x; i < a.vocab; i += kDThreads) set(g, i, some ? e(at(z, i)) * by : 0.0f);
         __syncthreads();
-        if (some) write_entries<T, kDThreads>(a, g, sums, keys);
+        if (some) write_entries<T, kDThreads>(a, g, table);
     }
 }
 
-// The row kernels by type, direction and vectors per thread: 128 threads (1, 2, 4, 8), 512
-// threads (4, 8).
 using DistillKernel = void (*)(DistillArgs);
 template <typename T, bool kGrad>
-constexpr DistillKernel kRowKernels[6] = {
-    distill_row_kernel<T, kGrad, 128, 1>, distill_row_kernel<T, kGrad, 128, 2>, distill_row_kernel<T, kGrad, 128, 4>,
-    distill_row_kernel<T, kGrad, 128, 8>, distill_row_kernel<T, kGrad, 512, 4>, distill_row_kernel<T, kGrad, 512, 8>};
+constexpr DistillKernel kRowKernels[2] = {distill_row_kernel<T, kGrad, 128>, distill_row_kernel<T, kGrad, 512>};
 
 }  // namespace
 
 cudaError_t prepare_distill() {
-    const int most = static_cast<int>(2 * kMaxDistillTopk * 12);
     cudaError_t e = cudaSuccess;
     const auto allow = [&](DistillKernel k) {
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kMaxSlice + 12 * 2 * kMaxDistillTopk);
     };
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 2; ++i) {
+        allow(kRowKernels<uint16_t, false>[i]);
         allow(kRowKernels<uint16_t, true>[i]);
+        allow(kRowKernels<float, false>[i]);
         allow(kRowKernels<float, true>[i]);
     }
     allow(distill_stream_kernel<uint16_t, true>);
@@ -550,9 +616,9 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     a.slots = 2;
     while (a.slots < 2 * entries) a.slots *= 2;
     const bool grad = a.grad != nullptr;
-    const uint64_t size = a.dtype ? 2 : 4, bytes = a.vocab * size;
+    const uint32_t size = a.dtype ? 2 : 4, table = grad ? a.slots * 12 : 0;
+    const uint64_t bytes = static_cast<uint64_t>(a.vocab) * size;
     cudaLaunchConfig_t cfg = {};
-    cfg.dynamicSmemBytes = grad ? static_cast<size_t>(a.slots) * 12 : 0;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -566,19 +632,15 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
                        : (grad ? distill_stream_kernel<float, true> : distill_stream_kernel<float, false>);
         a.cluster = 1;
         cfg.blockDim = dim3(kDThreads);
+        cfg.dynamicSmemBytes = table;
     } else {
-        // slices of whole vectors, so that they have the row's alignment
+        // slices of 16 elements' multiples, so that they all have the row's alignment
         a.cluster = cluster;
         a.slice = static_cast<uint32_t>((a.vocab + cluster * 16ull - 1) / (cluster * 16ull) * 16);
-        const uint64_t vecs = a.slice * size / 16 + 1;
-        int k = 5;
-        cfg.blockDim = dim3(512);
-        if (vecs <= 128 * 8) {
-            k = vecs <= 128 ? 0 : vecs <= 256 ? 1 : vecs <= 512 ? 2 : 3;
-            cfg.blockDim = dim3(128);
-        } else if (vecs <= 512 * 4) {
-            k = 4;
-        }
+        a.table_at = (a.slice < a.vocab ? a.slice : a.vocab) * size / 16 * 16;
+        const int k = a.table_at > 16384;
+        cfg.blockDim = dim3(k ? 512 : 128);
+        cfg.dynamicSmemBytes = a.table_at + table;
         kern = a.dtype ? (grad ? kRowKernels<uint16_t, true>[k] : kRowKernels<uint16_t, false>[k])
                        : (grad ? kRowKernels<float, true>[k] : kRowKernels<float, false>[k]);
     }

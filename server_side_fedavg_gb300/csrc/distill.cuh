@@ -33,13 +33,14 @@ struct DistillArgs {
     uint32_t nclients;
     uint32_t slots;            // hash slots: a power of two >= 2 * (sum of topk)
     uint32_t cluster, slice;   // CTAs per row and the elements of each
+    uint32_t table_at;         // bytes of a slice's vectors in shared memory: the table follows
     float temperature, inv_t;
     float total;               // sum of all n_j
     int dtype, value_dtype;
     DistillClient client[kMaxDistillClients];
 };
 
-// Fills slots, cluster and slice; the caller fills the rest.
+// Fills slots, cluster, slice and table_at; the caller fills the rest.
 cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream);
 cudaError_t prepare_distill();   // shared-memory limits, for the current device
 
