@@ -112,6 +112,19 @@ __device__ __forceinline__ uint32_t hash_of(int32_t key, uint32_t slots) {
 }
 
 // ----------------------------------------------------------------- the clients' lists
+// A share of p of entry e into the table.
+__device__ __forceinline__ void put_share(const Slots& table, uint32_t slots, int32_t e, float p, float share) {
+    uint32_t h = hash_of(e, slots);
+    for (;; h = (h + 1) & (slots - 1)) {
+        const int32_t was = atomicCAS(&table.key[h], -1, e);
+        if (was == -1 || was == e) break;
+    }
+    if (p != p)
+        atomicOr(&table.hi[h], kPoison);
+    else
+        add_share(table, h, p * share);
+}
+
 struct Lists {
     float on[kMaxDistillClients];       // n_j, 0 if absent (zeroed before)
     float loss[kMaxDistillClients];     // sum p (log p - z / T) of client j
@@ -157,17 +170,8 @@ __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uin
                 if (p == 0.0f) continue;      // nothing, also where the student's logit is -inf
                 mass += p;
                 if (want_loss) loss += p * (d - logsum - at(z, e) * a.inv_t);
-                if (kGrad && static_cast<uint32_t>(e) >= lo && static_cast<uint32_t>(e) < hi) {
-                    uint32_t h = hash_of(e, a.slots);
-                    for (;; h = (h + 1) & (a.slots - 1)) {
-                        const int32_t was = atomicCAS(&table.key[h], -1, e);
-                        if (was == -1 || was == e) break;
-                    }
-                    if (p != p)
-                        atomicOr(&table.hi[h], kPoison);
-                    else
-                        add_share(table, h, p * cl.share);
-                }
+                if (kGrad && static_cast<uint32_t>(e) >= lo && static_cast<uint32_t>(e) < hi)
+                    put_share(table, a.slots, e, p, cl.share);
             }
         loss = warp_sum(loss);
         mass = warp_sum(mass);
@@ -177,6 +181,83 @@ __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uin
             l.on[j] = on ? cl.weight : 0.0f;
         }
     }
+}
+
+// Lists of up to 64 places, a warp each: the places are loaded before anything else of the row,
+// and the student's logits there (for the loss) are asked for as soon as the places are known
+// and used after the row's statistics, so that no memory latency of the lists is waited for.
+constexpr int kShortTopk = 64;
+
+struct ShortList {
+    int32_t e[2];
+    float u[2];       // the client's value, then d - log sum
+    float p[2], z[2];
+};
+
+__device__ __forceinline__ void load_short(const DistillArgs& a, uint32_t row, uint32_t j, ShortList& s) {
+    const DistillClient& cl = a.client[j];
+    const uint64_t base = static_cast<uint64_t>(row) * cl.topk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t at = threadIdx.x % 32 + 32 * i;
+        s.e[i] = -1;
+        s.u[i] = 0.0f;
+        if (at < cl.topk) {
+            s.e[i] = cl.index[base + at];
+            s.u[i] = value_at(cl.value, base + at, a.value_dtype);
+        }
+    }
+}
+
+template <typename T, bool kGrad>
+__device__ __forceinline__ void use_short(const DistillArgs& a, const T* z, uint32_t j, bool want_loss, uint32_t lo,
+                                          uint32_t hi, ShortList& s, Lists& l, const Slots& table) {
+    const DistillClient& cl = a.client[j];
+    float top = -INFINITY;
+    bool nan = false, used[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        used[i] = static_cast<uint32_t>(s.e[i]) < a.vocab;
+        if (s.e[i] >= 0 && !used[i]) atomicOr(a.err, kErrListIndex);
+        s.z[i] = used[i] && want_loss ? at(z, s.e[i]) : 0.0f;
+        nan |= used[i] && s.u[i] != s.u[i];
+        if (used[i]) top = fmaxf(top, s.u[i]);
+    }
+    top = warp_max(top);
+    const bool on = __any_sync(~0u, nan) || top > -INFINITY;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        s.u[i] = (s.u[i] - top) * a.inv_t;
+        s.p[i] = used[i] ? ex2(s.u[i] * kLog2e) : 0.0f;
+        sum += s.p[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = on ? 1.0f / sum : 0.0f, logsum = logf(sum);
+    float mass = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        s.p[i] = on ? s.p[i] * inv : 0.0f;
+        s.u[i] -= logsum;
+        mass += s.p[i];
+        const uint32_t e = static_cast<uint32_t>(s.e[i]);
+        if (kGrad && !(s.p[i] == 0.0f) && e >= lo && e < hi) put_share(table, a.slots, s.e[i], s.p[i], cl.share);
+    }
+    mass = warp_sum(mass);
+    if (threadIdx.x % 32 == 0) {
+        l.mass[j] = mass;
+        l.on[j] = on ? cl.weight : 0.0f;
+    }
+}
+
+// Its part of the loss, once the row's statistics have been taken.
+__device__ __forceinline__ void end_short(const DistillArgs& a, uint32_t j, const ShortList& s, Lists& l) {
+    float loss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (!(s.p[i] == 0.0f)) loss += s.p[i] * (s.u[i] - s.z[i] * a.inv_t);
+    loss = warp_sum(loss);
+    if (threadIdx.x % 32 == 0) l.loss[j] = loss;
 }
 
 // N_r; 0: no client.  The lists have been read by the whole CTA.
@@ -221,12 +302,12 @@ __device__ __forceinline__ Exp from_lse(const DistillArgs& a, float lse, float& 
 
 // The entries' values of the gradient, into the table in place of the sums -- before the row is
 // written, since grad may be logits; then, after a barrier, over the written row.
-template <typename T, int kThreads>
-__device__ __forceinline__ void entry_values(const DistillArgs& a, const T* z, const Exp& e, float coef, float scale,
-                                             float back, const Slots& table) {
+template <int kThreads, typename At>
+__device__ __forceinline__ void entry_values(const DistillArgs& a, At z_at, const Exp& e, float coef, float scale, float back,
+                                             const Slots& table) {
     for (uint32_t h = threadIdx.x; h < a.slots; h += kThreads)
         if (table.key[h] >= 0)
-            table.hi[h] = __float_as_uint(coef * (e(at(z, table.key[h])) * scale - share_of(table, h) * back));
+            table.hi[h] = __float_as_uint(coef * (e(z_at(table.key[h])) * scale - share_of(table, h) * back));
 }
 
 template <typename T, int kThreads>
@@ -345,6 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
     __shared__ __align__(16) Lists lists;
     const uint32_t ctas = a.cluster, rank = ctas > 1 ? rank_in_cluster() : 0;
     const uint32_t row = blockIdx.x / ctas, t = threadIdx.x;
+    const bool brief = a.short_lists && a.nclients <= kWarps, has_list = brief && t / 32 < a.nclients;
+    ShortList list;
+    if (has_list) load_short(a, row, t / 32, list);
     const float w = a.row_weight ? a.row_weight[row] : 1.0f;
     const T* z = static_cast<const T*>(a.logits) + row * a.ld;
     T* g = kGrad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
@@ -394,7 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
         }
     if (t < kMaxDistillClients) lists.on[t] = 0.0f;
     __syncthreads();
-    read_lists<T, kGrad, kThreads>(a, z, row, rank == 0 && a.loss, lo, hi, lists, table);
+    const bool want_loss = rank == 0 && a.loss;
+    if (has_list)
+        use_short<T, kGrad>(a, z, t / 32, want_loss, lo, hi, list, lists, table);
+    else if (!brief)
+        read_lists<T, kGrad, kThreads>(a, z, row, want_loss, lo, hi, lists, table);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     const float c = a.inv_t * kLog2e, most = kFastMost / c;      // of a maximum, for the fast form
@@ -403,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
     if (a.lse_in) {
         lse = a.lse_in[row];
         e = from_lse(a, lse, scale);
+        if (has_list && want_loss) end_short(a, t / 32, list, lists);
         __syncthreads();
     } else {
         // each thread's own maximum, floored where the fast form ends
@@ -432,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
             tmp[t / 32] = m;
             tmp2[t / 32] = s;
         }
+        if (has_list && want_loss) end_short(a, t / 32, list, lists);
         __syncthreads();
         m = tmp[t % kWarps];
         s = tmp2[t % kWarps];
@@ -487,7 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
     if constexpr (kGrad) {
         if (total > 0.0f) {
             const float coef = w * a.temperature, back = a.total / total, by = scale * coef;
-            entry_values<T, kThreads>(a, z, e, coef, scale, back, table);
+            const auto z_at = [&](int32_t key) {
+                const uint32_t i = key - lo - head;          // below 0: beyond nvec * kV
+                return i < nvec * kV ? at(reinterpret_cast<const T*>(dyn), i) : at(z, key);
+            };
+            entry_values<kThreads>(a, z_at, e, coef, scale, back, table);
             __syncthreads();
             if (e.fast) {
                 const float2 cc = make_float2(e.c, e.c), kk = make_float2(-e.k, -e.k), bb = make_float2(by, by);
@@ -577,7 +671,7 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
     if constexpr (kGrad) {
         const bool some = total > 0.0f;
         const float coef = some ? w * a.temperature : 0.0f, back = some ? a.total / total : 0.0f, by = scale * coef;
-        if (some) entry_values<T, kDThreads>(a, z, e, coef, scale, back, table);
+        if (some) entry_values<kDThreads>(a, [&](int32_t i) { return at(z, i); }, e, coef, scale, back, table);
         __syncthreads();
 #pragma unroll 8
         for (uint32_t i = threadIdx.x; i < a.vocab; i += kDThreads) set(g, i, some ? e(at(z, i)) * by : 0.0f);
@@ -615,6 +709,8 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     for (uint32_t j = 0; j < a.nclients; ++j) entries += a.client[j].topk;
     a.slots = 2;
     while (a.slots < 2 * entries) a.slots *= 2;
+    a.short_lists = true;
+    for (uint32_t j = 0; j < a.nclients; ++j) a.short_lists = a.short_lists && a.client[j].topk <= kShortTopk;
     const bool grad = a.grad != nullptr;
     const uint32_t size = a.dtype ? 2 : 4, table = grad ? a.slots * 12 : 0;
     const uint64_t bytes = static_cast<uint64_t>(a.vocab) * size;

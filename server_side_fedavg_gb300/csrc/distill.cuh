@@ -37,10 +37,11 @@ struct DistillArgs {
     float temperature, inv_t;
     float total;               // sum of all n_j
     int dtype, value_dtype;
+    bool short_lists;          // every list has at most 64 places
     DistillClient client[kMaxDistillClients];
 };
 
-// Fills slots, cluster, slice and table_at; the caller fills the rest.
+// Fills slots, cluster, slice, table_at and short_lists; the caller fills the rest.
 cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream);
 cudaError_t prepare_distill();   // shared-memory limits, for the current device
 
