@@ -270,11 +270,14 @@ __device__ __forceinline__ float total_weight(const DistillArgs& a, const Lists&
     return total;
 }
 
+// By one whole warp, a lane per client.
 __device__ __forceinline__ void write_loss(const DistillArgs& a, const Lists& l, uint32_t row, float w, float total, float lse) {
+    const uint32_t j = threadIdx.x % 32;
     float loss = 0.0f;
     // n_j / N first: the terms of a logit near the type's lowest are near fp32's range
-    for (uint32_t j = 0; j < a.nclients; ++j)
-        if (l.on[j] > 0.0f) loss = fmaf(l.on[j] / total, fmaf(lse, l.mass[j], l.loss[j]), loss);
+    if (a.loss && j < a.nclients && l.on[j] > 0.0f) loss = l.on[j] / total * fmaf(lse, l.mass[j], l.loss[j]);
+    loss = warp_sum(loss);
+    if (j != 0) return;
     if (a.loss) a.loss[row] = total > 0.0f ? w * a.temperature * a.temperature * loss : 0.0f;
     if (a.lse_out) a.lse_out[row] = lse;
 }
@@ -361,10 +364,21 @@ __device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
     }
 }
 
-// (m, s): the sum of 2^(z c) is s 2^(m c) -- with m c rounded as Exp has it.
+// Pairs (m, s): the sum of 2^(z c) is s 2^(m c) -- with m c rounded as Exp has it.
+// Over the warp's lanes (kLanes: the first so many hold pairs, the others repeat them).
+template <int kLanes>
+__device__ __forceinline__ void merge_lanes(float& m, float& s, float c) {
+    float top;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+    s *= ex2(__fmul_rn(m, c) - __fmul_rn(top, c));      // the rounded products, as in k
+#pragma unroll
+    for (int d = kLanes / 2; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+    m = top;
+}
+
 __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
-    const float top = fmaxf(m, m2), k = top * c;
-    s = s * ex2(m * c - k) + s2 * ex2(m2 * c - k);
+    const float top = fmaxf(m, m2), k = __fmul_rn(top, c);
+    s = s * ex2(__fmul_rn(m, c) - k) + s2 * ex2(__fmul_rn(m2, c) - k);
     m = top;
 }
 
@@ -418,7 +432,7 @@ __device__ __forceinline__ float max_of(float m, const uint4& q) {
 // anywhere: elements before its first 16-byte boundary and after its last are held one per
 // thread in `edge`.
 template <typename T, bool kGrad, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(const __grid_constant__ DistillArgs a) {
     constexpr int kV = 16 / sizeof(T), kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint8_t dyn[];               // the slice's vectors, the table
     __shared__ float tmp[kWarps], tmp2[kWarps];
@@ -487,10 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
 
     const float c = a.inv_t * kLog2e, most = kFastMost / c;      // of a maximum, for the fast form
     Exp e{c, 0.0f, 0.0f, 0.0f, true};
-    float scale = 1.0f, lse;               // q = e(z) * scale
+    float scale = 1.0f, sum = 1.0f;        // q = e(z) * scale
     if (a.lse_in) {
-        lse = a.lse_in[row];
-        e = from_lse(a, lse, scale);
+        e = from_lse(a, a.lse_in[row], scale);
         if (has_list && want_loss) end_short(a, t / 32, list, lists);
         __syncthreads();
     } else {
@@ -498,10 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
         float m = fmaxf(edge, -most);
 #pragma unroll 4
         for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, held[v]);
-        e.k = m * c;
+        e.k = __fmul_rn(m, c);
         float2 s2 = make_float2(e.quick(edge), 0.0f);
         const float2 cc = make_float2(c, c), kk = make_float2(-e.k, -e.k);
-#pragma unroll 2
+#pragma unroll 4
         for (uint32_t v = t; v < nvec; v += kThreads) {
             float x[kV];
             unpack<T>(held[v], x);
@@ -515,8 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
         }
         float s = s2.x + s2.y;
         // merged over the warp, the CTA and the cluster, in a fixed order
-#pragma unroll
-        for (int d = 16; d; d >>= 1) merge(m, s, __shfl_xor_sync(~0u, m, d), __shfl_xor_sync(~0u, s, d), c);
+        merge_lanes<32>(m, s, c);
         if (t % 32 == 0) {
             tmp[t / 32] = m;
             tmp2[t / 32] = s;
@@ -525,8 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
         __syncthreads();
         m = tmp[t % kWarps];
         s = tmp2[t % kWarps];
-#pragma unroll
-        for (int d = kWarps / 2; d; d >>= 1) merge(m, s, __shfl_xor_sync(~0u, m, d), __shfl_xor_sync(~0u, s, d), c);
+        merge_lanes<kWarps>(m, s, c);
         if (ctas > 1) {
             if (t == 0) mine = make_float2(m, s);
             sync_cluster();
@@ -565,15 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
                 s = 0.0f;
                 for (uint32_t r = 0; r < ctas; ++r) s += peer2(&mine, r).x;
             }
-            lse = fmaf(m, a.inv_t, logf(s));
         } else {
-            e.k = m * c;
-            lse = (e.k + log2f(s)) * 0.69314718055994531f;
+            e.k = __fmul_rn(m, c);
         }
-        scale = 1.0f / s;
+        scale = __frcp_rn(s);
+        sum = s;
     }
     const float total = total_weight(a, lists);
-    if (t == 0 && rank == 0) write_loss(a, lists, row, w, total, lse);
     if constexpr (kGrad) {
         if (total > 0.0f) {
             const float coef = w * a.temperature, back = a.total / total, by = scale * coef;
@@ -585,8 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
             __syncthreads();
             if (e.fast) {
                 const float2 cc = make_float2(e.c, e.c), kk = make_float2(-e.k, -e.k), bb = make_float2(by, by);
-#pragma unroll 2
-                for (uint32_t v = t; v < nvec; v += kThreads) {
+                const auto grad_of = [&](uint32_t v) {
                     float x[kV];
                     unpack<T>(held[v], x);
 #pragma unroll
@@ -596,7 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
                         x[j] = y.x;
                         x[j + 1] = y.y;
                     }
-                    put_vec(v, pack<T>(x));
+                    return pack<T>(x);
+                };
+                if (same_phase) {
+                    uint4* to = reinterpret_cast<uint4*>(gs + head);
+#pragma unroll 4
+                    for (uint32_t v = t; v < nvec; v += kThreads) st_v4u(to + v, grad_of(v));
+                } else {
+                    for (uint32_t v = t; v < nvec; v += kThreads) put_vec(v, grad_of(v));
                 }
             } else {
                 for (uint32_t v = t; v < nvec; v += kThreads) {
@@ -613,6 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) distill_row_kernel(
         } else {
             write_zeros();
         }
+    }
+    // last, by the warp that has the fewest lists
+    if (t / 32 == kWarps - 1 && rank == 0 && (a.loss || a.lse_out)) {
+        const float lse = a.lse_in  ? a.lse_in[row]
+                          : e.fast ? (e.k + log2f(sum)) * 0.69314718055994531f
+                                   : fmaf(e.k, a.inv_t, logf(sum));
+        write_loss(a, lists, row, w, total, lse);
     }
     if (ctas > 1) sync_cluster();          // a peer may still read `mine`
 }
@@ -667,7 +689,7 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
         scale = 1.0f / s;
     }
     const float total = total_weight(a, lists);
-    if (threadIdx.x == 0) write_loss(a, lists, row, w, total, lse);
+    if (threadIdx.x < 32) write_loss(a, lists, row, w, total, lse);
     if constexpr (kGrad) {
         const bool some = total > 0.0f;
         const float coef = some ? w * a.temperature : 0.0f, back = some ? a.total / total : 0.0f, by = scale * coef;
@@ -682,7 +704,7 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
 
 using DistillKernel = void (*)(DistillArgs);
 template <typename T, bool kGrad>
-constexpr DistillKernel kRowKernels[2] = {distill_row_kernel<T, kGrad, 128>, distill_row_kernel<T, kGrad, 512>};
+constexpr DistillKernel kRowKernels[2] = {distill_row_kernel<T, kGrad, 128>, distill_row_kernel<T, kGrad, 256>};
 
 }  // namespace
 
@@ -735,7 +757,7 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
         a.slice = static_cast<uint32_t>((a.vocab + cluster * 16ull - 1) / (cluster * 16ull) * 16);
         a.table_at = (a.slice < a.vocab ? a.slice : a.vocab) * size / 16 * 16;
         const int k = a.table_at > 16384;
-        cfg.blockDim = dim3(k ? 512 : 128);
+        cfg.blockDim = dim3(k ? 256 : 128);
         cfg.dynamicSmemBytes = a.table_at + table;
         kern = a.dtype ? (grad ? kRowKernels<uint16_t, true>[k] : kRowKernels<uint16_t, false>[k])
                        : (grad ? kRowKernels<float, true>[k] : kRowKernels<float, false>[k]);
