@@ -4,16 +4,17 @@
 //   grad   w T (q - share), share being nonzero at the lists' entries alone
 //
 // Rows of up to 8 x 64 KB are held in shared memory: a CTA (or a cluster of 2, 4 or 8, each with
-// a slice) loads its row once with every load in flight at the same time, finds maximum and sum
-// -- each thread over its own maximum, pairs (maximum, sum) merged over warp, CTA and, through
-// distributed shared memory, cluster -- and writes the gradient from there.
+// a slice) loads its row once with every load in flight at the same time, sums its exponentials
+// -- each warp over a reference of its own, pairs (reference, sum) merged over the CTA and, through
+// distributed shared memory, the cluster -- and writes the gradient from there.
 // The row is read once and written once: bound by HBM.  Longer rows are streamed from memory
 // (and L2) twice or three times.
 //
-// An exponential is 2^(z c - k) with c = log2(e) / T and k = maximum c rounded: one FMA and one
+// An exponential is 2^(z c - k) with c = log2(e) / T and k = reference c rounded: one FMA and one
 // ex2.  k's rounding is the same in every term and in the statistic that is formed with the
-// same k, so it cancels.  Rows whose maximum is beyond 2^20 T / log2(e) in size (rows masked by
-// the type's lowest value throughout, or with infinities) take 2^((z - maximum) c) instead.
+// same k, so it cancels.  Rows whose reference is beyond 2^20 T / log2(e) in size or whose sum is
+// beyond 2^100 (masked by the type's lowest value or -inf where the reference was looked for, or
+// with infinities) take 2^((z - maximum) c) instead, in further passes over memory.
 //
 // The shares of the entries are gathered in a hash table in shared memory (entry -> sum of
 // (n_j / total) p_jc): several clients name the same entry, and integer adds of fixed-point
@@ -35,12 +36,26 @@ struct Slots {
     int32_t* key;          // -1: free
     uint32_t* hi;          // bit 31: the sum is NaN; once the sums are used, the value's bits
     uint32_t* lo;
+    uint16_t* taken;       // the slots in use, in no particular order
+    uint32_t* count;       // of them
 };
 constexpr uint32_t kPoison = 1u << 31;
 
-__device__ __forceinline__ Slots slots_at(void* p, uint32_t n) {
+constexpr uint32_t kSlotBytes = 13;       // 12, and 2 for every two slots: half of them can be taken
+
+__device__ __forceinline__ Slots slots_at(void* p, uint32_t n, uint32_t* count) {
     int32_t* key = static_cast<int32_t*>(p);
-    return {key, reinterpret_cast<uint32_t*>(key + n), reinterpret_cast<uint32_t*>(key + 2 * n)};
+    return {key, reinterpret_cast<uint32_t*>(key + n), reinterpret_cast<uint32_t*>(key + 2 * n),
+            reinterpret_cast<uint16_t*>(key + 3 * n), count};
+}
+
+template <int kThreads>
+__device__ __forceinline__ void empty_table(const Slots& s, uint32_t n) {
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+        s.key[i] = -1;
+        s.hi[i] = s.lo[i] = 0;
+    }
+    if (threadIdx.x == 0) *s.count = 0;
 }
 
 __device__ __forceinline__ void add_share(const Slots& s, uint32_t h, float x) {
@@ -117,7 +132,11 @@ __device__ __forceinline__ void put_share(const Slots& table, uint32_t slots, in
     uint32_t h = hash_of(e, slots);
     for (;; h = (h + 1) & (slots - 1)) {
         const int32_t was = atomicCAS(&table.key[h], -1, e);
-        if (was == -1 || was == e) break;
+        if (was == e) break;
+        if (was == -1) {
+            table.taken[atomicAdd(table.count, 1u)] = static_cast<uint16_t>(h);
+            break;
+        }
     }
     if (p != p)
         atomicOr(&table.hi[h], kPoison);
@@ -214,9 +233,12 @@ __device__ __forceinline__ void use_short(const DistillArgs& a, const T* z, uint
                                           uint32_t hi, ShortList& s, Lists& l, const Slots& table) {
     const DistillClient& cl = a.client[j];
     float top = -INFINITY;
-    bool nan = false, used[2];
+    bool nan = false, used[2] = {false, false};
+    const int places = cl.topk > 32 ? 2 : 1;      // of a lane
+    s.z[1] = s.p[1] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        if (i >= places) break;
         used[i] = static_cast<uint32_t>(s.e[i]) < a.vocab;
         if (s.e[i] >= 0 && !used[i]) atomicOr(a.err, kErrListIndex);
         s.z[i] = used[i] && want_loss ? at(z, s.e[i]) : 0.0f;
@@ -228,6 +250,7 @@ __device__ __forceinline__ void use_short(const DistillArgs& a, const T* z, uint
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        if (i >= places) break;
         s.u[i] = (s.u[i] - top) * a.inv_t;
         s.p[i] = used[i] ? ex2(s.u[i] * kLog2e) : 0.0f;
         sum += s.p[i];
@@ -237,6 +260,7 @@ __device__ __forceinline__ void use_short(const DistillArgs& a, const T* z, uint
     float mass = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        if (i >= places) break;
         s.p[i] = on ? s.p[i] * inv : 0.0f;
         s.u[i] -= logsum;
         mass += s.p[i];
@@ -293,6 +317,7 @@ struct Exp {
 
 // The fast form's k is at most 2^20 in size: its rounding, up to 2^-5, is in every exponent.
 constexpr float kFastMost = 1048576.0f;
+constexpr float kSumMost = 1.2676506e30f;      // 2^100
 
 // From a kept statistic: q = 2^(z c - lse log2 e), the product's rounding error moved to `scale`
 // (log2 e is kLog2e + 1.92596303e-8).
@@ -308,15 +333,21 @@ __device__ __forceinline__ Exp from_lse(const DistillArgs& a, float lse, float& 
 template <int kThreads, typename At>
 __device__ __forceinline__ void entry_values(const DistillArgs& a, At z_at, const Exp& e, float coef, float scale, float back,
                                              const Slots& table) {
-    for (uint32_t h = threadIdx.x; h < a.slots; h += kThreads)
-        if (table.key[h] >= 0)
-            table.hi[h] = __float_as_uint(coef * (e(z_at(table.key[h])) * scale - share_of(table, h) * back));
+    for (uint32_t i = threadIdx.x; i < *table.count; i += kThreads) {
+        const uint32_t h = table.taken[i];
+        table.hi[h] = __float_as_uint(coef * (e(z_at(table.key[h])) * scale - share_of(table, h) * back));
+    }
 }
 
+// ... leaving the slots free for the next row (the count is the caller's to reset).
 template <typename T, int kThreads>
-__device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, const Slots& table) {
-    for (uint32_t h = threadIdx.x; h < a.slots; h += kThreads)
-        if (table.key[h] >= 0) set(g, table.key[h], __uint_as_float(table.hi[h]));
+__device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, bool some, const Slots& table) {
+    for (uint32_t i = threadIdx.x; i < *table.count; i += kThreads) {
+        const uint32_t h = table.taken[i];
+        if (some) set(g, table.key[h], __uint_as_float(table.hi[h]));
+        table.key[h] = -1;
+        table.hi[h] = table.lo[h] = 0;
+    }
 }
 
 // ----------------------------------------------------------------- rows held on chip
@@ -364,12 +395,17 @@ __device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
     }
 }
 
-// Pairs (m, s): the sum of 2^(z c) is s 2^(m c) -- with m c rounded as Exp has it.
+// Pairs (m, s), a reference and a sum: the sum of 2^(z c) is s 2^(m c), m c rounded as in Exp.
 // Over the warp's lanes (kLanes: the first so many hold pairs, the others repeat them).
-template <int kLanes>
-__device__ __forceinline__ void merge_lanes(float& m, float& s, float c) {
+__device__ __forceinline__ float warp_largest(float m) {
     float top;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+    return top;
+}
+
+template <int kLanes>
+__device__ __forceinline__ void merge_lanes(float& m, float& s, float c) {
+    const float top = warp_largest(m);
     s *= ex2(__fmul_rn(m, c) - __fmul_rn(top, c));      // the rounded products, as in k
 #pragma unroll
     for (int d = kLanes / 2; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
@@ -427,178 +463,224 @@ __device__ __forceinline__ float max_of(float m, const uint4& q) {
     }
 }
 
-// One row (or slice) in shared memory: each thread copies its own 16-byte vectors there
-// (cp.async: no registers held, no barrier needed) and goes over them twice.  A slice starts
-// anywhere: elements before its first 16-byte boundary and after its last are held one per
-// thread in `edge`.
+// Where a row's slice lies: 16-byte vectors with `head` elements before them and `tail` after.
+template <typename T>
+struct Place {
+    static constexpr uint32_t kV = 16 / sizeof(T);
+    const T* z;             // the slice's first element
+    uint32_t head, nvec, tail;
+    __device__ __forceinline__ Place(const DistillArgs& a, uint32_t row, uint32_t lo, uint32_t n)
+        : z(static_cast<const T*>(a.logits) + row * a.ld + lo) {
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+        head = min(off ? kV - off : 0, n);
+        nvec = (n - head) / kV;
+        tail = n - head - nvec * kV;
+    }
+    // elements outside the vectors, one per thread: thread t's, if it has one
+    __device__ __forceinline__ bool edge(uint32_t t) const { return t < head || (t >= kV && t - kV < tail); }
+    __device__ __forceinline__ uint32_t edge_at(uint32_t t) const { return t < head ? t : head + nvec * kV + t - kV; }
+};
+
+// Rows (or a cluster's slices of them) held in shared memory.  Each thread copies its own
+// 16-byte vectors there (cp.async: no registers held, no barrier needed) and goes over them
+// twice; as it leaves a vector for the last time it asks for the next row's in its place, and
+// the next row's lists and weight are loaded as early, so that HBM is read while a row is being
+// worked on.  Elements beside the vectors are held one per thread in `edge`.
 template <typename T, bool kGrad, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(const __grid_constant__ DistillArgs a) {
-    constexpr int kV = 16 / sizeof(T), kWarps = kThreads / 32;
+    constexpr uint32_t kV = 16 / sizeof(T), kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint8_t dyn[];               // the slice's vectors, the table
     __shared__ float tmp[kWarps], tmp2[kWarps];
-    __shared__ float2 mine;
+    __shared__ float2 pairs[2];
     __shared__ __align__(16) Lists lists;
+    __shared__ uint32_t taken;
     const uint32_t ctas = a.cluster, rank = ctas > 1 ? rank_in_cluster() : 0;
-    const uint32_t row = blockIdx.x / ctas, t = threadIdx.x;
-    const bool brief = a.short_lists && a.nclients <= kWarps, has_list = brief && t / 32 < a.nclients;
-    ShortList list;
-    if (has_list) load_short(a, row, t / 32, list);
-    const float w = a.row_weight ? a.row_weight[row] : 1.0f;
-    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-    T* g = kGrad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
+    const uint32_t t = threadIdx.x, step = gridDim.x / ctas;
     const uint32_t lo = rank * a.slice, hi = min(lo + a.slice, a.vocab), n = hi > lo ? hi - lo : 0;
-    const T* zs = z + lo;
-    T* gs = kGrad ? g + lo : nullptr;
-    // 16-byte vectors of the slice: `head` elements before them, `tail` after
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(zs) % 16 / sizeof(T));
-    const uint32_t head = min(off ? kV - off : 0, n), nvec = (n - head) / kV, tail = n - head - nvec * kV;
-    const bool has_edge = t < head || (t >= kV && t - kV < tail);
-    const uint32_t edge_at = t < head ? t : head + nvec * kV + t - kV;
-    const bool same_phase = kGrad && reinterpret_cast<uintptr_t>(gs) % 16 == reinterpret_cast<uintptr_t>(zs) % 16;
-    const auto put_vec = [&](uint32_t v, const uint4& x) {
-        T* p = gs + head + v * kV;
-        if (same_phase) {
-            st_v4u(p, x);
-        } else {
-            const T* e = reinterpret_cast<const T*>(&x);
-#pragma unroll
-            for (int i = 0; i < kV; ++i) p[i] = e[i];
-        }
-    };
-    const auto write_zeros = [&] {
-        for (uint32_t v = t; v < nvec; v += kThreads) put_vec(v, make_uint4(0, 0, 0, 0));
-        if (has_edge) set(gs, edge_at, 0.0f);
-    };
-    if (!(w > 0.0f)) {
-        if (kGrad) write_zeros();
-        if (t == 0 && rank == 0) {
-            if (a.loss) a.loss[row] = 0.0f;
-            if (a.lse_out) a.lse_out[row] = 0.0f;
-        }
-        return;
-    }
-    const uint4* mem = reinterpret_cast<const uint4*>(zs + head);
+    const bool brief = a.short_lists && a.nclients <= kWarps, has_list = brief && t / 32 < a.nclients;
+    const bool want_loss = rank == 0 && a.loss;
     const uint4* held = reinterpret_cast<const uint4*>(dyn);
     const uint32_t held_at = smem_addr(dyn);
-    for (uint32_t v = t; v < nvec; v += kThreads)
+    const Slots table = slots_at(dyn + a.table_at, a.slots, &taken);
+    const auto weight_of = [&](uint32_t row) { return row < a.rows ? (a.row_weight ? a.row_weight[row] : 1.0f) : 0.0f; };
+    const auto fetch = [&](const uint4* mem, uint32_t v) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(held_at + v * 16), "l"(mem + v) : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    const float edge = has_edge ? at(zs, edge_at) : -INFINITY;
-    const Slots table = slots_at(dyn + a.table_at, a.slots);
-    if (kGrad)
-        for (uint32_t i = t; i < a.slots; i += kThreads) {
-            table.key[i] = -1;
-            table.hi[i] = table.lo[i] = 0;
-        }
-    if (t < kMaxDistillClients) lists.on[t] = 0.0f;
-    __syncthreads();
-    const bool want_loss = rank == 0 && a.loss;
-    if (has_list)
-        use_short<T, kGrad>(a, z, t / 32, want_loss, lo, hi, list, lists, table);
-    else if (!brief)
-        read_lists<T, kGrad, kThreads>(a, z, row, want_loss, lo, hi, lists, table);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    };
 
-    const float c = a.inv_t * kLog2e, most = kFastMost / c;      // of a maximum, for the fast form
-    Exp e{c, 0.0f, 0.0f, 0.0f, true};
-    float scale = 1.0f, sum = 1.0f;        // q = e(z) * scale
-    if (a.lse_in) {
-        e = from_lse(a, a.lse_in[row], scale);
-        if (has_list && want_loss) end_short(a, t / 32, list, lists);
-        __syncthreads();
-    } else {
-        // each thread's own maximum, floored where the fast form ends
-        float m = fmaxf(edge, -most);
-#pragma unroll 4
-        for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, held[v]);
-        e.k = __fmul_rn(m, c);
-        float2 s2 = make_float2(e.quick(edge), 0.0f);
-        const float2 cc = make_float2(c, c), kk = make_float2(-e.k, -e.k);
-#pragma unroll 4
-        for (uint32_t v = t; v < nvec; v += kThreads) {
-            float x[kV];
-            unpack<T>(held[v], x);
-            float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int j = 0; j < kV; j += 2) {
-                const float2 y = fma2(make_float2(x[j], x[j + 1]), cc, kk);
-                part = add2(part, make_float2(ex2(y.x), ex2(y.y)));
-            }
-            s2 = add2(s2, part);
-        }
-        float s = s2.x + s2.y;
-        // merged over the warp, the CTA and the cluster, in a fixed order
-        merge_lanes<32>(m, s, c);
-        if (t % 32 == 0) {
-            tmp[t / 32] = m;
-            tmp2[t / 32] = s;
-        }
-        if (has_list && want_loss) end_short(a, t / 32, list, lists);
-        __syncthreads();
-        m = tmp[t % kWarps];
-        s = tmp2[t % kWarps];
-        merge_lanes<kWarps>(m, s, c);
-        if (ctas > 1) {
-            if (t == 0) mine = make_float2(m, s);
-            sync_cluster();
-            const float2 first = peer2(&mine, 0);
-            m = first.x;
-            s = first.y;
-            for (uint32_t r = 1; r < ctas; ++r) {
-                const float2 v = peer2(&mine, r);
-                merge(m, s, v.x, v.y, c);
-            }
-        }
-        if (!(fabsf(m) < most)) {
-            // the same for every thread of the cluster: the plain form, maximum first
-            m = edge;
-            for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, held[v]);
-            m = block_reduce<kThreads, true>(m, tmp);
-            if (ctas > 1) {
-                sync_cluster();
-                if (t == 0) mine.x = m;
-                sync_cluster();
-                for (uint32_t r = 0; r < ctas; ++r) m = fmaxf(m, peer2(&mine, r).x);
-            }
-            e = {0.0f, m, 1.0f, c, false};
-            s = has_edge ? e.slow(edge) : 0.0f;
-            for (uint32_t v = t; v < nvec; v += kThreads) {
-                float x[kV];
-                unpack<T>(held[v], x);
-#pragma unroll
-                for (int j = 0; j < kV; ++j) s += e.slow(x[j]);
-            }
-            s = block_reduce<kThreads, false>(s, tmp);
-            if (ctas > 1) {
-                sync_cluster();
-                if (t == 0) mine.x = s;
-                sync_cluster();
-                s = 0.0f;
-                for (uint32_t r = 0; r < ctas; ++r) s += peer2(&mine, r).x;
-            }
-        } else {
-            e.k = __fmul_rn(m, c);
-        }
-        scale = __frcp_rn(s);
-        sum = s;
+    uint32_t row = blockIdx.x / ctas;
+    ShortList list;
+    if (has_list) load_short(a, row, t / 32, list);
+    float w = weight_of(row);
+    if (kGrad) empty_table<kThreads>(table, a.slots);
+    Place<T> at_row(a, row, lo, n);
+    float edge = -INFINITY;
+    if (w > 0.0f) {
+        const uint4* mem = reinterpret_cast<const uint4*>(at_row.z + at_row.head);
+        for (uint32_t v = t; v < at_row.nvec; v += kThreads) fetch(mem, v);
+        if (at_row.edge(t)) edge = at(at_row.z, at_row.edge_at(t));
     }
-    const float total = total_weight(a, lists);
-    if constexpr (kGrad) {
-        if (total > 0.0f) {
-            const float coef = w * a.temperature, back = a.total / total, by = scale * coef;
-            const auto z_at = [&](int32_t key) {
-                const uint32_t i = key - lo - head;          // below 0: beyond nvec * kV
-                return i < nvec * kV ? at(reinterpret_cast<const T*>(dyn), i) : at(z, key);
-            };
-            entry_values<kThreads>(a, z_at, e, coef, scale, back, table);
+    const float c = a.inv_t * kLog2e, most = kFastMost / c;      // of a maximum, for the fast form
+
+    uint32_t turn = 0;                     // rows with an exchange so far
+    while (row < a.rows) {
+        const uint32_t next = row + step;
+        const float w_next = weight_of(next);
+        const Place<T> place = at_row;
+        at_row = Place<T>(a, next < a.rows ? next : row, lo, n);
+        const uint4 *mem = reinterpret_cast<const uint4*>(place.z + place.head),
+                    *mem_next = reinterpret_cast<const uint4*>(at_row.z + at_row.head);
+        const T* z = place.z - lo;
+        T* g = kGrad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
+        T* gs = kGrad ? g + lo : nullptr;
+        const uint32_t nvec = place.nvec, head = place.head;
+        const bool has_edge = place.edge(t);
+        const bool same_phase = kGrad && reinterpret_cast<uintptr_t>(gs) % 16 == reinterpret_cast<uintptr_t>(place.z) % 16;
+        const auto put_vec = [&](uint32_t v, const uint4& x) {
+            T* p = gs + head + v * kV;
+            if (same_phase) {
+                st_v4u(p, x);
+            } else {
+                const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+                for (uint32_t i = 0; i < kV; ++i) p[i] = e[i];
+            }
+        };
+        const auto write_zeros = [&] {
+            for (uint32_t v = t; v < nvec; v += kThreads) put_vec(v, make_uint4(0, 0, 0, 0));
+            if (has_edge) set(gs, place.edge_at(t), 0.0f);
+        };
+        // a thread's vectors of the next row from v on, once the present ones are not needed
+        const auto fetch_next = [&](uint32_t v) {
+            if (w_next > 0.0f)
+                for (; v < at_row.nvec; v += kThreads) fetch(mem_next, v);
+        };
+        if (!(w > 0.0f)) {
+            if (kGrad) write_zeros();
+            if (t == 0 && rank == 0) {
+                if (a.loss) a.loss[row] = 0.0f;
+                if (a.lse_out) a.lse_out[row] = 0.0f;
+            }
+            fetch_next(t);
+        } else {
+            if (t < kMaxDistillClients) lists.on[t] = 0.0f;
             __syncthreads();
-            if (e.fast) {
-                const float2 cc = make_float2(e.c, e.c), kk = make_float2(-e.k, -e.k), bb = make_float2(by, by);
+            if (has_list)
+                use_short<T, kGrad>(a, z, t / 32, want_loss, lo, hi, list, lists, table);
+            else if (!brief)
+                read_lists<T, kGrad, kThreads>(a, z, row, want_loss, lo, hi, lists, table);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+
+            Exp e{c, 0.0f, 0.0f, 0.0f, true};
+            float scale = 1.0f, sum = 1.0f;        // q = e(z) * scale
+            if (a.lse_in) {
+                e = from_lse(a, a.lse_in[row], scale);
+                if (has_list && want_loss) end_short(a, t / 32, list, lists);
+                __syncthreads();
+                // in place, the peers may write their slices only when rank 0 has taken the
+                // loss's logits (below, the exchange of statistics sees to that)
+                if (ctas > 1 && a.loss) sync_cluster();
+            } else {
+                // One pass: the sum over a reference, the largest of what the warp has at two
+                // places of the row, in place of the maximum.  Terms over it are no harm up to
+                // 2^100 (beyond, the plain form below).
+                float m = fmaxf(edge, -most);
+                if (t < nvec) {
+                    m = max_of<T>(m, held[t]);
+                    m = max_of<T>(m, held[t + (nvec - 1 - t) / (2 * kThreads) * kThreads]);
+                }
+                m = warp_largest(m);
+                e.k = __fmul_rn(m, c);
+                float2 s2 = make_float2(e.quick(edge), 0.0f);
+                const float2 cc = make_float2(c, c), kk = make_float2(-e.k, -e.k);
+#pragma unroll 4
+                for (uint32_t v = t; v < nvec; v += kThreads) {
+                    float x[kV];
+                    unpack<T>(held[v], x);
+                    if (!kGrad && w_next > 0.0f && v < at_row.nvec) fetch(mem_next, v);
+                    float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (uint32_t j = 0; j < kV; j += 2) {
+                        const float2 y = fma2(make_float2(x[j], x[j + 1]), cc, kk);
+                        part = add2(part, make_float2(ex2(y.x), ex2(y.y)));
+                    }
+                    s2 = add2(s2, part);
+                }
+                if (!kGrad) fetch_next(t < nvec ? t + (nvec - t + kThreads - 1) / kThreads * kThreads : t);
+                // merged over the warp, the CTA and the cluster, in a fixed order
+                float s = warp_sum(s2.x + s2.y);
+                if (t % 32 == 0) {
+                    tmp[t / 32] = m;
+                    tmp2[t / 32] = s;
+                }
+                if (has_list && want_loss) end_short(a, t / 32, list, lists);
+                __syncthreads();
+                m = tmp[t % kWarps];
+                s = tmp2[t % kWarps];
+                merge_lanes<kWarps>(m, s, c);
+                if (ctas > 1) {
+                    // two places in turn: a peer may still read the last row's
+                    float2* mine = &pairs[turn++ % 2];
+                    if (t == 0) *mine = make_float2(m, s);
+                    sync_cluster();
+                    const float2 first = peer2(mine, 0);
+                    m = first.x;
+                    s = first.y;
+                    for (uint32_t r = 1; r < ctas; ++r) {
+                        const float2 v = peer2(mine, r);
+                        merge(m, s, v.x, v.y, c);
+                    }
+                }
+                if (!(fabsf(m) < most && s < kSumMost)) {
+                    // the same for every thread of the cluster: the plain form from memory,
+                    // maximum first
+                    float2* mine = &pairs[(turn + 1) % 2];       // the exchange's
+                    m = edge;
+                    for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, ld_plain_v4(mem + v));
+                    m = block_reduce<kThreads, true>(m, tmp);
+                    if (ctas > 1) {
+                        sync_cluster();
+                        if (t == 0) mine->x = m;
+                        sync_cluster();
+                        for (uint32_t r = 0; r < ctas; ++r) m = fmaxf(m, peer2(mine, r).x);
+                    }
+                    e = {0.0f, m, 1.0f, c, false};
+                    s = has_edge ? e.slow(edge) : 0.0f;
+                    for (uint32_t v = t; v < nvec; v += kThreads) {
+                        float x[kV];
+                        unpack<T>(ld_plain_v4(mem + v), x);
+#pragma unroll
+                        for (uint32_t j = 0; j < kV; ++j) s += e.slow(x[j]);
+                    }
+                    s = block_reduce<kThreads, false>(s, tmp);
+                    if (ctas > 1) {
+                        sync_cluster();
+                        if (t == 0) mine->x = s;
+                        sync_cluster();
+                        s = 0.0f;
+                        for (uint32_t r = 0; r < ctas; ++r) s += peer2(mine, r).x;
+                    }
+                } else {
+                    e.k = __fmul_rn(m, c);
+                }
+                scale = __frcp_rn(s);
+                sum = s;
+            }
+            if (has_list && next < a.rows) load_short(a, next, t / 32, list);
+            const float total = total_weight(a, lists);
+            if constexpr (kGrad) {
+                const float coef = w * a.temperature, back = a.total / total, by = scale * coef;
+                const auto z_at = [&](int32_t key) {
+                    const uint32_t i = key - lo - head;          // below 0: beyond nvec * kV
+                    return i < nvec * kV ? at(reinterpret_cast<const T*>(dyn), i) : at(z, key);
+                };
+                if (total > 0.0f) entry_values<kThreads>(a, z_at, e, coef, scale, back, table);
+                __syncthreads();
                 const auto grad_of = [&](uint32_t v) {
+                    const float2 cc = make_float2(e.c, e.c), kk = make_float2(-e.k, -e.k), bb = make_float2(by, by);
                     float x[kV];
                     unpack<T>(held[v], x);
 #pragma unroll
-                    for (int j = 0; j < kV; j += 2) {
+                    for (uint32_t j = 0; j < kV; j += 2) {
                         float2 y = fma2(make_float2(x[j], x[j + 1]), cc, kk);
                         y = mul2(make_float2(ex2(y.x), ex2(y.y)), bb);
                         x[j] = y.x;
@@ -606,37 +688,52 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
                     }
                     return pack<T>(x);
                 };
-                if (same_phase) {
+                if (!(total > 0.0f)) {
+                    write_zeros();
+                    fetch_next(t);
+                } else if (e.fast && same_phase) {
                     uint4* to = reinterpret_cast<uint4*>(gs + head);
+                    const uint32_t ahead = w_next > 0.0f ? at_row.nvec : 0;
 #pragma unroll 4
-                    for (uint32_t v = t; v < nvec; v += kThreads) st_v4u(to + v, grad_of(v));
+                    for (uint32_t v = t; v < nvec; v += kThreads) {
+                        st_v4u(to + v, grad_of(v));
+                        if (v < ahead) fetch(mem_next, v);
+                    }
+                    fetch_next(t < nvec ? t + (nvec - t + kThreads - 1) / kThreads * kThreads : t);
                 } else {
-                    for (uint32_t v = t; v < nvec; v += kThreads) put_vec(v, grad_of(v));
-                }
-            } else {
-                for (uint32_t v = t; v < nvec; v += kThreads) {
-                    float x[kV];
-                    unpack<T>(held[v], x);
+                    for (uint32_t v = t; v < nvec; v += kThreads) {
+                        if (e.fast) {
+                            put_vec(v, grad_of(v));
+                        } else {
+                            float x[kV];
+                            unpack<T>(held[v], x);
 #pragma unroll
-                    for (int j = 0; j < kV; ++j) x[j] = e.slow(x[j]) * by;
-                    put_vec(v, pack<T>(x));
+                            for (uint32_t j = 0; j < kV; ++j) x[j] = e.slow(x[j]) * by;
+                            put_vec(v, pack<T>(x));
+                        }
+                    }
+                    fetch_next(t);
                 }
+                if (has_edge && total > 0.0f) set(gs, place.edge_at(t), e(edge) * by);
+                __syncthreads();
+                write_entries<T, kThreads>(a, g, total > 0.0f, table);
             }
-            if (has_edge) set(gs, edge_at, e(edge) * by);
-            __syncthreads();
-            write_entries<T, kThreads>(a, g, table);
-        } else {
-            write_zeros();
+            // by the warp that has the fewest lists
+            if (t / 32 == kWarps - 1 && rank == 0 && (a.loss || a.lse_out)) {
+                const float lse = a.lse_in  ? a.lse_in[row]
+                                  : e.fast ? (e.k + log2f(sum)) * 0.69314718055994531f
+                                           : fmaf(e.k, a.inv_t, logf(sum));
+                write_loss(a, lists, row, w, total, lse);
+            }
+            __syncthreads();                   // the lists' and the reductions' places are free
+            if (kGrad && t == 0) taken = 0;
         }
+        if (!(w > 0.0f) && has_list && next < a.rows) load_short(a, next, t / 32, list);
+        edge = w_next > 0.0f && at_row.edge(t) ? at(at_row.z, at_row.edge_at(t)) : -INFINITY;
+        w = w_next;
+        row = next;
     }
-    // last, by the warp that has the fewest lists
-    if (t / 32 == kWarps - 1 && rank == 0 && (a.loss || a.lse_out)) {
-        const float lse = a.lse_in  ? a.lse_in[row]
-                          : e.fast ? (e.k + log2f(sum)) * 0.69314718055994531f
-                                   : fmaf(e.k, a.inv_t, logf(sum));
-        write_loss(a, lists, row, w, total, lse);
-    }
-    if (ctas > 1) sync_cluster();          // a peer may still read `mine`
+    if (ctas > 1) sync_cluster();          // a peer may still read this CTA's pair
 }
 
 // ----------------------------------------------------------------- rows streamed
@@ -647,7 +744,8 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
     extern __shared__ __align__(16) uint8_t dyn[];               // the table
     __shared__ float tmp[kDThreads / 32];
     __shared__ __align__(16) Lists lists;
-    const Slots table = slots_at(dyn, a.slots);
+    __shared__ uint32_t taken;
+    const Slots table = slots_at(dyn, a.slots, &taken);
     const uint32_t row = blockIdx.x;
     const float w = a.row_weight ? a.row_weight[row] : 1.0f;
     const T* z = static_cast<const T*>(a.logits) + row * a.ld;
@@ -661,11 +759,7 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
         }
         return;
     }
-    if (kGrad)
-        for (uint32_t i = threadIdx.x; i < a.slots; i += kDThreads) {
-            table.key[i] = -1;
-            table.hi[i] = table.lo[i] = 0;
-        }
+    if (kGrad) empty_table<kDThreads>(table, a.slots);
     if (threadIdx.x < kMaxDistillClients) lists.on[threadIdx.x] = 0.0f;
     __syncthreads();
     read_lists<T, kGrad, kDThreads>(a, z, row, a.loss != nullptr, 0, a.vocab, lists, table);
@@ -698,7 +792,7 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
 #pragma unroll 8
         for (uint32_t i = threadIdx.x; i < a.vocab; i += kDThreads) set(g, i, some ? e(at(z, i)) * by : 0.0f);
         __syncthreads();
-        if (some) write_entries<T, kDThreads>(a, g, table);
+        write_entries<T, kDThreads>(a, g, some, table);
     }
 }
 
@@ -713,7 +807,7 @@ cudaError_t prepare_distill() {
     const auto allow = [&](DistillKernel k) {
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kMaxSlice + 12 * 2 * kMaxDistillTopk);
+                                     kMaxSlice + kSlotBytes * 2 * kMaxDistillTopk);
     };
     for (int i = 0; i < 2; ++i) {
         allow(kRowKernels<uint16_t, false>[i]);
@@ -734,7 +828,7 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     a.short_lists = true;
     for (uint32_t j = 0; j < a.nclients; ++j) a.short_lists = a.short_lists && a.client[j].topk <= kShortTopk;
     const bool grad = a.grad != nullptr;
-    const uint32_t size = a.dtype ? 2 : 4, table = grad ? a.slots * 12 : 0;
+    const uint32_t size = a.dtype ? 2 : 4, table = grad ? a.slots * kSlotBytes : 0;
     const uint64_t bytes = static_cast<uint64_t>(a.vocab) * size;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
@@ -743,11 +837,13 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     DistillKernel kern;
+    bool held = true;                      // rows on chip
     uint32_t cluster = 1;
     while (cluster < 8 && bytes > static_cast<uint64_t>(cluster) * kMaxSlice) cluster *= 2;
     if (bytes > static_cast<uint64_t>(cluster) * kMaxSlice || static_cast<uint64_t>(a.rows) * cluster >= (1ull << 31)) {
         kern = a.dtype ? (grad ? distill_stream_kernel<uint16_t, true> : distill_stream_kernel<uint16_t, false>)
                        : (grad ? distill_stream_kernel<float, true> : distill_stream_kernel<float, false>);
+        held = false;
         a.cluster = 1;
         cfg.blockDim = dim3(kDThreads);
         cfg.dynamicSmemBytes = table;
@@ -765,6 +861,28 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     at[0].val.clusterDim.x = a.cluster;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
     cfg.gridDim = dim3(a.rows * a.cluster);
+    if (held) {
+        // as many clusters as run at one time; the same kernel and sizes as in the last call of
+        // this thread are not asked for again
+        static thread_local struct {
+            DistillKernel kern = nullptr;
+            uint32_t cluster = 0;
+            size_t smem = 0;
+            int device = -1, clusters = 0;
+        } last;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess &&
+            !(last.kern == kern && last.cluster == a.cluster && last.smem == cfg.dynamicSmemBytes && last.device == dev)) {
+            int n = 0;
+            cudaLaunchConfig_t ask = cfg;
+            ask.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kern), &ask);
+            last = {kern, a.cluster, cfg.dynamicSmemBytes, dev, n};
+        }
+        if (e != cudaSuccess) return e;
+        if (a.rows > static_cast<uint32_t>(last.clusters) && last.clusters > 0) cfg.gridDim = dim3(last.clusters * a.cluster);
+    }
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
