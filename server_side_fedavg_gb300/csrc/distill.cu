@@ -122,26 +122,37 @@ __device__ __forceinline__ void set(T* p, uint64_t e, float v) {
         p[e] = v;
 }
 
-__device__ __forceinline__ uint32_t hash_of(int32_t key, uint32_t slots) {
-    return (static_cast<uint32_t>(key) * 2654435761u) >> (__clz(slots) + 1);   // top log2(slots) bits
-}
-
 // ----------------------------------------------------------------- the clients' lists
-// A share of p of entry e into the table.
-__device__ __forceinline__ void put_share(const Slots& table, uint32_t slots, int32_t e, float p, float share) {
-    uint32_t h = hash_of(e, slots);
-    for (;; h = (h + 1) & (slots - 1)) {
-        const int32_t was = atomicCAS(&table.key[h], -1, e);
-        if (was == e) break;
-        if (was == -1) {
-            table.taken[atomicAdd(table.count, 1u)] = static_cast<uint16_t>(h);
-            break;
+// The warp's lanes each put a share of entry e into the table (if `mine`).  All lanes stay
+// together: lanes that leave the search one by one would each do the rest on their own.
+__device__ __forceinline__ void put_shares(const DistillArgs& a, const Slots& table, bool mine, int32_t e, float x) {
+    // two multiplications with the high bits folded down between: one alone leaves evenly spaced
+    // entries in clusters
+    uint32_t h = static_cast<uint32_t>(e) * 2654435761u;
+    h = (h ^ h >> 15) * 2246822519u >> a.hash_shift;
+    bool search = mine, won = false;
+    while (__any_sync(~0u, search))
+        if (search) {
+            const int32_t was = atomicCAS(&table.key[h], -1, e);
+            won = was == -1;
+            search = !won && was != e;
+            if (search) h = (h + 1) & (a.slots - 1);
         }
+    __syncwarp();
+    const uint32_t winners = __ballot_sync(~0u, won), lane = threadIdx.x % 32;
+    if (winners) {
+        uint32_t base = 0;
+        if (lane == 0) base = atomicAdd(table.count, static_cast<uint32_t>(__popc(winners)));
+        base = __shfl_sync(~0u, base, 0);
+        if (won) table.taken[base + __popc(winners & ((1u << lane) - 1))] = static_cast<uint16_t>(h);
     }
-    if (p != p)
-        atomicOr(&table.hi[h], kPoison);
-    else
-        add_share(table, h, p * share);
+    if (mine) {
+        if (x != x)
+            atomicOr(&table.hi[h], kPoison);
+        else
+            add_share(table, h, x);
+    }
+    __syncwarp();
 }
 
 struct Lists {
@@ -181,16 +192,18 @@ __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uin
         const float inv = 1.0f / sum, logsum = logf(sum);
         float loss = 0.0f, mass = 0.0f;
         if (on)
-            for (uint32_t i = lane; i < cl.topk; i += 32) {
-                const int32_t e = cl.index[base + i];
-                if (static_cast<uint32_t>(e) >= a.vocab) continue;
-                const float d = (value_at(cl.value, base + i, a.value_dtype) - top) * a.inv_t;
-                const float p = ex2(d * kLog2e) * inv;
-                if (p == 0.0f) continue;      // nothing, also where the student's logit is -inf
+            for (uint32_t i0 = 0; i0 < cl.topk; i0 += 32) {
+                const uint32_t i = i0 + lane;
+                const int32_t e = i < cl.topk ? cl.index[base + i] : -1;
+                const bool used = static_cast<uint32_t>(e) < a.vocab;
+                const float d = used ? (value_at(cl.value, base + i, a.value_dtype) - top) * a.inv_t : 0.0f;
+                const float p = used ? ex2(d * kLog2e) * inv : 0.0f;
+                // a p of 0 is nothing, also where the student's logit is -inf
+                const bool some = !(p == 0.0f);
                 mass += p;
-                if (want_loss) loss += p * (d - logsum - at(z, e) * a.inv_t);
-                if (kGrad && static_cast<uint32_t>(e) >= lo && static_cast<uint32_t>(e) < hi)
-                    put_share(table, a.slots, e, p, cl.share);
+                if (want_loss && some) loss += p * (d - logsum - at(z, e) * a.inv_t);
+                if (kGrad)
+                    put_shares(a, table, some && static_cast<uint32_t>(e) >= lo && static_cast<uint32_t>(e) < hi, e, p * cl.share);
             }
         loss = warp_sum(loss);
         mass = warp_sum(mass);
@@ -265,7 +278,7 @@ __device__ __forceinline__ void use_short(const DistillArgs& a, const T* z, uint
         s.u[i] -= logsum;
         mass += s.p[i];
         const uint32_t e = static_cast<uint32_t>(s.e[i]);
-        if (kGrad && !(s.p[i] == 0.0f) && e >= lo && e < hi) put_share(table, a.slots, s.e[i], s.p[i], cl.share);
+        if (kGrad) put_shares(a, table, !(s.p[i] == 0.0f) && e >= lo && e < hi, s.e[i], s.p[i] * cl.share);
     }
     mass = warp_sum(mass);
     if (threadIdx.x % 32 == 0) {
@@ -414,7 +427,7 @@ __device__ __forceinline__ void merge_lanes(float& m, float& s, float c) {
 
 __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
     const float top = fmaxf(m, m2), k = __fmul_rn(top, c);
-    s = s * ex2(__fmul_rn(m, c) - k) + s2 * ex2(__fmul_rn(m2, c) - k);
+    s = __fmaf_rn(s2, ex2(__fmul_rn(m2, c) - k), __fmul_rn(s, ex2(__fmul_rn(m, c) - k)));
     m = top;
 }
 
@@ -825,6 +838,8 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     for (uint32_t j = 0; j < a.nclients; ++j) entries += a.client[j].topk;
     a.slots = 2;
     while (a.slots < 2 * entries) a.slots *= 2;
+    a.hash_shift = 32;
+    for (uint32_t n = a.slots; n > 1; n /= 2) --a.hash_shift;          // the top log2(slots) bits
     a.short_lists = true;
     for (uint32_t j = 0; j < a.nclients; ++j) a.short_lists = a.short_lists && a.client[j].topk <= kShortTopk;
     const bool grad = a.grad != nullptr;

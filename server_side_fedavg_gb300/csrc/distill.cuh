@@ -32,6 +32,7 @@ struct DistillArgs {
     uint32_t rows, vocab;
     uint32_t nclients;
     uint32_t slots;            // hash slots: a power of two >= 2 * (sum of topk)
+    uint32_t hash_shift;
     uint32_t cluster, slice;   // CTAs per row and the elements of each
     uint32_t table_at;         // bytes of a slice's vectors in shared memory: the table follows
     float temperature, inv_t;
