@@ -200,7 +200,7 @@ def _ptr(x) -> int:
     if isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
+        return x.data_ptr()
     if hasattr(x, "ctypes"):
         return int(x.ctypes.data)
     raise TypeError(f"cannot take a pointer of {type(x)!r}")
@@ -484,11 +484,11 @@ def distill_lists(index, value, topk, weights, dtype_value="f32"):
     """The clients' top-logit lists for fa_distill_loss and fa_distill_grad, marshalled once:
     per client its index array [rows, topk] (int32, negative: unused), its value array, its
     topk and its weight (sample count).  The arrays are kept alive by the result."""
-    _same_length(index=index, value=value, topk=topk, weights=weights)
     n = len(index)
-    arr = (fa_distill_client * max(n, 1))()
-    for c, i, v, t, w in zip(arr, index, value, topk, weights):
-        c.index, c.value, c.topk, c.weight = _ptr(i), _ptr(v), t, w
+    if not n == len(value) == len(topk) == len(weights):
+        _same_length(index=index, value=value, topk=topk, weights=weights)
+    arr = (fa_distill_client * max(n, 1))(*[(_ptr(i), _ptr(v), t, 0, w)
+                                            for i, v, t, w in zip(index, value, topk, weights)])
     return arr, n, DTYPES[dtype_value], (list(index), list(value))
 
 

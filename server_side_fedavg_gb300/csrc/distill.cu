@@ -3,7 +3,7 @@
 //   loss   log sum exp of the row, and over the clients' lists sum p (log p - log q)
 //   grad   w T (q - share), share being nonzero at the lists' entries alone
 //
-// Rows of up to 8 x 64 KB are held in shared memory: a CTA (or a cluster of 2, 4 or 8, each with
+// Rows of up to 8 x 66 KB are held in shared memory: a CTA (or a cluster of 2, 4 or 8, each with
 // a slice) loads its row once with every load in flight at the same time, sums its exponentials
 // -- each warp over a reference of its own, pairs (reference, sum) merged over the CTA and, through
 // distributed shared memory, the cluster -- and writes the gradient from there.
@@ -364,7 +364,7 @@ __device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, bool s
 }
 
 // ----------------------------------------------------------------- rows held on chip
-constexpr uint32_t kMaxSlice = 65536;  // bytes of a row that a CTA holds: three CTAs per SM
+constexpr uint32_t kMaxSlice = 66 * 1024;   // bytes of a row that a CTA holds: three CTAs per SM
 
 __device__ __forceinline__ uint32_t rank_in_cluster() {
     uint32_t r;
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
                 __syncthreads();
                 // in place, the peers may write their slices only when rank 0 has taken the
                 // loss's logits (below, the exchange of statistics sees to that)
-                if (ctas > 1 && a.loss) sync_cluster();
+                if (ctas > 1 && a.loss && a.grad == a.logits) sync_cluster();
             } else {
                 // One pass: the sum over a reference, the largest of what the warp has at two
                 // places of the row, in place of the maximum.  Terms over it are no harm up to
