@@ -53,7 +53,7 @@ cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows,
 // ldz as fp32 (dz_planes 0), rounded to bf16 (1) or as three bf16 planes (3), m * ldz
 // elements apart; and its column sums over blocks of kColRows rows, to
 // part[ceil(m / kColRows)][n] (part != nullptr).
-constexpr uint32_t kColRows = 64;
+constexpr uint32_t kColRows = 32;
 struct ActGradArgs {
     uint32_t m, n;
     const void* dout;

@@ -25,22 +25,51 @@ __device__ __forceinline__ void put(void* p, uint64_t e, int dt, float v) {
         static_cast<float*>(p)[e] = v;
 }
 
+// exp(x), off by up to 2^-22 and |x| 2^-23 of its value.
+__device__ __forceinline__ float exp_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
+// Phi(z), the normal distribution, by the rational approximation 7.1.26 of Abramowitz and Stegun,
+// "Handbook of Mathematical Functions": erfc(x) = exp(-x^2) (a1 t + ... + a5 t^5), t = 1 / (1 + p x),
+// for x >= 0, absolute error up to 1.5e-7 -- of the size of fp32's rounding of Phi near 1.  `bell`
+// receives exp(-z^2 / 2), which the derivative needs too.  A third of the instructions of erff
+// and expf, which bounded the activation gradient (27 us at 2056 x 4096).
+__device__ __forceinline__ float normal_cdf(float z, float& bell) {
+    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
+    float s = fmaf(t, 1.061405429f, -1.453152027f);
+    s = fmaf(t, s, 1.421413741f);
+    s = fmaf(t, s, -0.284496736f);
+    s = fmaf(t, s, 0.254829592f);
+    bell = exp_fast(-0.5f * z * z);
+    const float tail = 0.5f * t * s * bell;
+    return z >= 0.0f ? 1.0f - tail : tail;
+}
+
 // act(z).  A NaN stays a NaN in each.
 __device__ __forceinline__ float act_fwd(int act, float z) {
     if (act == kActRelu) return z < 0.0f ? 0.0f : z;
-    if (act == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    if (act == kActSilu) return __fdividef(z, 1.0f + expf(-z));
+    if (act == kActGelu) {
+        float bell;
+        return z * normal_cdf(z, bell);
+    }
+    if (act == kActSilu) return __fdividef(z, 1.0f + exp_fast(-z));
     return z;
 }
 
 // act'(z):  relu [z > 0];  gelu Phi(z) + z phi(z);  silu s (1 + z (1 - s)), s = 1 / (1 + exp(-z)).
 __device__ __forceinline__ float act_grad(int act, float z) {
     if (act == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == kActGelu)
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    if (act == kActGelu) {
+        float bell;
+        const float cdf = normal_cdf(z, bell);
+        return fmaf(z * bell, 0.39894228040143268f, cdf);
+    }
     if (act == kActSilu) {
-        const float s = __fdividef(1.0f, 1.0f + expf(-z));
-        return s * (1.0f + z * (1.0f - s));
+        const float s = __fdividef(1.0f, 1.0f + exp_fast(-z));
+        return s * fmaf(z, 1.0f - s, 1.0f);
     }
     return 1.0f;
 }

@@ -70,28 +70,47 @@ __global__ void __launch_bounds__(256) split_kernel(const void* src, uint64_t ld
     }
 }
 
+template <int kAct>
+__device__ __forceinline__ void times_grad(float (&d)[8], const float (&z)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] *= act_grad(kAct, z[j]);
+}
+
+// Columns c .. c + 7 at p (those past the row's end as 0).
+template <typename T>
+__device__ __forceinline__ void load8t(const T* p, uint32_t c, uint32_t cols, bool vec, float (&x)[8]) {
+    if (vec && c + 8 <= cols)
+        plain_vec8(p, x);
+    else
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = c + i < cols ? elem(p, i, sizeof(T) == 2) : 0.0f;
+}
+
 // A block of kColRows rows by 256 columns per CTA: a lane holds 8 columns, a warp every
 // eighth row; the column sums join over the warps in warp order.
-__global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ ActGradArgs a, bool vd, bool vp, bool vz) {
+template <typename T>
+__global__ void __launch_bounds__(256, 4) act_grad_kernel(const __grid_constant__ ActGradArgs a, bool vec, bool vz) {
     __shared__ float sums[8][256];
     wait_predecessor();
     const uint32_t c = blockIdx.x * 256 + threadIdx.x % 32 * 8, warp = threadIdx.x / 32;
     const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
     const uint64_t plane = a.m * a.ldz;
+    const T *dout = static_cast<const T*>(a.dout), *pre = static_cast<const T*>(a.pre);
     for (uint32_t blk = blockIdx.y; blk < blocks; blk += gridDim.y) {
         float s[8] = {};
         if (c < a.n)
-            for (uint32_t i = 0; i < kColRows / 8; ++i) {
-                const uint32_t r = blk * kColRows + warp + 8 * i;
-                if (r >= a.m) break;
-                float d[8];
-                load8(a.dout, r * a.ldd, c, a.n, a.dtype, vd, d);
-                if (a.pre) {
-                    float z[8];
-                    load8(a.pre, r * a.ldp, c, a.n, a.dtype, vp, z);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) d[j] = c + j < a.n ? d[j] * act_grad(a.act, z[j]) : 0.0f;
-                }
+            // a row at a time, in small code: four CTAs per SM keep 32 KB of loads in flight
+#pragma unroll 1
+            for (uint32_t r = blk * kColRows + warp; r < min(a.m, (blk + 1) * kColRows); r += 8) {
+                float d[8], z[8];
+                load8t(dout + r * a.ldd + c, c, a.n, vec, d);
+                if (pre) load8t(pre + r * a.ldp + c, c, a.n, vec, z);
+                if (a.act == kActGelu)
+                    times_grad<kActGelu>(d, z);
+                else if (a.act == kActSilu)
+                    times_grad<kActSilu>(d, z);
+                else if (a.act == kActRelu)
+                    times_grad<kActRelu>(d, z);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[j] += d[j];
                 if (!a.dz) continue;
@@ -100,6 +119,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
                 } else if (vz && c + 8 <= a.n) {
                     store8_global<float>(a.dz, r * a.ldz + c, d);
                 } else {
+#pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (c + j < a.n) static_cast<float*>(a.dz)[r * a.ldz + c + j] = d[j];
                 }
@@ -124,6 +144,7 @@ __global__ void __launch_bounds__(256) col_sum_kernel(const float* part, uint32_
     const uint32_t c = blockIdx.x * 256 + threadIdx.x;
     if (c >= n) return;
     float s = 0.0f;
+#pragma unroll 16
     for (uint32_t b = 0; b < blocks; ++b) s += part[static_cast<uint64_t>(b) * n + c];
     put(out, c, out_dtype, s);
 }
@@ -144,8 +165,9 @@ cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows,
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream) {
     const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
-    return launch_next(act_grad_kernel, dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, stream, a,
-                       vec_ok(a.dout, a.ldd, a.dtype), vec_ok(a.pre, a.ldp, a.dtype), vec_ok(a.dz, a.ldz, 0));
+    return launch_next(a.dtype ? act_grad_kernel<uint16_t> : act_grad_kernel<float>,
+                       dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, stream, a,
+                       vec_ok(a.dout, a.ldd, a.dtype) && vec_ok(a.pre, a.ldp, a.dtype), vec_ok(a.dz, a.ldz, 0));
 }
 
 cudaError_t launch_col_sum(const float* part, uint32_t blocks, uint32_t n, void* out, int out_dtype,

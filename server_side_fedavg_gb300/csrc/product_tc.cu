@@ -14,9 +14,9 @@
 // while one is drained.
 //
 // kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates: 4.4e-6 off over 4096
-// terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms into
-// registers, which sum with rounding to nearest: 2.4e-7 (every block 1.6e-7, every 8 blocks
-// 4.8e-7).  The products of planes other than the first two have an accumulator of their own,
+// terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms (8 in the
+// 256-column form) into registers, which sum with rounding to nearest: 2.4e-7 (4.8e-7; every 2
+// blocks 1.6e-7, every 16 1e-6).  The products of planes other than the first two have an accumulator of their own,
 // which is 2^-8 of the first and is read once a tile.
 //
 // kSwap: Q (columns) holds the tokens and P the weights -- for few tokens, where the 128 lanes
@@ -1012,7 +1012,9 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.group = 8;
     a.splits = c.ctas == 2 ? 1 : p.splits;
     if (a.splits > a.kblocks) a.splits = a.kblocks;
-    a.chunk_kb = 4 / a.sub;
+    // the pair kernel drains every 8 blocks: with 4 the round trip from commit to drained and back
+    // took longer than the products (1024 x 4096 x 32000: 217 us against 181)
+    a.chunk_kb = c.bn == 256 ? 8 : 4 / a.sub;
     auto vec = [&](const void* q, uint64_t ld) { return !q || out_ready(q, ld, a.e.out_dtype); };
     a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
     const bool by_tma = a.vec && a.splits == 1 && !c.swap;
