@@ -39,7 +39,7 @@ struct ProdArgs {
 // Any types, strides and storage orders; for small m * n * k (and k == 0).
 cudaError_t launch_product_tiny(const ProdArgs& p, cudaStream_t stream);
 
-// Few rows of a; both operands K-major and of one type.
+// Few rows of a; a K-major, both operands of one type.
 cudaError_t launch_product_thin(const ProdArgs& p, cudaStream_t stream);
 
 // The products' operands where they are not as the tensor-core kernel reads them (bf16,

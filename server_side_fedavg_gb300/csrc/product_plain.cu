@@ -117,6 +117,120 @@ __global__ void __launch_bounds__(kBlockThreads) product_thin_kernel(const __gri
     }
 }
 
+// The same with b stored [k, n]: a lane per column (kVec: two), the eight warps and up to eight
+// CTAs of a cluster divide the summed index; a's rows are staged in shared memory, transposed,
+// and read as broadcasts.  Sums: per lane, over the warps in order, over the cluster in order.
+constexpr int kStage = 256;            // summed elements of a staged at a time
+
+template <typename T, int kRows, bool kVec>
+__global__ void __launch_bounds__(kBlockThreads) product_thin_n_kernel(const __grid_constant__ ProdArgs p, uint32_t splits) {
+    constexpr int kWarps = kBlockThreads / 32, kC = kVec ? 2 : 1, kOut = kRows * 32 * kC;
+    __shared__ __align__(16) float staged[kStage][kRows];
+    __shared__ float part[kWarps][kOut];
+    wait_predecessor();
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const uint32_t c0 = blockIdx.x / splits * 32 * kC, col = c0 + lane * kC;
+    const uint32_t k_lo = static_cast<uint64_t>(p.k) * rank / splits, k_hi = static_cast<uint64_t>(p.k) * (rank + 1) / splits;
+    const T *a = static_cast<const T*>(p.a.p), *b = static_cast<const T*>(p.b.p) + min(col, p.n - kC);
+    for (uint32_t r0 = 0; r0 < p.m; r0 += kRows) {
+        float acc[kRows][kC] = {};
+        for (uint32_t k0 = k_lo; k0 < k_hi; k0 += kStage) {
+            const uint32_t many = min(static_cast<uint32_t>(kStage), k_hi - k0);
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < kStage * kRows; i += kBlockThreads) {
+                const uint32_t r = i / kStage, kk = i % kStage;
+                staged[kk][r] = kk < many && r0 + r < p.m ? elem(a, (r0 + r) * p.a.ld + k0 + kk, sizeof(T) == 2) : 0.0f;
+            }
+            __syncthreads();
+#pragma unroll 8
+            for (uint32_t kk = warp; kk < many; kk += kWarps) {
+                float w[kC];
+                const T* at = b + (k0 + kk) * p.b.ld;
+                if constexpr (kVec && sizeof(T) == 4) {
+                    const float2 v = *reinterpret_cast<const float2*>(at);
+                    w[0] = v.x;
+                    w[1] = v.y;
+                } else if constexpr (kVec) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(at);
+                    w[0] = bf16_lo(v);
+                    w[1] = bf16_hi(v);
+                } else {
+                    w[0] = elem(at, 0, sizeof(T) == 2);
+                }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int c = 0; c < kC; ++c) acc[r][c] = fmaf(staged[kk][r], w[c], acc[r][c]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < kC; ++c) part[warp][(r * 32 + lane) * kC + c] = acc[r][c];
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < kOut; i += kBlockThreads) {
+            float sum = part[0][i];
+            for (int w = 1; w < kWarps; ++w) sum += part[w][i];
+            part[0][i] = sum;
+        }
+        if (splits > 1) {
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            if (rank != 0) {
+                // rank 0 reads this CTA's sums before it goes on
+                asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+                continue;
+            }
+        } else {
+            __syncthreads();
+        }
+        for (uint32_t i = threadIdx.x; i < kOut; i += kBlockThreads) {
+            float sum = part[0][i];
+            for (uint32_t q = 1; q < splits; ++q) {
+                float v;
+                asm volatile("{\n .reg .u32 r;\n mapa.shared::cluster.u32 r, %1, %2;\n ld.shared::cluster.f32 %0, [r];\n}"
+                             : "=f"(v)
+                             : "r"(smem_addr(&part[0][i])), "r"(q)
+                             : "memory");
+                sum += v;
+            }
+            const uint32_t r = r0 + i / (32 * kC), c = c0 + i % (32 * kC);
+            if (r < p.m && c < p.n) finish_one(p.e, sum, r, c);
+        }
+        if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        __syncthreads();
+    }
+}
+
+template <typename T, int kRows, bool kVec>
+cudaError_t thin_n(const ProdArgs& p, cudaStream_t stream) {
+    const uint32_t cols = kVec ? 64 : 32, blocks = (p.n + cols - 1) / cols;
+    // enough CTAs for four per SM, each with a stage's worth of the sum
+    uint32_t splits = 1;
+    while (splits < 8 && blocks * splits < 608 && p.k >= splits * 2 * 64) splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks * splits);
+    cfg.blockDim = dim3(kBlockThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, product_thin_n_kernel<T, kRows, kVec>, p, splits);
+}
+
+template <typename T, bool kVec>
+cudaError_t thin_n_rows(const ProdArgs& p, cudaStream_t stream) {
+    if (p.m == 1) return thin_n<T, 1, kVec>(p, stream);
+    if (p.m <= 4) return thin_n<T, 4, kVec>(p, stream);
+    return thin_n<T, 8, kVec>(p, stream);
+}
+
 template <typename T, bool kVec>
 cudaError_t thin(const ProdArgs& p, cudaStream_t stream) {
     if (p.m == 1)
@@ -139,6 +253,11 @@ cudaError_t launch_product_tiny(const ProdArgs& p, cudaStream_t stream) {
 
 cudaError_t launch_product_thin(const ProdArgs& p, cudaStream_t stream) {
     const uint64_t size = p.a.dtype ? 2 : 4;
+    if (!p.b.kmajor) {
+        const bool two = reinterpret_cast<uintptr_t>(p.b.p) % (2 * size) == 0 && p.b.ld % 2 == 0 && p.n % 2 == 0;
+        if (p.a.dtype) return two ? thin_n_rows<uint16_t, true>(p, stream) : thin_n_rows<uint16_t, false>(p, stream);
+        return two ? thin_n_rows<float, true>(p, stream) : thin_n_rows<float, false>(p, stream);
+    }
     const auto aligned = [&](const ProdOperand& o) {
         return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld * size % 16 == 0;
     };

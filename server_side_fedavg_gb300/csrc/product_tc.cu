@@ -255,6 +255,15 @@ __device__ __forceinline__ float4 ld_part(uint32_t addr, uint32_t q, uint32_t pa
     return v;
 }
 
+__device__ __forceinline__ float ld_part1(uint32_t addr, uint32_t q, uint32_t parts) {
+    float v;
+    if (parts == 1)
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(in_cta(addr, q)) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void st_shared1(uint32_t addr, float a) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
 }
@@ -411,7 +420,7 @@ __device__ __forceinline__ void finish_item(const TcArgs& a, uint32_t unit, uint
     const uint32_t row = row0 + r, c = col0 + j * 4;
     if (row >= a.rows || c >= a.cols) return;
     const ProdEpilogue& e = a.e;
-    const bool vec = a.vec && c + 8 <= a.cols, bf16 = e.out_dtype != 0;
+    const bool vec = c + 8 <= a.cols, bf16 = e.out_dtype != 0;
     float res[8] = {}, v[8] = {};
     if (e.res) {
         const uint64_t at = row * e.ldr + c;
@@ -450,6 +459,46 @@ __device__ __forceinline__ void finish_item(const TcArgs& a, uint32_t unit, uint
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = fmaf(e.beta, res[i], v[i]);
     write(e.out);
+}
+
+// The same eight rows where outputs are not 16-byte aligned: a lane per column, so that stores
+// (and residual loads) of a row are contiguous.
+__device__ __forceinline__ void finish_rows(const TcArgs& a, uint32_t unit, uint32_t part, uint32_t parts, uint32_t row0,
+                                            uint32_t col0) {
+    const uint32_t lane = threadIdx.x % 32, c = col0 + lane, r0 = 8 * part;
+    if (row0 + r0 >= a.rows || c >= a.cols) return;
+    const ProdEpilogue& e = a.e;
+    const uint32_t rows = min(8u, a.rows - row0 - r0);
+    float res[8] = {}, v[8] = {};
+    if (e.res)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < rows) res[i] = elem(e.res, (row0 + r0 + i) * e.ldr + c, e.out_dtype);
+    const float bias = e.bias ? elem(e.bias, c, e.bias_dtype) : 0.0f;
+    for (uint32_t q = 0; q < parts; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += ld_part1(unit + unit_at(r0 + i, lane / 4) + lane % 4 * 4, q, parts);
+    const auto write = [&](void* p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < rows) put(p, (row0 + r0 + i) * e.ldo + c, e.out_dtype, v[i]);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(e.alpha, v[i], bias);
+    if (e.pre) write(e.pre);
+    activate(e.act, v);
+    if (e.res)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.beta, res[i], v[i]);
+    write(e.out);
+}
+
+__device__ __forceinline__ void finish_any(const TcArgs& a, uint32_t unit, uint32_t part, uint32_t parts, uint32_t row0,
+                                           uint32_t col0) {
+    if (a.vec)
+        finish_item(a, unit, part, parts, row0, col0);
+    else
+        finish_rows(a, unit, part, parts, row0, col0);
 }
 
 // kSwap: lane = one output column (P row); four output rows, columns 4 `part` of the unit.
@@ -848,7 +897,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                             if constexpr (kSwap)
                                 finish_item_swapped(a, unit, i, 1, prow, qrow + u * 32);
                             else
-                                finish_item(a, unit, i, 1, prow, qrow + u * 32);
+                                finish_any(a, unit, i, 1, prow, qrow + u * 32);
                         __syncwarp();
                     }
                 }
@@ -880,7 +929,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                 if constexpr (kSwap)
                     finish_item_swapped(a, base + u * kUnit, i, a.splits, prow, qrow);
                 else
-                    finish_item(a, base + u * kUnit, i, a.splits, prow, qrow);
+                    finish_any(a, base + u * kUnit, i, a.splits, prow, qrow);
             }
         }
         cluster_sync();
@@ -957,20 +1006,20 @@ cudaError_t prepare_product_tc(TcShape* shape) {
             e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kKernels[c][d]),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     // how many clusters the GPCs hold (of 8 CTAs, fewer than SMs / 8)
-    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+    for (int i = 1; i <= 8 && e == cudaSuccess; ++i) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(1024);
+        cfg.gridDim = dim3(840 * i);
         cfg.blockDim = dim3(kTcThreads[kTc128][0]);
         cfg.dynamicSmemBytes = kSmemMost;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 1u << i;
+        at[0].val.clusterDim.x = i;
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kKernels[kTc128][0]), &cfg);
-        shape->split_ctas[i] = n << i;
+        shape->split_ctas[i] = n * i;
     }
     if (e == cudaSuccess && !g_encode) {
         void* f = nullptr;

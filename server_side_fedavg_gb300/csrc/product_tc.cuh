@@ -42,7 +42,7 @@ struct TcProduct {
 
 struct TcShape {
     int sms = 0;
-    int split_ctas[4] = {};   // CTAs at one time in clusters of 1, 2, 4, 8, one CTA per SM
+    int split_ctas[9] = {};   // [i]: CTAs at one time in clusters of i, one CTA per SM
 };
 
 struct TcArgs {

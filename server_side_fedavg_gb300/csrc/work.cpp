@@ -238,8 +238,7 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
     double best = 1e300;
     const auto consider = [&](int cfg, uint64_t tiles, uint32_t ctas, double kbytes, double latency, double mma,
                               double per_tile, uint32_t splits) {
-        const int at = splits == 8 ? 3 : splits == 4 ? 2 : splits == 2 ? 1 : 0;
-        const uint64_t room = std::max(1, shape.split_ctas[at]);      // larger clusters leave SMs of a GPC unused
+        const uint64_t room = std::max(1, shape.split_ctas[splits]);      // larger clusters leave SMs of a GPC unused
         const uint64_t all = tiles * splits * ctas, active = std::min(all, room);
         const double load = kbytes * 1.024 * planes / 2 / 112 * static_cast<double>(active) / static_cast<double>(n_sm);
         const double block = std::max(std::max(latency, load), mma * products);
@@ -258,13 +257,13 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
     if (p->m <= 64 && (p->a.kmajor || p->m > 32)) {
         const int cfg = p->m <= 16 ? fa::kTcSwap16 : p->m <= 32 ? fa::kTcSwap32 : fa::kTcSwap64;
         const double kbytes = p->m <= 16 ? 18 : p->m <= 32 ? 20 : 24;
-        for (uint32_t s = 1; s <= 8 && kb >= s; s *= 2) consider(cfg, n128, 1, kbytes, 0.15, 0.13, p->m > 32 ? 1.5 : 1.0, s);
+        for (uint32_t s = 1; s <= 8 && kb >= s; ++s) consider(cfg, n128, 1, kbytes, 0.15, 0.13, p->m > 32 ? 1.5 : 1.0, s);
         if (p->m <= 32) return;
     }
     // planes need TMEM and shared memory beside 256 columns
     if (planes == 2) consider(fa::kTcPair256, m256 * n256, 2, 32, 0.30, 0.30, 2.0, 1);
     consider(fa::kTcPair128, m256 * n128, 2, 24, 0.165, 0.16, 1.0, 1);
-    for (uint32_t s = 1; s <= 8 && kb >= s; s *= 2) {
+    for (uint32_t s = 1; s <= 8 && kb >= s; ++s) {
         consider(fa::kTc128, m128 * n128, 1, 32, 0.185, 0.165, 1.0, s);
         consider(fa::kTc64, m128 * n64, 1, 24, 0.16, 0.13, 1.0, s);
     }
@@ -275,8 +274,8 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
 // aligned copy): read as they are on the FP32 units.  Against 4096 x 4096 fp32 weights: 16
 // rows 23.5 us (tensor cores with their pass 46), 32 rows 46 (48), 64 rows 90 (50).
 bool use_thin(const fa::ProdArgs& q) {
-    if (!q.a.kmajor || !q.b.kmajor || q.a.dtype != q.b.dtype) return false;
-    return q.a.dtype == 0 ? q.m <= 24 : q.m <= 8 && !tma_ready(q.b);
+    if (!q.a.kmajor || q.a.dtype != q.b.dtype) return false;
+    return q.b.dtype == 0 ? q.m <= (q.b.kmajor ? 24 : 16) : q.m <= 8 && !tma_ready(q.b);
 }
 
 // A product by the kernel that suits its size.  run == false only adds up the workspace.
@@ -391,14 +390,15 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     const uint32_t m = static_cast<uint32_t>(p.m), n = static_cast<uint32_t>(p.n), k = static_cast<uint32_t>(p.k);
     const uint32_t blocks = (m + fa::kColRows - 1) / fa::kColRows;
     const int it = code_of(p.dtype_in), dt = code_of(p.dtype_dout), gt = code_of(p.dtype_grad);
-    // dZ is dout itself, or is written to the workspace: in fp32 for the tiny kernel, else
-    // as bf16 planes
+    // dZ is dout itself, or is written to the workspace: in fp32 for the tiny kernel and for few
+    // fp32 rows (see use_thin), else as bf16 planes
     const bool tiny = use_tiny(p.m, p.n, p.k);
+    const bool few = !tiny && it == 0 && p.m <= 16;
     const bool products = want_a || want_b;
     const fa::ProdOperand d_in{p.dout, p.ldd, dt, true};
-    const bool write_dz = products && m && n && (act || (!tiny && !tma_ready(d_in)));
-    const int planes = tiny ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
-    const uint64_t ldz = tiny ? p.n : (p.n + 7) / 8 * 8;
+    const bool write_dz = products && m && n && (act || (!tiny && !few && !tma_ready(d_in)));
+    const int planes = tiny || few ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
+    const uint64_t ldz = tiny || few ? p.n : (p.n + 7) / 8 * 8;
     const bool cap = capturing(s);
     // two passes over the same steps: the first adds up the workspace
     Carve c{nullptr};
@@ -434,7 +434,7 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
             if (tiny || n == 0)
                 r = run ? launched(w, fa::launch_product_tiny(q, s), "gradient of a") : FA_OK;
             else
-                r = do_product(w, q, ta ? nullptr : &tz, ta ? &tz : nullptr, &c, run, s, "gradient of a");
+                r = do_product(w, q, ta || few ? nullptr : &tz, ta && !few ? &tz : nullptr, &c, run, s, "gradient of a");
         }
         const uint64_t after_a = c.used;
         c.used = mark;                    // the second product's operand may take the first's place
@@ -446,7 +446,7 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
             if (tiny || m == 0)
                 r = run ? launched(w, fa::launch_product_tiny(q, s), "gradient of b") : FA_OK;
             else
-                r = do_product(w, q, tb ? &tz_n : nullptr, tb ? nullptr : &tz_n, &c, run, s, "gradient of b");
+                r = do_product(w, q, tb && !few ? &tz_n : nullptr, tb || few ? nullptr : &tz_n, &c, run, s, "gradient of b");
         }
         c.used = std::max(c.used, after_a);
         if (r != FA_OK) return r;
