@@ -489,8 +489,11 @@ const char* fa_last_error(const fa_ctx* ctx);
  * queued on other streams is the caller's to order.  No call waits for the GPU, except
  * to free a workspace that has to grow.  Calls can be captured into a CUDA graph once the
  * workspace is large enough (a call that would have to grow it returns FA_ERR_STATE while
- * capturing); replays use the handle's workspace, so they and direct calls on the handle
- * must be ordered by the caller.
+ * capturing); replays use the workspace of the time of the capture (kept until
+ * fa_work_close), so they and direct calls on the handle must be ordered by the caller.
+ * FA_TEST_WAIT_EXPIRES (the test aid above, in fa_work_opts.flags) makes the first data wait
+ * of every tensor-core product give up at once: its outputs are invalid and fa_work_sync
+ * returns FA_ERR_INTERNAL; the kernel waits (bounded) for its own loads and ends.
  */
 typedef struct fa_work fa_work;   /* opaque; owned by the library */
 
@@ -498,7 +501,7 @@ typedef struct {
     uint32_t size;             /* sizeof(fa_work_opts): lets the struct grow */
     uint32_t timeout_ms;       /* bound on every host-side wait (0 = default 60000) */
     uint64_t workspace_bytes;  /* device workspace allocated at open (0 = at first need) */
-    uint32_t flags;            /* 0 (or FA_TEST_WAIT_EXPIRES, see below) */
+    uint32_t flags;            /* 0 (or FA_TEST_WAIT_EXPIRES) */
     uint32_t reserved;         /* 0 */
 } fa_work_opts;
 

@@ -15,6 +15,7 @@
 #include <new>
 #include <string>
 #include <thread>
+#include <vector>
 
 #include "distill.cuh"
 #include "kernels.cuh"
@@ -27,6 +28,8 @@ struct fa_work {
     uint32_t flags = 0;
     uint8_t* ws = nullptr;               // the workspace shared by the handle's calls
     uint64_t ws_bytes = 0;
+    bool ws_captured = false;            // a captured call uses it: a graph may still
+    std::vector<void*> retired;          // workspaces that were, kept for such graphs
     cudaEvent_t chain = nullptr;         // recorded after the last queued call
     bool chain_valid = false;
     unsigned long long chain_stream_id = 0;
@@ -123,7 +126,10 @@ fa_status chain_out(fa_work* w, cudaStream_t s, bool capture) {
 // At least `bytes` of workspace.  Growing waits for the handle's queued calls, which may
 // still use the old one.
 fa_status ensure_ws(fa_work* w, uint64_t bytes, bool capture) {
-    if (bytes <= w->ws_bytes) return FA_OK;
+    if (bytes <= w->ws_bytes) {
+        w->ws_captured |= capture && bytes > 0;
+        return FA_OK;
+    }
     if (capture)
         return fail(w, FA_ERR_STATE, "the workspace would have to grow during capture: run the call once before, "
                                      "or open the handle with workspace_bytes");
@@ -132,9 +138,14 @@ fa_status ensure_ws(fa_work* w, uint64_t bytes, bool capture) {
         if (r != FA_OK) return r;
     }
     bytes = (bytes + (1ull << 21) - 1) >> 21 << 21;
-    if (w->ws) FW_CUDA(w, cudaFree(w->ws));
+    if (w->ws && w->ws_captured) {
+        w->retired.push_back(w->ws);
+    } else if (w->ws) {
+        FW_CUDA(w, cudaFree(w->ws));
+    }
     w->ws = nullptr;
     w->ws_bytes = 0;
+    w->ws_captured = false;
     FW_CUDA(w, cudaMalloc(reinterpret_cast<void**>(&w->ws), bytes));
     w->ws_bytes = bytes;
     w->stats.workspace_bytes = bytes;
@@ -536,6 +547,7 @@ fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStre
 
 void free_work(fa_work* w) {
     if (w->ws) cudaFree(w->ws);
+    for (void* p : w->retired) cudaFree(p);
     if (w->chain) cudaEventDestroy(w->chain);
     if (w->err_ev) cudaEventDestroy(w->err_ev);
     if (w->err_stream) cudaStreamDestroy(w->err_stream);
