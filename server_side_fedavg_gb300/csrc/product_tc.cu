@@ -763,7 +763,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
         const uint32_t stage_unit = o.buf;
         if (o.ahead && lane == 0) load_ahead<kCtas, kBN>(a, o, o.slots, first, step, width, rank);
         const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty, lead_small = lead_empty + 16;
-        uint32_t ch = 0;
+        uint32_t ch = 0, slot = 0, slot_phase = 0;     // slot: of block o.block
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
             const TcTile tile = tc_tile(a, t);
             const uint32_t prow = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0) + quad * 32;
@@ -832,7 +832,16 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
             if (!kSwap && by_tma) {
 #pragma unroll 1
                 for (uint32_t blk = 0; blk < o.blocks; ++blk, ++o.block) {
-                    const uint32_t slot = o.block % o.slots, out = o.buf + slot * kUnit, col = qrow + blk * width;
+                    const uint32_t out = o.buf + slot * kUnit, col = qrow + blk * width;
+                    // the next residuals are asked for before this block is worked on: buffers
+                    // whose last store has been read are free
+                    if (o.ahead && o.slots > 1 && lane == 0) {
+                        if (o.slots == 2)
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        else
+                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        load_ahead<kCtas, kBN>(a, o, o.block + (o.slots == 2 ? 2 : o.slots - 1), first, step, width, rank);
+                    }
                     if (a.e.bias)
                         for (uint32_t i = lane; i < width; i += 32)
                             st_shared1(bias_at + i * 4, col + i < a.cols ? elem(a.e.bias, col + i, a.e.bias_dtype) : 0.0f);
@@ -840,7 +849,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                     for (int pre = a.e.pre != nullptr; pre >= 0; --pre) {
                         // the block's buffer: its residual has come, or its last store has left
                         if (o.ahead)
-                            ok = bar_wait(o.bar + 8 * slot, (o.block / o.slots) & 1, gone, ctas);
+                            ok = bar_wait(o.bar + 8 * slot, slot_phase, gone, ctas);
                         else if (lane == 0 && (o.slots == 1 || a.e.pre))
                             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         else if (lane == 0)
@@ -865,14 +874,15 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                         if (lane == 0) {
                             if (prow < a.rows && col < a.cols) tma_store_2d(pre ? &a.map_pre : &a.map_out, out, col, prow);
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                            if (o.ahead) {
-                                if (o.slots == 1)
-                                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                                else
-                                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                                load_ahead<kCtas, kBN>(a, o, o.block + (o.slots > 1 ? o.slots : 2), first, step, width, rank);
+                            if (o.ahead && o.slots == 1) {
+                                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                                load_ahead<kCtas, kBN>(a, o, o.block + 2, first, step, width, rank);
                             }
                         }
+                    }
+                    if (++slot == o.slots) {
+                        slot = 0;
+                        slot_phase ^= 1;
                     }
                 }
             } else {
