@@ -35,7 +35,7 @@ namespace {
 constexpr int kBK = 64;                    // summed elements per block: 128 bytes, one swizzle row
 // Drain warps: each has the 32 lanes of its quadrant (warp % 4) and a part of the columns.
 // The epilogue is bound by instruction latency, so the pair kernel has 16 of them (with 8, the
-// adapter merge took 29 us instead of %MERGE%).
+// adapter merge of 4096 x 4096 took 29 us instead of 16).
 template <int kBN>
 constexpr int kDrainWarps = kBN == 256 ? 16 : kBN >= 64 ? 8 : 4;
 // Drain warps sharing a quadrant: a block of outputs by TMA is 64 columns wide, so that the
@@ -304,18 +304,23 @@ struct OutWarp {
     uint32_t row_off, col_off;     // of the warp's part within the CTA's tile
     uint32_t blocks;               // per tile
     bool ahead;                    // residuals come by TMA
+    TcWalk walk;                   // of the loads
+    uint32_t at_tile, at_block, load_slot;    // the next load's
 };
 
 template <int kCtas, int kBN>
-__device__ __forceinline__ void load_ahead(const TcArgs& a, OutWarp& o, uint32_t upto, uint32_t first, uint32_t step,
-                                           uint32_t width, uint32_t rank) {
-    for (; o.issued < upto; ++o.issued) {
-        const uint32_t t = first + o.issued / o.blocks * step;
-        if (t >= a.tiles) return;
-        const TcTile tile = tc_tile(a, t);
+__device__ __forceinline__ void load_ahead(const TcArgs& a, OutWarp& o, uint32_t upto, uint32_t step, uint32_t width,
+                                           uint32_t rank) {
+    for (; o.issued < upto && o.at_tile < a.tiles; ++o.issued) {
+        const TcTile tile = o.walk.at(a, o.at_tile);
         const uint32_t row = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0) + o.row_off;
-        const uint32_t col = tile.q * kBN + o.col_off + o.issued % o.blocks * width;
-        const uint32_t s = o.issued % o.slots;
+        const uint32_t col = tile.q * kBN + o.col_off + o.at_block * width;
+        const uint32_t s = o.load_slot;
+        if (++o.load_slot == o.slots) o.load_slot = 0;
+        if (++o.at_block == o.blocks) {
+            o.at_block = 0;
+            o.at_tile += step;
+        }
         // a block outside the output is all zeros: in range for a load
         mbar_expect(o.bar + 8 * s, kUnit);
         tma_load_2d(o.buf + s * kUnit, &a.map_res, col, row, o.bar + 8 * s);
@@ -623,8 +628,9 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                     for (int h = 0; h < kQRows / 64; ++h) tma_load<kCtas>(dst + h * 8192, mq, q0 + 64 * h, k, z, bar);
             };
             uint32_t s = 0, phase = 1;          // the first round of stages is free
+            TcWalk walk;
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
-                const TcTile tile = tc_tile(a, t);
+                const TcTile tile = walk.at(a, t);
                 const uint32_t p0 = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0);
                 const uint32_t q0 = tile.q * kBN + (kCtas == 2 ? rank * kQRows : 0);
                 for (uint32_t kb = kb0; kb < kb1; ++kb) {
@@ -756,16 +762,19 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
         o.buf = base + a.stages * stage_bytes + warp * a.slots * kUnit;
         o.bar = res_bars + warp * kTcMaxSlots * 8;
         o.issued = o.block = 0;
+        o.at_tile = first;
+        o.at_block = o.load_slot = 0;
         o.row_off = quad * 32;
         o.col_off = half * kHalf;
         o.blocks = kHalf / width;
         o.ahead = by_tma && a.e.res && !a.e.pre;
         const uint32_t stage_unit = o.buf;
-        if (o.ahead && lane == 0) load_ahead<kCtas, kBN>(a, o, o.slots, first, step, width, rank);
+        if (o.ahead && lane == 0) load_ahead<kCtas, kBN>(a, o, o.slots, step, width, rank);
         const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty, lead_small = lead_empty + 16;
         uint32_t ch = 0, slot = 0, slot_phase = 0;     // slot: of block o.block
+        TcWalk walk;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
-            const TcTile tile = tc_tile(a, t);
+            const TcTile tile = walk.at(a, t);
             const uint32_t prow = tile.p * 128 * kCtas + (kCtas == 2 ? rank * 128 : 0) + quad * 32;
             const uint32_t qrow = tile.q * kBN + half * kHalf;
             if constexpr (kDrain) {
@@ -840,14 +849,19 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         else
                             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        load_ahead<kCtas, kBN>(a, o, o.block + (o.slots == 2 ? 2 : o.slots - 1), first, step, width, rank);
+                        load_ahead<kCtas, kBN>(a, o, o.block + (o.slots == 2 ? 2 : o.slots - 1), step, width, rank);
                     }
                     if (a.e.bias)
                         for (uint32_t i = lane; i < width; i += 32)
                             st_shared1(bias_at + i * 4, col + i < a.cols ? elem(a.e.bias, col + i, a.e.bias_dtype) : 0.0f);
 #pragma unroll 1
                     for (int pre = a.e.pre != nullptr; pre >= 0; --pre) {
-                        // the block's buffer: its residual has come, or its last store has left
+                        // 32 columns at a time; the first on their way while the block's buffer
+                        // is waited for: its residual has come, or its last store has left
+                        const uint32_t from = mine + b * kBN + blk * width;
+                        float v[16], u[16];
+                        tmem_ld16(from, v);
+                        tmem_ld16(from + 16, u);
                         if (o.ahead)
                             ok = bar_wait(o.bar + 8 * slot, slot_phase, gone, ctas);
                         else if (lane == 0 && (o.slots == 1 || a.e.pre))
@@ -855,19 +869,19 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                         else if (lane == 0)
                             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         __syncwarp();
-                        float v[16], next[16] = {};
-                        tmem_ld16(mine + b * kBN + blk * width, v);
-                        tmem_wait16(v);
 #pragma unroll 1
-                        for (uint32_t in = 0; in < width; in += 16) {
-                            if (in + 16 < width)
-                                tmem_ld16(mine + b * kBN + blk * width + in + 16, next);
-                            else if (blk + 1 == o.blocks && !pre)
-                                release();
-                            finish_row(a, v, bias_at + in * 4, out, in * (bf16 ? 2 : 4) / 16, prow + lane, col + in, o.ahead, pre);
-                            tmem_wait16(next);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = next[i];
+                        for (uint32_t in = 0;;) {
+                            tmem_wait16(v);
+                            tmem_wait16(u);
+                            const bool last = in + 32 == width;
+                            if (last && blk + 1 == o.blocks && !pre) release();
+                            const uint32_t piece = in * (bf16 ? 2 : 4) / 16, row = prow + lane;
+                            finish_row(a, v, bias_at + in * 4, out, piece, row, col + in, o.ahead, pre);
+                            finish_row(a, u, bias_at + in * 4 + 64, out, piece + (bf16 ? 2 : 4), row, col + in + 16, o.ahead, pre);
+                            if (last) break;
+                            in += 32;
+                            tmem_ld16(from + in, v);
+                            tmem_ld16(from + in + 16, u);
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
@@ -876,7 +890,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                             if (o.ahead && o.slots == 1) {
                                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                                load_ahead<kCtas, kBN>(a, o, o.block + 2, first, step, width, rank);
+                                load_ahead<kCtas, kBN>(a, o, o.block + 2, step, width, rank);
                             }
                         }
                     }
@@ -930,7 +944,7 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
     if (kCtas == 1 && a.splits > 1) {
         // every CTA's part of the one tile is in place: this CTA finishes its share of the rows
         if (warp < kWarps) {
-            const TcTile tile = tc_tile(a, first);
+            const TcTile tile = TcWalk().at(a, first);
             constexpr uint32_t kPerQuad = kBN / kUnitCols, kItems = kSwap ? kUnitCols / 4 : 4;
 #pragma unroll 1
             for (uint32_t x = rank + a.splits * warp; x < 4 * kPerQuad * kItems; x += a.splits * kWarps) {
@@ -1068,7 +1082,6 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.tiles_p = (px + 128 * c.ctas - 1) / (128 * c.ctas);
     a.tiles_q = (qx + c.bn - 1) / c.bn;
     a.tiles = a.tiles_p * a.tiles_q;
-    a.group = 8;
     a.splits = c.ctas == 2 ? 1 : p.splits;
     if (a.splits > a.kblocks) a.splits = a.kblocks;
     // the pair kernel drains every 8 blocks: with 4 the round trip from commit to drained and back

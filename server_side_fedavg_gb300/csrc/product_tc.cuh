@@ -52,7 +52,7 @@ struct TcArgs {
     unsigned int* err;
     uint32_t rows, cols, k;                   // of the output and the sum
     uint32_t sub, kblocks;                    // blocks of 64 terms per stage (1 or 2); stages of a sum
-    uint32_t tiles, tiles_p, tiles_q, group;
+    uint32_t tiles, tiles_p, tiles_q;
     uint32_t splits, stages, chunk_kb, planes_p, planes_q;
     uint32_t slots;                           // 4 KB epilogue buffers per drain warp: 2..kTcMaxSlots
     bool p_kmajor, q_kmajor, vec, test_expire;
@@ -62,14 +62,23 @@ struct TcTile {
     uint32_t p, q;
 };
 
-// Tiles in bands of a.group tiles of P, down the band first: the CTAs at work at one time
-// share few rows of either operand, which stay in L2.
-__device__ __forceinline__ TcTile tc_tile(const TcArgs& a, uint32_t t) {
-    const uint32_t band = t / (a.group * a.tiles_q), p0 = band * a.group;
-    const uint32_t height = a.tiles_p - p0 < a.group ? a.tiles_p - p0 : a.group;
-    const uint32_t r = t - p0 * a.tiles_q;
-    return {p0 + r % height, r / height};
-}
+// Tiles in bands of kTcBand tiles of P, down the band first: the CTAs at work at one time share
+// few rows of either operand, which stay in L2.  A walker is asked for ascending tiles, and
+// keeps its band: divisions would cost each of its users some 200 cycles a tile.
+constexpr uint32_t kTcBand = 8;
+struct TcWalk {
+    uint32_t p0 = 0, start = 0;       // the band's first tile of P, and its first tile
+    __device__ __forceinline__ TcTile at(const TcArgs& a, uint32_t t) {
+        const uint32_t full = kTcBand * a.tiles_q;
+        while (t - start >= full) {
+            start += full;
+            p0 += kTcBand;
+        }
+        const uint32_t r = t - start, height = a.tiles_p - p0;
+        if (height >= kTcBand) return {p0 + r % kTcBand, r / kTcBand};
+        return {p0 + r % height, r / height};
+    }
+};
 
 cudaError_t prepare_product_tc(TcShape* shape);
 cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned int* err, bool test_expire,

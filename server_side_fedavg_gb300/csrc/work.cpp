@@ -237,8 +237,7 @@ fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, 
 
 // Tile configuration and split of the summed index: the least time by a model in
 // microseconds, fitted to sweeps of every configuration over 35 shapes on GB300.  A launch
-// takes 4, a tile 1 (256 columns: 2) beside its blocks of 64 terms, the exchange of a split
-// 1.5.  A block takes the larger of its latency and its MMA time, or its operand bytes at the
+// takes 4, a tile some 2 beside its blocks of 64 terms, the exchange of a split 1.5.  A block takes the larger of its latency and its MMA time, or its operand bytes at the
 // 112 GB/s that L2 gives each SM when all of them load.  The choice was within 15 % of the best
 // configuration in all but one of 35 shapes.
 void choose(fa::TcProduct* p, const fa::TcShape& shape) {
@@ -272,11 +271,11 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
         if (p->m <= 32) return;
     }
     // planes need TMEM and shared memory beside 256 columns
-    if (planes == 2) consider(fa::kTcPair256, m256 * n256, 2, 32, 0.30, 0.30, 2.0, 1);
-    consider(fa::kTcPair128, m256 * n128, 2, 24, 0.165, 0.16, 1.0, 1);
+    if (planes == 2) consider(fa::kTcPair256, m256 * n256, 2, 32, 0.30, 0.30, 2.3, 1);
+    consider(fa::kTcPair128, m256 * n128, 2, 24, 0.165, 0.16, 1.9, 1);
     for (uint32_t s = 1; s <= 8 && kb >= s; ++s) {
-        consider(fa::kTc128, m128 * n128, 1, 32, 0.185, 0.165, 1.0, s);
-        consider(fa::kTc64, m128 * n64, 1, 24, 0.16, 0.13, 1.0, s);
+        consider(fa::kTc128, m128 * n128, 1, 32, 0.185, 0.165, 1.9, s);
+        consider(fa::kTc64, m128 * n64, 1, 24, 0.16, 0.13, 1.7, s);
     }
 }
 
