@@ -82,8 +82,11 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
+// Arrive on a barrier of any CTA of the cluster.  What it hands over is TMEM, which the tcgen05
+// fences around it order; a release at cluster scope would wait for the thread's memory
+// operations besides (the drain forms' main stall).
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 constexpr uint32_t kSuspendNs = 1000000;   // a try may sleep this long before it answers no
