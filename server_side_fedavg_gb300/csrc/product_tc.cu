@@ -14,9 +14,9 @@
 // while one is drained.
 //
 // kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates: 4.4e-6 off over 4096
-// terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms (8 in the
-// 256-column form) into registers, which sum with rounding to nearest: 2.4e-7 (4.8e-7; every 2
-// blocks 1.6e-7, every 16 1e-6).  The products of planes other than the first two have an accumulator of their own,
+// terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms into
+// registers, which sum with rounding to nearest: 2.4e-7 (every 2 blocks 1.6e-7, every 8 4.8e-7,
+// for 2 % of the time).  The products of planes other than the first two have an accumulator of their own,
 // which is 2^-8 of the first and is read once a tile.
 //
 // kSwap: Q (columns) holds the tokens and P the weights -- for few tokens, where the 128 lanes
@@ -93,7 +93,7 @@ constexpr uint32_t kSuspendNs = 1000000;   // a try may sleep this long before i
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(done)
         : "r"(bar), "r"(parity), "r"(kSuspendNs)
@@ -101,8 +101,8 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return done;
 }
 
-// Wait for a phase, acquiring at cluster scope (the arrivals may come from another CTA).
-// False where the cluster has given up (`gone` is set) or the wait has lasted kMaxWaitClocks
+// Wait for a phase.  What the barriers guard is read by the tensor cores or from TMEM, which the
+// tcgen05 fences order, or came by TMA; no wider acquire is needed.  False where the cluster has given up (`gone` is set) or the wait has lasted kMaxWaitClocks
 // (some 20 s): it then sets the flag of every CTA of the cluster, so that every role leaves.
 constexpr long long kMaxWaitClocks = 40ll * 1000 * 1000 * 1000;
 __device__ __forceinline__ void give_up(uint32_t gone, uint32_t ctas) {
@@ -1087,9 +1087,7 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.tiles = a.tiles_p * a.tiles_q;
     a.splits = c.ctas == 2 ? 1 : p.splits;
     if (a.splits > a.kblocks) a.splits = a.kblocks;
-    // the pair kernel drains every 8 blocks: with 4 the round trip from commit to drained and back
-    // took longer than the products (1024 x 4096 x 32000: 217 us against 181)
-    a.chunk_kb = c.bn == 256 ? 8 : 4 / a.sub;
+    a.chunk_kb = 4 / a.sub;
     auto vec = [&](const void* q, uint64_t ld) { return !q || out_ready(q, ld, a.e.out_dtype); };
     a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
     const bool by_tma = a.vec && a.splits == 1 && !c.swap;

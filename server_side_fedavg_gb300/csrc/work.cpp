@@ -271,11 +271,11 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
         if (p->m <= 32) return;
     }
     // planes need TMEM and shared memory beside 256 columns
-    if (planes == 2) consider(fa::kTcPair256, m256 * n256, 2, 32, 0.30, 0.30, 2.3, 1);
-    consider(fa::kTcPair128, m256 * n128, 2, 24, 0.165, 0.16, 1.9, 1);
+    if (planes == 2) consider(fa::kTcPair256, m256 * n256, 2, 32, 0.30, 0.30, 1.8, 1);
+    consider(fa::kTcPair128, m256 * n128, 2, 24, 0.165, 0.16, 1.6, 1);
     for (uint32_t s = 1; s <= 8 && kb >= s; ++s) {
-        consider(fa::kTc128, m128 * n128, 1, 32, 0.185, 0.165, 1.9, s);
-        consider(fa::kTc64, m128 * n64, 1, 24, 0.16, 0.13, 1.7, s);
+        consider(fa::kTc128, m128 * n128, 1, 32, 0.185, 0.165, 1.6, s);
+        consider(fa::kTc64, m128 * n64, 1, 24, 0.16, 0.13, 1.5, s);
     }
 }
 
