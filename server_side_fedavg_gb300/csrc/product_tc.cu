@@ -469,30 +469,64 @@ __device__ __forceinline__ void finish_item(const TcArgs& a, uint32_t unit, uint
     write(e.out);
 }
 
-// The same eight rows where outputs are not 16-byte aligned: a lane per column, so that stores
-// (and residual loads) of a row are contiguous.
+// The same eight rows where outputs are not 16-byte aligned: a lane has kG adjacent columns (as
+// many as its stores can be aligned for, a.grain), and a store of the warp covers kG rows.
+template <int kG>
 __device__ __forceinline__ void finish_rows(const TcArgs& a, uint32_t unit, uint32_t part, uint32_t parts, uint32_t row0,
                                             uint32_t col0) {
-    const uint32_t lane = threadIdx.x % 32, c = col0 + lane, r0 = 8 * part;
-    if (row0 + r0 >= a.rows || c >= a.cols) return;
+    constexpr uint32_t kLanes = 32 / kG, kSteps = 8 / kG;
+    const uint32_t lane = threadIdx.x % 32, j0 = lane % kLanes * kG, c = col0 + j0, r0 = 8 * part + lane / kLanes;
+    if (c >= a.cols) return;
     const ProdEpilogue& e = a.e;
-    const uint32_t rows = min(8u, a.rows - row0 - r0);
-    float res[8] = {}, v[8] = {};
+    const bool whole = c + kG <= a.cols;
+    float bias[kG] = {}, res[8] = {}, v[8] = {};
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+        if (e.bias && c + g < a.cols) bias[g] = elem(e.bias, c + g, e.bias_dtype);
     if (e.res)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < rows) res[i] = elem(e.res, (row0 + r0 + i) * e.ldr + c, e.out_dtype);
-    const float bias = e.bias ? elem(e.bias, c, e.bias_dtype) : 0.0f;
+        for (int i = 0; i < kSteps; ++i) {
+            const uint64_t at = (row0 + r0 + i * kG) * e.ldr + c;
+            if (row0 + r0 + i * kG >= a.rows) break;
+            if (kG == 4 && whole && e.out_dtype) {
+                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.res) + at);
+                res[i * kG] = bf16_lo(q.x);
+                res[i * kG + 1 % kG] = bf16_hi(q.x);
+                res[i * kG + 2 % kG] = bf16_lo(q.y);
+                res[i * kG + 3 % kG] = bf16_hi(q.y);
+            } else {
+#pragma unroll
+                for (int g = 0; g < kG; ++g)
+                    if (c + g < a.cols) res[i * kG + g] = elem(e.res, at + g, e.out_dtype);
+            }
+        }
     for (uint32_t q = 0; q < parts; ++q)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += ld_part1(unit + unit_at(r0 + i, lane / 4) + lane % 4 * 4, q, parts);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t r = r0 + i / kG * kG, j = j0 + i % kG;
+            v[i] += ld_part1(unit + unit_at(r, j / 4) + j % 4 * 4, q, parts);
+        }
     const auto write = [&](void* p) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < rows) put(p, (row0 + r0 + i) * e.ldo + c, e.out_dtype, v[i]);
+        for (int i = 0; i < kSteps; ++i) {
+            if (row0 + r0 + i * kG >= a.rows) break;
+            const uint64_t at = (row0 + r0 + i * kG) * e.ldo + c;
+            const float* x = &v[i * kG];
+            if (kG == 4 && whole) {                      // bf16 (16-byte aligned fp32 is not for here)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = make_uint2(pack2(x[0], x[1 % kG]), pack2(x[2 % kG], x[3 % kG]));
+            } else if (kG == 2 && whole && e.out_dtype) {
+                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + at) = pack2(x[0], x[1 % kG]);
+            } else if (kG == 2 && whole) {
+                *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = make_float2(x[0], x[1 % kG]);
+            } else {
+#pragma unroll
+                for (int g = 0; g < kG; ++g)
+                    if (c + g < a.cols) put(p, at + g, e.out_dtype, x[g]);
+            }
+        }
     };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf(e.alpha, v[i], bias);
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(e.alpha, v[i], bias[i % kG]);
     if (e.pre) write(e.pre);
     activate(e.act, v);
     if (e.res)
@@ -505,8 +539,12 @@ __device__ __forceinline__ void finish_any(const TcArgs& a, uint32_t unit, uint3
                                            uint32_t col0) {
     if (a.vec)
         finish_item(a, unit, part, parts, row0, col0);
+    else if (a.grain == 4)
+        finish_rows<4>(a, unit, part, parts, row0, col0);
+    else if (a.grain == 2)
+        finish_rows<2>(a, unit, part, parts, row0, col0);
     else
-        finish_rows(a, unit, part, parts, row0, col0);
+        finish_rows<1>(a, unit, part, parts, row0, col0);
 }
 
 // kSwap: lane = one output column (P row); four output rows, columns 4 `part` of the unit.
@@ -1090,6 +1128,15 @@ cudaError_t launch_product_tc(const TcProduct& p, const TcShape& shape, unsigned
     a.chunk_kb = 4 / a.sub;
     auto vec = [&](const void* q, uint64_t ld) { return !q || out_ready(q, ld, a.e.out_dtype); };
     a.vec = vec(a.e.out, a.e.ldo) && vec(a.e.pre, a.e.ldo) && vec(a.e.res, a.e.ldr);
+    // elements that every output row's stores can be aligned for, where not 16 bytes
+    a.grain = a.e.out_dtype ? 4 : 2;
+    const auto aligned = [&](const void* q, uint64_t ld, uint32_t n) {
+        const uint64_t size = a.e.out_dtype ? 2 : 4;
+        return !q || (reinterpret_cast<uintptr_t>(q) % (n * size) == 0 && ld % n == 0);
+    };
+    while (a.grain > 1 && !(aligned(a.e.out, a.e.ldo, a.grain) && aligned(a.e.pre, a.e.ldo, a.grain) &&
+                            aligned(a.e.res, a.e.ldr, a.grain)))
+        a.grain /= 2;
     const bool by_tma = a.vec && a.splits == 1 && !c.swap;
     if (by_tma && !(encode_out(&a.map_out, a.e.out, a.e.ldo, a) && (!a.e.pre || encode_out(&a.map_pre, a.e.pre, a.e.ldo, a)) &&
                     (!a.e.res || encode_out(&a.map_res, a.e.res, a.e.ldr, a))))

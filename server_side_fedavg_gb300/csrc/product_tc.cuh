@@ -54,6 +54,7 @@ struct TcArgs {
     uint32_t sub, kblocks;                    // blocks of 64 terms per stage (1 or 2); stages of a sum
     uint32_t tiles, tiles_p, tiles_q;
     uint32_t splits, stages, chunk_kb, planes_p, planes_q;
+    uint32_t grain;                           // output elements a store may cover: 1, 2, 4 (without vec)
     uint32_t slots;                           // 4 KB epilogue buffers per drain warp: 2..kTcMaxSlots
     bool p_kmajor, q_kmajor, vec, test_expire;
 };

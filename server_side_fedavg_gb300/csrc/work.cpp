@@ -285,6 +285,9 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
 // rows 23.5 us (tensor cores with their pass 46), 32 rows 46 (48), 64 rows 90 (50).
 bool use_thin(const fa::ProdArgs& q) {
     if (!q.a.kmajor || q.a.dtype != q.b.dtype) return false;
+    // with b stored [k, n] a warp walks k / 64 rows of it, eight loads in flight, for every eight
+    // rows of a: some 60 us at 10 rows and k = 21360, where the tensor cores and their pass take 30
+    if (!q.b.kmajor && static_cast<uint64_t>(q.k) * ((q.m + 7) / 8) > 11000) return false;
     return q.b.dtype == 0 ? q.m <= (q.b.kmajor ? 24 : 16) : q.m <= 8 && !tma_ready(q.b);
 }
 
@@ -401,14 +404,16 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     const uint32_t blocks = (m + fa::kColRows - 1) / fa::kColRows;
     const int it = code_of(p.dtype_in), dt = code_of(p.dtype_dout), gt = code_of(p.dtype_grad);
     // dZ is dout itself, or is written to the workspace: in fp32 for the tiny kernel and for few
-    // fp32 rows (see use_thin), else as bf16 planes
+    // fp32 rows, else as bf16 planes.  few: the gradient of a is for the thin kernels (see
+    // use_thin), which take dZ as it lies
     const bool tiny = use_tiny(p.m, p.n, p.k);
-    const bool few = !tiny && it == 0 && p.m <= 16;
+    const bool few = !tiny && (it == 0 ? p.m <= 16
+                                       : gt == 1 && p.m <= 8 && want_a && !tma_ready({p.b, p.ldb, it, !tb}));
     const bool products = want_a || want_b;
     const fa::ProdOperand d_in{p.dout, p.ldd, dt, true};
     const bool write_dz = products && m && n && (act || (!tiny && !few && !tma_ready(d_in)));
-    const int planes = tiny || few ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
-    const uint64_t ldz = tiny || few ? p.n : (p.n + 7) / 8 * 8;
+    const int planes = tiny || (few && it == 0) ? 0 : (gt == 0 && (act || dt == 0)) ? 3 : 1;
+    const uint64_t ldz = planes == 0 ? p.n : (p.n + 7) / 8 * 8;
     const bool cap = capturing(s);
     // two passes over the same steps: the first adds up the workspace
     Carve c{nullptr};
