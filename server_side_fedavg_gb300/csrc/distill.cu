@@ -7,8 +7,14 @@
 // a slice) loads its row once with every load in flight at the same time, sums its exponentials
 // -- each warp over a reference of its own, pairs (reference, sum) merged over the CTA and, through
 // distributed shared memory, the cluster -- and writes the gradient from there.
-// The row is read once and written once: bound by HBM.  Longer rows are streamed from memory
-// (and L2) twice or three times.
+// The row is read once and written once: bound by HBM, with the exponentials (two per element of
+// a gradient) close behind.  Longer rows are streamed from memory (and L2) twice or three times.
+// Of rows whose statistic is given the slices are independent, and of any number.
+//
+// Measured, back to back (the measured copy rate is 6.80 TB/s): gradient and loss of 4096 rows of
+// 32000 bf16 logits, 8 lists of 32, 98 us, 5.4 TB/s (instruction issue 56 % busy, HBM at 4.8
+// TB/s, the rest of the traffic in L2); gradient of 700 x 131075 bf16 from a kept statistic
+// 77 us, 4.8 TB/s; loss of 1531 x 32003 fp32 37.4 us, 5.3 TB/s; one row of 32000 5.2 us.
 //
 // An exponential is 2^(z c - k) with c = log2(e) / T and k = reference c rounded: one FMA and one
 // ex2.  k's rounding is the same in every term and in the statistic that is formed with the
@@ -20,6 +26,8 @@
 // (n_j / total) p_jc): several clients name the same entry, and integer adds of fixed-point
 // units give the same sum in any order.  The row is written without the shares
 // first, then the table's entries are written over it.
+#include <algorithm>
+
 #include "distill.cuh"
 #include "device.cuh"
 
@@ -365,6 +373,8 @@ __device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, bool s
 
 // ----------------------------------------------------------------- rows held on chip
 constexpr uint32_t kMaxSlice = 66 * 1024;   // bytes of a row that a CTA holds: three CTAs per SM
+constexpr uint32_t kSmallSlice = 16 * 1024; // held by 128 threads, larger ones by 256
+constexpr uint32_t kSharedBytes = 227 * 1024, kSliceCost = 16 * 1024;
 
 __device__ __forceinline__ uint32_t rank_in_cluster() {
     uint32_t r;
@@ -372,16 +382,50 @@ __device__ __forceinline__ uint32_t rank_in_cluster() {
     return r;
 }
 
-__device__ __forceinline__ void sync_cluster() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// A pair from every CTA of a cluster to every CTA, in shared memory: two sets in turn, since a
+// peer that has this CTA's pair may go on to the next exchange while this one still waits for
+// others'.  The pairs are sent by st.async, which counts their bytes at the receiver's barrier:
+// a cluster barrier's release would wait for the row's stores and the next row's loads as well
+// (the loss of 1531 rows of 32003 fp32 logits: 42.9 us, against 39.4 this way).
+constexpr uint32_t kMaxCluster = 8;
+constexpr long long kMaxWaitClocks = 40ll * 1000 * 1000 * 1000;      // some 20 s
+struct Exchange {
+    unsigned long long bar[2];
+    float2 pair[2][kMaxCluster];
+    uint32_t gone;                         // a wait has run out: the CTA leaves
+};
+
+__device__ __forceinline__ void open_exchange(Exchange& x) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\nmbarrier.init.shared::cta.b64 [%1], 1;\n"
+                 "fence.mbarrier_init.release.cluster;" ::"r"(smem_addr(&x.bar[0])), "r"(smem_addr(&x.bar[1])) : "memory");
+    x.gone = 0;
 }
 
-__device__ __forceinline__ float2 peer2(const float2* p, uint32_t rank) {
-    uint32_t addr;
-    float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+// By one warp.  False: the peers' pairs have not come.
+__device__ __forceinline__ bool swap_pairs(Exchange& x, uint32_t turn, uint32_t ctas, uint32_t rank, float2 v, bool expire) {
+    const uint32_t lane = threadIdx.x % 32, bar = smem_addr(&x.bar[turn % 2]), to = smem_addr(&x.pair[turn % 2][rank]);
+    if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 8) : "memory");
+    if (lane < ctas)
+        asm volatile(
+            "{\n .reg .b32 to, bar;\n mapa.shared::cluster.u32 to, %0, %2;\n mapa.shared::cluster.u32 bar, %1, %2;\n"
+            " st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [to], {%3, %4}, [bar];\n}" ::"r"(to),
+            "r"(bar), "r"(lane), "f"(v.x), "f"(v.y)
+            : "memory");
+    const long long t0 = clock64();
+    for (uint32_t done = 0; !done;) {
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000000;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(bar), "r"(turn / 2 % 2)
+            : "memory");
+        if (!done && clock64() - t0 > kMaxWaitClocks) return false;
+    }
+    return !expire;
 }
 
 // The elements of 16 loaded bytes.
@@ -494,20 +538,30 @@ struct Place {
     __device__ __forceinline__ uint32_t edge_at(uint32_t t) const { return t < head ? t : head + nvec * kV + t - kV; }
 };
 
-// Rows (or a cluster's slices of them) held in shared memory.  Each thread copies its own
-// 16-byte vectors there (cp.async: no registers held, no barrier needed) and goes over them
-// twice; as it leaves a vector for the last time it asks for the next row's in its place, and
-// the next row's lists and weight are loaded as early, so that HBM is read while a row is being
-// worked on.  Elements beside the vectors are held one per thread in `edge`.
-template <typename T, bool kGrad, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(const __grid_constant__ DistillArgs a) {
+// Rows (or slices of them: kJoint, a cluster's, kSlices, independent ones) held in shared memory.
+// Three or four CTAs of 256 threads per SM, whose slices in flight hide HBM's latency.  Slices of
+// a cluster are larger, three per SM, and take the registers for it (1531 x 32003 fp32: 37.3 us,
+// with a bound for four 39.0); whole rows fit four (6000 rows of 20000 bf16, with the gradient:
+// 98 us, with three 107).  Each thread copies its own 16-byte vectors there (cp.async: no registers held, no barrier needed) and
+// goes over them twice; as it leaves a vector for the last time it asks for the next row's in
+// its place, and the next row's lists and weight are loaded as early, so that HBM is read while
+// a row is being worked on.  Elements beside the vectors are held one per thread in `edge`.
+enum RowForm { kWhole, kSlices, kJoint };
+template <typename T, bool kGrad, int kThreads, RowForm kForm>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : kForm == kWhole ? 4 : 3) distill_row_kernel(const __grid_constant__ DistillArgs a) {
     constexpr uint32_t kV = 16 / sizeof(T), kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint8_t dyn[];               // the slice's vectors, the table
     __shared__ float tmp[kWarps], tmp2[kWarps];
-    __shared__ float2 pairs[2];
+    __shared__ Exchange exchange;
     __shared__ __align__(16) Lists lists;
     __shared__ uint32_t taken;
-    const uint32_t ctas = a.cluster, rank = ctas > 1 ? rank_in_cluster() : 0;
+    const uint32_t ctas = kForm == kWhole ? 1 : a.parts;
+    const uint32_t rank = kForm == kJoint ? rank_in_cluster() : kForm == kSlices ? blockIdx.x % ctas : 0;
+    if constexpr (kForm == kJoint) {
+        if (threadIdx.x == 0) open_exchange(exchange);
+        __syncwarp();
+        cluster_arrive();
+    }
     const uint32_t t = threadIdx.x, step = gridDim.x / ctas;
     const uint32_t lo = rank * a.slice, hi = min(lo + a.slice, a.vocab), n = hi > lo ? hi - lo : 0;
     const bool brief = a.short_lists && a.nclients <= kWarps, has_list = brief && t / 32 < a.nclients;
@@ -534,7 +588,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
     }
     const float c = a.inv_t * kLog2e, most = kFastMost / c;      // of a maximum, for the fast form
 
-    uint32_t turn = 0;                     // rows with an exchange so far
+    uint32_t turn = 0;                     // exchanges so far
+    const float2* pairs = nullptr;         // the last one's
+    const auto give = [&](float x, float y) {          // the same in every thread; false: the CTA leaves
+        if (t < 32 && !swap_pairs(exchange, turn, ctas, rank, make_float2(x, y), a.test_expire)) {
+            exchange.gone = 1;
+            atomicOr(a.err, kErrWaitTimeout);
+        }
+        pairs = exchange.pair[turn++ % 2];
+        __syncthreads();
+        return exchange.gone == 0;
+    };
+    if (kForm == kJoint) cluster_wait();           // the peers' barriers are set up
     while (row < a.rows) {
         const uint32_t next = row + step;
         const float w_next = weight_of(next);
@@ -591,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
                 __syncthreads();
                 // in place, the peers may write their slices only when rank 0 has taken the
                 // loss's logits (below, the exchange of statistics sees to that)
-                if (ctas > 1 && a.loss && a.grad == a.logits) sync_cluster();
+                if (kForm == kJoint && !give(0.0f, 0.0f)) break;
             } else {
                 // One pass: the sum over a reference, the largest of what the warp has at two
                 // places of the row, in place of the maximum.  Terms over it are no harm up to
@@ -630,31 +695,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
                 m = tmp[t % kWarps];
                 s = tmp2[t % kWarps];
                 merge_lanes<kWarps>(m, s, c);
-                if (ctas > 1) {
-                    // two places in turn: a peer may still read the last row's
-                    float2* mine = &pairs[turn++ % 2];
-                    if (t == 0) *mine = make_float2(m, s);
-                    sync_cluster();
-                    const float2 first = peer2(mine, 0);
-                    m = first.x;
-                    s = first.y;
-                    for (uint32_t r = 1; r < ctas; ++r) {
-                        const float2 v = peer2(mine, r);
-                        merge(m, s, v.x, v.y, c);
-                    }
+                if constexpr (kForm == kJoint) {
+                    if (!give(m, s)) break;
+                    m = pairs[0].x;
+                    s = pairs[0].y;
+                    for (uint32_t r = 1; r < ctas; ++r) merge(m, s, pairs[r].x, pairs[r].y, c);
                 }
                 if (!(fabsf(m) < most && s < kSumMost)) {
                     // the same for every thread of the cluster: the plain form from memory,
                     // maximum first
-                    float2* mine = &pairs[(turn + 1) % 2];       // the exchange's
                     m = edge;
                     for (uint32_t v = t; v < nvec; v += kThreads) m = max_of<T>(m, ld_plain_v4(mem + v));
                     m = block_reduce<kThreads, true>(m, tmp);
-                    if (ctas > 1) {
-                        sync_cluster();
-                        if (t == 0) mine->x = m;
-                        sync_cluster();
-                        for (uint32_t r = 0; r < ctas; ++r) m = fmaxf(m, peer2(mine, r).x);
+                    if constexpr (kForm == kJoint) {
+                        if (!give(m, 0.0f)) break;
+                        for (uint32_t r = 0; r < ctas; ++r) m = fmaxf(m, pairs[r].x);
                     }
                     e = {0.0f, m, 1.0f, c, false};
                     s = has_edge ? e.slow(edge) : 0.0f;
@@ -665,12 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
                         for (uint32_t j = 0; j < kV; ++j) s += e.slow(x[j]);
                     }
                     s = block_reduce<kThreads, false>(s, tmp);
-                    if (ctas > 1) {
-                        sync_cluster();
-                        if (t == 0) mine->x = s;
-                        sync_cluster();
+                    if constexpr (kForm == kJoint) {
+                        if (!give(s, 0.0f)) break;
                         s = 0.0f;
-                        for (uint32_t r = 0; r < ctas; ++r) s += peer2(mine, r).x;
+                        for (uint32_t r = 0; r < ctas; ++r) s += pairs[r].x;
                     }
                 } else {
                     e.k = __fmul_rn(m, c);
@@ -746,7 +799,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_row_kernel(
         w = w_next;
         row = next;
     }
-    if (ctas > 1) sync_cluster();          // a peer may still read this CTA's pair
+    if constexpr (kForm == kJoint) {
+        asm volatile("cp.async.wait_all;" ::: "memory");     // a wait has run out: loads of the next row
+        // a peer may still send to this CTA
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // ----------------------------------------------------------------- rows streamed
@@ -810,8 +868,14 @@ __global__ void __launch_bounds__(kDThreads) distill_stream_kernel(const __grid_
 }
 
 using DistillKernel = void (*)(DistillArgs);
+// A kernel for a row's form and a slice's size (a cluster's slices are of 33 KB and more).
 template <typename T, bool kGrad>
-constexpr DistillKernel kRowKernels[2] = {distill_row_kernel<T, kGrad, 128>, distill_row_kernel<T, kGrad, 256>};
+DistillKernel row_kernel(RowForm form, bool small) {
+    if (form == kJoint) return distill_row_kernel<T, kGrad, 256, kJoint>;
+    if constexpr (kGrad)
+        if (form == kSlices) return small ? distill_row_kernel<T, true, 128, kSlices> : distill_row_kernel<T, true, 256, kSlices>;
+    return small ? distill_row_kernel<T, kGrad, 128, kWhole> : distill_row_kernel<T, kGrad, 256, kWhole>;
+}
 
 }  // namespace
 
@@ -822,12 +886,13 @@ cudaError_t prepare_distill() {
             e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kMaxSlice + kSlotBytes * 2 * kMaxDistillTopk);
     };
-    for (int i = 0; i < 2; ++i) {
-        allow(kRowKernels<uint16_t, false>[i]);
-        allow(kRowKernels<uint16_t, true>[i]);
-        allow(kRowKernels<float, false>[i]);
-        allow(kRowKernels<float, true>[i]);
-    }
+    for (RowForm form : {kWhole, kSlices, kJoint})
+        for (bool small : {false, true}) {
+            allow(row_kernel<uint16_t, false>(form, small));
+            allow(row_kernel<uint16_t, true>(form, small));
+            allow(row_kernel<float, false>(form, small));
+            allow(row_kernel<float, true>(form, small));
+        }
     allow(distill_stream_kernel<uint16_t, true>);
     allow(distill_stream_kernel<float, true>);
     return e;
@@ -852,33 +917,60 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     DistillKernel kern;
+    // slices of 16 elements' multiples, so that they all have the row's alignment
+    const auto slice_of = [&](uint64_t n) { return static_cast<uint32_t>((a.vocab + n * 16 - 1) / (n * 16) * 16); };
     bool held = true;                      // rows on chip
-    uint32_t cluster = 1;
-    while (cluster < 8 && bytes > static_cast<uint64_t>(cluster) * kMaxSlice) cluster *= 2;
-    if (bytes > static_cast<uint64_t>(cluster) * kMaxSlice || static_cast<uint64_t>(a.rows) * cluster >= (1ull << 31)) {
+    uint64_t parts = 1;
+    // With the statistic given, a row's slices need nothing of one another -- but for the loss at
+    // the logits that the gradient replaces.  Their number is then free: the one with the least
+    // work on the SM that has the most, a slice's lists and barriers costing as much as some
+    // kSliceCost bytes.  Against the least power of two: 700 rows of 131075 bf16 logits 77.3 us
+    // and 81.2, 1000 of 50000 42.9 and 47.1, 8 of 131075 8.2 and 10.3 (700 of 131072 in fp32
+    // 134.0 and 131.8).
+    const bool apart = grad && a.lse_in && !(a.loss && a.grad == a.logits);
+    if (apart) {
+        const uint64_t least = (bytes + kMaxSlice - 1) / kMaxSlice, top = std::max<uint64_t>(16, std::min(4 * least, least + 64));
+        uint64_t best = ~0ull;
+        for (uint64_t n = least; n <= top && n * 1024 <= bytes + 1024 * least; ++n) {
+            const uint64_t held_bytes = static_cast<uint64_t>(slice_of(n)) * size;
+            const uint64_t fit = kSharedBytes / (held_bytes + table + 2048), most = held_bytes > kSmallSlice ? 3 : 8;
+            const uint64_t per_sm = std::min({fit, most, (a.rows * n + a.sms - 1) / a.sms});
+            const uint64_t at_once = std::max<uint64_t>(1, a.sms * per_sm / n);      // rows
+            const uint64_t turns = (a.rows + at_once - 1) / at_once;
+            if (turns * per_sm * (held_bytes + kSliceCost) < best) {
+                best = turns * per_sm * (held_bytes + kSliceCost);
+                parts = n;
+            }
+        }
+    } else {
+        while (parts < kMaxCluster && bytes > parts * kMaxSlice) parts *= 2;
+    }
+    a.joint = !apart && parts > 1;
+    if (bytes > parts * kMaxSlice || a.rows * parts >= (1ull << 31)) {
         kern = a.dtype ? (grad ? distill_stream_kernel<uint16_t, true> : distill_stream_kernel<uint16_t, false>)
                        : (grad ? distill_stream_kernel<float, true> : distill_stream_kernel<float, false>);
         held = false;
-        a.cluster = 1;
+        a.parts = 1;
         cfg.blockDim = dim3(kDThreads);
         cfg.dynamicSmemBytes = table;
     } else {
-        // slices of 16 elements' multiples, so that they all have the row's alignment
-        a.cluster = cluster;
-        a.slice = static_cast<uint32_t>((a.vocab + cluster * 16ull - 1) / (cluster * 16ull) * 16);
+        a.parts = static_cast<uint32_t>(parts);
+        a.slice = slice_of(parts);
         a.table_at = (a.slice < a.vocab ? a.slice : a.vocab) * size / 16 * 16;
-        const int k = a.table_at > 16384;
-        cfg.blockDim = dim3(k ? 256 : 128);
+        const bool small = !a.joint && a.table_at <= kSmallSlice;
+        const RowForm form = a.joint ? kJoint : parts > 1 ? kSlices : kWhole;
+        cfg.blockDim = dim3(small ? 128 : 256);
         cfg.dynamicSmemBytes = a.table_at + table;
-        kern = a.dtype ? (grad ? kRowKernels<uint16_t, true>[k] : kRowKernels<uint16_t, false>[k])
-                       : (grad ? kRowKernels<float, true>[k] : kRowKernels<float, false>[k]);
+        kern = a.dtype ? (grad ? row_kernel<uint16_t, true>(form, small) : row_kernel<uint16_t, false>(form, small))
+                       : (grad ? row_kernel<float, true>(form, small) : row_kernel<float, false>(form, small));
     }
-    at[0].val.clusterDim.x = a.cluster;
-    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    cfg.gridDim = dim3(a.rows * a.cluster);
+    const uint32_t cluster = a.joint ? a.parts : 1;
+    at[0].val.clusterDim.x = cluster;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.gridDim = dim3(a.rows * a.parts);
     if (held) {
-        // as many clusters as run at one time; the same kernel and sizes as in the last call of
-        // this thread are not asked for again
+        // as many rows as run at one time; the same kernel and sizes as in the last call of this
+        // thread are not asked for again
         static thread_local struct {
             DistillKernel kern = nullptr;
             uint32_t cluster = 0;
@@ -888,15 +980,16 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess &&
-            !(last.kern == kern && last.cluster == a.cluster && last.smem == cfg.dynamicSmemBytes && last.device == dev)) {
+            !(last.kern == kern && last.cluster == cluster && last.smem == cfg.dynamicSmemBytes && last.device == dev)) {
             int n = 0;
             cudaLaunchConfig_t ask = cfg;
             ask.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kern), &ask);
-            last = {kern, a.cluster, cfg.dynamicSmemBytes, dev, n};
+            last = {kern, cluster, cfg.dynamicSmemBytes, dev, n};
         }
         if (e != cudaSuccess) return e;
-        if (a.rows > static_cast<uint32_t>(last.clusters) && last.clusters > 0) cfg.gridDim = dim3(last.clusters * a.cluster);
+        const uint32_t rows = static_cast<uint32_t>(last.clusters) * cluster / a.parts;
+        if (rows > 0 && a.rows > rows) cfg.gridDim = dim3(rows * a.parts);
     }
     return cudaLaunchKernelEx(&cfg, kern, a);
 }

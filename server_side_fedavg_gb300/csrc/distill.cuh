@@ -33,16 +33,20 @@ struct DistillArgs {
     uint32_t nclients;
     uint32_t slots;            // hash slots: a power of two >= 2 * (sum of topk)
     uint32_t hash_shift;
-    uint32_t cluster, slice;   // CTAs per row and the elements of each
+    uint32_t parts, slice;     // CTAs per row and the elements of each
+    uint32_t sms;              // of the device
     uint32_t table_at;         // bytes of a slice's vectors in shared memory: the table follows
     float temperature, inv_t;
     float total;               // sum of all n_j
     int dtype, value_dtype;
     bool short_lists;          // every list has at most 64 places
+    bool joint;                // a row's CTAs are a cluster and exchange their statistics
+    bool test_expire;          // the first exchange's wait counts as run out
     DistillClient client[kMaxDistillClients];
 };
 
-// Fills slots, cluster, slice, table_at and short_lists; the caller fills the rest.
+// Fills slots, hash_shift, parts, slice, table_at, short_lists and joint; the caller fills the
+// rest.
 cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream);
 cudaError_t prepare_distill();   // shared-memory limits, for the current device
 

@@ -534,6 +534,8 @@ fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStre
     a.lse_in = grad ? p.lse : nullptr;
     a.lse_out = grad ? nullptr : p.lse;
     a.err = w->err_dev;
+    a.sms = static_cast<uint32_t>(w->tc.sms);
+    a.test_expire = (w->flags & FA_TEST_WAIT_EXPIRES) != 0;
     a.ld = p.ld;
     a.ldg = p.ldg;
     a.rows = static_cast<uint32_t>(p.rows);

@@ -346,3 +346,60 @@ def test_refusals(work):
     fa.fa_distill_grad(work, **{**ok, "rows": 0})
     fa.fa_distill_grad(work, **ok)
     fa.fa_work_sync(work)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype,topk", [
+    (1, 5000, "f32", 16), (2, 33000, "bf16", 16), (9, 131075, "bf16", 64), (300, 131075, "bf16", 8), (40, 200003, "f32", 100),
+    (3, 800001, "bf16", 16), (700, 40000, "f32", 4), (2000, 16500, "bf16", 3)])
+def test_slices_of_rows_with_a_given_statistic(work, rows, vocab, dtype, topk):
+    """With the statistic given a row may be divided in any number of slices: few rows, many
+    rows, rows longer than a cluster holds, with and without the loss, in place or not."""
+    z, index, value, weight, _ = make(rows, vocab, 3, topk, dtype, seed=5)
+    rw = torch.ones(rows, device="cuda")
+    rw[::7] = 0.0
+    rw[0] = 0.5
+    for inplace, fused_loss in ((False, True), (False, False), (True, False), (True, True)):
+        check(work, z, index, value, weight, rw, 1.5, dtype, saved=True, inplace=inplace, fused_loss=fused_loss)
+
+
+@pytest.mark.parametrize("dtype,vocab", [("f32", 20011), ("bf16", 70001), ("f32", 130000)])
+def test_many_rows_over_clusters_take_turns(work, dtype, vocab):
+    """More rows than run at one time, with masked rows and rows that need the plain form (and
+    its further exchanges) between ordinary ones."""
+    rows = 600
+    z, index, value, weight, _ = make(rows, vocab, 2, 8, dtype, seed=6)
+    z[3::5, :] += 3.0e6
+    z[4::11, vocab // 3:] = -INF
+    z[5::13, : vocab - 40] = torch.finfo(TORCH[dtype]).min
+    rw = torch.ones(rows, device="cuda")
+    rw[::3] = 0.0            # below: A <= 14 at these logits, 2^-20 (1 + A / 4) < 2^-17
+    lists = fa.distill_lists(index, value, [8, 8], weight, "f32")
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    grad = torch.empty_like(z)
+    fa.fa_distill_loss(work, rows, vocab, z, vocab, dtype, lists, 2.0, rw, loss, lse)
+    fa.fa_distill_grad(work, rows, vocab, z, vocab, dtype, lists, 2.0, rw, None, None, grad, vocab)
+    fa.fa_work_sync(work)
+    want = torch.where(rw > 0, torch.logsumexp(z.double() / 2.0, 1), 0.0)
+    assert ((lse.double() - want).abs() <= 2.0 ** -20 + 2.0 ** -22 * want.abs()).all()
+    # the gradient beside the lists' entries
+    q = torch.softmax(z.double() / 2.0, 1) * rw[:, None].double() * 2.0
+    d = (grad.double() - q)
+    d.scatter_(1, index[0].long(), 0.0)
+    d.scatter_(1, index[1].long(), 0.0)
+    tol = q * ((2.0 ** -7.99 if dtype == "bf16" else 0.0) + 2.0 ** -17 + 2.0 ** -22 * want.abs()[:, None]) + 1e-30
+    assert (d.abs() <= tol).all()
+
+
+def test_an_expired_exchange_is_reported_and_ends():
+    z, index, value, weight, _ = make(50, 70001, 2, 8, "f32", seed=7)
+    lists = fa.distill_lists(index, value, [8, 8], weight, "f32")
+    loss, lse = torch.empty(50, device="cuda"), torch.empty(50, device="cuda")
+    bad = fa.fa_work_open(flags=fa.FA_TEST_WAIT_EXPIRES)
+    try:
+        fa.fa_distill_loss(bad, 50, 70001, z, 70001, "f32", lists, 1.0, None, loss, lse)
+        with pytest.raises(fa.FedAvgError) as e:
+            fa.fa_work_sync(bad)
+        assert e.value.status == fa.FA_ERR_INTERNAL and "device-side wait" in e.value.detail
+        fa.fa_work_sync(bad)
+    finally:
+        fa.fa_work_close(bad)
