@@ -16,8 +16,8 @@
 // kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates: 4.4e-6 off over 4096
 // terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms into
 // registers, which sum with rounding to nearest: 2.4e-7 (every 2 blocks 1.6e-7, every 8 4.8e-7,
-// for 2 % of the time).  The products of planes other than the first two have an accumulator of their own,
-// which is 2^-8 of the first and is read once a tile.
+// for 2 % of the time).  The products of planes other than the first two have an accumulator of
+// their own, which is 2^-8 of the first and is read once a tile.
 //
 // kSwap: Q (columns) holds the tokens and P the weights -- for few tokens, where the 128 lanes
 // are better filled with weights.  The output is then written column by column.
@@ -25,6 +25,18 @@
 // splits > 1 (kCtas == 1): a cluster of `splits` CTAs divides the summed index; each puts its
 // part into its own shared memory, and each finishes a share of the tile, summing the parts
 // in rank order over distributed shared memory.
+//
+// What bounds it: the MMAs (measured peak 1922 TFLOP/s) and, before those, the operands' way
+// from L2 -- a 256 x 256 tile reads 64 KB per 64 terms, 12 TB/s over all SMs -- and the epilogue
+// of tiles with short sums.  Measured, back to back:
+//   4096 x 4864 x 16384 bf16                    361 us  1809 TFLOP/s  (94 %)
+//   4096 x 11008 x 4096 bf16, silu and pre      231 us  1600 TFLOP/s  (83 %; tensor pipe 73 % active)
+//   1024 x 4096 x 32000 bf16 to fp32            187 us  1435 TFLOP/s  (75 %; 128 CTAs have a tile)
+//   32000 x 4096 x 1024 bf16 to fp32            218 us  1231 TFLOP/s  (64 %; a 256 x 256 fp32 tile
+//                                               written every 16 blocks, HBM writes 0.52 GB)
+//   2056 x 1024 x 4096 bf16, bias, residual     18.8 us  920 TFLOP/s  (48 %: one wave, 4 us of launch)
+//   1 x 32000 x 4096 bf16                       41 us   6.4 TB/s of weights (94 % of measured)
+//   777 x 4096 x 1024 fp32, bias, gelu          50 us with the passes, 778 TFLOP/s of bf16 products
 #include "product_tc.cuh"
 #include "product_device.cuh"
 
@@ -102,8 +114,9 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 
 // Wait for a phase.  What the barriers guard is read by the tensor cores or from TMEM, which the
-// tcgen05 fences order, or came by TMA; no wider acquire is needed.  False where the cluster has given up (`gone` is set) or the wait has lasted kMaxWaitClocks
-// (some 20 s): it then sets the flag of every CTA of the cluster, so that every role leaves.
+// tcgen05 fences order, or came by TMA; no wider acquire is needed.  False where the cluster has
+// given up (`gone` is set) or the wait has lasted kMaxWaitClocks (some 20 s): it then sets the
+// flag of every CTA of the cluster, so that every role leaves.
 constexpr long long kMaxWaitClocks = 40ll * 1000 * 1000 * 1000;
 __device__ __forceinline__ void give_up(uint32_t gone, uint32_t ctas) {
     for (uint32_t r = 0; r < ctas; ++r)

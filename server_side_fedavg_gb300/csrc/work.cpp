@@ -212,8 +212,13 @@ struct Carve {
     }
 };
 
-// Too little work to fill a tensor-core tile: a thread or warp per output.
-bool use_tiny(uint64_t m, uint64_t n, uint64_t k) { return k == 0 || (m * n * k <= (1ull << 16) && k <= 1024); }
+// Too little work to fill a tensor-core tile: a thread or warp per output, where no sum is longer
+// than `most`.  In a CUDA graph 40 x 40 x 40 takes 1.9 us so, 4.7 (bf16) and 9.2 (fp32) on the
+// tensor cores; 256 x 256 x 8, the limit of the work, 4.3 and 4.4; 4 x 10 x 256 bf16 2.5 and
+// 3.1, but 8 x 8 x 1000 bf16 6.9 and 4.0, fp32 6.7 and 8.2.
+bool use_tiny(uint64_t m, uint64_t n, uint64_t k, uint64_t longest, uint64_t most) {
+    return k == 0 || (m * n * k <= (1ull << 16) && longest <= most);
+}
 
 bool tma_ready(const fa::ProdOperand& o) {
     return o.dtype == 1 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 && o.ld < (1ull << 36);
@@ -237,9 +242,10 @@ fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, 
 
 // Tile configuration and split of the summed index: the least time by a model in
 // microseconds, fitted to sweeps of every configuration over 35 shapes on GB300.  A launch
-// takes 4, a tile some 2 beside its blocks of 64 terms, the exchange of a split 1.5.  A block takes the larger of its latency and its MMA time, or its operand bytes at the
-// 112 GB/s that L2 gives each SM when all of them load.  The choice was within 15 % of the best
-// configuration in all but one of 35 shapes.
+// takes 4, a tile 1 to 2 beside its blocks of 64 terms, the exchange of a split 1.5.  A block
+// takes the largest of its latency, its MMA time, and its operand bytes at the 112 GB/s that
+// L2 gives each SM when all of them load.  The choice was within 15 % of the best configuration
+// in 34 of the 35 shapes.
 void choose(fa::TcProduct* p, const fa::TcShape& shape) {
     const auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
     const uint64_t kb = up(p->k, 64), n_sm = static_cast<uint64_t>(shape.sms);
@@ -282,13 +288,22 @@ void choose(fa::TcProduct* p, const fa::TcShape& shape) {
 // Few rows that the tensor cores could only take after a pass over the weights (fp32 ones into
 // three planes, 16 bytes moved per weight instead of 4; bf16 ones of an odd stride into an
 // aligned copy): read as they are on the FP32 units.  Against 4096 x 4096 fp32 weights: 16
-// rows 23.5 us (tensor cores with their pass 46), 32 rows 46 (48), 64 rows 90 (50).
+// rows 23.5 us (tensor cores with their pass 46), 32 rows 46 (48), 64 rows 90 (50).  Against
+// 4097 x 4095 bf16 ones: stored [n, k] 1 row 8.1 us (20.5), 8 rows 16.3 (20.7); stored [k, n]
+// 1 row 13.8 (20.9), 4 rows 17.4 (21.1), 8 rows 25.8 (21.3).
 bool use_thin(const fa::ProdArgs& q) {
     if (!q.a.kmajor || q.a.dtype != q.b.dtype) return false;
-    // with b stored [k, n] a warp walks k / 64 rows of it, eight loads in flight, for every eight
-    // rows of a: some 60 us at 10 rows and k = 21360, where the tensor cores and their pass take 30
-    if (!q.b.kmajor && static_cast<uint64_t>(q.k) * ((q.m + 7) / 8) > 11000) return false;
-    return q.b.dtype == 0 ? q.m <= (q.b.kmajor ? 24 : 16) : q.m <= 8 && !tma_ready(q.b);
+    // With b stored [k, n] a warp walks down its share of the rows, eight loads in flight, for
+    // every eight rows of a: 1.3 ns per row of b, or b's bytes at some 3.3 TB/s where that is
+    // more.  The tensor cores with their pass over fp32 weights (16 bytes moved for each) take
+    // some 9 us, 1.2 ns per row, and those bytes at 6.5 TB/s: measured 10 rows by 21360 x 88
+    // 56.5 us (thin) and 40.3, 8 rows by 20000 x 2000 66.5 and 122.9, 16 by 4096 x 4096 28.8
+    // and 50.7.
+    if (!q.b.kmajor && q.b.dtype == 0) {
+        const double groups = (q.m + 7) / 8, k = q.k, kn = static_cast<double>(q.k) * q.n;
+        if (groups * std::max(0.0013 * k, kn * 4 / 3.3e6) > 9 + 0.0012 * k + kn * 16 / 6.5e6) return false;
+    }
+    return q.b.dtype == 0 ? q.m <= (q.b.kmajor ? 24 : 16) : q.m <= (q.b.kmajor ? 8 : 4) && !tma_ready(q.b);
 }
 
 // A product by the kernel that suits its size.  run == false only adds up the workspace.
@@ -353,7 +368,9 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     q.b = {p.b, p.ldb, code_of(p.dtype_in), tb};
     q.e = {static_cast<float>(p.alpha), static_cast<float>(p.beta), p.bias, res, p.out, p.pre, p.ldr, p.ldo,
            code_of(p.dtype_in), code_of(p.dtype_out), p.act};
-    const bool tiny = use_tiny(p.m, p.n, p.k);
+    // a few long sums of fp32 operands have more lanes in the thin kernel (8 x 8 x 1000: 2.3 us
+    // against 6.7, 4 x 10 x 256: 1.7 against 2.4)
+    const bool tiny = use_tiny(p.m, p.n, p.k, p.k, p.dtype_in == FA_F32 ? 1024 : 256) && !(p.k > 128 && tb && p.dtype_in == FA_F32 && use_thin(q));
     Carve need{nullptr};
     if (!tiny) do_product(w, q, nullptr, nullptr, &need, false, s, "product");
     r = ensure_ws(w, need.used, cap);
@@ -405,10 +422,13 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     const int it = code_of(p.dtype_in), dt = code_of(p.dtype_dout), gt = code_of(p.dtype_grad);
     // dZ is dout itself, or is written to the workspace: in fp32 for the tiny kernel and for few
     // fp32 rows, else as bf16 planes.  few: the gradient of a is for the thin kernels (see
-    // use_thin), which take dZ as it lies
-    const bool tiny = use_tiny(p.m, p.n, p.k);
+    // use_thin), which take dZ as it lies; both gradients of 1 x 1024 x 4096 fp32 then take 19.0
+    // us (28.5 on the tensor cores), of 8 x 4096 x 1024 26.9 (30.8), of 16 x 4096 x 4096 85.0
+    // (86.2), of 1 x 10387 x 9180 bf16 160 (201), of 4 x 4097 x 4095 bf16 54.6 (55.0)
+    const bool tiny = use_tiny(p.m, p.n, p.k, p.m * p.n * p.k ? std::max({p.m, p.n, p.k}) : 0, 1024);
     const bool few = !tiny && (it == 0 ? p.m <= 16
-                                       : gt == 1 && p.m <= 8 && want_a && !tma_ready({p.b, p.ldb, it, !tb}));
+                                       : gt == 1 && p.m <= 4 && want_a && (act || dt == it) &&
+                                             !tma_ready({p.b, p.ldb, it, !tb}));
     const bool products = want_a || want_b;
     const fa::ProdOperand d_in{p.dout, p.ldd, dt, true};
     const bool write_dz = products && m && n && (act || (!tiny && !few && !tma_ready(d_in)));
