@@ -197,10 +197,11 @@ def lib():
 def _ptr(x) -> int:
     if x is None:
         return 0
+    of = getattr(x, "data_ptr", None)      # a tensor, most often
+    if of is not None:
+        return of()
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):
         return int(x.ctypes.data)
     raise TypeError(f"cannot take a pointer of {type(x)!r}")

@@ -51,11 +51,10 @@ cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows,
 
 // dZ[m,n] = dout * act'(pre), computed in fp32 and written (dz != nullptr) with row stride
 // ldz as fp32 (dz_planes 0), rounded to bf16 (1) or as three bf16 planes (3), m * ldz
-// elements apart; and its column sums over blocks of kColRows rows, to
-// part[ceil(m / kColRows)][n] (part != nullptr).
-constexpr uint32_t kColRows = 32;
+// elements apart; and its column sums over blocks of `rows` rows (a multiple of 8),
+// to part[ceil(m / rows)][n] (part != nullptr).
 struct ActGradArgs {
-    uint32_t m, n;
+    uint32_t m, n, rows;
     const void* dout;
     const void* pre;        // nullptr: act is none
     uint64_t ldd, ldp;

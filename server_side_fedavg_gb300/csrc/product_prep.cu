@@ -89,14 +89,14 @@ __device__ __forceinline__ void load8t(const T* p, uint32_t c, uint32_t cols, bo
         for (int i = 0; i < 8; ++i) x[i] = c + i < cols ? elem(p, i, sizeof(T) == 2) : 0.0f;
 }
 
-// A block of kColRows rows by 256 columns per CTA: a lane holds 8 columns, a warp every
+// A block of a.rows rows by 256 columns per CTA: a lane holds 8 columns, a warp every
 // eighth row; the column sums join over the warps in warp order.
 template <typename T>
 __global__ void __launch_bounds__(256, 4) act_grad_kernel(const __grid_constant__ ActGradArgs a, bool vec, bool vz) {
     __shared__ float sums[8][256];
     wait_predecessor();
     const uint32_t c = blockIdx.x * 256 + threadIdx.x % 32 * 8, warp = threadIdx.x / 32;
-    const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
+    const uint32_t blocks = (a.m + a.rows - 1) / a.rows;
     const uint64_t plane = a.m * a.ldz;
     const T *dout = static_cast<const T*>(a.dout), *pre = static_cast<const T*>(a.pre);
     for (uint32_t blk = blockIdx.y; blk < blocks; blk += gridDim.y) {
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(256, 4) act_grad_kernel(const __grid_constant_
         if (c < a.n)
             // a row at a time, in small code: four CTAs per SM keep 32 KB of loads in flight
 #pragma unroll 1
-            for (uint32_t r = blk * kColRows + warp; r < min(a.m, (blk + 1) * kColRows); r += 8) {
+            for (uint32_t r = blk * a.rows + warp; r < min(a.m, (blk + 1) * a.rows); r += 8) {
                 float d[8], z[8];
                 load8t(dout + r * a.ldd + c, c, a.n, vec, d);
                 if (pre) load8t(pre + r * a.ldp + c, c, a.n, vec, z);
@@ -167,7 +167,7 @@ cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows,
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream) {
-    const uint32_t blocks = (a.m + kColRows - 1) / kColRows;
+    const uint32_t blocks = (a.m + a.rows - 1) / a.rows;
     return launch_next(a.dtype ? act_grad_kernel<uint16_t> : act_grad_kernel<float>,
                        dim3((a.n + 255) / 256, blocks < 65535 ? blocks : 65535), 256, stream, a,
                        vec_ok(a.dout, a.ldd, a.dtype) && vec_ok(a.pre, a.ldp, a.dtype), vec_ok(a.dz, a.ldz, 0));
