@@ -46,8 +46,16 @@ cudaError_t launch_product_thin(const ProdArgs& p, cudaStream_t stream);
 // 16-byte aligned base and row stride): the matrix [rows][cols] as `planes` bf16 planes
 // [plane][rows][ldd], ldd a multiple of 8 -- one plane for bf16 sources, three for fp32:
 // x = x0 + x1 + x2, each term the remainder rounded to nearest, 24 bits in all.
-cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols, uint32_t planes, void* dst,
-                         uint64_t ldd, cudaStream_t stream);
+struct SplitJob {
+    const void* src;
+    uint64_t ld;
+    int dtype;
+    uint32_t rows, cols, planes;
+    void* dst;
+    uint64_t ldd;
+};
+// One or two operands in one launch.
+cudaError_t launch_split(const SplitJob* jobs, int n, cudaStream_t stream);
 
 // dZ[m,n] = dout * act'(pre), computed in fp32 and written (dz != nullptr) with row stride
 // ldz as fp32 (dz_planes 0), rounded to bf16 (1) or as three bf16 planes (3), m * ldz

@@ -3,6 +3,8 @@
 // which holds what a pass has just written for the product after it).  Measured: 6262 x 7231
 // fp32 into three planes 71 us, 6.4 TB/s of bytes read and written; gelu's gradient of
 // 2056 x 4096 bf16 with the column sums 20 us, where the activations' arithmetic shows.
+#include <algorithm>
+
 #include "product_device.cuh"
 
 namespace fa {
@@ -59,12 +61,26 @@ __device__ __forceinline__ void load8(const void* p, uint64_t row_at, uint32_t c
     }
 }
 
-// Eight elements per thread and step, rows in turn.
-__global__ void __launch_bounds__(256) split_kernel(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols,
-                                                    int planes, uint16_t* dst, uint64_t ldd, bool vec) {
+// Eight elements per thread and step, rows in turn; the blocks from `second` on have the second
+// operand.
+struct SplitArgs {
+    SplitJob job[2];
+    bool vec[2];
+    uint32_t second;
+};
+
+__global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ SplitArgs a) {
     wait_predecessor();
-    const uint64_t per = ldd / 8, all = per * rows, plane = rows * ldd;
-    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
+    const bool last = blockIdx.x >= a.second;
+    const SplitJob& j = a.job[last];
+    const uint32_t block = last ? blockIdx.x - a.second : blockIdx.x, blocks = last ? gridDim.x - a.second : a.second;
+    const void* src = j.src;
+    const bool vec = a.vec[last];
+    const int dtype = j.dtype;
+    const uint32_t cols = j.cols, planes = j.planes;
+    const uint64_t ld = j.ld, ldd = j.ldd, per = ldd / 8, all = per * j.rows, plane = j.rows * ldd;
+    uint16_t* dst = static_cast<uint16_t*>(j.dst);
+    for (uint64_t i = block * 256ull + threadIdx.x; i < all; i += blocks * 256ull) {
         const uint64_t r = i / per;
         const uint32_t c = static_cast<uint32_t>(i - r * per) * 8;
         float x[8];
@@ -158,12 +174,21 @@ bool vec_ok(const void* p, uint64_t ld, int dtype) {
 
 }  // namespace
 
-cudaError_t launch_split(const void* src, uint64_t ld, int dtype, uint32_t rows, uint32_t cols, uint32_t planes, void* dst,
-                         uint64_t ldd, cudaStream_t stream) {
-    const uint64_t groups = ldd / 8 * rows, blocks = (groups + 255) / 256;
-    const uint32_t grid = blocks < 152 * 8 ? static_cast<uint32_t>(blocks) : 152 * 8;
-    return launch_next(split_kernel, dim3(grid), 256, stream, src, ld, dtype, rows, cols, planes, static_cast<uint16_t*>(dst),
-                       ldd, vec_ok(src, ld, dtype));
+cudaError_t launch_split(const SplitJob* jobs, int n, cudaStream_t stream) {
+    constexpr uint64_t kMost = 152 * 8;
+    SplitArgs a = {};
+    uint64_t blocks[2] = {};
+    for (int i = 0; i < n; ++i) {
+        a.job[i] = jobs[i];
+        a.vec[i] = vec_ok(jobs[i].src, jobs[i].ld, jobs[i].dtype);
+        blocks[i] = (jobs[i].ldd / 8 * jobs[i].rows + 255) / 256;
+    }
+    // shares of the most that run at one time, at least one each
+    const uint64_t all = blocks[0] + blocks[1];
+    if (all > kMost)
+        for (int i = 0; i < n; ++i) blocks[i] = std::max<uint64_t>(1, blocks[i] * kMost / all);
+    a.second = static_cast<uint32_t>(blocks[0]);
+    return launch_next(split_kernel, dim3(static_cast<uint32_t>(blocks[0] + blocks[1])), 256, stream, a);
 }
 
 cudaError_t launch_act_grad(const ActGradArgs& a, cudaStream_t stream) {

@@ -224,20 +224,15 @@ bool tma_ready(const fa::ProdOperand& o) {
     return o.dtype == 1 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 && o.ld < (1ull << 36);
 }
 
-// The operand as the tensor-core kernel reads it: as it is, or laid out in the workspace
-// (launching that if `run`).  x: its extent beside the summed one.
-fa_status lay_out(fa_work* w, const fa::ProdOperand& o, uint32_t x, uint32_t k, Carve* c, fa::TcOperand* t, bool run,
-                  cudaStream_t s) {
-    if (tma_ready(o)) {
-        *t = {o.p, o.ld, 0, 1, o.kmajor};
-        return FA_OK;
-    }
+// The operand as the tensor-core kernel reads it: as it is, or to be laid out in the workspace
+// by `jobs`.  x: its extent beside the summed one.
+fa::TcOperand lay_out(const fa::ProdOperand& o, uint32_t x, uint32_t k, Carve* c, fa::SplitJob* jobs, int* n) {
+    if (tma_ready(o)) return {o.p, o.ld, 0, 1, o.kmajor};
     const uint32_t rows = o.kmajor ? x : k, cols = o.kmajor ? k : x, planes = o.dtype ? 1 : 3;
     const uint64_t ldd = (cols + 7ull) / 8 * 8;
     void* dst = c->take(ldd * rows * planes * 2);
-    *t = {dst, ldd, ldd * rows, planes, o.kmajor};
-    if (!run) return FA_OK;
-    return launched(w, fa::launch_split(o.p, o.ld, o.dtype, rows, cols, planes, dst, ldd, s), "operand layout");
+    jobs[(*n)++] = {o.p, o.ld, o.dtype, rows, cols, planes, dst, ldd};
+    return {dst, ldd, ldd * rows, planes, o.kmajor};
 }
 
 // Tile configuration and split of the summed index: the least time by a model in
@@ -314,17 +309,16 @@ fa_status do_product(fa_work* w, const fa::ProdArgs& q, const fa::TcOperand* rea
     t.n = q.n;
     t.k = q.k;
     t.e = q.e;
-    fa_status r = FA_OK;
     if (!ready_a && !ready_b && use_thin(q)) return run ? launched(w, fa::launch_product_thin(q, s), what) : FA_OK;
-    if (ready_a)
-        t.a = *ready_a;
-    else
-        r = lay_out(w, q.a, q.m, q.k, c, &t.a, run, s);
-    if (ready_b)
-        t.b = *ready_b;
-    else if (r == FA_OK)
-        r = lay_out(w, q.b, q.n, q.k, c, &t.b, run, s);
-    if (r != FA_OK || !run) return r;
+    fa::SplitJob jobs[2];
+    int n = 0;
+    t.a = ready_a ? *ready_a : lay_out(q.a, q.m, q.k, c, jobs, &n);
+    t.b = ready_b ? *ready_b : lay_out(q.b, q.n, q.k, c, jobs, &n);
+    if (!run) return FA_OK;
+    if (n > 0) {
+        const fa_status r = launched(w, fa::launch_split(jobs, n, s), "operand layout");
+        if (r != FA_OK) return r;
+    }
     choose(&t, w->tc);
     return launched(w, fa::launch_product_tc(t, w->tc, w->err_dev, (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s), what);
 }
