@@ -12,8 +12,8 @@
 // Of rows whose statistic is given the slices are independent, and of any number.
 //
 // Measured, back to back (the measured copy rate is 6.80 TB/s): gradient and loss of 4096 rows of
-// 32000 bf16 logits, 8 lists of 32, 98 us, 5.4 TB/s (instruction issue 56 % busy, HBM at 4.8
-// TB/s, the rest of the traffic in L2); gradient of 700 x 131075 bf16 from a kept statistic
+// 32000 bf16 logits, 8 lists of 32, 98 us, 5.4 TB/s (issue slots 52 % busy, HBM at 4.7 TB/s,
+// the rest of the traffic in L2); gradient of 700 x 131075 bf16 from a kept statistic
 // 77 us, 4.8 TB/s; loss of 1531 x 32003 fp32 37.4 us, 5.3 TB/s; one row of 32000 5.2 us.
 //
 // An exponential is 2^(z c - k) with c = log2(e) / T and k = reference c rounded: one FMA and one
