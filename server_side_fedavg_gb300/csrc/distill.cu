@@ -19,7 +19,7 @@
 // An exponential is 2^(z c - k) with c = log2(e) / T and k = reference c rounded: one FMA and one
 // ex2.  k's rounding is the same in every term and in the statistic that is formed with the
 // same k, so it cancels.  Rows whose reference is beyond 2^20 T / log2(e) in size or whose sum is
-// beyond 2^100 (masked by the type's lowest value or -inf where the reference was looked for, or
+// beyond 2^90 (masked by the type's lowest value or -inf where the reference was looked for, or
 // with infinities) take 2^((z - maximum) c) instead, in further passes over memory.
 //
 // The shares of the entries are gathered in a hash table in shared memory (entry -> sum of
@@ -338,7 +338,13 @@ struct Exp {
 
 // The fast form's k is at most 2^20 in size: its rounding, up to 2^-5, is in every exponent.
 constexpr float kFastMost = 1048576.0f;
-constexpr float kSumMost = 1.2676506e30f;      // 2^100
+// Every partial sum is held to this before it is scaled to a larger reference: the scale is 0
+// beyond a gap of 126 (ex2.approx flushes), and a sum that may be dropped then has to be small
+// beside the larger reference's own term of 1 -- 2^90 leaves 2^-36 of it.
+constexpr float kSumMost = 0x1p90f;
+// A partial sum beyond it (or NaN) is passed on as an infinity, which no scale turns into a
+// number below kSumMost: the row takes the plain form.
+__device__ __forceinline__ float bounded(float s) { return s < kSumMost ? s : INFINITY; }
 
 // From a kept statistic: q = 2^(z c - lse log2 e), the product's rounding error moved to `scale`
 // (log2 e is kLog2e + 1.92596303e-8).
@@ -660,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : kForm == kWhol
             } else {
                 // One pass: the sum over a reference, the largest of what the warp has at two
                 // places of the row, in place of the maximum.  Terms over it are no harm up to
-                // 2^100 (beyond, the plain form below).
+                // kSumMost (beyond, the plain form below).
                 float m = fmaxf(edge, -most);
                 if (t < nvec) {
                     m = max_of<T>(m, held[t]);
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : kForm == kWhol
                 }
                 if (!kGrad) fetch_next(t < nvec ? t + (nvec - t + kThreads - 1) / kThreads * kThreads : t);
                 // merged over the warp, the CTA and the cluster, in a fixed order
-                float s = warp_sum(s2.x + s2.y);
+                float s = bounded(warp_sum(s2.x + s2.y));
                 if (t % 32 == 0) {
                     tmp[t / 32] = m;
                     tmp2[t / 32] = s;
@@ -696,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : kForm == kWhol
                 s = tmp2[t % kWarps];
                 merge_lanes<kWarps>(m, s, c);
                 if constexpr (kForm == kJoint) {
-                    if (!give(m, s)) break;
+                    if (!give(m, bounded(s))) break;
                     m = pairs[0].x;
                     s = pairs[0].y;
                     for (uint32_t r = 1; r < ctas; ++r) merge(m, s, pairs[r].x, pairs[r].y, c);
