@@ -612,7 +612,8 @@ typedef struct {
     const void* value;         /* [rows, topk] that client's logits there (dtype_value) */
     uint32_t topk;             /* 1..FA_DISTILL_MAX_TOPK */
     uint32_t reserved;         /* 0 */
-    double weight;             /* n_j: finite, >= 0, <= 2^24 (its sample count) */
+    double weight;             /* n_j: finite, >= 0, <= 2^24 (its sample count); below 2^-225 of the
+                                  call's largest it counts as 0 */
 } fa_distill_client;
 
 #define FA_DISTILL_MAX_CLIENTS 16
@@ -633,7 +634,8 @@ typedef struct {
  * its logits are not looked at), has loss 0 and a zero gradient.  An entry of z at -inf
  * has q = 0 (a closed vocabulary entry); a row whose every entry is -inf gives NaN.
  * Several clients (or places) may name the same entry; their shares are added in fixed
- * point (2^-51 units), so the order of the sum does not matter. */
+ * point, so the order of the sum does not matter: in units of 2^-51 of the clients' whole
+ * weight, or of N_r in rows whose N_r is below 2^-8 of that. */
 typedef struct {
     uint32_t size;                    /* sizeof(fa_distill_args) */
     uint32_t n_clients;               /* 1..FA_DISTILL_MAX_CLIENTS */

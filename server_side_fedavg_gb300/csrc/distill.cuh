@@ -10,13 +10,15 @@ namespace fa {
 constexpr int kMaxDistillClients = 16;
 constexpr uint32_t kMaxDistillTopk = 2048;   // summed over the clients
 
+constexpr float kLightest = 256.0f;          // all weight / a client's: above, it is a light one
+
 constexpr unsigned int kErrListIndex = 2u;   // device error bit: a list entry >= vocab
 
 struct DistillClient {
     const int32_t* index;   // [rows][topk]
     const void* value;      // [rows][topk]
     uint32_t topk;
-    float weight;           // n_j
+    float weight;           // n_j, times a power of two that the call's weights share
     float share;            // n_j / (sum of all n_j), 0 if that sum is 0
 };
 
@@ -37,9 +39,10 @@ struct DistillArgs {
     uint32_t sms;              // of the device
     uint32_t table_at;         // bytes of a slice's vectors in shared memory: the table follows
     float temperature, inv_t;
-    float total;               // sum of all n_j
+    float total;               // sum of all weights
     int dtype, value_dtype;
     bool short_lists;          // every list has at most 64 places
+    bool light;                // a client has a weight, but less than 1 / kLightest of all
     bool joint;                // a row's CTAs are a cluster and exchange their statistics
     bool test_expire;          // the first exchange's wait counts as run out
     DistillClient client[kMaxDistillClients];

@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <new>
 #include <string>
@@ -511,24 +512,35 @@ fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStre
         return fail(w, FA_ERR_RANGE, "rows or vocab out of range");
     fa::DistillArgs a{};
     uint64_t entries = 0;
-    double total = 0.0;
+    double heaviest = 0.0, total = 0.0;
     for (uint32_t j = 0; j < p.n_clients; ++j) {
         const fa_distill_client& c = p.clients[j];
         if (c.topk < 1 || c.topk > FA_DISTILL_MAX_TOPK) return fail(w, FA_ERR_RANGE, "topk out of range");
         if (!std::isfinite(c.weight) || c.weight < 0.0 || c.weight > 16777216.0)
             return fail(w, FA_ERR_WEIGHT, "client weight");
         entries += c.topk;
-        total += c.weight;
+        heaviest = std::max(heaviest, c.weight);
     }
     if (entries > FA_DISTILL_MAX_TOPK) return fail(w, FA_ERR_RANGE, "more than 2048 list places per row");
     if (p.rows == 0) return FA_OK;
+    // The kernels' fp32 weights: only their ratios matter, so the largest is moved to 2^99 by a power
+    // of two (exact).  Those that fall below fp32's normal numbers, 2^-225 of the largest, count as 0.
+    double weight[FA_DISTILL_MAX_CLIENTS];
+    const int shift = heaviest > 0.0 ? 99 - std::ilogb(heaviest) : 0;
+    for (uint32_t j = 0; j < p.n_clients; ++j) {
+        weight[j] = std::ldexp(p.clients[j].weight, shift);
+        if (weight[j] < std::numeric_limits<float>::min()) weight[j] = 0.0;
+        total += weight[j];
+    }
+    for (uint32_t j = 0; j < p.n_clients; ++j)
+        a.light |= weight[j] > 0.0 && weight[j] * fa::kLightest < total * (1.0 + 1e-6);   // (1e-6: fp32 in the kernel)
     fa_status r = check_mat(w, p.logits, p.rows, p.vocab, p.ld, p.dtype, "logits");
     for (uint32_t j = 0; r == FA_OK && j < p.n_clients; ++j) {
         const fa_distill_client& c = p.clients[j];
         r = check_mat(w, c.index, p.rows, c.topk, c.topk, FA_F32, "index");
         if (r == FA_OK) r = check_mat(w, c.value, p.rows, c.topk, c.topk, p.dtype_value, "value");
-        a.client[j] = {c.index, c.value, c.topk, static_cast<float>(c.weight),
-                       total > 0.0 ? static_cast<float>(c.weight / total) : 0.0f};
+        a.client[j] = {c.index, c.value, c.topk, static_cast<float>(weight[j]),
+                       total > 0.0 ? static_cast<float>(weight[j] / total) : 0.0f};
     }
     if (r == FA_OK && p.row_weight) r = check_mat(w, p.row_weight, 1, p.rows, p.rows, FA_F32, "row_weight");
     if (r == FA_OK && (p.loss || !grad)) r = check_mat(w, p.loss, 1, p.rows, p.rows, FA_F32, "loss");
