@@ -116,13 +116,39 @@ fa_status chain_in(fa_work* w, cudaStream_t s, bool capture) {
     return FA_OK;
 }
 
-fa_status chain_out(fa_work* w, cudaStream_t s, bool capture) {
-    if (capture) return FA_OK;
-    FW_CUDA(w, cudaEventRecord(w->chain, s));
-    FW_CUDA(w, cudaStreamGetId(s, &w->chain_stream_id));
-    w->chain_valid = true;
-    return FA_OK;
-}
+// From a call's first launch to its end, however it ends: the handle's next call, and a wait for
+// the handle, come after everything that this call has queued.  A call that fails half-way has
+// kernels on its stream that still use the workspace.
+class ChainOut {
+public:
+    ChainOut(fa_work* w, cudaStream_t s, bool capture) : w_(w), s_(s), open_(!capture) {}
+    ChainOut(const ChainOut&) = delete;
+    ChainOut& operator=(const ChainOut&) = delete;
+    ~ChainOut() {
+        if (open_ && record() != cudaSuccess) cudaGetLastError();
+    }
+    // r, or the event's own error where r is none.
+    fa_status end(fa_status r) {
+        if (r != FA_OK || !open_) return r;
+        open_ = false;
+        const cudaError_t e = record();
+        return e == cudaSuccess ? FA_OK : cuda_fail(w_, e, "cudaEventRecord");
+    }
+
+private:
+    cudaError_t record() {
+        unsigned long long id = 0;
+        cudaError_t e = cudaEventRecord(w_->chain, s_);
+        if (e == cudaSuccess) e = cudaStreamGetId(s_, &id);
+        if (e != cudaSuccess) return e;
+        w_->chain_stream_id = id;
+        w_->chain_valid = true;
+        return e;
+    }
+    fa_work* w_;
+    cudaStream_t s_;
+    bool open_;
+};
 
 // At least `bytes` of workspace.  Growing waits for the handle's queued calls, which may
 // still use the old one.
@@ -371,11 +397,10 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     r = ensure_ws(w, need.used, cap);
     if (r == FA_OK) r = chain_in(w, s, cap);
     if (r != FA_OK) return r;
+    ChainOut chain(w, s, cap);
     Carve c{w->ws};
-    r = tiny ? launched(w, fa::launch_product_tiny(q, s), "product")
-              : do_product(w, q, nullptr, nullptr, &c, true, s, "product");
-    if (r != FA_OK) return r;
-    return chain_out(w, s, cap);
+    return chain.end(tiny ? launched(w, fa::launch_product_tiny(q, s), "product")
+                          : do_product(w, q, nullptr, nullptr, &c, true, s, "product"));
 }
 
 // Rows per block of the activation's gradient: the number with the least work in the last of the
@@ -449,14 +474,7 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     const uint64_t ldz = planes == 0 ? p.n : (p.n + 7) / 8 * 8;
     const bool cap = capturing(s);
     // two passes over the same steps: the first adds up the workspace
-    Carve c{nullptr};
-    for (int run = 0; run < 2; ++run) {
-        if (run) {
-            r = ensure_ws(w, c.used, cap);
-            if (r == FA_OK) r = chain_in(w, s, cap);
-            if (r != FA_OK) return r;
-            c = Carve{w->ws};
-        }
+    const auto pass = [&](Carve& c, bool run) {
         void* dz = write_dz ? c.take(p.m * ldz * (planes ? 2 * planes : 4)) : nullptr;
         float* part = want_bias ? static_cast<float*>(c.take(blocks * p.n * 4)) : nullptr;
         if (run && (write_dz || want_bias) && m && n) {
@@ -497,9 +515,16 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
                 r = do_product(w, q, tb && !few ? &tz_n : nullptr, tb || few ? nullptr : &tz_n, &c, run, s, "gradient of b");
         }
         c.used = std::max(c.used, after_a);
-        if (r != FA_OK) return r;
-    }
-    return chain_out(w, s, cap);
+    };
+    Carve need{nullptr}, c{nullptr};
+    pass(need, false);
+    if (r == FA_OK) r = ensure_ws(w, need.used, cap);
+    if (r == FA_OK) r = chain_in(w, s, cap);
+    if (r != FA_OK) return r;
+    ChainOut chain(w, s, cap);
+    c.base = w->ws;
+    pass(c, true);
+    return chain.end(r);
 }
 
 fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStream_t s) {
@@ -590,9 +615,8 @@ fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStre
     a.total = static_cast<float>(total);
     a.dtype = code_of(p.dtype);
     a.value_dtype = code_of(p.dtype_value);
-    r = launched(w, fa::launch_distill(a, s), grad ? "distillation gradient" : "distillation loss");
-    if (r != FA_OK) return r;
-    return chain_out(w, s, cap);
+    ChainOut chain(w, s, cap);
+    return chain.end(launched(w, fa::launch_distill(a, s), grad ? "distillation gradient" : "distillation loss"));
 }
 
 void free_work(fa_work* w) {
