@@ -515,7 +515,7 @@ typedef struct {
 fa_status fa_work_open(const fa_work_opts* opts, fa_work** out);
 
 /* Wait (bounded) for the handle's work and free it.  NULL is a no-op.  On FA_ERR_TIMEOUT
- * the handle stays open. */
+ * and FA_ERR_NOMEM (host memory) the handle stays open. */
 fa_status fa_work_close(fa_work* w);
 
 /* Wait (bounded) for the handle's last call and report what its kernels found since the

@@ -630,23 +630,49 @@ void free_work(fa_work* w) {
     delete w;
 }
 
-// Every operator entry point: the argument struct copied up to the caller's size, the
-// handle locked, its device current, no exception past the C boundary.
+// No exception past the C boundary.
+template <typename F>
+fa_status guarded(F f) {
+    try {
+        return f();
+    } catch (const std::bad_alloc&) {
+        return FA_ERR_NOMEM;
+    } catch (...) {
+        return FA_ERR_INTERNAL;
+    }
+}
+
+// Every operator entry point: the argument struct checked for its size, the handle locked, its
+// device current.
 template <typename Args, typename F>
 fa_status enter(const char* name, fa_work* w, const Args* args, F f) {
     if (!w) return FA_ERR_ARG;
-    try {
+    return guarded([&] {
         Range range(name);
         std::lock_guard<std::mutex> lk(w->mu);
         DeviceGuard dg(w->device);
         w->err.clear();
         if (!args || args->size < sizeof(Args)) return fail(w, FA_ERR_ARG, "args is NULL or args.size too small");
         return f(*args);
-    } catch (const std::bad_alloc&) {
-        return FA_ERR_NOMEM;
-    } catch (...) {
-        return FA_ERR_INTERNAL;
+    });
+}
+
+fa_status sync_impl(fa_work* w) {
+    if (w->chain_valid) {
+        const fa_status r = wait_event(w, w->chain, "fa_work_sync");
+        if (r != FA_OK) return r;
     }
+    *w->err_host = 0;
+    FW_CUDA(w, cudaMemcpyAsync(w->err_host, w->err_dev, sizeof(unsigned int), cudaMemcpyDeviceToHost, w->err_stream));
+    FW_CUDA(w, cudaMemsetAsync(w->err_dev, 0, sizeof(unsigned int), w->err_stream));
+    FW_CUDA(w, cudaEventRecord(w->err_ev, w->err_stream));
+    const fa_status r = wait_event(w, w->err_ev, "fa_work_sync (error word)");
+    if (r != FA_OK) return r;
+    if (*w->err_host & fa::kErrWaitTimeout)
+        return fail(w, FA_ERR_INTERNAL, "a device-side wait gave up (bounded mbarrier wait): outputs are invalid");
+    if (*w->err_host & fa::kErrListIndex)
+        return fail(w, FA_ERR_RANGE, "a client's list named a vocabulary entry >= vocab (left out)");
+    return FA_OK;
 }
 
 }  // namespace
@@ -693,39 +719,28 @@ fa_status fa_work_open(const fa_work_opts* opts, fa_work** out) {
 
 fa_status fa_work_close(fa_work* w) {
     if (!w) return FA_OK;
-    {
-        std::lock_guard<std::mutex> lk(w->mu);
+    return guarded([&]() -> fa_status {
         DeviceGuard dg(w->device);
-        if (w->chain_valid) {
-            const fa_status r = wait_event(w, w->chain, "fa_work_close");
-            if (r == FA_ERR_TIMEOUT) return r;
+        {
+            std::lock_guard<std::mutex> lk(w->mu);
+            if (w->chain_valid) {
+                const fa_status r = wait_event(w, w->chain, "fa_work_close");
+                if (r == FA_ERR_TIMEOUT) return r;
+            }
         }
-    }
-    DeviceGuard dg(w->device);
-    free_work(w);
-    return FA_OK;
+        free_work(w);
+        return FA_OK;
+    });
 }
 
 fa_status fa_work_sync(fa_work* w) {
     if (!w) return FA_ERR_ARG;
-    std::lock_guard<std::mutex> lk(w->mu);
-    DeviceGuard dg(w->device);
-    w->err.clear();
-    if (w->chain_valid) {
-        const fa_status r = wait_event(w, w->chain, "fa_work_sync");
-        if (r != FA_OK) return r;
-    }
-    *w->err_host = 0;
-    FW_CUDA(w, cudaMemcpyAsync(w->err_host, w->err_dev, sizeof(unsigned int), cudaMemcpyDeviceToHost, w->err_stream));
-    FW_CUDA(w, cudaMemsetAsync(w->err_dev, 0, sizeof(unsigned int), w->err_stream));
-    FW_CUDA(w, cudaEventRecord(w->err_ev, w->err_stream));
-    const fa_status r = wait_event(w, w->err_ev, "fa_work_sync (error word)");
-    if (r != FA_OK) return r;
-    if (*w->err_host & fa::kErrWaitTimeout)
-        return fail(w, FA_ERR_INTERNAL, "a device-side wait gave up (bounded mbarrier wait): outputs are invalid");
-    if (*w->err_host & fa::kErrListIndex)
-        return fail(w, FA_ERR_RANGE, "a client's list named a vocabulary entry >= vocab (left out)");
-    return FA_OK;
+    return guarded([&] {
+        std::lock_guard<std::mutex> lk(w->mu);
+        DeviceGuard dg(w->device);
+        w->err.clear();
+        return sync_impl(w);
+    });
 }
 
 fa_status fa_work_get_stats(fa_work* w, fa_work_stats* out) {
