@@ -18,3 +18,26 @@ def test_no_exception_leaves_a_wait(entry):
     assert w.sync() == fa.FA_OK            # the handle is still open
     assert w.product(300, 260, 516, A, B, OUT, stream=1) == fa.FA_OK
     assert w.close() == fa.FA_OK
+
+
+def test_the_error_word_is_zero_before_the_handle_is_handed_out():
+    """Kernels on the caller's streams may set it at once, and fa_work_sync reads it on a stream of
+    its own: neither waits for a memset that is still queued."""
+    w = Work()
+    log = w.opened
+    memset = next(i for i, c in enumerate(log) if c.startswith("memset"))
+    stream = log[memset].split(":")[1]
+    assert f"synchronize:{stream}" in log[memset:]
+    assert w.close() == fa.FA_OK
+
+
+@pytest.mark.parametrize("name", ["malloc", "memset", "event", "stream", "host_alloc", "synchronize"])
+def test_a_failed_open_says_so(name):
+    import ctypes
+    w = Work()
+    w.close()
+    w.L.ws_reset()
+    w.fail(name)
+    h = ctypes.c_void_p()
+    status = w.L.fa_work_open(None, ctypes.byref(h))
+    assert status in (fa.FA_ERR_NOMEM, fa.FA_ERR_CUDA) and h.value is None
