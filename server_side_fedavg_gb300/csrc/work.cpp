@@ -171,7 +171,7 @@ fa_status ensure_ws(fa_work* w, uint64_t bytes, bool capture) {
         FW_CUDA(w, cudaFree(w->ws));
     }
     w->ws = nullptr;
-    w->ws_bytes = 0;
+    w->ws_bytes = w->stats.workspace_bytes = 0;
     w->ws_captured = false;
     FW_CUDA(w, cudaMalloc(reinterpret_cast<void**>(&w->ws), bytes));
     w->ws_bytes = bytes;

@@ -41,3 +41,17 @@ def test_a_failed_open_says_so(name):
     h = ctypes.c_void_p()
     status = w.L.fa_work_open(None, ctypes.byref(h))
     assert status in (fa.FA_ERR_NOMEM, fa.FA_ERR_CUDA) and h.value is None
+
+
+def test_the_workspace_is_as_large_as_the_handle_says():
+    w = Work()
+    assert w.product(300, 260, 516, A, B, OUT) == fa.FA_OK
+    before = w.stats().workspace_bytes
+    assert before > 0
+    w.fail("malloc")
+    assert w.product(3000, 2600, 5160, A, B, OUT) == fa.FA_ERR_NOMEM
+    assert w.stats().workspace_bytes == 0          # the old one had been given up for the larger
+    w.L.ws_clear_log()
+    assert w.product(300, 260, 516, A, B, OUT) == fa.FA_OK
+    assert "malloc" in w.log() and w.stats().workspace_bytes == before
+    assert w.close() == fa.FA_OK
