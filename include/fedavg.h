@@ -486,7 +486,9 @@ const char* fa_last_error(const fa_ctx* ctx);
  * Calls on one handle may use any streams; each starts after the handle's previous call
  * (they share the workspace).  All tensors are in the handle's device memory, row-major
  * with a row stride in elements (`ld...`), and are read and written on `stream`; what was
- * queued on other streams is the caller's to order.  No call waits for the GPU, except
+ * queued on other streams is the caller's to order.  An output shares no element with another
+ * tensor of its call, but for the exceptions named below; column slices of one buffer are
+ * apart (matrices whose rows are different distances apart must have spans that are).  No call waits for the GPU, except
  * to free a workspace that has to grow.  Calls can be captured into a CUDA graph once the
  * workspace is large enough (a call that would have to grow it returns FA_ERR_STATE while
  * capturing); replays use the workspace of the time of the capture (kept until

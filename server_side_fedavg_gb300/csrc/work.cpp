@@ -209,12 +209,33 @@ fa_status check_mat(fa_work* w, const void* p, uint64_t rows, uint64_t width, ui
     return check_ptr(w, p, name);
 }
 
-bool overlap(const void* p, uint64_t prows, uint64_t pwidth, uint64_t pld, uint64_t ps, const void* q, uint64_t qrows,
-             uint64_t qwidth, uint64_t qld, uint64_t qs) {
-    if (!p || !q || !prows || !pwidth || !qrows || !qwidth) return false;
-    const uintptr_t p0 = reinterpret_cast<uintptr_t>(p), q0 = reinterpret_cast<uintptr_t>(q);
-    const uintptr_t p1 = p0 + ((prows - 1) * pld + pwidth) * ps, q1 = q0 + ((qrows - 1) * qld + qwidth) * qs;
-    return p0 < q1 && q0 < p1;
+// Whether two matrices share an element: rows of `width` elements of `size` bytes, `ld` apart.
+// Exact where one of them is one run of bytes or both have rows the same distance apart (column
+// slices of one buffer); else where their spans meet.
+struct Extent {
+    const void* p;
+    uint64_t rows, width, ld, size;
+};
+
+bool overlap(const Extent& x, const Extent& y) {
+    if (!x.p || !y.p || !x.rows || !x.width || !y.rows || !y.width) return false;
+    typedef __int128 Wide;               // 2^31 rows of 2^40 elements
+    const auto rows = [](const Extent& e) -> Wide { return e.width == e.ld ? 1 : e.rows; };
+    const auto row = [](const Extent& e) -> Wide { return Wide(e.width == e.ld ? e.rows * e.width : e.width) * e.size; };
+    const Wide x_row = row(x), y_row = row(y), x_rows = rows(x), y_rows = rows(y);
+    const Wide x_step = Wide(x.ld) * x.size, y_step = Wide(y.ld) * y.size;
+    // from x's first byte to y's
+    const Wide apart = Wide(reinterpret_cast<uintptr_t>(y.p)) - Wide(reinterpret_cast<uintptr_t>(x.p));
+    if (apart >= (x_rows - 1) * x_step + x_row || -apart >= (y_rows - 1) * y_step + y_row) return false;
+    if (x_rows > 1 && y_rows > 1 && x_step != y_step) return true;
+    const Wide step = x_rows > 1 ? x_step : y_step;
+    // Row j of y begins apart + (j - i) step bytes after row i of x: they meet where that lies in
+    // (-y_row, x_row).  The least difference of rows that is above the lower end:
+    const Wide from = -y_row - apart;
+    Wide least = from / step;                                     // rounded towards 0
+    if (from % step != 0 && from < 0) --least;                    // down
+    least = std::max<Wide>(least + 1, 1 - x_rows);
+    return least <= y_rows - 1 && apart + least * step < x_row;
 }
 
 constexpr uint64_t kMaxSize = 1ull << 31;
@@ -369,16 +390,13 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
     if (r == FA_OK && res) r = check_mat(w, res, p.m, p.n, p.ldr, p.dtype_out, "residual");
     if (r == FA_OK && p.pre) r = check_mat(w, p.pre, p.m, p.n, p.ldo, p.dtype_out, "pre");
     if (r != FA_OK) return r;
-    for (const void* o : {static_cast<const void*>(p.out), static_cast<const void*>(p.pre)})
-        if (overlap(o, p.m, p.n, p.ldo, so, p.a, ar, aw, p.lda, si) ||
-            overlap(o, p.m, p.n, p.ldo, so, p.b, br, bw, p.ldb, si) ||
-            overlap(o, p.m, p.n, p.ldo, so, p.bias, 1, p.n, p.n, si))
-            return fail(w, FA_ERR_ARG, "an output overlaps a, b or bias");
-    if (overlap(p.out, p.m, p.n, p.ldo, so, p.pre, p.m, p.n, p.ldo, so))
-        return fail(w, FA_ERR_ARG, "out overlaps pre");
-    if (res && overlap(p.pre, p.m, p.n, p.ldo, so, res, p.m, p.n, p.ldr, so))
-        return fail(w, FA_ERR_ARG, "pre overlaps residual");
-    if (res && !(res == p.out && p.ldr == p.ldo) && overlap(p.out, p.m, p.n, p.ldo, so, res, p.m, p.n, p.ldr, so))
+    const Extent out{p.out, p.m, p.n, p.ldo, so}, pre{p.pre, p.m, p.n, p.ldo, so}, residual{res, p.m, p.n, p.ldr, so};
+    const Extent in[] = {{p.a, ar, aw, p.lda, si}, {p.b, br, bw, p.ldb, si}, {p.bias, 1, p.n, p.n, si}};
+    for (const Extent& e : in)
+        if (overlap(out, e) || overlap(pre, e)) return fail(w, FA_ERR_ARG, "an output overlaps a, b or bias");
+    if (overlap(out, pre)) return fail(w, FA_ERR_ARG, "out overlaps pre");
+    if (overlap(pre, residual)) return fail(w, FA_ERR_ARG, "pre overlaps residual");
+    if (!(res == p.out && p.ldr == p.ldo) && overlap(out, residual))
         return fail(w, FA_ERR_ARG, "out overlaps residual without being it");
     const bool cap = capturing(s);
     fa::ProdArgs q{};
@@ -441,18 +459,12 @@ fa_status backward_impl(fa_work* w, const fa_product_backward_args& p, cudaStrea
     if (r == FA_OK && p.d_b) r = check_mat(w, p.d_b, br, bw, p.lddb, p.dtype_grad, "d_b");
     if (r == FA_OK && p.d_bias) r = check_mat(w, p.d_bias, 1, p.n, p.n, p.dtype_grad, "d_bias");
     if (r != FA_OK) return r;
-    const struct {
-        const void* p;
-        uint64_t rows, width, ld, size;
-        bool out;
-    } t[] = {{p.d_a, ar, aw, p.ldda, sg, true}, {p.d_b, br, bw, p.lddb, sg, true}, {p.d_bias, 1, p.n, p.n, sg, true},
-             {p.d_b ? p.a : nullptr, ar, aw, p.lda, si, false}, {p.d_a ? p.b : nullptr, br, bw, p.ldb, si, false},
-             {p.dout, p.m, p.n, p.ldd, sd, false}, {act ? p.pre : nullptr, p.m, p.n, p.ldp, sd, false}};
+    const Extent t[] = {{p.d_a, ar, aw, p.ldda, sg}, {p.d_b, br, bw, p.lddb, sg}, {p.d_bias, 1, p.n, p.n, sg},
+                        {p.d_b ? p.a : nullptr, ar, aw, p.lda, si}, {p.d_a ? p.b : nullptr, br, bw, p.ldb, si},
+                        {p.dout, p.m, p.n, p.ldd, sd}, {act ? p.pre : nullptr, p.m, p.n, p.ldp, sd}};
     for (int i = 0; i < 3; ++i)
         for (int j = i + 1; j < 7; ++j)
-            if (overlap(t[i].p, t[i].rows, t[i].width, t[i].ld, t[i].size, t[j].p, t[j].rows, t[j].width, t[j].ld,
-                        t[j].size))
-                return fail(w, FA_ERR_ARG, "a gradient overlaps another tensor of the call");
+            if (overlap(t[i], t[j])) return fail(w, FA_ERR_ARG, "a gradient overlaps another tensor of the call");
     const bool want_a = p.d_a && p.m && p.k, want_b = p.d_b && p.n && p.k, want_bias = p.d_bias && p.n;
     if (!want_a && !want_b && !want_bias) return FA_OK;
     const uint32_t m = static_cast<uint32_t>(p.m), n = static_cast<uint32_t>(p.n), k = static_cast<uint32_t>(p.k);
@@ -574,23 +586,18 @@ fa_status distill_impl(fa_work* w, const fa_distill_args& p, bool grad, cudaStre
     if (r != FA_OK) return r;
     const uint64_t sz = size_of(p.dtype);
     const bool inplace = grad && p.grad == p.logits && p.ldg == p.ld;
-    const struct {
-        const void* p;
-        uint64_t rows, width, ld, size;
-    } out[] = {{p.loss, 1, p.rows, p.rows, 4},
-               {grad ? nullptr : p.lse, 1, p.rows, p.rows, 4},
-               {grad ? p.grad : nullptr, p.rows, p.vocab, p.ldg, sz}};
+    const auto vector = [&](const void* v) { return Extent{v, 1, p.rows, p.rows, 4}; };
+    const Extent out[] = {vector(p.loss), vector(grad ? nullptr : p.lse), {grad ? p.grad : nullptr, p.rows, p.vocab, p.ldg, sz}};
+    const Extent logits{p.logits, p.rows, p.vocab, p.ld, sz};
     for (int i = 0; i < 3; ++i) {
-        const auto& o = out[i];
-        auto hits = [&](const void* q, uint64_t rows, uint64_t width, uint64_t ld, uint64_t size) {
-            return overlap(o.p, o.rows, o.width, o.ld, o.size, q, rows, width, ld, size);
-        };
-        bool bad = (!(i == 2 && inplace) && hits(p.logits, p.rows, p.vocab, p.ld, sz)) ||
-                   hits(p.row_weight, 1, p.rows, p.rows, 4) || (grad && hits(p.lse, 1, p.rows, p.rows, 4));
-        for (uint32_t j = 0; !bad && j < p.n_clients; ++j)
-            bad = hits(p.clients[j].index, p.rows, p.clients[j].topk, p.clients[j].topk, 4) ||
-                  hits(p.clients[j].value, p.rows, p.clients[j].topk, p.clients[j].topk, size_of(p.dtype_value));
-        for (int k = 0; !bad && k < i; ++k) bad = hits(out[k].p, out[k].rows, out[k].width, out[k].ld, out[k].size);
+        bool bad = (!(i == 2 && inplace) && overlap(out[i], logits)) || overlap(out[i], vector(p.row_weight)) ||
+                   (grad && overlap(out[i], vector(p.lse)));
+        for (uint32_t j = 0; !bad && j < p.n_clients; ++j) {
+            const uint64_t k = p.clients[j].topk;
+            bad = overlap(out[i], {p.clients[j].index, p.rows, k, k, 4}) ||
+                  overlap(out[i], {p.clients[j].value, p.rows, k, k, size_of(p.dtype_value)});
+        }
+        for (int k = 0; !bad && k < i; ++k) bad = overlap(out[i], out[k]);
         if (bad) return fail(w, FA_ERR_ARG, "an output overlaps another tensor of the call");
     }
     const bool cap = capturing(s);
