@@ -481,16 +481,35 @@ def fa_product_backward(work, m, n, k, a, lda, b, ldb, dout, ldd, d_a, ldda, d_b
     _check_work(lib().fa_product_backward(work, args, _stream(stream)), work)
 
 
+# the element types of lists, by name: what is read as int32, as fp32 and as bf16 bits; the types
+# seen to be right are kept (None: a plain address)
+_INDEX_TYPES, _VALUE_TYPES = ("int32", "uint32"), {FA_F32: ("float32",), FA_BF16: ("bfloat16", "uint16", "int16")}
+_index_seen, _value_seen = {None}, {FA_F32: {None}, FA_BF16: {None}}
+
+
+def _check_types(arrays, names, seen, what):
+    for x in arrays:
+        dt = getattr(x, "dtype", None)
+        if dt not in seen:
+            if str(dt).rsplit(".", 1)[-1] not in names:
+                raise TypeError(f"{what}, not {dt}")
+            seen.add(dt)
+
+
 def distill_lists(index, value, topk, weights, dtype_value="f32"):
     """The clients' top-logit lists for fa_distill_loss and fa_distill_grad, marshalled once:
-    per client its index array [rows, topk] (int32, negative: unused), its value array, its
-    topk and its weight (sample count).  The arrays are kept alive by the result."""
+    per client its index array [rows, topk] (int32, negative: unused; torch.topk gives int64:
+    TypeError), its value array, its topk and its weight (sample count).  The arrays are kept
+    alive by the result."""
     n = len(index)
     if not n == len(value) == len(topk) == len(weights):
         _same_length(index=index, value=value, topk=topk, weights=weights)
+    kind = DTYPES[dtype_value]
+    _check_types(index, _INDEX_TYPES, _index_seen, "an index array is int32")
+    _check_types(value, _VALUE_TYPES[kind], _value_seen[kind], f"a value array is of dtype_value, {dtype_value}")
     arr = (fa_distill_client * max(n, 1))(*[(_ptr(i), _ptr(v), t, 0, w)
                                             for i, v, t, w in zip(index, value, topk, weights)])
-    return arr, n, DTYPES[dtype_value], (list(index), list(value))
+    return arr, n, kind, (list(index), list(value))
 
 
 def _distill_args(rows, vocab, logits, ld, dtype, lists, temperature, row_weight, loss, lse, grad, ldg):
