@@ -32,19 +32,26 @@ __device__ __forceinline__ float exp_fast(float x) {
     return y;
 }
 
-// Phi(z), the normal distribution, by the rational approximation 7.1.26 of Abramowitz and Stegun,
-// "Handbook of Mathematical Functions": erfc(x) = exp(-x^2) (a1 t + ... + a5 t^5), t = 1 / (1 + p x),
-// for x >= 0, absolute error up to 1.5e-7 -- of the size of fp32's rounding of Phi near 1.  `bell`
-// receives exp(-z^2 / 2), which the derivative needs too.  A third of the instructions of erff
-// and expf, which bounded the activation gradient (27 us at 2056 x 4096).
+// Phi(z), the normal distribution: its tail beyond |z| is exp(-z^2 / 2) times a polynomial in
+// t = 1 / (1 + 0.48 |z|), fitted to it here by weighted least squares, relative error up to 8.6e-8
+// for |z| up to 14.  With so large a factor of |z| the rounding of t costs little at 0: over
+// normally distributed z gelu in fp32 is off by 2.5e-8 (root mean square), as z times half of
+// 1 + erf is, its derivative by 3.8e-8 (2.8e-8); below -1 both are relatively exact.  `bell`
+// receives exp(-z^2 / 2), which the derivative needs too.  A third of the instructions of erff and
+// expf, with which the activation gradient took 27 us at 2056 x 4096 (now 17).  Five terms, good to
+// 1.5e-7 absolute (2.2 times the error over normal z), saved 1 % of bf16 products and gradients with gelu.
 __device__ __forceinline__ float normal_cdf(float z, float& bell) {
-    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
-    float s = fmaf(t, 1.061405429f, -1.453152027f);
-    s = fmaf(t, s, 1.421413741f);
-    s = fmaf(t, s, -0.284496736f);
-    s = fmaf(t, s, 0.254829592f);
+    const float t = __fdividef(1.0f, fmaf(0.48f, fabsf(z), 1.0f));
+    float s = fmaf(t, 0.053876061f, -0.282321781f);
+    s = fmaf(t, s, 0.584696114f);
+    s = fmaf(t, s, -0.54503572f);
+    s = fmaf(t, s, 0.137284324f);
+    s = fmaf(t, s, 0.0152480444f);
+    s = fmaf(t, s, 0.153758347f);
+    s = fmaf(t, s, 0.19098562f);
+    s = fmaf(t, s, 0.191509038f);
     bell = exp_fast(-0.5f * z * z);
-    const float tail = 0.5f * t * s * bell;
+    const float tail = t * s * bell;
     return z >= 0.0f ? 1.0f - tail : tail;
 }
 
