@@ -632,9 +632,10 @@ typedef struct {
  *   grad[r] = d loss[r] / d z[r] = row_weight[r] * T * (q - sum_j (n_j / N_r) p_j)
  *
  * -- the weighted mean over the clients that sent something for the row, as the per-key
- * means of this library.  A row with no client present, or with row_weight 0 (padding:
- * its logits are not looked at), has loss 0 and a zero gradient.  An entry of z at -inf
- * has q = 0 (a closed vocabulary entry); a row whose every entry is -inf gives NaN.
+ * means of this library.  A client of weight 0 has no part in any row.  A row with no
+ * client present, or with row_weight 0 (padding: its logits are not looked at), has loss 0
+ * and a zero gradient.  An entry of z at -inf has q = 0 (a closed vocabulary entry); a row
+ * whose every entry is -inf gives NaN.
  * Several clients (or places) may name the same entry; their shares are added in fixed
  * point, so the order of the sum does not matter: in units of 2^-51 of the clients' whole
  * weight, or of N_r in rows whose N_r is below 2^-8 of that. */

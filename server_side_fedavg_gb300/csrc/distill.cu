@@ -174,7 +174,8 @@ struct Lists {
 };
 
 // The largest value over client cl's used places of a row and the sum of the exponentials over
-// it, by one warp; false: the client has nothing for the row.
+// it, by one warp; false: the client has nothing for the row, or no weight (then its values are
+// nothing to the row, whatever they are).
 __device__ __forceinline__ bool list_statistics(const DistillArgs& a, const DistillClient& cl, uint64_t base, float& top,
                                                 float& sum) {
     const int lane = threadIdx.x % 32;
@@ -191,7 +192,7 @@ __device__ __forceinline__ bool list_statistics(const DistillArgs& a, const Dist
         }
     }
     top = warp_max(top);
-    const bool on = __any_sync(~0u, nan) || top > -INFINITY;
+    const bool on = cl.weight > 0.0f && (__any_sync(~0u, nan) || top > -INFINITY);
     sum = 0.0f;
     for (uint32_t i = lane; i < cl.topk; i += 32)
         if (static_cast<uint32_t>(cl.index[base + i]) < a.vocab)
@@ -281,7 +282,7 @@ __device__ __forceinline__ void use_short(const DistillArgs& a, const T* z, uint
         if (used[i]) top = fmaxf(top, s.u[i]);
     }
     top = warp_max(top);
-    const bool on = __any_sync(~0u, nan) || top > -INFINITY;
+    const bool on = cl.weight > 0.0f && (__any_sync(~0u, nan) || top > -INFINITY);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

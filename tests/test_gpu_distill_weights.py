@@ -94,3 +94,24 @@ def test_a_weight_of_no_share_at_all_is_none(work):  # noqa: F811
         assert loss[2] == 0 and not grad[2].any()
         got.append((grad, loss))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("vocab,dtype,topk", [(500, "f32", 8), (500, "bf16", 200), (70001, "f32", 30), (200000, "f32", 16)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_client_of_no_weight_has_no_part_in_a_row(work, vocab, dtype, topk, bad):  # noqa: F811
+    """Whatever its values are: the loss leaves it out, and so does the loss's derivative."""
+    z, index, value, _, rw = make(10, vocab, 3, topk, dtype, seed=4)
+    value[1][::3, 1] = bad
+    weight, without = [2.0, 0.0, 5.0], ([index[0], index[2]], [value[0], value[2]], [2.0, 5.0])
+    for saved, inplace, with_loss in ((False, False, True), (False, True, True), (True, False, False)):
+        lse = torch.logsumexp(z.double() / 1.5, 1).float() if saved else None
+        got = []
+        for i, v, w in ((index, value, weight), without):
+            out = z.clone()
+            loss = torch.zeros(10, device="cuda")
+            fa.fa_distill_grad(work, 10, vocab, out if inplace else z, vocab, dtype,
+                               fa.distill_lists(i, v, [topk] * len(i), w), 1.5, rw, lse, loss if with_loss else None, out, vocab)
+            torch.cuda.synchronize()
+            got.append((out, loss))
+        assert torch.equal(got[0][0], got[1][0])
+        assert ((got[0][1] - got[1][1]).abs() <= 2.0 ** -22 * got[1][1].abs()).all()      # (the clients' order in a sum)
