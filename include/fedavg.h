@@ -638,7 +638,7 @@ typedef struct {
  * whose every entry is -inf gives NaN.
  * Several clients (or places) may name the same entry; their shares are added in fixed
  * point, so the order of the sum does not matter: in units of 2^-51 of the clients' whole
- * weight, or of N_r in rows whose N_r is below 2^-8 of that. */
+ * weight, or of N_r in rows whose N_r is below 2^-12 of that. */
 typedef struct {
     uint32_t size;                    /* sizeof(fa_distill_args) */
     uint32_t n_clients;               /* 1..FA_DISTILL_MAX_CLIENTS */

@@ -25,11 +25,11 @@
 // The shares of the entries are gathered in a hash table in shared memory (entry -> sum of
 // (n_j / total) p_jc, total being all the clients' weight): several clients name the same entry,
 // and integer adds of fixed-point units give the same sum in any order.  Which clients a row has
-// is known after its lists have been read; where they have less than 2^-8 of the total, so that
-// the units would be coarse beside N_r, the shares are taken once more as parts of N_r.  Only calls
-// with such a client have kernels that do (kLight): with the code for it in every kernel, 4096 rows
-// of 32000 from clients of like weights take 118 us instead of 99.  The row is written without
-// the shares first, then the table's entries are written over it.
+// is known after its lists have been read; where they have less than 2^-12 of the total, so that
+// the units would be beyond 2^-40 of N_r, the shares are taken once more as parts of N_r.  Only
+// calls with such a client have kernels that do (kLight): 4096 rows of 32000 bf16 logits with 8
+// lists of 32 in each take 133 us with them and 114 without.  The row is written without the
+// shares first, then the table's entries are written over it.
 #include <algorithm>
 
 #include "distill.cuh"

@@ -10,7 +10,7 @@ namespace fa {
 constexpr int kMaxDistillClients = 16;
 constexpr uint32_t kMaxDistillTopk = 2048;   // summed over the clients
 
-constexpr float kLightest = 256.0f;          // all weight / a client's: above, it is a light one
+constexpr float kLightest = 4096.0f;         // all weight / a client's: above, it is a light one
 
 constexpr unsigned int kErrListIndex = 2u;   // device error bit: a list entry >= vocab
 

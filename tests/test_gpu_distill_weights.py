@@ -55,7 +55,7 @@ def test_rows_that_only_light_clients_sent(work, vocab, dtype, topk, weight):  #
         compare(work, z, index, value, weight, rw, 1.5, dtype, saved, inplace, with_loss)
 
 
-@pytest.mark.parametrize("ratio", [254.0, 255.0, 256.0, 257.0, 300.0])
+@pytest.mark.parametrize("ratio", [254.0, 256.0, 300.0, 4094.0, 4095.0, 4096.0, 4097.0, 5000.0])
 def test_weights_about_the_ratio_at_which_shares_are_taken_again(work, ratio):  # noqa: F811
     z, index, value, _, rw = make(20, 4000, 2, 40, "f32", seed=9)
     index[0][::2] = -1
