@@ -918,10 +918,8 @@ __global__ void __launch_bounds__((kThreads<kBN, kDrain>), 1) product_tc_kernel(
                         tmem_ld16(from + 16, u);
                         if (o.ahead)
                             ok = bar_wait(o.bar + 8 * slot, slot_phase, gone, ctas);
-                        else if (lane == 0 && (o.slots == 1 || a.e.pre))
+                        else if (lane == 0)              // one buffer
                             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        else if (lane == 0)
-                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         __syncwarp();
 #pragma unroll 1
                         for (uint32_t in = 0;;) {
