@@ -540,7 +540,9 @@ typedef enum { FA_ACT_NONE = 0, FA_ACT_RELU = 1, FA_ACT_GELU = 2, FA_ACT_SILU = 
  *
  * Products of bf16 operands are exact and summed in fp32; fp32 operands are each split
  * exactly enough into three bf16 terms (24 bits) and the products down to 2^-24 of the
- * largest are summed in fp32, so an fp32 result keeps fp32 accuracy.  Bias, activation
+ * largest are summed in fp32, so an fp32 result keeps fp32 accuracy.  For bf16 results the
+ * tensor cores' own fp32 sum is used, which truncates: 4.4e-6 off over 4096 terms, growing
+ * with k, against the result's own rounding of up to 2^-8.  Bias, activation
  * and residual are applied to the fp32 sum and the result is rounded once (RNE).  A NaN
  * or an infinity in an operand makes the outputs that depend on it non-finite; where an
  * operand is fp32 these may be NaN where IEEE arithmetic gives an infinity (the terms of
@@ -638,7 +640,10 @@ typedef struct {
  * whose every entry is -inf gives NaN.
  * Several clients (or places) may name the same entry; their shares are added in fixed
  * point, so the order of the sum does not matter: in units of 2^-51 of the clients' whole
- * weight, or of N_r in rows whose N_r is below 2^-12 of that. */
+ * weight, or of N_r in rows whose N_r is below 2^-12 of that.
+ * Arithmetic is fp32: a loss is off by some 2^-22 of its terms' size (z / T, lse, times
+ * T^2), a gradient by some 2^-20 of row_weight * T * (q + share); one from a kept lse also by
+ * 2^-24 |lse| of q, which at low temperatures is the larger. */
 typedef struct {
     uint32_t size;                    /* sizeof(fa_distill_args) */
     uint32_t n_clients;               /* 1..FA_DISTILL_MAX_CLIENTS */

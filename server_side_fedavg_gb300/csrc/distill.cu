@@ -11,10 +11,11 @@
 // a gradient) close behind.  Longer rows are streamed from memory (and L2) twice or three times.
 // Of rows whose statistic is given the slices are independent, and of any number.
 //
-// Measured, back to back (the measured copy rate is 6.80 TB/s): gradient and loss of 4096 rows of
-// 32000 bf16 logits, 8 lists of 32, 98 us, 5.4 TB/s (issue slots 52 % busy, HBM at 4.7 TB/s,
-// the rest of the traffic in L2); gradient of 700 x 131075 bf16 from a kept statistic
-// 77 us, 4.8 TB/s; loss of 1531 x 32003 fp32 37.4 us, 5.3 TB/s; one row of 32000 5.2 us.
+// Measured, back to back (the measured copy rate is 6.77 TB/s): gradient and loss of 4096 rows of
+// 32000 bf16 logits, 8 lists of 32, a tenth of the rows masked and a fifth of the lists empty,
+// 99 us, 5.4 TB/s (issue slots 52 % busy, HBM at 4.7 TB/s, the rest of the traffic in L2), all rows
+// and lists full 114; gradient of 700 x 131075 bf16 from a kept statistic 77 us, 4.8 TB/s; loss
+// of 1531 x 32003 fp32 38 us, 5.2 TB/s; one row of 32000 5.2 us.
 //
 // An exponential is 2^(z c - k) with c = log2(e) / T and k = reference c rounded: one FMA and one
 // ex2.  k's rounding is the same in every term and in the statistic that is formed with the
@@ -240,7 +241,11 @@ __device__ __forceinline__ void read_lists(const DistillArgs& a, const T* z, uin
 
 // Lists of up to 64 places, a warp each: the places are loaded before anything else of the row,
 // and the student's logits there (for the loss) are asked for as soon as the places are known
-// and used after the row's statistics, so that no memory latency of the lists is waited for.
+// and used after the row's statistics, so that no memory latency of the lists is waited for.  More
+// places, or more lists than the CTA has warps (8; 4 for rows of up to 16 KB), are read in place,
+// which is slower: the gradient of 4096 x 32000 bf16 logits takes 114 us with 8 lists of 32 and 176
+// with 9, 160 with 8 lists of 64 and 194 with 8 of 65; of 16384 x 8000 127 us with 4 lists of 32
+// and 171 with 5.
 constexpr int kShortTopk = 64;
 
 struct ShortList {
@@ -435,7 +440,9 @@ __device__ __forceinline__ void write_entries(const DistillArgs& a, T* g, bool s
 }
 
 // ----------------------------------------------------------------- rows held on chip
-constexpr uint32_t kMaxSlice = 66 * 1024;   // bytes of a row that a CTA holds: three CTAs per SM
+// Bytes of a row that a CTA holds: three CTAs per SM.  With 48 KB, four of them: the gradient of 4096
+// x 32000 bf16 149 us (this way 102), of 2048 x 65536 149 (110), of 1531 x 32003 fp32 95 (75).
+constexpr uint32_t kMaxSlice = 66 * 1024;
 constexpr uint32_t kSmallSlice = 16 * 1024; // held by 128 threads, larger ones by 256
 constexpr uint32_t kSharedBytes = 227 * 1024, kSliceCost = 16 * 1024;
 
@@ -1019,6 +1026,9 @@ cudaError_t launch_distill(DistillArgs& a, cudaStream_t stream) {
         while (parts < kMaxCluster && bytes > parts * kMaxSlice) parts *= 2;
     }
     a.joint = !apart && parts > 1;
+    // Rows that a cluster does not hold, and without a statistic, are streamed: of 1024 fp32 rows with
+    // 4 lists of 32, loss and gradient take 100 and 212 us at 135168 entries (held), 174 and 723 at
+    // 135200 (streamed); of 512 bf16 rows 57 and 121 at 270336, 142 and 703 at 270400.
     if (bytes > parts * kMaxSlice || a.rows * parts >= (1ull << 31)) {
         kern = a.dtype ? (grad ? distill_stream_kernel<uint16_t, true> : distill_stream_kernel<uint16_t, false>)
                        : (grad ? distill_stream_kernel<float, true> : distill_stream_kernel<float, false>);

@@ -9,8 +9,8 @@ namespace {
 constexpr int kBlockThreads = 256;
 
 // ----------------------------------------------------------------- tiny products
-// One output per kLanes lanes (1 or 32), any storage order.  Bound by launch and load latency:
-// 4 x 10 x 256 in 3 us, where a tensor-core tile with its operands' pass takes 12.
+// One output per kLanes lanes (1 or 32), any storage order.  Bound by launch and load latency: in a
+// CUDA graph 4 x 10 x 256 bf16 takes 2.4 us (on the tensor cores 3.1).
 template <int kLanes>
 __global__ void __launch_bounds__(kBlockThreads) product_tiny_kernel(const __grid_constant__ ProdArgs p) {
     wait_predecessor();

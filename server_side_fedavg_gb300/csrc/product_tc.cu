@@ -9,9 +9,9 @@
 //
 // A CTA's tile is 128 rows of P (TMEM lanes) by kBN rows of Q (TMEM columns); with kCtas == 2
 // a pair of SMs holds 256 rows of P and each half of the Q rows (cta_group::2), which halves
-// the operand traffic from L2.  Warps 0-7 drain and finish tiles, warp 8 issues TMA loads,
-// warp 9 the MMAs.  TMEM holds two accumulators, so the next tile's (or chunk's) products run
-// while one is drained.
+// the operand traffic from L2.  The first warps (4, 8, or 16 in the 256-column forms) drain and
+// finish tiles, the next issues TMA loads, the one after it the MMAs.  TMEM holds two
+// accumulators, so the next tile's (or chunk's) products run while one is drained.
 //
 // kDrain: for fp32 results.  The tensor core's fp32 accumulation truncates: 4.4e-6 off over 4096
 // terms (relative, 2-norm).  So the accumulator is emptied every 4 blocks of 64 terms into
@@ -26,17 +26,17 @@
 // part into its own shared memory, and each finishes a share of the tile, summing the parts
 // in rank order over distributed shared memory.
 //
-// What bounds it: the MMAs (measured peak 1922 TFLOP/s) and, before those, the operands' way
+// What bounds it: the MMAs (measured peak 1954 TFLOP/s) and, before those, the operands' way
 // from L2 -- a 256 x 256 tile reads 64 KB per 64 terms, 12 TB/s over all SMs -- and the epilogue
-// of tiles with short sums.  Measured, back to back:
-//   4096 x 4864 x 16384 bf16                    361 us  1809 TFLOP/s  (94 %)
-//   4096 x 11008 x 4096 bf16, silu and pre      231 us  1600 TFLOP/s  (83 %; tensor pipe 73 % active)
-//   1024 x 4096 x 32000 bf16 to fp32            187 us  1435 TFLOP/s  (75 %; 128 CTAs have a tile)
-//   32000 x 4096 x 1024 bf16 to fp32            218 us  1231 TFLOP/s  (64 %; a 256 x 256 fp32 tile
+// of tiles with short sums.  Measured, calls queued one after the other:
+//   4096 x 4864 x 16384 bf16                    360 us  1815 TFLOP/s  (93 %; 380 under the power cap)
+//   4096 x 11008 x 4096 bf16, silu and pre      250 us  1480 TFLOP/s  (76 %; tensor pipe 73 % active)
+//   1024 x 4096 x 32000 bf16 to fp32            188 us  1425 TFLOP/s  (73 %; 128 CTAs have a tile)
+//   32000 x 4096 x 1024 bf16 to fp32            218 us  1231 TFLOP/s  (63 %; a 256 x 256 fp32 tile
 //                                               written every 16 blocks, HBM writes 0.52 GB)
-//   2056 x 1024 x 4096 bf16, bias, residual     18.8 us  920 TFLOP/s  (48 %: one wave, 4 us of launch)
+//   2056 x 1024 x 4096 bf16, bias, residual     18.9 us  912 TFLOP/s  (47 %: one wave, 4 us of launch)
 //   1 x 32000 x 4096 bf16                       41 us   6.4 TB/s of weights (94 % of measured)
-//   777 x 4096 x 1024 fp32, bias, gelu          45 us with the pass, 877 TFLOP/s of bf16 products
+//   777 x 4096 x 1024 fp32, bias, gelu          47 us with the pass, 834 TFLOP/s of bf16 products
 #include "product_tc.cuh"
 #include "product_device.cuh"
 
@@ -47,7 +47,8 @@ namespace {
 constexpr int kBK = 64;                    // summed elements per block: 128 bytes, one swizzle row
 // Drain warps: each has the 32 lanes of its quadrant (warp % 4) and a part of the columns.
 // The epilogue is bound by instruction latency, so the pair kernel has 16 of them (with 8, the
-// adapter merge of 4096 x 4096 took 29 us instead of 16).
+// adapter merge of 4096 x 4096 took 29 us instead of 16 when this was chosen; with inputs from
+// HBM it takes 18).
 template <int kBN>
 constexpr int kDrainWarps = kBN == 256 ? 16 : kBN >= 64 ? 8 : 4;
 // Drain warps sharing a quadrant: a block of outputs by TMA is 64 columns wide, so that the

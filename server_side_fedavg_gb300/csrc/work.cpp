@@ -423,8 +423,8 @@ fa_status product_impl(fa_work* w, const fa_product_args& p, cudaStream_t s) {
 
 // Rows per block of the activation's gradient: the number with the least work in the last of the
 // turns that four blocks per SM take, a block's start and end costing as much as some 8 rows.
-// Both gradients of 8192 x 1024 x 512 bf16 with gelu and bias: 47.3 us, always 32 rows 51.4; of
-// 2056 x 4096 x 1024 52.0 and 52.9; of 777 x 4096 x 256 fp32 50.5 and 54.2.
+// In a CUDA graph both gradients of 8192 x 1024 x 512 bf16 with gelu and bias: 48.4 us, always 32
+// rows 52.5; of 2056 x 4096 x 1024 53.2 and 55; of 777 x 4096 x 256 fp32 51.8 and 55.2.
 uint32_t grad_rows(uint32_t m, uint32_t n, uint32_t sms) {
     const uint64_t across = (n + 255) / 256;
     uint64_t best = ~0ull;
