@@ -29,7 +29,7 @@
 // What bounds it: the MMAs (measured peak 1954 TFLOP/s) and, before those, the operands' way
 // from L2 -- a 256 x 256 tile reads 64 KB per 64 terms, 12 TB/s over all SMs -- and the epilogue
 // of tiles with short sums.  Measured, calls queued one after the other:
-//   4096 x 4864 x 16384 bf16                    360 us  1815 TFLOP/s  (93 %; 380 under the power cap)
+//   4096 x 4864 x 16384 bf16                    380 us  1718 TFLOP/s  (88 %; 360 and 93 % in a CUDA graph)
 //   4096 x 11008 x 4096 bf16, silu and pre      250 us  1480 TFLOP/s  (76 %; tensor pipe 73 % active)
 //   1024 x 4096 x 32000 bf16 to fp32            188 us  1425 TFLOP/s  (73 %; 128 CTAs have a tile)
 //   32000 x 4096 x 1024 bf16 to fp32            218 us  1231 TFLOP/s  (63 %; a 256 x 256 fp32 tile
