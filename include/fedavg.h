@@ -669,6 +669,135 @@ typedef struct {
 fa_status fa_distill_loss(fa_work* w, const fa_distill_args* args, void* stream);
 fa_status fa_distill_grad(fa_work* w, const fa_distill_args* args, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Layers of the student beside its products, on the same work handle.
+ *
+ * Rotary positions: pair i of a head, (u, v), becomes
+ *
+ *   scale * (u cos t - v sin t),  scale * (v cos t + u sin t),      t = position * f_i
+ *
+ * The pair is elements (i, i + rotary_dim / 2) of the head, or (2 i, 2 i + 1) with
+ * FA_ROTARY_INTERLEAVED; elements from rotary_dim on are copied (they stay where `out` is the
+ * input itself).  FA_ROTARY_INVERSE takes -t: with the same scale that is the gradient.
+ * Angles are exact to some 2^-24 of a quarter turn at any position up to 2^31 - 1; the pair is
+ * turned in fp32 and rounded once. */
+#define FA_ROTARY_INTERLEAVED 1u
+#define FA_ROTARY_INVERSE     2u
+#define FA_ROTARY_MAX_DIM     512
+
+typedef enum {
+    FA_ROTARY_PLAIN = 0,   /* f_i = base^(-2 i / rotary_dim) */
+    FA_ROTARY_LINEAR = 1,  /* f_i / factor: positions squeezed into the first context */
+    FA_ROTARY_BASE = 2,    /* with base * factor^(rotary_dim / (rotary_dim - 2)): the lowest
+                              frequency is divided by factor, the highest kept */
+    FA_ROTARY_BANDED = 3   /* f_i * (g + (1 - g) / factor), g = clamp((context f_i / 2 pi - low) /
+                              (high - low), 0, 1): pairs that turn `high` times or more over the
+                              first context are kept, those below `low` turns divided */
+} fa_rotary_scaling;
+
+/* The frequencies of a model, once: turns[rotary_dim / 2], each f_i / (2 pi) in units of 2^-64.
+ * base >= 1; factor >= 1 (not read with FA_ROTARY_PLAIN); context, low < high: FA_ROTARY_BANDED
+ * alone.  Host code, no handle.  Errors: FA_ERR_ARG. */
+fa_status fa_rotary_turns(uint32_t rotary_dim, double base, int32_t scaling, double factor, double context,
+                          double low, double high, uint64_t* turns);
+
+/* Strides in elements; element e of head h of token s of batch entry b is at
+ * x[b batch_stride + s token_stride + h head_stride + e].  Strides of a dimension of one are not
+ * used.  Those of an input may be 0 (a shared tensor). */
+typedef struct {
+    const void* x;
+    void* out;                 /* may be x itself, with the same strides */
+    uint32_t heads;            /* 0: this tensor is left out */
+    uint32_t reserved;         /* 0 */
+    uint64_t batch_stride, token_stride, head_stride;
+    uint64_t out_batch_stride, out_token_stride, out_head_stride;
+} fa_rotary_part;
+
+typedef struct {
+    uint32_t size;             /* sizeof(fa_rotary_args) */
+    uint32_t flags;            /* FA_ROTARY_INTERLEAVED | FA_ROTARY_INVERSE */
+    int32_t dtype;
+    uint32_t head_dim;         /* up to 65536, as the heads */
+    uint32_t rotary_dim;       /* even, 2 to head_dim and FA_ROTARY_MAX_DIM */
+    uint32_t reserved;         /* 0 */
+    uint64_t batch, seq;       /* fewer than 2^31 tokens; 0 is a no-op */
+    const uint64_t* turns;     /* [rotary_dim / 2], host memory, read before the call returns */
+    const int32_t* position;   /* [batch, seq]; negative: padding, whose outputs are left as they
+                                  are.  NULL: first + s */
+    int64_t first;             /* >= 0, < 2^62 */
+    double scale;              /* finite; used in fp32 */
+    fa_rotary_part q, k;
+} fa_rotary_args;
+
+/* Errors: FA_ERR_ARG (null or host pointer, unknown flag, scale not finite, overlap),
+ * FA_ERR_DTYPE, FA_ERR_RANGE (sizes, strides, outputs whose own rows overlap), FA_ERR_CUDA. */
+fa_status fa_rotary(fa_work* w, const fa_rotary_args* args, void* stream);
+
+#define FA_NORM_MAX_CHANNELS 8192
+
+/* Group norm with an activation, channels last: of sample i, position s, channel c in group g,
+ *
+ *   xhat = (x - mean[i, g]) * rstd[i, g],   y = act(xhat * gamma[c] + beta[c])
+ *
+ * mean and the variance are over the sample's positions and the group's channels / groups
+ * channels, rstd = 1 / sqrt(variance + eps).  Sums are fp32 of differences from a value of the
+ * same channel, so an offset costs no digits; their order does not depend on the run. */
+typedef struct {
+    uint32_t size;             /* sizeof(fa_group_norm_args) */
+    uint32_t flags;            /* 0 */
+    int32_t dtype;             /* x and y */
+    int32_t dtype_param;       /* gamma and beta */
+    int32_t act;               /* fa_act */
+    uint32_t reserved;         /* 0 */
+    uint64_t n, positions;     /* each < 2^31; 0 is a no-op */
+    uint64_t channels, groups; /* channels: 1 to FA_NORM_MAX_CHANNELS, a multiple of groups */
+    const void* x;
+    uint64_t ldx, step_x;      /* elements from a position to the next, from a sample to the next
+                                  (0: positions * ldx) */
+    void* y;                   /* may be x itself, with the same strides */
+    uint64_t ldy, step_y;
+    const void* gamma;         /* [channels], or NULL for 1 */
+    const void* beta;          /* [channels], or NULL for 0 */
+    double eps;                /* finite, >= 0; used in fp32 */
+    float* mean;               /* [n, groups], for the backward call; or NULL */
+    float* rstd;               /* [n, groups]; or NULL */
+} fa_group_norm_args;
+
+/* Errors: FA_ERR_ARG, FA_ERR_DTYPE, FA_ERR_RANGE (sizes, strides, outputs whose own rows
+ * overlap), FA_ERR_STATE (workspace growth while capturing), FA_ERR_NOMEM, FA_ERR_CUDA. */
+fa_status fa_group_norm(fa_work* w, const fa_group_norm_args* args, void* stream);
+
+/* Gradients of fa_group_norm from dout, x and the kept mean and rstd: with
+ * dz = dout * act'(xhat * gamma + beta),
+ *   d_beta[c] = sum dz,   d_gamma[c] = sum dz * xhat   (over samples and positions),
+ *   dx = rstd * (gamma dz - m1 - xhat * m2),  m1 and m2 the means of gamma dz and gamma dz xhat
+ *                                             over the sample's group. */
+typedef struct {
+    uint32_t size;             /* sizeof(fa_group_norm_backward_args) */
+    uint32_t flags;            /* 0 */
+    int32_t dtype;             /* x, dout and dx */
+    int32_t dtype_param;       /* gamma, beta, d_gamma and d_beta */
+    int32_t act;
+    uint32_t reserved;         /* 0 */
+    uint64_t n, positions;     /* 0: zero gradients of gamma and beta */
+    uint64_t channels, groups;
+    const void* x;
+    uint64_t ldx, step_x;
+    const void* dout;
+    uint64_t ldd, step_d;
+    const void* gamma;
+    const void* beta;
+    const float* mean;
+    const float* rstd;
+    void* dx;                  /* may be x or dout itself, with the same strides */
+    uint64_t lddx, step_dx;
+    void* d_gamma;             /* [channels], or NULL */
+    void* d_beta;              /* [channels], or NULL */
+} fa_group_norm_backward_args;
+
+/* Errors: as fa_group_norm. */
+fa_status fa_group_norm_backward(fa_work* w, const fa_group_norm_backward_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

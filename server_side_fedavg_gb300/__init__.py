@@ -45,10 +45,22 @@ FA_TRANS_A = 1
 FA_TRANS_B = 2
 FA_DISTILL_MAX_CLIENTS = 16
 FA_DISTILL_MAX_TOPK = 2048
+FA_ROTARY_INTERLEAVED = 1
+FA_ROTARY_INVERSE = 2
+FA_ROTARY_MAX_DIM = 512
+FA_ROTARY_PLAIN = 0
+FA_ROTARY_LINEAR = 1
+FA_ROTARY_BASE = 2
+FA_ROTARY_BANDED = 3
+FA_NORM_MAX_CHANNELS = 8192
 
 ACTS = {"none": FA_ACT_NONE, "relu": FA_ACT_RELU, "gelu": FA_ACT_GELU, "silu": FA_ACT_SILU,
         FA_ACT_NONE: FA_ACT_NONE, FA_ACT_RELU: FA_ACT_RELU, FA_ACT_GELU: FA_ACT_GELU,
         FA_ACT_SILU: FA_ACT_SILU}
+
+SCALINGS = {"none": FA_ROTARY_PLAIN, "linear": FA_ROTARY_LINEAR, "base": FA_ROTARY_BASE, "banded": FA_ROTARY_BANDED,
+            FA_ROTARY_PLAIN: FA_ROTARY_PLAIN, FA_ROTARY_LINEAR: FA_ROTARY_LINEAR, FA_ROTARY_BASE: FA_ROTARY_BASE,
+            FA_ROTARY_BANDED: FA_ROTARY_BANDED}
 
 DTYPES = {"f32": FA_F32, "bf16": FA_BF16, FA_F32: FA_F32, FA_BF16: FA_BF16}
 
@@ -122,6 +134,44 @@ class fa_distill_args(ctypes.Structure):
                 ("ldg", ctypes.c_uint64)]
 
 
+class fa_rotary_part(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("batch_stride", ctypes.c_uint64),
+                ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64),
+                ("out_batch_stride", ctypes.c_uint64), ("out_token_stride", ctypes.c_uint64),
+                ("out_head_stride", ctypes.c_uint64)]
+
+
+class fa_rotary_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("dtype", ctypes.c_int32),
+                ("head_dim", ctypes.c_uint32), ("rotary_dim", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("batch", ctypes.c_uint64), ("seq", ctypes.c_uint64), ("turns", ctypes.c_void_p),
+                ("position", ctypes.c_void_p), ("first", ctypes.c_int64), ("scale", ctypes.c_double),
+                ("q", fa_rotary_part), ("k", fa_rotary_part)]
+
+
+class fa_group_norm_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("dtype", ctypes.c_int32),
+                ("dtype_param", ctypes.c_int32), ("act", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("n", ctypes.c_uint64), ("positions", ctypes.c_uint64), ("channels", ctypes.c_uint64),
+                ("groups", ctypes.c_uint64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_uint64),
+                ("step_x", ctypes.c_uint64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_uint64),
+                ("step_y", ctypes.c_uint64), ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+                ("eps", ctypes.c_double), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class fa_group_norm_backward_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("dtype", ctypes.c_int32),
+                ("dtype_param", ctypes.c_int32), ("act", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("n", ctypes.c_uint64), ("positions", ctypes.c_uint64), ("channels", ctypes.c_uint64),
+                ("groups", ctypes.c_uint64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_uint64),
+                ("step_x", ctypes.c_uint64), ("dout", ctypes.c_void_p), ("ldd", ctypes.c_uint64),
+                ("step_d", ctypes.c_uint64), ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_uint64), ("step_dx", ctypes.c_uint64), ("d_gamma", ctypes.c_void_p),
+                ("d_beta", ctypes.c_void_p)]
+
+
 class FedAvgError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
@@ -177,6 +227,11 @@ def lib():
         L.fa_work_last_error.restype = ctypes.c_char_p
         L.fa_product.argtypes = [vp, ctypes.POINTER(fa_product_args), vp]
         L.fa_product_backward.argtypes = [vp, ctypes.POINTER(fa_product_backward_args), vp]
+        L.fa_rotary_turns.argtypes = [ctypes.c_uint32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_double,
+                                      ctypes.c_double, ctypes.c_double, ctypes.POINTER(ctypes.c_uint64)]
+        L.fa_rotary.argtypes = [vp, ctypes.POINTER(fa_rotary_args), vp]
+        L.fa_group_norm.argtypes = [vp, ctypes.POINTER(fa_group_norm_args), vp]
+        L.fa_group_norm_backward.argtypes = [vp, ctypes.POINTER(fa_group_norm_backward_args), vp]
         L.fa_distill_loss.argtypes = [vp, ctypes.POINTER(fa_distill_args), vp]
         L.fa_distill_grad.argtypes = [vp, ctypes.POINTER(fa_distill_args), vp]
         L.fa_strerror.argtypes = [i32]
@@ -532,3 +587,67 @@ def fa_distill_grad(work, rows, vocab, logits, ld, dtype, lists, temperature, ro
     lse: kept by fa_distill_loss, or None to compute it here; loss: written unless None."""
     args = _distill_args(rows, vocab, logits, ld, dtype, lists, temperature, row_weight, loss, lse, grad, ldg)
     _check_work(lib().fa_distill_grad(work, args, _stream(stream)), work)
+
+
+# ---------------------------------------------------------------- layers of the student
+def rotary_turns(rotary_dim, base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0, high=32.0):
+    """A model's rotary frequencies for fa_rotary, made once (fa_rotary_turns): base^(-2 i /
+    rotary_dim) per pair, for long contexts divided by `factor` ("linear"), taken from a larger
+    base ("base"), or divided where a pair turns fewer than low..high times over the first
+    `context` positions ("banded")."""
+    turns = (ctypes.c_uint64 * max(1, rotary_dim // 2))()
+    _check(lib().fa_rotary_turns(rotary_dim, base, SCALINGS[scaling], factor, context, low, high, turns))
+    return turns
+
+
+def _rotary_part(x, heads, out, strides, out_strides, seq, head_dim):
+    own = (seq * heads * head_dim, heads * head_dim, head_dim)
+    strides = own if strides is None else strides
+    return fa_rotary_part(_ptr(x), _ptr(out), heads, 0, *strides,
+                          *(strides if out_strides is None and out is x else own if out_strides is None else out_strides))
+
+
+def fa_rotary(work, batch, seq, head_dim, turns, dtype, q, q_heads, q_out, k=None, k_heads=0, k_out=None,
+              position=None, first=0, layout="half", inverse=False, scale=1.0, q_strides=None,
+              q_out_strides=None, k_strides=None, k_out_strides=None, stream=None):
+    """Rotary positions of q and k, [batch, seq, heads, head_dim] unless strides = (batch, token,
+    head) in elements are given.  turns: a rotary_turns result; its length sets rotary_dim.
+    position: int32 [batch, seq], negative in padding (left as it is), or None for first + s.
+    layout "half" pairs (i, i + rotary_dim / 2), "interleaved" (2 i, 2 i + 1).  inverse: the
+    gradient's direction.  An output may be its input itself."""
+    _check_types((position,), ("int32",), _position_seen, "position is int32")
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout is 'half' or 'interleaved', not {layout!r}")
+    args = fa_rotary_args(
+        ctypes.sizeof(fa_rotary_args), (layout == "interleaved") | bool(inverse) << 1, DTYPES[dtype], head_dim,
+        2 * len(turns), 0, batch, seq, ctypes.addressof(turns), _ptr(position), first, scale,
+        _rotary_part(q, q_heads, q_out, q_strides, q_out_strides, seq, head_dim),
+        _rotary_part(k, k_heads, k_out, k_strides, k_out_strides, seq, head_dim))
+    _check_work(lib().fa_rotary(work, args, _stream(stream)), work)
+
+
+_position_seen = {None}
+
+
+def fa_group_norm(work, n, positions, channels, groups, x, y, dtype, gamma=None, beta=None, dtype_param="f32",
+                  act="none", eps=1e-5, mean=None, rstd=None, ldx=None, step_x=0, ldy=None, step_y=0, stream=None):
+    """Group norm with an activation of x [n, positions, channels] (channels last), to y, which may
+    be x.  mean and rstd [n, groups] fp32 receive the statistics for the backward call."""
+    args = fa_group_norm_args(
+        ctypes.sizeof(fa_group_norm_args), 0, DTYPES[dtype], DTYPES[dtype_param], ACTS[act], 0, n, positions, channels,
+        groups, _ptr(x), channels if ldx is None else ldx, step_x, _ptr(y), channels if ldy is None else ldy, step_y,
+        _ptr(gamma), _ptr(beta), eps, _ptr(mean), _ptr(rstd))
+    _check_work(lib().fa_group_norm(work, args, _stream(stream)), work)
+
+
+def fa_group_norm_backward(work, n, positions, channels, groups, x, dout, dx, dtype, gamma, beta, dtype_param, mean, rstd,
+                           act="none", d_gamma=None, d_beta=None, ldx=None, step_x=0, ldd=None, step_d=0, lddx=None,
+                           step_dx=0, stream=None):
+    """Gradients of fa_group_norm from dout, x and the kept mean and rstd: dx (which may be x or
+    dout), and d_gamma and d_beta [channels] unless None."""
+    args = fa_group_norm_backward_args(
+        ctypes.sizeof(fa_group_norm_backward_args), 0, DTYPES[dtype], DTYPES[dtype_param], ACTS[act], 0, n, positions,
+        channels, groups, _ptr(x), channels if ldx is None else ldx, step_x, _ptr(dout), channels if ldd is None else ldd,
+        step_d, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd), _ptr(dx), channels if lddx is None else lddx, step_dx,
+        _ptr(d_gamma), _ptr(d_beta))
+    _check_work(lib().fa_group_norm_backward(work, args, _stream(stream)), work)

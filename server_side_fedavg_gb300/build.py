@@ -18,7 +18,8 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["accumulate.cu", "reduce.cu", "gather.cu", "finalize.cu", "noalloc.cu", "fedavg.cpp",
            "ledger.cpp", "partition.cpp", "gather_plan.cpp", "product_plain.cu", "product_prep.cu", "product_tc.cu",
-           "distill.cu", "work.cpp"]
+           "distill.cu", "work.cpp",
+           "rotary.cu", "group_norm.cu", "layers.cpp"]
 
 
 def _common():

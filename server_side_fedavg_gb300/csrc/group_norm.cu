@@ -1,0 +1,552 @@
+// Group norm with an activation, channels last, and its gradients.
+//
+//   xhat = (x - mean) * rstd,  z = xhat * gamma + beta,  y = act(z)
+//   dz = dout * act'(z),  d_beta = sum dz,  d_gamma = sum dz xhat
+//   dx = rstd * (gamma dz - mean_g(gamma dz) - xhat * mean_g(gamma dz xhat))
+//
+// mean and rstd are over a sample's positions and a group's channels, mean_g likewise.
+//
+// Two passes over the data: the statistics, then the result.  A thread keeps V channels (one
+// vector) and walks down positions, so that nothing of a channel is fetched twice; a CTA has a
+// run of a sample's positions.  The second pass walks its run backwards: what the first pass read
+// last is still in L2.  A channel's sums are taken of x less the channel's first value in the
+// sample, and means are kept as differences from the group's first such value until the end, so
+// that an offset far larger than the spread costs no digits; a run's channels, and then the runs,
+// are joined as (mean, sum of squares about it) pairs, in a fixed order.
+//
+// What bounds it: HBM, x read once or twice and the result written once.
+#include <algorithm>
+
+#include "group_norm.cuh"
+#include "product_device.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr uint32_t kNormThreads = 256, kNormWarps = kNormThreads / 32;
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T e[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[V]) {
+    const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if constexpr (sizeof(T) == 2)
+            x[i] = __uint_as_float(static_cast<uint32_t>(q.e[i]) << 16);
+        else
+            x[i] = q.e[i];
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
+    Vec<T, V> q;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if constexpr (sizeof(T) == 2)
+            q.e[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+        else
+            q.e[i] = x[i];
+    *reinterpret_cast<Vec<T, V>*>(p) = q;
+}
+
+template <int V>
+__device__ __forceinline__ void times_act_grad(int act, float (&d)[V], const float (&z)[V]) {
+    if (act == kActRelu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= act_grad(kActRelu, z[i]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= act_grad(kActGelu, z[i]);
+    } else if (act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= act_grad(kActSilu, z[i]);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+// A CTA's columns in turn: `width` vectors by `tall` positions at a time.
+struct Tile {
+    uint32_t width, tall, col, row;
+    bool on;
+    __device__ __forceinline__ Tile(uint32_t vectors, uint32_t c0)
+        : width(min(vectors - c0, kNormThreads)), tall(kNormThreads / width), col(threadIdx.x % width),
+          row(threadIdx.x / width), on(row < tall) {}
+};
+
+// Sums over a tile's positions: s[i][j] of every thread of a column end up in its first one.
+template <int N, int V>
+__device__ __forceinline__ void sum_rows(float (&s)[N][V], float* red, const Tile& t) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) red[(i * V + j) * kNormThreads + threadIdx.x] = s[i][j];
+    __syncthreads();
+    for (uint32_t left = t.tall; left > 1;) {
+        const uint32_t half = (left + 1) / 2;
+        if (t.row < left - half)
+#pragma unroll
+            for (int k = 0; k < N * V; ++k) {
+                s[k / V][k % V] += red[k * kNormThreads + threadIdx.x + half * t.width];
+                red[k * kNormThreads + threadIdx.x] = s[k / V][k % V];
+            }
+        left = half;
+        __syncthreads();
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
+    return static_cast<const T*>(t.p) + sample * t.step;
+}
+
+// ----------------------------------------------------------------- forward
+// part[sample][chunk][group] = (mean, sum of squares about it) over the chunk's positions, the mean
+// less ref[sample][group], the group's first value.
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormThreads) norm_stat_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ float sm[];
+    float *mean = sm, *sq = sm + a.channels, *red = sm + 2 * a.channels;
+    wait_predecessor();
+    const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
+    const float count = static_cast<float>(r1 - r0);
+    for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
+        const T* x = at<T, V>(a.x, sample);
+        for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
+            const Tile t(vectors, c0);
+            const uint32_t c = (c0 + t.col) * V;
+            float s[2][V] = {}, from[V] = {};
+            if (t.on) {
+                load_vec<T, V>(x + c, from);
+                constexpr uint32_t kU = 4;
+                uint32_t r = r0 + t.row;
+                for (; r + (kU - 1) * t.tall < r1; r += kU * t.tall) {
+                    float v[kU][V];
+#pragma unroll
+                    for (uint32_t u = 0; u < kU; ++u) load_vec<T, V>(x + (r + u * t.tall) * a.x.ld + c, v[u]);
+#pragma unroll
+                    for (uint32_t u = 0; u < kU; ++u)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float d = v[u][i] - from[i];
+                            s[0][i] += d;
+                            s[1][i] = fmaf(d, d, s[1][i]);
+                        }
+                }
+                for (; r < r1; r += t.tall) {
+                    float v[V];
+                    load_vec<T, V>(x + r * a.x.ld + c, v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float d = v[i] - from[i];
+                        s[0][i] += d;
+                        s[1][i] = fmaf(d, d, s[1][i]);
+                    }
+                }
+            }
+            sum_rows<2, V>(s, red, t);
+            if (t.row == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float m = s[0][i] / count;
+                    mean[c + i] = m;
+                    sq[c + i] = fmaxf(s[1][i] - s[0][i] * m, 0.0f);
+                }
+            __syncthreads();
+        }
+        for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+            float m = 0.0f, q = 0.0f, ref;
+            load_vec<T, 1>(x + g * per, reinterpret_cast<float(&)[1]>(ref));
+            for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
+                float from[1];
+                load_vec<T, 1>(x + c, from);
+                mean[c] += from[0] - ref;
+                m += mean[c];
+            }
+            m = warp_sum(m) / static_cast<float>(per);
+            for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
+                const float d = mean[c] - m;
+                q += fmaf(count * d, d, sq[c]);
+            }
+            q = warp_sum(q);
+            if (lane == 0) {
+                a.part[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float2(m, q);
+                if (blockIdx.x == 0) a.ref[static_cast<uint64_t>(sample) * a.groups + g] = ref;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// A sample's mean (less the reference) and 1 / sqrt(variance + eps) per group, from its chunks' parts, into shared memory.
+__device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, float* mean, float* rstd) {
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, per = a.channels / a.groups;
+    const float all = static_cast<float>(a.positions);
+    for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+        const float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
+        float m = 0.0f, q = 0.0f;
+        for (uint32_t i = lane; i < a.chunks; i += 32) {
+            const float rows = static_cast<float>(min(a.rows, a.positions - i * a.rows));
+            m = fmaf(part[static_cast<uint64_t>(i) * a.groups].x, rows, m);
+        }
+        m = warp_sum(m) / all;
+        for (uint32_t i = lane; i < a.chunks; i += 32) {
+            const float2 p = part[static_cast<uint64_t>(i) * a.groups];
+            const float rows = static_cast<float>(min(a.rows, a.positions - i * a.rows)), d = p.x - m;
+            q += fmaf(rows * static_cast<float>(per) * d, d, p.y);
+        }
+        q = warp_sum(q) / (all * static_cast<float>(per));
+        if (lane == 0) {
+            mean[g] = m;
+            rstd[g] = 1.0f / sqrtf(q + a.eps);
+        }
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ float sm[];
+    float *mean = sm, *rstd = sm + a.groups, *ref = sm + 2 * a.groups;
+    wait_predecessor();
+    const uint32_t vectors = a.channels / V, per = a.channels / a.groups;
+    const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
+    const int act = a.act;
+    for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
+        const uint64_t first = static_cast<uint64_t>(sample) * a.groups;
+        for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) ref[g] = a.ref[first + g];
+        join_chunks(a, sample, mean, rstd);
+        __syncthreads();
+        if (blockIdx.x == 0 && a.mean_out)
+            for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.mean_out[first + g] = ref[g] + mean[g];
+        if (blockIdx.x == 0 && a.rstd_out)
+            for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.rstd_out[first + g] = rstd[g];
+        const T* x = at<T, V>(a.x, sample);
+        T* y = const_cast<T*>(at<T, V>(a.out, sample));
+        for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
+            const Tile t(vectors, c0);
+            const uint32_t c = (c0 + t.col) * V;
+            float from[V], m[V], scale[V], shift[V];
+            if (!t.on) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t g = (c + i) / per;
+                from[i] = ref[g];
+                m[i] = mean[g];
+                scale[i] = rstd[g] * (a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f);
+                shift[i] = a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f;
+            }
+            constexpr uint32_t kU = 4;
+            const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
+            for (uint32_t left = mine; left > 0;) {
+                const uint32_t now = left >= kU ? kU : 1;
+                left -= now;
+                float v[kU][V];
+                const uint32_t r = r0 + t.row + left * t.tall;
+#pragma unroll
+                for (uint32_t u = 0; u < kU; ++u)
+                    if (u < now) load_vec<T, V>(x + (r + u * t.tall) * a.x.ld + c, v[u]);
+#pragma unroll
+                for (uint32_t u = 0; u < kU; ++u) {
+                    if (u >= now) break;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[u][i] = fmaf(v[u][i] - from[i] - m[i], scale[i], shift[i]);
+                    activate(act, v[u]);
+                    store_vec<T, V>(y + (r + u * t.tall) * a.out.ld + c, v[u]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ----------------------------------------------------------------- backward
+// What a thread keeps of its channels.
+template <int V>
+struct Channels {
+    float mean[V], rstd[V], gamma[V], beta[V];
+    __device__ __forceinline__ Channels(const NormArgs& a, uint32_t sample, uint32_t c) {
+        const uint32_t per = a.channels / a.groups;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint64_t g = static_cast<uint64_t>(sample) * a.groups + (c + i) / per;
+            mean[i] = a.mean[g];
+            rstd[i] = a.rstd[g];
+            gamma[i] = a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f;
+            beta[i] = a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f;
+        }
+    }
+    // x to xhat, d to dz
+    __device__ __forceinline__ void step(int act, float (&x)[V], float (&d)[V]) const {
+        float z[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = (x[i] - mean[i]) * rstd[i];
+            z[i] = fmaf(x[i], gamma[i], beta[i]);
+        }
+        times_act_grad(act, d, z);
+    }
+};
+
+// part[sample][chunk][group] = sums of gamma dz and gamma dz xhat over the chunk;
+// cpart[its CTA][channel] = sums of dz and dz xhat over the CTA's chunks.
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ float sm[];
+    float *s0 = sm, *s1 = sm + a.channels, *t0 = sm + 2 * a.channels, *t1 = sm + 3 * a.channels, *red = sm + 4 * a.channels;
+    wait_predecessor();
+    const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
+    const int act = a.act;
+    for (uint32_t c = threadIdx.x; c < a.channels; c += kNormThreads) t0[c] = t1[c] = 0.0f;
+    __syncthreads();
+    for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
+        const T *x = at<T, V>(a.x, sample), *dout = at<T, V>(a.dout, sample);
+        for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
+            const Tile t(vectors, c0);
+            const uint32_t c = (c0 + t.col) * V;
+            float s[2][V] = {};
+            if (t.on) {
+                const Channels<V> ch(a, sample, c);
+                constexpr uint32_t kU = 2;
+                uint32_t r = r0 + t.row;
+                for (; r < r1; r += kU * t.tall) {
+                    float v[kU][V], d[kU][V];
+#pragma unroll
+                    for (uint32_t u = 0; u < kU; ++u) {
+                        const uint32_t q = r + u * t.tall;
+                        if (q >= r1) break;
+                        load_vec<T, V>(x + q * a.x.ld + c, v[u]);
+                        load_vec<T, V>(dout + q * a.dout.ld + c, d[u]);
+                    }
+#pragma unroll
+                    for (uint32_t u = 0; u < kU; ++u) {
+                        if (r + u * t.tall >= r1) break;
+                        ch.step(act, v[u], d[u]);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            s[0][i] += d[u][i];
+                            s[1][i] = fmaf(d[u][i], v[u][i], s[1][i]);
+                        }
+                    }
+                }
+            }
+            sum_rows<2, V>(s, red, t);
+            if (t.row == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float g = a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f;
+                    s0[c + i] = g * s[0][i];
+                    s1[c + i] = g * s[1][i];
+                    t0[c + i] += s[0][i];
+                    t1[c + i] += s[1][i];
+                }
+            __syncthreads();
+        }
+        for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+            float p = 0.0f, q = 0.0f;
+            for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
+                p += s0[c];
+                q += s1[c];
+            }
+            p = warp_sum(p);
+            q = warp_sum(q);
+            if (lane == 0) a.part[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float2(p, q);
+        }
+        __syncthreads();
+    }
+    if (a.cpart) {
+        float2* to = a.cpart + (static_cast<uint64_t>(a.row0 + blockIdx.y) * a.chunks + blockIdx.x) * a.channels;
+        for (uint32_t c = threadIdx.x; c < a.channels; c += kNormThreads) to[c] = make_float2(t0[c], t1[c]);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ float sm[];
+    float *c1 = sm, *c2 = sm + a.groups;
+    wait_predecessor();
+    const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
+    const int act = a.act;
+    const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(per));
+    for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
+        for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+            const float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
+            float p = 0.0f, q = 0.0f;
+            for (uint32_t i = lane; i < a.chunks; i += 32) {
+                const float2 v = part[static_cast<uint64_t>(i) * a.groups];
+                p += v.x;
+                q += v.y;
+            }
+            p = warp_sum(p);
+            q = warp_sum(q);
+            if (lane == 0) {
+                c1[g] = p * inv;
+                c2[g] = q * inv;
+            }
+        }
+        __syncthreads();
+        const T *x = at<T, V>(a.x, sample), *dout = at<T, V>(a.dout, sample);
+        T* dx = const_cast<T*>(at<T, V>(a.out, sample));
+        for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
+            const Tile t(vectors, c0);
+            const uint32_t c = (c0 + t.col) * V;
+            if (!t.on) continue;
+            const Channels<V> ch(a, sample, c);
+            float k1[V], k2[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                k1[i] = c1[(c + i) / per];
+                k2[i] = c2[(c + i) / per];
+            }
+            const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
+            constexpr uint32_t kU = 2;
+            for (uint32_t left = mine; left > 0;) {
+                const uint32_t now = left >= kU ? kU : 1;
+                left -= now;
+                float v[kU][V], d[kU][V];
+                const uint32_t r = r0 + t.row + left * t.tall;
+#pragma unroll
+                for (uint32_t u = 0; u < kU; ++u)
+                    if (u < now) {
+                        load_vec<T, V>(x + (r + u * t.tall) * a.x.ld + c, v[u]);
+                        load_vec<T, V>(dout + (r + u * t.tall) * a.dout.ld + c, d[u]);
+                    }
+#pragma unroll
+                for (uint32_t u = 0; u < kU; ++u) {
+                    if (u >= now) break;
+                    ch.step(act, v[u], d[u]);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        d[u][i] = ch.rstd[i] * (fmaf(d[u][i], ch.gamma[i], -k1[i]) - v[u][i] * k2[i]);
+                    store_vec<T, V>(dx + (r + u * t.tall) * a.out.ld + c, d[u]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// The parameters' gradients: columns of cpart summed in row order, eight strands of rows each.
+__global__ void __launch_bounds__(256) norm_param_kernel(const float2* part, uint32_t rows, uint32_t channels, void* d_gamma,
+                                                         void* d_beta, int dtype) {
+    __shared__ float2 sums[8][32];
+    wait_predecessor();
+    const uint32_t lane = threadIdx.x % 32, strand = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (c < channels)
+#pragma unroll 8
+        for (uint32_t r = strand; r < rows; r += 8) {
+            const float2 v = part[static_cast<uint64_t>(r) * channels + c];
+            s.x += v.x;
+            s.y += v.y;
+        }
+    sums[strand][lane] = s;
+    __syncthreads();
+    if (strand > 0 || c >= channels) return;
+    for (int w = 1; w < 8; ++w) {
+        s.x += sums[w][lane].x;
+        s.y += sums[w][lane].y;
+    }
+    if (d_beta) put(d_beta, c, dtype, s.x);
+    if (d_gamma) put(d_gamma, c, dtype, s.y);
+}
+
+using Kernel = void (*)(NormArgs);
+struct Set {
+    Kernel stat, apply, grad_stat, grad;
+};
+template <typename T, int V>
+constexpr Set set_of() {
+    return {norm_stat_kernel<T, V>, norm_apply_kernel<T, V>, norm_grad_stat_kernel<T, V>, norm_grad_kernel<T, V>};
+}
+
+// The longest vectors that the channels and every address allow.
+uint32_t vector_of(const NormArgs& a, bool backward) {
+    const uint32_t size = a.dtype ? 2 : 4;
+    const auto ok = [&](const NormTensor& t, uint32_t v) {
+        return reinterpret_cast<uintptr_t>(t.p) % (v * size) == 0 && t.ld % v == 0 && (a.n == 1 || t.step % v == 0);
+    };
+    for (uint32_t v = 16 / size; v > 1; v = v == 8 ? 2 : v / 2)
+        if (a.channels % v == 0 && ok(a.x, v) && ok(a.out, v) && (!backward || ok(a.dout, v))) return v;
+    return 1;
+}
+
+const Set& kernels(const NormArgs& a, uint32_t v) {
+    static const Set sets[2][3] = {{set_of<float, 1>(), set_of<float, 2>(), set_of<float, 4>()},
+                                   {set_of<uint16_t, 1>(), set_of<uint16_t, 2>(), set_of<uint16_t, 8>()}};
+    return sets[a.dtype][v == 1 ? 0 : v == 2 ? 1 : 2];
+}
+
+cudaError_t launch_one(Kernel k, const NormArgs& a, uint32_t smem, cudaStream_t stream) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.chunks, std::min(a.across, a.last - a.first));
+    cfg.blockDim = dim3(kNormThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+cudaError_t passes(NormArgs a, bool backward, cudaStream_t stream, unsigned* launches) {
+    const uint32_t v = vector_of(a, backward), red = 2 * v * kNormThreads * 4;
+    const Set& k = kernels(a, v);
+    cudaError_t e = cudaSuccess;
+    const uint32_t n = a.n;
+    a.row0 = 0;
+    for (a.first = 0; a.first < n && e == cudaSuccess; a.first = a.last) {
+        a.last = a.first + std::min(n - a.first, a.batch);
+        e = launch_one(backward ? k.grad_stat : k.stat, a, (backward ? 16 : 8) * a.channels + red, stream);
+        if (e == cudaSuccess) e = launch_one(backward ? k.grad : k.apply, a, (backward ? 8 : 12) * a.groups, stream);
+        *launches += 2;
+        a.row0 += a.across;
+    }
+    return e;
+}
+
+}  // namespace
+
+void plan_norm(NormArgs& a, bool backward, uint32_t sms) {
+    // Samples per pair of launches: as many as L2 holds for the second pass (64 MB of its 129), one at
+    // least; and four CTAs per SM over all of these.
+    const uint64_t sample = static_cast<uint64_t>(a.positions) * a.channels * (a.dtype ? 2 : 4) * (backward ? 2 : 1);
+    a.batch = static_cast<uint32_t>(std::min<uint64_t>(a.n, std::max<uint64_t>(1, (64ull << 20) / sample)));
+    a.across = std::min(a.batch, 4 * sms);
+    const uint32_t v = vector_of(a, backward), vectors = std::min(a.channels / v, kNormThreads), tall = kNormThreads / vectors;
+    const uint64_t want = std::max(1u, 4 * sms / std::max(1u, a.across)), least = 4ull * tall;
+    uint64_t rows = (a.positions + want - 1) / want;
+    rows = std::max((rows + tall - 1) / tall * tall, least);
+    a.rows = static_cast<uint32_t>(std::min<uint64_t>(rows, a.positions));
+    a.chunks = (a.positions + a.rows - 1) / a.rows;
+}
+
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream, unsigned* launches) { return passes(a, false, stream, launches); }
+
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream, unsigned* launches) {
+    cudaError_t e = a.n && a.positions ? passes(a, true, stream, launches) : cudaSuccess;
+    if (e != cudaSuccess || !(a.d_gamma || a.d_beta)) return e;
+    ++*launches;
+    return launch_next(norm_param_kernel, dim3((a.channels + 31) / 32), 256, stream, a.cpart,
+                       a.n && a.positions ? static_cast<uint32_t>(norm_rows(a) * a.chunks) : 0u, a.channels, a.d_gamma, a.d_beta, a.param_dtype);
+}
+
+}  // namespace fa

@@ -1,0 +1,44 @@
+// Group norm with an activation, channels last: launch interface (internal to the library).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace fa {
+
+constexpr uint32_t kNormMaxChannels = 8192;
+
+// A tensor [n][positions][channels]: positions `ld` elements apart, samples `step`.
+struct NormTensor {
+    const void* p;
+    uint64_t ld, step;
+};
+
+struct NormArgs {
+    NormTensor x, dout, out;       // out: y, or the gradient of x
+    const void *gamma, *beta;      // of param_dtype, or nullptr (1 and 0)
+    const float *mean, *rstd;      // backward: [n][groups]
+    float *mean_out, *rstd_out;    // forward, or nullptr
+    void *d_gamma, *d_beta;        // backward, of param_dtype, or nullptr
+    float* ref;                    // forward: [n][groups]
+    float2* part;                  // [n][chunks][groups] of the statistics' partial results
+    float2* cpart;                 // [norm_rows * chunks][channels] of the parameters' gradients, or nullptr
+    uint32_t n, positions, channels, groups;
+    uint32_t rows, chunks;         // positions per CTA, and CTAs of a sample
+    uint32_t batch, across;        // samples per pair of launches, and of these at work at one time
+    uint32_t first, last, row0;    // samples of this launch, and its first row of across in cpart
+    int dtype, param_dtype, act;
+    float eps;
+};
+
+// rows, chunks, batch and across for these sizes; the workspace of `part` and `cpart` follows from them.
+void plan_norm(NormArgs& a, bool backward, uint32_t sms);
+// Rows of `across` over all launches.
+inline uint64_t norm_rows(const NormArgs& a) {
+    const uint64_t whole = (a.n - 1) / a.batch, rest = a.n - whole * a.batch;
+    return whole * a.across + (rest < a.across ? rest : a.across);
+}
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream, unsigned* launches);
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream, unsigned* launches);
+
+}  // namespace fa

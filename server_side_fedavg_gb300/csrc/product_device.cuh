@@ -81,6 +81,21 @@ __device__ __forceinline__ float act_grad(int act, float z) {
     return 1.0f;
 }
 
+// act(v) of several values, the choice made once.
+template <int kN>
+__device__ __forceinline__ void activate(int act, float (&v)[kN]) {
+    if (act == kActRelu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActRelu, v[i]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActGelu, v[i]);
+    } else if (act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActSilu, v[i]);
+    }
+}
+
 // One output element from its fp32 sum: bias, activation and residual in fp32, one
 // rounding at the store.
 __device__ __forceinline__ void finish_one(const ProdEpilogue& e, float sum, uint64_t row, uint32_t col) {

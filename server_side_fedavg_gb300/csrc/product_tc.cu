@@ -363,20 +363,6 @@ __device__ __forceinline__ void store_row(uint32_t at, uint32_t piece0, const fl
     }
 }
 
-template <int kN>
-__device__ __forceinline__ void activate(int act, float (&v)[kN]) {
-    if (act == kActRelu) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActRelu, v[i]);
-    } else if (act == kActGelu) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActGelu, v[i]);
-    } else if (act == kActSilu) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = act_fwd(kActSilu, v[i]);
-    }
-}
-
 __device__ __forceinline__ void finish_row(const TcArgs& a, float (&v)[16], uint32_t bias, uint32_t out, uint32_t piece0,
                                            uint32_t row, uint32_t col, bool res_here, bool pre) {
     const uint32_t lane = threadIdx.x % 32;
