@@ -494,7 +494,7 @@ const char* fa_last_error(const fa_ctx* ctx);
  * capturing); replays use the workspace of the time of the capture (kept until
  * fa_work_close), so they and direct calls on the handle must be ordered by the caller.
  * FA_TEST_WAIT_EXPIRES (the test aid above, in fa_work_opts.flags) makes the first data wait
- * of every tensor-core product give up at once: its outputs are invalid and fa_work_sync
+ * of every tensor-core product (those of fa_orthogonalise among them) give up at once: its outputs are invalid and fa_work_sync
  * returns FA_ERR_INTERNAL; the kernel waits (bounded) for its own loads and ends.
  */
 typedef struct fa_work fa_work;   /* opaque; owned by the library */
@@ -797,6 +797,59 @@ typedef struct {
 
 /* Errors: as fa_group_norm. */
 fa_status fa_group_norm_backward(fa_work* w, const fa_group_norm_backward_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The weight step, on the same work handle: the aggregated update (a mean of the clients' deltas
+ * or a gradient) with momentum, made orthogonal by Newton-Schulz products, scaled and added to
+ * the weight.  For each of `count` matrices [rows, cols]:
+ *
+ *   g = mu * momentum + update         (update itself without a momentum), to momentum_out
+ *   x = update + mu * g                (FA_ORTHO_NESTEROV; else g; update without a momentum)
+ *   X = x / (|x| + eps)                |x|: the root of the sum of its elements' squares
+ *   `steps` times:  A = X X^T,  X <- a X + (b A + c A^2) X
+ *   out = alpha * X + beta * residual
+ *
+ * With the quintic 3.4445, -4.7750, 2.0315 five steps bring singular values from 1e-3 to 1 near 1.
+ * Between its first and last pass a matrix is held as pairs of fp16 terms (22 bits, scaled), and
+ * multiplied pair by pair with fp32 sums.  Errors start at some 2^-22 of X's norm and grow by at
+ * most the polynomial's slope, |a| at 0, per step; against an update of many directions the result
+ * is as near to fp64 as the same products in fp32.  It is rounded once.  A NaN or an infinity in x
+ * spoils the matrix's whole result. */
+#define FA_ORTHO_NESTEROV  1u
+#define FA_ORTHO_MAX_STEPS 32
+
+typedef struct {
+    uint32_t size;             /* sizeof(fa_orthogonalise_args) */
+    uint32_t flags;            /* FA_ORTHO_NESTEROV */
+    int32_t dtype_in;          /* update */
+    int32_t dtype_out;         /* out and residual */
+    uint32_t steps;            /* 0 (X is scaled alone) to FA_ORTHO_MAX_STEPS */
+    uint32_t reserved;         /* 0 */
+    uint64_t count;            /* matrices; < 2^31; 0 (or rows or cols of 0) is a no-op */
+    uint64_t rows, cols;       /* each < 2^24, the lesser at most 2^15, rows * cols at most 2^32 */
+    const void* update;
+    uint64_t ldu, step_u;      /* elements from a row to the next, from a matrix to the next (0: rows *
+                                  ldu); likewise below */
+    const float* momentum;     /* [count, rows, cols], or NULL */
+    uint64_t ldm, step_m;
+    float* momentum_out;       /* or NULL; may be momentum itself, with the same strides */
+    uint64_t ldmo, step_mo;
+    const void* residual;      /* or NULL; not read if beta == 0 */
+    uint64_t ldr, step_r;
+    void* out;                 /* may be residual or update itself, with the same type and strides */
+    uint64_t ldo, step_o;
+    double mu;                 /* read with a momentum */
+    double eps;                /* 1e-30 to 1e30 */
+    double alpha, beta;
+    double a, b, c;            /* refused if a singular value of up to 1 could pass 4 on the way */
+} fa_orthogonalise_args;
+
+/* Errors: FA_ERR_ARG (null or host pointer, unknown flag, factors not finite or above 1e30, eps,
+ * overlap), FA_ERR_DTYPE, FA_ERR_RANGE (sizes, steps, strides, coefficients, outputs whose own rows
+ * overlap), FA_ERR_STATE (workspace growth while capturing), FA_ERR_NOMEM, FA_ERR_CUDA.  The
+ * workspace takes up to 1 GiB, or what one matrix needs where that is more: 8 bytes an element, and
+ * 8 (square) or 28 (else) for each of the short side's square. */
+fa_status fa_orthogonalise(fa_work* w, const fa_orthogonalise_args* args, void* stream);
 
 #ifdef __cplusplus
 }

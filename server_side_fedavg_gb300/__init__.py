@@ -53,6 +53,8 @@ FA_ROTARY_LINEAR = 1
 FA_ROTARY_BASE = 2
 FA_ROTARY_BANDED = 3
 FA_NORM_MAX_CHANNELS = 8192
+FA_ORTHO_NESTEROV = 1
+FA_ORTHO_MAX_STEPS = 32
 
 ACTS = {"none": FA_ACT_NONE, "relu": FA_ACT_RELU, "gelu": FA_ACT_GELU, "silu": FA_ACT_SILU,
         FA_ACT_NONE: FA_ACT_NONE, FA_ACT_RELU: FA_ACT_RELU, FA_ACT_GELU: FA_ACT_GELU,
@@ -172,6 +174,19 @@ class fa_group_norm_backward_args(ctypes.Structure):
                 ("d_beta", ctypes.c_void_p)]
 
 
+class fa_orthogonalise_args(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("dtype_in", ctypes.c_int32),
+                ("dtype_out", ctypes.c_int32), ("steps", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("count", ctypes.c_uint64), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64),
+                ("update", ctypes.c_void_p), ("ldu", ctypes.c_uint64), ("step_u", ctypes.c_uint64),
+                ("momentum", ctypes.c_void_p), ("ldm", ctypes.c_uint64), ("step_m", ctypes.c_uint64),
+                ("momentum_out", ctypes.c_void_p), ("ldmo", ctypes.c_uint64), ("step_mo", ctypes.c_uint64),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_uint64), ("step_r", ctypes.c_uint64),
+                ("out", ctypes.c_void_p), ("ldo", ctypes.c_uint64), ("step_o", ctypes.c_uint64),
+                ("mu", ctypes.c_double), ("eps", ctypes.c_double), ("alpha", ctypes.c_double), ("beta", ctypes.c_double),
+                ("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double)]
+
+
 class FedAvgError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
@@ -229,6 +244,7 @@ def lib():
         L.fa_product_backward.argtypes = [vp, ctypes.POINTER(fa_product_backward_args), vp]
         L.fa_rotary_turns.argtypes = [ctypes.c_uint32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                                       ctypes.c_double, ctypes.c_double, ctypes.POINTER(ctypes.c_uint64)]
+        L.fa_orthogonalise.argtypes = [vp, ctypes.POINTER(fa_orthogonalise_args), vp]
         L.fa_rotary.argtypes = [vp, ctypes.POINTER(fa_rotary_args), vp]
         L.fa_group_norm.argtypes = [vp, ctypes.POINTER(fa_group_norm_args), vp]
         L.fa_group_norm_backward.argtypes = [vp, ctypes.POINTER(fa_group_norm_backward_args), vp]
@@ -243,7 +259,8 @@ def lib():
                      "fa_finalize_apply", "fa_reduce_resident", "fa_reduce_subsets", "fa_reset",
                      "fa_close", "fa_key_total", "fa_sync", "fa_get_stats", "fa_work_open", "fa_work_close",
                      "fa_work_sync", "fa_work_get_stats", "fa_product", "fa_product_backward",
-                     "fa_distill_loss", "fa_distill_grad"):
+                     "fa_distill_loss", "fa_distill_grad", "fa_rotary_turns", "fa_rotary", "fa_group_norm",
+                     "fa_group_norm_backward", "fa_orthogonalise"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -651,3 +668,19 @@ def fa_group_norm_backward(work, n, positions, channels, groups, x, dout, dx, dt
         step_d, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd), _ptr(dx), channels if lddx is None else lddx, step_dx,
         _ptr(d_gamma), _ptr(d_beta))
     _check_work(lib().fa_group_norm_backward(work, args, _stream(stream)), work)
+
+
+# ---------------------------------------------------------------- the weight step
+def fa_orthogonalise(work, count, rows, cols, update, out, dtype_in, dtype_out, steps=5,
+                     coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, momentum=None, momentum_out=None, mu=0.0,
+                     nesterov=False, residual=None, alpha=1.0, beta=1.0, ldu=None, step_u=0, ldm=None, step_m=0, ldmo=None,
+                     step_mo=0, ldr=None, step_r=0, ldo=None, step_o=0, stream=None):
+    """out = alpha * orthogonalised(update with momentum) + beta * residual, for `count` matrices
+    [rows, cols] that lie ld... and step_... elements apart (a row, a matrix; by default one after
+    the other).  momentum and momentum_out are fp32, and may be one buffer."""
+    args = fa_orthogonalise_args(
+        ctypes.sizeof(fa_orthogonalise_args), bool(nesterov), DTYPES[dtype_in], DTYPES[dtype_out], steps, 0, count, rows, cols,
+        _ptr(update), cols if ldu is None else ldu, step_u, _ptr(momentum), cols if ldm is None else ldm, step_m,
+        _ptr(momentum_out), cols if ldmo is None else ldmo, step_mo, _ptr(residual), cols if ldr is None else ldr, step_r,
+        _ptr(out), cols if ldo is None else ldo, step_o, mu, eps, alpha, beta, *coefficients)
+    _check_work(lib().fa_orthogonalise(work, args, _stream(stream)), work)

@@ -1,0 +1,435 @@
+// The products of an orthogonalised weight step, on the tensor cores (tcgen05): operands as two
+// fp16 terms, fp32 sums, results as two fp16 terms again.
+//
+//   v = c1 * sum_k P(x,k) Q(y,k) + c2 * e1 + c3 * e2
+//
+// x = hi + lo has 22 bits, so hi lo' + lo hi' + hi hi' is the product to 2^-22 of its size: three
+// products of fp16 where three bf16 terms would need six.  The matrices' scales keep |x| below
+// 2^15, and their typical elements far above the 2^-24 where fp16 ends.
+//
+// A CTA's tile is 128 rows of P (TMEM lanes) by kBN rows of Q (TMEM columns); with kCtas == 2 a
+// pair of SMs has 256 by 256 (cta_group::2).  The tensor cores' fp32 sum truncates, so it is
+// emptied every 4 blocks of 64 terms into registers, which round to nearest; TMEM has two such
+// accumulators.  The last emptying leaves the tile in registers, from where it is finished: the
+// accumulators are free for the next tile meanwhile.
+//
+// Polynomials of a symmetric matrix commute and are symmetric: of these the tiles on and above
+// the diagonal are computed, and written twice.
+#include <cuda_fp16.h>
+
+#include "ortho.cuh"
+#include "tc_ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kBK = 64;                          // summed elements per block: 128 bytes, one swizzle row
+constexpr uint32_t kPlane = 128 * kBK * 2;       // of an operand's 128 rows
+constexpr uint32_t kStageBytes = 4 * kPlane;
+constexpr uint32_t kRing = 3;                    // stages
+constexpr uint32_t kUnit = 2048;                 // a drain warp's block of 32 x 32 results on its way out
+constexpr uint32_t kChunk = 4;                   // blocks between two emptyings
+constexpr uint32_t kBand = 8;                    // rows of tiles walked together
+constexpr int kCols = 64;                        // of a drain warp
+
+template <int kBN>
+constexpr int kDrain = 4 * kBN / kCols;          // drain warps
+// The pair's last warpgroup (loads, MMAs, two idle warps) gives registers to the drain warps, as in
+// the product kernels: 128 x 56 + 512 x 104 <= 640 x 96.
+template <int kBN>
+constexpr int kOrthoThreads = (kDrain<kBN> + (kBN == 256 ? 4 : 2)) * 32;
+template <int kBN>
+constexpr uint32_t kSmem = kRing * kStageBytes + kDrain<kBN> * kUnit;
+
+struct Args {
+    CUtensorMap p, q, out;
+    const uint16_t *e1, *e2;
+    uint64_t ld, plane;                          // of e1 and e2
+    unsigned int* err;
+    float c1, c2, c3;
+    uint32_t rows, cols, kblocks;
+    uint32_t tiles_p, tiles_q, per, tiles;       // per: of an item
+    bool p_kmajor, q_kmajor, symmetric, test_expire;
+};
+
+struct Tile {
+    uint32_t item, p, q;
+    __device__ __forceinline__ Tile(const Args& a, uint32_t t) {
+        item = t / a.per;
+        uint32_t r = t - item * a.per;
+        if (a.symmetric) {                       // column by column, p <= q
+            q = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+            while (q * (q + 1) / 2 > r) --q;
+            while ((q + 1) * (q + 2) / 2 <= r) ++q;
+            p = r - q * (q + 1) / 2;
+        } else {
+            const uint32_t full = kBand * a.tiles_q, band = r / full;
+            r -= band * full;
+            const uint32_t height = min(kBand, a.tiles_p - band * kBand);
+            q = r / height;
+            p = band * kBand + r - q * height;
+        }
+    }
+};
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(z), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float half_of(float x) { return __half2float(__float2half_rn(x)); }
+
+// v += c * (hi + lo) of eight elements
+__device__ __forceinline__ void add_planes(float* v, const uint16_t* hi, uint64_t plane, float c) {
+    const uint4 h = *reinterpret_cast<const uint4*>(hi), l = *reinterpret_cast<const uint4*>(hi + plane);
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hw[i]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&lw[i]));
+        v[2 * i] = fmaf(c, a.x + b.x, v[2 * i]);
+        v[2 * i + 1] = fmaf(c, a.y + b.y, v[2 * i + 1]);
+    }
+}
+
+// The block of 32 x 32 results at (row, col) from v, this lane's row of it: e1 and e2 added, then
+// either plane by way of the warp's buffer, and its mirror image.  64-byte rows in the 64-byte
+// swizzle: 16-byte piece j of row r is at j ^ (r / 2 % 4).
+__device__ __forceinline__ void finish(const Args& a, float* v, uint32_t buf, uint32_t item, uint32_t row0, uint32_t col,
+                                       bool mirror) {
+    const uint32_t lane = threadIdx.x % 32, row = row0 + lane;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= a.c1;
+    if (row < a.rows) {
+        const uint64_t at = 2ull * item * a.plane + row * a.ld + col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (a.e1 && col + 8 * j < a.cols) add_planes(v + 8 * j, a.e1 + at + 8 * j, a.plane, a.c2);
+            if (a.e2 && col + 8 * j < a.cols) add_planes(v + 8 * j, a.e2 + at + 8 * j, a.plane, a.c3);
+        }
+    }
+#pragma unroll
+    for (uint32_t z = 0; z < 2; ++z) {
+        if (z == 1)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] -= half_of(v[i]);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+            st_shared4u(buf + lane * 64 + ((j ^ (lane / 2 % 4)) << 4), pack_half(v[8 * j], v[8 * j + 1]),
+                        pack_half(v[8 * j + 2], v[8 * j + 3]), pack_half(v[8 * j + 4], v[8 * j + 5]),
+                        pack_half(v[8 * j + 6], v[8 * j + 7]));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&a.out, buf, col, row0, 2 * item + z);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        if (!mirror) continue;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (uint32_t c = 0; c < 32; ++c)
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + c * 64 + ((lane / 8 ^ (c / 2 % 4)) << 4) + lane % 8 * 2),
+                         "h"(__half_as_ushort(__float2half_rn(v[c])))
+                         : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&a.out, buf, row0, col, 2 * item + z);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
+template <int kCtas, int kBN>
+__global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(const __grid_constant__ Args a) {
+    static_assert(kBN / kCtas == 128, "128 rows of either operand per CTA");
+    constexpr int kWarps = kDrain<kBN>, kLoadWarp = kWarps, kMmaWarp = kWarps + 1;
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    __shared__ uint64_t bars[2 * kRing + 4];
+    __shared__ uint32_t tmem_slot, gone_flag;
+    const uint32_t base = smem_addr(dyn), full = smem_addr(&bars[0]), empty = full + 8 * kRing;
+    const uint32_t acc_full = full + 16 * kRing, acc_empty = acc_full + 16;
+    const uint32_t warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const uint32_t rank = kCtas == 2 ? cluster_rank() : 0, gone = smem_addr(&gone_flag);
+    const bool leader = rank == 0;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.p) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.q) : "memory");
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        for (uint32_t s = 0; s < kRing; ++s) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(acc_full + 8 * b, 1);
+            bar_init(acc_empty + 8 * b, kCtas * kWarps);
+        }
+        gone_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc<kCtas>(smem_addr(&tmem_slot), 2 * kBN);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (kCtas == 2) cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    bool ok = true;                      // of this thread: no wait gave up
+
+    if (warp >= kWarps) {
+        if constexpr (kBN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kLoadWarp && elect_one()) {
+            const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
+            const bool pk = a.p_kmajor, qk = a.q_kmajor;
+            const uint32_t kblocks = a.kblocks, tiles = a.tiles;
+            const CUtensorMap *mp = &a.p, *mq = &a.q;
+            const auto load = [&](uint32_t dst, const CUtensorMap* m, bool kmajor, uint32_t k, uint32_t x, uint32_t z, uint32_t bar) {
+                if (kmajor) {
+                    tma_load<kCtas>(dst, m, k, x, z, bar);
+                } else {
+                    tma_load<kCtas>(dst, m, x, k, z, bar);
+                    tma_load<kCtas>(dst + 8192, m, x + 64, k, z, bar);
+                }
+            };
+            uint32_t s = 0, phase = 1;
+            for (uint32_t t = first; ok && t < tiles; t += step) {
+                const Tile tile(a, t);
+                const uint32_t p0 = tile.p * 128 * kCtas + rank * 128, q0 = tile.q * kBN + rank * 128, z = 2 * tile.item;
+                for (uint32_t kb = 0; kb < kblocks; ++kb) {
+                    const uint32_t bar = lead_full + 8 * s, at = base + s * kStageBytes;
+                    if (!bar_wait(empty + 8 * s, phase, gone, kCtas)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_expect(full + 8 * s, kStageBytes * kCtas);
+                    load(at, mp, pk, kb * kBK, p0, z, bar);
+                    load(at + kPlane, mp, pk, kb * kBK, p0, z + 1, bar);
+                    load(at + 2 * kPlane, mq, qk, kb * kBK, q0, z, bar);
+                    load(at + 3 * kPlane, mq, qk, kb * kBK, q0, z + 1, bar);
+                    if (++s == kRing) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == kMmaWarp && leader && elect_one()) {
+            // fp32 sums of fp16 by fp16
+            const uint32_t idesc = 1u << 4 | (a.p_kmajor ? 0u : 1u << 15) | (a.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 |
+                                   (128 * kCtas / 16) << 24;
+            const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
+            const uint32_t desc_p = operand_desc_lo(base, a.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, a.q_kmajor);
+            const uint32_t kblocks = a.kblocks, tiles = a.tiles;
+            uint32_t it = 0, ch = 0, s = 0, phase = 0;
+            for (uint32_t t = first; ok && t < tiles; t += step) {
+                for (uint32_t kb = 0; ok && kb < kblocks; ++ch) {
+                    const uint32_t b = ch & 1;
+                    if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, kCtas)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t d = tmem + b * kBN, end = min(kblocks, kb + kChunk);
+                    bool add = false;
+                    for (; kb < end; ++kb, ++it) {
+                        const uint32_t dp = desc_p + (s * kStageBytes >> 4), dq = desc_q + (s * kStageBytes >> 4);
+                        if (a.test_expire || !bar_wait(full + 8 * s, phase, gone, kCtas)) {
+                            ok = false;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        // lo hi, hi lo, hi hi: the small products meet a small accumulator
+#pragma unroll
+                        for (uint32_t pair = 0; pair < 3; ++pair) {
+                            const uint32_t op = pair == 0 ? kPlane >> 4 : 0, oq = pair == 1 ? kPlane >> 4 : 0;
+#pragma unroll
+                            for (uint32_t x = 0; x < kBK / 16; ++x) {
+                                mma<kCtas>(d, dp + op + x * step_p, dq + oq + x * step_q, kDescHi, idesc, add);
+                                add = true;
+                            }
+                        }
+                        commit<kCtas>(empty + 8 * s);
+                        if (++s == kRing) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (ok) commit<kCtas>(acc_full + 8 * b);
+                }
+            }
+            if (!ok) {
+                // the loads in flight land before the CTA leaves
+                atomicOr(a.err, kErrWaitTimeout);
+                give_up(gone, kCtas);
+                const uint32_t blocks = kblocks * ((tiles - first + step - 1) / step);
+                for (uint32_t n = 0; n < kRing && it < blocks; ++n, ++it) {
+                    for (uint32_t i = 0; i < 1000 && !bar_try(full + 8 * (it % kRing), (it / kRing) & 1); ++i) {}
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        if constexpr (kBN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const uint32_t quad = warp % 4, part = warp / 4;
+        const uint32_t mine = tmem + (quad << 21) + part * kCols;       // lane 32 quad, column part * kCols
+        const uint32_t buf = base + kRing * kStageBytes + warp * kUnit;
+        const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty;
+        const uint32_t chunks = (a.kblocks + kChunk - 1) / kChunk;
+        uint32_t ch = 0;
+        for (uint32_t t = first; ok && t < a.tiles; t += step) {
+            float acc[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+            for (uint32_t n = 0; n < chunks; ++n, ++ch) {
+                const uint32_t b = ch & 1;
+                if (!bar_wait(acc_full + 8 * b, (ch / 2) & 1, gone, kCtas)) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    float v[16];
+                    tmem_ld16(mine + b * kBN + c, v);
+                    tmem_wait16(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive_cluster(lead_empty + 8 * b);
+            }
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            const Tile tile(a, t);
+            const uint32_t row0 = tile.p * 128 * kCtas + rank * 128 + quad * 32, col0 = tile.q * kBN + part * kCols;
+            const bool mirror = a.symmetric && tile.p != tile.q;
+            if (row0 < a.rows) {
+                if (col0 < a.cols) finish(a, acc, buf, tile.item, row0, col0, mirror);
+                if (col0 + 32 < a.cols) finish(a, acc + 32, buf, tile.item, row0, col0 + 32, mirror);
+            }
+        }
+        if (lane == 0) {
+            if (!ok) atomicOr(a.err, kErrWaitTimeout);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (kCtas == 2) cluster_sync();
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        tmem_free<kCtas>(tmem, 2 * kBN);
+    }
+}
+
+EncodeTiled g_encode = nullptr;
+
+bool encode(CUtensorMap* map, const OrthoBuf& b, uint32_t items, uint32_t box_x, uint32_t box_y, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[3] = {b.cols, b.rows, 2ull * items};
+    const cuuint64_t strides[2] = {b.ld * 2, b.plane() * 2};
+    const cuuint32_t box[3] = {box_x, box_y, 1}, one[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, b.p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kCtas, int kBN>
+cudaError_t launch(const Args& a, uint32_t room, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.tiles < room ? a.tiles : room) * kCtas);
+    cfg.blockDim = dim3(kOrthoThreads<kBN>);
+    cfg.dynamicSmemBytes = kSmem<kBN>;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kCtas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = kCtas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, ortho_product_kernel<kCtas, kBN>, a);
+}
+
+}  // namespace
+
+cudaError_t prepare_ortho(OrthoShape* shape) {
+    if (shape->ready) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&shape->sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_product_kernel<2, 256>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<256>);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_product_kernel<1, 128>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<128>);
+    if (e == cudaSuccess) e = tensor_map_encoder(&g_encode);
+    shape->ready = e == cudaSuccess;
+    return e;
+}
+
+cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
+    return encode(&b->k, *b, items, kBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                   encode(&b->mn, *b, items, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                   encode(&b->out, *b, items, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_ortho_product(const OrthoProduct& p, const OrthoShape& shape, unsigned int* err, bool test_expire,
+                                 cudaStream_t stream) {
+    Args a{};
+    a.p = p.p_kmajor ? p.P->k : p.P->mn;
+    a.q = p.q_kmajor ? p.Q->k : p.Q->mn;
+    a.out = p.out->out;
+    a.e1 = p.e1 ? p.e1->p : nullptr;
+    a.e2 = p.e2 ? p.e2->p : nullptr;
+    a.ld = p.out->ld;
+    a.plane = p.out->plane();
+    a.err = err;
+    a.c1 = p.c1;
+    a.c2 = p.c2;
+    a.c3 = p.c3;
+    a.rows = p.out->rows;
+    a.cols = p.out->cols;
+    a.kblocks = (p.k + kBK - 1) / kBK;
+    a.p_kmajor = p.p_kmajor;
+    a.q_kmajor = p.q_kmajor;
+    a.symmetric = p.symmetric;
+    a.test_expire = test_expire;
+    const auto tiles = [&](uint32_t size) {
+        a.tiles_p = (a.rows + size - 1) / size;
+        a.tiles_q = (a.cols + size - 1) / size;
+        a.per = a.symmetric ? a.tiles_q * (a.tiles_q + 1) / 2 : a.tiles_p * a.tiles_q;
+        a.tiles = a.per * p.items;
+    };
+    // Turns of tiles over the SMs, in microseconds: a block of a pair takes 0.8, of a single SM 0.42
+    // or, with all SMs loading 64 KB for each, 0.58; a tile's end 1.5.
+    const uint32_t sms = static_cast<uint32_t>(shape.sms), pairs = sms / 2;
+    tiles(256);
+    const double pair = (a.tiles + pairs - 1) / pairs * (0.8 * a.kblocks + 1.5);
+    tiles(128);
+    const double busy = a.tiles < sms ? static_cast<double>(a.tiles) / sms : 1.0;
+    const double single = (a.tiles + sms - 1) / sms * ((0.58 * busy > 0.42 ? 0.58 * busy : 0.42) * a.kblocks + 1.5);
+    if (pair <= single) {
+        tiles(256);
+        return launch<2, 256>(a, pairs, stream);
+    }
+    return launch<1, 128>(a, sms, stream);
+}
+
+}  // namespace fa

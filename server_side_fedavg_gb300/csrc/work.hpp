@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "kernels.cuh"
+#include "ortho.cuh"
 #include "product_tc.cuh"
 
 struct fa_work {
@@ -41,6 +42,7 @@ struct fa_work {
     cudaStream_t err_stream = nullptr;
     cudaEvent_t err_ev = nullptr;
     fa::TcShape tc;
+    fa::OrthoShape ortho;                // filled in by the first fa_orthogonalise
     fa_work_stats stats{};
     std::string err;
 };
