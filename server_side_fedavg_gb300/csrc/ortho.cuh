@@ -25,6 +25,7 @@ struct OrthoProduct {
     bool p_kmajor, q_kmajor;
     bool symmetric;                           // the tiles on and above the diagonal, and their mirror images
     uint32_t items, k;
+    uint32_t chunk;                           // blocks of 64 terms that the tensor cores sum by themselves
     float c1, c2, c3;
 };
 
@@ -55,6 +56,15 @@ struct OrthoEnds {
     int shift;                                // the scaled update's, in powers of two
     bool nesterov;
 };
+// The whole step in one kernel: a short side of up to 64, in fp32, each matrix in the shared memory
+// of a cluster.  False where it does not fit.
+struct OrthoSmall {
+    uint32_t steps, parts;                    // in so many segments, the first ones longer by one at most
+    float a, b, c;
+};
+bool ortho_small_fits(uint32_t rows, uint32_t cols);
+cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall& s, cudaStream_t stream);
+
 uint32_t ortho_blocks(uint32_t items, uint32_t rows, uint32_t cols, uint32_t sms);
 cudaError_t launch_ortho_norm(const OrthoEnds& a, cudaStream_t stream);
 cudaError_t launch_ortho_scale(const OrthoEnds& a, cudaStream_t stream);

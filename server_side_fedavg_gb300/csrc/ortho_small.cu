@@ -1,0 +1,394 @@
+// A whole orthogonalised weight step for matrices with a short side of up to 64 (adapters, small
+// classifiers), in fp32: one kernel, a matrix per cluster.
+//
+// Each CTA of the cluster holds a run of the long side in shared memory, as fp32 rows x_j of kM
+// elements, from the first pass to the last.  A = sum_j x_j x_j^T: every CTA sums its run, and all
+// read each other's sums over distributed shared memory, in rank order.  The steps' polynomials in A
+// are then kM x kM products in shared memory, which every CTA does for itself, and x_j <- (q + Q) x_j
+// closes a segment of up to three steps (see the host's `segments`).
+//
+// Rows are kM + 4 floats apart: lanes that read 16 bytes of rows next to each other then meet no
+// bank conflict.
+#include <algorithm>
+
+#include "ortho_device.cuh"
+#include "tc_ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr uint32_t kSmallThreads = 256, kSmallWarps = kSmallThreads / 32, kSmallCtas = 8;
+constexpr uint32_t kSmallRun = 512;            // rows per CTA, unless eight CTAs have to hold more
+constexpr uint32_t kSmallMost = 226 * 1024;    // bytes of shared memory
+constexpr uint32_t kSmallAhead = 4;            // pieces of eight elements whose loads a thread has in flight
+
+template <int kM>
+constexpr uint32_t kPitch = kM + 4;
+template <int kM>
+constexpr uint32_t kMat = kM * kPitch<kM>;     // floats of a kM x kM matrix
+// six matrices (two where segments are of one step), two buffers of this CTA's sums for the others,
+// the warps' sums
+template <int kM>
+constexpr uint32_t kMats = kM == 64 ? 2 : 6;
+template <int kM>
+constexpr uint32_t kFixed = (kMats<kM> * kMat<kM> + 2 * kM * kM + (kM == 64 ? 0 : kSmallWarps * kM * kM)) * 4;
+
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 d, {%0, %1};\n"
+        " fma.rn.f32x2 d, a, b, d;\n mov.b64 {%0, %1}, d;\n}"
+        : "+f"(d.x), "+f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+}
+
+// C = c1 A B + c2 E + c3 F, all symmetric; C is none of the others.  A thread has kB x kB elements.
+template <int kM>
+__device__ __forceinline__ void mul(float* C, const float* A, const float* B, float c1, const float* E, float c2, const float* F,
+                                    float c3) {
+    constexpr uint32_t kB = kM <= 16 ? 1 : kM / 16, kSide = kM / kB;
+    if (threadIdx.x < kSide * kSide) {
+        const uint32_t r = threadIdx.x / kSide, c = threadIdx.x % kSide;
+        float2 s[kB][kB];
+#pragma unroll
+        for (uint32_t i = 0; i < kB * kB; ++i) s[i / kB][i % kB] = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+        for (uint32_t k = 0; k < kM; k += 4) {
+            float4 x[kB], y[kB];
+#pragma unroll
+            for (uint32_t i = 0; i < kB; ++i) {
+                x[i] = *reinterpret_cast<const float4*>(A + (r + kSide * i) * kPitch<kM> + k);
+                y[i] = *reinterpret_cast<const float4*>(B + (c + kSide * i) * kPitch<kM> + k);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kB * kB; ++i) {
+                const float4 p = x[i / kB], q = y[i % kB];
+                fma2(s[i / kB][i % kB], make_float2(p.x, p.y), make_float2(q.x, q.y));
+                fma2(s[i / kB][i % kB], make_float2(p.z, p.w), make_float2(q.z, q.w));
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kB * kB; ++i) {
+            const uint32_t at = (r + kSide * (i / kB)) * kPitch<kM> + c + kSide * (i % kB);
+            float v = fmaf(c2, E[at], c1 * (s[i / kB][i % kB].x + s[i / kB][i % kB].y));
+            if (F) v = fmaf(c3, F[at], v);
+            C[at] = v;
+        }
+    }
+    __syncthreads();
+}
+
+// This CTA's sum of x_j x_j^T over its run, to out[kM][kM].  A lane has an 8 x 8 tile of the result
+// and every so-manieth row; lanes with one tile, then warps, are summed in a fixed order.
+template <int kM>
+__device__ __forceinline__ void gram(const float* xs, uint32_t run, float* red, float* out) {
+    constexpr uint32_t kSide = kM / 8, kTiles = kSide * kSide, kStrands = kSmallThreads / kTiles;
+    const uint32_t tile = threadIdx.x % kTiles, strand = threadIdx.x / kTiles, ti = tile / kSide * 8, tk = tile % kSide * 8;
+    float2 s[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[i][k] = make_float2(0.0f, 0.0f);
+    for (uint32_t j = strand; j < run; j += kStrands) {
+        const float* x = xs + j * kPitch<kM>;
+        const float4 a0 = *reinterpret_cast<const float4*>(x + ti), a1 = *reinterpret_cast<const float4*>(x + ti + 4);
+        const float4 b0 = *reinterpret_cast<const float4*>(x + tk), b1 = *reinterpret_cast<const float4*>(x + tk + 4);
+        const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const float2 bv[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y), make_float2(b1.z, b1.w)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) fma2(s[i][k], make_float2(av[i], av[i]), bv[k]);
+    }
+    float* v = &s[0][0].x;
+    if constexpr (kTiles <= 32) {
+        // lanes with one tile: each exchange halves what a lane keeps
+        const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        uint32_t first = 0;
+#pragma unroll
+        for (uint32_t o = 16, half = 32; o >= kTiles; o /= 2, half /= 2) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (uint32_t e = 0; e < half; ++e) {
+                const float got = __shfl_xor_sync(~0u, upper ? v[e] : v[e + half], o);
+                v[e] = (upper ? v[e + half] : v[e]) + got;
+            }
+            if (upper) first += half;
+        }
+        constexpr uint32_t kKeep = 64 * kTiles / 32;
+#pragma unroll
+        for (uint32_t e = 0; e < kKeep; ++e)
+            red[(warp * kM + ti + (first + e) / 8) * kM + tk + (first + e) % 8] = v[e];
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < kM * kM; i += kSmallThreads) {
+            float t = 0.0f;
+#pragma unroll
+            for (uint32_t w = 0; w < kSmallWarps; ++w) t += red[w * kM * kM + i];
+            out[i] = t;
+        }
+    } else {
+        for (uint32_t turn = 0; turn < kStrands; ++turn) {
+            if (strand == turn)
+#pragma unroll
+                for (uint32_t e = 0; e < 64; ++e) {
+                    float* to = out + (ti + e / 8) * kM + tk + e % 8;
+                    *to = turn ? *to + v[e] : v[e];
+                }
+            __syncthreads();
+        }
+    }
+}
+
+// x_j <- q x_j + Q x_j, two rows of the run per thread at a time.
+template <int kM>
+__device__ __forceinline__ void apply(float* xs, uint32_t run, const float* Q, float q) {
+    for (uint32_t j = threadIdx.x; j < run; j += 2 * kSmallThreads) {
+        const uint32_t j1 = j + kSmallThreads;
+        const bool two = j1 < run;
+        float2 x[2][kM / 2];
+        float* at[2] = {xs + j * kPitch<kM>, xs + (two ? j1 : j) * kPitch<kM>};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < kM / 4; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(at[n] + 4 * k);
+                x[n][2 * k] = make_float2(v.x, v.y);
+                x[n][2 * k + 1] = make_float2(v.z, v.w);
+            }
+#pragma unroll 1
+        for (int i = 0; i < kM; i += 4) {
+            float y[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int k = 0; k < kM; k += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(Q + (i + e) * kPitch<kM> + k);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        fma2(s[n], make_float2(v.x, v.y), x[n][k / 2]);
+                        fma2(s[n], make_float2(v.z, v.w), x[n][k / 2 + 1]);
+                    }
+                }
+                y[0][e] = s[0].x + s[0].y;
+                y[1][e] = s[1].x + s[1].y;
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (n == 1 && !two) break;
+                float4* to = reinterpret_cast<float4*>(at[n] + i);
+                const float4 own = *to;
+                *to = make_float4(fmaf(q, own.x, y[n][0]), fmaf(q, own.y, y[n][1]), fmaf(q, own.z, y[n][2]), fmaf(q, own.w, y[n][3]));
+            }
+        }
+    }
+}
+
+struct SmallArgs {
+    OrthoEnds e;
+    OrthoSmall s;
+    Vecs v;
+    uint32_t run, ctas;                        // run: a multiple of 8
+};
+
+template <int kM>
+__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid_constant__ SmallArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ double sums[kSmallWarps], mine;
+    __shared__ float2 factor;
+    const OrthoEnds& e = a.e;
+    float *A = sm, *P0 = A + kMat<kM>, *P1 = P0 + kMat<kM>, *R = P1 + kMat<kM>, *Q0 = R + kMat<kM>, *Q1 = Q0 + kMat<kM>;
+    float *part = sm + kMats<kM> * kMat<kM>, *red = part + 2 * kM * kM, *xs = sm + kFixed<kM> / 4;
+    const uint32_t rank = a.ctas > 1 ? cluster_rank() : 0, item = blockIdx.x / a.ctas;
+    const bool wide = e.rows <= e.cols;
+    const uint32_t n = wide ? e.cols : e.rows, m = wide ? e.rows : e.cols;
+    const uint32_t j0 = min(n, rank * a.run), run = min(a.run, n - j0), run8 = (run + 7) / 8 * 8;
+    wait_predecessor();
+
+    // The rows eight elements at a time: along the long side of the matrix (wide), or of a row x_j.
+    const uint32_t all = wide ? run8 / 8 * kM : run * (kM / 8);
+    // the matrix's row and column of piece t, and its place in shared memory
+    const auto row_at = [&](uint32_t t) { return wide ? t % kM : j0 + t / (kM / 8); };
+    const auto col_at = [&](uint32_t t) { return wide ? j0 + t / kM * 8 : t % (kM / 8) * 8; };
+    const auto in_use = [&](uint32_t t) { return t < all && (wide ? t % kM : t % (kM / 8) * 8) < m; };
+    double sum = 0.0;
+    for (uint32_t t0 = threadIdx.x; t0 < all; t0 += kSmallAhead * kSmallThreads) {
+        float x[kSmallAhead][8], g[kSmallAhead][8];
+#pragma unroll
+        for (uint32_t u = 0; u < kSmallAhead; ++u) {
+            const uint32_t t = t0 + u * kSmallThreads;
+            if (!in_use(t)) continue;
+            load8(e.update, row_of(e.update, item, row_at(t)), col_at(t), e.cols, a.v.update, x[u]);
+            if (e.momentum.p) load8(e.momentum, row_of(e.momentum, item, row_at(t)), col_at(t), e.cols, a.v.momentum, g[u]);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kSmallAhead; ++u) {
+            const uint32_t t = t0 + u * kSmallThreads;
+            if (t >= all) break;
+            if (in_use(t)) {
+                momentum_step(e, x[u], g[u]);
+                if (e.momentum_out.p)
+                    store8(e.momentum_out, row_of(e.momentum_out, item, row_at(t)), col_at(t), e.cols, a.v.momentum_out, g[u]);
+                sum += squares(x[u]);
+            } else {
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) x[u][k] = 0.0f;
+            }
+            if (wide) {
+                float* to = xs + t / kM * 8 * kPitch<kM> + t % kM;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) to[k * kPitch<kM>] = x[u][k];
+            } else {
+                float* to = xs + t / (kM / 8) * kPitch<kM> + t % (kM / 8) * 8;
+                *reinterpret_cast<float4*>(to) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+                *reinterpret_cast<float4*>(to + 4) = make_float4(x[u][4], x[u][5], x[u][6], x[u][7]);
+            }
+        }
+    }
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    sum = warp_sum(sum);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (uint32_t w = 1; w < kSmallWarps; ++w) sum += sums[w];
+        mine = sum;
+    }
+    if (a.ctas > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.0;
+        for (uint32_t q = 0; q < a.ctas; ++q) {
+            double v;
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a.ctas > 1 ? in_cta(smem_addr(&mine), q) : smem_addr(&mine)) : "memory");
+            sum += v;
+        }
+        factor = factor_of(sum, e.eps, 0);
+    }
+    __syncthreads();
+    const float f0 = factor.x, f1 = factor.y;
+    for (uint32_t t = threadIdx.x; t < run * kM; t += kSmallThreads) {
+        float* x = xs + t / kM * kPitch<kM> + t % kM;
+        *x = *x * f1 * f0;
+    }
+    __syncthreads();
+
+    uint32_t left = a.s.steps, parity = 0;
+    for (uint32_t n_part = a.s.parts; n_part > 0; --n_part, parity ^= 1) {
+        const uint32_t steps = (left + n_part - 1) / n_part;
+        left -= steps;
+        float* own = part + parity * kM * kM;
+        gram<kM>(xs, run, red, own);
+        // the others' sums; they have read this buffer's last ones before the last exchange
+        if (a.ctas > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        for (uint32_t i = threadIdx.x; i < kM * kM; i += kSmallThreads) {
+            float v = 0.0f;
+            for (uint32_t q = 0; q < a.ctas; ++q) v += ld_part1(smem_addr(own + i), q, a.ctas);
+            A[i / kM * kPitch<kM> + i % kM] = v;
+        }
+        __syncthreads();
+        float *P = P0, *Q = P0, *next = Q0;
+        float q = 1.0f;
+        for (uint32_t j = 0; j < steps; ++j) {
+            P = j % 2 ? P1 : P0;                 // (kM == 64: one step, P0 alone)
+            mul<kM>(P, A, A, a.s.c, A, a.s.b, nullptr, 0.0f);
+            if (j == 0) {
+                Q = P;
+                q = a.s.a;
+            } else {
+                mul<kM>(next, P, Q, 1.0f, Q, a.s.a, P, q);
+                Q = next;
+                next = next == Q0 ? Q1 : Q0;
+                q *= a.s.a;
+            }
+            if (j + 1 < steps) {
+                mul<kM>(R, A, P, 1.0f, A, a.s.a, nullptr, 0.0f);
+                mul<kM>(A, R, P, 1.0f, R, a.s.a, nullptr, 0.0f);
+            }
+        }
+        apply<kM>(xs, run, Q, q);
+        __syncthreads();
+    }
+
+    for (uint32_t t0 = threadIdx.x; t0 < all; t0 += kSmallAhead * kSmallThreads) {
+        float res[kSmallAhead][8];
+        if (e.residual.p)
+#pragma unroll
+            for (uint32_t u = 0; u < kSmallAhead; ++u) {
+                const uint32_t t = t0 + u * kSmallThreads;
+                if (in_use(t)) load8(e.residual, row_of(e.residual, item, row_at(t)), col_at(t), e.cols, a.v.residual, res[u]);
+            }
+#pragma unroll
+        for (uint32_t u = 0; u < kSmallAhead; ++u) {
+            const uint32_t t = t0 + u * kSmallThreads;
+            if (!in_use(t)) continue;
+            float x[8];
+            const float* from = wide ? xs + t / kM * 8 * kPitch<kM> + t % kM : xs + t / (kM / 8) * kPitch<kM> + t % (kM / 8) * 8;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                x[k] = e.alpha * from[wide ? k * kPitch<kM> : k];
+                if (e.residual.p) x[k] = fmaf(e.beta, res[u][k], x[k]);
+            }
+            store8(e.out, row_of(e.out, item, row_at(t)), col_at(t), e.cols, a.v.out, x);
+        }
+    }
+    if (a.ctas > 1) cluster_sync();          // no CTA leaves while another may read its sums
+}
+
+uint32_t side(uint32_t m) { return m <= 8 ? 8 : m <= 16 ? 16 : m <= 32 ? 32 : 64; }
+
+// CTAs of a cluster, and rows of each: runs of about kSmallRun, powers of two.
+void split(uint32_t n, uint32_t* ctas, uint32_t* run) {
+    *ctas = 1;
+    while (*ctas < kSmallCtas && *ctas * kSmallRun < n) *ctas *= 2;
+    *run = ((n + *ctas - 1) / *ctas + 7) / 8 * 8;
+}
+
+template <int kM>
+cudaError_t launch(SmallArgs a, cudaStream_t stream) {
+    const uint32_t smem = kFixed<kM> + a.run * kPitch<kM> * 4;
+    cudaError_t r = cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_small_kernel<kM>),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (r != cudaSuccess) return r;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.e.items * a.ctas);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = a.ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, ortho_small_kernel<kM>, a);
+}
+
+}  // namespace
+
+bool ortho_small_fits(uint32_t rows, uint32_t cols) {
+    const uint32_t m = std::min(rows, cols), n = std::max(rows, cols);
+    uint32_t ctas, run;
+    split(n, &ctas, &run);
+    if (m > 64) return false;
+    const uint32_t fixed = m <= 8 ? kFixed<8> : m <= 16 ? kFixed<16> : m <= 32 ? kFixed<32> : kFixed<64>;
+    return static_cast<uint64_t>(run) * (side(m) + 4) * 4 + fixed <= kSmallMost;
+}
+
+cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall& s, cudaStream_t stream) {
+    SmallArgs a{};
+    a.e = e;
+    a.s = s;
+    a.v = vecs(e);
+    split(std::max(e.rows, e.cols), &a.ctas, &a.run);
+    const uint32_t m = side(std::min(e.rows, e.cols));
+    if (m == 64) a.s.parts = a.s.steps;          // no room for the squares of longer segments
+    return m == 8 ? launch<8>(a, stream) : m == 16 ? launch<16>(a, stream) : m == 32 ? launch<32>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace fa

@@ -29,7 +29,6 @@ constexpr uint32_t kPlane = 128 * kBK * 2;       // of an operand's 128 rows
 constexpr uint32_t kStageBytes = 4 * kPlane;
 constexpr uint32_t kRing = 3;                    // stages
 constexpr uint32_t kUnit = 2048;                 // a drain warp's block of 32 x 32 results on its way out
-constexpr uint32_t kChunk = 4;                   // blocks between two emptyings
 constexpr uint32_t kBand = 8;                    // rows of tiles walked together
 constexpr int kCols = 64;                        // of a drain warp
 
@@ -48,7 +47,7 @@ struct Args {
     uint64_t ld, plane;                          // of e1 and e2
     unsigned int* err;
     float c1, c2, c3;
-    uint32_t rows, cols, kblocks;
+    uint32_t rows, cols, kblocks, chunk;         // chunk: blocks between two emptyings
     uint32_t tiles_p, tiles_q, per, tiles;       // per: of an item
     bool p_kmajor, q_kmajor, symmetric, test_expire;
 };
@@ -232,7 +231,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                                    (128 * kCtas / 16) << 24;
             const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
             const uint32_t desc_p = operand_desc_lo(base, a.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, a.q_kmajor);
-            const uint32_t kblocks = a.kblocks, tiles = a.tiles;
+            const uint32_t kblocks = a.kblocks, tiles = a.tiles, chunk = a.chunk;
             uint32_t it = 0, ch = 0, s = 0, phase = 0;
             for (uint32_t t = first; ok && t < tiles; t += step) {
                 for (uint32_t kb = 0; ok && kb < kblocks; ++ch) {
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t d = tmem + b * kBN, end = min(kblocks, kb + kChunk);
+                    const uint32_t d = tmem + b * kBN, end = min(kblocks, kb + chunk);
                     bool add = false;
                     for (; kb < end; ++kb, ++it) {
                         const uint32_t dp = desc_p + (s * kStageBytes >> 4), dq = desc_q + (s * kStageBytes >> 4);
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         const uint32_t mine = tmem + (quad << 21) + part * kCols;       // lane 32 quad, column part * kCols
         const uint32_t buf = base + kRing * kStageBytes + warp * kUnit;
         const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty;
-        const uint32_t chunks = (a.kblocks + kChunk - 1) / kChunk;
+        const uint32_t chunks = (a.kblocks + a.chunk - 1) / a.chunk;
         uint32_t ch = 0;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
             float acc[kCols];
@@ -407,6 +406,7 @@ cudaError_t launch_ortho_product(const OrthoProduct& p, const OrthoShape& shape,
     a.rows = p.out->rows;
     a.cols = p.out->cols;
     a.kblocks = (p.k + kBK - 1) / kBK;
+    a.chunk = p.chunk;
     a.p_kmajor = p.p_kmajor;
     a.q_kmajor = p.q_kmajor;
     a.symmetric = p.symmetric;

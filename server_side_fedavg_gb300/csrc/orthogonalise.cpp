@@ -54,8 +54,8 @@ constexpr int kSquares = 7;          // m x m matrices of the longest segment
 // square of what X's own does (12 per step), so after three steps A is formed anew: simulated in
 // fp64 with fp16 pairs, 5 steps in one segment are off by up to 2.7e-5 on an update with a few
 // strong directions, 3 + 2 by 1.1e-6, 1 + 1 + 1 + 1 + 1 by 1.4e-6.
-std::vector<uint32_t> segments(uint32_t steps, const Sizes& z) {
-    const bool joined = z.n * 5ull >= z.m * 6ull;
+std::vector<uint32_t> segments(uint32_t steps, const Sizes& z, bool bf16) {
+    const bool joined = bf16 && z.n * 5ull >= z.m * 6ull;
     const uint32_t parts = joined ? (steps + 2) / 3 : steps;
     std::vector<uint32_t> s;
     for (uint32_t left = steps, n = parts; n > 0; --n) {
@@ -69,7 +69,7 @@ struct Run {
     fa_work* w;
     cudaStream_t s;
     Sizes z;
-    uint32_t items;
+    uint32_t items, chunk;
     double a, b, c;
     fa::OrthoBuf x[2], sq[kSquares];
 
@@ -86,6 +86,7 @@ struct Run {
         p.symmetric = symmetric;
         p.items = items;
         p.k = k;
+        p.chunk = chunk;
         // from true values to held ones
         p.c1 = static_cast<float>(std::ldexp(c1, out.shift - P.shift - Q.shift));
         p.c2 = e1 ? static_cast<float>(std::ldexp(c2, out.shift - e1->shift)) : 0.0f;
@@ -177,7 +178,8 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
 
     const uint32_t rows = static_cast<uint32_t>(p.rows), cols = static_cast<uint32_t>(p.cols);
     const Sizes z{rows, cols, std::min(rows, cols), std::max(rows, cols), rows <= cols};
-    const std::vector<uint32_t> parts = segments(p.steps, z);
+    const std::vector<uint32_t> parts = segments(p.steps, z, p.dtype_out == FA_BF16);
+    const bool small = fa::ortho_small_fits(rows, cols);
     uint32_t longest = 0;
     for (uint32_t v : parts) longest = std::max(longest, v);
     // A segment of one holds A and P, longer ones up to seven squares.
@@ -185,7 +187,8 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
     const uint64_t ldx = (cols + 7ull) / 8 * 8, ldm = (z.m + 7ull) / 8 * 8;
     const uint64_t each = 4 * ((longest ? 2 : 1) * rows * ldx + squares * z.m * ldm);
     // Matrices at one time: what fits 1 GiB of workspace, one at least.
-    const uint32_t group = static_cast<uint32_t>(std::min<uint64_t>({p.count, std::max<uint64_t>(1, (1ull << 30) / each), 32768}));
+    const uint32_t group = static_cast<uint32_t>(
+        small ? std::min<uint64_t>(p.count, 1u << 20) : std::min<uint64_t>({p.count, std::max<uint64_t>(1, (1ull << 30) / each), 32768}));
     const bool cap = capturing(s);
     Run run{};
     double* part = nullptr;
@@ -205,18 +208,23 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
         part = static_cast<double*>(c.take(8ull * group * blocks));
     };
     Carve need{nullptr}, c{nullptr};
-    carve(need);
-    FW_CUDA(w, fa::prepare_ortho(&w->ortho));
+    if (!small) {
+        carve(need);
+        FW_CUDA(w, fa::prepare_ortho(&w->ortho));
+    }
     r = ensure_ws(w, need.used, cap);
     if (r == FA_OK) r = chain_in(w, s, cap);
     if (r != FA_OK) return r;
-    c.base = w->ws;
-    carve(c);
-    for (int i = 0; i < (longest ? 2 : 1); ++i) FW_CUDA(w, fa::map_ortho(&run.x[i], group));
-    for (int i = 0; i < squares; ++i) FW_CUDA(w, fa::map_ortho(&run.sq[i], group));
+    if (!small) {
+        c.base = w->ws;
+        carve(c);
+        for (int i = 0; i < (longest ? 2 : 1); ++i) FW_CUDA(w, fa::map_ortho(&run.x[i], group));
+        for (int i = 0; i < squares; ++i) FW_CUDA(w, fa::map_ortho(&run.sq[i], group));
+    }
     run.w = w;
     run.s = s;
     run.z = z;
+    run.chunk = p.dtype_out == FA_BF16 ? 16 : z.m <= 512 ? 1 : z.m <= 1024 ? 2 : 4;
     run.a = p.a;
     run.b = p.b;
     run.c = p.c;
@@ -241,20 +249,26 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
     ChainOut chain(w, s, cap);
     for (uint64_t first = 0; first < p.count && r == FA_OK; first += group) {
         run.items = e.items = static_cast<uint32_t>(std::min<uint64_t>(group, p.count - first));
-        Held X;
-        X.set(&run.x[0], 1.0);
-        e.x = run.x[0].p;
-        e.shift = X.shift;
-        r = launched(w, fa::launch_ortho_norm(e, s), "update's norm");
-        if (r == FA_OK) r = launched(w, fa::launch_ortho_scale(e, s), "update's scale");
-        uint32_t done = 0;
-        for (uint32_t n : parts) {
-            done += n;
-            if (r == FA_OK) r = run.segment(n, X, top[done]);
+        if (small) {
+            const fa::OrthoSmall steps{p.steps, p.dtype_out == FA_BF16 ? (p.steps + 2) / 3 : p.steps, static_cast<float>(p.a), static_cast<float>(p.b), static_cast<float>(p.c)};
+            e.alpha = static_cast<float>(p.alpha);
+            r = launched(w, fa::launch_ortho_small(e, steps, s), "weight step");
+        } else {
+            Held X;
+            X.set(&run.x[0], 1.0);
+            e.x = run.x[0].p;
+            e.shift = X.shift;
+            r = launched(w, fa::launch_ortho_norm(e, s), "update's norm");
+            if (r == FA_OK) r = launched(w, fa::launch_ortho_scale(e, s), "update's scale");
+            uint32_t done = 0;
+            for (uint32_t n : parts) {
+                done += n;
+                if (r == FA_OK) r = run.segment(n, X, top[done]);
+            }
+            e.x = X.buf->p;
+            e.alpha = static_cast<float>(std::ldexp(p.alpha, -X.shift));
+            if (r == FA_OK) r = launched(w, fa::launch_ortho_finish(e, s), "weight step");
         }
-        e.x = X.buf->p;
-        e.alpha = static_cast<float>(std::ldexp(p.alpha, -X.shift));
-        if (r == FA_OK) r = launched(w, fa::launch_ortho_finish(e, s), "weight step");
         for (fa::OrthoMat* t : {&e.update, &e.momentum, &e.momentum_out, &e.residual, &e.out})
             if (t->p) t->p = static_cast<const uint8_t*>(t->p) + group * t->step * (t->dtype ? 2 : 4);
     }
