@@ -48,7 +48,7 @@ struct OrthoMat {
 struct OrthoEnds {
     OrthoMat update, momentum, momentum_out, residual, out;
     uint32_t items, rows, cols, blocks;       // blocks per item
-    double* part;                             // [items][blocks] sums of squares
+    float3* part;                             // [items][blocks] sums of squares, by size
     uint16_t* x;                              // planes of the scaled update, or of the result
     uint64_t ld;
     double eps;

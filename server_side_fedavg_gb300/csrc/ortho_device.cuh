@@ -66,33 +66,61 @@ __device__ __forceinline__ void step_of(const OrthoEnds& a, const Vecs& v, uint3
     momentum_step(a, x, g);
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+// A sum of squares of fp32 numbers of any size, in fp32: those from 2^-50 to 2^45 as they are,
+// smaller and larger ones scaled by 2^84 and 2^-84, so that no square of up to 2^32 of them leaves
+// fp32's range.  (In fp64, whose units are few on this GPU, the sum and the root took 5 us of a small
+// matrix's 20.)
+struct Squares {
+    float mid = 0.0f, high = 0.0f, low = 0.0f;
+    __device__ __forceinline__ void add(const float (&x)[8]) {
+        float most = 0.0f, least = 0x1p45f, q = 0.0f;
+        bool nan = false;
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(~0u, v, o);
-    return v;
-}
-
-// Sum of eight squares: in fp32 where none can leave its range, else in fp64.
-__device__ __forceinline__ double squares(const float (&x)[8]) {
-    float most = 0.0f, q = 0.0f;
+        for (int j = 0; j < 8; ++j) {
+            const float v = fabsf(x[j]);
+            most = fmaxf(most, v);
+            if (v > 0.0f) least = fminf(least, v);
+            nan |= v != v;
+            q = fmaf(v, v, q);
+        }
+        if (most < 0x1p45f && least >= 0x1p-50f && !nan) {
+            mid += q;
+            return;
+        }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        most = fmaxf(most, fabsf(x[j]));
-        q = fmaf(x[j], x[j], q);
+        for (int j = 0; j < 8; ++j) {
+            const float v = fabsf(x[j]), h = v * 0x1p-84f, l = v * 0x1p84f;
+            if (!(v < 0x1p45f))
+                high = fmaf(h, h, high);
+            else if (v < 0x1p-50f)
+                low = fmaf(l, l, low);
+            else
+                mid = fmaf(v, v, mid);
+        }
     }
-    if (most < 0x1p60f && (most > 0x1p-40f || most == 0.0f) && q == q) return static_cast<double>(q);
-    double s = 0.0;
+    __device__ __forceinline__ void add(const Squares& o) {
+        mid += o.mid;
+        high += o.high;
+        low += o.low;
+    }
+    __device__ __forceinline__ void over_warp() {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += static_cast<double>(x[j]) * static_cast<double>(x[j]);
-    return s;
-}
-
-// 2^shift / (root of s + eps) as a fraction of 1 and a power of two, which fp32 has down to 2^-149.
-__device__ __forceinline__ float2 factor_of(double s, double eps, int shift) {
-    int e;
-    const float f = static_cast<float>(frexp(1.0 / (sqrt(s) + eps), &e));
-    return make_float2(f, ldexpf(1.0f, e + shift));
-}
+        for (int o = 16; o > 0; o /= 2) {
+            mid += __shfl_xor_sync(~0u, mid, o);
+            high += __shfl_xor_sync(~0u, high, o);
+            low += __shfl_xor_sync(~0u, low, o);
+        }
+    }
+    // 1 / (root + eps) as x * y, y a power of two that brings the largest element into fp32's middle
+    __device__ __forceinline__ float2 factor(double eps) const {
+        if (high > 0.0f || high != high)
+            return make_float2(1.0f / (sqrtf(high + mid * 0x1p-84f * 0x1p-84f) + static_cast<float>(eps * 0x1p-84)), 0x1p-84f);
+        const float s = mid + low * 0x1p-84f * 0x1p-84f;
+        if (mid > 0.0f) return make_float2(1.0f / (sqrtf(s) + static_cast<float>(eps)), 1.0f);
+        const double e = eps * 0x1p84;
+        return make_float2(1.0f / (sqrtf(low) + static_cast<float>(e < 1e38 ? e : 1e38)), 0x1p84f);
+    }
+};
 
 bool vec_ok(const OrthoMat& m, uint32_t items) {
     const uint64_t size = m.dtype ? 2 : 4;

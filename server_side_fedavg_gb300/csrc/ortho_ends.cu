@@ -14,23 +14,23 @@ namespace {
 constexpr uint32_t kEndThreads = 256;
 
 __global__ void __launch_bounds__(kEndThreads) ortho_norm_kernel(const __grid_constant__ OrthoEnds a, Vecs v) {
-    __shared__ double sums[kEndThreads / 32];
+    __shared__ Squares sums[kEndThreads / 32];
     wait_predecessor();
     const uint32_t item = blockIdx.y, per = (a.cols + 7) / 8, all = per * a.rows;
-    double s = 0.0;
+    Squares s;
     for (uint32_t i = blockIdx.x * kEndThreads + threadIdx.x; i < all; i += gridDim.x * kEndThreads) {
         const uint32_t r = i / per, c = (i - r * per) * 8;
         float x[8], g[8];
         step_of(a, v, item, r, c, false, x, g);
         if (a.momentum_out.p) store8(a.momentum_out, row_of(a.momentum_out, item, r), c, a.cols, v.momentum_out, g);
-        s += squares(x);
+        s.add(x);
     }
-    s = warp_sum(s);
+    s.over_warp();
     if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x > 0) return;
-    for (uint32_t w = 1; w < kEndThreads / 32; ++w) s += sums[w];
-    a.part[static_cast<uint64_t>(item) * a.blocks + blockIdx.x] = s;
+    for (uint32_t w = 1; w < kEndThreads / 32; ++w) s.add(sums[w]);
+    a.part[static_cast<uint64_t>(item) * a.blocks + blockIdx.x] = make_float3(s.mid, s.high, s.low);
 }
 
 // x / (|x| + eps) * 2^shift as two fp16 terms.
@@ -39,10 +39,18 @@ __global__ void __launch_bounds__(kEndThreads) ortho_scale_kernel(const __grid_c
     wait_predecessor();
     const uint32_t item = blockIdx.y, per = static_cast<uint32_t>(a.ld / 8), all = per * a.rows;
     if (threadIdx.x < 32) {
-        double s = 0.0;
-        for (uint32_t i = threadIdx.x; i < a.blocks; i += 32) s += a.part[static_cast<uint64_t>(item) * a.blocks + i];
-        s = warp_sum(s);
-        if (threadIdx.x == 0) factor = factor_of(s, a.eps, a.shift);
+        Squares s;
+        for (uint32_t i = threadIdx.x; i < a.blocks; i += 32) {
+            const float3 p = a.part[static_cast<uint64_t>(item) * a.blocks + i];
+            s.mid += p.x;
+            s.high += p.y;
+            s.low += p.z;
+        }
+        s.over_warp();
+        if (threadIdx.x == 0) {
+            factor = s.factor(a.eps);
+            factor.x = ldexpf(factor.x, a.shift);
+        }
     }
     __syncthreads();
     const float f0 = factor.x, f1 = factor.y;

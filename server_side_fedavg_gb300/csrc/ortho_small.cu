@@ -19,7 +19,10 @@ namespace fa {
 namespace {
 
 constexpr uint32_t kSmallThreads = 256, kSmallWarps = kSmallThreads / 32, kSmallCtas = 8;
-constexpr uint32_t kSmallRun = 512;            // rows per CTA, unless eight CTAs have to hold more
+// Rows per CTA, unless eight CTAs have to hold more: for a few matrices, and for more than would
+// fill the SMs twice.  What every CTA does for itself counts: one of 16 x 4096 bf16 takes 16 us with
+// runs of 512 and 22 with 1024; 128 take 89 and 68 us.
+constexpr uint32_t kSmallRun = 512, kManyRun = 1024, kMany = 304;
 constexpr uint32_t kSmallMost = 226 * 1024;    // bytes of shared memory
 constexpr uint32_t kSmallAhead = 4;            // pieces of eight elements whose loads a thread has in flight
 
@@ -138,48 +141,43 @@ __device__ __forceinline__ void gram(const float* xs, uint32_t run, float* red, 
     }
 }
 
-// x_j <- q x_j + Q x_j, two rows of the run per thread at a time.
+// x_j <- q x_j + Q x_j.  A thread has kRows rows, 256 kRows 8 / kM apart, by 8 elements, kM / 8 apart:
+// neighbouring lanes read neighbouring rows.
 template <int kM>
 __device__ __forceinline__ void apply(float* xs, uint32_t run, const float* Q, float q) {
-    for (uint32_t j = threadIdx.x; j < run; j += 2 * kSmallThreads) {
-        const uint32_t j1 = j + kSmallThreads;
-        const bool two = j1 < run;
-        float2 x[2][kM / 2];
-        float* at[2] = {xs + j * kPitch<kM>, xs + (two ? j1 : j) * kPitch<kM>};
+    constexpr uint32_t kSide = kM / 8, kGroups = kSmallThreads / kSide, kRows = kM >= 32 ? 8 : kM / 4;
+    const uint32_t i0 = threadIdx.x % kSide, g = threadIdx.x / kSide;
+    for (uint32_t j0 = 0; j0 < run; j0 += kGroups * kRows) {
+        float y[kRows][8];
+        uint32_t at[kRows];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (uint32_t n = 0; n < kRows; ++n) {
+            at[n] = min(j0 + g + kGroups * n, run - 1) * kPitch<kM>;
 #pragma unroll
-            for (int k = 0; k < kM / 4; ++k) {
-                const float4 v = *reinterpret_cast<const float4*>(at[n] + 4 * k);
-                x[n][2 * k] = make_float2(v.x, v.y);
-                x[n][2 * k + 1] = make_float2(v.z, v.w);
-            }
-#pragma unroll 1
-        for (int i = 0; i < kM; i += 4) {
-            float y[2][4];
+            for (uint32_t e = 0; e < 8; ++e) y[n][e] = 0.0f;
+        }
+#pragma unroll 2
+        for (uint32_t k = 0; k < kM; k += 4) {
+            float4 x[kRows];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            for (uint32_t n = 0; n < kRows; ++n) x[n] = *reinterpret_cast<const float4*>(xs + at[n] + k);
 #pragma unroll
-                for (int k = 0; k < kM; k += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(Q + (i + e) * kPitch<kM> + k);
+            for (uint32_t e = 0; e < 8; ++e) {
+                const float4 v = *reinterpret_cast<const float4*>(Q + (i0 + kSide * e) * kPitch<kM> + k);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        fma2(s[n], make_float2(v.x, v.y), x[n][k / 2]);
-                        fma2(s[n], make_float2(v.z, v.w), x[n][k / 2 + 1]);
-                    }
-                }
-                y[0][e] = s[0].x + s[0].y;
-                y[1][e] = s[1].x + s[1].y;
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                if (n == 1 && !two) break;
-                float4* to = reinterpret_cast<float4*>(at[n] + i);
-                const float4 own = *to;
-                *to = make_float4(fmaf(q, own.x, y[n][0]), fmaf(q, own.y, y[n][1]), fmaf(q, own.z, y[n][2]), fmaf(q, own.w, y[n][3]));
+                for (uint32_t n = 0; n < kRows; ++n)
+                    y[n][e] = fmaf(v.w, x[n].w, fmaf(v.z, x[n].z, fmaf(v.y, x[n].y, fmaf(v.x, x[n].x, y[n][e]))));
             }
         }
+        __syncthreads();                 // every lane of these rows has read them
+#pragma unroll
+        for (uint32_t n = 0; n < kRows; ++n)
+            if (j0 + g + kGroups * n < run)
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e) {
+                    float* to = xs + at[n] + i0 + kSide * e;
+                    *to = fmaf(q, *to, y[n][e]);
+                }
     }
 }
 
@@ -191,9 +189,9 @@ struct SmallArgs {
 };
 
 template <int kM>
-__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid_constant__ SmallArgs a) {
+__global__ void __launch_bounds__(kSmallThreads, kM <= 16 ? 2 : 1) ortho_small_kernel(const __grid_constant__ SmallArgs a) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ double sums[kSmallWarps], mine;
+    __shared__ Squares sums[kSmallWarps], mine;
     __shared__ float2 factor;
     const OrthoEnds& e = a.e;
     float *A = sm, *P0 = A + kMat<kM>, *P1 = P0 + kMat<kM>, *R = P1 + kMat<kM>, *Q0 = R + kMat<kM>, *Q1 = Q0 + kMat<kM>;
@@ -210,7 +208,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
     const auto row_at = [&](uint32_t t) { return wide ? t % kM : j0 + t / (kM / 8); };
     const auto col_at = [&](uint32_t t) { return wide ? j0 + t / kM * 8 : t % (kM / 8) * 8; };
     const auto in_use = [&](uint32_t t) { return t < all && (wide ? t % kM : t % (kM / 8) * 8) < m; };
-    double sum = 0.0;
+    Squares sum;
     for (uint32_t t0 = threadIdx.x; t0 < all; t0 += kSmallAhead * kSmallThreads) {
         float x[kSmallAhead][8], g[kSmallAhead][8];
 #pragma unroll
@@ -228,7 +226,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
                 momentum_step(e, x[u], g[u]);
                 if (e.momentum_out.p)
                     store8(e.momentum_out, row_of(e.momentum_out, item, row_at(t)), col_at(t), e.cols, a.v.momentum_out, g[u]);
-                sum += squares(x[u]);
+                sum.add(x[u]);
             } else {
 #pragma unroll
                 for (uint32_t k = 0; k < 8; ++k) x[u][k] = 0.0f;
@@ -245,11 +243,11 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
         }
     }
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    sum = warp_sum(sum);
+    sum.over_warp();
     if (lane == 0) sums[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (uint32_t w = 1; w < kSmallWarps; ++w) sum += sums[w];
+        for (uint32_t w = 1; w < kSmallWarps; ++w) sum.add(sums[w]);
         mine = sum;
     }
     if (a.ctas > 1)
@@ -257,21 +255,22 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
     else
         __syncthreads();
     if (threadIdx.x == 0) {
-        sum = 0.0;
+        sum = Squares();
         for (uint32_t q = 0; q < a.ctas; ++q) {
-            double v;
-            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a.ctas > 1 ? in_cta(smem_addr(&mine), q) : smem_addr(&mine)) : "memory");
-            sum += v;
+            sum.mid += ld_part1(smem_addr(&mine.mid), q, a.ctas);
+            sum.high += ld_part1(smem_addr(&mine.high), q, a.ctas);
+            sum.low += ld_part1(smem_addr(&mine.low), q, a.ctas);
         }
-        factor = factor_of(sum, e.eps, 0);
+        factor = sum.factor(e.eps);
     }
     __syncthreads();
+    // The rows stay as they are, but for a power of two where their squares could leave fp32's
+    // range; A and the result take the factor.
     const float f0 = factor.x, f1 = factor.y;
-    for (uint32_t t = threadIdx.x; t < run * kM; t += kSmallThreads) {
-        float* x = xs + t / kM * kPitch<kM> + t % kM;
-        *x = *x * f1 * f0;
+    if (f1 != 1.0f) {
+        for (uint32_t t = threadIdx.x; t < run * kM; t += kSmallThreads) xs[t / kM * kPitch<kM> + t % kM] *= f1;
+        __syncthreads();
     }
-    __syncthreads();
 
     uint32_t left = a.s.steps, parity = 0;
     for (uint32_t n_part = a.s.parts; n_part > 0; --n_part, parity ^= 1) {
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
         for (uint32_t i = threadIdx.x; i < kM * kM; i += kSmallThreads) {
             float v = 0.0f;
             for (uint32_t q = 0; q < a.ctas; ++q) v += ld_part1(smem_addr(own + i), q, a.ctas);
-            A[i / kM * kPitch<kM> + i % kM] = v;
+            A[i / kM * kPitch<kM> + i % kM] = v * f0 * f0;
         }
         __syncthreads();
         float *P = P0, *Q = P0, *next = Q0;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
             const float* from = wide ? xs + t / kM * 8 * kPitch<kM> + t % kM : xs + t / (kM / 8) * kPitch<kM> + t % (kM / 8) * 8;
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
-                x[k] = e.alpha * from[wide ? k * kPitch<kM> : k];
+                x[k] = e.alpha * (f0 * from[wide ? k * kPitch<kM> : k]);
                 if (e.residual.p) x[k] = fmaf(e.beta, res[u][k], x[k]);
             }
             store8(e.out, row_of(e.out, item, row_at(t)), col_at(t), e.cols, a.v.out, x);
@@ -340,11 +339,20 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const __grid
 
 uint32_t side(uint32_t m) { return m <= 8 ? 8 : m <= 16 ? 16 : m <= 32 ? 32 : 64; }
 
-// CTAs of a cluster, and rows of each: runs of about kSmallRun, powers of two.
-void split(uint32_t n, uint32_t* ctas, uint32_t* run) {
-    *ctas = 1;
-    while (*ctas < kSmallCtas && *ctas * kSmallRun < n) *ctas *= 2;
-    *run = ((n + *ctas - 1) / *ctas + 7) / 8 * 8;
+uint32_t fixed(uint32_t m) { return m <= 8 ? kFixed<8> : m <= 16 ? kFixed<16> : m <= 32 ? kFixed<32> : kFixed<64>; }
+
+// CTAs of a cluster (a power of two), and rows of each; shared memory of a CTA.
+uint64_t split(uint32_t m, uint32_t n, uint32_t items, uint32_t* ctas, uint32_t* run) {
+    const auto fill = [&](uint32_t rows) {
+        *ctas = 1;
+        while (*ctas < kSmallCtas && *ctas * rows < n) *ctas *= 2;
+        *run = ((n + *ctas - 1) / *ctas + 7) / 8 * 8;
+        return static_cast<uint64_t>(*run) * (side(m) + 4) * 4 + fixed(m);
+    };
+    const uint64_t few = fill(kSmallRun);
+    if (static_cast<uint64_t>(items) * *ctas <= kMany) return few;
+    const uint64_t many = fill(kManyRun);
+    return many <= kSmallMost ? many : fill(kSmallRun);
 }
 
 template <int kM>
@@ -374,10 +382,7 @@ cudaError_t launch(SmallArgs a, cudaStream_t stream) {
 bool ortho_small_fits(uint32_t rows, uint32_t cols) {
     const uint32_t m = std::min(rows, cols), n = std::max(rows, cols);
     uint32_t ctas, run;
-    split(n, &ctas, &run);
-    if (m > 64) return false;
-    const uint32_t fixed = m <= 8 ? kFixed<8> : m <= 16 ? kFixed<16> : m <= 32 ? kFixed<32> : kFixed<64>;
-    return static_cast<uint64_t>(run) * (side(m) + 4) * 4 + fixed <= kSmallMost;
+    return m <= 64 && split(m, n, 1, &ctas, &run) <= kSmallMost;
 }
 
 cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall& s, cudaStream_t stream) {
@@ -385,10 +390,15 @@ cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall& s, cudaStre
     a.e = e;
     a.s = s;
     a.v = vecs(e);
-    split(std::max(e.rows, e.cols), &a.ctas, &a.run);
-    const uint32_t m = side(std::min(e.rows, e.cols));
-    if (m == 64) a.s.parts = a.s.steps;          // no room for the squares of longer segments
-    return m == 8 ? launch<8>(a, stream) : m == 16 ? launch<16>(a, stream) : m == 32 ? launch<32>(a, stream) : launch<64>(a, stream);
+    const uint32_t m = std::min(e.rows, e.cols);
+    split(m, std::max(e.rows, e.cols), e.items, &a.ctas, &a.run);
+    if (side(m) == 64) a.s.parts = a.s.steps;    // no room for the squares of longer segments
+    switch (side(m)) {
+    case 8: return launch<8>(a, stream);
+    case 16: return launch<16>(a, stream);
+    case 32: return launch<32>(a, stream);
+    default: return launch<64>(a, stream);
+    }
 }
 
 }  // namespace fa

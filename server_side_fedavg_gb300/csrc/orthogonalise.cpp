@@ -191,7 +191,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
         small ? std::min<uint64_t>(p.count, 1u << 20) : std::min<uint64_t>({p.count, std::max<uint64_t>(1, (1ull << 30) / each), 32768}));
     const bool cap = capturing(s);
     Run run{};
-    double* part = nullptr;
+    float3* part = nullptr;
     const uint32_t blocks = fa::ortho_blocks(group, rows, cols, static_cast<uint32_t>(w->tc.sms));
     const auto carve = [&](Carve& c) {
         for (int i = 0; i < (longest ? 2 : 1); ++i) {
@@ -205,7 +205,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
             run.sq[i].rows = run.sq[i].cols = z.m;
             run.sq[i].ld = ldm;
         }
-        part = static_cast<double*>(c.take(8ull * group * blocks));
+        part = static_cast<float3*>(c.take(sizeof(float3) * group * blocks));
     };
     Carve need{nullptr}, c{nullptr};
     if (!small) {
