@@ -19,7 +19,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["accumulate.cu", "reduce.cu", "gather.cu", "finalize.cu", "noalloc.cu", "fedavg.cpp",
            "ledger.cpp", "partition.cpp", "gather_plan.cpp", "product_plain.cu", "product_prep.cu", "product_tc.cu",
            "distill.cu", "work.cpp",
-           "rotary.cu", "group_norm.cu", "layers.cpp", "ortho_ends.cu", "ortho_small.cu", "ortho_tc.cu", "orthogonalise.cpp"]
+           "rotary.cu", "group_norm.cu", "group_norm_one.cu", "layers.cpp", "ortho_ends.cu", "ortho_small.cu", "ortho_tc.cu", "orthogonalise.cpp"]
 
 
 def _common():

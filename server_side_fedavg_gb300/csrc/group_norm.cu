@@ -17,62 +17,14 @@
 // What bounds it: HBM, x read once or twice and the result written once.
 #include <algorithm>
 
-#include "group_norm.cuh"
-#include "product_device.cuh"
+#include "group_norm_device.cuh"
 
 namespace fa {
 
 namespace {
 
 constexpr uint32_t kNormThreads = 256, kNormWarps = kNormThreads / 32;
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-    T e[V];
-};
-
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[V]) {
-    const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if constexpr (sizeof(T) == 2)
-            x[i] = __uint_as_float(static_cast<uint32_t>(q.e[i]) << 16);
-        else
-            x[i] = q.e[i];
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
-    Vec<T, V> q;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if constexpr (sizeof(T) == 2)
-            q.e[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
-        else
-            q.e[i] = x[i];
-    *reinterpret_cast<Vec<T, V>*>(p) = q;
-}
-
-template <int V>
-__device__ __forceinline__ void times_act_grad(int act, float (&d)[V], const float (&z)[V]) {
-    if (act == kActRelu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] *= act_grad(kActRelu, z[i]);
-    } else if (act == kActGelu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] *= act_grad(kActGelu, z[i]);
-    } else if (act == kActSilu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] *= act_grad(kActSilu, z[i]);
-    }
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(~0u, v, o);
-    return v;
-}
+constexpr uint32_t kNormCtas = 4, kNormGradCtas = 2;                     // per SM
 
 // A CTA's columns in turn: `width` vectors by `tall` positions at a time.
 struct Tile {
@@ -104,9 +56,34 @@ __device__ __forceinline__ void sum_rows(float (&s)[N][V], float* red, const Til
     }
 }
 
-template <typename T, int V>
+template <typename T>
 __device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
     return static_cast<const T*>(t.p) + sample * t.step;
+}
+
+// f(vector of p0, vector of p1, position) for this thread's positions of [r0, r1), channels from c.
+template <bool kReverse, int kStreams, int V, typename T, typename F>
+__device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t ld0, const T* p1, uint64_t ld1, uint32_t r0,
+                                          uint32_t r1, uint32_t c, F f) {
+    if (!t.on) return;
+    constexpr uint32_t kU = 4;
+    const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
+    const auto row_of = [&](uint32_t i) { return r0 + t.row + (kReverse ? mine - 1 - i : i) * t.tall; };
+    uint32_t i = 0;
+    for (; i + kU <= mine; i += kU) {
+        Vec<T, V> q[kU], p[kU];
+#pragma unroll
+        for (uint32_t u = 0; u < kU; ++u) {
+            q[u] = load_raw<T, V>(p0 + row_of(i + u) * ld0 + c);
+            p[u] = kStreams == 2 ? load_raw<T, V>(p1 + row_of(i + u) * ld1 + c) : q[u];
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kU; ++u) f(q[u], p[u], row_of(i + u));
+    }
+    for (; i < mine; ++i) {
+        const Vec<T, V> q = load_raw<T, V>(p0 + row_of(i) * ld0 + c);
+        f(q, kStreams == 2 ? load_raw<T, V>(p1 + row_of(i) * ld1 + c) : q, row_of(i));
+    }
 }
 
 // ----------------------------------------------------------------- forward
@@ -115,45 +92,28 @@ __device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads) norm_stat_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *mean = sm, *sq = sm + a.channels, *red = sm + 2 * a.channels;
+    float *mean = sm, *sq = mean + a.channels, *red = sq + a.channels;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
     const float count = static_cast<float>(r1 - r0);
     for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
-        const T* x = at<T, V>(a.x, sample);
+        const T* x = at<T>(a.x, sample);
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
             const Tile t(vectors, c0);
             const uint32_t c = (c0 + t.col) * V;
             float s[2][V] = {}, from[V] = {};
-            if (t.on) {
-                load_vec<T, V>(x + c, from);
-                constexpr uint32_t kU = 4;
-                uint32_t r = r0 + t.row;
-                for (; r + (kU - 1) * t.tall < r1; r += kU * t.tall) {
-                    float v[kU][V];
+            if (t.on) widen(load_raw<T, V>(x + c), from);
+            float less[V];
 #pragma unroll
-                    for (uint32_t u = 0; u < kU; ++u) load_vec<T, V>(x + (r + u * t.tall) * a.x.ld + c, v[u]);
-#pragma unroll
-                    for (uint32_t u = 0; u < kU; ++u)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float d = v[u][i] - from[i];
-                            s[0][i] += d;
-                            s[1][i] = fmaf(d, d, s[1][i]);
-                        }
-                }
-                for (; r < r1; r += t.tall) {
-                    float v[V];
-                    load_vec<T, V>(x + r * a.x.ld + c, v);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float d = v[i] - from[i];
-                        s[0][i] += d;
-                        s[1][i] = fmaf(d, d, s[1][i]);
-                    }
-                }
-            }
+            for (int i = 0; i < V; ++i) less[i] = -from[i];
+            over_rows<false, 1, V>(t, x, a.x.ld, x, a.x.ld, r0, r1, c, [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t) {
+                float d[V];
+                widen(q, d);
+                add(d, d, less);
+                add(s[0], s[0], d);
+                fma(s[1], d, d, s[1]);
+            });
             sum_rows<2, V>(s, red, t);
             if (t.row == 0)
 #pragma unroll
@@ -165,12 +125,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_stat_kernel(const __grid_co
             __syncthreads();
         }
         for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
-            float m = 0.0f, q = 0.0f, ref;
-            load_vec<T, 1>(x + g * per, reinterpret_cast<float(&)[1]>(ref));
+            float m = 0.0f, q = 0.0f;
+            const float ref = elem(x, g * per, sizeof(T) == 2);
             for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
-                float from[1];
-                load_vec<T, 1>(x + c, from);
-                mean[c] += from[0] - ref;
+                mean[c] += elem(x, c, sizeof(T) == 2) - ref;
                 m += mean[c];
             }
             m = warp_sum(m) / static_cast<float>(per);
@@ -216,7 +174,7 @@ __device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, 
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *mean = sm, *rstd = sm + a.groups, *ref = sm + 2 * a.groups;
+    float *mean = sm, *rstd = mean + a.groups, *ref = rstd + a.groups;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
@@ -230,79 +188,42 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const __grid_c
             for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.mean_out[first + g] = ref[g] + mean[g];
         if (blockIdx.x == 0 && a.rstd_out)
             for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.rstd_out[first + g] = rstd[g];
-        const T* x = at<T, V>(a.x, sample);
-        T* y = const_cast<T*>(at<T, V>(a.out, sample));
+        const T* x = at<T>(a.x, sample);
+        T* y = const_cast<T*>(at<T>(a.out, sample));
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
             const Tile t(vectors, c0);
             const uint32_t c = (c0 + t.col) * V;
-            float from[V], m[V], scale[V], shift[V];
-            if (!t.on) continue;
+            // y = act((x - ref) scale + shift): the mean, less the reference, is in the shift
+            float less[V] = {}, scale[V] = {}, shift[V] = {};
+            if (t.on)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t g = (c + i) / per;
-                from[i] = ref[g];
-                m[i] = mean[g];
-                scale[i] = rstd[g] * (a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f);
-                shift[i] = a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f;
-            }
-            constexpr uint32_t kU = 4;
-            const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
-            for (uint32_t left = mine; left > 0;) {
-                const uint32_t now = left >= kU ? kU : 1;
-                left -= now;
-                float v[kU][V];
-                const uint32_t r = r0 + t.row + left * t.tall;
-#pragma unroll
-                for (uint32_t u = 0; u < kU; ++u)
-                    if (u < now) load_vec<T, V>(x + (r + u * t.tall) * a.x.ld + c, v[u]);
-#pragma unroll
-                for (uint32_t u = 0; u < kU; ++u) {
-                    if (u >= now) break;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[u][i] = fmaf(v[u][i] - from[i] - m[i], scale[i], shift[i]);
-                    activate(act, v[u]);
-                    store_vec<T, V>(y + (r + u * t.tall) * a.out.ld + c, v[u]);
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t g = (c + i) / per;
+                    less[i] = -ref[g];
+                    scale[i] = rstd[g] * (a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f);
+                    shift[i] = fmaf(-mean[g], scale[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
                 }
-            }
+            over_rows<true, 1, V>(t, x, a.x.ld, x, a.x.ld, r0, r1, c, [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t r) {
+                float v[V];
+                widen(q, v);
+                add(v, v, less);
+                fma(v, v, scale, shift);
+                act_of(act, v);
+                store_vec<T, V>(y + r * a.out.ld + c, v);
+            });
         }
         __syncthreads();
     }
 }
 
 // ----------------------------------------------------------------- backward
-// What a thread keeps of its channels.
-template <int V>
-struct Channels {
-    float mean[V], rstd[V], gamma[V], beta[V];
-    __device__ __forceinline__ Channels(const NormArgs& a, uint32_t sample, uint32_t c) {
-        const uint32_t per = a.channels / a.groups;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint64_t g = static_cast<uint64_t>(sample) * a.groups + (c + i) / per;
-            mean[i] = a.mean[g];
-            rstd[i] = a.rstd[g];
-            gamma[i] = a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f;
-            beta[i] = a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f;
-        }
-    }
-    // x to xhat, d to dz
-    __device__ __forceinline__ void step(int act, float (&x)[V], float (&d)[V]) const {
-        float z[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            x[i] = (x[i] - mean[i]) * rstd[i];
-            z[i] = fmaf(x[i], gamma[i], beta[i]);
-        }
-        times_act_grad(act, d, z);
-    }
-};
-
 // part[sample][chunk][group] = sums of gamma dz and gamma dz xhat over the chunk;
 // cpart[its CTA][channel] = sums of dz and dz xhat over the CTA's chunks.
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *s0 = sm, *s1 = sm + a.channels, *t0 = sm + 2 * a.channels, *t1 = sm + 3 * a.channels, *red = sm + 4 * a.channels;
+    float *s0 = sm, *s1 = s0 + a.channels, *t0 = s1 + a.channels, *t1 = t0 + a.channels,
+          *red = t1 + a.channels;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
@@ -310,36 +231,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __gr
     for (uint32_t c = threadIdx.x; c < a.channels; c += kNormThreads) t0[c] = t1[c] = 0.0f;
     __syncthreads();
     for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
-        const T *x = at<T, V>(a.x, sample), *dout = at<T, V>(a.dout, sample);
+        const T *x = at<T>(a.x, sample), *dout = at<T>(a.dout, sample);
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
             const Tile t(vectors, c0);
             const uint32_t c = (c0 + t.col) * V;
             float s[2][V] = {};
-            if (t.on) {
-                const Channels<V> ch(a, sample, c);
-                constexpr uint32_t kU = 2;
-                uint32_t r = r0 + t.row;
-                for (; r < r1; r += kU * t.tall) {
-                    float v[kU][V], d[kU][V];
+            const Channels<V> ch(a, sample, t.on ? c : 0);
+            over_rows<false, 2, V>(t, x, a.x.ld, dout, a.dout.ld, r0, r1, c,
+                                          [&](const Vec<T, V>& q, const Vec<T, V>& p, uint32_t) {
+                                              float v[V], d[V];
+                                              widen(q, v);
+                                              widen(p, d);
+                                              ch.step(act, v, d);
+                                              add(s[0], s[0], d);
+                                              fma(s[1], d, v, s[1]);
+                                          });
+            // sums of dz h so far: of dz xhat
+            if (t.on)
 #pragma unroll
-                    for (uint32_t u = 0; u < kU; ++u) {
-                        const uint32_t q = r + u * t.tall;
-                        if (q >= r1) break;
-                        load_vec<T, V>(x + q * a.x.ld + c, v[u]);
-                        load_vec<T, V>(dout + q * a.dout.ld + c, d[u]);
-                    }
-#pragma unroll
-                    for (uint32_t u = 0; u < kU; ++u) {
-                        if (r + u * t.tall >= r1) break;
-                        ch.step(act, v[u], d[u]);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            s[0][i] += d[u][i];
-                            s[1][i] = fmaf(d[u][i], v[u][i], s[1][i]);
-                        }
-                    }
-                }
-            }
+                for (int i = 0; i < V; ++i) s[1][i] *= a.rstd[static_cast<uint64_t>(sample) * a.groups + (c + i) / per];
             sum_rows<2, V>(s, red, t);
             if (t.row == 0)
 #pragma unroll
@@ -373,7 +283,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __gr
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *c1 = sm, *c2 = sm + a.groups;
+    float *c1 = sm, *c2 = c1 + a.groups;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
@@ -396,68 +306,62 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_co
             }
         }
         __syncthreads();
-        const T *x = at<T, V>(a.x, sample), *dout = at<T, V>(a.dout, sample);
-        T* dx = const_cast<T*>(at<T, V>(a.out, sample));
+        const T *x = at<T>(a.x, sample), *dout = at<T>(a.dout, sample);
+        T* dx = const_cast<T*>(at<T>(a.out, sample));
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
             const Tile t(vectors, c0);
             const uint32_t c = (c0 + t.col) * V;
-            if (!t.on) continue;
-            const Channels<V> ch(a, sample, c);
-            float k1[V], k2[V];
+            const Channels<V> ch(a, sample, t.on ? c : 0);
+            // dx = scale dz - rstd m1 - h rstd^2 m2
+            float k1[V] = {}, k2[V] = {};
+            if (t.on)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                k1[i] = c1[(c + i) / per];
-                k2[i] = c2[(c + i) / per];
-            }
-            const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
-            constexpr uint32_t kU = 2;
-            for (uint32_t left = mine; left > 0;) {
-                const uint32_t now = left >= kU ? kU : 1;
-                left -= now;
-                float v[kU][V], d[kU][V];
-                const uint32_t r = r0 + t.row + left * t.tall;
-#pragma unroll
-                for (uint32_t u = 0; u < kU; ++u)
-                    if (u < now) {
-                        load_vec<T, V>(x + (r + u * t.tall) * a.x.ld + c, v[u]);
-                        load_vec<T, V>(dout + (r + u * t.tall) * a.dout.ld + c, d[u]);
-                    }
-#pragma unroll
-                for (uint32_t u = 0; u < kU; ++u) {
-                    if (u >= now) break;
-                    ch.step(act, v[u], d[u]);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        d[u][i] = ch.rstd[i] * (fmaf(d[u][i], ch.gamma[i], -k1[i]) - v[u][i] * k2[i]);
-                    store_vec<T, V>(dx + (r + u * t.tall) * a.out.ld + c, d[u]);
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t g = (c + i) / per;
+                    const float r = a.rstd[static_cast<uint64_t>(sample) * a.groups + g];
+                    k1[i] = -r * c1[g];
+                    k2[i] = -r * r * c2[g];
                 }
-            }
+            over_rows<true, 2, V>(t, x, a.x.ld, dout, a.dout.ld, r0, r1, c,
+                                         [&](const Vec<T, V>& q, const Vec<T, V>& p, uint32_t r) {
+                                             float v[V], d[V];
+                                             widen(q, v);
+                                             widen(p, d);
+                                             ch.step(act, v, d);
+                                             fma(v, v, k2, k1);
+                                             fma(d, d, ch.scale, v);
+                                             store_vec<T, V>(dx + r * a.out.ld + c, d);
+                                         });
         }
         __syncthreads();
     }
 }
 
-// The parameters' gradients: columns of cpart summed in row order, eight strands of rows each.
-__global__ void __launch_bounds__(256) norm_param_kernel(const float2* part, uint32_t rows, uint32_t channels, void* d_gamma,
-                                                         void* d_beta, int dtype) {
-    __shared__ float2 sums[8][32];
+// The parameters' gradients: columns of cpart, eight a block, summed in 128 strands of rows and these
+// in order.
+__global__ void __launch_bounds__(1024) norm_param_kernel(const float2* part, uint32_t rows, uint32_t channels, void* d_gamma,
+                                                          void* d_beta, int dtype) {
+    __shared__ float2 sums[1024];
     wait_predecessor();
-    const uint32_t lane = threadIdx.x % 32, strand = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    const uint32_t c = blockIdx.x * 8 + threadIdx.x % 8;
     float2 s = make_float2(0.0f, 0.0f);
     if (c < channels)
 #pragma unroll 8
-        for (uint32_t r = strand; r < rows; r += 8) {
+        for (uint32_t r = threadIdx.x / 8; r < rows; r += 128) {
             const float2 v = part[static_cast<uint64_t>(r) * channels + c];
             s.x += v.x;
             s.y += v.y;
         }
-    sums[strand][lane] = s;
-    __syncthreads();
-    if (strand > 0 || c >= channels) return;
-    for (int w = 1; w < 8; ++w) {
-        s.x += sums[w][lane].x;
-        s.y += sums[w][lane].y;
+    sums[threadIdx.x] = s;
+    for (uint32_t left = 512; left >= 8; left /= 2) {
+        __syncthreads();
+        if (threadIdx.x < left) {
+            s.x += sums[threadIdx.x + left].x;
+            s.y += sums[threadIdx.x + left].y;
+            sums[threadIdx.x] = s;
+        }
     }
+    if (threadIdx.x >= 8 || c >= channels) return;
     if (d_beta) put(d_beta, c, dtype, s.x);
     if (d_gamma) put(d_gamma, c, dtype, s.y);
 }
@@ -527,12 +431,13 @@ cudaError_t passes(NormArgs a, bool backward, cudaStream_t stream, unsigned* lau
 
 void plan_norm(NormArgs& a, bool backward, uint32_t sms) {
     // Samples per pair of launches: as many as L2 holds for the second pass (64 MB of its 129), one at
-    // least; and four CTAs per SM over all of these.
+    // least; and as many CTAs as run at one time over all of these.
     const uint64_t sample = static_cast<uint64_t>(a.positions) * a.channels * (a.dtype ? 2 : 4) * (backward ? 2 : 1);
     a.batch = static_cast<uint32_t>(std::min<uint64_t>(a.n, std::max<uint64_t>(1, (64ull << 20) / sample)));
-    a.across = std::min(a.batch, 4 * sms);
+    const uint32_t ctas = (backward ? kNormGradCtas : kNormCtas) * sms;
+    a.across = std::min(a.batch, ctas);
     const uint32_t v = vector_of(a, backward), vectors = std::min(a.channels / v, kNormThreads), tall = kNormThreads / vectors;
-    const uint64_t want = std::max(1u, 4 * sms / std::max(1u, a.across)), least = 4ull * tall;
+    const uint64_t want = std::max(1u, ctas / std::max(1u, a.across)), least = 4ull * tall;
     uint64_t rows = (a.positions + want - 1) / want;
     rows = std::max((rows + tall - 1) / tall * tall, least);
     a.rows = static_cast<uint32_t>(std::min<uint64_t>(rows, a.positions));
@@ -541,12 +446,11 @@ void plan_norm(NormArgs& a, bool backward, uint32_t sms) {
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream, unsigned* launches) { return passes(a, false, stream, launches); }
 
-cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream, unsigned* launches) {
-    cudaError_t e = a.n && a.positions ? passes(a, true, stream, launches) : cudaSuccess;
-    if (e != cudaSuccess || !(a.d_gamma || a.d_beta)) return e;
-    ++*launches;
-    return launch_next(norm_param_kernel, dim3((a.channels + 31) / 32), 256, stream, a.cpart,
-                       a.n && a.positions ? static_cast<uint32_t>(norm_rows(a) * a.chunks) : 0u, a.channels, a.d_gamma, a.d_beta, a.param_dtype);
+cudaError_t launch_norm_param(const NormArgs& a, uint32_t rows, cudaStream_t stream) {
+    return launch_next(norm_param_kernel, dim3((a.channels + 7) / 8), 1024, stream, a.cpart, rows, a.channels, a.d_gamma, a.d_beta,
+                       a.param_dtype);
 }
+
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream, unsigned* launches) { return passes(a, true, stream, launches); }
 
 }  // namespace fa

@@ -25,13 +25,22 @@ struct NormArgs {
     float2* cpart;                 // [norm_rows * chunks][channels] of the parameters' gradients, or nullptr
     uint32_t n, positions, channels, groups;
     uint32_t rows, chunks;         // positions per CTA, and CTAs of a sample
+    uint32_t stage_rows, slots;    // one kernel: positions per stage, stages in shared memory
+    uint32_t* counters;            // one kernel: 81, zero between launches
+    unsigned int* err;
     uint32_t batch, across;        // samples per pair of launches, and of these at work at one time
     uint32_t first, last, row0;    // samples of this launch, and its first row of across in cpart
     int dtype, param_dtype, act;
     float eps;
 };
 
-// rows, chunks, batch and across for these sizes; the workspace of `part` and `cpart` follows from them.
+// In one kernel, where the positions are one run of 16-byte pieces: false where they are not.  Else
+// fills in rows, chunks (CTAs per sample), across (samples at one time), stage_rows and slots; part is
+// [n][chunks][groups], cpart [across * chunks][channels].
+bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms);
+cudaError_t launch_norm_one(const NormArgs& a, bool backward, cudaStream_t stream);
+
+// In two passes: rows, chunks, batch and across for these sizes; the workspace of `part` and `cpart` follows from them.
 void plan_norm(NormArgs& a, bool backward, uint32_t sms);
 // Rows of `across` over all launches.
 inline uint64_t norm_rows(const NormArgs& a) {
@@ -40,5 +49,7 @@ inline uint64_t norm_rows(const NormArgs& a) {
 }
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream, unsigned* launches);
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream, unsigned* launches);
+// d_gamma and d_beta from `rows` rows of cpart.
+cudaError_t launch_norm_param(const NormArgs& a, uint32_t rows, cudaStream_t stream);
 
 }  // namespace fa

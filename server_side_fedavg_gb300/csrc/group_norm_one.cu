@@ -1,0 +1,406 @@
+// Group norm and its gradients in one kernel, where a sample's positions are one run of bytes.
+//
+// k CTAs share a sample, each a run of its positions; one CTA per SM, launched cooperatively.  A
+// warp of its own fetches the run by bulk copies into a ring of 32 KB stages; 16 warps compute.
+// After the statistics' pass the CTAs meet at a counter in global memory, join their parts, and
+// walk their runs backwards for the result: the stages fetched last are still in shared memory,
+// some 28 MB of a sample over all SMs, and are not fetched again; the next sample's first stages
+// are fetched meanwhile.  A sample that fits is read once.
+//
+// What bounds it: HBM, x (and dout) read once and beyond 28 MB a second time, the result written once.
+#include <algorithm>
+
+#include "group_norm_device.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr uint32_t kOneThreads = 512, kOneWarps = kOneThreads / 32;
+constexpr uint32_t kOneStage = 32768, kOneSlots = 6;
+constexpr uint32_t kOneMost = 225 * 1024;             // dynamic shared memory
+constexpr uint32_t kOneGroups = 80;                   // counters for samples at one time, and one for the end
+
+// The computing warps of a CTA; whether all of their threads say so.
+__device__ __forceinline__ void sync_compute() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+
+__device__ __forceinline__ bool sync_and(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(all)
+        : "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return all;
+}
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Until `counter` has reached `target`; false after some 20 s.
+constexpr long long kMeetClocks = 40ll * 1000 * 1000 * 1000;
+__device__ __forceinline__ bool meet(uint32_t* counter, uint32_t target) {
+    __threadfence();
+    atomicAdd(counter, 1u);
+    const long long t0 = clock64();
+    while (ld_acquire(counter) < target)
+        if (clock64() - t0 > kMeetClocks) return false;
+    return true;
+}
+
+// The ring's slots in the order of their use.  A sample's n stages go to slots b, b + d, ... (d is 1
+// or -1); the result's pass takes them from the last to the first, so that slots come free in the
+// order b + d (n - 1), ..., b, and the next sample starts at b - d the other way round.
+struct Slots {
+    uint32_t count;
+    int b = 0, d = 1;
+    uint32_t full = 0, empty = 0, used = 0;           // a bit per slot: phases, and whether it has been filled
+    __device__ __forceinline__ uint32_t at(uint32_t i) const {
+        const int n = static_cast<int>(count), s = (b + d * static_cast<int>(i % count)) % n;
+        return s < 0 ? s + n : s;
+    }
+    __device__ __forceinline__ void next() {
+        b = (b - d + static_cast<int>(count)) % static_cast<int>(count);
+        d = -d;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
+    return static_cast<const T*>(t.p) + sample * t.step;
+}
+
+template <typename T, int V, bool kBackward>
+__global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid_constant__ NormArgs a) {
+    constexpr uint32_t kStreams = kBackward ? 2 : 1, kPlane = kOneStage / kStreams;
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ uint64_t bars[2 * kOneSlots];
+    float* red = reinterpret_cast<float*>(dyn + a.slots * kOneStage);
+    float *s0 = red + 4 * kOneThreads, *s1 = s0 + a.channels;                      // of a channel
+    float *t0 = s1 + a.channels, *t1 = t0 + (kBackward ? a.channels : 0);          // gradients so far (backward)
+    float *g0 = t1 + (kBackward ? a.channels : 0), *g1 = g0 + a.groups, *ref = g1 + a.groups;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kOneSlots;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < a.slots; ++s) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(full + 8 * s) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(empty + 8 * s), "r"(kOneWarps) : "memory");
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    wait_predecessor();
+
+    const uint32_t group = blockIdx.x / a.chunks, rank = blockIdx.x % a.chunks, row = a.channels * sizeof(T);
+    const uint32_t r0 = rank * a.rows, r1 = min(a.positions, r0 + a.rows), n = (r1 - r0 + a.stage_rows - 1) / a.stage_rows;
+    Slots ring;
+    ring.count = a.slots;
+    bool ok = true;
+
+    if (warp == kOneWarps) {
+        if (lane == 0) {
+            const auto fetch = [&](const T* x, const T* dout, uint32_t stage, uint32_t s) {
+                if (ring.used >> s & 1) {
+                    ok = mbar_wait(empty + 8 * s, ring.empty >> s & 1);
+                    ring.empty ^= 1u << s;
+                    if (!ok) return;
+                }
+                ring.used |= 1u << s;
+                const uint32_t first = r0 + stage * a.stage_rows, bytes = min(a.stage_rows, r1 - first) * row;
+                mbar_expect(full + 8 * s, bytes * kStreams);
+                bulk_load(dyn + s * kOneStage, x + static_cast<uint64_t>(first) * a.channels, bytes, full + 8 * s);
+                if (kBackward) bulk_load(dyn + s * kOneStage + kPlane, dout + static_cast<uint64_t>(first) * a.channels, bytes, full + 8 * s);
+                ring.full ^= 1u << s;
+            };
+            for (uint32_t sample = group; ok && sample < a.n; sample += a.across) {
+                const T *x = at<T>(a.x, sample), *dout = kBackward ? at<T>(a.dout, sample) : nullptr;
+                for (uint32_t i = 0; ok && i < n; ++i) fetch(x, dout, i, ring.at(i));
+                for (uint32_t i = a.slots; ok && i < n; ++i) fetch(x, dout, n - 1 - i, ring.at(n - 1 - i));
+                ring.next();
+            }
+            if (!ok) {
+                atomicOr(a.err, kErrWaitTimeout);
+                // the loads in flight land before the CTA leaves: the last phase of every slot's
+                for (uint32_t s = 0; s < a.slots; ++s)
+                    if (ring.used >> s & 1) mbar_wait(full + 8 * s, (ring.full >> s & 1) ^ 1);
+            }
+        }
+        return;
+    }
+
+    const uint32_t vectors = a.channels / V, per = a.channels / a.groups;
+    const uint32_t tall = kOneThreads / vectors, my_row = threadIdx.x / vectors, c = threadIdx.x % vectors * V;
+    const bool on = my_row < tall;
+    const float count = static_cast<float>(r1 - r0), all = static_cast<float>(a.positions);
+    const int act = a.act;
+    const auto wait_full = [&](uint32_t s) {
+        const bool got = mbar_wait(full + 8 * s, ring.full >> s & 1);
+        ring.full ^= 1u << s;
+        return got;
+    };
+    const auto release = [&](uint32_t s) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * s);
+    };
+    // f(vector of x, vector of dout, position) of a stage
+    const auto over = [&](uint32_t stage, uint32_t s, auto f) {
+        const uint32_t first = r0 + stage * a.stage_rows, rows = min(a.stage_rows, r1 - first);
+        const uint8_t* from = dyn + s * kOneStage + c * sizeof(T);
+        if (on)
+#pragma unroll 2
+            for (uint32_t r = my_row; r < rows; r += tall) {
+                const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(from + r * row);
+                Vec<T, V> p = q;
+                if (kBackward) p = *reinterpret_cast<const Vec<T, V>*>(from + kPlane + r * row);
+                f(q, p, first + r);
+            }
+    };
+    if (kBackward) {
+        for (uint32_t i = threadIdx.x; i < a.channels; i += kOneThreads) t0[i] = t1[i] = 0.0f;
+        sync_compute();
+    }
+    uint32_t round = 0;
+    for (uint32_t sample = group; ok && sample < a.n; sample += a.across, ++round) {
+        const T* x = at<T>(a.x, sample);
+        T* out = const_cast<T*>(at<T>(a.out, sample));
+        // the statistics' pass
+        float s[2][V] = {}, less[V] = {};
+        Channels<V> ch;
+        if (kBackward) {
+            if (on) ch = Channels<V>(a, sample, c);
+        } else if (on) {
+            widen(load_raw<T, V>(x + c), less);
+#pragma unroll
+            for (int i = 0; i < V; ++i) less[i] = -less[i];
+        }
+        for (uint32_t i = 0; ok && i < n; ++i) {
+            const uint32_t slot = ring.at(i);
+            ok = __all_sync(~0u, wait_full(slot));
+            if (!ok) break;
+            over(i, slot, [&](const Vec<T, V>& q, const Vec<T, V>& p, uint32_t) {
+                float v[V], d[V];
+                widen(q, v);
+                if constexpr (kBackward) {
+                    widen(p, d);
+                    ch.step(act, v, d);
+                    add(s[0], s[0], d);
+                    fma(s[1], d, v, s[1]);
+                } else {
+                    add(v, v, less);
+                    add(s[0], s[0], v);
+                    fma(s[1], v, v, s[1]);
+                }
+            });
+            if (i + a.slots < n) release(slot);               // the last ones are kept
+        }
+        // over the positions: four of the sums at a time
+#pragma unroll
+        for (int k0 = 0; k0 < 2 * V; k0 += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) red[k * kOneThreads + threadIdx.x] = s[(k0 + k) / V][(k0 + k) % V];
+            sync_compute();
+            for (uint32_t left = tall; left > 1;) {
+                const uint32_t half = (left + 1) / 2;
+                if (my_row < left - half)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float& v = s[(k0 + k) / V][(k0 + k) % V];
+                        v += red[k * kOneThreads + threadIdx.x + half * vectors];
+                        red[k * kOneThreads + threadIdx.x] = v;
+                    }
+                left = half;
+                sync_compute();
+            }
+        }
+        if (my_row == 0)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if constexpr (kBackward) {
+                    const float rstd = a.rstd[static_cast<uint64_t>(sample) * a.groups + (c + i) / per];
+                    const float g = a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f;
+                    s[1][i] *= rstd;                          // from dz h to dz xhat
+                    s0[c + i] = g * s[0][i];
+                    s1[c + i] = g * s[1][i];
+                    t0[c + i] += s[0][i];
+                    t1[c + i] += s[1][i];
+                } else {
+                    const float m = s[0][i] / count;
+                    s0[c + i] = m;
+                    s1[c + i] = fmaxf(s[1][i] - s[0][i] * m, 0.0f);
+                }
+            }
+        sync_compute();
+        // of each group, for the sample's other CTAs
+        float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups;
+        for (uint32_t g = warp; g < a.groups; g += kOneWarps) {
+            float p = 0.0f, q = 0.0f;
+            if constexpr (kBackward) {
+                for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
+                    p += s0[k];
+                    q += s1[k];
+                }
+                p = warp_sum(p);
+            } else {
+                const float from = elem(x, g * per, sizeof(T) == 2);
+                for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
+                    s0[k] += elem(x, k, sizeof(T) == 2) - from;
+                    p += s0[k];
+                }
+                p = warp_sum(p) / static_cast<float>(per);
+                for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
+                    const float d = s0[k] - p;
+                    q += fmaf(count * d, d, s1[k]);
+                }
+                if (lane == 0) ref[g] = from;
+            }
+            q = warp_sum(q);
+            if (lane == 0) __stcg(part + rank * a.groups + g, make_float2(p, q));
+        }
+        ok = sync_and(ok);
+        if (a.chunks > 1) {
+            if (threadIdx.x == 0) ok = meet(a.counters + group, (round + 1) * a.chunks) && ok;
+            ok = sync_and(ok);
+        }
+        for (uint32_t g = warp; g < a.groups; g += kOneWarps) {
+            float p = 0.0f, q = 0.0f;
+            for (uint32_t i = lane; i < a.chunks; i += 32) {
+                const float2 v = __ldcg(part + i * a.groups + g);
+                p = kBackward ? p + v.x : fmaf(v.x, static_cast<float>(min(a.rows, a.positions - i * a.rows)), p);
+                q += kBackward ? v.y : 0.0f;
+            }
+            if constexpr (kBackward) {
+                const float inv = 1.0f / (all * static_cast<float>(per));
+                p = warp_sum(p) * inv;
+                q = warp_sum(q) * inv;
+            } else {
+                p = warp_sum(p) / all;
+                for (uint32_t i = lane; i < a.chunks; i += 32) {
+                    const float2 v = __ldcg(part + i * a.groups + g);
+                    const float rows = static_cast<float>(min(a.rows, a.positions - i * a.rows)), d = v.x - p;
+                    q += fmaf(rows * static_cast<float>(per) * d, d, v.y);
+                }
+                q = 1.0f / sqrtf(warp_sum(q) / (all * static_cast<float>(per)) + a.eps);
+                if (lane == 0 && rank == 0) {
+                    const uint64_t to = static_cast<uint64_t>(sample) * a.groups + g;
+                    if (a.mean_out) a.mean_out[to] = ref[g] + p;
+                    if (a.rstd_out) a.rstd_out[to] = q;
+                }
+            }
+            if (lane == 0) {
+                g0[g] = p;
+                g1[g] = q;
+            }
+        }
+        sync_compute();
+        // the result's pass, from the last stage to the first
+        float k1[V] = {}, k2[V] = {};
+        if (on)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t g = (c + i) / per;
+                if constexpr (kBackward) {
+                    // dx = scale dz - rstd m1 - h rstd^2 m2
+                    const float r = a.rstd[static_cast<uint64_t>(sample) * a.groups + g];
+                    k1[i] = -r * g0[g];
+                    k2[i] = -r * r * g1[g];
+                } else {
+                    // y = act((x - ref) scale + shift): the mean, less the reference, is in the shift
+                    less[i] = -ref[g];
+                    k1[i] = g1[g] * (a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f);
+                    k2[i] = fmaf(-g0[g], k1[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
+                }
+            }
+        for (uint32_t i = 0; ok && i < n; ++i) {
+            const uint32_t stage = n - 1 - i, slot = ring.at(stage);
+            if (i >= a.slots) {
+                ok = __all_sync(~0u, wait_full(slot));
+                if (!ok) break;
+            }
+            over(stage, slot, [&](const Vec<T, V>& q, const Vec<T, V>& p, uint32_t r) {
+                float v[V], d[V];
+                widen(q, v);
+                if constexpr (kBackward) {
+                    widen(p, d);
+                    ch.step(act, v, d);
+                    fma(v, v, k2, k1);
+                    fma(v, d, ch.scale, v);
+                } else {
+                    add(v, v, less);
+                    fma(v, v, k1, k2);
+                    act_of(act, v);
+                }
+                store_vec<T, V>(out + r * a.out.ld + c, v);
+            });
+            release(slot);
+        }
+        ring.next();
+        ok = sync_and(ok);
+    }
+    if (kBackward && a.cpart)
+        for (uint32_t i = threadIdx.x; i < a.channels; i += kOneThreads)
+            a.cpart[static_cast<uint64_t>(blockIdx.x) * a.channels + i] = make_float2(t0[i], t1[i]);
+    if (threadIdx.x == 0) {
+        if (!ok) atomicOr(a.err, kErrWaitTimeout);
+        // the last CTA to leave sets the counters back
+        if (a.chunks > 1 && atomicAdd(a.counters + kOneGroups, 1u) == gridDim.x - 1) {
+            for (uint32_t i = 0; i <= kOneGroups; ++i) a.counters[i] = 0;
+            __threadfence();
+        }
+    }
+}
+
+// Shared memory beside the ring.
+uint32_t fixed_bytes(const NormArgs& a, bool backward) { return (4 * kOneThreads + (backward ? 4 : 2) * a.channels + 3 * a.groups) * 4; }
+
+}  // namespace
+
+bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms) {
+    const uint32_t size = a.dtype ? 2 : 4, v = 16 / size, streams = backward ? 2 : 1;
+    if (a.channels % v || a.channels > 1024) return false;
+    const auto dense = [&](const NormTensor& t) {
+        return reinterpret_cast<uintptr_t>(t.p) % 16 == 0 && (a.positions == 1 || t.ld == a.channels) && (a.n == 1 || t.step % v == 0);
+    };
+    const auto aligned = [&](const NormTensor& t) {
+        return reinterpret_cast<uintptr_t>(t.p) % 16 == 0 && t.ld % v == 0 && (a.n == 1 || t.step % v == 0);
+    };
+    if (!dense(a.x) || (backward && !dense(a.dout)) || !aligned(a.out)) return false;
+    const uint32_t row = a.channels * size, tall = kOneThreads / (a.channels / v);
+    a.stage_rows = kOneStage / streams / row / tall * tall;
+    a.slots = std::min(kOneSlots, (kOneMost - fixed_bytes(a, backward)) / kOneStage);
+    // CTAs per sample: so many that it stays in their shared memory, and so many that all SMs have
+    // work, but a stage each at least.
+    const uint64_t stages = (a.positions + a.stage_rows - 1) / a.stage_rows, hold = (stages + a.slots - 1) / a.slots;
+    uint64_t k = std::max<uint64_t>(hold, std::min<uint64_t>(std::max<uint64_t>(1, sms / a.n), stages));
+    k = std::min<uint64_t>(k, sms);
+    a.rows = static_cast<uint32_t>((a.positions + k - 1) / k);
+    a.chunks = (a.positions + a.rows - 1) / a.rows;
+    a.across = std::min({a.n, sms / a.chunks, a.chunks > 1 ? kOneGroups : sms});
+    return true;
+}
+
+cudaError_t launch_norm_one(const NormArgs& a, bool backward, cudaStream_t stream) {
+    using Kernel = void (*)(NormArgs);
+    static const Kernel kernels[2][2] = {{norm_one_kernel<float, 4, false>, norm_one_kernel<float, 4, true>},
+                                         {norm_one_kernel<uint16_t, 8, false>, norm_one_kernel<uint16_t, 8, true>}};
+    const Kernel k = kernels[a.dtype][backward];
+    const uint32_t smem = a.slots * kOneStage + fixed_bytes(a, backward);
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.across * a.chunks);
+    cfg.blockDim = dim3(kOneThreads + 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.chunks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+}  // namespace fa

@@ -105,7 +105,7 @@ fa::NormTensor norm_tensor(const Args& p, const void* t, uint64_t ld, uint64_t s
 }
 
 template <typename Args>
-void norm_sizes(fa::NormArgs& a, const Args& p) {
+void norm_sizes(fa::NormArgs& a, const Args& p, unsigned int* err) {
     a.n = static_cast<uint32_t>(p.n);
     a.positions = static_cast<uint32_t>(p.positions);
     a.channels = static_cast<uint32_t>(p.channels);
@@ -113,6 +113,8 @@ void norm_sizes(fa::NormArgs& a, const Args& p) {
     a.dtype = code_of(p.dtype);
     a.param_dtype = code_of(p.dtype_param);
     a.act = p.act;
+    a.err = err;
+    a.counters = err + kNormCounters;
     a.gamma = p.gamma;
     a.beta = p.beta;
 }
@@ -141,13 +143,15 @@ fa_status norm_impl(fa_work* w, const fa_group_norm_args& p, cudaStream_t s) {
             if (overlap(out[i], out[j])) return fail(w, FA_ERR_ARG, "an output overlaps another tensor of the call");
     }
     fa::NormArgs a{};
-    norm_sizes(a, p);
+    norm_sizes(a, p, w->err_dev);
     a.x = norm_tensor(p, p.x, p.ldx, p.step_x);
     a.out = norm_tensor(p, p.y, p.ldy, p.step_y);
     a.mean_out = p.mean;
     a.rstd_out = p.rstd;
     a.eps = static_cast<float>(p.eps);
-    fa::plan_norm(a, false, static_cast<uint32_t>(w->tc.sms));
+    const uint32_t sms = static_cast<uint32_t>(w->tc.sms);
+    const bool one = fa::plan_norm_one(a, false, sms);
+    if (!one) fa::plan_norm(a, false, sms);
     const bool cap = capturing(s);
     Carve need{nullptr}, c{nullptr};
     const auto carve = [&](Carve& from) {
@@ -161,8 +165,8 @@ fa_status norm_impl(fa_work* w, const fa_group_norm_args& p, cudaStream_t s) {
     c.base = w->ws;
     carve(c);
     ChainOut chain(w, s, cap);
-    unsigned launches = 0;
-    const cudaError_t e = fa::launch_norm(a, s, &launches);
+    unsigned launches = one;
+    const cudaError_t e = one ? fa::launch_norm_one(a, false, s) : fa::launch_norm(a, s, &launches);
     w->stats.kernel_launches += launches;
     return chain.end(e == cudaSuccess ? FA_OK : cuda_fail(w, e, "group norm"));
 }
@@ -198,7 +202,7 @@ fa_status norm_backward_impl(fa_work* w, const fa_group_norm_backward_args& p, c
     }
     if (!any && !p.d_gamma && !p.d_beta) return FA_OK;
     fa::NormArgs a{};
-    norm_sizes(a, p);
+    norm_sizes(a, p, w->err_dev);
     a.x = norm_tensor(p, p.x, p.ldx, p.step_x);
     a.dout = norm_tensor(p, p.dout, p.ldd, p.step_d);
     a.out = norm_tensor(p, p.dx, p.lddx, p.step_dx);
@@ -207,13 +211,18 @@ fa_status norm_backward_impl(fa_work* w, const fa_group_norm_backward_args& p, c
     a.d_gamma = p.d_gamma;
     a.d_beta = p.d_beta;
     const bool cap = capturing(s), params = p.d_gamma || p.d_beta;
+    const uint32_t sms = static_cast<uint32_t>(w->tc.sms);
+    bool one = false;
+    uint32_t rows = 0;                   // of the parameters' partial sums
     Carve need{nullptr}, c{nullptr};
     const auto carve = [&](Carve& from) {
         a.part = static_cast<float2*>(from.take(stats * a.chunks * sizeof(float2)));
-        a.cpart = params ? static_cast<float2*>(from.take(fa::norm_rows(a) * a.chunks * C * sizeof(float2))) : nullptr;
+        a.cpart = params ? static_cast<float2*>(from.take(rows * C * sizeof(float2))) : nullptr;
     };
     if (any) {
-        fa::plan_norm(a, true, static_cast<uint32_t>(w->tc.sms));
+        one = fa::plan_norm_one(a, true, sms);
+        if (!one) fa::plan_norm(a, true, sms);
+        rows = static_cast<uint32_t>(one ? a.across * a.chunks : fa::norm_rows(a) * a.chunks);
         carve(need);
     }
     r = ensure_ws(w, need.used, cap);
@@ -222,8 +231,12 @@ fa_status norm_backward_impl(fa_work* w, const fa_group_norm_backward_args& p, c
     c.base = w->ws;
     if (any) carve(c);
     ChainOut chain(w, s, cap);
-    unsigned launches = 0;
-    const cudaError_t e = fa::launch_norm_backward(a, s, &launches);
+    unsigned launches = one;
+    cudaError_t e = !any ? cudaSuccess : one ? fa::launch_norm_one(a, true, s) : fa::launch_norm_backward(a, s, &launches);
+    if (e == cudaSuccess && params) {
+        e = fa::launch_norm_param(a, rows, s);
+        ++launches;
+    }
     w->stats.kernel_launches += launches;
     return chain.end(e == cudaSuccess ? FA_OK : cuda_fail(w, e, "group norm gradient"));
 }

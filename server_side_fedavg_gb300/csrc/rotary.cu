@@ -26,6 +26,19 @@ struct alignas(sizeof(T) * V) Pack {
     T e[V];
 };
 
+// (16 bytes by a load that stays where it is written)
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+    Pack<T, V> q;
+    if constexpr (sizeof(T) * V == 16) {
+        const uint4 w = ld_plain_v4(p);
+        memcpy(&q, &w, 16);
+    } else {
+        q = *reinterpret_cast<const Pack<T, V>*>(p);
+    }
+    return q;
+}
+
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 __device__ __forceinline__ void narrow(float x, float& y) { y = x; }
@@ -59,6 +72,28 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     const uint32_t token = static_cast<uint32_t>(which), in = static_cast<uint32_t>(at - which * per);
     const uint32_t slot = in / a.chunks, chunk = in - slot * a.chunks;
     const uint32_t b = token / a.seq, s = token - b * a.seq;
+    // the two vectors of this thread in a head
+    const bool turn = chunk < a.turning;
+    const uint32_t e0 = !turn ? a.rotary_dim + (chunk - a.turning) * 2 * V : kInterleaved ? chunk * 2 * V : chunk * V;
+    const uint32_t e1 = turn && !kInterleaved ? e0 + half : e0 + V;
+    const bool second = e1 < a.head_dim;
+    const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
+    const T* x0 = static_cast<const T*>(a.part[0].x) + b * a.part[0].xb + s * a.part[0].xt;
+    const T* x1 = static_cast<const T*>(a.part[1].x) + b * a.part[1].xb + s * a.part[1].xt;
+    T* o0 = static_cast<T*>(a.part[0].out) + b * a.part[0].ob + s * a.part[0].ot;
+    T* o1 = static_cast<T*>(a.part[1].out) + b * a.part[1].ob + s * a.part[1].ot;
+    P u[kAhead], v[kAhead];
+    const auto fetch = [&](uint32_t h0) {
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t h = h0 + k * a.slots;
+            if (h >= heads) break;
+            const T* x = h < heads0 ? x0 + h * a.part[0].xh : x1 + (h - heads0) * a.part[1].xh;
+            u[k] = load_pack<T, V>(x + e0);
+            if (second) v[k] = load_pack<T, V>(x + e1);
+        }
+    };
+    fetch(slot);                         // on their way while the sines are computed
     uint64_t pos;
     if (a.position) {
         const int32_t p = a.position[token];
@@ -67,13 +102,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     } else {
         pos = static_cast<uint64_t>(a.first) + s;
     }
-    // the two vectors of this thread in a head, and the turns of its pairs
-    const bool turn = chunk < a.turning;
-    uint32_t e0, e1;
     float cs[V], sn[V];
     if (turn) {
-        e0 = kInterleaved ? chunk * 2 * V : chunk * V;
-        e1 = kInterleaved ? e0 + V : e0 + half;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint64_t t = pos * turns[chunk * V + i];
@@ -81,26 +111,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
             sn[i] *= a.scale;
             cs[i] *= a.scale;
         }
-    } else {
-        e0 = a.rotary_dim + (chunk - a.turning) * 2 * V;
-        e1 = e0 + V;
     }
-    const bool second = e1 < a.head_dim;
-    const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
-    const T* x0 = static_cast<const T*>(a.part[0].x) + b * a.part[0].xb + s * a.part[0].xt;
-    const T* x1 = static_cast<const T*>(a.part[1].x) + b * a.part[1].xb + s * a.part[1].xt;
-    T* o0 = static_cast<T*>(a.part[0].out) + b * a.part[0].ob + s * a.part[0].ot;
-    T* o1 = static_cast<T*>(a.part[1].out) + b * a.part[1].ob + s * a.part[1].ot;
-    for (uint32_t h0 = slot; h0 < heads; h0 += kAhead * a.slots) {
-        P u[kAhead], v[kAhead];
-#pragma unroll
-        for (uint32_t k = 0; k < kAhead; ++k) {
-            const uint32_t h = h0 + k * a.slots;
-            if (h >= heads) break;
-            const T* x = h < heads0 ? x0 + h * a.part[0].xh : x1 + (h - heads0) * a.part[1].xh;
-            u[k] = *reinterpret_cast<const P*>(x + e0);
-            if (second) v[k] = *reinterpret_cast<const P*>(x + e1);
-        }
+    for (uint32_t h0 = slot;;) {
 #pragma unroll
         for (uint32_t k = 0; k < kAhead; ++k) {
             const uint32_t h = h0 + k * a.slots;
@@ -120,6 +132,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
             *reinterpret_cast<P*>(o + e0) = u[k];
             if (second) *reinterpret_cast<P*>(o + e1) = v[k];
         }
+        h0 += kAhead * a.slots;
+        if (h0 >= heads) return;
+        fetch(h0);
     }
 }
 

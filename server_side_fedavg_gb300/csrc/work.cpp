@@ -423,12 +423,12 @@ fa_status fa_work_open(const fa_work_opts* opts, fa_work** out) {
     cudaError_t ce = cudaGetDevice(&w->device);
     if (ce == cudaSuccess) ce = fa::prepare_distill();
     if (ce == cudaSuccess) ce = fa::prepare_product_tc(&w->tc);
-    if (ce == cudaSuccess) ce = cudaMalloc(reinterpret_cast<void**>(&w->err_dev), 256);
+    if (ce == cudaSuccess) ce = cudaMalloc(reinterpret_cast<void**>(&w->err_dev), kErrBytes);
     if (ce == cudaSuccess) ce = cudaEventCreateWithFlags(&w->chain, cudaEventDisableTiming);
     if (ce == cudaSuccess) ce = cudaEventCreateWithFlags(&w->err_ev, cudaEventDisableTiming);
     if (ce == cudaSuccess) ce = cudaStreamCreateWithFlags(&w->err_stream, cudaStreamNonBlocking);
     // zero before any caller's stream can set it: a memset does not wait for its own end
-    if (ce == cudaSuccess) ce = cudaMemsetAsync(w->err_dev, 0, 256, w->err_stream);
+    if (ce == cudaSuccess) ce = cudaMemsetAsync(w->err_dev, 0, kErrBytes, w->err_stream);
     if (ce == cudaSuccess) ce = cudaStreamSynchronize(w->err_stream);
     if (ce == cudaSuccess)
         ce = cudaHostAlloc(reinterpret_cast<void**>(&w->err_host), sizeof(unsigned int), cudaHostAllocDefault);

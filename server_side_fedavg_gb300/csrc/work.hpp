@@ -37,7 +37,7 @@ struct fa_work {
     cudaEvent_t chain = nullptr;         // recorded after the last queued call
     bool chain_valid = false;
     unsigned long long chain_stream_id = 0;
-    unsigned int* err_dev = nullptr;     // device error word (kernels OR bits in)
+    unsigned int* err_dev = nullptr;     // kErrBytes, zero at first: error word (kernels OR bits in), counters
     unsigned int* err_host = nullptr;    // pinned copy
     cudaStream_t err_stream = nullptr;
     cudaEvent_t err_ev = nullptr;
@@ -243,6 +243,9 @@ bool overlap(const Extent& x, const Extent& y) {
 }
 
 constexpr uint64_t kMaxSize = 1ull << 31;
+
+// err_dev: the error word, and from word kNormCounters on those in which the CTAs of a group norm meet.
+constexpr uint32_t kErrBytes = 1024, kNormCounters = 16;
 
 fa_status launched(fa_work* w, cudaError_t e, const char* what) {
     if (e != cudaSuccess) return cuda_fail(w, e, what);

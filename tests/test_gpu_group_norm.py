@@ -66,7 +66,9 @@ def check_forward(work, n, P, C, G, dtype, param, act, seed, offset=1.0, eps=1e-
     (4, 64, 256, 32, "bf16", "bf16", "relu"), (2, 4097, 32, 8, "bf16", "f32", "silu"), (1, 30000, 16, 4, "f32", "f32", "gelu"),
     (5, 77, 33, 3, "f32", "f32", "silu"), (5, 77, 33, 33, "bf16", "bf16", "silu"), (2, 999, 6, 1, "bf16", "f32", "gelu"),
     (1, 50, 8192, 1, "bf16", "f32", "silu"), (1, 33, 5001, 3, "f32", "bf16", "none"), (700, 3, 24, 4, "f32", "f32", "relu"),
-    (1, 100000, 48, 8, "bf16", "f32", "silu"), (1, 1, 1, 1, "f32", "f32", "none"), (64, 512, 64, 8, "bf16", "f32", "none")])
+    (1, 100000, 48, 8, "bf16", "f32", "silu"), (1, 1, 1, 1, "f32", "f32", "none"), (64, 512, 64, 8, "bf16", "f32", "none"),
+    (3, 300000, 32, 8, "bf16", "f32", "silu"), (2, 700001, 16, 16, "f32", "f32", "relu"), (5, 40000, 64, 8, "f32", "bf16", "gelu"),
+    (200, 16, 1024, 32, "bf16", "f32", "silu"), (1, 2000, 1024, 1024, "f32", "f32", "none"), (33, 3000, 24, 3, "bf16", "f32", "silu")])
 def test_forward(work, n, P, C, G, dtype, param, act):
     check_forward(work, n, P, C, G, dtype, param, act, 1)
 
@@ -113,7 +115,9 @@ def check_backward(work, n, P, C, G, dtype, param, act, seed, call=None):
     (2, 4097, 32, 8, "bf16", "f32", "silu"), (1, 30000, 16, 4, "f32", "f32", "gelu"), (5, 77, 33, 3, "f32", "f32", "silu"),
     (5, 77, 33, 33, "bf16", "bf16", "gelu"), (2, 999, 6, 1, "bf16", "f32", "silu"), (1, 50, 8192, 1, "bf16", "f32", "none"),
     (1, 33, 5001, 3, "f32", "bf16", "gelu"), (700, 3, 24, 4, "f32", "f32", "silu"), (1, 100000, 48, 8, "bf16", "f32", "silu"),
-    (64, 512, 64, 8, "bf16", "f32", "none")])
+    (64, 512, 64, 8, "bf16", "f32", "none"), (3, 300000, 32, 8, "bf16", "f32", "silu"), (2, 400001, 16, 16, "f32", "f32", "gelu"),
+    (5, 40000, 64, 8, "f32", "bf16", "none"), (200, 16, 1024, 32, "bf16", "f32", "silu"), (1, 2000, 1024, 1024, "f32", "f32", "none"),
+    (33, 3000, 24, 3, "bf16", "f32", "silu")])
 def test_backward(work, n, P, C, G, dtype, param, act):
     check_backward(work, n, P, C, G, dtype, param, act, 3)
 
