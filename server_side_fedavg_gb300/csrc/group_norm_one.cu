@@ -1,7 +1,8 @@
 // Group norm and its gradients in one kernel, where a sample's positions are one run of bytes.
 //
 // k CTAs share a sample, each a run of its positions; one CTA per SM, launched cooperatively.  A
-// warp of its own fetches the run by bulk copies into a ring of 32 KB stages; 16 warps compute.
+// warp of its own fetches the run by bulk copies into a ring of 40 KB stages; 20 warps compute, which
+// leaves each thread 80 registers.
 // After the statistics' pass the CTAs meet at a counter in global memory, join their parts, and
 // walk their runs backwards for the result: the stages fetched last are still in shared memory,
 // some 28 MB of a sample over all SMs, and are not fetched again; the next sample's first stages
@@ -16,20 +17,23 @@ namespace fa {
 
 namespace {
 
-constexpr uint32_t kOneThreads = 512, kOneWarps = kOneThreads / 32;
-constexpr uint32_t kOneStage = 32768, kOneSlots = 6;
+constexpr uint32_t kOneThreads = 640, kOneWarps = kOneThreads / 32;           // that compute
+constexpr uint32_t kOneStage = 40960, kOneSlots = 5;
+constexpr uint32_t kOneRed = 128 * (kOneWarps + 2);   // floats: the sums over the positions
+static_assert(kOneRed >= 4 * kOneThreads, "four of every thread's sums");
+constexpr uint32_t kOneChunks = 160;                  // CTAs of a sample: five per lane of a warp
 constexpr uint32_t kOneMost = 225 * 1024;             // dynamic shared memory
 constexpr uint32_t kOneGroups = 80;                   // counters for samples at one time, and one for the end
 
 // The computing warps of a CTA; whether all of their threads say so.
-__device__ __forceinline__ void sync_compute() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void sync_compute() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kOneThreads) : "memory"); }
 
 __device__ __forceinline__ bool sync_and(bool ok) {
     uint32_t all;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 512, p;\n selp.u32 %0, 1, 0, q;\n}"
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
         : "=r"(all)
-        : "r"(static_cast<uint32_t>(ok))
+        : "r"(static_cast<uint32_t>(ok)), "n"(kOneThreads)
         : "memory");
     return all;
 }
@@ -62,6 +66,8 @@ struct Slots {
         const int n = static_cast<int>(count), s = (b + d * static_cast<int>(i % count)) % n;
         return s < 0 ? s + n : s;
     }
+    __device__ __forceinline__ uint32_t after(uint32_t s) const { return d > 0 ? (s + 1 == count ? 0 : s + 1) : (s == 0 ? count : s) - 1; }
+    __device__ __forceinline__ uint32_t before(uint32_t s) const { return d < 0 ? (s + 1 == count ? 0 : s + 1) : (s == 0 ? count : s) - 1; }
     __device__ __forceinline__ void next() {
         b = (b - d + static_cast<int>(count)) % static_cast<int>(count);
         d = -d;
@@ -73,13 +79,62 @@ __device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
     return static_cast<const T*>(t.p) + sample * t.step;
 }
 
+// The threads' sums over the positions, for each channel, in its first thread.  Where lanes of a warp
+// share columns by a power of two, over these first, then over the warps in order.  Else four sums at a time over a tree.
+template <int V>
+__device__ __forceinline__ void over_positions(float (&s)[2][V], float* red, uint32_t vectors, uint32_t tall) {
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, my_row = threadIdx.x / vectors;
+    if (vectors <= 32 && 32 % vectors == 0 && 2 * V * vectors <= 4 * 32) {
+        float v[2 * V];
+#pragma unroll
+        for (int k = 0; k < 2 * V; ++k) v[k] = s[k / V][k % V];
+        for (uint32_t o = 16; o >= vectors; o /= 2)
+#pragma unroll
+            for (int k = 0; k < 2 * V; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+        // [sum][warp][column]
+        if (lane < vectors)
+#pragma unroll
+            for (int k = 0; k < 2 * V; ++k) red[(k * kOneWarps + warp) * vectors + lane] = v[k];
+        sync_compute();
+        for (uint32_t i = threadIdx.x; i < 2 * V * vectors; i += kOneThreads) {
+            float t = 0.0f;
+#pragma unroll
+            for (uint32_t w = 0; w < kOneWarps; ++w) t += red[(i / vectors * kOneWarps + w) * vectors + i % vectors];
+            red[2 * V * kOneWarps * vectors + i] = t;
+        }
+        sync_compute();
+        if (threadIdx.x < vectors)
+#pragma unroll
+            for (int k = 0; k < 2 * V; ++k) s[k / V][k % V] = red[2 * V * (kOneWarps * vectors) + k * vectors + threadIdx.x];
+        return;
+    }
+#pragma unroll
+    for (int k0 = 0; k0 < 2 * V; k0 += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) red[k * kOneThreads + threadIdx.x] = s[(k0 + k) / V][(k0 + k) % V];
+        sync_compute();
+        for (uint32_t left = tall; left > 1;) {
+            const uint32_t half = (left + 1) / 2;
+            if (my_row < left - half)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float& v = s[(k0 + k) / V][(k0 + k) % V];
+                    v += red[k * kOneThreads + threadIdx.x + half * vectors];
+                    red[k * kOneThreads + threadIdx.x] = v;
+                }
+            left = half;
+            sync_compute();
+        }
+    }
+}
+
 template <typename T, int V, bool kBackward>
 __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid_constant__ NormArgs a) {
     constexpr uint32_t kStreams = kBackward ? 2 : 1, kPlane = kOneStage / kStreams;
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ uint64_t bars[2 * kOneSlots];
     float* red = reinterpret_cast<float*>(dyn + a.slots * kOneStage);
-    float *s0 = red + 4 * kOneThreads, *s1 = s0 + a.channels;                      // of a channel
+    float *s0 = red + kOneRed, *s1 = s0 + a.channels;                      // of a channel
     float *t0 = s1 + a.channels, *t1 = t0 + (kBackward ? a.channels : 0);          // gradients so far (backward)
     float *g0 = t1 + (kBackward ? a.channels : 0), *g1 = g0 + a.groups, *ref = g1 + a.groups;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kOneSlots;
@@ -145,18 +200,31 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * s);
     };
-    // f(vector of x, vector of dout, position) of a stage
-    const auto over = [&](uint32_t stage, uint32_t s, auto f) {
+    // f(vector of x, vector of dout, where its result goes) of a stage, four at a time
+    const uint32_t step = tall * row, mine = my_row * row + c * sizeof(T);
+    const uint64_t step_out = tall * a.out.ld;
+    const auto over = [&](uint32_t stage, uint32_t s, T* out, auto f) {
+        if (!on) return;
         const uint32_t first = r0 + stage * a.stage_rows, rows = min(a.stage_rows, r1 - first);
-        const uint8_t* from = dyn + s * kOneStage + c * sizeof(T);
-        if (on)
-#pragma unroll 2
-            for (uint32_t r = my_row; r < rows; r += tall) {
-                const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(from + r * row);
-                Vec<T, V> p = q;
-                if (kBackward) p = *reinterpret_cast<const Vec<T, V>*>(from + kPlane + r * row);
-                f(q, p, first + r);
+        const uint8_t* from = dyn + s * kOneStage + mine;
+        T* to = out + (first + my_row) * a.out.ld + c;
+        uint32_t r = my_row;
+        for (; r + 3 * tall < rows; r += 4 * tall) {
+            Vec<T, V> q[4], p[4];
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                q[u] = *reinterpret_cast<const Vec<T, V>*>(from + u * step);
+                if (kBackward) p[u] = *reinterpret_cast<const Vec<T, V>*>(from + kPlane + u * step);
             }
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) f(q[u], kBackward ? p[u] : q[u], to + u * step_out);
+            from += 4 * step;
+            to += 4 * step_out;
+        }
+        for (; r < rows; r += tall, from += step, to += step_out) {
+            const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(from);
+            f(q, kBackward ? *reinterpret_cast<const Vec<T, V>*>(from + kPlane) : q, to);
+        }
     };
     if (kBackward) {
         for (uint32_t i = threadIdx.x; i < a.channels; i += kOneThreads) t0[i] = t1[i] = 0.0f;
@@ -176,11 +244,10 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < V; ++i) less[i] = -less[i];
         }
-        for (uint32_t i = 0; ok && i < n; ++i) {
-            const uint32_t slot = ring.at(i);
+        for (uint32_t i = 0, slot = ring.at(0); ok && i < n; ++i, slot = ring.after(slot)) {
             ok = __all_sync(~0u, wait_full(slot));
             if (!ok) break;
-            over(i, slot, [&](const Vec<T, V>& q, const Vec<T, V>& p, uint32_t) {
+            over(i, slot, out, [&](const Vec<T, V>& q, const Vec<T, V>& p, T*) {
                 float v[V], d[V];
                 widen(q, v);
                 if constexpr (kBackward) {
@@ -196,25 +263,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
             });
             if (i + a.slots < n) release(slot);               // the last ones are kept
         }
-        // over the positions: four of the sums at a time
-#pragma unroll
-        for (int k0 = 0; k0 < 2 * V; k0 += 4) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) red[k * kOneThreads + threadIdx.x] = s[(k0 + k) / V][(k0 + k) % V];
-            sync_compute();
-            for (uint32_t left = tall; left > 1;) {
-                const uint32_t half = (left + 1) / 2;
-                if (my_row < left - half)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float& v = s[(k0 + k) / V][(k0 + k) % V];
-                        v += red[k * kOneThreads + threadIdx.x + half * vectors];
-                        red[k * kOneThreads + threadIdx.x] = v;
-                    }
-                left = half;
-                sync_compute();
-            }
-        }
+        over_positions<V>(s, red, vectors, tall);
         if (my_row == 0)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -265,11 +314,21 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
             ok = sync_and(ok);
         }
         for (uint32_t g = warp; g < a.groups; g += kOneWarps) {
-            float p = 0.0f, q = 0.0f;
-            for (uint32_t i = lane; i < a.chunks; i += 32) {
-                const float2 v = __ldcg(part + i * a.groups + g);
-                p = kBackward ? p + v.x : fmaf(v.x, static_cast<float>(min(a.rows, a.positions - i * a.rows)), p);
-                q += kBackward ? v.y : 0.0f;
+            float p = 0.0f, q = 0.0f, rows[kOneChunks / 32];
+            float2 v[kOneChunks / 32];
+#pragma unroll
+            for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
+                const uint32_t i = lane + 32 * u;
+                v[u] = make_float2(0.0f, 0.0f);
+                rows[u] = 0.0f;
+                if (i >= a.chunks) continue;
+                v[u] = __ldcg(part + i * a.groups + g);
+                rows[u] = static_cast<float>(min(a.rows, a.positions - i * a.rows));
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
+                p = kBackward ? p + v[u].x : fmaf(v[u].x, rows[u], p);
+                q += kBackward ? v[u].y : 0.0f;
             }
             if constexpr (kBackward) {
                 const float inv = 1.0f / (all * static_cast<float>(per));
@@ -277,10 +336,10 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 q = warp_sum(q) * inv;
             } else {
                 p = warp_sum(p) / all;
-                for (uint32_t i = lane; i < a.chunks; i += 32) {
-                    const float2 v = __ldcg(part + i * a.groups + g);
-                    const float rows = static_cast<float>(min(a.rows, a.positions - i * a.rows)), d = v.x - p;
-                    q += fmaf(rows * static_cast<float>(per) * d, d, v.y);
+#pragma unroll
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
+                    const float d = v[u].x - p;
+                    q += rows[u] > 0.0f ? fmaf(rows[u] * static_cast<float>(per) * d, d, v[u].y) : 0.0f;
                 }
                 q = 1.0f / sqrtf(warp_sum(q) / (all * static_cast<float>(per)) + a.eps);
                 if (lane == 0 && rank == 0) {
@@ -313,13 +372,12 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     k2[i] = fmaf(-g0[g], k1[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
                 }
             }
-        for (uint32_t i = 0; ok && i < n; ++i) {
-            const uint32_t stage = n - 1 - i, slot = ring.at(stage);
+        for (uint32_t i = 0, slot = ring.at(n - 1); ok && i < n; ++i, slot = ring.before(slot)) {
             if (i >= a.slots) {
                 ok = __all_sync(~0u, wait_full(slot));
                 if (!ok) break;
             }
-            over(stage, slot, [&](const Vec<T, V>& q, const Vec<T, V>& p, uint32_t r) {
+            over(n - 1 - i, slot, out, [&](const Vec<T, V>& q, const Vec<T, V>& p, T* to) {
                 float v[V], d[V];
                 widen(q, v);
                 if constexpr (kBackward) {
@@ -332,7 +390,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     fma(v, v, k1, k2);
                     act_of(act, v);
                 }
-                store_vec<T, V>(out + r * a.out.ld + c, v);
+                store_vec<T, V>(to, v);
             });
             release(slot);
         }
@@ -353,7 +411,12 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
 }
 
 // Shared memory beside the ring.
-uint32_t fixed_bytes(const NormArgs& a, bool backward) { return (4 * kOneThreads + (backward ? 4 : 2) * a.channels + 3 * a.groups) * 4; }
+uint32_t fixed_bytes(const NormArgs& a, bool backward) {
+    return (kOneRed + (backward ? 4 : 2) * a.channels + 3 * a.groups) * 4;
+}
+// Channels of a thread: 16 bytes, but for the gradients of bf16 four, whose state would not fit its
+// registers otherwise.
+uint32_t channels_of(int dtype, bool backward) { return dtype && !backward ? 8 : 4; }
 
 }  // namespace
 
@@ -367,14 +430,14 @@ bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms) {
         return reinterpret_cast<uintptr_t>(t.p) % 16 == 0 && t.ld % v == 0 && (a.n == 1 || t.step % v == 0);
     };
     if (!dense(a.x) || (backward && !dense(a.dout)) || !aligned(a.out)) return false;
-    const uint32_t row = a.channels * size, tall = kOneThreads / (a.channels / v);
+    const uint32_t row = a.channels * size, tall = kOneThreads / (a.channels / channels_of(a.dtype, backward));
     a.stage_rows = kOneStage / streams / row / tall * tall;
     a.slots = std::min(kOneSlots, (kOneMost - fixed_bytes(a, backward)) / kOneStage);
     // CTAs per sample: so many that it stays in their shared memory, and so many that all SMs have
     // work, but a stage each at least.
     const uint64_t stages = (a.positions + a.stage_rows - 1) / a.stage_rows, hold = (stages + a.slots - 1) / a.slots;
     uint64_t k = std::max<uint64_t>(hold, std::min<uint64_t>(std::max<uint64_t>(1, sms / a.n), stages));
-    k = std::min<uint64_t>(k, sms);
+    k = std::min<uint64_t>({k, sms, kOneChunks});
     a.rows = static_cast<uint32_t>((a.positions + k - 1) / k);
     a.chunks = (a.positions + a.rows - 1) / a.rows;
     a.across = std::min({a.n, sms / a.chunks, a.chunks > 1 ? kOneGroups : sms});
@@ -384,7 +447,7 @@ bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms) {
 cudaError_t launch_norm_one(const NormArgs& a, bool backward, cudaStream_t stream) {
     using Kernel = void (*)(NormArgs);
     static const Kernel kernels[2][2] = {{norm_one_kernel<float, 4, false>, norm_one_kernel<float, 4, true>},
-                                         {norm_one_kernel<uint16_t, 8, false>, norm_one_kernel<uint16_t, 8, true>}};
+                                         {norm_one_kernel<uint16_t, 8, false>, norm_one_kernel<uint16_t, 4, true>}};
     const Kernel k = kernels[a.dtype][backward];
     const uint32_t smem = a.slots * kOneStage + fixed_bytes(a, backward);
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
