@@ -1,10 +1,10 @@
 // Group norm and its gradients in one kernel, where a sample's positions are one run of bytes.
 //
-// k CTAs share a sample, each a run of its positions; one CTA per SM, launched cooperatively.  A
-// warp of its own fetches the run by bulk copies into a ring of 40 KB stages; 20 warps compute, which
+// k CTAs share a sample, each every k-th stage of its positions; one CTA per SM, launched cooperatively.  A
+// warp of its own fetches them by bulk copies into a ring of 40 KB stages; 20 warps compute, which
 // leaves each thread 80 registers.
 // After the statistics' pass the CTAs meet at a counter in global memory, join their parts, and
-// walk their runs backwards for the result: the stages fetched last are still in shared memory,
+// walk their stages backwards for the result: the stages fetched last are still in shared memory,
 // some 28 MB of a sample over all SMs, and are not fetched again; the next sample's first stages
 // are fetched meanwhile.  A sample that fits is read once.
 //
@@ -73,6 +73,15 @@ struct Slots {
         d = -d;
     }
 };
+
+// Stages of a sample's CTA, and the positions in them.
+__device__ __forceinline__ uint32_t stages_of(const NormArgs& a, uint32_t rank) {
+    return ((a.positions + a.stage_rows - 1) / a.stage_rows + a.chunks - 1 - rank) / a.chunks;
+}
+__device__ __forceinline__ float rows_of(const NormArgs& a, uint32_t rank) {
+    const uint32_t n = stages_of(a, rank), last = ((n - 1) * a.chunks + rank) * a.stage_rows;
+    return static_cast<float>((n - 1) * a.stage_rows + min(a.stage_rows, a.positions - last));
+}
 
 template <typename T>
 __device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
@@ -150,7 +159,9 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
     wait_predecessor();
 
     const uint32_t group = blockIdx.x / a.chunks, rank = blockIdx.x % a.chunks, row = a.channels * sizeof(T);
-    const uint32_t r0 = rank * a.rows, r1 = min(a.positions, r0 + a.rows), n = (r1 - r0 + a.stage_rows - 1) / a.stage_rows;
+    // this CTA's stages: rank, rank + k, ...: what all fetch at one time lies together
+    const uint32_t n = stages_of(a, rank);
+    const auto first_of = [&](uint32_t stage) { return (stage * a.chunks + rank) * a.stage_rows; };
     Slots ring;
     ring.count = a.slots;
     bool ok = true;
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     if (!ok) return;
                 }
                 ring.used |= 1u << s;
-                const uint32_t first = r0 + stage * a.stage_rows, bytes = min(a.stage_rows, r1 - first) * row;
+                const uint32_t first = first_of(stage), bytes = min(a.stage_rows, a.positions - first) * row;
                 mbar_expect(full + 8 * s, bytes * kStreams);
                 bulk_load(dyn + s * kOneStage, x + static_cast<uint64_t>(first) * a.channels, bytes, full + 8 * s);
                 if (kBackward) bulk_load(dyn + s * kOneStage + kPlane, dout + static_cast<uint64_t>(first) * a.channels, bytes, full + 8 * s);
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups;
     const uint32_t tall = kOneThreads / vectors, my_row = threadIdx.x / vectors, c = threadIdx.x % vectors * V;
     const bool on = my_row < tall;
-    const float count = static_cast<float>(r1 - r0), all = static_cast<float>(a.positions);
+    const float count = rows_of(a, rank), all = static_cast<float>(a.positions);
     const int act = a.act;
     const auto wait_full = [&](uint32_t s) {
         const bool got = mbar_wait(full + 8 * s, ring.full >> s & 1);
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
     const uint64_t step_out = tall * a.out.ld;
     const auto over = [&](uint32_t stage, uint32_t s, T* out, auto f) {
         if (!on) return;
-        const uint32_t first = r0 + stage * a.stage_rows, rows = min(a.stage_rows, r1 - first);
+        const uint32_t first = first_of(stage), rows = min(a.stage_rows, a.positions - first);
         const uint8_t* from = dyn + s * kOneStage + mine;
         T* to = out + (first + my_row) * a.out.ld + c;
         uint32_t r = my_row;
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 rows[u] = 0.0f;
                 if (i >= a.chunks) continue;
                 v[u] = __ldcg(part + i * a.groups + g);
-                rows[u] = static_cast<float>(min(a.rows, a.positions - i * a.rows));
+                rows[u] = rows_of(a, i);
             }
 #pragma unroll
             for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
@@ -438,8 +449,7 @@ bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms) {
     const uint64_t stages = (a.positions + a.stage_rows - 1) / a.stage_rows, hold = (stages + a.slots - 1) / a.slots;
     uint64_t k = std::max<uint64_t>(hold, std::min<uint64_t>(std::max<uint64_t>(1, sms / a.n), stages));
     k = std::min<uint64_t>({k, sms, kOneChunks});
-    a.rows = static_cast<uint32_t>((a.positions + k - 1) / k);
-    a.chunks = (a.positions + a.rows - 1) / a.rows;
+    a.chunks = static_cast<uint32_t>(std::min(k, stages));
     a.across = std::min({a.n, sms / a.chunks, a.chunks > 1 ? kOneGroups : sms});
     return true;
 }
