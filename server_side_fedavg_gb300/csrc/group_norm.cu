@@ -35,6 +35,9 @@ struct Tile {
           row(threadIdx.x / width), on(row < tall) {}
 };
 
+// Lanes for each of a warp's sums of n terms: a power of two.
+__device__ __forceinline__ uint32_t lanes_for(uint32_t n) { return n >= 32 ? 32 : n <= 1 ? 1 : 2u << (31 - __clz(n - 1)); }
+
 // Sums over a tile's positions: s[i][j] of every thread of a column end up in its first one.
 template <int N, int V>
 __device__ __forceinline__ void sum_rows(float (&s)[N][V], float* red, const Tile& t) {
@@ -66,7 +69,8 @@ template <bool kReverse, int kStreams, int V, typename T, typename F>
 __device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t ld0, const T* p1, uint64_t ld1, uint32_t r0,
                                           uint32_t r1, uint32_t c, F f) {
     if (!t.on) return;
-    constexpr uint32_t kU = 4;
+    // 64 bytes of either stream in flight per thread, and no more than eight positions
+    constexpr uint32_t kU = sizeof(T) * V >= 16 ? 4 : 8;
     const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
     const auto row_of = [&](uint32_t i) { return r0 + t.row + (kReverse ? mine - 1 - i : i) * t.tall; };
     uint32_t i = 0;
@@ -90,9 +94,9 @@ __device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t l
 // part[sample][chunk][group] = (mean, sum of squares about it) over the chunk's positions, the mean
 // less ref[sample][group], the group's first value.
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormThreads) norm_stat_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *mean = sm, *sq = mean + a.channels, *red = sq + a.channels;
+    float *mean = sm, *sq = mean + a.channels, *from0 = sq + a.channels, *red = from0 + a.channels;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
@@ -120,24 +124,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_stat_kernel(const __grid_co
                 for (int i = 0; i < V; ++i) {
                     const float m = s[0][i] / count;
                     mean[c + i] = m;
+                    from0[c + i] = from[i];
                     sq[c + i] = fmaxf(s[1][i] - s[0][i] * m, 0.0f);
                 }
             __syncthreads();
         }
-        for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+        // a group per `lanes` lanes
+        const uint32_t lanes = lanes_for(per), sub = lane % lanes;
+        for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
+            const uint32_t g = g0 + lane / lanes, end = g < a.groups ? (g + 1) * per : 0;
+            const float ref = g < a.groups ? from0[g * per] : 0.0f;
             float m = 0.0f, q = 0.0f;
-            const float ref = elem(x, g * per, sizeof(T) == 2);
-            for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
-                mean[c] += elem(x, c, sizeof(T) == 2) - ref;
+            for (uint32_t c = g * per + sub; c < end; c += lanes) {
+                mean[c] += from0[c] - ref;
                 m += mean[c];
             }
-            m = warp_sum(m) / static_cast<float>(per);
-            for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
+            m = lane_sum(m, lanes) / static_cast<float>(per);
+            for (uint32_t c = g * per + sub; c < end; c += lanes) {
                 const float d = mean[c] - m;
                 q += fmaf(count * d, d, sq[c]);
             }
-            q = warp_sum(q);
-            if (lane == 0) {
+            q = lane_sum(q, lanes);
+            if (sub == 0 && g < a.groups) {
                 a.part[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float2(m, q);
                 if (blockIdx.x == 0) a.ref[static_cast<uint64_t>(sample) * a.groups + g] = ref;
             }
@@ -149,22 +157,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_stat_kernel(const __grid_co
 // A sample's mean (less the reference) and 1 / sqrt(variance + eps) per group, from its chunks' parts, into shared memory.
 __device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, float* mean, float* rstd) {
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, per = a.channels / a.groups;
+    const uint32_t lanes = lanes_for(a.chunks), sub = lane % lanes;
     const float all = static_cast<float>(a.positions);
-    for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+    const auto rows_of = [&](uint32_t i) { return static_cast<float>(min(a.rows, a.positions - i * a.rows)); };
+    for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
+        const uint32_t g = g0 + lane / lanes, end = g < a.groups ? a.chunks : 0;
         const float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
         float m = 0.0f, q = 0.0f;
-        for (uint32_t i = lane; i < a.chunks; i += 32) {
-            const float rows = static_cast<float>(min(a.rows, a.positions - i * a.rows));
-            m = fmaf(part[static_cast<uint64_t>(i) * a.groups].x, rows, m);
-        }
-        m = warp_sum(m) / all;
-        for (uint32_t i = lane; i < a.chunks; i += 32) {
-            const float2 p = part[static_cast<uint64_t>(i) * a.groups];
-            const float rows = static_cast<float>(min(a.rows, a.positions - i * a.rows)), d = p.x - m;
-            q += fmaf(rows * static_cast<float>(per) * d, d, p.y);
-        }
-        q = warp_sum(q) / (all * static_cast<float>(per));
-        if (lane == 0) {
+        float2 own = make_float2(0.0f, 0.0f);        // this lane's first: with few chunks its only one
+        if (sub < end) own = part[static_cast<uint64_t>(sub) * a.groups];
+        if (sub < end) m = own.x * rows_of(sub);
+#pragma unroll 4
+        for (uint32_t i = sub + lanes; i < end; i += lanes) m = fmaf(part[static_cast<uint64_t>(i) * a.groups].x, rows_of(i), m);
+        m = lane_sum(m, lanes) / all;
+        const auto square = [&](float2 p, uint32_t i) {
+            const float d = p.x - m;
+            return fmaf(rows_of(i) * static_cast<float>(per) * d, d, p.y);
+        };
+        if (sub < end) q = square(own, sub);
+#pragma unroll 4
+        for (uint32_t i = sub + lanes; i < end; i += lanes) q += square(part[static_cast<uint64_t>(i) * a.groups], i);
+        q = lane_sum(q, lanes) / (all * static_cast<float>(per));
+        if (sub == 0 && g < a.groups) {
             mean[g] = m;
             rstd[g] = 1.0f / sqrtf(q + a.eps);
         }
@@ -172,7 +186,7 @@ __device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, 
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_apply_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
     float *mean = sm, *rstd = mean + a.groups, *ref = rstd + a.groups;
     wait_predecessor();
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const __grid_c
 // part[sample][chunk][group] = sums of gamma dz and gamma dz xhat over the chunk;
 // cpart[its CTA][channel] = sums of dz and dz xhat over the CTA's chunks.
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, kNormGradCtas) norm_grad_stat_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
     float *s0 = sm, *s1 = s0 + a.channels, *t0 = s1 + a.channels, *t1 = t0 + a.channels,
           *red = t1 + a.channels;
@@ -262,15 +276,18 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __gr
                 }
             __syncthreads();
         }
-        for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+        const uint32_t lanes = lanes_for(per), sub = lane % lanes;
+        for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
+            const uint32_t g = g0 + lane / lanes, end = g < a.groups ? (g + 1) * per : 0;
             float p = 0.0f, q = 0.0f;
-            for (uint32_t c = g * per + lane; c < (g + 1) * per; c += 32) {
+            for (uint32_t c = g * per + sub; c < end; c += lanes) {
                 p += s0[c];
                 q += s1[c];
             }
-            p = warp_sum(p);
-            q = warp_sum(q);
-            if (lane == 0) a.part[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float2(p, q);
+            p = lane_sum(p, lanes);
+            q = lane_sum(q, lanes);
+            if (sub == 0 && g < a.groups)
+                a.part[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float2(p, q);
         }
         __syncthreads();
     }
@@ -281,7 +298,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_stat_kernel(const __gr
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, kNormGradCtas) norm_grad_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
     float *c1 = sm, *c2 = c1 + a.groups;
     wait_predecessor();
@@ -290,17 +307,20 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_co
     const int act = a.act;
     const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(per));
     for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
-        for (uint32_t g = warp; g < a.groups; g += kNormWarps) {
+        const uint32_t lanes = lanes_for(a.chunks), sub = lane % lanes;
+        for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
+            const uint32_t g = g0 + lane / lanes, end = g < a.groups ? a.chunks : 0;
             const float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
             float p = 0.0f, q = 0.0f;
-            for (uint32_t i = lane; i < a.chunks; i += 32) {
+#pragma unroll 4
+            for (uint32_t i = sub; i < end; i += lanes) {
                 const float2 v = part[static_cast<uint64_t>(i) * a.groups];
                 p += v.x;
                 q += v.y;
             }
-            p = warp_sum(p);
-            q = warp_sum(q);
-            if (lane == 0) {
+            p = lane_sum(p, lanes);
+            q = lane_sum(q, lanes);
+            if (sub == 0 && g < a.groups) {
                 c1[g] = p * inv;
                 c2[g] = q * inv;
             }
@@ -419,7 +439,7 @@ cudaError_t passes(NormArgs a, bool backward, cudaStream_t stream, unsigned* lau
     a.row0 = 0;
     for (a.first = 0; a.first < n && e == cudaSuccess; a.first = a.last) {
         a.last = a.first + std::min(n - a.first, a.batch);
-        e = launch_one(backward ? k.grad_stat : k.stat, a, (backward ? 16 : 8) * a.channels + red, stream);
+        e = launch_one(backward ? k.grad_stat : k.stat, a, (backward ? 16 : 12) * a.channels + red, stream);
         if (e == cudaSuccess) e = launch_one(backward ? k.grad : k.apply, a, (backward ? 8 : 12) * a.groups, stream);
         *launches += 2;
         a.row0 += a.across;

@@ -14,15 +14,26 @@ struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
 
-// (16 bytes by a load that stays where it is written: the loops below ask for several, then use them)
+// By a load that stays where it is written: the loops below ask for several, then use them.
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load_raw(const T* p) {
     Vec<T, V> q;
-    if constexpr (sizeof(T) * V == 16) {
+    constexpr size_t kSize = sizeof(T) * V;
+    if constexpr (kSize == 16) {
         const uint4 w = ld_plain_v4(p);
-        memcpy(&q, &w, 16);
+        memcpy(&q, &w, kSize);
+    } else if constexpr (kSize == 8) {
+        uint2 w;
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+        memcpy(&q, &w, kSize);
+    } else if constexpr (kSize == 4) {
+        uint32_t w;
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(p));
+        memcpy(&q, &w, kSize);
     } else {
-        q = *reinterpret_cast<const Vec<T, V>*>(p);
+        uint16_t w;
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(w) : "l"(p));
+        memcpy(&q, &w, kSize);
     }
     return q;
 }
@@ -149,6 +160,12 @@ __device__ __forceinline__ void times_act_grad(int act, float (&d)[V], const flo
         fma(t, t, r, s);
         mul(d, d, t);
     }
+}
+
+// Over `lanes` neighbouring lanes, a power of two.
+__device__ __forceinline__ float lane_sum(float v, uint32_t lanes) {
+    for (uint32_t o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+    return v;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -1,6 +1,7 @@
 // Group norm and its gradients in one kernel, where a sample's positions are one run of bytes.
 //
-// k CTAs share a sample, each every k-th stage of its positions; one CTA per SM, launched cooperatively.  A
+// k CTAs share a sample, each every k-th stage of its positions; one CTA per SM, launched
+// cooperatively or as clusters.  A
 // warp of its own fetches them by bulk copies into a ring of 40 KB stages; 20 warps compute, which
 // leaves each thread 80 registers.
 // After the statistics' pass the CTAs meet at a counter in global memory, join their parts, and
@@ -22,6 +23,9 @@ constexpr uint32_t kOneStage = 40960, kOneSlots = 5;
 constexpr uint32_t kOneRed = 128 * (kOneWarps + 2);   // floats: the sums over the positions
 static_assert(kOneRed >= 4 * kOneThreads, "four of every thread's sums");
 constexpr uint32_t kOneChunks = 160;                  // CTAs of a sample: five per lane of a warp
+// Bytes of a sample's inputs from which on one kernel is faster: 32 of 4096 x 128 bf16 (1 MB) take 27
+// us so and 22 in two passes, one of 32768 x 64 bf16 (4 MB) 14 and 15, 2 of 32768 x 256 fp32 31 and 39.
+constexpr double kOneLeast = 4e6;
 constexpr uint32_t kOneMost = 225 * 1024;             // dynamic shared memory
 constexpr uint32_t kOneGroups = 80;                   // counters for samples at one time, and one for the end
 
@@ -144,8 +148,8 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
     __shared__ uint64_t bars[2 * kOneSlots];
     float* red = reinterpret_cast<float*>(dyn + a.slots * kOneStage);
     float *s0 = red + kOneRed, *s1 = s0 + a.channels;                      // of a channel
-    float *t0 = s1 + a.channels, *t1 = t0 + (kBackward ? a.channels : 0);          // gradients so far (backward)
-    float *g0 = t1 + (kBackward ? a.channels : 0), *g1 = g0 + a.groups, *ref = g1 + a.groups;
+    float *t0 = s1 + a.channels, *t1 = t0 + (kBackward ? a.channels : 0);          // gradients so far; forward: first values
+    float *g0 = t1 + a.channels, *g1 = g0 + a.groups, *ref = g1 + a.groups;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kOneSlots;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -290,6 +294,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     const float m = s[0][i] / count;
                     s0[c + i] = m;
                     s1[c + i] = fmaxf(s[1][i] - s[0][i] * m, 0.0f);
+                    t0[c + i] = -less[i];
                 }
             }
         sync_compute();
@@ -304,9 +309,9 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 }
                 p = warp_sum(p);
             } else {
-                const float from = elem(x, g * per, sizeof(T) == 2);
+                const float from = t0[g * per];
                 for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
-                    s0[k] += elem(x, k, sizeof(T) == 2) - from;
+                    s0[k] += t0[k] - from;
                     p += s0[k];
                 }
                 p = warp_sum(p) / static_cast<float>(per);
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
 
 // Shared memory beside the ring.
 uint32_t fixed_bytes(const NormArgs& a, bool backward) {
-    return (kOneRed + (backward ? 4 : 2) * a.channels + 3 * a.groups) * 4;
+    return (kOneRed + (backward ? 4 : 3) * a.channels + 3 * a.groups) * 4;
 }
 // Channels of a thread: 16 bytes, but for the gradients of bf16 four, whose state would not fit its
 // registers otherwise.
@@ -444,13 +449,28 @@ bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms) {
     const uint32_t row = a.channels * size, tall = kOneThreads / (a.channels / channels_of(a.dtype, backward));
     a.stage_rows = kOneStage / streams / row / tall * tall;
     a.slots = std::min(kOneSlots, (kOneMost - fixed_bytes(a, backward)) / kOneStage);
-    // CTAs per sample: so many that it stays in their shared memory, and so many that all SMs have
-    // work, but a stage each at least.
-    const uint64_t stages = (a.positions + a.stage_rows - 1) / a.stage_rows, hold = (stages + a.slots - 1) / a.slots;
-    uint64_t k = std::max<uint64_t>(hold, std::min<uint64_t>(std::max<uint64_t>(1, sms / a.n), stages));
-    k = std::min<uint64_t>({k, sms, kOneChunks});
-    a.chunks = static_cast<uint32_t>(std::min(k, stages));
-    a.across = std::min({a.n, sms / a.chunks, a.chunks > 1 ? kOneGroups : sms});
+    // Samples at one time, each with its share of the SMs: the least by a model of the rounds that takes.
+    // A round moves its samples' bytes, with what is not kept in shared memory read again, at the SMs'
+    // share of 6.5 TB/s, and has some 9 us of sums and waiting.  Two of 128^3 x 32 bf16 take 135 us side
+    // by side and 141 one after the other, the gradients of three of 45 x 47 x 51 x 64 fp32 68 and 81.
+    const uint64_t stages = (a.positions + a.stage_rows - 1) / a.stage_rows;
+    const double out = static_cast<double>(a.positions) * row, in = out * streams;
+    if (in < kOneLeast) return false;
+    double best = 1e300;
+    for (uint32_t rounds = 1; rounds <= std::min(a.n, 64u); ++rounds) {
+        const uint32_t g = (a.n + rounds - 1) / rounds;
+        if (g > sms) continue;
+        const uint32_t k = static_cast<uint32_t>(std::min<uint64_t>({sms / g, stages, kOneChunks}));
+        if (k > 1 && g > kOneGroups) continue;
+        const double again = std::max(0.0, in - static_cast<double>(k) * a.slots * kOneStage);
+        const double cost = rounds * ((in + again + out) / (6.5e6 * k / sms) + 9.0);
+        if (cost < best) {
+            best = cost;
+            a.chunks = k;
+            a.across = g;
+        }
+    }
+    if (best > 1e299) return false;
     return true;
 }
 
@@ -468,9 +488,16 @@ cudaError_t launch_norm_one(const NormArgs& a, bool backward, cudaStream_t strea
     cfg.blockDim = dim3(kOneThreads + 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    // CTAs that meet run at the same time: those of a cluster do, others in a cooperative launch
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeCooperative;
-    at[0].val.cooperative = 1;
+    if (a.chunks <= 8) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = a.chunks;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    } else {
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+    }
     cfg.attrs = at;
     cfg.numAttrs = a.chunks > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k, a);

@@ -7,9 +7,11 @@
 // exactly: no table of cosines is read, and a far position is as exact as a near one.  The
 // quadrant is taken off in integers too; the rest, |t| <= pi / 4, goes through sincospif.
 //
-// A thread has V pairs (its vectors are V elements) and turns them in several heads of one token,
-// so that the sines are computed once for all of these.  What bounds it: HBM, each element read
-// and written once.
+// A CTA has a few tokens, or for a few tokens some of their heads.  Its threads compute the sines of
+// the tokens' pairs into shared memory, each once, while their first vectors are on their way;
+// then each takes the vectors of one place in the heads, all heads and tokens in turn.
+//
+// What bounds it: HBM, each element read and written once.
 #include "product_device.cuh"
 #include "rotary.cuh"
 
@@ -18,7 +20,8 @@ namespace fa {
 namespace {
 
 constexpr uint32_t kRotThreads = 256;
-constexpr uint32_t kAhead = 4;            // heads whose loads are in flight together
+constexpr uint32_t kRotTokens = 4;        // of a CTA
+constexpr uint32_t kAhead = 4;            // heads whose loads a thread has in flight
 
 // V elements of T, as they lie in memory.
 template <typename T, int V>
@@ -44,97 +47,101 @@ __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(stat
 __device__ __forceinline__ void narrow(float x, float& y) { y = x; }
 __device__ __forceinline__ void narrow(float x, uint16_t& y) { y = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-__device__ __forceinline__ void sin_cos_turn(uint64_t turn, float& s, float& c) {
+__device__ __forceinline__ float2 cos_sin_turn(uint64_t turn) {
     // to the nearest quarter, and what is left in 2^-33 of half a turn
     const uint64_t q = turn + (1ull << 61);
     const int32_t rest = static_cast<int32_t>(static_cast<int64_t>(turn - (q >> 62 << 62)) >> 30);
     float sn, cs;
     sincospif(static_cast<float>(rest) * 0x1p-33f, &sn, &cs);
     const uint32_t quad = static_cast<uint32_t>(q >> 62);
-    s = quad & 1 ? cs : sn;
-    c = quad & 1 ? sn : cs;
-    if (quad & 2) s = -s;
-    if (quad == 1 || quad == 2) c = -c;
+    const float c = quad & 1 ? sn : cs, s = quad & 1 ? cs : sn;
+    return make_float2(quad == 1 || quad == 2 ? -c : c, quad & 2 ? -s : s);
 }
 
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     typedef Pack<T, V> P;
-    __shared__ uint64_t turns[kRotaryMaxPairs];
-    const uint32_t half = a.rotary_dim / 2;
-    for (uint32_t i = threadIdx.x; i < half; i += kRotThreads) turns[i] = a.turns[i];
-    __syncthreads();
+    extern __shared__ __align__(16) float table[];      // [tokens][cos, sin][rotary_dim / 2]
+    __shared__ int live[kRotTokens];
     wait_predecessor();
-    const uint64_t at = blockIdx.x * static_cast<uint64_t>(kRotThreads) + threadIdx.x;
-    const uint32_t per = a.chunks * a.slots;
-    const uint64_t which = at >> 32 ? at / per : static_cast<uint32_t>(at) / per;
-    if (which >= a.tokens) return;
-    const uint32_t token = static_cast<uint32_t>(which), in = static_cast<uint32_t>(at - which * per);
-    const uint32_t slot = in / a.chunks, chunk = in - slot * a.chunks;
-    const uint32_t b = token / a.seq, s = token - b * a.seq;
-    // the two vectors of this thread in a head
-    const bool turn = chunk < a.turning;
+    const uint32_t half = a.rotary_dim / 2;
+    const uint32_t token0 = blockIdx.x * a.cta_tokens, tokens = min(a.cta_tokens, a.tokens - token0);
+    const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
+    const uint32_t head0 = blockIdx.y * a.cta_heads, mine = min(a.cta_heads, heads - head0);
+
+    // This thread's place in a head, its two vectors there, and the row (token, head) it begins with;
+    // the CTA has `tall` rows at a time.
+    const uint32_t tall = kRotThreads / a.chunks, chunk = threadIdx.x % a.chunks, row0 = threadIdx.x / a.chunks;
+    const bool on = row0 < tall, turn = chunk < a.turning;
     const uint32_t e0 = !turn ? a.rotary_dim + (chunk - a.turning) * 2 * V : kInterleaved ? chunk * 2 * V : chunk * V;
     const uint32_t e1 = turn && !kInterleaved ? e0 + half : e0 + V;
     const bool second = e1 < a.head_dim;
-    const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
-    const T* x0 = static_cast<const T*>(a.part[0].x) + b * a.part[0].xb + s * a.part[0].xt;
-    const T* x1 = static_cast<const T*>(a.part[1].x) + b * a.part[1].xb + s * a.part[1].xt;
-    T* o0 = static_cast<T*>(a.part[0].out) + b * a.part[0].ob + s * a.part[0].ot;
-    T* o1 = static_cast<T*>(a.part[1].out) + b * a.part[1].ob + s * a.part[1].ot;
+    const uint32_t rows = tokens * mine;
     P u[kAhead], v[kAhead];
-    const auto fetch = [&](uint32_t h0) {
+    const auto place = [&](uint32_t row, uint32_t& t, bool out) {
+        t = row / mine;
+        const uint32_t h = head0 + row - t * mine, token = token0 + t, b = token / a.seq, s = token - b * a.seq;
+        const bool k = h >= heads0;
+        const RotaryPart& p = a.part[k];
+        return out ? b * p.ob + s * p.ot + (k ? h - heads0 : h) * p.oh : b * p.xb + s * p.xt + (k ? h - heads0 : h) * p.xh;
+    };
+    const auto is_k = [&](uint32_t row) { return head0 + row % mine >= heads0; };
+    const auto fetch = [&](uint32_t row) {
 #pragma unroll
-        for (uint32_t k = 0; k < kAhead; ++k) {
-            const uint32_t h = h0 + k * a.slots;
-            if (h >= heads) break;
-            const T* x = h < heads0 ? x0 + h * a.part[0].xh : x1 + (h - heads0) * a.part[1].xh;
-            u[k] = load_pack<T, V>(x + e0);
-            if (second) v[k] = load_pack<T, V>(x + e1);
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            if (row + i * tall >= rows) break;
+            uint32_t t;
+            const uint64_t at = place(row + i * tall, t, false);
+            const T* x = static_cast<const T*>(a.part[is_k(row + i * tall)].x) + at;
+            u[i] = load_pack<T, V>(x + e0);
+            if (second) v[i] = load_pack<T, V>(x + e1);
         }
     };
-    fetch(slot);                         // on their way while the sines are computed
-    uint64_t pos;
-    if (a.position) {
-        const int32_t p = a.position[token];
-        if (p < 0) return;               // padding: left as it is
-        pos = static_cast<uint64_t>(p);
-    } else {
-        pos = static_cast<uint64_t>(a.first) + s;
-    }
-    float cs[V], sn[V];
-    if (turn) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint64_t t = pos * turns[chunk * V + i];
-            sin_cos_turn(a.inverse ? 0 - t : t, sn[i], cs[i]);
-            sn[i] *= a.scale;
-            cs[i] *= a.scale;
+    if (on) fetch(row0);
+    for (uint32_t i = threadIdx.x; i < tokens * half; i += kRotThreads) {
+        const uint32_t t = i / half, pair = i - t * half, token = token0 + t;
+        uint64_t pos;
+        if (a.position) {
+            const int32_t p = a.position[token];
+            if (pair == 0) live[t] = p >= 0;             // negative: padding, left as it is
+            pos = static_cast<uint64_t>(static_cast<int64_t>(p));
+        } else {
+            if (pair == 0) live[t] = 1;
+            pos = static_cast<uint64_t>(a.first) + token % a.seq;
         }
+        const uint64_t angle = pos * a.turns[pair];
+        const float2 cs = cos_sin_turn(a.inverse ? 0 - angle : angle);
+        table[2 * t * half + pair] = cs.x * a.scale;
+        table[(2 * t + 1) * half + pair] = cs.y * a.scale;
     }
-    for (uint32_t h0 = slot;;) {
+    __syncthreads();
+    if (!on) return;
+    for (uint32_t row = row0;;) {
 #pragma unroll
-        for (uint32_t k = 0; k < kAhead; ++k) {
-            const uint32_t h = h0 + k * a.slots;
-            if (h >= heads) break;
-            T* o = h < heads0 ? o0 + h * a.part[0].oh : o1 + (h - heads0) * a.part[1].oh;
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            if (row + i * tall >= rows) break;
+            uint32_t t;
+            const uint64_t at = place(row + i * tall, t, true);
+            if (!live[t]) continue;
+            T* o = static_cast<T*>(a.part[is_k(row + i * tall)].out) + at;
             if (turn) {
+                const float *cs = table + 2 * t * half + chunk * V, *sn = cs + half;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    // interleaved: pair i is elements 2 i and 2 i + 1 of the two vectors in a row
-                    T& p = !kInterleaved ? u[k].e[i] : 2 * i < V ? u[k].e[2 * i % V] : v[k].e[2 * i % V];
-                    T& q = !kInterleaved ? v[k].e[i] : 2 * i + 1 < V ? u[k].e[(2 * i + 1) % V] : v[k].e[(2 * i + 1) % V];
+                for (int j = 0; j < V; ++j) {
+                    // interleaved: pair j is elements 2 j and 2 j + 1 of the two vectors in a row
+                    T& p = !kInterleaved ? u[i].e[j] : 2 * j < V ? u[i].e[2 * j % V] : v[i].e[2 * j % V];
+                    T& q = !kInterleaved ? v[i].e[j] : 2 * j + 1 < V ? u[i].e[(2 * j + 1) % V] : v[i].e[(2 * j + 1) % V];
                     const float f = widen(p), g = widen(q);
-                    narrow(fmaf(f, cs[i], -(g * sn[i])), p);
-                    narrow(fmaf(g, cs[i], f * sn[i]), q);
+                    narrow(fmaf(f, cs[j], -(g * sn[j])), p);
+                    narrow(fmaf(g, cs[j], f * sn[j]), q);
                 }
             }
-            *reinterpret_cast<P*>(o + e0) = u[k];
-            if (second) *reinterpret_cast<P*>(o + e1) = v[k];
+            *reinterpret_cast<P*>(o + e0) = u[i];
+            if (second) *reinterpret_cast<P*>(o + e1) = v[i];
         }
-        h0 += kAhead * a.slots;
-        if (h0 >= heads) return;
-        fetch(h0);
+        row += kAhead * tall;
+        if (row >= rows) return;
+        fetch(row);
     }
 }
 
@@ -142,16 +149,24 @@ template <typename T, int V>
 cudaError_t launch_v(RotaryArgs& a, uint32_t sms, cudaStream_t stream) {
     a.turning = a.rotary_dim / 2 / V;
     a.chunks = a.turning + (a.copy ? (a.head_dim - a.rotary_dim + 2 * V - 1) / (2 * V) : 0);
-    // Eight heads a thread where that leaves the SMs full (1536 threads each, twice over), else
-    // fewer, down to one.
+    // kRotTokens tokens a CTA where that leaves eight CTAs per SM, else fewer; for fewer tokens than
+    // twice the SMs the heads are shared out too.
     const uint32_t heads = a.part[0].heads + a.part[1].heads;
-    const uint64_t each = static_cast<uint64_t>(a.tokens) * a.chunks, want = 2ull * 1536 * sms;
-    uint64_t slots = std::max<uint64_t>((heads + 7) / 8, (want + each - 1) / each);
-    a.slots = static_cast<uint32_t>(std::min<uint64_t>(slots, heads));
-    const uint64_t blocks = (each * a.slots + kRotThreads - 1) / kRotThreads;
-    if (blocks >= 1ull << 31) return cudaErrorInvalidValue;
-    return launch_next(a.interleaved ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>,
-                       dim3(static_cast<uint32_t>(blocks)), kRotThreads, stream, a);
+    a.cta_tokens = std::max(1u, std::min(kRotTokens, a.tokens / (8 * sms)));
+    const uint32_t blocks = (a.tokens + a.cta_tokens - 1) / a.cta_tokens, share = std::min(heads, std::max(1u, 2 * sms / blocks));
+    a.cta_heads = (heads + share - 1) / share;
+    if (a.chunks > kRotThreads) return launch_rotary_wide(a, stream);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, (heads + a.cta_heads - 1) / a.cta_heads);
+    cfg.blockDim = dim3(kRotThreads);
+    cfg.dynamicSmemBytes = a.cta_tokens * a.rotary_dim * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, a.interleaved ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>, a);
 }
 
 }  // namespace
