@@ -21,11 +21,11 @@ namespace {
 
 constexpr uint32_t kRotThreads = 256;
 constexpr uint32_t kRotTokens = 4;        // of a CTA
-constexpr uint32_t kAhead = 4;            // heads whose loads a thread has in flight
+constexpr uint32_t kAhead = 2;            // heads whose loads a thread has in flight
 
 // V elements of T, as they lie in memory.
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
+struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
     T e[V];
 };
 
@@ -47,6 +47,14 @@ __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(stat
 __device__ __forceinline__ void narrow(float x, float& y) { y = x; }
 __device__ __forceinline__ void narrow(float x, uint16_t& y) { y = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
+// V floats of shared memory, at a multiple of V.
+template <int V>
+__device__ __forceinline__ void load_table(const float* p, float (&x)[V]) {
+    const Pack<float, V> q = *reinterpret_cast<const Pack<float, V>*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = q.e[i];
+}
+
 __device__ __forceinline__ float2 cos_sin_turn(uint64_t turn) {
     // to the nearest quarter, and what is left in 2^-33 of half a turn
     const uint64_t q = turn + (1ull << 61);
@@ -62,70 +70,81 @@ template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     typedef Pack<T, V> P;
     extern __shared__ __align__(16) float table[];      // [tokens][cos, sin][rotary_dim / 2]
-    __shared__ int live[kRotTokens];
+    __shared__ uint64_t at_in[kRotTokens][2], at_out[kRotTokens][2];
+    __shared__ int64_t position[kRotTokens];             // -1: padding, left as it is
     wait_predecessor();
     const uint32_t half = a.rotary_dim / 2;
     const uint32_t token0 = blockIdx.x * a.cta_tokens, tokens = min(a.cta_tokens, a.tokens - token0);
     const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
     const uint32_t head0 = blockIdx.y * a.cta_heads, mine = min(a.cta_heads, heads - head0);
+    if (threadIdx.x < tokens) {
+        const uint32_t t = threadIdx.x, b = (token0 + t) / a.seq, s = token0 + t - b * a.seq;
+        const int32_t p = a.position ? a.position[token0 + t] : 0;
+        position[t] = a.position ? (p < 0 ? -1 : p) : a.first + s;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            at_in[t][k] = b * a.part[k].xb + s * a.part[k].xt;
+            at_out[t][k] = b * a.part[k].ob + s * a.part[k].ot;
+        }
+    }
+    __syncthreads();
 
     // This thread's place in a head, its two vectors there, and the row (token, head) it begins with;
     // the CTA has `tall` rows at a time.
-    const uint32_t tall = kRotThreads / a.chunks, chunk = threadIdx.x % a.chunks, row0 = threadIdx.x / a.chunks;
-    const bool on = row0 < tall, turn = chunk < a.turning;
+    const uint32_t chunk0 = blockIdx.z * kRotThreads, width = min(a.chunks - chunk0, kRotThreads), tall = kRotThreads / width;
+    const uint32_t chunk = chunk0 + threadIdx.x % width, row0 = threadIdx.x / width;
+    const bool turn = chunk < a.turning;
     const uint32_t e0 = !turn ? a.rotary_dim + (chunk - a.turning) * 2 * V : kInterleaved ? chunk * 2 * V : chunk * V;
     const uint32_t e1 = turn && !kInterleaved ? e0 + half : e0 + V;
     const bool second = e1 < a.head_dim;
-    const uint32_t rows = tokens * mine;
-    P u[kAhead], v[kAhead];
-    const auto place = [&](uint32_t row, uint32_t& t, bool out) {
-        t = row / mine;
-        const uint32_t h = head0 + row - t * mine, token = token0 + t, b = token / a.seq, s = token - b * a.seq;
-        const bool k = h >= heads0;
-        const RotaryPart& p = a.part[k];
-        return out ? b * p.ob + s * p.ot + (k ? h - heads0 : h) * p.oh : b * p.xb + s * p.xt + (k ? h - heads0 : h) * p.xh;
+    struct Row {
+        uint32_t t, h;                       // of the CTA's tokens and heads
     };
-    const auto is_k = [&](uint32_t row) { return head0 + row % mine >= heads0; };
-    const auto fetch = [&](uint32_t row) {
+    const auto on = [&](Row r) {             // tall rows on
+        r.h += tall;
+        while (r.h >= mine) {
+            r.h -= mine;
+            ++r.t;
+        }
+        return r;
+    };
+    Row row = {0, row0};
+    while (row.h >= mine) {
+        row.h -= mine;
+        ++row.t;
+    }
+    if (row0 >= tall) row.t = tokens;
+    P u[kAhead], v[kAhead];
+    const auto fetch = [&](Row r) {
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i) {
-            if (row + i * tall >= rows) break;
-            uint32_t t;
-            const uint64_t at = place(row + i * tall, t, false);
-            const T* x = static_cast<const T*>(a.part[is_k(row + i * tall)].x) + at;
+        for (uint32_t i = 0; i < kAhead; ++i, r = on(r)) {
+            if (r.t >= tokens) break;
+            const bool k = head0 + r.h >= heads0;
+            const T* x = static_cast<const T*>(a.part[k].x) + at_in[r.t][k] + (head0 + r.h - (k ? heads0 : 0)) * a.part[k].xh;
             u[i] = load_pack<T, V>(x + e0);
             if (second) v[i] = load_pack<T, V>(x + e1);
         }
     };
-    if (on) fetch(row0);
-    for (uint32_t i = threadIdx.x; i < tokens * half; i += kRotThreads) {
-        const uint32_t t = i / half, pair = i - t * half, token = token0 + t;
-        uint64_t pos;
-        if (a.position) {
-            const int32_t p = a.position[token];
-            if (pair == 0) live[t] = p >= 0;             // negative: padding, left as it is
-            pos = static_cast<uint64_t>(static_cast<int64_t>(p));
-        } else {
-            if (pair == 0) live[t] = 1;
-            pos = static_cast<uint64_t>(a.first) + token % a.seq;
+    fetch(row);
+    for (uint32_t t = 0; t < tokens; ++t)
+        for (uint32_t pair = threadIdx.x; pair < half; pair += kRotThreads) {
+            const uint64_t angle = static_cast<uint64_t>(position[t]) * a.turns[pair];
+            const float2 cs = cos_sin_turn(a.inverse ? 0 - angle : angle);
+            table[2 * t * half + pair] = cs.x * a.scale;
+            table[(2 * t + 1) * half + pair] = cs.y * a.scale;
         }
-        const uint64_t angle = pos * a.turns[pair];
-        const float2 cs = cos_sin_turn(a.inverse ? 0 - angle : angle);
-        table[2 * t * half + pair] = cs.x * a.scale;
-        table[(2 * t + 1) * half + pair] = cs.y * a.scale;
-    }
     __syncthreads();
-    if (!on) return;
-    for (uint32_t row = row0;;) {
+    while (row.t < tokens) {
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i) {
-            if (row + i * tall >= rows) break;
-            uint32_t t;
-            const uint64_t at = place(row + i * tall, t, true);
-            if (!live[t]) continue;
-            T* o = static_cast<T*>(a.part[is_k(row + i * tall)].out) + at;
+        for (uint32_t i = 0; i < kAhead; ++i, row = on(row)) {
+            if (row.t >= tokens) return;
+            if (position[row.t] < 0) continue;
+            const bool k = head0 + row.h >= heads0;
+            T* o = static_cast<T*>(a.part[k].out) + at_out[row.t][k] + (head0 + row.h - (k ? heads0 : 0)) * a.part[k].oh;
             if (turn) {
-                const float *cs = table + 2 * t * half + chunk * V, *sn = cs + half;
+                float cs[V], sn[V];
+                load_table(table + 2 * row.t * half + chunk * V, cs);
+                load_table(table + (2 * row.t + 1) * half + chunk * V, sn);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     // interleaved: pair j is elements 2 j and 2 j + 1 of the two vectors in a row
@@ -139,8 +158,6 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_con
             *reinterpret_cast<P*>(o + e0) = u[i];
             if (second) *reinterpret_cast<P*>(o + e1) = v[i];
         }
-        row += kAhead * tall;
-        if (row >= rows) return;
         fetch(row);
     }
 }
@@ -155,9 +172,8 @@ cudaError_t launch_v(RotaryArgs& a, uint32_t sms, cudaStream_t stream) {
     a.cta_tokens = std::max(1u, std::min(kRotTokens, a.tokens / (8 * sms)));
     const uint32_t blocks = (a.tokens + a.cta_tokens - 1) / a.cta_tokens, share = std::min(heads, std::max(1u, 2 * sms / blocks));
     a.cta_heads = (heads + share - 1) / share;
-    if (a.chunks > kRotThreads) return launch_rotary_wide(a, stream);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, (heads + a.cta_heads - 1) / a.cta_heads);
+    cfg.gridDim = dim3(blocks, (heads + a.cta_heads - 1) / a.cta_heads, (a.chunks + kRotThreads - 1) / kRotThreads);
     cfg.blockDim = dim3(kRotThreads);
     cfg.dynamicSmemBytes = a.cta_tokens * a.rotary_dim * 4;
     cfg.stream = stream;

@@ -58,7 +58,8 @@ def inputs(batch, seq, heads, dim, dtype, seed):
 @pytest.mark.parametrize("batch,seq,qh,kh,dim,r,dtype", [
     (1, 1, 32, 32, 128, 128, "bf16"), (1, 1, 1, 0, 2, 2, "f32"), (2, 37, 8, 2, 64, 64, "bf16"), (3, 5, 3, 1, 80, 20, "f32"),
     (1, 300, 5, 5, 72, 72, "bf16"), (2, 19, 4, 4, 33, 22, "bf16"), (2, 19, 4, 2, 33, 6, "f32"), (1, 64, 2, 2, 512, 512, "f32"),
-    (2, 1000, 20, 4, 128, 64, "bf16"), (1, 2, 64, 64, 600, 512, "bf16"), (4, 129, 12, 12, 96, 48, "f32")])
+    (2, 1000, 20, 4, 128, 64, "bf16"), (1, 2, 64, 64, 600, 512, "bf16"), (2, 3, 2, 2, 1201, 10, "f32"), (1, 2, 1, 1, 5000, 512, "bf16"),
+    (3000, 1, 3, 1, 64, 64, "bf16"), (4, 129, 12, 12, 96, 48, "f32")])
 def test_queries_and_keys(work, layout, batch, seq, qh, kh, dim, r, dtype):
     q, k = inputs(batch, seq, qh, dim, dtype, 1), inputs(batch, seq, max(kh, 1), dim, dtype, 2)
     g = torch.Generator(device="cuda").manual_seed(3)
