@@ -23,6 +23,7 @@ struct OrthoBuf {
 struct OrthoProduct {
     const OrthoBuf *P, *Q, *out, *e1, *e2;    // e1, e2: laid out as out, or nullptr
     bool p_kmajor, q_kmajor;
+    bool single;                              // the hi terms alone
     bool symmetric;                           // the tiles on and above the diagonal, and their mirror images
     uint32_t items, k;
     uint32_t chunk;                           // blocks of 64 terms that the tensor cores sum by themselves

@@ -4,7 +4,7 @@
 //   v = c1 * sum_k P(x,k) Q(y,k) + c2 * e1 + c3 * e2
 //
 // x = hi + lo has 22 bits, so hi lo' + lo hi' + hi hi' is the product to 2^-22 of its size: three
-// products of fp16 where three bf16 terms would need six.  The matrices' scales keep |x| below
+// products of fp16 where three bf16 terms would need six.  `single` takes hi hi' alone.  The matrices' scales keep |x| below
 // 2^15, and their typical elements far above the 2^-24 where fp16 ends.
 //
 // A CTA's tile is 128 rows of P (TMEM lanes) by kBN rows of Q (TMEM columns); with kCtas == 2 a
@@ -49,7 +49,7 @@ struct Args {
     float c1, c2, c3;
     uint32_t rows, cols, kblocks, chunk;         // chunk: blocks between two emptyings
     uint32_t tiles_p, tiles_q, per, tiles;       // per: of an item
-    bool p_kmajor, q_kmajor, symmetric, test_expire;
+    bool p_kmajor, q_kmajor, symmetric, single, test_expire;
 };
 
 struct Tile {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         if constexpr (kBN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kLoadWarp && elect_one()) {
             const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
-            const bool pk = a.p_kmajor, qk = a.q_kmajor;
+            const bool pk = a.p_kmajor, qk = a.q_kmajor, single = a.single;
             const uint32_t kblocks = a.kblocks, tiles = a.tiles;
             const CUtensorMap *mp = &a.p, *mq = &a.q;
             const auto load = [&](uint32_t dst, const CUtensorMap* m, bool kmajor, uint32_t k, uint32_t x, uint32_t z, uint32_t bar) {
@@ -215,10 +215,12 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                         break;
                     }
                     if (leader) mbar_expect(full + 8 * s, kStageBytes * kCtas);
-                    load(at, mp, pk, kb * kBK, p0, z, bar);
-                    load(at + kPlane, mp, pk, kb * kBK, p0, z + 1, bar);
-                    load(at + 2 * kPlane, mq, qk, kb * kBK, q0, z, bar);
-                    load(at + 3 * kPlane, mq, qk, kb * kBK, q0, z + 1, bar);
+                    // hi and lo of one block of terms, or hi of two blocks
+                    const uint32_t k0 = kb * (single ? 2 * kBK : kBK), k1 = single ? k0 + kBK : k0, z1 = single ? z : z + 1;
+                    load(at, mp, pk, k0, p0, z, bar);
+                    load(at + kPlane, mp, pk, k1, p0, z1, bar);
+                    load(at + 2 * kPlane, mq, qk, k0, q0, z, bar);
+                    load(at + 3 * kPlane, mq, qk, k1, q0, z1, bar);
                     if (++s == kRing) {
                         s = 0;
                         phase ^= 1;
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
             const uint32_t desc_p = operand_desc_lo(base, a.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, a.q_kmajor);
             const uint32_t kblocks = a.kblocks, tiles = a.tiles, chunk = a.chunk;
+            const bool single = a.single;
             uint32_t it = 0, ch = 0, s = 0, phase = 0;
             for (uint32_t t = first; ok && t < tiles; t += step) {
                 for (uint32_t kb = 0; ok && kb < kblocks; ++ch) {
@@ -250,10 +253,12 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        // lo hi, hi lo, hi hi: the small products meet a small accumulator
+                        // lo hi, hi lo, hi hi: the small products meet a small accumulator; or hi hi twice
 #pragma unroll
                         for (uint32_t pair = 0; pair < 3; ++pair) {
-                            const uint32_t op = pair == 0 ? kPlane >> 4 : 0, oq = pair == 1 ? kPlane >> 4 : 0;
+                            if (pair == 1 && single) continue;
+                            const uint32_t op = pair == 0 ? kPlane >> 4 : 0;
+                            const uint32_t oq = pair == 1 || (pair == 0 && single) ? kPlane >> 4 : 0;
 #pragma unroll
                             for (uint32_t x = 0; x < kBK / 16; ++x) {
                                 mma<kCtas>(d, dp + op + x * step_p, dq + oq + x * step_q, kDescHi, idesc, add);
@@ -405,7 +410,8 @@ cudaError_t launch_ortho_product(const OrthoProduct& p, const OrthoShape& shape,
     a.c3 = p.c3;
     a.rows = p.out->rows;
     a.cols = p.out->cols;
-    a.kblocks = (p.k + kBK - 1) / kBK;
+    a.single = p.single;
+    a.kblocks = (p.k + (p.single ? 2 : 1) * kBK - 1) / ((p.single ? 2 : 1) * kBK);
     a.chunk = p.chunk;
     a.p_kmajor = p.p_kmajor;
     a.q_kmajor = p.q_kmajor;
@@ -417,11 +423,11 @@ cudaError_t launch_ortho_product(const OrthoProduct& p, const OrthoShape& shape,
         a.per = a.symmetric ? a.tiles_q * (a.tiles_q + 1) / 2 : a.tiles_p * a.tiles_q;
         a.tiles = a.per * p.items;
     };
-    // Turns of tiles over the SMs, in microseconds: a block of a pair takes 0.8, of a single SM 0.42
-    // or, with all SMs loading 64 KB for each, 0.58; a tile's end 1.5.
+    // Turns of tiles over the SMs, in microseconds: a block of a pair takes 0.8 (two of one product 0.6),
+    // of a single SM 0.42 or, with all SMs loading 64 KB for each, 0.58; a tile's end 1.5.
     const uint32_t sms = static_cast<uint32_t>(shape.sms), pairs = sms / 2;
     tiles(256);
-    const double pair = (a.tiles + pairs - 1) / pairs * (0.8 * a.kblocks + 1.5);
+    const double pair = (a.tiles + pairs - 1) / pairs * ((p.single ? 0.6 : 0.8) * a.kblocks + 1.5);
     tiles(128);
     const double busy = a.tiles < sms ? static_cast<double>(a.tiles) / sms : 1.0;
     const double single = (a.tiles + sms - 1) / sms * ((0.58 * busy > 0.42 ? 0.58 * busy : 0.42) * a.kblocks + 1.5);

@@ -7,11 +7,9 @@
 // exactly: no table of cosines is read, and a far position is as exact as a near one.  The
 // quadrant is taken off in integers too; the rest, |t| <= pi / 4, goes through sincospif.
 //
-// A CTA has a few tokens, or for a few tokens some of their heads.  Its threads compute the sines of
-// the tokens' pairs into shared memory, each once, while their first vectors are on their way;
-// then each takes the vectors of one place in the heads, all heads and tokens in turn.
-//
-// What bounds it: HBM, each element read and written once.
+// A thread has V pairs (its vectors are V elements) and turns them in several heads of one token,
+// so that the sines are computed once for all of these.  What bounds it: HBM, each element read
+// and written once.
 #include "product_device.cuh"
 #include "rotary.cuh"
 
@@ -20,12 +18,11 @@ namespace fa {
 namespace {
 
 constexpr uint32_t kRotThreads = 256;
-constexpr uint32_t kRotTokens = 4;        // of a CTA
-constexpr uint32_t kAhead = 2;            // heads whose loads a thread has in flight
+constexpr uint32_t kAhead = 2;            // heads whose loads are in flight together
 
 // V elements of T, as they lie in memory.
 template <typename T, int V>
-struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+struct alignas(sizeof(T) * V) Pack {
     T e[V];
 };
 
@@ -47,118 +44,97 @@ __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(stat
 __device__ __forceinline__ void narrow(float x, float& y) { y = x; }
 __device__ __forceinline__ void narrow(float x, uint16_t& y) { y = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// V floats of shared memory, at a multiple of V.
-template <int V>
-__device__ __forceinline__ void load_table(const float* p, float (&x)[V]) {
-    const Pack<float, V> q = *reinterpret_cast<const Pack<float, V>*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = q.e[i];
-}
-
-__device__ __forceinline__ float2 cos_sin_turn(uint64_t turn) {
+__device__ __forceinline__ void sin_cos_turn(uint64_t turn, float& s, float& c) {
     // to the nearest quarter, and what is left in 2^-33 of half a turn
     const uint64_t q = turn + (1ull << 61);
     const int32_t rest = static_cast<int32_t>(static_cast<int64_t>(turn - (q >> 62 << 62)) >> 30);
     float sn, cs;
     sincospif(static_cast<float>(rest) * 0x1p-33f, &sn, &cs);
     const uint32_t quad = static_cast<uint32_t>(q >> 62);
-    const float c = quad & 1 ? sn : cs, s = quad & 1 ? cs : sn;
-    return make_float2(quad == 1 || quad == 2 ? -c : c, quad & 2 ? -s : s);
+    s = quad & 1 ? cs : sn;
+    c = quad & 1 ? sn : cs;
+    if (quad & 2) s = -s;
+    if (quad == 1 || quad == 2) c = -c;
 }
 
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kRotThreads, sizeof(T) * V == 16 ? 4 : 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     typedef Pack<T, V> P;
-    extern __shared__ __align__(16) float table[];      // [tokens][cos, sin][rotary_dim / 2]
-    __shared__ uint64_t at_in[kRotTokens][2], at_out[kRotTokens][2];
-    __shared__ int64_t position[kRotTokens];             // -1: padding, left as it is
-    wait_predecessor();
+    __shared__ uint64_t turns[kRotaryMaxPairs];
     const uint32_t half = a.rotary_dim / 2;
-    const uint32_t token0 = blockIdx.x * a.cta_tokens, tokens = min(a.cta_tokens, a.tokens - token0);
-    const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
-    const uint32_t head0 = blockIdx.y * a.cta_heads, mine = min(a.cta_heads, heads - head0);
-    if (threadIdx.x < tokens) {
-        const uint32_t t = threadIdx.x, b = (token0 + t) / a.seq, s = token0 + t - b * a.seq;
-        const int32_t p = a.position ? a.position[token0 + t] : 0;
-        position[t] = a.position ? (p < 0 ? -1 : p) : a.first + s;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            at_in[t][k] = b * a.part[k].xb + s * a.part[k].xt;
-            at_out[t][k] = b * a.part[k].ob + s * a.part[k].ot;
-        }
-    }
+    for (uint32_t i = threadIdx.x; i < half; i += kRotThreads) turns[i] = a.turns[i];
     __syncthreads();
-
-    // This thread's place in a head, its two vectors there, and the row (token, head) it begins with;
-    // the CTA has `tall` rows at a time.
-    const uint32_t chunk0 = blockIdx.z * kRotThreads, width = min(a.chunks - chunk0, kRotThreads), tall = kRotThreads / width;
-    const uint32_t chunk = chunk0 + threadIdx.x % width, row0 = threadIdx.x / width;
+    wait_predecessor();
+    const uint64_t at = blockIdx.x * static_cast<uint64_t>(kRotThreads) + threadIdx.x;
+    const uint32_t per = a.chunks * a.slots;
+    const uint64_t which = at >> 32 ? at / per : static_cast<uint32_t>(at) / per;
+    if (which >= a.tokens) return;
+    const uint32_t token = static_cast<uint32_t>(which), in = static_cast<uint32_t>(at - which * per);
+    const uint32_t slot = in / a.chunks, chunk = in - slot * a.chunks;
+    const uint32_t b = token / a.seq, s = token - b * a.seq;
+    // the two vectors of this thread in a head
     const bool turn = chunk < a.turning;
     const uint32_t e0 = !turn ? a.rotary_dim + (chunk - a.turning) * 2 * V : kInterleaved ? chunk * 2 * V : chunk * V;
     const uint32_t e1 = turn && !kInterleaved ? e0 + half : e0 + V;
     const bool second = e1 < a.head_dim;
-    struct Row {
-        uint32_t t, h;                       // of the CTA's tokens and heads
-    };
-    const auto on = [&](Row r) {             // tall rows on
-        r.h += tall;
-        while (r.h >= mine) {
-            r.h -= mine;
-            ++r.t;
-        }
-        return r;
-    };
-    Row row = {0, row0};
-    while (row.h >= mine) {
-        row.h -= mine;
-        ++row.t;
-    }
-    if (row0 >= tall) row.t = tokens;
+    const uint32_t heads0 = a.part[0].heads, heads = heads0 + a.part[1].heads;
+    const T* x0 = static_cast<const T*>(a.part[0].x) + b * a.part[0].xb + s * a.part[0].xt;
+    const T* x1 = static_cast<const T*>(a.part[1].x) + b * a.part[1].xb + s * a.part[1].xt;
+    T* o0 = static_cast<T*>(a.part[0].out) + b * a.part[0].ob + s * a.part[0].ot;
+    T* o1 = static_cast<T*>(a.part[1].out) + b * a.part[1].ob + s * a.part[1].ot;
     P u[kAhead], v[kAhead];
-    const auto fetch = [&](Row r) {
+    const auto fetch = [&](uint32_t h0) {
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i, r = on(r)) {
-            if (r.t >= tokens) break;
-            const bool k = head0 + r.h >= heads0;
-            const T* x = static_cast<const T*>(a.part[k].x) + at_in[r.t][k] + (head0 + r.h - (k ? heads0 : 0)) * a.part[k].xh;
-            u[i] = load_pack<T, V>(x + e0);
-            if (second) v[i] = load_pack<T, V>(x + e1);
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t h = h0 + k * a.slots;
+            if (h >= heads) break;
+            const T* x = h < heads0 ? x0 + h * a.part[0].xh : x1 + (h - heads0) * a.part[1].xh;
+            u[k] = load_pack<T, V>(x + e0);
+            if (second) v[k] = load_pack<T, V>(x + e1);
         }
     };
-    fetch(row);
-    for (uint32_t t = 0; t < tokens; ++t)
-        for (uint32_t pair = threadIdx.x; pair < half; pair += kRotThreads) {
-            const uint64_t angle = static_cast<uint64_t>(position[t]) * a.turns[pair];
-            const float2 cs = cos_sin_turn(a.inverse ? 0 - angle : angle);
-            table[2 * t * half + pair] = cs.x * a.scale;
-            table[(2 * t + 1) * half + pair] = cs.y * a.scale;
+    fetch(slot);                         // on their way while the sines are computed
+    uint64_t pos;
+    if (a.position) {
+        const int32_t p = a.position[token];
+        if (p < 0) return;               // padding: left as it is
+        pos = static_cast<uint64_t>(p);
+    } else {
+        pos = static_cast<uint64_t>(a.first) + s;
+    }
+    float cs[V], sn[V];
+    if (turn) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint64_t t = pos * turns[chunk * V + i];
+            sin_cos_turn(a.inverse ? 0 - t : t, sn[i], cs[i]);
+            sn[i] *= a.scale;
+            cs[i] *= a.scale;
         }
-    __syncthreads();
-    while (row.t < tokens) {
+    }
+    for (uint32_t h0 = slot;;) {
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i, row = on(row)) {
-            if (row.t >= tokens) return;
-            if (position[row.t] < 0) continue;
-            const bool k = head0 + row.h >= heads0;
-            T* o = static_cast<T*>(a.part[k].out) + at_out[row.t][k] + (head0 + row.h - (k ? heads0 : 0)) * a.part[k].oh;
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t h = h0 + k * a.slots;
+            if (h >= heads) break;
+            T* o = h < heads0 ? o0 + h * a.part[0].oh : o1 + (h - heads0) * a.part[1].oh;
             if (turn) {
-                float cs[V], sn[V];
-                load_table(table + 2 * row.t * half + chunk * V, cs);
-                load_table(table + (2 * row.t + 1) * half + chunk * V, sn);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    // interleaved: pair j is elements 2 j and 2 j + 1 of the two vectors in a row
-                    T& p = !kInterleaved ? u[i].e[j] : 2 * j < V ? u[i].e[2 * j % V] : v[i].e[2 * j % V];
-                    T& q = !kInterleaved ? v[i].e[j] : 2 * j + 1 < V ? u[i].e[(2 * j + 1) % V] : v[i].e[(2 * j + 1) % V];
+                for (int i = 0; i < V; ++i) {
+                    // interleaved: pair i is elements 2 i and 2 i + 1 of the two vectors in a row
+                    T& p = !kInterleaved ? u[k].e[i] : 2 * i < V ? u[k].e[2 * i % V] : v[k].e[2 * i % V];
+                    T& q = !kInterleaved ? v[k].e[i] : 2 * i + 1 < V ? u[k].e[(2 * i + 1) % V] : v[k].e[(2 * i + 1) % V];
                     const float f = widen(p), g = widen(q);
-                    narrow(fmaf(f, cs[j], -(g * sn[j])), p);
-                    narrow(fmaf(g, cs[j], f * sn[j]), q);
+                    narrow(fmaf(f, cs[i], -(g * sn[i])), p);
+                    narrow(fmaf(g, cs[i], f * sn[i]), q);
                 }
             }
-            *reinterpret_cast<P*>(o + e0) = u[i];
-            if (second) *reinterpret_cast<P*>(o + e1) = v[i];
+            *reinterpret_cast<P*>(o + e0) = u[k];
+            if (second) *reinterpret_cast<P*>(o + e1) = v[k];
         }
-        fetch(row);
+        h0 += kAhead * a.slots;
+        if (h0 >= heads) return;
+        fetch(h0);
     }
 }
 
@@ -166,23 +142,16 @@ template <typename T, int V>
 cudaError_t launch_v(RotaryArgs& a, uint32_t sms, cudaStream_t stream) {
     a.turning = a.rotary_dim / 2 / V;
     a.chunks = a.turning + (a.copy ? (a.head_dim - a.rotary_dim + 2 * V - 1) / (2 * V) : 0);
-    // kRotTokens tokens a CTA where that leaves eight CTAs per SM, else fewer; for fewer tokens than
-    // twice the SMs the heads are shared out too.
+    // Eight heads a thread where that leaves the SMs full (1536 threads each, twice over), else
+    // fewer, down to one.
     const uint32_t heads = a.part[0].heads + a.part[1].heads;
-    a.cta_tokens = std::max(1u, std::min(kRotTokens, a.tokens / (8 * sms)));
-    const uint32_t blocks = (a.tokens + a.cta_tokens - 1) / a.cta_tokens, share = std::min(heads, std::max(1u, 2 * sms / blocks));
-    a.cta_heads = (heads + share - 1) / share;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, (heads + a.cta_heads - 1) / a.cta_heads, (a.chunks + kRotThreads - 1) / kRotThreads);
-    cfg.blockDim = dim3(kRotThreads);
-    cfg.dynamicSmemBytes = a.cta_tokens * a.rotary_dim * 4;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, a.interleaved ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>, a);
+    const uint64_t each = static_cast<uint64_t>(a.tokens) * a.chunks, want = 2ull * 1536 * sms;
+    uint64_t slots = std::max<uint64_t>((heads + 7) / 8, (want + each - 1) / each);
+    a.slots = static_cast<uint32_t>(std::min<uint64_t>(slots, heads));
+    const uint64_t blocks = (each * a.slots + kRotThreads - 1) / kRotThreads;
+    if (blocks >= 1ull << 31) return cudaErrorInvalidValue;
+    return launch_next(a.interleaved ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>,
+                       dim3(static_cast<uint32_t>(blocks)), kRotThreads, stream, a);
 }
 
 }  // namespace

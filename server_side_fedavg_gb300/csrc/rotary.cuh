@@ -24,14 +24,14 @@ struct RotaryArgs {
     uint32_t tokens, seq;       // batch * seq of them
     uint32_t head_dim, rotary_dim;
     uint32_t chunks, turning;   // per head: pieces of 2 V elements, and those of them that turn
-    uint32_t cta_tokens, cta_heads;
+    uint32_t slots;             // heads of a token are shared out over so many threads per piece
     int dtype;
     float scale;
     bool interleaved, inverse, copy;   // copy: what does not turn goes to out too
     uint64_t turns[kRotaryMaxPairs];   // of a pair per position, in 2^-64 of a whole turn
 };
 
-// Fills in chunks, turning, cta_tokens and cta_heads.
+// Fills in chunks, turning and slots.
 cudaError_t launch_rotary(RotaryArgs& a, uint32_t sms, cudaStream_t stream);
 
 }  // namespace fa
