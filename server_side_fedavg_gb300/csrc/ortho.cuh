@@ -18,6 +18,8 @@ struct OrthoBuf {
     CUtensorMap k, mn, out;            // summed index along rows, across them; as a result
 };
 
+constexpr uint32_t kOrthoOps = 24, kOrthoBufs = 12;    // products of a launch; buffers of these, and three
+
 // out = c1 * sum_k P(x,k) Q(y,k) + c2 * e1 + c3 * e2 of every item, on the tensor cores.  An
 // operand's element (x, k) is at its row x if it is K-major, else at its row k.
 struct OrthoProduct {
@@ -25,7 +27,7 @@ struct OrthoProduct {
     bool p_kmajor, q_kmajor;
     bool single;                              // the hi terms alone
     bool symmetric;                           // the tiles on and above the diagonal, and their mirror images
-    uint32_t items, k;
+    uint32_t k;
     uint32_t chunk;                           // blocks of 64 terms that the tensor cores sum by themselves
     float c1, c2, c3;
 };
@@ -37,8 +39,11 @@ struct OrthoShape {
 
 cudaError_t prepare_ortho(OrthoShape* shape);
 cudaError_t map_ortho(OrthoBuf* b, uint32_t items);
-cudaError_t launch_ortho_product(const OrthoProduct& p, const OrthoShape& shape, unsigned int* err, bool test_expire,
-                                 cudaStream_t stream);
+// n <= kOrthoOps products one after the other, of `items` items each.  done: [items], counts of what
+// is done of an item, zero before its first product; *count: what they are when these begin, and then
+// when they are done.
+cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
+                                  const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream);
 
 // The first pass and the last.  Items are `step` elements apart.
 struct OrthoMat {
@@ -50,6 +55,7 @@ struct OrthoEnds {
     OrthoMat update, momentum, momentum_out, residual, out;
     uint32_t items, rows, cols, blocks;       // blocks per item
     float3* part;                             // [items][blocks] sums of squares, by size
+    uint32_t* done;                           // [items], set to 0 by the first pass
     uint16_t* x;                              // planes of the scaled update, or of the result
     uint64_t ld;
     double eps;

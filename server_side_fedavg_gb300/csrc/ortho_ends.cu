@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kEndThreads) ortho_norm_kernel(const __grid_co
     if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x > 0) return;
+    if (blockIdx.x == 0) a.done[item] = 0;
     for (uint32_t w = 1; w < kEndThreads / 32; ++w) s.add(sums[w]);
     a.part[static_cast<uint64_t>(item) * a.blocks + blockIdx.x] = make_float3(s.mid, s.high, s.low);
 }

@@ -15,6 +15,16 @@
 //
 // Polynomials of a symmetric matrix commute and are symmetric: of these the tiles on and above
 // the diagonal are computed, and written twice.
+//
+// A launch runs a list of products one after the other, for all items: the tiles of a product of
+// all items, then those of the next, dealt out to the clusters in turn.  A product of an item needs
+// the one before it whole.  A tile's drain warps count it when its stores are done; who works on a
+// later product of the item waits for the count (acquire, then a proxy fence before TMA).  All
+// clusters are resident (a cooperative launch), and a tile waits for earlier ones alone, so that the
+// first that is not done can always go on.  Against a launch for each product, 24 items of 1024 x
+// 1024 fill the last turns of 240 and 384 tiles over 76 pairs, and small matrices save the launches.
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "ortho.cuh"
@@ -41,36 +51,68 @@ constexpr int kOrthoThreads = (kDrain<kBN> + (kBN == 256 ? 4 : 2)) * 32;
 template <int kBN>
 constexpr uint32_t kSmem = kRing * kStageBytes + kDrain<kBN> * kUnit;
 
-struct Args {
-    CUtensorMap p, q, out;
+struct Op {
     const uint16_t *e1, *e2;
     uint64_t ld, plane;                          // of e1 and e2
-    unsigned int* err;
     float c1, c2, c3;
     uint32_t rows, cols, kblocks, chunk;         // chunk: blocks between two emptyings
-    uint32_t tiles_p, tiles_q, per, tiles;       // per: of an item
-    bool p_kmajor, q_kmajor, symmetric, single, test_expire;
+    uint32_t tiles_p, tiles_q, per;              // per: tiles of an item
+    uint32_t first, need;                        // the first tile; an item's count when its earlier products are done
+    uint8_t p, q, out;                           // maps
+    bool p_kmajor, q_kmajor, symmetric, single;
 };
 
-struct Tile {
+struct Args {
+    CUtensorMap map[3 * kOrthoBufs];             // of each buffer: k, mn, out
+    Op op[kOrthoOps];
+    uint32_t* done;                              // [items]
+    unsigned int* err;
+    uint32_t ops, items, tiles;
+    bool test_expire;
+};
+
+// A cluster's tiles in turn.
+struct Walk {
+    uint32_t n = 0;                              // the product
     uint32_t item, p, q;
-    __device__ __forceinline__ Tile(const Args& a, uint32_t t) {
-        item = t / a.per;
-        uint32_t r = t - item * a.per;
-        if (a.symmetric) {                       // column by column, p <= q
+    __device__ __forceinline__ void at(const Args& a, uint32_t t) {
+        while (n + 1 < a.ops && t >= a.op[n + 1].first) ++n;
+        const Op& o = a.op[n];
+        const uint32_t u = t - o.first;
+        item = u / o.per;
+        uint32_t r = u - item * o.per;
+        if (o.symmetric) {                       // column by column, p <= q
             q = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
             while (q * (q + 1) / 2 > r) --q;
             while ((q + 1) * (q + 2) / 2 <= r) ++q;
             p = r - q * (q + 1) / 2;
         } else {
-            const uint32_t full = kBand * a.tiles_q, band = r / full;
+            const uint32_t full = kBand * o.tiles_q, band = r / full;
             r -= band * full;
-            const uint32_t height = min(kBand, a.tiles_p - band * kBand);
+            const uint32_t height = min(kBand, o.tiles_p - band * kBand);
             q = r / height;
             p = band * kBand + r - q * height;
         }
     }
 };
+
+// Until an item's earlier products are done; false where the cluster has given up, or after some 20 s.
+__device__ __forceinline__ bool wait_done(const Args& a, const Op& o, uint32_t item, uint32_t gone, uint32_t ctas) {
+    long long t0 = 0;
+    for (;;) {
+        uint32_t v, g;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.done + item) : "memory");
+        if (v >= o.need) return true;
+        asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(g) : "r"(gone) : "memory");
+        if (g) return false;
+        if (t0 == 0) {
+            t0 = clock64();
+        } else if (clock64() - t0 > kMaxWaitClocks) {
+            give_up(gone, ctas);
+            return false;
+        }
+    }
+}
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
@@ -87,7 +129,8 @@ __device__ __forceinline__ float half_of(float x) { return __half2float(__float2
 
 // v += c * (hi + lo) of eight elements
 __device__ __forceinline__ void add_planes(float* v, const uint16_t* hi, uint64_t plane, float c) {
-    const uint4 h = *reinterpret_cast<const uint4*>(hi), l = *reinterpret_cast<const uint4*>(hi + plane);
+    // from L2: other SMs have written them during this launch
+    const uint4 h = __ldcg(reinterpret_cast<const uint4*>(hi)), l = __ldcg(reinterpret_cast<const uint4*>(hi + plane));
     const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -101,8 +144,8 @@ __device__ __forceinline__ void add_planes(float* v, const uint16_t* hi, uint64_
 // The block of 32 x 32 results at (row, col) from v, this lane's row of it: e1 and e2 added, then
 // either plane by way of the warp's buffer, and its mirror image.  64-byte rows in the 64-byte
 // swizzle: 16-byte piece j of row r is at j ^ (r / 2 % 4).
-__device__ __forceinline__ void finish(const Args& a, float* v, uint32_t buf, uint32_t item, uint32_t row0, uint32_t col,
-                                       bool mirror) {
+__device__ __forceinline__ void finish(const Op& a, const CUtensorMap* out, float* v, uint32_t buf, uint32_t item, uint32_t row0,
+                                       uint32_t col, bool mirror) {
     const uint32_t lane = threadIdx.x % 32, row = row0 + lane;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= a.c1;
@@ -129,7 +172,7 @@ __device__ __forceinline__ void finish(const Args& a, float* v, uint32_t buf, ui
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-            tma_store_3d(&a.out, buf, col, row0, 2 * item + z);
+            tma_store_3d(out, buf, col, row0, 2 * item + z);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         if (!mirror) continue;
@@ -143,7 +186,7 @@ __device__ __forceinline__ void finish(const Args& a, float* v, uint32_t buf, ui
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-            tma_store_3d(&a.out, buf, row0, col, 2 * item + z);
+            tma_store_3d(out, buf, row0, col, 2 * item + z);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
     }
@@ -164,8 +207,8 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0 && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.p) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.map[a.op[0].p]) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.map[a.op[0].q]) : "memory");
     }
     if (warp == kLoadWarp && lane == 0) {
         for (uint32_t s = 0; s < kRing; ++s) {
@@ -193,9 +236,6 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         if constexpr (kBN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kLoadWarp && elect_one()) {
             const uint32_t lead_full = kCtas == 2 ? in_cta(full, 0) : full;
-            const bool pk = a.p_kmajor, qk = a.q_kmajor, single = a.single;
-            const uint32_t kblocks = a.kblocks, tiles = a.tiles;
-            const CUtensorMap *mp = &a.p, *mq = &a.q;
             const auto load = [&](uint32_t dst, const CUtensorMap* m, bool kmajor, uint32_t k, uint32_t x, uint32_t z, uint32_t bar) {
                 if (kmajor) {
                     tma_load<kCtas>(dst, m, k, x, z, bar);
@@ -205,9 +245,19 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 }
             };
             uint32_t s = 0, phase = 1;
-            for (uint32_t t = first; ok && t < tiles; t += step) {
-                const Tile tile(a, t);
+            Walk tile;
+            for (uint32_t t = first; ok && t < a.tiles; t += step) {
+                tile.at(a, t);
+                const Op& o = a.op[tile.n];
+                const CUtensorMap *mp = &a.map[o.p], *mq = &a.map[o.q];
+                const bool pk = o.p_kmajor, qk = o.q_kmajor, single = o.single;
+                const uint32_t kblocks = o.kblocks;
                 const uint32_t p0 = tile.p * 128 * kCtas + rank * 128, q0 = tile.q * kBN + rank * 128, z = 2 * tile.item;
+                if (!wait_done(a, o, tile.item, gone, kCtas)) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("fence.proxy.async;" ::: "memory");
                 for (uint32_t kb = 0; kb < kblocks; ++kb) {
                     const uint32_t bar = lead_full + 8 * s, at = base + s * kStageBytes;
                     if (!bar_wait(empty + 8 * s, phase, gone, kCtas)) {
@@ -228,15 +278,18 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 }
             }
         } else if (warp == kMmaWarp && leader && elect_one()) {
-            // fp32 sums of fp16 by fp16
-            const uint32_t idesc = 1u << 4 | (a.p_kmajor ? 0u : 1u << 15) | (a.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 |
-                                   (128 * kCtas / 16) << 24;
-            const uint32_t step_p = a.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = a.q_kmajor ? 32 >> 4 : 2048 >> 4;
-            const uint32_t desc_p = operand_desc_lo(base, a.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, a.q_kmajor);
-            const uint32_t kblocks = a.kblocks, tiles = a.tiles, chunk = a.chunk;
-            const bool single = a.single;
-            uint32_t it = 0, ch = 0, s = 0, phase = 0;
-            for (uint32_t t = first; ok && t < tiles; t += step) {
+            uint32_t ch = 0, it = 0, s = 0, phase = 0;
+            Walk tile;
+            for (uint32_t t = first; ok && t < a.tiles; t += step) {
+                tile.at(a, t);
+                const Op& o = a.op[tile.n];
+                // fp32 sums of fp16 by fp16
+                const uint32_t idesc = 1u << 4 | (o.p_kmajor ? 0u : 1u << 15) | (o.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 |
+                                       (128 * kCtas / 16) << 24;
+                const uint32_t step_p = o.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = o.q_kmajor ? 32 >> 4 : 2048 >> 4;
+                const uint32_t desc_p = operand_desc_lo(base, o.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, o.q_kmajor);
+                const uint32_t kblocks = o.kblocks, chunk = o.chunk;
+                const bool single = o.single;
                 for (uint32_t kb = 0; ok && kb < kblocks; ++ch) {
                     const uint32_t b = ch & 1;
                     if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, kCtas)) {
@@ -278,10 +331,8 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 // the loads in flight land before the CTA leaves
                 atomicOr(a.err, kErrWaitTimeout);
                 give_up(gone, kCtas);
-                const uint32_t blocks = kblocks * ((tiles - first + step - 1) / step);
-                for (uint32_t n = 0; n < kRing && it < blocks; ++n, ++it) {
+                for (uint32_t n = 0; n < kRing; ++n, ++it)
                     for (uint32_t i = 0; i < 1000 && !bar_try(full + 8 * (it % kRing), (it / kRing) & 1); ++i) {}
-                }
             }
         }
         __syncwarp();
@@ -291,9 +342,12 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         const uint32_t mine = tmem + (quad << 21) + part * kCols;       // lane 32 quad, column part * kCols
         const uint32_t buf = base + kRing * kStageBytes + warp * kUnit;
         const uint32_t lead_empty = kCtas == 2 ? in_cta(acc_empty, 0) : acc_empty;
-        const uint32_t chunks = (a.kblocks + a.chunk - 1) / a.chunk;
         uint32_t ch = 0;
+        Walk tile;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
+            tile.at(a, t);
+            const Op& o = a.op[tile.n];
+            const uint32_t chunks = (o.kblocks + o.chunk - 1) / o.chunk;
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
@@ -318,12 +372,20 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             }
             ok = __all_sync(~0u, ok);
             if (!ok) break;
-            const Tile tile(a, t);
             const uint32_t row0 = tile.p * 128 * kCtas + rank * 128 + quad * 32, col0 = tile.q * kBN + part * kCols;
-            const bool mirror = a.symmetric && tile.p != tile.q;
-            if (row0 < a.rows) {
-                if (col0 < a.cols) finish(a, acc, buf, tile.item, row0, col0, mirror);
-                if (col0 + 32 < a.cols) finish(a, acc + 32, buf, tile.item, row0, col0 + 32, mirror);
+            const bool mirror = o.symmetric && tile.p != tile.q;
+            if (row0 < o.rows && col0 < o.cols) {
+                // e1 and e2 are there, as the operands were: seen by every lane
+                ok = wait_done(a, o, tile.item, gone, kCtas);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                finish(o, &a.map[o.out], acc, buf, tile.item, row0, col0, mirror);
+                if (col0 + 32 < o.cols) finish(o, &a.map[o.out], acc + 32, buf, tile.item, row0, col0 + 32, mirror);
+            }
+            if (lane == 0) {
+                // this warp's part of the tile is in memory: for other SMs' TMA and loads
+                asm volatile("cp.async.bulk.wait_group 0;\nfence.proxy.async;" ::: "memory");
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.done + tile.item) : "memory");
             }
         }
         if (lane == 0) {
@@ -358,8 +420,8 @@ cudaError_t launch(const Args& a, uint32_t room, cudaStream_t stream) {
     cfg.dynamicSmemBytes = kSmem<kBN>;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = kCtas;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
@@ -394,48 +456,88 @@ cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
                : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_ortho_product(const OrthoProduct& p, const OrthoShape& shape, unsigned int* err, bool test_expire,
-                                 cudaStream_t stream) {
+cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
+                                  const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream) {
+    if (n > kOrthoOps) return cudaErrorInvalidValue;
     Args a{};
-    a.p = p.p_kmajor ? p.P->k : p.P->mn;
-    a.q = p.q_kmajor ? p.Q->k : p.Q->mn;
-    a.out = p.out->out;
-    a.e1 = p.e1 ? p.e1->p : nullptr;
-    a.e2 = p.e2 ? p.e2->p : nullptr;
-    a.ld = p.out->ld;
-    a.plane = p.out->plane();
-    a.err = err;
-    a.c1 = p.c1;
-    a.c2 = p.c2;
-    a.c3 = p.c3;
-    a.rows = p.out->rows;
-    a.cols = p.out->cols;
-    a.single = p.single;
-    a.kblocks = (p.k + (p.single ? 2 : 1) * kBK - 1) / ((p.single ? 2 : 1) * kBK);
-    a.chunk = p.chunk;
-    a.p_kmajor = p.p_kmajor;
-    a.q_kmajor = p.q_kmajor;
-    a.symmetric = p.symmetric;
-    a.test_expire = test_expire;
-    const auto tiles = [&](uint32_t size) {
-        a.tiles_p = (a.rows + size - 1) / size;
-        a.tiles_q = (a.cols + size - 1) / size;
-        a.per = a.symmetric ? a.tiles_q * (a.tiles_q + 1) / 2 : a.tiles_p * a.tiles_q;
-        a.tiles = a.per * p.items;
+    const OrthoBuf* bufs[kOrthoBufs] = {};
+    uint32_t held = 0;
+    const auto index = [&](const OrthoBuf* b) {
+        for (uint32_t i = 0; i < held; ++i)
+            if (bufs[i] == b) return 3 * i;
+        bufs[held] = b;
+        a.map[3 * held] = b->k;
+        a.map[3 * held + 1] = b->mn;
+        a.map[3 * held + 2] = b->out;
+        return 3 * held++;
     };
-    // Turns of tiles over the SMs, in microseconds: a block of a pair takes 0.8 (two of one product 0.6),
-    // of a single SM 0.42 or, with all SMs loading 64 KB for each, 0.58; a tile's end 1.5.
-    const uint32_t sms = static_cast<uint32_t>(shape.sms), pairs = sms / 2;
-    tiles(256);
-    const double pair = (a.tiles + pairs - 1) / pairs * ((p.single ? 0.6 : 0.8) * a.kblocks + 1.5);
-    tiles(128);
-    const double busy = a.tiles < sms ? static_cast<double>(a.tiles) / sms : 1.0;
-    const double single = (a.tiles + sms - 1) / sms * ((0.58 * busy > 0.42 ? 0.58 * busy : 0.42) * a.kblocks + 1.5);
-    if (pair <= single) {
-        tiles(256);
-        return launch<2, 256>(a, pairs, stream);
+    a.ops = n;
+    a.items = items;
+    a.done = done;
+    a.err = err;
+    a.test_expire = test_expire;
+    for (uint32_t i = 0; i < n; ++i) {
+        if (held + 3 > kOrthoBufs) return cudaErrorInvalidValue;
+        Op& o = a.op[i];
+        o.p = static_cast<uint8_t>(index(p[i].P) + (p[i].p_kmajor ? 0 : 1));
+        o.q = static_cast<uint8_t>(index(p[i].Q) + (p[i].q_kmajor ? 0 : 1));
+        o.out = static_cast<uint8_t>(index(p[i].out) + 2);
+        o.e1 = p[i].e1 ? p[i].e1->p : nullptr;
+        o.e2 = p[i].e2 ? p[i].e2->p : nullptr;
+        o.ld = p[i].out->ld;
+        o.plane = p[i].out->plane();
+        o.c1 = p[i].c1;
+        o.c2 = p[i].c2;
+        o.c3 = p[i].c3;
+        o.rows = p[i].out->rows;
+        o.cols = p[i].out->cols;
+        o.single = p[i].single;
+        const uint32_t block = (p[i].single ? 2 : 1) * kBK;
+        o.kblocks = (p[i].k + block - 1) / block;
+        o.chunk = p[i].chunk;
+        o.p_kmajor = p[i].p_kmajor;
+        o.q_kmajor = p[i].q_kmajor;
+        o.symmetric = p[i].symmetric;
     }
-    return launch<1, 128>(a, sms, stream);
+    // The tile for all of them: turns over the SMs, in microseconds.  A block of a pair takes 0.8 (two of
+    // one product 0.6), of a single SM 0.42 or, with all SMs loading 64 KB for each, 0.58; a tile's end
+    // 1.5, and a product 3 more before its first tile's data is there.
+    const uint32_t sms = static_cast<uint32_t>(shape.sms), pairs = sms / 2;
+    const auto tiles = [&](uint32_t size) {
+        a.tiles = 0;
+        for (uint32_t i = 0; i < n; ++i) {
+            Op& o = a.op[i];
+            o.tiles_p = (o.rows + size - 1) / size;
+            o.tiles_q = (o.cols + size - 1) / size;
+            o.per = o.symmetric ? o.tiles_q * (o.tiles_q + 1) / 2 : o.tiles_p * o.tiles_q;
+            o.first = a.tiles;
+            a.tiles += o.per * items;
+        }
+    };
+    const auto cost = [&](bool pair) {
+        double c = 0.0;
+        for (uint32_t i = 0; i < n; ++i) {
+            const Op& o = a.op[i];
+            const uint32_t t = o.per * items, room = pair ? pairs : sms;
+            const double busy = t < sms ? static_cast<double>(t) / sms : 1.0;
+            const double block = pair ? (o.single ? 0.6 : 0.8) : std::max(0.42, 0.58 * busy);
+            // items go on without one another: whole turns for one, parts of turns for many
+            const double turns = items > 1 ? std::max(1.0, static_cast<double>(t) / room) : (t + room - 1) / room;
+            c += turns * (block * o.kblocks + 1.5) + 3.0;
+        }
+        return c;
+    };
+    tiles(256);
+    const double by_pair = cost(true);
+    tiles(128);
+    const bool pair = by_pair <= cost(false);
+    if (pair) tiles(256);
+    const uint32_t warps = pair ? 2 * kDrain<256> : kDrain<128>;
+    for (uint32_t i = 0; i < n; ++i) {
+        a.op[i].need = *count;
+        *count += warps * a.op[i].per;
+    }
+    return pair ? launch<2, 256>(a, pairs, stream) : launch<1, 128>(a, sms, stream);
 }
 
 }  // namespace fa

@@ -66,15 +66,14 @@ std::vector<uint32_t> segments(uint32_t steps, const Sizes& z, bool bf16) {
 }
 
 struct Run {
-    fa_work* w;
-    cudaStream_t s;
     Sizes z;
-    uint32_t items, chunk;
+    uint32_t chunk;
     bool bf16, single;               // of the result; of the next products
     double a, b, c;
     fa::OrthoBuf x[2], sq[kSquares];
+    std::vector<fa::OrthoProduct> list;
 
-    fa_status product(const Held& P, bool pk, const Held& Q, bool qk, uint32_t k, const Held& out, bool symmetric, double c1,
+    void product(const Held& P, bool pk, const Held& Q, bool qk, uint32_t k, const Held& out, bool symmetric, double c1,
                       const Held* e1, double c2, const Held* e2, double c3) {
         fa::OrthoProduct p{};
         p.P = P.buf;
@@ -86,19 +85,17 @@ struct Run {
         p.q_kmajor = qk;
         p.symmetric = symmetric;
         p.single = single;
-        p.items = items;
         p.k = k;
         p.chunk = chunk;
         // from true values to held ones
         p.c1 = static_cast<float>(std::ldexp(c1, out.shift - P.shift - Q.shift));
         p.c2 = e1 ? static_cast<float>(std::ldexp(c2, out.shift - e1->shift)) : 0.0f;
         p.c3 = e2 ? static_cast<float>(std::ldexp(c3, out.shift - e2->shift)) : 0.0f;
-        return launched(w, fa::launch_ortho_product(p, w->ortho, w->err_dev, (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s),
-                        "orthogonalisation");
+        list.push_back(p);
     }
 
     // `steps` steps from X, which is replaced; `next` bounds its singular values then.
-    fa_status segment(uint32_t steps, Held& X, double next, bool last) {
+    void segment(uint32_t steps, Held& X, double next, bool last) {
         // The last step towards a bf16 result takes one product of three, the hi terms' (11 bits), where
         // it is a segment of its own.  What that costs is not multiplied by later steps: measured against
         // fp64, 2.0e-3 of a square result in place of 1.7e-3, its own rounding.  (In a longer segment q X
@@ -112,40 +109,39 @@ struct Run {
             return h;
         };
         Held A = square(X.bound * X.bound), Q, P;
-        fa_status r = z.wide ? product(X, true, X, true, z.n, A, true, 1.0, nullptr, 0, nullptr, 0)
-                             : product(X, false, X, false, z.n, A, true, 1.0, nullptr, 0, nullptr, 0);
+        product(X, z.wide, X, z.wide, z.n, A, true, 1.0, nullptr, 0, nullptr, 0);
         double q = 1.0, top = X.bound;
-        for (uint32_t j = 0; r == FA_OK && j < steps; ++j) {
+        for (uint32_t j = 0; j < steps; ++j) {
             const double vertex = c != 0.0 ? -b / (2.0 * c) : -1.0, most = top * top;
             double bound = std::fabs(most * (b + c * most));
             if (vertex > 0.0 && vertex < most) bound = std::max(bound, std::fabs(vertex * (b + c * vertex)));
             P = square(bound);
-            r = product(A, true, A, true, z.m, P, true, c, &A, b, nullptr, 0);
+            product(A, true, A, true, z.m, P, true, c, &A, b, nullptr, 0);
             if (j == 0) {
                 Q = P;
                 q = a;
-            } else if (r == FA_OK) {
+            } else {
                 Held N = square(P.bound * Q.bound + std::fabs(a) * Q.bound + std::fabs(q) * P.bound);
-                r = product(P, true, Q, true, z.m, N, true, 1.0, &Q, a, &P, q);
+                product(P, true, Q, true, z.m, N, true, 1.0, &Q, a, &P, q);
                 Q = N;
                 q *= a;
             }
-            if (j + 1 < steps && r == FA_OK) {
+            if (j + 1 < steps) {
                 Held R = square(A.bound * (std::fabs(a) + P.bound));
-                r = product(A, true, P, true, z.m, R, true, 1.0, &A, a, nullptr, 0);
+                product(A, true, P, true, z.m, R, true, 1.0, &A, a, nullptr, 0);
                 top = most_of(a, b, c, top);
                 Held N = square(top * top);
-                if (r == FA_OK) r = product(R, true, P, true, z.m, N, true, 1.0, &R, a, nullptr, 0);
+                product(R, true, P, true, z.m, N, true, 1.0, &R, a, nullptr, 0);
                 A = N;
             }
         }
-        if (r != FA_OK) return r;
         Held N;
         N.set(X.buf == &x[0] ? &x[1] : &x[0], next);
-        r = z.wide ? product(Q, true, X, false, z.m, N, false, 1.0, &X, q, nullptr, 0)
-                   : product(X, true, Q, true, z.m, N, false, 1.0, &X, q, nullptr, 0);
+        if (z.wide)
+            product(Q, true, X, false, z.m, N, false, 1.0, &X, q, nullptr, 0);
+        else
+            product(X, true, Q, true, z.m, N, false, 1.0, &X, q, nullptr, 0);
         X = N;
-        return r;
     }
 };
 
@@ -200,6 +196,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
     const bool cap = capturing(s);
     Run run{};
     float3* part = nullptr;
+    uint32_t* done = nullptr;
     const uint32_t blocks = fa::ortho_blocks(group, rows, cols, static_cast<uint32_t>(w->tc.sms));
     const auto carve = [&](Carve& c) {
         for (int i = 0; i < (longest ? 2 : 1); ++i) {
@@ -214,6 +211,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
             run.sq[i].ld = ldm;
         }
         part = static_cast<float3*>(c.take(sizeof(float3) * group * blocks));
+        done = static_cast<uint32_t*>(c.take(sizeof(uint32_t) * group));
     };
     Carve need{nullptr}, c{nullptr};
     if (!small) {
@@ -229,8 +227,6 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
         for (int i = 0; i < (longest ? 2 : 1); ++i) FW_CUDA(w, fa::map_ortho(&run.x[i], group));
         for (int i = 0; i < squares; ++i) FW_CUDA(w, fa::map_ortho(&run.sq[i], group));
     }
-    run.w = w;
-    run.s = s;
     run.z = z;
     run.bf16 = p.dtype_out == FA_BF16;
     run.chunk = p.dtype_out == FA_BF16 ? 16 : z.m <= 512 ? 1 : z.m <= 1024 ? 2 : 4;
@@ -250,6 +246,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
     e.cols = cols;
     e.blocks = blocks;
     e.part = part;
+    e.done = done;
     e.ld = ldx;
     e.eps = p.eps;
     e.mu = static_cast<float>(p.mu);
@@ -257,7 +254,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
     e.nesterov = p.flags & FA_ORTHO_NESTEROV;
     ChainOut chain(w, s, cap);
     for (uint64_t first = 0; first < p.count && r == FA_OK; first += group) {
-        run.items = e.items = static_cast<uint32_t>(std::min<uint64_t>(group, p.count - first));
+        e.items = static_cast<uint32_t>(std::min<uint64_t>(group, p.count - first));
         if (small) {
             const fa::OrthoSmall steps{p.steps, p.dtype_out == FA_BF16 ? (p.steps + 2) / 3 : p.steps, static_cast<float>(p.a), static_cast<float>(p.b), static_cast<float>(p.c)};
             e.alpha = static_cast<float>(p.alpha);
@@ -269,11 +266,18 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
             e.shift = X.shift;
             r = launched(w, fa::launch_ortho_norm(e, s), "update's norm");
             if (r == FA_OK) r = launched(w, fa::launch_ortho_scale(e, s), "update's scale");
-            uint32_t done = 0;
+            run.list.clear();
+            uint32_t steps = 0, counted = 0;
             for (uint32_t n : parts) {
-                done += n;
-                if (r == FA_OK) r = run.segment(n, X, top[done], done == p.steps);
+                steps += n;
+                run.segment(n, X, top[steps], steps == p.steps);
             }
+            const size_t all = run.list.size();
+            for (size_t at = 0; r == FA_OK && at < all; at += fa::kOrthoOps)
+                r = launched(w, fa::launch_ortho_products(run.list.data() + at, static_cast<uint32_t>(std::min<size_t>(fa::kOrthoOps, all - at)),
+                                                          e.items, done, &counted, w->ortho, w->err_dev,
+                                                          (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s),
+                             "orthogonalisation");
             e.x = X.buf->p;
             e.alpha = static_cast<float>(std::ldexp(p.alpha, -X.shift));
             if (r == FA_OK) r = launched(w, fa::launch_ortho_finish(e, s), "weight step");
