@@ -43,7 +43,7 @@ cudaError_t map_ortho(OrthoBuf* b, uint32_t items);
 // is done of an item, zero before its first product; *count: what they are when these begin, and then
 // when they are done.
 cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
-                                  const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream);
+                                  const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream, uint64_t* launches);
 
 // The first pass and the last.  Items are `step` elements apart.
 struct OrthoMat {

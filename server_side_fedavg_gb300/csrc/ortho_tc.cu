@@ -21,8 +21,10 @@
 // the one before it whole.  A tile's drain warps count it when its stores are done; who works on a
 // later product of the item waits for the count (acquire, then a proxy fence before TMA).  All
 // clusters are resident (a cooperative launch), and a tile waits for earlier ones alone, so that the
-// first that is not done can always go on.  Against a launch for each product, 24 items of 1024 x
-// 1024 fill the last turns of 240 and 384 tiles over 76 pairs, and small matrices save the launches.
+// first that is not done can always go on.  Where the items have a few turns of tiles that fills each
+// product's last turn with the next one's tiles: 24 of 1024 x 1024 bf16, 240 and 384 tiles over 76
+// pairs, take 1.25 ms so and 1.39 with a launch for each product.  One matrix gains nothing (4096 x
+// 4096 fp32 2.98 ms so, 2.85 by launches, each with the tiles that suit it), and is done by launches.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -62,9 +64,11 @@ struct Op {
     bool p_kmajor, q_kmajor, symmetric, single;
 };
 
+// kMany: a list of products; else one, with what a launch of that needs alone.
+template <bool kMany>
 struct Args {
-    CUtensorMap map[3 * kOrthoBufs];             // of each buffer: k, mn, out
-    Op op[kOrthoOps];
+    CUtensorMap map[3 * (kMany ? kOrthoBufs : 3)];    // of each buffer: k, mn, out
+    Op op[kMany ? kOrthoOps : 1];
     uint32_t* done;                              // [items]
     unsigned int* err;
     uint32_t ops, items, tiles;
@@ -75,9 +79,11 @@ struct Args {
 struct Walk {
     uint32_t n = 0;                              // the product
     uint32_t item, p, q;
-    __device__ __forceinline__ void at(const Args& a, uint32_t t) {
-        while (n + 1 < a.ops && t >= a.op[n + 1].first) ++n;
-        const Op& o = a.op[n];
+    template <bool kMany>
+    __device__ __forceinline__ const Op& at(const Args<kMany>& a, uint32_t t) {
+        if constexpr (kMany)
+            while (n + 1 < a.ops && t >= a.op[n + 1].first) ++n;
+        const Op& o = a.op[kMany ? n : 0];
         const uint32_t u = t - o.first;
         item = u / o.per;
         uint32_t r = u - item * o.per;
@@ -93,11 +99,12 @@ struct Walk {
             q = r / height;
             p = band * kBand + r - q * height;
         }
+        return o;
     }
 };
 
 // Until an item's earlier products are done; false where the cluster has given up, or after some 20 s.
-__device__ __forceinline__ bool wait_done(const Args& a, const Op& o, uint32_t item, uint32_t gone, uint32_t ctas) {
+__device__ __forceinline__ bool wait_done(const Args<true>& a, const Op& o, uint32_t item, uint32_t gone, uint32_t ctas) {
     long long t0 = 0;
     for (;;) {
         uint32_t v, g;
@@ -192,8 +199,8 @@ __device__ __forceinline__ void finish(const Op& a, const CUtensorMap* out, floa
     }
 }
 
-template <int kCtas, int kBN>
-__global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(const __grid_constant__ Args a) {
+template <int kCtas, int kBN, bool kMany>
+__global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(const __grid_constant__ Args<kMany> a) {
     static_assert(kBN / kCtas == 128, "128 rows of either operand per CTA");
     constexpr int kWarps = kDrain<kBN>, kLoadWarp = kWarps, kMmaWarp = kWarps + 1;
     extern __shared__ __align__(1024) uint8_t dyn[];
@@ -247,17 +254,18 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             uint32_t s = 0, phase = 1;
             Walk tile;
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
-                tile.at(a, t);
-                const Op& o = a.op[tile.n];
+                const Op& o = tile.at(a, t);
                 const CUtensorMap *mp = &a.map[o.p], *mq = &a.map[o.q];
                 const bool pk = o.p_kmajor, qk = o.q_kmajor, single = o.single;
                 const uint32_t kblocks = o.kblocks;
                 const uint32_t p0 = tile.p * 128 * kCtas + rank * 128, q0 = tile.q * kBN + rank * 128, z = 2 * tile.item;
-                if (!wait_done(a, o, tile.item, gone, kCtas)) {
-                    ok = false;
-                    break;
+                if constexpr (kMany) {
+                    if (!wait_done(a, o, tile.item, gone, kCtas)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("fence.proxy.async;" ::: "memory");
                 }
-                asm volatile("fence.proxy.async;" ::: "memory");
                 for (uint32_t kb = 0; kb < kblocks; ++kb) {
                     const uint32_t bar = lead_full + 8 * s, at = base + s * kStageBytes;
                     if (!bar_wait(empty + 8 * s, phase, gone, kCtas)) {
@@ -281,8 +289,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             uint32_t ch = 0, it = 0, s = 0, phase = 0;
             Walk tile;
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
-                tile.at(a, t);
-                const Op& o = a.op[tile.n];
+                const Op& o = tile.at(a, t);
                 // fp32 sums of fp16 by fp16
                 const uint32_t idesc = 1u << 4 | (o.p_kmajor ? 0u : 1u << 15) | (o.q_kmajor ? 0u : 1u << 16) | (kBN / 8) << 17 |
                                        (128 * kCtas / 16) << 24;
@@ -345,8 +352,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         uint32_t ch = 0;
         Walk tile;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
-            tile.at(a, t);
-            const Op& o = a.op[tile.n];
+            const Op& o = kMany ? tile.at(a, t) : a.op[0];      // (the order that spills least)
             const uint32_t chunks = (o.kblocks + o.chunk - 1) / o.chunk;
             float acc[kCols];
 #pragma unroll
@@ -372,17 +378,19 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             }
             ok = __all_sync(~0u, ok);
             if (!ok) break;
+            if constexpr (!kMany) tile.at(a, t);
             const uint32_t row0 = tile.p * 128 * kCtas + rank * 128 + quad * 32, col0 = tile.q * kBN + part * kCols;
             const bool mirror = o.symmetric && tile.p != tile.q;
             if (row0 < o.rows && col0 < o.cols) {
-                // e1 and e2 are there, as the operands were: seen by every lane
-                ok = wait_done(a, o, tile.item, gone, kCtas);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
+                if constexpr (kMany) {
+                    // e1 and e2 are there, as the operands were: seen by every lane
+                    ok = __all_sync(~0u, wait_done(a, o, tile.item, gone, kCtas));
+                    if (!ok) break;
+                }
                 finish(o, &a.map[o.out], acc, buf, tile.item, row0, col0, mirror);
                 if (col0 + 32 < o.cols) finish(o, &a.map[o.out], acc + 32, buf, tile.item, row0, col0 + 32, mirror);
             }
-            if (lane == 0) {
+            if (kMany && lane == 0) {
                 // this warp's part of the tile is in memory: for other SMs' TMA and loads
                 asm volatile("cp.async.bulk.wait_group 0;\nfence.proxy.async;" ::: "memory");
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.done + tile.item) : "memory");
@@ -412,54 +420,35 @@ bool encode(CUtensorMap* map, const OrthoBuf& b, uint32_t items, uint32_t box_x,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCtas, int kBN>
-cudaError_t launch(const Args& a, uint32_t room, cudaStream_t stream) {
+// A list waits within itself and is launched cooperatively; a single product overlaps its start with
+// its predecessor's end.
+template <int kCtas, int kBN, bool kMany>
+cudaError_t launch(const Args<kMany>& a, uint32_t room, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.tiles < room ? a.tiles : room) * kCtas);
     cfg.blockDim = dim3(kOrthoThreads<kBN>);
     cfg.dynamicSmemBytes = kSmem<kBN>;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeCooperative;
-    at[0].val.cooperative = 1;
+    if (kMany) {
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+    } else {
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = kCtas;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = kCtas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, ortho_product_kernel<kCtas, kBN>, a);
+    return cudaLaunchKernelEx(&cfg, ortho_product_kernel<kCtas, kBN, kMany>, a);
 }
 
-}  // namespace
-
-cudaError_t prepare_ortho(OrthoShape* shape) {
-    if (shape->ready) return cudaSuccess;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&shape->sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_product_kernel<2, 256>),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<256>);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_product_kernel<1, 128>),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<128>);
-    if (e == cudaSuccess) e = tensor_map_encoder(&g_encode);
-    shape->ready = e == cudaSuccess;
-    return e;
-}
-
-cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
-    return encode(&b->k, *b, items, kBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
-                   encode(&b->mn, *b, items, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
-                   encode(&b->out, *b, items, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-
-cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
-                                  const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream) {
-    if (n > kOrthoOps) return cudaErrorInvalidValue;
-    Args a{};
+template <bool kMany>
+cudaError_t run(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count, const OrthoShape& shape,
+                unsigned int* err, bool test_expire, cudaStream_t stream) {
+    Args<kMany> a{};
     const OrthoBuf* bufs[kOrthoBufs] = {};
     uint32_t held = 0;
     const auto index = [&](const OrthoBuf* b) {
@@ -522,7 +511,7 @@ cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t it
             const double busy = t < sms ? static_cast<double>(t) / sms : 1.0;
             const double block = pair ? (o.single ? 0.6 : 0.8) : std::max(0.42, 0.58 * busy);
             // items go on without one another: whole turns for one, parts of turns for many
-            const double turns = items > 1 ? std::max(1.0, static_cast<double>(t) / room) : (t + room - 1) / room;
+            const double turns = kMany ? std::max(1.0, static_cast<double>(t) / room) : (t + room - 1) / room;
             c += turns * (block * o.kblocks + 1.5) + 3.0;
         }
         return c;
@@ -533,11 +522,56 @@ cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t it
     const bool pair = by_pair <= cost(false);
     if (pair) tiles(256);
     const uint32_t warps = pair ? 2 * kDrain<256> : kDrain<128>;
-    for (uint32_t i = 0; i < n; ++i) {
+    for (uint32_t i = 0; kMany && i < n; ++i) {
         a.op[i].need = *count;
         *count += warps * a.op[i].per;
     }
-    return pair ? launch<2, 256>(a, pairs, stream) : launch<1, 128>(a, sms, stream);
+    return pair ? launch<2, 256, kMany>(a, pairs, stream) : launch<1, 128, kMany>(a, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t prepare_ortho(OrthoShape* shape) {
+    if (shape->ready) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&shape->sms, cudaDevAttrMultiProcessorCount, dev);
+    const auto room = [&](const void* kernel, uint32_t smem) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    };
+    room(reinterpret_cast<const void*>(ortho_product_kernel<2, 256, false>), kSmem<256>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<2, 256, true>), kSmem<256>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, false>), kSmem<128>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, true>), kSmem<128>);
+    if (e == cudaSuccess) e = tensor_map_encoder(&g_encode);
+    shape->ready = e == cudaSuccess;
+    return e;
+}
+
+cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
+    return encode(&b->k, *b, items, kBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                   encode(&b->mn, *b, items, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                   encode(&b->out, *b, items, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
+                                  const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream, uint64_t* launches) {
+    if (n > kOrthoOps) return cudaErrorInvalidValue;
+    // one at a time: one matrix, or turns enough that a part of one does not count
+    uint64_t most = 0;
+    for (uint32_t i = 0; i < n; ++i)
+        most = std::max<uint64_t>(most, (p[i].out->rows + 255ull) / 256 * ((p[i].out->cols + 255ull) / 256) * items);
+    if (n > 1 && (items == 1 || most > 8ull * shape.sms / 2)) {
+        cudaError_t e = cudaSuccess;
+        for (uint32_t i = 0; i < n && e == cudaSuccess; ++i)
+            e = launch_ortho_products(p + i, 1, items, done, count, shape, err, test_expire, stream, launches);
+        return e;
+    }
+    *launches += 1;
+    return n == 1 ? run<false>(p, n, items, done, count, shape, err, test_expire, stream)
+                  : run<true>(p, n, items, done, count, shape, err, test_expire, stream);
 }
 
 }  // namespace fa

@@ -273,11 +273,12 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
                 run.segment(n, X, top[steps], steps == p.steps);
             }
             const size_t all = run.list.size();
-            for (size_t at = 0; r == FA_OK && at < all; at += fa::kOrthoOps)
-                r = launched(w, fa::launch_ortho_products(run.list.data() + at, static_cast<uint32_t>(std::min<size_t>(fa::kOrthoOps, all - at)),
-                                                          e.items, done, &counted, w->ortho, w->err_dev,
-                                                          (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s),
-                             "orthogonalisation");
+            for (size_t at = 0; r == FA_OK && at < all; at += fa::kOrthoOps) {
+                const cudaError_t ce = fa::launch_ortho_products(
+                    run.list.data() + at, static_cast<uint32_t>(std::min<size_t>(fa::kOrthoOps, all - at)), e.items, done, &counted,
+                    w->ortho, w->err_dev, (w->flags & FA_TEST_WAIT_EXPIRES) != 0, s, &w->stats.kernel_launches);
+                if (ce != cudaSuccess) r = cuda_fail(w, ce, "orthogonalisation");
+            }
             e.x = X.buf->p;
             e.alpha = static_cast<float>(std::ldexp(p.alpha, -X.shift));
             if (r == FA_OK) r = launched(w, fa::launch_ortho_finish(e, s), "weight step");

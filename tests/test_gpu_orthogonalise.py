@@ -70,7 +70,7 @@ def near(got, x64, alpha, res, dtype, steps, coefficients=QUINTIC, full=True):
 
 SIZES = [(1, 1, 1), (1, 1, 300), (1, 300, 1), (1, 10, 256), (3, 16, 70), (2, 64, 64), (1, 65, 130), (2, 128, 128), (1, 129, 257),
          (1, 300, 200), (3, 256, 1000), (1, 1000, 256), (2, 513, 520), (5, 33, 4099), (1, 4099, 31), (1, 1024, 1024),
-         (40, 16, 512), (40, 512, 16), (1, 600, 2100), (2, 8, 20000), (200, 30, 1100), (500, 700, 7), (80, 60, 2100), (3, 2060, 30), (1, 32, 7000), (1, 31, 9000)]
+         (40, 16, 512), (40, 512, 16), (1, 600, 2100), (70, 100, 120), (9, 300, 700), (2, 8, 20000), (200, 30, 1100), (500, 700, 7), (80, 60, 2100), (3, 2060, 30), (1, 32, 7000), (1, 31, 9000)]
 
 
 @pytest.mark.parametrize("count,rows,cols", SIZES)
