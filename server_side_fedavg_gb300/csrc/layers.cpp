@@ -60,6 +60,7 @@ fa_status rotary_impl(fa_work* w, const fa_rotary_args& p, cudaStream_t s) {
     }
     a.position = p.position;
     a.first = p.first;
+    a.err = w->err_dev;
     a.tokens = static_cast<uint32_t>(tokens);
     a.seq = static_cast<uint32_t>(p.seq);
     a.head_dim = p.head_dim;

@@ -25,6 +25,8 @@ struct RotaryArgs {
     uint32_t head_dim, rotary_dim;
     uint32_t chunks, turning;   // per head: pieces of 2 V elements, and those of them that turn
     uint32_t slots;             // heads of a token are shared out over so many threads per piece
+    uint32_t cta_tokens;        // the ring's, of a stage
+    unsigned int* err;
     int dtype;
     float scale;
     bool interleaved, inverse, copy;   // copy: what does not turn goes to out too

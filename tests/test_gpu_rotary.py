@@ -205,3 +205,34 @@ def test_infinities_and_nan_stay_in_their_pair(work):
     want = torch.zeros_like(bad)
     want[0, 1, 0, 3] = want[0, 1, 0, 11] = want[0, 2, 1, 4] = want[0, 2, 1, 12] = True
     assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("batch,seq,qh,kh,dim,r,dtype", [(3, 1900, 16, 16, 128, 128, "bf16"), (2, 2777, 24, 8, 96, 48, "bf16"),
+                                                         (1, 9001, 32, 0, 72, 36, "bf16"), (5, 1500, 16, 2, 128, 26, "bf16")])
+def test_many_tokens(work, layout, batch, seq, qh, kh, dim, r, dtype):
+    """Large enough for the form that streams tokens through shared memory: out of place with padding,
+    and in place in a packed buffer, both as the fp64 rotation has it."""
+    width = (qh + kh) * dim + 8
+    packed = inputs(batch, seq, 1, width, dtype, 21).view(batch, seq, width)
+    before = packed.clone()
+    q, k = packed[:, :, :qh * dim], packed[:, :, qh * dim:]
+    pos = torch.randint(0, 100000, (batch, seq), device="cuda", dtype=torch.int32)
+    pos[:, seq - 300:] = -1
+    live = (pos >= 0)[:, :, None, None]
+    st, turns = (seq * width, width, dim), fa.rotary_turns(r)
+    outs = [torch.full((batch, seq, max(h, 1), dim), 3.0, device="cuda", dtype=T[dtype]) for h in (qh, kh)]
+    fa.fa_rotary(work, batch, seq, dim, turns, dtype, q, qh, outs[0], k, kh, outs[1], position=pos, layout=layout, inverse=True,
+                 q_strides=st, k_strides=st)
+    fa.fa_rotary(work, batch, seq, dim, turns, dtype, q, qh, q, k, kh, k, position=pos, layout=layout, inverse=True, q_strides=st,
+                 k_strides=st)
+    fa.fa_work_sync(work)
+    for at, heads, out in ((0, qh, outs[0]), (qh * dim, kh, outs[1])):
+        if heads == 0:
+            continue
+        x = before[:, :, at:at + heads * dim].reshape(batch, seq, heads, dim)
+        want, size = expect(x, pos, frequencies(r), layout, True)
+        assert torch.where(live, (out.double() - want).abs() <= size, out == 3).all()
+        got = packed[:, :, at:at + heads * dim].reshape(batch, seq, heads, dim)
+        assert torch.equal(torch.where(live, out, x), got)
+    assert torch.equal(packed[:, :, (qh + kh) * dim:], before[:, :, (qh + kh) * dim:])
