@@ -617,13 +617,6 @@ def rotary_turns(rotary_dim, base=10000.0, scaling="none", factor=1.0, context=0
     return turns
 
 
-def _rotary_part(x, heads, out, strides, out_strides, seq, head_dim):
-    own = (seq * heads * head_dim, heads * head_dim, head_dim)
-    strides = own if strides is None else strides
-    return fa_rotary_part(_ptr(x), _ptr(out), heads, 0, *strides,
-                          *(strides if out_strides is None and out is x else own if out_strides is None else out_strides))
-
-
 def fa_rotary(work, batch, seq, head_dim, turns, dtype, q, q_heads, q_out, k=None, k_heads=0, k_out=None,
               position=None, first=0, layout="half", inverse=False, scale=1.0, q_strides=None,
               q_out_strides=None, k_strides=None, k_out_strides=None, stream=None):
@@ -632,17 +625,36 @@ def fa_rotary(work, batch, seq, head_dim, turns, dtype, q, q_heads, q_out, k=Non
     position: int32 [batch, seq], negative in padding (left as it is), or None for first + s.
     layout "half" pairs (i, i + rotary_dim / 2), "interleaved" (2 i, 2 i + 1).  inverse: the
     gradient's direction.  An output may be its input itself."""
-    _check_types((position,), ("int32",), _position_seen, "position is int32")
-    if layout not in ("half", "interleaved"):
+    dt = getattr(position, "dtype", None)
+    if dt not in _position_seen:
+        _check_types((position,), ("int32",), _position_seen, "position is int32")
+    flags = _LAYOUTS.get(layout)
+    if flags is None:
         raise ValueError(f"layout is 'half' or 'interleaved', not {layout!r}")
+    if q_strides is None or (q_out_strides is None and q_out is not q):
+        row = q_heads * head_dim
+        q_own = (seq * row, row, head_dim)
+    if k_strides is None or (k_out_strides is None and k_out is not k):
+        row = k_heads * head_dim
+        k_own = (seq * row, row, head_dim)
+    if q_strides is None:
+        q_strides = q_own
+    if q_out_strides is None:
+        q_out_strides = q_strides if q_out is q else q_own
+    if k_strides is None:
+        k_strides = k_own
+    if k_out_strides is None:
+        k_out_strides = k_strides if k_out is k else k_own
     args = fa_rotary_args(
-        ctypes.sizeof(fa_rotary_args), (layout == "interleaved") | bool(inverse) << 1, DTYPES[dtype], head_dim,
-        2 * len(turns), 0, batch, seq, ctypes.addressof(turns), _ptr(position), first, scale,
-        _rotary_part(q, q_heads, q_out, q_strides, q_out_strides, seq, head_dim),
-        _rotary_part(k, k_heads, k_out, k_strides, k_out_strides, seq, head_dim))
+        _ROTARY_SIZE, flags | FA_ROTARY_INVERSE if inverse else flags, DTYPES[dtype], head_dim, 2 * len(turns), 0, batch, seq,
+        ctypes.addressof(turns), _ptr(position), first, scale,
+        (_ptr(q), _ptr(q_out), q_heads, 0, *q_strides, *q_out_strides),
+        (_ptr(k), _ptr(k_out), k_heads, 0, *k_strides, *k_out_strides))
     _check_work(lib().fa_rotary(work, args, _stream(stream)), work)
 
 
+_LAYOUTS = {"half": 0, "interleaved": FA_ROTARY_INTERLEAVED}
+_ROTARY_SIZE = ctypes.sizeof(fa_rotary_args)
 _position_seen = {None}
 
 
