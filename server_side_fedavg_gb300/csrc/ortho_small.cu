@@ -20,9 +20,13 @@ namespace {
 
 constexpr uint32_t kSmallThreads = 256, kSmallWarps = kSmallThreads / 32, kSmallCtas = 8;
 // Rows per CTA, unless eight CTAs have to hold more: for a few matrices, and for more than would
-// fill the SMs twice.  What every CTA does for itself counts: one of 16 x 4096 bf16 takes 16 us with
-// runs of 512 and 22 with 1024; 128 take 89 and 68 us.
+// fill the SMs twice.  What every CTA does for itself counts: one of 16 x 4096 bf16 takes 17 us with
+// runs of 512 and 25 with 1024; 128 take 98 and 79 us.
 constexpr uint32_t kSmallRun = 512, kManyRun = 1024, kMany = 304;
+// Sides above 32, an SM's registers to a CTA: 128 rows while the SMs (of which whole clusters of eight
+// find 14 to 16 places) hold all clusters at once, else 256, or 512.  1 x 64 x 1024 fp32 71 us in runs of
+// 128 and 92 of 256, 16 x 48 x 1000 bf16 141 and 93, 300 x 48 x 700 809 in runs of 256 and 520 of 512.
+constexpr uint32_t kRun64 = 128, kMany64 = 112;
 constexpr uint32_t kSmallMost = 226 * 1024;    // bytes of shared memory
 constexpr uint32_t kSmallAhead = 4;            // pieces of eight elements whose loads a thread has in flight
 
@@ -80,21 +84,36 @@ __device__ __forceinline__ void mul(float* C, const float* A, const float* B, fl
     __syncthreads();
 }
 
+// Element i of 8 of a piece `at`: four rows (or columns) of either half of the matrix, so that lanes with
+// neighbouring pieces read neighbouring 16 bytes.
+template <int kM>
+__device__ __forceinline__ uint32_t piece_row(uint32_t at, uint32_t i) {
+    return 4 * at + i % 4 + i / 4 * (kM / 2);
+}
+
 // This CTA's sum of x_j x_j^T over its run, to out[kM][kM].  A lane has an 8 x 8 tile of the result
-// and every so-manieth row; lanes with one tile, then warps, are summed in a fixed order.
+// and every so-manieth row; lanes with one tile, then warps, are summed in a fixed order.  kM == 64: the
+// tiles on and above the diagonal alone.
 template <int kM>
 __device__ __forceinline__ void gram(const float* xs, uint32_t run, float* red, float* out) {
-    constexpr uint32_t kSide = kM / 8, kTiles = kSide * kSide, kStrands = kSmallThreads / kTiles;
-    const uint32_t tile = threadIdx.x % kTiles, strand = threadIdx.x / kTiles, ti = tile / kSide * 8, tk = tile % kSide * 8;
+    constexpr bool kHalf = kM == 64;
+    constexpr uint32_t kSide = kM / 8, kTiles = kHalf ? kSide * (kSide + 1) / 2 : kSide * kSide, kStrands = kSmallThreads / kTiles;
+    const uint32_t tile = threadIdx.x % kTiles, strand = threadIdx.x / kTiles;
+    uint32_t ti = tile / kSide, tk = tile % kSide;
+    if constexpr (kHalf) {
+        uint32_t r = tile;
+        for (ti = 0; r >= kSide - ti; ++ti) r -= kSide - ti;
+        tk = ti + r;
+    }
     float2 s[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[i][k] = make_float2(0.0f, 0.0f);
-    for (uint32_t j = strand; j < run; j += kStrands) {
+    for (uint32_t j = strand < kStrands ? strand : run; j < run; j += kStrands) {
         const float* x = xs + j * kPitch<kM>;
-        const float4 a0 = *reinterpret_cast<const float4*>(x + ti), a1 = *reinterpret_cast<const float4*>(x + ti + 4);
-        const float4 b0 = *reinterpret_cast<const float4*>(x + tk), b1 = *reinterpret_cast<const float4*>(x + tk + 4);
+        const float4 a0 = *reinterpret_cast<const float4*>(x + 4 * ti), a1 = *reinterpret_cast<const float4*>(x + 4 * ti + kM / 2);
+        const float4 b0 = *reinterpret_cast<const float4*>(x + 4 * tk), b1 = *reinterpret_cast<const float4*>(x + 4 * tk + kM / 2);
         const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
         const float2 bv[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y), make_float2(b1.z, b1.w)};
 #pragma unroll
@@ -102,8 +121,8 @@ __device__ __forceinline__ void gram(const float* xs, uint32_t run, float* red, 
 #pragma unroll
             for (int k = 0; k < 4; ++k) fma2(s[i][k], make_float2(av[i], av[i]), bv[k]);
     }
-    float* v = &s[0][0].x;
-    if constexpr (kTiles <= 32) {
+    if constexpr (!kHalf) {
+        float* v = &s[0][0].x;
         // lanes with one tile: each exchange halves what a lane keeps
         const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         uint32_t first = 0;
@@ -120,7 +139,7 @@ __device__ __forceinline__ void gram(const float* xs, uint32_t run, float* red, 
         constexpr uint32_t kKeep = 64 * kTiles / 32;
 #pragma unroll
         for (uint32_t e = 0; e < kKeep; ++e)
-            red[(warp * kM + ti + (first + e) / 8) * kM + tk + (first + e) % 8] = v[e];
+            red[(warp * kM + piece_row<kM>(ti, (first + e) / 8)) * kM + piece_row<kM>(tk, (first + e) % 8)] = v[e];
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < kM * kM; i += kSmallThreads) {
             float t = 0.0f;
@@ -132,20 +151,62 @@ __device__ __forceinline__ void gram(const float* xs, uint32_t run, float* red, 
         for (uint32_t turn = 0; turn < kStrands; ++turn) {
             if (strand == turn)
 #pragma unroll
-                for (uint32_t e = 0; e < 64; ++e) {
-                    float* to = out + (ti + e / 8) * kM + tk + e % 8;
-                    *to = turn ? *to + v[e] : v[e];
-                }
+                for (uint32_t i = 0; i < 8; ++i)
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        float4* to = reinterpret_cast<float4*>(out + piece_row<kM>(ti, i) * kM + piece_row<kM>(tk, 4 * h));
+                        float4 t = turn ? *to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        t.x += s[i][2 * h].x;
+                        t.y += s[i][2 * h].y;
+                        t.z += s[i][2 * h + 1].x;
+                        t.w += s[i][2 * h + 1].y;
+                        *to = t;
+                    }
             __syncthreads();
         }
     }
+}
+
+// A = f * the CTAs' sums, in rank order.
+template <int kM>
+__device__ __forceinline__ void join(float* A, const float* own, uint32_t ctas, float f) {
+    if constexpr (kM < 64) {
+        for (uint32_t i = threadIdx.x; i < kM * kM; i += kSmallThreads) {
+            float v = 0.0f;
+            for (uint32_t q = 0; q < ctas; ++q) v += ld_part1(smem_addr(own + i), q, ctas);
+            A[i / kM * kPitch<kM> + i % kM] = v * f;
+        }
+    } else {
+        for (uint32_t i = threadIdx.x; i < kM * kM / 4; i += kSmallThreads) {
+            const uint32_t r = i / (kM / 4), c = i % (kM / 4) * 4, pr = r % (kM / 2) / 4, pc = c % (kM / 2) / 4;
+            if (pr > pc) continue;                   // below the diagonal
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (uint32_t q = 0; q < ctas; ++q) {
+                const float4 t = ld_part(smem_addr(own + 4 * i), q, ctas);
+                v.x += t.x;
+                v.y += t.y;
+                v.z += t.z;
+                v.w += t.w;
+            }
+            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            *reinterpret_cast<float4*>(A + r * kPitch<kM> + c) = v;
+            if (pr < pc) {
+                float* to = A + c * kPitch<kM> + r;
+                to[0] = v.x;
+                to[kPitch<kM>] = v.y;
+                to[2 * kPitch<kM>] = v.z;
+                to[3 * kPitch<kM>] = v.w;
+            }
+        }
+    }
+    __syncthreads();
 }
 
 // x_j <- q x_j + Q x_j.  A thread has kRows rows, 256 kRows 8 / kM apart, by 8 elements, kM / 8 apart:
 // neighbouring lanes read neighbouring rows.
 template <int kM>
 __device__ __forceinline__ void apply(float* xs, uint32_t run, const float* Q, float q) {
-    constexpr uint32_t kSide = kM / 8, kGroups = kSmallThreads / kSide, kRows = kM >= 32 ? 8 : kM / 4;
+    constexpr uint32_t kSide = kM / 8, kGroups = kSmallThreads / kSide, kRows = kM == 32 ? 8 : kM == 64 ? 4 : kM / 4;
     const uint32_t i0 = threadIdx.x % kSide, g = threadIdx.x / kSide;
     for (uint32_t j0 = 0; j0 < run; j0 += kGroups * kRows) {
         float y[kRows][8];
@@ -181,6 +242,19 @@ __device__ __forceinline__ void apply(float* xs, uint32_t run, const float* Q, f
     }
 }
 
+// x[k] <- x[(k + by) % 8].  Lanes that write (or read) a column of xs each, eight rows apart, start at
+// different rows of their eight, so that they meet no bank conflict: kPitch is four times an odd number.
+__device__ __forceinline__ void rotate(float (&x)[8], uint32_t by) {
+#pragma unroll
+    for (uint32_t b = 1; b < 8; b *= 2) {
+        float y[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) y[k] = by & b ? x[(k + b) % 8] : x[k];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) x[k] = y[k];
+    }
+}
+
 struct SmallArgs {
     OrthoEnds e;
     OrthoSmall s;
@@ -202,12 +276,17 @@ __global__ void __launch_bounds__(kSmallThreads, kM <= 16 ? 2 : 1) ortho_small_k
     const uint32_t j0 = min(n, rank * a.run), run = min(a.run, n - j0), run8 = (run + 7) / 8 * 8;
     wait_predecessor();
 
-    // The rows eight elements at a time: along the long side of the matrix (wide), or of a row x_j.
-    const uint32_t all = wide ? run8 / 8 * kM : run * (kM / 8);
-    // the matrix's row and column of piece t, and its place in shared memory
-    const auto row_at = [&](uint32_t t) { return wide ? t % kM : j0 + t / (kM / 8); };
-    const auto col_at = [&](uint32_t t) { return wide ? j0 + t / kM * 8 : t % (kM / 8) * 8; };
-    const auto in_use = [&](uint32_t t) { return t < all && (wide ? t % kM : t % (kM / 8) * 8) < m; };
+    // The rows eight elements at a time: along the long side of the matrix (wide), or of a row x_j.  Wide,
+    // eight neighbouring lanes have neighbouring pieces of one row of the matrix, a line of memory, and a
+    // warp four rows (lanes with a row each took three times as long: 128 of 16 x 4096 98 us, so 79).
+    const uint32_t pieces = run8 / 8, all = wide ? (pieces + 7) / 8 * 8 * kM : run * (kM / 8), turn = threadIdx.x % 8;
+    // a piece's row of the matrix less m's part, or of x_j; and its place along the other side
+    const auto row_in = [&](uint32_t t) { return wide ? t / 32 % (kM / 4) * 4 + t % 32 / 8 : t / (kM / 8); };
+    const auto piece_in = [&](uint32_t t) { return wide ? t / (8 * kM) * 8 + t % 8 : t % (kM / 8); };
+    const auto row_at = [&](uint32_t t) { return wide ? row_in(t) : j0 + row_in(t); };
+    const auto col_at = [&](uint32_t t) { return wide ? j0 + piece_in(t) * 8 : piece_in(t) * 8; };
+    const auto held = [&](uint32_t t) { return t < all && (!wide || piece_in(t) < pieces); };
+    const auto in_use = [&](uint32_t t) { return held(t) && (wide ? row_in(t) : piece_in(t) * 8) < m; };
     Squares sum;
     for (uint32_t t0 = threadIdx.x; t0 < all; t0 += kSmallAhead * kSmallThreads) {
         float x[kSmallAhead][8], g[kSmallAhead][8];
@@ -221,7 +300,7 @@ __global__ void __launch_bounds__(kSmallThreads, kM <= 16 ? 2 : 1) ortho_small_k
 #pragma unroll
         for (uint32_t u = 0; u < kSmallAhead; ++u) {
             const uint32_t t = t0 + u * kSmallThreads;
-            if (t >= all) break;
+            if (!held(t)) break;
             if (in_use(t)) {
                 momentum_step(e, x[u], g[u]);
                 if (e.momentum_out.p)
@@ -232,11 +311,12 @@ __global__ void __launch_bounds__(kSmallThreads, kM <= 16 ? 2 : 1) ortho_small_k
                 for (uint32_t k = 0; k < 8; ++k) x[u][k] = 0.0f;
             }
             if (wide) {
-                float* to = xs + t / kM * 8 * kPitch<kM> + t % kM;
+                float* to = xs + piece_in(t) * 8 * kPitch<kM> + row_in(t);
+                rotate(x[u], turn);
 #pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) to[k * kPitch<kM>] = x[u][k];
+                for (uint32_t k = 0; k < 8; ++k) to[((k + turn) % 8) * kPitch<kM>] = x[u][k];
             } else {
-                float* to = xs + t / (kM / 8) * kPitch<kM> + t % (kM / 8) * 8;
+                float* to = xs + row_in(t) * kPitch<kM> + piece_in(t) * 8;
                 *reinterpret_cast<float4*>(to) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
                 *reinterpret_cast<float4*>(to + 4) = make_float4(x[u][4], x[u][5], x[u][6], x[u][7]);
             }
@@ -283,12 +363,7 @@ __global__ void __launch_bounds__(kSmallThreads, kM <= 16 ? 2 : 1) ortho_small_k
             cluster_sync();
         else
             __syncthreads();
-        for (uint32_t i = threadIdx.x; i < kM * kM; i += kSmallThreads) {
-            float v = 0.0f;
-            for (uint32_t q = 0; q < a.ctas; ++q) v += ld_part1(smem_addr(own + i), q, a.ctas);
-            A[i / kM * kPitch<kM> + i % kM] = v * f0 * f0;
-        }
-        __syncthreads();
+        join<kM>(A, own, a.ctas, f0 * f0);
         float *P = P0, *Q = P0, *next = Q0;
         float q = 1.0f;
         for (uint32_t j = 0; j < steps; ++j) {
@@ -325,10 +400,13 @@ __global__ void __launch_bounds__(kSmallThreads, kM <= 16 ? 2 : 1) ortho_small_k
             const uint32_t t = t0 + u * kSmallThreads;
             if (!in_use(t)) continue;
             float x[8];
-            const float* from = wide ? xs + t / kM * 8 * kPitch<kM> + t % kM : xs + t / (kM / 8) * kPitch<kM> + t % (kM / 8) * 8;
+            const float* from = wide ? xs + piece_in(t) * 8 * kPitch<kM> + row_in(t) : xs + row_in(t) * kPitch<kM> + piece_in(t) * 8;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) x[k] = from[wide ? (k + turn) % 8 * kPitch<kM> : k];
+            if (wide) rotate(x, 8 - turn);
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
-                x[k] = e.alpha * (f0 * from[wide ? k * kPitch<kM> : k]);
+                x[k] = e.alpha * (f0 * x[k]);
                 if (e.residual.p) x[k] = fmaf(e.beta, res[u][k], x[k]);
             }
             store8(e.out, row_of(e.out, item, row_at(t)), col_at(t), e.cols, a.v.out, x);
@@ -349,6 +427,13 @@ uint64_t split(uint32_t m, uint32_t n, uint32_t items, uint32_t* ctas, uint32_t*
         *run = ((n + *ctas - 1) / *ctas + 7) / 8 * 8;
         return static_cast<uint64_t>(*run) * (side(m) + 4) * 4 + fixed(m);
     };
+    if (side(m) == 64) {
+        for (const uint32_t rows : {kRun64, 2 * kRun64}) {
+            const uint64_t bytes = fill(rows);
+            if (static_cast<uint64_t>(items) * *ctas <= kMany64) return bytes;
+        }
+        return fill(4 * kRun64);
+    }
     const uint64_t few = fill(kSmallRun);
     if (static_cast<uint64_t>(items) * *ctas <= kMany) return few;
     const uint64_t many = fill(kManyRun);
