@@ -41,6 +41,9 @@ constexpr uint32_t kPlane = 128 * kBK * 2;       // of an operand's 128 rows
 constexpr uint32_t kStageBytes = 4 * kPlane;
 constexpr uint32_t kRing = 3;                    // stages
 constexpr uint32_t kUnit = 2048;                 // a drain warp's block of 32 x 32 results on its way out
+// Such blocks that a drain warp has under way after the CTA's last tile.  With one alone each store waited
+// for the one before to be read.
+constexpr uint32_t kUnits = 6;
 constexpr uint32_t kBand = 8;                    // rows of tiles walked together
 constexpr int kCols = 64;                        // of a drain warp
 
@@ -50,6 +53,7 @@ constexpr int kDrain = 4 * kBN / kCols;          // drain warps
 // the product kernels: 128 x 56 + 512 x 104 <= 640 x 96.
 template <int kBN>
 constexpr int kOrthoThreads = (kDrain<kBN> + (kBN == 256 ? 4 : 2)) * 32;
+static_assert(kDrain<256> * kUnits * kUnit <= kRing * kStageBytes && kRing * kStageBytes / kDrain<256> % kUnit == 0);
 template <int kBN>
 constexpr uint32_t kSmem = kRing * kStageBytes + kDrain<kBN> * kUnit;
 
@@ -148,54 +152,73 @@ __device__ __forceinline__ void add_planes(float* v, const uint16_t* hi, uint64_
     }
 }
 
-// The block of 32 x 32 results at (row, col) from v, this lane's row of it: e1 and e2 added, then
-// either plane by way of the warp's buffer, and its mirror image.  64-byte rows in the 64-byte
-// swizzle: 16-byte piece j of row r is at j ^ (r / 2 % 4).
-__device__ __forceinline__ void finish(const Op& a, const CUtensorMap* out, float* v, uint32_t buf, uint32_t item, uint32_t row0,
-                                       uint32_t col, bool mirror) {
-    const uint32_t lane = threadIdx.x % 32, row = row0 + lane;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= a.c1;
-    if (row < a.rows) {
-        const uint64_t at = 2ull * item * a.plane + row * a.ld + col;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (a.e1 && col + 8 * j < a.cols) add_planes(v + 8 * j, a.e1 + at + 8 * j, a.plane, a.c2);
-            if (a.e2 && col + 8 * j < a.cols) add_planes(v + 8 * j, a.e2 + at + 8 * j, a.plane, a.c3);
+// A warp's results as they leave: units of 32 x 32, each free again when its store has read it.
+struct Units {
+    uint32_t at, n, next;                        // n: kUnits, or 1
+    __device__ __forceinline__ uint32_t take() {
+        if (threadIdx.x % 32 == 0) {
+            if (n == 1)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else
+                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kUnits - 1) : "memory");
+        }
+        __syncwarp();
+        const uint32_t u = at + next * kUnit;
+        next = next + 1 == n ? 0 : next + 1;
+        return u;
+    }
+    __device__ __forceinline__ void store(const CUtensorMap* out, uint32_t u, uint32_t x, uint32_t y, uint32_t z) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) {
+            tma_store_3d(out, u, x, y, z);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
     }
+};
+
+// v = c1 v + c2 e1 + c3 e2: this lane's row of kCols results from (row, col) on.
+__device__ __forceinline__ void join(const Op& a, float* v, uint32_t item, uint32_t row, uint32_t col) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] *= a.c1;
+    if (row >= a.rows) return;
+    const uint64_t at = 2ull * item * a.plane + row * a.ld + col;
+    if (a.e1)
+#pragma unroll
+        for (int j = 0; j < kCols; j += 8)
+            if (col + j < a.cols) add_planes(v + j, a.e1 + at + j, a.plane, a.c2);
+    if (a.e2)
+#pragma unroll
+        for (int j = 0; j < kCols; j += 8)
+            if (col + j < a.cols) add_planes(v + j, a.e2 + at + j, a.plane, a.c3);
+}
+
+// The block of 32 x 32 results at (row, col) from v, this lane's row of it: either plane by way of a
+// unit, and its mirror image.  64-byte rows in the 64-byte swizzle: 16-byte piece j of row r is at
+// j ^ (r / 2 % 4).
+__device__ __forceinline__ void finish(const CUtensorMap* out, float* v, Units& units, uint32_t item, uint32_t row0, uint32_t col,
+                                       bool mirror) {
+    const uint32_t lane = threadIdx.x % 32;
 #pragma unroll
     for (uint32_t z = 0; z < 2; ++z) {
         if (z == 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] -= half_of(v[i]);
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
+        uint32_t u = units.take();
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j)
-            st_shared4u(buf + lane * 64 + ((j ^ (lane / 2 % 4)) << 4), pack_half(v[8 * j], v[8 * j + 1]),
+            st_shared4u(u + lane * 64 + ((j ^ (lane / 2 % 4)) << 4), pack_half(v[8 * j], v[8 * j + 1]),
                         pack_half(v[8 * j + 2], v[8 * j + 3]), pack_half(v[8 * j + 4], v[8 * j + 5]),
                         pack_half(v[8 * j + 6], v[8 * j + 7]));
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(out, buf, col, row0, 2 * item + z);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        units.store(out, u, col, row0, 2 * item + z);
         if (!mirror) continue;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
+        u = units.take();
 #pragma unroll
         for (uint32_t c = 0; c < 32; ++c)
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + c * 64 + ((lane / 8 ^ (c / 2 % 4)) << 4) + lane % 8 * 2),
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(u + c * 64 + ((lane / 8 ^ (c / 2 % 4)) << 4) + lane % 8 * 2),
                          "h"(__half_as_ushort(__float2half_rn(v[c])))
                          : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(out, buf, row0, col, 2 * item + z);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        units.store(out, u, row0, col, 2 * item + z);
     }
 }
 
@@ -387,8 +410,12 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                     ok = __all_sync(~0u, wait_done(a, o, tile.item, gone, kCtas));
                     if (!ok) break;
                 }
-                finish(o, &a.map[o.out], acc, buf, tile.item, row0, col0, mirror);
-                if (col0 + 32 < o.cols) finish(o, &a.map[o.out], acc + 32, buf, tile.item, row0, col0 + 32, mirror);
+                // the last tile's results leave by way of the stages, which nothing needs any more
+                Units units{buf, 1, 0};
+                if (t + step >= a.tiles) units = {base + warp * (kRing * kStageBytes / kWarps), kUnits, 0};
+                join(o, acc, tile.item, row0 + lane, col0);
+                finish(&a.map[o.out], acc, units, tile.item, row0, col0, mirror);
+                if (col0 + 32 < o.cols) finish(&a.map[o.out], acc + 32, units, tile.item, row0, col0 + 32, mirror);
             }
             if (kMany && lane == 0) {
                 // this warp's part of the tile is in memory: for other SMs' TMA and loads
