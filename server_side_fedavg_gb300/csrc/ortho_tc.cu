@@ -138,20 +138,6 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 
 __device__ __forceinline__ float half_of(float x) { return __half2float(__float2half_rn(x)); }
 
-// v += c * (hi + lo) of eight elements
-__device__ __forceinline__ void add_planes(float* v, const uint16_t* hi, uint64_t plane, float c) {
-    // from L2: other SMs have written them during this launch
-    const uint4 h = __ldcg(reinterpret_cast<const uint4*>(hi)), l = __ldcg(reinterpret_cast<const uint4*>(hi + plane));
-    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hw[i]));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&lw[i]));
-        v[2 * i] = fmaf(c, a.x + b.x, v[2 * i]);
-        v[2 * i + 1] = fmaf(c, a.y + b.y, v[2 * i + 1]);
-    }
-}
-
 // A warp's results as they leave: units of 32 x 32, each free again when its store has read it.
 struct Units {
     uint32_t at, n, next;                        // n: kUnits, or 1
@@ -177,20 +163,52 @@ struct Units {
     }
 };
 
-// v = c1 v + c2 e1 + c3 e2: this lane's row of kCols results from (row, col) on.
-__device__ __forceinline__ void join(const Op& a, float* v, uint32_t item, uint32_t row, uint32_t col) {
+// v += c * e: the warp's 32 rows from row0 of kCols columns from col on, of which v is this lane's row.  Four
+// lanes read 64 bytes of a row, and a unit hands the rows over (a row for each lane touched a line for
+// each: 3.3 us of the 9 that a product of 230 x 230 took).  kPlanes of a block's two are fetched at a
+// time, as registers allow.
+template <uint32_t kPlanes>
+__device__ __forceinline__ void add_to(const Op& a, const uint16_t* e, float c, float* v, Units& units, uint32_t item, uint32_t row0,
+                                       uint32_t col) {
+    const uint32_t lane = threadIdx.x % 32, r0 = lane / 4, j0 = lane % 4;
+    const uint16_t* from = e + 2ull * item * a.plane + (row0 + r0) * a.ld + col + 8 * j0;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) v[i] *= a.c1;
-    if (row >= a.rows) return;
-    const uint64_t at = 2ull * item * a.plane + row * a.ld + col;
-    if (a.e1)
+    for (uint32_t n = 0; n < kCols / 32 * 2; n += kPlanes) {
+        const uint32_t h = n / 2;
+        uint4 q[kPlanes][4];
+        const bool in = col + 32 * h + 8 * j0 < a.cols;
 #pragma unroll
-        for (int j = 0; j < kCols; j += 8)
-            if (col + j < a.cols) add_planes(v + j, a.e1 + at + j, a.plane, a.c2);
-    if (a.e2)
+        for (uint32_t z = 0; z < kPlanes; ++z)
 #pragma unroll
-        for (int j = 0; j < kCols; j += 8)
-            if (col + j < a.cols) add_planes(v + j, a.e2 + at + j, a.plane, a.c3);
+            for (uint32_t i = 0; i < 4; ++i) {
+                q[z][i] = make_uint4(0, 0, 0, 0);
+                // from L2: other SMs may have written them during this launch
+                if (in && row0 + r0 + 8 * i < a.rows)
+                    q[z][i] = __ldcg(reinterpret_cast<const uint4*>(from + (n + z) % 2 * a.plane + 8 * i * a.ld + 32 * h));
+            }
+#pragma unroll
+        for (uint32_t z = 0; z < kPlanes; ++z) {
+            const uint32_t u = units.take();
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t r = r0 + 8 * i;
+                st_shared4u(u + r * 64 + ((j0 ^ (r / 2 % 4)) << 4), q[z][i].x, q[z][i].y, q[z][i].z, q[z][i].w);
+            }
+            __syncwarp();
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint4 w = ld_shared4u(u + lane * 64 + ((j ^ (lane / 2 % 4)) << 4));
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[k]));
+                    float* to = v + 32 * h + 8 * j + 2 * k;
+                    to[0] = fmaf(c, f.x, to[0]);
+                    to[1] = fmaf(c, f.y, to[1]);
+                }
+            }
+        }
+    }
 }
 
 // The block of 32 x 32 results at (row, col) from v, this lane's row of it: either plane by way of a
@@ -413,7 +431,10 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 // the last tile's results leave by way of the stages, which nothing needs any more
                 Units units{buf, 1, 0};
                 if (t + step >= a.tiles) units = {base + warp * (kRing * kStageBytes / kWarps), kUnits, 0};
-                join(o, acc, tile.item, row0 + lane, col0);
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) acc[i] *= o.c1;
+                if (o.e1) add_to<kBN == 128 ? 2 : 1>(o, o.e1, o.c2, acc, units, tile.item, row0, col0);
+                if (o.e2) add_to<kBN == 128 ? 2 : 1>(o, o.e2, o.c3, acc, units, tile.item, row0, col0);
                 finish(&a.map[o.out], acc, units, tile.item, row0, col0, mirror);
                 if (col0 + 32 < o.cols) finish(&a.map[o.out], acc + 32, units, tile.item, row0, col0 + 32, mirror);
             }
