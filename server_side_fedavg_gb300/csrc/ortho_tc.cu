@@ -44,8 +44,11 @@ constexpr uint32_t kUnit = 2048;                 // a drain warp's block of 32 x
 // Such blocks that a drain warp has under way after the CTA's last tile.  With one alone each store waited
 // for the one before to be read.
 constexpr uint32_t kUnits = 6;
+constexpr uint32_t kSplitUnits = 4;              // of a split tile's block: its four stores
 constexpr uint32_t kBand = 8;                    // rows of tiles walked together
 constexpr int kCols = 64;                        // of a drain warp
+
+constexpr uint32_t kOrthoSplits = 8;
 
 template <int kBN>
 constexpr int kDrain = 4 * kBN / kCols;          // drain warps
@@ -53,6 +56,7 @@ constexpr int kDrain = 4 * kBN / kCols;          // drain warps
 // the product kernels: 128 x 56 + 512 x 104 <= 640 x 96.
 template <int kBN>
 constexpr int kOrthoThreads = (kDrain<kBN> + (kBN == 256 ? 4 : 2)) * 32;
+static_assert(kDrain<128> * kSplitUnits * kUnit <= kStageBytes && kSplitUnits < kUnits);
 static_assert(kDrain<256> * kUnits * kUnit <= kRing * kStageBytes && kRing * kStageBytes / kDrain<256> % kUnit == 0);
 template <int kBN>
 constexpr uint32_t kSmem = kRing * kStageBytes + kDrain<kBN> * kUnit;
@@ -75,7 +79,7 @@ struct Args {
     Op op[kMany ? kOrthoOps : 1];
     uint32_t* done;                              // [items]
     unsigned int* err;
-    uint32_t ops, items, tiles;
+    uint32_t ops, items, tiles, splits;
     bool test_expire;
 };
 
@@ -163,17 +167,17 @@ struct Units {
     }
 };
 
-// v += c * e: the warp's 32 rows from row0 of kCols columns from col on, of which v is this lane's row.  Four
+// v += c * e: the warp's 32 rows from row0 of kWidth columns from col on, of which v is this lane's row.  Four
 // lanes read 64 bytes of a row, and a unit hands the rows over (a row for each lane touched a line for
 // each: 3.3 us of the 9 that a product of 230 x 230 took).  kPlanes of a block's two are fetched at a
 // time, as registers allow.
-template <uint32_t kPlanes>
+template <uint32_t kPlanes, uint32_t kWidth>
 __device__ __forceinline__ void add_to(const Op& a, const uint16_t* e, float c, float* v, Units& units, uint32_t item, uint32_t row0,
                                        uint32_t col) {
     const uint32_t lane = threadIdx.x % 32, r0 = lane / 4, j0 = lane % 4;
     const uint16_t* from = e + 2ull * item * a.plane + (row0 + r0) * a.ld + col + 8 * j0;
 #pragma unroll
-    for (uint32_t n = 0; n < kCols / 32 * 2; n += kPlanes) {
+    for (uint32_t n = 0; n < kWidth / 32 * 2; n += kPlanes) {
         const uint32_t h = n / 2;
         uint4 q[kPlanes][4];
         const bool in = col + 32 * h + 8 * j0 < a.cols;
@@ -240,9 +244,40 @@ __device__ __forceinline__ void finish(const CUtensorMap* out, float* v, Units& 
     }
 }
 
-template <int kCtas, int kBN, bool kMany>
+// A split tile's sums: this warp's to the CTA's shared memory, as 32 x 32 blocks of fp32 (128-byte rows, see
+// unit_at); block b is of rows b / 4 * 32 and columns b % 4 * 32 of the tile.
+__device__ __forceinline__ void put_sums(uint32_t base, const float (&acc)[kCols], uint32_t quad, uint32_t part) {
+    const uint32_t lane = threadIdx.x % 32;
+#pragma unroll
+    for (uint32_t i = 0; i < kCols; i += 4)
+        st_shared4(base + (quad * 4 + part * 2 + i / 32) * 4096 + unit_at(lane, i % 32 / 4), acc[i], acc[i + 1], acc[i + 2],
+                   acc[i + 3]);
+}
+
+// The blocks that this CTA finishes, 16 / splits of them, summed over the cluster in rank order, to `to`.
+__device__ __forceinline__ void sum_blocks(uint32_t base, uint32_t to, uint32_t rank, uint32_t splits) {
+    const uint32_t first = rank * (16 / splits) * 4096, bytes = 16 / splits * 4096;
+    for (uint32_t at = threadIdx.x * 16; at < bytes; at += kDrain<128> * 32 * 16) {
+        float4 v = ld_part(base + first + at, 0, splits);
+#pragma unroll 8
+        for (uint32_t q = 1; q < splits; ++q) {
+            const float4 t = ld_part(base + first + at, q, splits);
+            v.x += t.x;
+            v.y += t.y;
+            v.z += t.z;
+            v.w += t.w;
+        }
+        st_shared4(to + at, v.x, v.y, v.z, v.w);
+    }
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(kDrain<128> * 32) : "memory");
+}
+
+// kSplit: a cluster of a.splits CTAs has one tile, and each a part of its blocks of terms.  The sums
+// meet over distributed shared memory, and each CTA finishes a part of the tile.
+template <int kCtas, int kBN, bool kMany, bool kSplit>
 __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(const __grid_constant__ Args<kMany> a) {
     static_assert(kBN / kCtas == 128, "128 rows of either operand per CTA");
+    static_assert(!kSplit || (kCtas == 1 && !kMany), "single SMs, one product");
     constexpr int kWarps = kDrain<kBN>, kLoadWarp = kWarps, kMmaWarp = kWarps + 1;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ uint64_t bars[2 * kRing + 4];
@@ -252,6 +287,10 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
     const uint32_t warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0, gone = smem_addr(&gone_flag);
     const bool leader = rank == 0;
+    const uint32_t splits = kSplit ? a.splits : 1, part_rank = kSplit ? cluster_rank() : 0, ctas = kSplit ? splits : kCtas;
+    // of a product's blocks, this CTA's
+    const auto from_block = [&](uint32_t kblocks) { return kSplit ? part_rank * kblocks / splits : 0; };
+    const auto to_block = [&](uint32_t kblocks) { return kSplit ? (part_rank + 1) * kblocks / splits : kblocks; };
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0 && lane == 0) {
@@ -273,11 +312,11 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
     if (warp == kMmaWarp) tmem_alloc<kCtas>(smem_addr(&tmem_slot), 2 * kBN);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (kCtas == 2) cluster_sync();
+    if (kCtas == 2 || kSplit) cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint32_t first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    const uint32_t first = blockIdx.x / ctas, step = gridDim.x / ctas;
     bool ok = true;                      // of this thread: no wait gave up
 
     if (warp >= kWarps) {
@@ -298,18 +337,18 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 const Op& o = tile.at(a, t);
                 const CUtensorMap *mp = &a.map[o.p], *mq = &a.map[o.q];
                 const bool pk = o.p_kmajor, qk = o.q_kmajor, single = o.single;
-                const uint32_t kblocks = o.kblocks;
+                const uint32_t end = to_block(o.kblocks);
                 const uint32_t p0 = tile.p * 128 * kCtas + rank * 128, q0 = tile.q * kBN + rank * 128, z = 2 * tile.item;
                 if constexpr (kMany) {
-                    if (!wait_done(a, o, tile.item, gone, kCtas)) {
+                    if (!wait_done(a, o, tile.item, gone, ctas)) {
                         ok = false;
                         break;
                     }
                     asm volatile("fence.proxy.async;" ::: "memory");
                 }
-                for (uint32_t kb = 0; kb < kblocks; ++kb) {
+                for (uint32_t kb = from_block(o.kblocks); kb < end; ++kb) {
                     const uint32_t bar = lead_full + 8 * s, at = base + s * kStageBytes;
-                    if (!bar_wait(empty + 8 * s, phase, gone, kCtas)) {
+                    if (!bar_wait(empty + 8 * s, phase, gone, ctas)) {
                         ok = false;
                         break;
                     }
@@ -336,11 +375,11 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                                        (128 * kCtas / 16) << 24;
                 const uint32_t step_p = o.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = o.q_kmajor ? 32 >> 4 : 2048 >> 4;
                 const uint32_t desc_p = operand_desc_lo(base, o.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, o.q_kmajor);
-                const uint32_t kblocks = o.kblocks, chunk = o.chunk;
+                const uint32_t kblocks = to_block(o.kblocks), chunk = o.chunk;
                 const bool single = o.single;
-                for (uint32_t kb = 0; ok && kb < kblocks; ++ch) {
+                for (uint32_t kb = from_block(o.kblocks); ok && kb < kblocks; ++ch) {
                     const uint32_t b = ch & 1;
-                    if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, kCtas)) {
+                    if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, ctas)) {
                         ok = false;
                         break;
                     }
@@ -349,7 +388,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                     bool add = false;
                     for (; kb < end; ++kb, ++it) {
                         const uint32_t dp = desc_p + (s * kStageBytes >> 4), dq = desc_q + (s * kStageBytes >> 4);
-                        if (a.test_expire || !bar_wait(full + 8 * s, phase, gone, kCtas)) {
+                        if (a.test_expire || !bar_wait(full + 8 * s, phase, gone, ctas)) {
                             ok = false;
                             break;
                         }
@@ -378,7 +417,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             if (!ok) {
                 // the loads in flight land before the CTA leaves
                 atomicOr(a.err, kErrWaitTimeout);
-                give_up(gone, kCtas);
+                give_up(gone, ctas);
                 for (uint32_t n = 0; n < kRing; ++n, ++it)
                     for (uint32_t i = 0; i < 1000 && !bar_try(full + 8 * (it % kRing), (it / kRing) & 1); ++i) {}
             }
@@ -394,13 +433,13 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         Walk tile;
         for (uint32_t t = first; ok && t < a.tiles; t += step) {
             const Op& o = kMany ? tile.at(a, t) : a.op[0];      // (the order that spills least)
-            const uint32_t chunks = (o.kblocks + o.chunk - 1) / o.chunk;
+            const uint32_t chunks = (to_block(o.kblocks) - from_block(o.kblocks) + o.chunk - 1) / o.chunk;
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
             for (uint32_t n = 0; n < chunks; ++n, ++ch) {
                 const uint32_t b = ch & 1;
-                if (!bar_wait(acc_full + 8 * b, (ch / 2) & 1, gone, kCtas)) {
+                if (!bar_wait(acc_full + 8 * b, (ch / 2) & 1, gone, ctas)) {
                     ok = false;
                     break;
                 }
@@ -419,13 +458,17 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             }
             ok = __all_sync(~0u, ok);
             if (!ok) break;
+            if constexpr (kSplit) {
+                put_sums(base, acc, quad, part);
+                break;
+            }
             if constexpr (!kMany) tile.at(a, t);
             const uint32_t row0 = tile.p * 128 * kCtas + rank * 128 + quad * 32, col0 = tile.q * kBN + part * kCols;
             const bool mirror = o.symmetric && tile.p != tile.q;
             if (row0 < o.rows && col0 < o.cols) {
                 if constexpr (kMany) {
                     // e1 and e2 are there, as the operands were: seen by every lane
-                    ok = __all_sync(~0u, wait_done(a, o, tile.item, gone, kCtas));
+                    ok = __all_sync(~0u, wait_done(a, o, tile.item, gone, ctas));
                     if (!ok) break;
                 }
                 // the last tile's results leave by way of the stages, which nothing needs any more
@@ -433,8 +476,8 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 if (t + step >= a.tiles) units = {base + warp * (kRing * kStageBytes / kWarps), kUnits, 0};
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) acc[i] *= o.c1;
-                if (o.e1) add_to<kBN == 128 ? 2 : 1>(o, o.e1, o.c2, acc, units, tile.item, row0, col0);
-                if (o.e2) add_to<kBN == 128 ? 2 : 1>(o, o.e2, o.c3, acc, units, tile.item, row0, col0);
+                if (o.e1) add_to<kBN == 128 ? 2 : 1, kCols>(o, o.e1, o.c2, acc, units, tile.item, row0, col0);
+                if (o.e2) add_to<kBN == 128 ? 2 : 1, kCols>(o, o.e2, o.c3, acc, units, tile.item, row0, col0);
                 finish(&a.map[o.out], acc, units, tile.item, row0, col0, mirror);
                 if (col0 + 32 < o.cols) finish(&a.map[o.out], acc + 32, units, tile.item, row0, col0 + 32, mirror);
             }
@@ -446,12 +489,41 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
         }
         if (lane == 0) {
             if (!ok) atomicOr(a.err, kErrWaitTimeout);
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!kSplit) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+    }
+    if constexpr (kSplit) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kWarps) {
+            const uint32_t sums = base + kStageBytes, own = 16 / splits;
+            sum_blocks(base, sums, part_rank, splits);
+            Walk tile;
+            const Op& o = tile.at(a, first);
+            const uint32_t block = part_rank * own + warp;
+            const uint32_t row0 = tile.p * 128 + block / 4 * 32, col0 = tile.q * 128 + block % 4 * 32;
+            if (warp < own && row0 < o.rows && col0 < o.cols) {
+                float v[32];
+#pragma unroll
+                for (uint32_t i = 0; i < 32; i += 4) {
+                    const float4 t = ld_part(sums + warp * 4096 + unit_at(lane, i / 4), 0, 1);
+                    v[i] = t.x * o.c1;
+                    v[i + 1] = t.y * o.c1;
+                    v[i + 2] = t.z * o.c1;
+                    v[i + 3] = t.w * o.c1;
+                }
+                Units units{base + 2 * kStageBytes + warp * kSplitUnits * kUnit, kSplitUnits, 0};
+                if (o.e1) add_to<2, 32>(o, o.e1, o.c2, v, units, tile.item, row0, col0);
+                if (o.e2) add_to<2, 32>(o, o.e2, o.c3, v, units, tile.item, row0, col0);
+                finish(&a.map[o.out], v, units, tile.item, row0, col0, o.symmetric && tile.p != tile.q);
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            }
+            __syncwarp();
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (kCtas == 2) cluster_sync();
+    if (kCtas == 2 || kSplit) cluster_sync();        // no CTA leaves while another may read its sums
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         tmem_free<kCtas>(tmem, 2 * kBN);
@@ -470,10 +542,11 @@ bool encode(CUtensorMap* map, const OrthoBuf& b, uint32_t items, uint32_t box_x,
 
 // A list waits within itself and is launched cooperatively; a single product overlaps its start with
 // its predecessor's end.
-template <int kCtas, int kBN, bool kMany>
+template <int kCtas, int kBN, bool kMany, bool kSplit>
 cudaError_t launch(const Args<kMany>& a, uint32_t room, cudaStream_t stream) {
+    const uint32_t ctas = kSplit ? a.splits : kCtas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.tiles < room ? a.tiles : room) * kCtas);
+    cfg.gridDim = dim3((kSplit || a.tiles < room ? a.tiles : room) * ctas);
     cfg.blockDim = dim3(kOrthoThreads<kBN>);
     cfg.dynamicSmemBytes = kSmem<kBN>;
     cfg.stream = stream;
@@ -486,11 +559,60 @@ cudaError_t launch(const Args<kMany>& a, uint32_t room, cudaStream_t stream) {
         at[0].val.programmaticStreamSerializationAllowed = 1;
     }
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = kCtas;
+    at[1].val.clusterDim.x = ctas;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = kCtas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, ortho_product_kernel<kCtas, kBN, kMany>, a);
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, ortho_product_kernel<kCtas, kBN, kMany, kSplit>, a);
+}
+
+uint32_t blocks_of(const OrthoProduct& p) {
+    const uint32_t block = (p.single ? 2 : 1) * kBK;
+    return (p.k + block - 1) / block;
+}
+
+uint32_t tiles_of(const OrthoProduct& p, uint32_t side) {
+    const uint32_t r = (p.out->rows + side - 1) / side, c = (p.out->cols + side - 1) / side;
+    return p.symmetric ? c * (c + 1) / 2 : r * c;
+}
+
+// The tile of a launch's products, the CTAs of a tile, and the time that this is thought to take.
+struct Plan {
+    bool pair;
+    uint32_t splits;
+    double cost;
+    uint32_t side() const { return pair ? 256 : 128; }
+};
+
+// Turns over the SMs, in microseconds.  A block of a pair takes 0.8 (two of one product 0.6), of a
+// single SM 0.42 or, with all SMs loading 64 KB for each, 0.58; a tile's end 1.5, and a product 3 more
+// before its first tile's data is there.
+//
+// One product whose tiles occupy a part of the SMs has a tile's blocks shared out over a cluster.
+// Launching the cluster and exchanging the sums takes 1.9, of eight CTAs 4 (which have to be free in
+// one part of the GPU): 512 x 512 bf16, 10 tiles of 8 blocks, 154 us unsplit, 143 by four, 169 by eight;
+// 128 x 11008 bf16, first products of one tile and 172 blocks, 299, 180 and 160; 100 x 10000 fp32
+// 711, 282 and 206.
+Plan plan_of(const OrthoProduct* p, uint32_t n, uint32_t items, bool many, uint32_t sms) {
+    const auto cost = [&](bool pair, uint32_t splits) {
+        double c = 0.0;
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint64_t t = static_cast<uint64_t>(tiles_of(p[i], pair ? 256 : 128)) * items, room = pair ? sms / 2 : sms;
+            const double busy = std::min(1.0, static_cast<double>(t * splits) / sms);
+            const double block = pair ? (p[i].single ? 0.6 : 0.8) : std::max(0.42, 0.58 * busy);
+            // items go on without one another: whole turns for one, parts of turns for many
+            const double turns = many ? std::max(1.0, static_cast<double>(t) / room) : static_cast<double>((t + room - 1) / room);
+            c += turns * (block * ((blocks_of(p[i]) + splits - 1) / splits) + 1.5) + 3.0 + (splits == 1 ? 0.0 : splits < 8 ? 1.9 : 4.0);
+        }
+        return c;
+    };
+    Plan best{true, 1, cost(true, 1)};
+    for (uint32_t splits = 1; splits <= (many ? 1 : kOrthoSplits); splits *= 2) {
+        if (splits > 1 && (blocks_of(*p) < splits || static_cast<uint64_t>(tiles_of(*p, 128)) * items * splits > sms)) break;
+        const double c = cost(false, splits);
+        if (c < best.cost) best = {false, splits, c};
+    }
+    return best;
 }
 
 template <bool kMany>
@@ -529,52 +651,33 @@ cudaError_t run(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* don
         o.rows = p[i].out->rows;
         o.cols = p[i].out->cols;
         o.single = p[i].single;
-        const uint32_t block = (p[i].single ? 2 : 1) * kBK;
-        o.kblocks = (p[i].k + block - 1) / block;
+        o.kblocks = blocks_of(p[i]);
         o.chunk = p[i].chunk;
         o.p_kmajor = p[i].p_kmajor;
         o.q_kmajor = p[i].q_kmajor;
         o.symmetric = p[i].symmetric;
     }
-    // The tile for all of them: turns over the SMs, in microseconds.  A block of a pair takes 0.8 (two of
-    // one product 0.6), of a single SM 0.42 or, with all SMs loading 64 KB for each, 0.58; a tile's end
-    // 1.5, and a product 3 more before its first tile's data is there.
     const uint32_t sms = static_cast<uint32_t>(shape.sms), pairs = sms / 2;
-    const auto tiles = [&](uint32_t size) {
-        a.tiles = 0;
-        for (uint32_t i = 0; i < n; ++i) {
-            Op& o = a.op[i];
-            o.tiles_p = (o.rows + size - 1) / size;
-            o.tiles_q = (o.cols + size - 1) / size;
-            o.per = o.symmetric ? o.tiles_q * (o.tiles_q + 1) / 2 : o.tiles_p * o.tiles_q;
-            o.first = a.tiles;
-            a.tiles += o.per * items;
-        }
-    };
-    const auto cost = [&](bool pair) {
-        double c = 0.0;
-        for (uint32_t i = 0; i < n; ++i) {
-            const Op& o = a.op[i];
-            const uint32_t t = o.per * items, room = pair ? pairs : sms;
-            const double busy = t < sms ? static_cast<double>(t) / sms : 1.0;
-            const double block = pair ? (o.single ? 0.6 : 0.8) : std::max(0.42, 0.58 * busy);
-            // items go on without one another: whole turns for one, parts of turns for many
-            const double turns = kMany ? std::max(1.0, static_cast<double>(t) / room) : (t + room - 1) / room;
-            c += turns * (block * o.kblocks + 1.5) + 3.0;
-        }
-        return c;
-    };
-    tiles(256);
-    const double by_pair = cost(true);
-    tiles(128);
-    const bool pair = by_pair <= cost(false);
-    if (pair) tiles(256);
+    const Plan plan = plan_of(p, n, items, kMany, sms);
+    const bool pair = plan.pair;
+    a.splits = plan.splits;
+    a.tiles = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+        Op& o = a.op[i];
+        o.tiles_p = (o.rows + plan.side() - 1) / plan.side();
+        o.tiles_q = (o.cols + plan.side() - 1) / plan.side();
+        o.per = tiles_of(p[i], plan.side());
+        o.first = a.tiles;
+        a.tiles += o.per * items;
+    }
     const uint32_t warps = pair ? 2 * kDrain<256> : kDrain<128>;
     for (uint32_t i = 0; kMany && i < n; ++i) {
         a.op[i].need = *count;
         *count += warps * a.op[i].per;
     }
-    return pair ? launch<2, 256, kMany>(a, pairs, stream) : launch<1, 128, kMany>(a, sms, stream);
+    if constexpr (!kMany)
+        if (a.splits > 1) return launch<1, 128, false, true>(a, sms, stream);
+    return pair ? launch<2, 256, kMany, false>(a, pairs, stream) : launch<1, 128, kMany, false>(a, sms, stream);
 }
 
 }  // namespace
@@ -587,10 +690,11 @@ cudaError_t prepare_ortho(OrthoShape* shape) {
     const auto room = [&](const void* kernel, uint32_t smem) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     };
-    room(reinterpret_cast<const void*>(ortho_product_kernel<2, 256, false>), kSmem<256>);
-    room(reinterpret_cast<const void*>(ortho_product_kernel<2, 256, true>), kSmem<256>);
-    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, false>), kSmem<128>);
-    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, true>), kSmem<128>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<2, 256, false, false>), kSmem<256>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<2, 256, true, false>), kSmem<256>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, false, false>), kSmem<128>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, true, false>), kSmem<128>);
+    room(reinterpret_cast<const void*>(ortho_product_kernel<1, 128, false, true>), kSmem<128>);
     if (e == cudaSuccess) e = tensor_map_encoder(&g_encode);
     shape->ready = e == cudaSuccess;
     return e;
@@ -607,15 +711,22 @@ cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
 cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
                                   const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream, uint64_t* launches) {
     if (n > kOrthoOps) return cudaErrorInvalidValue;
-    // one at a time: one matrix, or turns enough that a part of one does not count
-    uint64_t most = 0;
-    for (uint32_t i = 0; i < n; ++i)
-        most = std::max<uint64_t>(most, (p[i].out->rows + 255ull) / 256 * ((p[i].out->cols + 255ull) / 256) * items);
-    if (n > 1 && (items == 1 || most > 8ull * shape.sms / 2)) {
-        cudaError_t e = cudaSuccess;
-        for (uint32_t i = 0; i < n && e == cudaSuccess; ++i)
-            e = launch_ortho_products(p + i, 1, items, done, count, shape, err, test_expire, stream, launches);
-        return e;
+    // one at a time: one matrix; turns enough that a part of one does not count; or tiles so few that
+    // splitting them is worth more (5 of 10192 x 40 bf16 167 us so and 375 by the list)
+    const uint32_t sms = static_cast<uint32_t>(shape.sms);
+    if (n > 1) {
+        uint64_t most = 0;
+        double each = 0.0;
+        for (uint32_t i = 0; i < n; ++i) {
+            most = std::max<uint64_t>(most, (p[i].out->rows + 255ull) / 256 * ((p[i].out->cols + 255ull) / 256) * items);
+            each += plan_of(p + i, 1, items, false, sms).cost;
+        }
+        if (items == 1 || most > 8ull * sms / 2 || each < plan_of(p, n, items, true, sms).cost) {
+            cudaError_t e = cudaSuccess;
+            for (uint32_t i = 0; i < n && e == cudaSuccess; ++i)
+                e = launch_ortho_products(p + i, 1, items, done, count, shape, err, test_expire, stream, launches);
+            return e;
+        }
     }
     *launches += 1;
     return n == 1 ? run<false>(p, n, items, done, count, shape, err, test_expire, stream)
