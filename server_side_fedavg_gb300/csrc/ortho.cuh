@@ -69,7 +69,7 @@ struct OrthoSmall {
     uint32_t steps, parts;                    // in so many segments, the first ones longer by one at most
     float a, b, c;
 };
-bool ortho_small_fits(uint32_t rows, uint32_t cols);
+bool ortho_small_fits(uint64_t items, uint32_t rows, uint32_t cols);
 cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall& s, cudaStream_t stream);
 
 uint32_t ortho_blocks(uint32_t items, uint32_t rows, uint32_t cols, uint32_t sms);

@@ -23,9 +23,10 @@ constexpr uint32_t kSmallThreads = 256, kSmallWarps = kSmallThreads / 32, kSmall
 // fill the SMs twice.  What every CTA does for itself counts: one of 16 x 4096 bf16 takes 17 us with
 // runs of 512 and 25 with 1024; 128 take 98 and 79 us.
 constexpr uint32_t kSmallRun = 512, kManyRun = 1024, kMany = 304;
-// Sides above 32, an SM's registers to a CTA: 128 rows while the SMs (of which whole clusters of eight
-// find 14 to 16 places) hold all clusters at once, else 256, or 512.  1 x 64 x 1024 fp32 71 us in runs of
-// 128 and 92 of 256, 16 x 48 x 1000 bf16 141 and 93, 300 x 48 x 700 809 in runs of 256 and 520 of 512.
+// Sides above 32, an SM's registers to a CTA: 128 rows, or 256, while the SMs (of which whole clusters of
+// eight find 14 to 16 places) hold all clusters at once.  1 x 64 x 1024 fp32 71 us in runs of 128 and 92 of
+// 256, 16 x 48 x 1000 bf16 141 and 93.  Others are left to the tensor cores: 1 x 64 x 1024 117 us there, 1 x
+// 33 x 3000 bf16 119 and 133 here, 16 x 48 x 1000 124, 4 x 64 x 4096 125 and 164, 300 x 48 x 700 328 and 520.
 constexpr uint32_t kRun64 = 128, kMany64 = 112;
 constexpr uint32_t kSmallMost = 226 * 1024;    // bytes of shared memory
 constexpr uint32_t kSmallAhead = 4;            // pieces of eight elements whose loads a thread has in flight
@@ -419,25 +420,23 @@ uint32_t side(uint32_t m) { return m <= 8 ? 8 : m <= 16 ? 16 : m <= 32 ? 32 : 64
 
 uint32_t fixed(uint32_t m) { return m <= 8 ? kFixed<8> : m <= 16 ? kFixed<16> : m <= 32 ? kFixed<32> : kFixed<64>; }
 
-// CTAs of a cluster (a power of two), and rows of each; shared memory of a CTA.
-uint64_t split(uint32_t m, uint32_t n, uint32_t items, uint32_t* ctas, uint32_t* run) {
+// CTAs of a cluster (a power of two), and rows of each; false where the matrices are not for this kernel.
+bool split(uint32_t m, uint32_t n, uint64_t items, uint32_t* ctas, uint32_t* run) {
+    if (m > 64) return false;
     const auto fill = [&](uint32_t rows) {
         *ctas = 1;
         while (*ctas < kSmallCtas && *ctas * rows < n) *ctas *= 2;
         *run = ((n + *ctas - 1) / *ctas + 7) / 8 * 8;
-        return static_cast<uint64_t>(*run) * (side(m) + 4) * 4 + fixed(m);
+        return static_cast<uint64_t>(*run) * (side(m) + 4) * 4 + fixed(m) <= kSmallMost;
     };
     if (side(m) == 64) {
-        for (const uint32_t rows : {kRun64, 2 * kRun64}) {
-            const uint64_t bytes = fill(rows);
-            if (static_cast<uint64_t>(items) * *ctas <= kMany64) return bytes;
-        }
-        return fill(4 * kRun64);
+        for (const uint32_t rows : {kRun64, 2 * kRun64})
+            if (fill(rows) && *run <= rows && items * *ctas <= kMany64) return true;
+        return false;
     }
-    const uint64_t few = fill(kSmallRun);
-    if (static_cast<uint64_t>(items) * *ctas <= kMany) return few;
-    const uint64_t many = fill(kManyRun);
-    return many <= kSmallMost ? many : fill(kSmallRun);
+    const bool few = fill(kSmallRun);
+    if (items * *ctas <= kMany || !few) return few;
+    return fill(kManyRun) || fill(kSmallRun);
 }
 
 template <int kM>
@@ -464,10 +463,9 @@ cudaError_t launch(SmallArgs a, cudaStream_t stream) {
 
 }  // namespace
 
-bool ortho_small_fits(uint32_t rows, uint32_t cols) {
-    const uint32_t m = std::min(rows, cols), n = std::max(rows, cols);
+bool ortho_small_fits(uint64_t items, uint32_t rows, uint32_t cols) {
     uint32_t ctas, run;
-    return m <= 64 && split(m, n, 1, &ctas, &run) <= kSmallMost;
+    return split(std::min(rows, cols), std::max(rows, cols), items, &ctas, &run);
 }
 
 cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall& s, cudaStream_t stream) {

@@ -183,7 +183,7 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
     const uint32_t rows = static_cast<uint32_t>(p.rows), cols = static_cast<uint32_t>(p.cols);
     const Sizes z{rows, cols, std::min(rows, cols), std::max(rows, cols), rows <= cols};
     const std::vector<uint32_t> parts = segments(p.steps, z, p.dtype_out == FA_BF16);
-    const bool small = fa::ortho_small_fits(rows, cols);
+    const bool small = fa::ortho_small_fits(p.count, rows, cols);
     uint32_t longest = 0;
     for (uint32_t v : parts) longest = std::max(longest, v);
     // A segment of one holds A and P, longer ones up to seven squares.

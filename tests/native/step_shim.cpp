@@ -63,7 +63,7 @@ cudaError_t launch_ortho_norm(const OrthoEnds& e, cudaStream_t) {
 }
 cudaError_t launch_ortho_scale(const OrthoEnds&, cudaStream_t) { return call(); }
 cudaError_t launch_ortho_finish(const OrthoEnds&, cudaStream_t) { return call(); }
-bool ortho_small_fits(uint32_t rows, uint32_t cols) { return rows <= 32 || cols <= 32; }
+bool ortho_small_fits(uint64_t, uint32_t rows, uint32_t cols) { return rows <= 32 || cols <= 32; }
 cudaError_t launch_ortho_small(const OrthoEnds& e, const OrthoSmall&, cudaStream_t) {
     seen.ends = e;
     ++seen.small;

@@ -83,6 +83,21 @@ def test_sizes(work, count, rows, cols, din, dout):
     near(out, iterate(u, 5, QUINTIC, 1e-7), 1.0, None, dout, 5)
 
 
+@pytest.mark.parametrize("count,rows,cols", [(1, 100, 10007), (1, 9000, 40), (1, 130, 900), (1, 300, 1500), (3, 65, 2600), (5, 3333, 70),
+                                             (1, 512, 512), (1, 700, 4100), (40, 64, 4096), (12, 130, 260)])
+@pytest.mark.parametrize("din,dout", [("f32", "f32"), ("bf16", "bf16")])
+def test_few_tiles(work, count, rows, cols, din, dout):
+    """Products of few tiles, whose sums are shared out; momentum and weight beside them; the same bits twice."""
+    u, mom = make(count, rows, cols, din, 31), make(count, rows, cols, "f32", 32)
+    weight = (torch.randn((count, rows, cols), device="cuda") * 0.02).to(T[dout])
+    outs = [torch.full((count, rows, cols), 7.0, device="cuda", dtype=T[dout]) for _ in range(2)]
+    for out in outs:
+        fa.fa_orthogonalise(work, count, rows, cols, u, out, din, dout, momentum=mom, mu=0.5, residual=weight, alpha=-0.1)
+    fa.fa_work_sync(work)
+    near(outs[0], iterate(0.5 * mom.double() + u.double(), 5, QUINTIC, 1e-7), -0.1, weight.double(), dout, 5)
+    assert torch.equal(outs[0], outs[1])
+
+
 @pytest.mark.parametrize("rows,cols", [(96, 96), (96, 200), (200, 40)])
 @pytest.mark.parametrize("steps", [0, 1, 2, 3, 4, 6, 7])
 def test_steps(work, rows, cols, steps):
