@@ -494,8 +494,9 @@ const char* fa_last_error(const fa_ctx* ctx);
  * capturing); replays use the workspace of the time of the capture (kept until
  * fa_work_close), so they and direct calls on the handle must be ordered by the caller.
  * FA_TEST_WAIT_EXPIRES (the test aid above, in fa_work_opts.flags) makes the first data wait
- * of every tensor-core product (those of fa_orthogonalise among them) give up at once: its outputs are invalid and fa_work_sync
- * returns FA_ERR_INTERNAL; the kernel waits (bounded) for its own loads and ends.
+ * of every tensor-core product (those of fa_orthogonalise among them) give up at once: its
+ * outputs are invalid and fa_work_sync returns FA_ERR_INTERNAL; the kernel waits (bounded) for
+ * its own loads and ends.
  */
 typedef struct fa_work fa_work;   /* opaque; owned by the library */
 
@@ -848,7 +849,8 @@ typedef struct {
  * overlap), FA_ERR_DTYPE, FA_ERR_RANGE (sizes, steps, strides, coefficients, outputs whose own rows
  * overlap), FA_ERR_STATE (workspace growth while capturing), FA_ERR_NOMEM, FA_ERR_CUDA.  The
  * workspace takes up to 1 GiB, or what one matrix needs where that is more: 8 bytes an element, and
- * 8 (square) or 28 (else) for each of the short side's square. */
+ * 8 (square, or an fp32 result) or 28 (else) for each of the short side's square; a short side of
+ * up to 64 may need none. */
 fa_status fa_orthogonalise(fa_work* w, const fa_orthogonalise_args* args, void* stream);
 
 #ifdef __cplusplus

@@ -39,6 +39,8 @@ struct OrthoShape {
 
 cudaError_t prepare_ortho(OrthoShape* shape);
 cudaError_t map_ortho(OrthoBuf* b, uint32_t items);
+// What a list of products is thought to take, in microseconds.
+double ortho_cost(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t sms);
 // n <= kOrthoOps products one after the other, of `items` items each.  done: [items], counts of what
 // is done of an item, zero before its first product; *count: what they are when these begin, and then
 // when they are done.

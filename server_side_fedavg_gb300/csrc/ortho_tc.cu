@@ -9,7 +9,7 @@
 //
 // A CTA's tile is 128 rows of P (TMEM lanes) by kBN rows of Q (TMEM columns); with kCtas == 2 a
 // pair of SMs has 256 by 256 (cta_group::2).  The tensor cores' fp32 sum truncates, so it is
-// emptied every 4 blocks of 64 terms into registers, which round to nearest; TMEM has two such
+// emptied every few blocks of 64 terms into registers, which round to nearest; TMEM has two such
 // accumulators.  The last emptying leaves the tile in registers, from where it is finished: the
 // accumulators are free for the next tile meanwhile.
 //
@@ -23,8 +23,9 @@
 // clusters are resident (a cooperative launch), and a tile waits for earlier ones alone, so that the
 // first that is not done can always go on.  Where the items have a few turns of tiles that fills each
 // product's last turn with the next one's tiles: 24 of 1024 x 1024 bf16, 240 and 384 tiles over 76
-// pairs, take 1.25 ms so and 1.39 with a launch for each product.  One matrix gains nothing (4096 x
-// 4096 fp32 2.98 ms so, 2.85 by launches, each with the tiles that suit it), and is done by launches.
+// pairs, take 1.17 ms so and 1.34 with a launch for each product.  One matrix gains nothing (4096 x
+// 4096 fp32 2.86 ms both ways, 512 x 512 bf16 183 us so and 173 by launches, each with the tiles that suit
+// it), and is done by launches.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -708,25 +709,40 @@ cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
                : cudaErrorInvalidValue;
 }
 
+// Whether a list is launched one at a time: one matrix; turns enough that a part of one does not count; or
+// tiles so few that splitting them is worth more (5 of 10192 x 40 bf16 167 us so and 375 by the list).
+// *cost: the time.
+static bool one_by_one(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t sms, double* cost) {
+    uint64_t most = 0;
+    double each = 0.0;
+    for (uint32_t i = 0; i < n; ++i) {
+        most = std::max<uint64_t>(most, (p[i].out->rows + 255ull) / 256 * ((p[i].out->cols + 255ull) / 256) * items);
+        each += plan_of(p + i, 1, items, false, sms).cost;
+    }
+    const double list = n > 1 ? plan_of(p, n, items, true, sms).cost : each;
+    const bool so = n == 1 || items == 1 || most > 8ull * sms / 2 || each < list;
+    *cost = so ? each : list;
+    return so;
+}
+
+double ortho_cost(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t sms) {
+    double c = 0.0, part;
+    for (uint32_t at = 0; at < n; at += kOrthoOps) {
+        one_by_one(p + at, std::min(kOrthoOps, n - at), items, sms, &part);
+        c += part;
+    }
+    return c;
+}
+
 cudaError_t launch_ortho_products(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* done, uint32_t* count,
                                   const OrthoShape& shape, unsigned int* err, bool test_expire, cudaStream_t stream, uint64_t* launches) {
     if (n > kOrthoOps) return cudaErrorInvalidValue;
-    // one at a time: one matrix; turns enough that a part of one does not count; or tiles so few that
-    // splitting them is worth more (5 of 10192 x 40 bf16 167 us so and 375 by the list)
-    const uint32_t sms = static_cast<uint32_t>(shape.sms);
-    if (n > 1) {
-        uint64_t most = 0;
-        double each = 0.0;
-        for (uint32_t i = 0; i < n; ++i) {
-            most = std::max<uint64_t>(most, (p[i].out->rows + 255ull) / 256 * ((p[i].out->cols + 255ull) / 256) * items);
-            each += plan_of(p + i, 1, items, false, sms).cost;
-        }
-        if (items == 1 || most > 8ull * sms / 2 || each < plan_of(p, n, items, true, sms).cost) {
-            cudaError_t e = cudaSuccess;
-            for (uint32_t i = 0; i < n && e == cudaSuccess; ++i)
-                e = launch_ortho_products(p + i, 1, items, done, count, shape, err, test_expire, stream, launches);
-            return e;
-        }
+    double cost;
+    if (n > 1 && one_by_one(p, n, items, static_cast<uint32_t>(shape.sms), &cost)) {
+        cudaError_t e = cudaSuccess;
+        for (uint32_t i = 0; i < n && e == cudaSuccess; ++i)
+            e = launch_ortho_products(p + i, 1, items, done, count, shape, err, test_expire, stream, launches);
+        return e;
     }
     *launches += 1;
     return n == 1 ? run<false>(p, n, items, done, count, shape, err, test_expire, stream)

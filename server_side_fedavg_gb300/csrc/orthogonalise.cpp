@@ -47,15 +47,13 @@ struct Sizes {
 constexpr double kMostSingular = 4.0;
 constexpr int kSquares = 7;          // m x m matrices of the longest segment
 
-// The steps in segments of up to three.  Within one, everything is a polynomial in A = X X^T: with
-// P_j = b A_j + c A_j^2, the product of the (a + P_j) is kept as q + Q, A_{j+1} = (a + P_j)^2 A_j,
-// and X is read by two products in all instead of two per step.  Where X is square that saves
-// nothing: segments of one, which are the iteration as it stands.  An error in A grows with the
-// square of what X's own does (12 per step), so after three steps A is formed anew: simulated in
-// fp64 with fp16 pairs, 5 steps in one segment are off by up to 2.7e-5 on an update with a few
-// strong directions, 3 + 2 by 1.1e-6, 1 + 1 + 1 + 1 + 1 by 1.4e-6.
-std::vector<uint32_t> segments(uint32_t steps, const Sizes& z, bool bf16) {
-    const bool joined = bf16 && z.n * 5ull >= z.m * 6ull;
+// The steps in segments: of one, which are the iteration as it stands, or (joined) of up to three.
+// Within a longer one everything is a polynomial in A = X X^T: with P_j = b A_j + c A_j^2, the product of
+// the (a + P_j) is kept as q + Q, A_{j+1} = (a + P_j)^2 A_j, and X is read by two products in all instead
+// of two per step.  An error in A grows with the square of what X's own does (12 per step), so after
+// three steps A is formed anew: simulated in fp64 with fp16 pairs, 5 steps in one segment are off by up to
+// 2.7e-5 on an update with a few strong directions, 3 + 2 by 1.1e-6, 1 + 1 + 1 + 1 + 1 by 1.4e-6.
+std::vector<uint32_t> segments(uint32_t steps, bool joined) {
     const uint32_t parts = joined ? (steps + 2) / 3 : steps;
     std::vector<uint32_t> s;
     for (uint32_t left = steps, n = parts; n > 0; --n) {
@@ -94,13 +92,26 @@ struct Run {
         list.push_back(p);
     }
 
+    // The whole list of products; where X is then.
+    Held products(const std::vector<uint32_t>& parts, const std::vector<double>& top) {
+        list.clear();
+        Held X;
+        X.set(&x[0], 1.0);
+        uint32_t steps = 0;
+        for (uint32_t n : parts) {
+            steps += n;
+            segment(n, X, top[steps], steps + 1 == top.size());
+        }
+        return X;
+    }
+
     // `steps` steps from X, which is replaced; `next` bounds its singular values then.
     void segment(uint32_t steps, Held& X, double next, bool last) {
         // The last step towards a bf16 result takes one product of three, the hi terms' (11 bits), where
         // it is a segment of its own.  What that costs is not multiplied by later steps: measured against
         // fp64, 2.0e-3 of a square result in place of 1.7e-3, its own rounding.  (In a longer segment q X
-        // and Q X are several times the result and cancel: 3.1e-3 to 4.9e-3.)  24 of 1024 x 1024 take 1.41
-        // ms, all in full 1.51.
+        // and Q X are several times the result and cancel: 3.1e-3 to 4.9e-3.)  24 of 1024 x 1024 take 1.17
+        // ms, all in full 1.25.
         single = last && bf16 && steps == 1;
         int used = 0;
         const auto square = [&](double bound) {
@@ -182,33 +193,58 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
 
     const uint32_t rows = static_cast<uint32_t>(p.rows), cols = static_cast<uint32_t>(p.cols);
     const Sizes z{rows, cols, std::min(rows, cols), std::max(rows, cols), rows <= cols};
-    const std::vector<uint32_t> parts = segments(p.steps, z, p.dtype_out == FA_BF16);
     const bool small = fa::ortho_small_fits(p.count, rows, cols);
+    Run run{};
+    run.z = z;
+    run.bf16 = p.dtype_out == FA_BF16;
+    // blocks that the tensor cores' truncating sum takes before it is emptied.  bf16 results round more than
+    // 16 cost; fp32 ones lose half a digit at small sizes with 4, where emptying is cheap (1024 x 1024 190
+    // us, with 4 187), 4096 x 4096 takes 2.86 ms with 4 and 2.76 with 16.
+    run.chunk = run.bf16 ? 16 : z.m <= 512 ? 1 : z.m <= 1024 ? 2 : 4;
+    run.a = p.a;
+    run.b = p.b;
+    run.c = p.c;
+    for (fa::OrthoBuf& b : run.x) {
+        b.rows = rows;
+        b.cols = cols;
+        b.ld = (cols + 7ull) / 8 * 8;
+    }
+    for (fa::OrthoBuf& b : run.sq) {
+        b.rows = b.cols = z.m;
+        b.ld = (z.m + 7ull) / 8 * 8;
+    }
+    // Towards a bf16 result steps are joined where that takes less time, by the products' cost model: 11008 x
+    // 4096 4.20 ms joined, 5.21 as they stand; 900 x 1120 225 and 185 us, 4 of 1000 x 1300 490 and 457.
+    // (fp32 results were 2 to 5 times further off when joined.)
+    std::vector<uint32_t> parts = segments(p.steps, false);
+    if (!small && run.bf16) {
+        const auto cost = [&](const std::vector<uint32_t>& of) {
+            run.products(of, top);
+            return fa::ortho_cost(run.list.data(), static_cast<uint32_t>(run.list.size()),
+                                  static_cast<uint32_t>(std::min<uint64_t>(p.count, 1024)), static_cast<uint32_t>(w->tc.sms));
+        };
+        const std::vector<uint32_t> joined = segments(p.steps, true);
+        if (joined.size() < parts.size() && cost(joined) < cost(parts)) parts = joined;
+    }
     uint32_t longest = 0;
     for (uint32_t v : parts) longest = std::max(longest, v);
     // A segment of one holds A and P, longer ones up to seven squares.
     const int squares = longest == 0 ? 0 : longest == 1 ? 2 : kSquares;
-    const uint64_t ldx = (cols + 7ull) / 8 * 8, ldm = (z.m + 7ull) / 8 * 8;
+    const uint64_t ldx = run.x[0].ld, ldm = run.sq[0].ld;
     const uint64_t each = 4 * ((longest ? 2 : 1) * rows * ldx + squares * z.m * ldm);
     // Matrices at one time: what fits 1 GiB of workspace, one at least.
     const uint32_t group = static_cast<uint32_t>(
         small ? std::min<uint64_t>(p.count, 1u << 20) : std::min<uint64_t>({p.count, std::max<uint64_t>(1, (1ull << 30) / each), 32768}));
     const bool cap = capturing(s);
-    Run run{};
     float3* part = nullptr;
     uint32_t* done = nullptr;
     const uint32_t blocks = fa::ortho_blocks(group, rows, cols, static_cast<uint32_t>(w->tc.sms));
     const auto carve = [&](Carve& c) {
         for (int i = 0; i < (longest ? 2 : 1); ++i) {
             run.x[i].p = static_cast<uint16_t*>(c.take(4ull * group * rows * ldx));
-            run.x[i].rows = rows;
-            run.x[i].cols = cols;
-            run.x[i].ld = ldx;
         }
         for (int i = 0; i < squares; ++i) {
             run.sq[i].p = static_cast<uint16_t*>(c.take(4ull * group * z.m * ldm));
-            run.sq[i].rows = run.sq[i].cols = z.m;
-            run.sq[i].ld = ldm;
         }
         part = static_cast<float3*>(c.take(sizeof(float3) * group * blocks));
         done = static_cast<uint32_t*>(c.take(sizeof(uint32_t) * group));
@@ -227,12 +263,6 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
         for (int i = 0; i < (longest ? 2 : 1); ++i) FW_CUDA(w, fa::map_ortho(&run.x[i], group));
         for (int i = 0; i < squares; ++i) FW_CUDA(w, fa::map_ortho(&run.sq[i], group));
     }
-    run.z = z;
-    run.bf16 = p.dtype_out == FA_BF16;
-    run.chunk = p.dtype_out == FA_BF16 ? 16 : z.m <= 512 ? 1 : z.m <= 1024 ? 2 : 4;
-    run.a = p.a;
-    run.b = p.b;
-    run.c = p.c;
     fa::OrthoEnds e{};
     const auto mat = [&](const void* t, int32_t dt, uint64_t ld, uint64_t given) {
         return fa::OrthoMat{t, rows > 1 ? ld : 0, p.count > 1 ? step(ld, given) : 0, code_of(dt)};
@@ -260,18 +290,12 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
             e.alpha = static_cast<float>(p.alpha);
             r = launched(w, fa::launch_ortho_small(e, steps, s), "weight step");
         } else {
-            Held X;
-            X.set(&run.x[0], 1.0);
             e.x = run.x[0].p;
-            e.shift = X.shift;
+            e.shift = shift_of(1.0);
             r = launched(w, fa::launch_ortho_norm(e, s), "update's norm");
             if (r == FA_OK) r = launched(w, fa::launch_ortho_scale(e, s), "update's scale");
-            run.list.clear();
-            uint32_t steps = 0, counted = 0;
-            for (uint32_t n : parts) {
-                steps += n;
-                run.segment(n, X, top[steps], steps == p.steps);
-            }
+            const Held X = run.products(parts, top);
+            uint32_t counted = 0;
             const size_t all = run.list.size();
             for (size_t at = 0; r == FA_OK && at < all; at += fa::kOrthoOps) {
                 const cudaError_t ce = fa::launch_ortho_products(

@@ -50,6 +50,12 @@ cudaError_t prepare_ortho(OrthoShape* shape) {
     return cudaSuccess;
 }
 cudaError_t map_ortho(OrthoBuf*, uint32_t) { return cudaSuccess; }
+// by their operations
+double ortho_cost(const OrthoProduct* p, uint32_t n, uint32_t, uint32_t) {
+    double c = 0.0;
+    for (uint32_t i = 0; i < n; ++i) c += (p[i].symmetric ? 0.5 : 1.0) * p[i].out->rows * p[i].out->cols * p[i].k;
+    return c;
+}
 cudaError_t launch_ortho_products(const OrthoProduct*, uint32_t n, uint32_t, uint32_t*, uint32_t*, const OrthoShape&, unsigned int*, bool,
                                   cudaStream_t, uint64_t* launches) {
     seen.products += n;
