@@ -7,6 +7,9 @@
 // are then kM x kM products in shared memory, which every CTA does for itself, and x_j <- (q + Q) x_j
 // closes a segment of up to three steps (see the host's `segments`).
 //
+// What bounds it: the chain of phases.  10 x 256 16 us, 128 of 16 x 4096 bf16 with momentum 80 us (100 MB, 15
+// us of HBM): two turns of CTAs, each 11 us loading, 24 in two segments, 4 storing.
+//
 // Rows are kM + 4 floats apart: lanes that read 16 bytes of rows next to each other then meet no
 // bank conflict.
 #include <algorithm>
