@@ -14,6 +14,7 @@ struct Dim {
 
 struct Grid {
     const void* p = nullptr;
+    Dim given[3] = {{1, 0}, {1, 0}, {1, 0}};   // as the caller names them
     Dim dim[3] = {{1, 0}, {1, 0}, {1, 0}};     // by ascending stride, those of one element left out
     int dims = 0;
     uint64_t width = 0, size = 0;
@@ -21,7 +22,9 @@ struct Grid {
 
     Grid() = default;
     Grid(const void* at, uint64_t w, uint64_t elem, std::initializer_list<Dim> ds) : p(at), width(w), size(elem), empty(at == nullptr || w == 0) {
+        int n = 0;
         for (const Dim& d : ds) {
+            given[n++] = d;
             if (d.extent == 0) empty = true;
             if (d.extent > 1) dim[dims++] = d;
         }
@@ -62,10 +65,12 @@ struct Grid {
         if (i == dims && rows.stride >= w) return {p, rows.extent, w, rows.stride, size};
         return {p, 1, span(), span(), size};
     }
+    // Every element where the other has it: the strides are compared dimension by dimension, but for
+    // those of one element.  (Sorted ones would take a transposition of equal extents for the same.)
     bool same(const Grid& o) const {
-        if (p != o.p || dims != o.dims || width != o.width || size != o.size) return false;
-        for (int i = 0; i < dims; ++i)
-            if (dim[i].extent != o.dim[i].extent || dim[i].stride != o.dim[i].stride) return false;
+        if (p != o.p || width != o.width || size != o.size) return false;
+        for (int i = 0; i < 3; ++i)
+            if (given[i].extent != o.given[i].extent || (given[i].extent > 1 && given[i].stride != o.given[i].stride)) return false;
         return true;
     }
 };

@@ -185,3 +185,41 @@ def test_structs_have_the_headers_fields():
             kind, names = decl.replace("const ", "").replace("*", " ").split(None, 1)
             want += [(n.strip(), ctypes.c_void_p if pointer else ctype[kind]) for n in names.split(",")]
         assert list(getattr(fa, name)._fields_) == want, name
+
+
+def test_an_output_in_place_has_its_inputs_strides_dimension_by_dimension(step):
+    """Two dimensions of one extent whose strides are exchanged cover the same elements, each at
+    another place: the kernels would write what they still have to read."""
+    def taken(name, args):
+        step.L.ss_reset(0)
+        status = step.call(name, args)
+        assert (status == fa.FA_OK) == (step.L.ss_launches() > 0), name
+        return status
+
+    one = dict(batch=1, seq=4, qh=4, kh=0, k=None, ko=None, qo=FAR[0], qs=(0, 256, 64))
+    assert taken("fa_rotary", rotary(**one, qos=(0, 256, 64))) == fa.FA_OK
+    assert taken("fa_rotary", rotary(**one, qos=(0, 64, 256))) == ARG
+    batch = dict(batch=4, seq=4, qh=1, kh=0, k=None, ko=None, qo=FAR[0], qs=(256, 64, 64))
+    assert taken("fa_rotary", rotary(**batch, qos=(256, 64, 999))) == fa.FA_OK            # a single head: its stride is not used
+    assert taken("fa_rotary", rotary(**batch, qos=(64, 256, 64))) == ARG
+    # only q is where it was: what does not turn is still copied for k
+    assert taken("fa_rotary", rotary(r=32, qo=FAR[0])) == fa.FA_OK and step.L.ss_copies()
+    square = dict(n=4, P=4, ldx=32, sx=128, y=FAR[0])
+    assert taken("fa_group_norm", norm(**square, ldy=32, sy=128)) == fa.FA_OK
+    assert taken("fa_group_norm", norm(**square, ldy=128, sy=32)) == ARG
+    assert taken("fa_group_norm", norm(n=1, P=4, ldx=32, sx=128, y=FAR[0], ldy=32, sy=4096)) == fa.FA_OK    # a single sample
+    for over in (FAR[0], FAR[1]):
+        for lddx, step_dx, want in ((32, 128, fa.FA_OK), (128, 32, ARG)):
+            args = norm_backward(n=4, P=4, dx=over, ldx=32, ldd=32, lddx=lddx)
+            args.step_x = args.step_d = 128
+            args.step_dx = step_dx
+            assert taken("fa_group_norm_backward", args) == want
+    many = dict(count=100, rows=100, ldu=60, su=6000, out=FAR[0])
+    assert taken("fa_orthogonalise", ortho(**many, ldo=60, so=6000)) == fa.FA_OK
+    assert taken("fa_orthogonalise", ortho(**many, ldo=6000, so=60)) == ARG
+    far = dict(count=100, rows=100, ldm=60, sm=6000, m=FAR[2], mo=FAR[2])
+    assert taken("fa_orthogonalise", ortho(**far, ldmo=60, smo=6000)) == fa.FA_OK
+    assert taken("fa_orthogonalise", ortho(**far, ldmo=6000, smo=60)) == ARG
+    weight = dict(count=100, rows=100, res=FAR[4], ldr=60, sr=6000)
+    assert taken("fa_orthogonalise", ortho(**weight, ldo=60, so=6000)) == fa.FA_OK
+    assert taken("fa_orthogonalise", ortho(**weight, ldo=6000, so=60)) == ARG
