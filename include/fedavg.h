@@ -741,8 +741,9 @@ fa_status fa_rotary(fa_work* w, const fa_rotary_args* args, void* stream);
  *   xhat = (x - mean[i, g]) * rstd[i, g],   y = act(xhat * gamma[c] + beta[c])
  *
  * mean and the variance are over the sample's positions and the group's channels / groups
- * channels, rstd = 1 / sqrt(variance + eps).  Sums are fp32 of differences from a value of the
- * same channel, so an offset costs no digits; their order does not depend on the run. */
+ * channels, rstd = 1 / sqrt(variance + eps).  Sums are fp32 of differences from a reference that
+ * follows the mean, so neither an offset nor positions far from the others (a corner of
+ * background, an outlier) cost digits; their order does not depend on the run. */
 typedef struct {
     uint32_t size;             /* sizeof(fa_group_norm_args) */
     uint32_t flags;            /* 0 */

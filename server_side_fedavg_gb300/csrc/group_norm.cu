@@ -9,10 +9,11 @@
 // Two passes over the data: the statistics, then the result.  A thread keeps V channels (one
 // vector) and walks down positions, so that nothing of a channel is fetched twice; a CTA has a
 // run of a sample's positions.  The second pass walks its run backwards: what the first pass read
-// last is still in L2.  A channel's sums are taken of x less the channel's first value in the
-// sample, and means are kept as differences from the group's first such value until the end, so
-// that an offset far larger than the spread costs no digits; a run's channels, and then the runs,
-// are joined as (mean, sum of squares about it) pairs, in a fixed order.
+// last is still in L2.  A thread's sums are taken of x less a reference that follows the mean (see
+// Moments); threads, a run's channels, and then the runs, are joined as means and sums of squares about
+// them, in a fixed order, each time first to a common mean in fp32 and then as differences from
+// that, of which the statistics come.  So neither an offset far larger than the spread nor positions
+// unlike the others cost digits, and the mean is off by its own rounding alone.
 //
 // What bounds it: small samples, the launches (4 x 9216 x 64 fp32 10.9 us, 1 x 216 x 256 7.4); large ones
 // that the one kernel does not take, HBM, x read twice and the result written once: 2 x 128^3 x 32 bf16 in
@@ -66,14 +67,20 @@ __device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
     return static_cast<const T*>(t.p) + sample * t.step;
 }
 
-// f(vector of p0, vector of p1, position) for this thread's positions of [r0, r1), channels from c.
-template <bool kReverse, int kStreams, int V, typename T, typename F>
+// How many positions of [r0, r1) are this thread's.
+__device__ __forceinline__ uint32_t rows_mine(const Tile& t, uint32_t r0, uint32_t r1) {
+    return t.on && r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
+}
+
+// f(vector of p0, vector of p1, position) for this thread's positions of [r0, r1), channels from c;
+// after(positions so far) now and then.
+template <bool kReverse, int kStreams, int V, typename T, typename F, typename G>
 __device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t ld0, const T* p1, uint64_t ld1, uint32_t r0,
-                                          uint32_t r1, uint32_t c, F f) {
+                                          uint32_t r1, uint32_t c, F f, G after) {
     if (!t.on) return;
     // 64 bytes of either stream in flight per thread, and no more than eight positions
     constexpr uint32_t kU = sizeof(T) * V >= 16 ? 4 : 8;
-    const uint32_t mine = r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
+    const uint32_t mine = rows_mine(t, r0, r1);
     const auto row_of = [&](uint32_t i) { return r0 + t.row + (kReverse ? mine - 1 - i : i) * t.tall; };
     uint32_t i = 0;
     for (; i + kU <= mine; i += kU) {
@@ -85,20 +92,25 @@ __device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t l
         }
 #pragma unroll
         for (uint32_t u = 0; u < kU; ++u) f(q[u], p[u], row_of(i + u));
+        after(i + kU);
     }
     for (; i < mine; ++i) {
         const Vec<T, V> q = load_raw<T, V>(p0 + row_of(i) * ld0 + c);
         f(q, kStreams == 2 ? load_raw<T, V>(p1 + row_of(i) * ld1 + c) : q, row_of(i));
     }
 }
+template <bool kReverse, int kStreams, int V, typename T, typename F>
+__device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t ld0, const T* p1, uint64_t ld1, uint32_t r0,
+                                          uint32_t r1, uint32_t c, F f) {
+    over_rows<kReverse, kStreams, V>(t, p0, ld0, p1, ld1, r0, r1, c, f, [](uint32_t) {});
+}
 
 // ----------------------------------------------------------------- forward
-// part[sample][chunk][group] = (mean, sum of squares about it) over the chunk's positions, the mean
-// less ref[sample][group], the group's first value.
+// stat[sample][chunk][group] = (mean, as a sum of two; sum of squares about it) over the chunk's positions.
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *mean = sm, *sq = mean + a.channels, *from0 = sq + a.channels, *red = from0 + a.channels;
+    float *mean = sm, *sq = mean + a.channels, *base = sq + a.channels, *red = base + a.channels;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
@@ -108,26 +120,43 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(cons
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
             const Tile t(vectors, c0);
             const uint32_t c = (c0 + t.col) * V;
-            float s[2][V] = {}, from[V] = {};
-            if (t.on) widen(load_raw<T, V>(x + c), from);
-            float less[V];
+            Moments<V> o;
+            const uint32_t mine = rows_mine(t, r0, r1);
+            if (mine) {
+                float from[V];
+                widen(load_raw<T, V>(x + (r0 + t.row) * a.x.ld + c), from);
+                o.begin(from);
+            }
+            uint32_t next = 1;
+            over_rows<false, 1, V>(
+                t, x, a.x.ld, x, a.x.ld, r0, r1, c,
+                [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t) {
+                    float d[V];
+                    widen(q, d);
+                    o.step(d);
+                },
+                [&](uint32_t done) {
+                    if (done < next) return;
+                    o.move(static_cast<float>(done));
+                    next = 2 * done;
+                });
+            // the threads' common mean, then their sums about it
+            const float n = static_cast<float>(mine);
+            float m[1][V];
+            o.mean_part(n, count, m[0]);
+            sum_rows<1, V>(m, red, t);
+            if (t.row == 0)
 #pragma unroll
-            for (int i = 0; i < V; ++i) less[i] = -from[i];
-            over_rows<false, 1, V>(t, x, a.x.ld, x, a.x.ld, r0, r1, c, [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t) {
-                float d[V];
-                widen(q, d);
-                add(d, d, less);
-                add(s[0], s[0], d);
-                fma(s[1], d, d, s[1]);
-            });
-            sum_rows<2, V>(s, red, t);
+                for (int i = 0; i < V; ++i) base[c + i] = m[0][i];
+            __syncthreads();
+            if (t.on) o.about(n, base + c);
+            sum_rows<2, V>(o.s, red, t);
             if (t.row == 0)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float m = s[0][i] / count;
-                    mean[c + i] = m;
-                    from0[c + i] = from[i];
-                    sq[c + i] = fmaxf(s[1][i] - s[0][i] * m, 0.0f);
+                    const float d = o.s[0][i] / count;
+                    mean[c + i] = d;
+                    sq[c + i] = fmaxf(fmaf(-o.s[0][i], d, o.s[1][i]), 0.0f);
                 }
             __syncthreads();
         }
@@ -135,53 +164,61 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(cons
         const uint32_t lanes = lanes_for(per), sub = lane % lanes;
         for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
             const uint32_t g = g0 + lane / lanes, end = g < a.groups ? (g + 1) * per : 0;
-            const float ref = g < a.groups ? from0[g * per] : 0.0f;
-            float m = 0.0f, q = 0.0f;
+            const float all = static_cast<float>(per);
+            float hi = 0.0f, m = 0.0f, q = 0.0f;
+            for (uint32_t c = g * per + sub; c < end; c += lanes) hi += (base[c] + mean[c]) / all;
+            hi = lane_sum(hi, lanes);
             for (uint32_t c = g * per + sub; c < end; c += lanes) {
-                mean[c] += from0[c] - ref;
+                mean[c] += base[c] - hi;
                 m += mean[c];
             }
-            m = lane_sum(m, lanes) / static_cast<float>(per);
+            m = lane_sum(m, lanes) / all;
             for (uint32_t c = g * per + sub; c < end; c += lanes) {
                 const float d = mean[c] - m;
                 q += fmaf(count * d, d, sq[c]);
             }
             q = lane_sum(q, lanes);
-            if (sub == 0 && g < a.groups) {
-                a.part[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float2(m, q);
-                if (blockIdx.x == 0) a.ref[static_cast<uint64_t>(sample) * a.groups + g] = ref;
-            }
+            if (sub == 0 && g < a.groups)
+                a.stat[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float4(hi, m, q, 0.0f);
         }
         __syncthreads();
     }
 }
 
-// A sample's mean (less the reference) and 1 / sqrt(variance + eps) per group, from its chunks' parts, into shared memory.
-__device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, float* mean, float* rstd) {
+// A sample's mean, what its rounding to fp32 left, and 1 / sqrt(variance + eps) per group, from its chunks'
+// parts, into shared memory.
+__device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, float* mean, float* left, float* rstd) {
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, per = a.channels / a.groups;
     const uint32_t lanes = lanes_for(a.chunks), sub = lane % lanes;
     const float all = static_cast<float>(a.positions);
     const auto rows_of = [&](uint32_t i) { return static_cast<float>(min(a.rows, a.positions - i * a.rows)); };
     for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
         const uint32_t g = g0 + lane / lanes, end = g < a.groups ? a.chunks : 0;
-        const float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
-        float m = 0.0f, q = 0.0f;
-        float2 own = make_float2(0.0f, 0.0f);        // this lane's first: with few chunks its only one
+        const float4* part = a.stat + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
+        float hi = 0.0f, m = 0.0f, q = 0.0f;
+        float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);        // this lane's first: with few chunks its only one
         if (sub < end) own = part[static_cast<uint64_t>(sub) * a.groups];
-        if (sub < end) m = own.x * rows_of(sub);
+        const auto common = [&](float4 p, uint32_t i) { return (p.x + p.y) * (rows_of(i) / all); };
+        if (sub < end) hi = common(own, sub);
 #pragma unroll 4
-        for (uint32_t i = sub + lanes; i < end; i += lanes) m = fmaf(part[static_cast<uint64_t>(i) * a.groups].x, rows_of(i), m);
-        m = lane_sum(m, lanes) / all;
-        const auto square = [&](float2 p, uint32_t i) {
-            const float d = p.x - m;
-            return fmaf(rows_of(i) * static_cast<float>(per) * d, d, p.y);
+        for (uint32_t i = sub + lanes; i < end; i += lanes) hi += common(part[static_cast<uint64_t>(i) * a.groups], i);
+        hi = lane_sum(hi, lanes);
+        const auto rest = [&](float4 p, uint32_t i) { return ((p.x - hi) + p.y) * (rows_of(i) / all); };
+        if (sub < end) m = rest(own, sub);
+#pragma unroll 4
+        for (uint32_t i = sub + lanes; i < end; i += lanes) m += rest(part[static_cast<uint64_t>(i) * a.groups], i);
+        m = lane_sum(m, lanes);
+        const auto square = [&](float4 p, uint32_t i) {
+            const float d = ((p.x - hi) + p.y) - m;
+            return fmaf(rows_of(i) * static_cast<float>(per) * d, d, p.z);
         };
         if (sub < end) q = square(own, sub);
 #pragma unroll 4
         for (uint32_t i = sub + lanes; i < end; i += lanes) q += square(part[static_cast<uint64_t>(i) * a.groups], i);
         q = lane_sum(q, lanes) / (all * static_cast<float>(per));
         if (sub == 0 && g < a.groups) {
-            mean[g] = m;
+            mean[g] = hi + m;
+            left[g] = (hi - mean[g]) + m;
             rstd[g] = 1.0f / sqrtf(q + a.eps);
         }
     }
@@ -190,18 +227,17 @@ __device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, 
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_apply_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
-    float *mean = sm, *rstd = mean + a.groups, *ref = rstd + a.groups;
+    float *mean = sm, *rstd = mean + a.groups, *left = rstd + a.groups;
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
     const int act = a.act;
     for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
         const uint64_t first = static_cast<uint64_t>(sample) * a.groups;
-        for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) ref[g] = a.ref[first + g];
-        join_chunks(a, sample, mean, rstd);
+        join_chunks(a, sample, mean, left, rstd);
         __syncthreads();
         if (blockIdx.x == 0 && a.mean_out)
-            for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.mean_out[first + g] = ref[g] + mean[g];
+            for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.mean_out[first + g] = mean[g];
         if (blockIdx.x == 0 && a.rstd_out)
             for (uint32_t g = threadIdx.x; g < a.groups; g += kNormThreads) a.rstd_out[first + g] = rstd[g];
         const T* x = at<T>(a.x, sample);
@@ -209,15 +245,15 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_apply_kernel(con
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
             const Tile t(vectors, c0);
             const uint32_t c = (c0 + t.col) * V;
-            // y = act((x - ref) scale + shift): the mean, less the reference, is in the shift
+            // y = act((x - mean) scale + shift): what the mean's rounding left is in the shift
             float less[V] = {}, scale[V] = {}, shift[V] = {};
             if (t.on)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const uint32_t g = (c + i) / per;
-                    less[i] = -ref[g];
+                    less[i] = -mean[g];
                     scale[i] = rstd[g] * (a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f);
-                    shift[i] = fmaf(-mean[g], scale[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
+                    shift[i] = fmaf(-left[g], scale[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
                 }
             over_rows<true, 1, V>(t, x, a.x.ld, x, a.x.ld, r0, r1, c, [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t r) {
                 float v[V];

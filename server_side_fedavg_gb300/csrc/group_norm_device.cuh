@@ -174,6 +174,52 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A thread's sums over the positions of its run: s[0] of d = x - reference, s[1] of d^2, for each channel,
+// and how the variance comes from them without cancelling.  A run's squares about a point r are its squares
+// about its mean m and n (m - r)^2.  Where r is the mean of the first k positions, these have at least
+// k (m - r)^2 of the squares about m, so that the second part is at most n / k times the first, whatever
+// the values are.  The reference begins as the thread's first value and is moved to the mean so far
+// whenever the run has doubled: no sum is more than a few times what is kept of it.  (With one reference
+// for a run, its first value, one voxel 1000 spreads off left 3 digits of the variance.)
+template <int V>
+struct Moments {
+    float less[V] = {}, s[2][V] = {};                // less: the reference, negated
+    __device__ __forceinline__ void begin(const float (&x)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) less[i] = -x[i];
+    }
+    __device__ __forceinline__ void step(float (&x)[V]) {
+        add(x, x, less);
+        add(s[0], s[0], x);
+        fma(s[1], x, x, s[1]);
+    }
+    // to the mean of the n positions so far
+    __device__ __forceinline__ void move(float n) {
+        const float inv = 1.0f / n;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float to = less[i] - s[0][i] * inv, by = less[i] - to, rest = fmaf(-n, by, s[0][i]);
+            s[1][i] = fmaf(-by, s[0][i] + rest, s[1][i]);
+            s[0][i] = rest;
+            less[i] = to;
+        }
+    }
+    // this thread's part of the mean of `count` positions, n of them its own
+    __device__ __forceinline__ void mean_part(float n, float count, float (&to)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) to[i] = n > 0.0f ? fmaf(-less[i], n / count, s[0][i] / count) : 0.0f;
+    }
+    // the same sums about `base`
+    __device__ __forceinline__ void about(float n, const float* base) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float m = n > 0.0f ? s[0][i] / n : 0.0f, d = n > 0.0f ? (-less[i] - base[i]) + m : 0.0f;
+            s[1][i] = fmaf(n * d, d, fmaxf(fmaf(-s[0][i], m, s[1][i]), 0.0f));
+            s[0][i] = n * d;
+        }
+    }
+};
+
 // What a thread keeps of its channels: with h = x - mean, z = h scale + beta, scale = rstd gamma.
 template <int V>
 struct Channels {

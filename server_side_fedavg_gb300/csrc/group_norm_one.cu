@@ -95,35 +95,35 @@ __device__ __forceinline__ const T* at(const NormTensor& t, uint32_t sample) {
 
 // The threads' sums over the positions, for each channel, in its first thread.  Where lanes of a warp
 // share columns by a power of two, over these first, then over the warps in order.  Else four sums at a time over a tree.
-template <int V>
-__device__ __forceinline__ void over_positions(float (&s)[2][V], float* red, uint32_t vectors, uint32_t tall) {
+template <int N, int V>
+__device__ __forceinline__ void over_positions(float (&s)[N][V], float* red, uint32_t vectors, uint32_t tall) {
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, my_row = threadIdx.x / vectors;
-    if (vectors <= 32 && 32 % vectors == 0 && 2 * V * vectors <= 4 * 32) {
-        float v[2 * V];
+    if (vectors <= 32 && 32 % vectors == 0 && N * V * vectors <= 4 * 32) {
+        float v[N * V];
 #pragma unroll
-        for (int k = 0; k < 2 * V; ++k) v[k] = s[k / V][k % V];
+        for (int k = 0; k < N * V; ++k) v[k] = s[k / V][k % V];
         for (uint32_t o = 16; o >= vectors; o /= 2)
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
+            for (int k = 0; k < N * V; ++k) v[k] += __shfl_xor_sync(~0u, v[k], o);
         // [sum][warp][column]
         if (lane < vectors)
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) red[(k * kOneWarps + warp) * vectors + lane] = v[k];
+            for (int k = 0; k < N * V; ++k) red[(k * kOneWarps + warp) * vectors + lane] = v[k];
         sync_compute();
-        for (uint32_t i = threadIdx.x; i < 2 * V * vectors; i += kOneThreads) {
+        for (uint32_t i = threadIdx.x; i < N * V * vectors; i += kOneThreads) {
             float t = 0.0f;
 #pragma unroll
             for (uint32_t w = 0; w < kOneWarps; ++w) t += red[(i / vectors * kOneWarps + w) * vectors + i % vectors];
-            red[2 * V * kOneWarps * vectors + i] = t;
+            red[N * V * kOneWarps * vectors + i] = t;
         }
         sync_compute();
         if (threadIdx.x < vectors)
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) s[k / V][k % V] = red[2 * V * (kOneWarps * vectors) + k * vectors + threadIdx.x];
+            for (int k = 0; k < N * V; ++k) s[k / V][k % V] = red[N * V * (kOneWarps * vectors) + k * vectors + threadIdx.x];
         return;
     }
 #pragma unroll
-    for (int k0 = 0; k0 < 2 * V; k0 += 4) {
+    for (int k0 = 0; k0 < N * V; k0 += 4) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) red[k * kOneThreads + threadIdx.x] = s[(k0 + k) / V][(k0 + k) % V];
         sync_compute();
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
     __shared__ uint64_t bars[2 * kOneSlots];
     float* red = reinterpret_cast<float*>(dyn + a.slots * kOneStage);
     float *s0 = red + kOneRed, *s1 = s0 + a.channels;                      // of a channel
-    float *t0 = s1 + a.channels, *t1 = t0 + (kBackward ? a.channels : 0);          // gradients so far; forward: first values
-    float *g0 = t1 + a.channels, *g1 = g0 + a.groups, *ref = g1 + a.groups;
+    float *t0 = s1 + a.channels, *t1 = t0 + (kBackward ? a.channels : 0);          // gradients so far; forward: means
+    float *g0 = t1 + a.channels, *g1 = g0 + a.groups, *left = g1 + a.groups;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kOneSlots;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
 
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups;
     const uint32_t tall = kOneThreads / vectors, my_row = threadIdx.x / vectors, c = threadIdx.x % vectors * V;
+    const uint32_t stage_each = a.stage_rows / tall;           // of a whole stage's positions, a thread's
     const bool on = my_row < tall;
     const float count = rows_of(a, rank), all = static_cast<float>(a.positions);
     const int act = a.act;
@@ -251,18 +252,23 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
         const T* x = at<T>(a.x, sample);
         T* out = const_cast<T*>(at<T>(a.out, sample));
         // the statistics' pass
-        float s[2][V] = {}, less[V] = {};
+        Moments<V> o;                                          // (backward: its sums alone)
+        float (&s)[2][V] = o.s;
         Channels<V> ch;
-        if (kBackward) {
-            if (on) ch = Channels<V>(a, sample, c);
-        } else if (on) {
-            widen(load_raw<T, V>(x + c), less);
-#pragma unroll
-            for (int i = 0; i < V; ++i) less[i] = -less[i];
-        }
+        if (kBackward && on) ch = Channels<V>(a, sample, c);
+        uint32_t my_rows = 0;                                  // forward: positions so far
         for (uint32_t i = 0, slot = ring.at(0); ok && i < n; ++i, slot = ring.after(slot)) {
             ok = __all_sync(~0u, wait_full(slot));
             if (!ok) break;
+            if (!kBackward && on) {
+                const uint32_t rows = min(a.stage_rows, a.positions - first_of(i));
+                if (i == 0 && my_row < rows) {
+                    float from[V];
+                    widen(*reinterpret_cast<const Vec<T, V>*>(dyn + slot * kOneStage + mine), from);
+                    o.begin(from);
+                }
+                my_rows += rows == a.stage_rows ? stage_each : my_row < rows ? (rows - my_row + tall - 1) / tall : 0;
+            }
             over(i, slot, out, [&](const Vec<T, V>& q, const Vec<T, V>& p, T*) {
                 float v[V], d[V];
                 widen(q, v);
@@ -272,14 +278,24 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     add(s[0], s[0], d);
                     fma(s[1], d, v, s[1]);
                 } else {
-                    add(v, v, less);
-                    add(s[0], s[0], v);
-                    fma(s[1], v, v, s[1]);
+                    o.step(v);
                 }
             });
             if (i + a.slots < n) release(slot);               // the last ones are kept
+            if (!kBackward && (i & (i + 1)) == 0 && my_rows > 0) o.move(static_cast<float>(my_rows));
         }
-        over_positions<V>(s, red, vectors, tall);
+        if constexpr (!kBackward) {
+            // the threads' common mean, then their sums about it
+            float m[1][V];
+            o.mean_part(static_cast<float>(my_rows), count, m[0]);
+            over_positions(m, red, vectors, tall);
+            if (my_row == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) t0[c + i] = m[0][i];
+            sync_compute();
+            if (on) o.about(static_cast<float>(my_rows), t0 + c);
+        }
+        over_positions(s, red, vectors, tall);
         if (my_row == 0)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -294,13 +310,12 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 } else {
                     const float m = s[0][i] / count;
                     s0[c + i] = m;
-                    s1[c + i] = fmaxf(s[1][i] - s[0][i] * m, 0.0f);
-                    t0[c + i] = -less[i];
+                    s1[c + i] = fmaxf(fmaf(-s[0][i], m, s[1][i]), 0.0f);
                 }
             }
         sync_compute();
         // of each group, for the sample's other CTAs
-        float2* part = a.part + static_cast<uint64_t>(sample) * a.chunks * a.groups;
+        const uint64_t parts = static_cast<uint64_t>(sample) * a.chunks * a.groups;
         for (uint32_t g = warp; g < a.groups; g += kOneWarps) {
             float p = 0.0f, q = 0.0f;
             if constexpr (kBackward) {
@@ -309,21 +324,25 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     q += s1[k];
                 }
                 p = warp_sum(p);
+                q = warp_sum(q);
+                if (lane == 0) __stcg(a.part + parts + rank * a.groups + g, make_float2(p, q));
             } else {
-                const float from = t0[g * per];
+                const float each = static_cast<float>(per);
+                float hi = 0.0f;
+                for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) hi += (t0[k] + s0[k]) / each;
+                hi = warp_sum(hi);
                 for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
-                    s0[k] += t0[k] - from;
+                    s0[k] += t0[k] - hi;
                     p += s0[k];
                 }
-                p = warp_sum(p) / static_cast<float>(per);
+                p = warp_sum(p) / each;
                 for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
                     const float d = s0[k] - p;
                     q += fmaf(count * d, d, s1[k]);
                 }
-                if (lane == 0) ref[g] = from;
+                q = warp_sum(q);
+                if (lane == 0) __stcg(a.stat + parts + rank * a.groups + g, make_float4(hi, p, q, 0.0f));
             }
-            q = warp_sum(q);
-            if (lane == 0) __stcg(part + rank * a.groups + g, make_float2(p, q));
         }
         ok = sync_and(ok);
         if (a.chunks > 1) {
@@ -331,38 +350,51 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
             ok = sync_and(ok);
         }
         for (uint32_t g = warp; g < a.groups; g += kOneWarps) {
-            float p = 0.0f, q = 0.0f, rows[kOneChunks / 32];
-            float2 v[kOneChunks / 32];
-#pragma unroll
-            for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
-                const uint32_t i = lane + 32 * u;
-                v[u] = make_float2(0.0f, 0.0f);
-                rows[u] = 0.0f;
-                if (i >= a.chunks) continue;
-                v[u] = __ldcg(part + i * a.groups + g);
-                rows[u] = rows_of(a, i);
-            }
-#pragma unroll
-            for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
-                p = kBackward ? p + v[u].x : fmaf(v[u].x, rows[u], p);
-                q += kBackward ? v[u].y : 0.0f;
-            }
+            float p = 0.0f, q = 0.0f;
             if constexpr (kBackward) {
+                float2 v[kOneChunks / 32];
+#pragma unroll
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
+                    const uint32_t i = lane + 32 * u;
+                    v[u] = i < a.chunks ? __ldcg(a.part + parts + i * a.groups + g) : make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
+                    p += v[u].x;
+                    q += v[u].y;
+                }
                 const float inv = 1.0f / (all * static_cast<float>(per));
                 p = warp_sum(p) * inv;
                 q = warp_sum(q) * inv;
             } else {
-                p = warp_sum(p) / all;
+                float4 v[kOneChunks / 32];                     // w: its share of the positions
+                float hi = 0.0f, m = 0.0f;
 #pragma unroll
                 for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
-                    const float d = v[u].x - p;
-                    q += rows[u] > 0.0f ? fmaf(rows[u] * static_cast<float>(per) * d, d, v[u].y) : 0.0f;
+                    const uint32_t i = lane + 32 * u;
+                    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i >= a.chunks) continue;
+                    v[u] = __ldcg(a.stat + parts + i * a.groups + g);
+                    v[u].w = rows_of(a, i) / all;
                 }
-                q = 1.0f / sqrtf(warp_sum(q) / (all * static_cast<float>(per)) + a.eps);
-                if (lane == 0 && rank == 0) {
+#pragma unroll
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) hi += (v[u].x + v[u].y) * v[u].w;
+                hi = warp_sum(hi);
+#pragma unroll
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) m += ((v[u].x - hi) + v[u].y) * v[u].w;
+                m = warp_sum(m);
+#pragma unroll
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
+                    const float d = ((v[u].x - hi) + v[u].y) - m;
+                    q += v[u].w > 0.0f ? fmaf(v[u].w * d, d, v[u].z / (all * static_cast<float>(per))) : 0.0f;
+                }
+                p = hi + m;
+                q = 1.0f / sqrtf(warp_sum(q) + a.eps);
+                if (lane == 0) {
+                    left[g] = (hi - p) + m;
                     const uint64_t to = static_cast<uint64_t>(sample) * a.groups + g;
-                    if (a.mean_out) a.mean_out[to] = ref[g] + p;
-                    if (a.rstd_out) a.rstd_out[to] = q;
+                    if (rank == 0 && a.mean_out) a.mean_out[to] = p;
+                    if (rank == 0 && a.rstd_out) a.rstd_out[to] = q;
                 }
             }
             if (lane == 0) {
@@ -372,7 +404,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
         }
         sync_compute();
         // the result's pass, from the last stage to the first
-        float k1[V] = {}, k2[V] = {};
+        float less[V] = {}, k1[V] = {}, k2[V] = {};
         if (on)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -383,10 +415,10 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     k1[i] = -r * g0[g];
                     k2[i] = -r * r * g1[g];
                 } else {
-                    // y = act((x - ref) scale + shift): the mean, less the reference, is in the shift
-                    less[i] = -ref[g];
+                    // y = act((x - mean) scale + shift): what the mean's rounding left is in the shift
+                    less[i] = -g0[g];
                     k1[i] = g1[g] * (a.gamma ? elem(a.gamma, c + i, a.param_dtype) : 1.0f);
-                    k2[i] = fmaf(-g0[g], k1[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
+                    k2[i] = fmaf(-left[g], k1[i], a.beta ? elem(a.beta, c + i, a.param_dtype) : 0.0f);
                 }
             }
         for (uint32_t i = 0, slot = ring.at(n - 1); ok && i < n; ++i, slot = ring.before(slot)) {

@@ -156,8 +156,7 @@ fa_status norm_impl(fa_work* w, const fa_group_norm_args& p, cudaStream_t s) {
     const bool cap = capturing(s);
     Carve need{nullptr}, c{nullptr};
     const auto carve = [&](Carve& from) {
-        a.part = static_cast<float2*>(from.take(stats * a.chunks * sizeof(float2)));
-        a.ref = static_cast<float*>(from.take(stats * sizeof(float)));
+        a.stat = static_cast<float4*>(from.take(stats * a.chunks * sizeof(float4)));
     };
     carve(need);
     r = ensure_ws(w, need.used, cap);
