@@ -28,6 +28,7 @@ namespace {
 
 constexpr uint32_t kNormThreads = 256, kNormWarps = kNormThreads / 32;
 constexpr uint32_t kNormCtas = 4, kNormGradCtas = 2;                     // per SM
+constexpr uint32_t kNormMost = 16 * kNormMaxChannels + 2 * 8 * kNormThreads * 4;   // bytes of shared memory
 
 // A CTA's columns in turn: `width` vectors by `tall` positions at a time.
 struct Tile {
@@ -452,8 +453,7 @@ const Set& kernels(const NormArgs& a, uint32_t v) {
 
 cudaError_t launch_one(Kernel k, const NormArgs& a, uint32_t smem, cudaStream_t stream) {
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        const cudaError_t e = allow_shared(reinterpret_cast<const void*>(k), kNormMost);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -513,8 +513,7 @@ cudaError_t launch_norm_one(const NormArgs& a, bool backward, cudaStream_t strea
                                          {norm_one_kernel<uint16_t, 8, false>, norm_one_kernel<uint16_t, 4, true>}};
     const Kernel k = kernels[a.dtype][backward];
     const uint32_t smem = a.slots * kOneStage + fixed_bytes(a, backward);
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(k), kOneMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.across * a.chunks);

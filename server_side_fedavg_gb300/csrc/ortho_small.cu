@@ -445,8 +445,7 @@ bool split(uint32_t m, uint32_t n, uint64_t items, uint32_t* ctas, uint32_t* run
 template <int kM>
 cudaError_t launch(SmallArgs a, cudaStream_t stream) {
     const uint32_t smem = kFixed<kM> + a.run * kPitch<kM> * 4;
-    cudaError_t r = cudaFuncSetAttribute(reinterpret_cast<const void*>(ortho_small_kernel<kM>),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t r = allow_shared(reinterpret_cast<const void*>(ortho_small_kernel<kM>), kSmallMost);
     if (r != cudaSuccess) return r;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.e.items * a.ctas);

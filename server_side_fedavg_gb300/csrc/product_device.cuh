@@ -114,6 +114,12 @@ __device__ __forceinline__ void wait_predecessor() {
     asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
 }
 
+// `most`: what any call of the kernel may take.  The attribute is the function's, for all threads and
+// handles of the process: a call's own size could be lowered by another's between here and the launch.
+inline cudaError_t allow_shared(const void* kernel, uint32_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_next(void (*kern)(Params...), dim3 grid, uint32_t block, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kRotThreads, sizeof(T) * V == 16 ? 4 : 1) rota
 // 128) in 82.7 us, 6.49 TB/s; six slots of 16 KB 85.0, three CTAs of four such 92.8, one CTA of three
 // slots of 64 KB 83.8.
 constexpr uint32_t kRingStage = 32768, kRingSlots = 3, kRingTokens = 8, kRingCtas = 2;
+constexpr uint32_t kRingMost = kRingSlots * kRingStage + 2 * kRingTokens * 2 * kRotaryMaxPairs * 4;    // shared memory
 
 // The computing warps of a CTA; whether all of their threads say so.
 __device__ __forceinline__ bool sync_and(bool ok) {
@@ -328,8 +329,7 @@ template <int V>
 cudaError_t launch_ring(const RotaryArgs& a, uint32_t sms, cudaStream_t stream) {
     const auto kernel = a.interleaved ? rotary_ring_kernel<uint16_t, V, true> : rotary_ring_kernel<uint16_t, V, false>;
     const uint32_t smem = kRingSlots * kRingStage + 2 * a.cta_tokens * a.rotary_dim * 4;
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), kRingMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min((a.tokens + a.cta_tokens - 1) / a.cta_tokens, kRingCtas * sms));
