@@ -812,11 +812,15 @@ fa_status fa_group_norm_backward(fa_work* w, const fa_group_norm_backward_args* 
  *   out = alpha * X + beta * residual
  *
  * With the quintic 3.4445, -4.7750, 2.0315 five steps bring singular values from 1e-3 to 1 near 1.
- * Between its first and last pass a matrix is held as pairs of fp16 terms (22 bits, scaled), and
- * multiplied pair by pair with fp32 sums.  Errors start at some 2^-22 of X's norm and grow by at
- * most the polynomial's slope, |a| at 0, per step; against an update of many directions the result
- * is as near to fp64 as the same products in fp32.  It is rounded once.  A NaN or an infinity in x
- * spoils the matrix's whole result. */
+ * Between its first and last pass a matrix is held as pairs of fp16 terms, hi + lo (22 bits, scaled), and
+ * every product takes three of these terms' (hi hi, hi lo, lo hi) with fp32 sums; with a short side of
+ * up to 64 it may be held and multiplied in fp32 instead.  Errors start at some 2^-22 of X's norm and
+ * grow by at most the polynomial's slope, |a| at 0, per step; against an update of many directions an
+ * fp32 result is as near to fp64 as the same products in fp32.  Towards a bf16 result up to three steps
+ * may be taken as one polynomial of X X^T, and longer sums by the tensor cores, which truncate, between
+ * two rounded ones: five steps are off by up to 4e-5 (measured, 2-norm) before the rounding to bf16,
+ * which is 1.7e-3 of them.  The result is rounded once.  A NaN or an infinity in x spoils the matrix's
+ * whole result. */
 #define FA_ORTHO_NESTEROV  1u
 #define FA_ORTHO_MAX_STEPS 32
 

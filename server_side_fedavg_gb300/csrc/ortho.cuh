@@ -25,7 +25,6 @@ constexpr uint32_t kOrthoOps = 24, kOrthoBufs = 12;    // products of a launch; 
 struct OrthoProduct {
     const OrthoBuf *P, *Q, *out, *e1, *e2;    // e1, e2: laid out as out, or nullptr
     bool p_kmajor, q_kmajor;
-    bool single;                              // the hi terms alone
     bool symmetric;                           // the tiles on and above the diagonal, and their mirror images
     uint32_t k;
     uint32_t chunk;                           // blocks of 64 terms that the tensor cores sum by themselves

@@ -4,8 +4,8 @@
 //   v = c1 * sum_k P(x,k) Q(y,k) + c2 * e1 + c3 * e2
 //
 // x = hi + lo has 22 bits, so hi lo' + lo hi' + hi hi' is the product to 2^-22 of its size: three
-// products of fp16 where three bf16 terms would need six.  `single` takes hi hi' alone.  The matrices' scales keep |x| below
-// 2^15, and their typical elements far above the 2^-24 where fp16 ends.
+// products of fp16 where three bf16 terms would need six.  The matrices' scales keep |x| below 2^15, and
+// their typical elements far above the 2^-24 where fp16 ends.
 //
 // A CTA's tile is 128 rows of P (TMEM lanes) by kBN rows of Q (TMEM columns); with kCtas == 2 a
 // pair of SMs has 256 by 256 (cta_group::2).  The tensor cores' fp32 sum truncates, so it is
@@ -70,7 +70,7 @@ struct Op {
     uint32_t tiles_p, tiles_q, per;              // per: tiles of an item
     uint32_t first, need;                        // the first tile; an item's count when its earlier products are done
     uint8_t p, q, out;                           // maps
-    bool p_kmajor, q_kmajor, symmetric, single;
+    bool p_kmajor, q_kmajor, symmetric;
 };
 
 // kMany: a list of products; else one, with what a launch of that needs alone.
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
             for (uint32_t t = first; ok && t < a.tiles; t += step) {
                 const Op& o = tile.at(a, t);
                 const CUtensorMap *mp = &a.map[o.p], *mq = &a.map[o.q];
-                const bool pk = o.p_kmajor, qk = o.q_kmajor, single = o.single;
+                const bool pk = o.p_kmajor, qk = o.q_kmajor;
                 const uint32_t end = to_block(o.kblocks);
                 const uint32_t p0 = tile.p * 128 * kCtas + rank * 128, q0 = tile.q * kBN + rank * 128, z = 2 * tile.item;
                 if constexpr (kMany) {
@@ -354,12 +354,11 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                         break;
                     }
                     if (leader) mbar_expect(full + 8 * s, kStageBytes * kCtas);
-                    // hi and lo of one block of terms, or hi of two blocks
-                    const uint32_t k0 = kb * (single ? 2 * kBK : kBK), k1 = single ? k0 + kBK : k0, z1 = single ? z : z + 1;
-                    load(at, mp, pk, k0, p0, z, bar);
-                    load(at + kPlane, mp, pk, k1, p0, z1, bar);
-                    load(at + 2 * kPlane, mq, qk, k0, q0, z, bar);
-                    load(at + 3 * kPlane, mq, qk, k1, q0, z1, bar);
+                    const uint32_t k = kb * kBK;
+                    load(at, mp, pk, k, p0, z, bar);
+                    load(at + kPlane, mp, pk, k, p0, z + 1, bar);
+                    load(at + 2 * kPlane, mq, qk, k, q0, z, bar);
+                    load(at + 3 * kPlane, mq, qk, k, q0, z + 1, bar);
                     if (++s == kRing) {
                         s = 0;
                         phase ^= 1;
@@ -377,7 +376,6 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                 const uint32_t step_p = o.p_kmajor ? 32 >> 4 : 2048 >> 4, step_q = o.q_kmajor ? 32 >> 4 : 2048 >> 4;
                 const uint32_t desc_p = operand_desc_lo(base, o.p_kmajor), desc_q = operand_desc_lo(base + 2 * kPlane, o.q_kmajor);
                 const uint32_t kblocks = to_block(o.kblocks), chunk = o.chunk;
-                const bool single = o.single;
                 for (uint32_t kb = from_block(o.kblocks); ok && kb < kblocks; ++ch) {
                     const uint32_t b = ch & 1;
                     if (ch >= 2 && !bar_wait(acc_empty + 8 * b, (ch / 2 - 1) & 1, gone, ctas)) {
@@ -394,12 +392,10 @@ __global__ void __launch_bounds__((kOrthoThreads<kBN>), 1) ortho_product_kernel(
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        // lo hi, hi lo, hi hi: the small products meet a small accumulator; or hi hi twice
+                        // lo hi, hi lo, hi hi: the small products meet a small accumulator
 #pragma unroll
                         for (uint32_t pair = 0; pair < 3; ++pair) {
-                            if (pair == 1 && single) continue;
-                            const uint32_t op = pair == 0 ? kPlane >> 4 : 0;
-                            const uint32_t oq = pair == 1 || (pair == 0 && single) ? kPlane >> 4 : 0;
+                            const uint32_t op = pair == 0 ? kPlane >> 4 : 0, oq = pair == 1 ? kPlane >> 4 : 0;
 #pragma unroll
                             for (uint32_t x = 0; x < kBK / 16; ++x) {
                                 mma<kCtas>(d, dp + op + x * step_p, dq + oq + x * step_q, kDescHi, idesc, add);
@@ -567,10 +563,7 @@ cudaError_t launch(const Args<kMany>& a, uint32_t room, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, ortho_product_kernel<kCtas, kBN, kMany, kSplit>, a);
 }
 
-uint32_t blocks_of(const OrthoProduct& p) {
-    const uint32_t block = (p.single ? 2 : 1) * kBK;
-    return (p.k + block - 1) / block;
-}
+uint32_t blocks_of(const OrthoProduct& p) { return (p.k + kBK - 1) / kBK; }
 
 uint32_t tiles_of(const OrthoProduct& p, uint32_t side) {
     const uint32_t r = (p.out->rows + side - 1) / side, c = (p.out->cols + side - 1) / side;
@@ -585,9 +578,8 @@ struct Plan {
     uint32_t side() const { return pair ? 256 : 128; }
 };
 
-// Turns over the SMs, in microseconds.  A block of a pair takes 0.8 (two of one product 0.6), of a
-// single SM 0.42 or, with all SMs loading 64 KB for each, 0.58; a tile's end 1.5, and a product 3 more
-// before its first tile's data is there.
+// Turns over the SMs, in microseconds.  A block of a pair takes 0.8, of a single SM 0.42 or, with all SMs
+// loading 64 KB for each, 0.58; a tile's end 1.5, and a product 3 more before its first tile's data is there.
 //
 // One product whose tiles occupy a part of the SMs has a tile's blocks shared out over a cluster.
 // Launching the cluster and exchanging the sums takes 1.9, of eight CTAs 4 (which have to be free in
@@ -600,7 +592,7 @@ Plan plan_of(const OrthoProduct* p, uint32_t n, uint32_t items, bool many, uint3
         for (uint32_t i = 0; i < n; ++i) {
             const uint64_t t = static_cast<uint64_t>(tiles_of(p[i], pair ? 256 : 128)) * items, room = pair ? sms / 2 : sms;
             const double busy = std::min(1.0, static_cast<double>(t * splits) / sms);
-            const double block = pair ? (p[i].single ? 0.6 : 0.8) : std::max(0.42, 0.58 * busy);
+            const double block = pair ? 0.8 : std::max(0.42, 0.58 * busy);
             // items go on without one another: whole turns for one, parts of turns for many
             const double turns = many ? std::max(1.0, static_cast<double>(t) / room) : static_cast<double>((t + room - 1) / room);
             c += turns * (block * ((blocks_of(p[i]) + splits - 1) / splits) + 1.5) + 3.0 + (splits == 1 ? 0.0 : splits < 8 ? 1.9 : 4.0);
@@ -651,7 +643,6 @@ cudaError_t run(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t* don
         o.c3 = p[i].c3;
         o.rows = p[i].out->rows;
         o.cols = p[i].out->cols;
-        o.single = p[i].single;
         o.kblocks = blocks_of(p[i]);
         o.chunk = p[i].chunk;
         o.p_kmajor = p[i].p_kmajor;

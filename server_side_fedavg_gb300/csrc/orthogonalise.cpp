@@ -66,7 +66,7 @@ std::vector<uint32_t> segments(uint32_t steps, bool joined) {
 struct Run {
     Sizes z;
     uint32_t chunk;
-    bool bf16, single;               // of the result; of the next products
+    bool bf16;                       // of the result
     double a, b, c;
     fa::OrthoBuf x[2], sq[kSquares];
     std::vector<fa::OrthoProduct> list;
@@ -82,7 +82,6 @@ struct Run {
         p.p_kmajor = pk;
         p.q_kmajor = qk;
         p.symmetric = symmetric;
-        p.single = single;
         p.k = k;
         p.chunk = chunk;
         // from true values to held ones
@@ -100,19 +99,13 @@ struct Run {
         uint32_t steps = 0;
         for (uint32_t n : parts) {
             steps += n;
-            segment(n, X, top[steps], steps + 1 == top.size());
+            segment(n, X, top[steps]);
         }
         return X;
     }
 
     // `steps` steps from X, which is replaced; `next` bounds its singular values then.
-    void segment(uint32_t steps, Held& X, double next, bool last) {
-        // The last step towards a bf16 result takes one product of three, the hi terms' (11 bits), where
-        // it is a segment of its own.  What that costs is not multiplied by later steps: measured against
-        // fp64, 2.0e-3 of a square result in place of 1.7e-3, its own rounding.  (In a longer segment q X
-        // and Q X are several times the result and cancel: 3.1e-3 to 4.9e-3.)  24 of 1024 x 1024 take 1.17
-        // ms, all in full 1.25.
-        single = last && bf16 && steps == 1;
+    void segment(uint32_t steps, Held& X, double next) {
         int used = 0;
         const auto square = [&](double bound) {
             Held h;
