@@ -806,7 +806,8 @@ fa_status fa_group_norm_backward(fa_work* w, const fa_group_norm_backward_args* 
  * the weight.  For each of `count` matrices [rows, cols]:
  *
  *   g = mu * momentum + update         (update itself without a momentum), to momentum_out
- *   x = update + mu * g                (FA_ORTHO_NESTEROV; else g; update without a momentum)
+ *   x = update + mu * g                (FA_ORTHO_NESTEROV; else g; update itself without a
+ *                                       momentum: a first round with momentum_out alone does not read mu)
  *   X = x / (|x| + eps)                |x|: the root of the sum of its elements' squares
  *   `steps` times:  A = X X^T,  X <- a X + (b A + c A^2) X
  *   out = alpha * X + beta * residual

@@ -42,11 +42,11 @@ struct Vecs {
 
 __device__ __forceinline__ uint64_t row_of(const OrthoMat& m, uint32_t item, uint32_t r) { return item * m.step + r * m.ld; }
 
-// x: u, then u + mu g' or g'; g: m, then g' = mu m + u (u itself without a momentum).
+// x: u, then u + mu g' or g'; g: m, then g' = mu m + u.  Without a momentum both are u: mu is not read.
 __device__ __forceinline__ void momentum_step(const OrthoEnds& a, float (&x)[8], float (&g)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = a.momentum.p ? fmaf(a.mu, g[i], x[i]) : x[i];
-    if (!a.momentum.p && !a.momentum_out.p) return;
+    if (!a.momentum.p) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = a.nesterov ? fmaf(a.mu, g[i], x[i]) : g[i];
 }
@@ -56,7 +56,7 @@ __device__ __forceinline__ void momentum_step(const OrthoEnds& a, float (&x)[8],
 __device__ __forceinline__ void step_of(const OrthoEnds& a, const Vecs& v, uint32_t item, uint32_t r, uint32_t c, bool kept,
                                         float (&x)[8], float (&g)[8]) {
     load8(a.update, row_of(a.update, item, r), c, a.cols, v.update, x);
-    if (kept && a.momentum_out.p) {
+    if (kept && a.momentum.p && a.momentum_out.p) {
         load8(a.momentum_out, row_of(a.momentum_out, item, r), c, a.cols, v.momentum_out, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = a.nesterov ? fmaf(a.mu, g[i], x[i]) : g[i];
