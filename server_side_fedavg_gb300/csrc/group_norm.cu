@@ -10,10 +10,12 @@
 // vector) and walks down positions, so that nothing of a channel is fetched twice; a CTA has a
 // run of a sample's positions.  The second pass walks its run backwards: what the first pass read
 // last is still in L2.  A thread's sums are taken of x less a reference that follows the mean (see
-// Moments); threads, a run's channels, and then the runs, are joined as means and sums of squares about
-// them, in a fixed order, each time first to a common mean in fp32 and then as differences from
-// that, of which the statistics come.  So neither an offset far larger than the spread nor positions
-// unlike the others cost digits, and the mean is off by its own rounding alone.
+// Moments).  Threads, a run's channels, and then the runs, are joined in a fixed order as means and sums of
+// squares about them, by their differences from a point near the common mean: for threads that mean
+// itself, for channels the mean of up to 32, for runs the first one's.  (The mean of 1 / k of the positions
+// is within k^(1/2) spreads of the whole's: such a point costs roundings of that size, nothing squared.)
+// So neither an offset far larger than the spread nor positions unlike the others cost digits, and the
+// kept mean is off by its own rounding.
 //
 // What bounds it: small samples, the launches (4 x 9216 x 64 fp32 10.9 us, 1 x 216 x 256 7.4); large ones
 // that the one kernel does not take, HBM, x read twice and the result written once: 2 x 128^3 x 32 bf16 in
@@ -73,18 +75,19 @@ __device__ __forceinline__ uint32_t rows_mine(const Tile& t, uint32_t r0, uint32
     return t.on && r0 + t.row < r1 ? (r1 - r0 - t.row + t.tall - 1) / t.tall : 0;
 }
 
-// f(vector of p0, vector of p1, position) for this thread's positions of [r0, r1), channels from c;
-// after(positions so far) now and then.
-template <bool kReverse, int kStreams, int V, typename T, typename F, typename G>
+// f(vector of p0, vector of p1, position) for this thread's positions `from` to `to` of [r0, r1), channels
+// from c.
+template <typename T, int V>
+constexpr uint32_t kAtOnce = sizeof(T) * V >= 16 ? 4 : 8;    // 64 bytes of a stream in flight, no more than eight positions
+template <bool kReverse, int kStreams, int V, typename T, typename F>
 __device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t ld0, const T* p1, uint64_t ld1, uint32_t r0,
-                                          uint32_t r1, uint32_t c, F f, G after) {
+                                          uint32_t r1, uint32_t c, F f, uint32_t from = 0, uint32_t to = ~0u) {
     if (!t.on) return;
-    // 64 bytes of either stream in flight per thread, and no more than eight positions
-    constexpr uint32_t kU = sizeof(T) * V >= 16 ? 4 : 8;
-    const uint32_t mine = rows_mine(t, r0, r1);
+    constexpr uint32_t kU = kAtOnce<T, V>;
+    const uint32_t mine = rows_mine(t, r0, r1), end = min(mine, to);
     const auto row_of = [&](uint32_t i) { return r0 + t.row + (kReverse ? mine - 1 - i : i) * t.tall; };
-    uint32_t i = 0;
-    for (; i + kU <= mine; i += kU) {
+    uint32_t i = from;
+    for (; i + kU <= end; i += kU) {
         Vec<T, V> q[kU], p[kU];
 #pragma unroll
         for (uint32_t u = 0; u < kU; ++u) {
@@ -93,21 +96,15 @@ __device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t l
         }
 #pragma unroll
         for (uint32_t u = 0; u < kU; ++u) f(q[u], p[u], row_of(i + u));
-        after(i + kU);
     }
-    for (; i < mine; ++i) {
+    for (; i < end; ++i) {
         const Vec<T, V> q = load_raw<T, V>(p0 + row_of(i) * ld0 + c);
         f(q, kStreams == 2 ? load_raw<T, V>(p1 + row_of(i) * ld1 + c) : q, row_of(i));
     }
 }
-template <bool kReverse, int kStreams, int V, typename T, typename F>
-__device__ __forceinline__ void over_rows(const Tile& t, const T* p0, uint64_t ld0, const T* p1, uint64_t ld1, uint32_t r0,
-                                          uint32_t r1, uint32_t c, F f) {
-    over_rows<kReverse, kStreams, V>(t, p0, ld0, p1, ld1, r0, r1, c, f, [](uint32_t) {});
-}
 
 // ----------------------------------------------------------------- forward
-// stat[sample][chunk][group] = (mean, as a sum of two; sum of squares about it) over the chunk's positions.
+// stat[sample][group][chunk] = (mean, as a sum of two; sum of squares about it) over the chunk's positions.
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ float sm[];
@@ -115,7 +112,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(cons
     wait_predecessor();
     const uint32_t vectors = a.channels / V, per = a.channels / a.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t r0 = blockIdx.x * a.rows, r1 = min(a.positions, r0 + a.rows);
-    const float count = static_cast<float>(r1 - r0);
+    const float count = static_cast<float>(r1 - r0), inv = 1.0f / count, inv_per = 1.0f / static_cast<float>(per);
     for (uint32_t sample = a.first + blockIdx.y; sample < a.last; sample += gridDim.y) {
         const T* x = at<T>(a.x, sample);
         for (uint32_t c0 = 0; c0 < vectors; c0 += kNormThreads) {
@@ -123,24 +120,24 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(cons
             const uint32_t c = (c0 + t.col) * V;
             Moments<V> o;
             const uint32_t mine = rows_mine(t, r0, r1);
-            if (mine) {
+            {
+                // (where a thread has no position, the last one's: it then weighs nothing)
                 float from[V];
-                widen(load_raw<T, V>(x + (r0 + t.row) * a.x.ld + c), from);
+                widen(load_raw<T, V>(x + min(r0 + t.row, r1 - 1) * a.x.ld + c), from);
                 o.begin(from);
             }
-            uint32_t next = 1;
-            over_rows<false, 1, V>(
-                t, x, a.x.ld, x, a.x.ld, r0, r1, c,
-                [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t) {
-                    float d[V];
-                    widen(q, d);
-                    o.step(d);
-                },
-                [&](uint32_t done) {
-                    if (done < next) return;
-                    o.move(static_cast<float>(done));
-                    next = 2 * done;
-                });
+            for (uint32_t i = 0, end = kAtOnce<T, V>;; i = end, end *= kGrow) {
+                over_rows<false, 1, V>(
+                    t, x, a.x.ld, x, a.x.ld, r0, r1, c,
+                    [&](const Vec<T, V>& q, const Vec<T, V>&, uint32_t) {
+                        float d[V];
+                        widen(q, d);
+                        o.step(d);
+                    },
+                    i, end);
+                if (end >= mine) break;
+                o.move(static_cast<float>(end));
+            }
             // the threads' common mean, then their sums about it
             const float n = static_cast<float>(mine);
             float m[1][V];
@@ -155,7 +152,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(cons
             if (t.row == 0)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float d = o.s[0][i] / count;
+                    const float d = o.s[0][i] * inv;
                     mean[c + i] = d;
                     sq[c + i] = fmaxf(fmaf(-o.s[0][i], d, o.s[1][i]), 0.0f);
                 }
@@ -165,22 +162,21 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_stat_kernel(cons
         const uint32_t lanes = lanes_for(per), sub = lane % lanes;
         for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
             const uint32_t g = g0 + lane / lanes, end = g < a.groups ? (g + 1) * per : 0;
-            const float all = static_cast<float>(per);
-            float hi = 0.0f, m = 0.0f, q = 0.0f;
-            for (uint32_t c = g * per + sub; c < end; c += lanes) hi += (base[c] + mean[c]) / all;
-            hi = lane_sum(hi, lanes);
+            // a point near the group's mean: that of its first channels, one a lane
+            float hi = g * per + sub < end ? base[g * per + sub] + mean[g * per + sub] : 0.0f, m = 0.0f, q = 0.0f;
+            hi = lane_sum(hi * (1.0f / static_cast<float>(min(lanes, per))), lanes);
             for (uint32_t c = g * per + sub; c < end; c += lanes) {
                 mean[c] += base[c] - hi;
                 m += mean[c];
             }
-            m = lane_sum(m, lanes) / all;
+            m = lane_sum(m, lanes) * inv_per;
             for (uint32_t c = g * per + sub; c < end; c += lanes) {
                 const float d = mean[c] - m;
                 q += fmaf(count * d, d, sq[c]);
             }
             q = lane_sum(q, lanes);
             if (sub == 0 && g < a.groups)
-                a.stat[(static_cast<uint64_t>(sample) * a.chunks + blockIdx.x) * a.groups + g] = make_float4(hi, m, q, 0.0f);
+                a.stat[(static_cast<uint64_t>(sample) * a.groups + g) * a.chunks + blockIdx.x] = make_float4(hi, m, q, 0.0f);
         }
         __syncthreads();
     }
@@ -195,27 +191,23 @@ __device__ __forceinline__ void join_chunks(const NormArgs& a, uint32_t sample, 
     const auto rows_of = [&](uint32_t i) { return static_cast<float>(min(a.rows, a.positions - i * a.rows)); };
     for (uint32_t g0 = warp * (32 / lanes); g0 < a.groups; g0 += kNormWarps * (32 / lanes)) {
         const uint32_t g = g0 + lane / lanes, end = g < a.groups ? a.chunks : 0;
-        const float4* part = a.stat + static_cast<uint64_t>(sample) * a.chunks * a.groups + g;
-        float hi = 0.0f, m = 0.0f, q = 0.0f;
+        const float4* part = a.stat + (static_cast<uint64_t>(sample) * a.groups + g) * a.chunks;
+        float m = 0.0f, q = 0.0f, hi = 0.0f;       // hi: a point near the mean, the first chunk's
         float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);        // this lane's first: with few chunks its only one
-        if (sub < end) own = part[static_cast<uint64_t>(sub) * a.groups];
-        const auto common = [&](float4 p, uint32_t i) { return (p.x + p.y) * (rows_of(i) / all); };
-        if (sub < end) hi = common(own, sub);
+        if (sub < end) own = part[sub];
+        hi = __shfl_sync(~0u, own.x + own.y, lane - sub);
+        const auto rest = [&](float4 p, uint32_t i, float to) { return fmaf((p.x - hi) + p.y, rows_of(i), to); };
+        if (sub < end) m = rest(own, sub, 0.0f);
 #pragma unroll 4
-        for (uint32_t i = sub + lanes; i < end; i += lanes) hi += common(part[static_cast<uint64_t>(i) * a.groups], i);
-        hi = lane_sum(hi, lanes);
-        const auto rest = [&](float4 p, uint32_t i) { return ((p.x - hi) + p.y) * (rows_of(i) / all); };
-        if (sub < end) m = rest(own, sub);
-#pragma unroll 4
-        for (uint32_t i = sub + lanes; i < end; i += lanes) m += rest(part[static_cast<uint64_t>(i) * a.groups], i);
-        m = lane_sum(m, lanes);
+        for (uint32_t i = sub + lanes; i < end; i += lanes) m = rest(part[i], i, m);
+        m = lane_sum(m, lanes) / all;
         const auto square = [&](float4 p, uint32_t i) {
             const float d = ((p.x - hi) + p.y) - m;
             return fmaf(rows_of(i) * static_cast<float>(per) * d, d, p.z);
         };
         if (sub < end) q = square(own, sub);
 #pragma unroll 4
-        for (uint32_t i = sub + lanes; i < end; i += lanes) q += square(part[static_cast<uint64_t>(i) * a.groups], i);
+        for (uint32_t i = sub + lanes; i < end; i += lanes) q += square(part[i], i);
         q = lane_sum(q, lanes) / (all * static_cast<float>(per));
         if (sub == 0 && g < a.groups) {
             mean[g] = hi + m;

@@ -20,7 +20,7 @@ struct NormArgs {
     const float *mean, *rstd;      // backward: [n][groups]
     float *mean_out, *rstd_out;    // forward, or nullptr
     void *d_gamma, *d_beta;        // backward, of param_dtype, or nullptr
-    float4* stat;                  // forward: [n][chunks][groups] of the statistics' parts, the mean as a sum of two
+    float4* stat;                  // forward: [n][groups][chunks] of the statistics' parts, the mean as a sum of two
     float2* part;                  // backward: [n][chunks][groups] of the sums' parts
     float2* cpart;                 // [norm_rows * chunks][channels] of the parameters' gradients, or nullptr
     uint32_t n, positions, channels, groups;
@@ -35,8 +35,8 @@ struct NormArgs {
 };
 
 // In one kernel, where the positions are one run of 16-byte pieces: false where they are not.  Else
-// fills in rows, chunks (CTAs per sample), across (samples at one time), stage_rows and slots; stat and part
-// are [n][chunks][groups], cpart [across * chunks][channels].
+// fills in rows, chunks (CTAs per sample), across (samples at one time), stage_rows and slots; cpart is
+// [across * chunks][channels].
 bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms);
 cudaError_t launch_norm_one(const NormArgs& a, bool backward, cudaStream_t stream);
 

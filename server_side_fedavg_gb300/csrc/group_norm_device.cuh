@@ -178,9 +178,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // and how the variance comes from them without cancelling.  A run's squares about a point r are its squares
 // about its mean m and n (m - r)^2.  Where r is the mean of the first k positions, these have at least
 // k (m - r)^2 of the squares about m, so that the second part is at most n / k times the first, whatever
-// the values are.  The reference begins as the thread's first value and is moved to the mean so far
-// whenever the run has doubled: no sum is more than a few times what is kept of it.  (With one reference
-// for a run, its first value, one voxel 1000 spreads off left 3 digits of the variance.)
+// the values are.  The reference begins as the thread's first value and is moved to the mean so far after
+// the first few positions and whenever the run has grown kGrow times: no sum is more than some ten times
+// what is kept of it.  (With one reference for a run, its first value, one voxel 1000 spreads off left 3
+// digits of the variance.)
+constexpr uint32_t kGrow = 8;
 template <int V>
 struct Moments {
     float less[V] = {}, s[2][V] = {};                // less: the reference, negated
@@ -204,16 +206,18 @@ struct Moments {
             less[i] = to;
         }
     }
-    // this thread's part of the mean of `count` positions, n of them its own
+    // this thread's part of the mean of `count` positions, n of them its own (if n is 0, all here is 0)
     __device__ __forceinline__ void mean_part(float n, float count, float (&to)[V]) const {
+        const float inv = 1.0f / count, share = n * inv;
 #pragma unroll
-        for (int i = 0; i < V; ++i) to[i] = n > 0.0f ? fmaf(-less[i], n / count, s[0][i] / count) : 0.0f;
+        for (int i = 0; i < V; ++i) to[i] = fmaf(-less[i], share, s[0][i] * inv);
     }
     // the same sums about `base`
     __device__ __forceinline__ void about(float n, const float* base) {
+        const float inv = n > 0.0f ? 1.0f / n : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float m = n > 0.0f ? s[0][i] / n : 0.0f, d = n > 0.0f ? (-less[i] - base[i]) + m : 0.0f;
+            const float m = s[0][i] * inv, d = (-less[i] - base[i]) + m;
             s[1][i] = fmaf(n * d, d, fmaxf(fmaf(-s[0][i], m, s[1][i]), 0.0f));
             s[0][i] = n * d;
         }

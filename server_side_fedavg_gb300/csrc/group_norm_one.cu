@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
     const uint32_t tall = kOneThreads / vectors, my_row = threadIdx.x / vectors, c = threadIdx.x % vectors * V;
     const uint32_t stage_each = a.stage_rows / tall;           // of a whole stage's positions, a thread's
     const bool on = my_row < tall;
-    const float count = rows_of(a, rank), all = static_cast<float>(a.positions);
+    const float count = rows_of(a, rank), inv_count = 1.0f / count, all = static_cast<float>(a.positions);
     const int act = a.act;
     const auto wait_full = [&](uint32_t s) {
         const bool got = mbar_wait(full + 8 * s, ring.full >> s & 1);
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
         float (&s)[2][V] = o.s;
         Channels<V> ch;
         if (kBackward && on) ch = Channels<V>(a, sample, c);
-        uint32_t my_rows = 0;                                  // forward: positions so far
+        uint32_t my_rows = 0, next = 1;                        // forward: positions so far; stages when the reference moves
         for (uint32_t i = 0, slot = ring.at(0); ok && i < n; ++i, slot = ring.after(slot)) {
             ok = __all_sync(~0u, wait_full(slot));
             if (!ok) break;
@@ -282,7 +282,10 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 }
             });
             if (i + a.slots < n) release(slot);               // the last ones are kept
-            if (!kBackward && (i & (i + 1)) == 0 && my_rows > 0) o.move(static_cast<float>(my_rows));
+            if (!kBackward && i + 1 == next && my_rows > 0) {
+                o.move(static_cast<float>(my_rows));
+                next *= kGrow;
+            }
         }
         if constexpr (!kBackward) {
             // the threads' common mean, then their sums about it
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                     t0[c + i] += s[0][i];
                     t1[c + i] += s[1][i];
                 } else {
-                    const float m = s[0][i] / count;
+                    const float m = s[0][i] * inv_count;
                     s0[c + i] = m;
                     s1[c + i] = fmaxf(fmaf(-s[0][i], m, s[1][i]), 0.0f);
                 }
@@ -327,21 +330,20 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 q = warp_sum(q);
                 if (lane == 0) __stcg(a.part + parts + rank * a.groups + g, make_float2(p, q));
             } else {
-                const float each = static_cast<float>(per);
-                float hi = 0.0f;
-                for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) hi += (t0[k] + s0[k]) / each;
-                hi = warp_sum(hi);
+                // a point near the group's mean: that of its first channels, one a lane
+                float hi = lane < per ? t0[g * per + lane] + s0[g * per + lane] : 0.0f;
+                hi = warp_sum(hi) / static_cast<float>(min(per, 32u));
                 for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
                     s0[k] += t0[k] - hi;
                     p += s0[k];
                 }
-                p = warp_sum(p) / each;
+                p = warp_sum(p) / static_cast<float>(per);
                 for (uint32_t k = g * per + lane; k < (g + 1) * per; k += 32) {
                     const float d = s0[k] - p;
                     q += fmaf(count * d, d, s1[k]);
                 }
                 q = warp_sum(q);
-                if (lane == 0) __stcg(a.stat + parts + rank * a.groups + g, make_float4(hi, p, q, 0.0f));
+                if (lane == 0) __stcg(a.stat + parts + g * a.chunks + rank, make_float4(hi, p, q, 0.0f));
             }
         }
         ok = sync_and(ok);
@@ -367,29 +369,27 @@ __global__ void __launch_bounds__(kOneThreads + 32) norm_one_kernel(const __grid
                 p = warp_sum(p) * inv;
                 q = warp_sum(q) * inv;
             } else {
-                float4 v[kOneChunks / 32];                     // w: its share of the positions
-                float hi = 0.0f, m = 0.0f;
+                float4 v[kOneChunks / 32];                     // w: its positions
 #pragma unroll
                 for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
                     const uint32_t i = lane + 32 * u;
                     v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (i >= a.chunks) continue;
-                    v[u] = __ldcg(a.stat + parts + i * a.groups + g);
-                    v[u].w = rows_of(a, i) / all;
+                    v[u] = __ldcg(a.stat + parts + g * a.chunks + i);
+                    v[u].w = rows_of(a, i);
                 }
+                const float hi = __shfl_sync(~0u, v[0].x + v[0].y, 0);       // a point near the mean, the first CTA's
+                float m = 0.0f;
 #pragma unroll
-                for (uint32_t u = 0; u < kOneChunks / 32; ++u) hi += (v[u].x + v[u].y) * v[u].w;
-                hi = warp_sum(hi);
-#pragma unroll
-                for (uint32_t u = 0; u < kOneChunks / 32; ++u) m += ((v[u].x - hi) + v[u].y) * v[u].w;
-                m = warp_sum(m);
+                for (uint32_t u = 0; u < kOneChunks / 32; ++u) m = v[u].w > 0.0f ? fmaf((v[u].x - hi) + v[u].y, v[u].w, m) : m;
+                m = warp_sum(m) / all;
 #pragma unroll
                 for (uint32_t u = 0; u < kOneChunks / 32; ++u) {
                     const float d = ((v[u].x - hi) + v[u].y) - m;
-                    q += v[u].w > 0.0f ? fmaf(v[u].w * d, d, v[u].z / (all * static_cast<float>(per))) : 0.0f;
+                    q += v[u].w > 0.0f ? fmaf(v[u].w * static_cast<float>(per) * d, d, v[u].z) : 0.0f;
                 }
                 p = hi + m;
-                q = 1.0f / sqrtf(warp_sum(q) + a.eps);
+                q = 1.0f / sqrtf(warp_sum(q) / (all * static_cast<float>(per)) + a.eps);
                 if (lane == 0) {
                     left[g] = (hi - p) + m;
                     const uint64_t to = static_cast<uint64_t>(sample) * a.groups + g;
