@@ -17,9 +17,9 @@
 // So neither an offset far larger than the spread nor positions unlike the others cost digits, and the
 // kept mean is off by its own rounding.
 //
-// What bounds it: small samples, the launches (4 x 9216 x 64 fp32 10.9 us, 1 x 216 x 256 7.4); large ones
+// What bounds it: small samples, the launches (4 x 9216 x 64 fp32 11.7 us, 1 x 216 x 256 6.8); large ones
 // that the one kernel does not take, HBM, x read twice and the result written once: 2 x 128^3 x 32 bf16 in
-// rows of 40 elements 283 us, 3.3 TB/s of whole lines, gradients of 2 x 96^3 in such rows 182.
+// rows of 40 elements 278 us, 3.4 TB/s of whole lines, gradients of 2 x 96^3 in such rows 182.
 #include <algorithm>
 
 #include "group_norm_device.cuh"

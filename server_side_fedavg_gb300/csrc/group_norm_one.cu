@@ -9,7 +9,7 @@
 // are fetched meanwhile.  A sample that fits is read once.
 //
 // What bounds it: HBM, x (and dout) read once and beyond 28 MB a second time, the result written once.  2 x
-// 128^3 x 32 bf16 138 us, 702 MB moved at 5.2 TB/s; gradients of 2 x 96^3 x 32 bf16 with silu 97 us, instruction
+// 128^3 x 32 bf16 135 us, 698 MB moved at 5.2 TB/s; gradients of 2 x 96^3 x 32 bf16 with silu 97 us, instruction
 // issue (62 % of the slots), those of 3 x 107865 x 64 fp32 68 us.
 #include <algorithm>
 
@@ -24,8 +24,8 @@ constexpr uint32_t kOneStage = 40960, kOneSlots = 5;
 constexpr uint32_t kOneRed = 128 * (kOneWarps + 2);   // floats: the sums over the positions
 static_assert(kOneRed >= 4 * kOneThreads, "four of every thread's sums");
 constexpr uint32_t kOneChunks = 160;                  // CTAs of a sample: five per lane of a warp
-// Bytes of a sample's inputs from which on one kernel is faster: 32 of 4096 x 128 bf16 (1 MB) take 27
-// us so and 22 in two passes, one of 32768 x 64 bf16 (4 MB) 14 and 15, 2 of 32768 x 256 fp32 31 and 39.
+// Bytes of a sample's inputs from which on one kernel is faster: 32 of 4096 x 128 bf16 (1 MB) take 28
+// us so and 22 in two passes, one of 32768 x 64 bf16 (4 MB) 14 and 15, 2 of 32768 x 256 fp32 31 and 36.
 constexpr double kOneLeast = 4e6;
 constexpr uint32_t kOneMost = 225 * 1024;             // dynamic shared memory
 constexpr uint32_t kOneGroups = 80;                   // counters for samples at one time, and one for the end
@@ -485,7 +485,7 @@ bool plan_norm_one(NormArgs& a, bool backward, uint32_t sms) {
     // Samples at one time, each with its share of the SMs: the least by a model of the rounds that takes.
     // A round moves its samples' bytes, with what is not kept in shared memory read again, at the SMs'
     // share of 6.5 TB/s, and has some 9 us of sums and waiting.  Two of 128^3 x 32 bf16 take 135 us side
-    // by side and 141 one after the other, the gradients of three of 45 x 47 x 51 x 64 fp32 68 and 81.
+    // by side and 141 one after the other, the gradients of three of 45 x 47 x 51 x 64 fp32 68 and 80.
     const uint64_t stages = (a.positions + a.stage_rows - 1) / a.stage_rows;
     const double out = static_cast<double>(a.positions) * row, in = out * streams;
     if (in < kOneLeast) return false;

@@ -23,8 +23,8 @@
 // clusters are resident (a cooperative launch), and a tile waits for earlier ones alone, so that the
 // first that is not done can always go on.  Where the items have a few turns of tiles that fills each
 // product's last turn with the next one's tiles: 24 of 1024 x 1024 bf16, 240 and 384 tiles over 76
-// pairs, take 1.17 ms so and 1.34 with a launch for each product.  One matrix gains nothing (4096 x
-// 4096 fp32 2.86 ms both ways, 512 x 512 bf16 183 us so and 173 by launches, each with the tiles that suit
+// pairs, take 1.30 ms so and 1.49 with a launch for each product.  One matrix gains nothing (4096 x
+// 4096 fp32 2.89 ms both ways, 512 x 512 bf16 174 us so and 141 by launches, each with the tiles that suit
 // it), and is done by launches.
 #include <algorithm>
 
@@ -54,7 +54,8 @@ constexpr uint32_t kOrthoSplits = 8;
 template <int kBN>
 constexpr int kDrain = 4 * kBN / kCols;          // drain warps
 // The pair's last warpgroup (loads, MMAs, two idle warps) gives registers to the drain warps, as in
-// the product kernels: 128 x 56 + 512 x 104 <= 640 x 96.
+// the product kernels: 128 x 56 + 512 x 104 <= 640 x 96.  At those 96 registers ptxas spills 216 bytes (stores)
+// and 428 (loads) of one product's kernel, 40 and 80 of the list's, in the tiles' ends.
 template <int kBN>
 constexpr int kOrthoThreads = (kDrain<kBN> + (kBN == 256 ? 4 : 2)) * 32;
 static_assert(kDrain<128> * kSplitUnits * kUnit <= kStageBytes && kSplitUnits < kUnits);
@@ -583,9 +584,9 @@ struct Plan {
 //
 // One product whose tiles occupy a part of the SMs has a tile's blocks shared out over a cluster.
 // Launching the cluster and exchanging the sums takes 1.9, of eight CTAs 4 (which have to be free in
-// one part of the GPU): 512 x 512 bf16, 10 tiles of 8 blocks, 154 us unsplit, 143 by four, 169 by eight;
-// 128 x 11008 bf16, first products of one tile and 172 blocks, 299, 180 and 160; 100 x 10000 fp32
-// 711, 282 and 206.
+// one part of the GPU): 512 x 512 bf16, 10 tiles of 8 blocks, 157 us unsplit, 139 by four, 175 by eight;
+// 128 x 11008 bf16, first products of one tile and 172 blocks, 299, 178 and 157; 100 x 10000 fp32
+// 705, 276 and 201.
 Plan plan_of(const OrthoProduct* p, uint32_t n, uint32_t items, bool many, uint32_t sms) {
     const auto cost = [&](bool pair, uint32_t splits) {
         double c = 0.0;
@@ -701,7 +702,7 @@ cudaError_t map_ortho(OrthoBuf* b, uint32_t items) {
 }
 
 // Whether a list is launched one at a time: one matrix; turns enough that a part of one does not count; or
-// tiles so few that splitting them is worth more (5 of 10192 x 40 bf16 167 us so and 375 by the list).
+// tiles so few that splitting them is worth more (5 of 10192 x 40 bf16 160 us so and 366 by the list).
 // *cost: the time.
 static bool one_by_one(const OrthoProduct* p, uint32_t n, uint32_t items, uint32_t sms, double* cost) {
     uint64_t most = 0;

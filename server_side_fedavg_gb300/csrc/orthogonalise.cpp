@@ -207,7 +207,8 @@ fa_status ortho_impl(fa_work* w, const fa_orthogonalise_args& p, cudaStream_t s)
         b.ld = (z.m + 7ull) / 8 * 8;
     }
     // Towards a bf16 result steps are joined where that takes less time, by the products' cost model: 11008 x
-    // 4096 4.20 ms joined, 5.21 as they stand; 900 x 1120 225 and 185 us, 4 of 1000 x 1300 490 and 457.
+    // 4096 4.17 ms joined, 5.92 as they stand; 700 x 4100 246 and 277 us, 900 x 1120 220 and 184.  (Where both are
+    // near it may err: 4 of 1000 x 1300 are joined, 488 us, and take 471 as they stand.)
     // (fp32 results were 2 to 5 times further off when joined.)
     std::vector<uint32_t> parts = segments(p.steps, false);
     if (!small && run.bf16) {
