@@ -707,7 +707,7 @@ fa_status fa_rotary_turns(uint32_t rotary_dim, double base, int32_t scaling, dou
  * used.  Those of an input may be 0 (a shared tensor). */
 typedef struct {
     const void* x;
-    void* out;                 /* may be x itself, with the same strides */
+    void* out;                 /* may be x itself, with the same strides, dimension by dimension */
     uint32_t heads;            /* 0: this tensor is left out */
     uint32_t reserved;         /* 0 */
     uint64_t batch_stride, token_stride, head_stride;
@@ -821,7 +821,7 @@ fa_status fa_group_norm_backward(fa_work* w, const fa_group_norm_backward_args* 
  * may be taken as one polynomial of X X^T, and longer sums by the tensor cores, which truncate, between
  * two rounded ones: five steps are off by up to 4e-5 (measured, 2-norm) before the rounding to bf16,
  * which is 1.7e-3 of them.  The result is rounded once.  A NaN or an infinity in x spoils the matrix's
- * whole result. */
+ * whole result (with 0 steps an infinity leaves X 0 elsewhere). */
 #define FA_ORTHO_NESTEROV  1u
 #define FA_ORTHO_MAX_STEPS 32
 
